@@ -30,7 +30,11 @@ __all__ = ["SgemmError", "SgemmUnavailable", "load_library", "library_path",
            "splitk_auto_splits", "splitk_workspace_size", "sgemm_f32_ex", "selftest_wait_timeout",
            "sgemm_f32_streamk", "streamk_workspace_size",
            "sgemm_f32_ex_strided_batched", "sgemm_f32_tf32x3_ex", "set_raster_group",
-           "set_tf32x3_chunk_k", "marshalling"]
+           "set_tf32x3_chunk_k", "marshalling", "sgemm_linear", "sgemm_linear_backward",
+           "sgemm_add_rmsnorm", "sgemm_add_rmsnorm_backward", "sgemm_quantize_rows",
+           "linear_workspace_size", "linear_backward_workspace_size",
+           "add_rmsnorm_backward_workspace_size", "linear", "linear_backward", "add_rmsnorm",
+           "add_rmsnorm_backward", "quantize_rows"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "libsgemm_gb300.so")
@@ -39,14 +43,15 @@ SGEMM_OK = 0
 STATUS_NAMES = {
     0: "SGEMM_OK", 1: "SGEMM_EINVAL_DIM", 2: "SGEMM_EINVAL_LD", 3: "SGEMM_EINVAL_PTR",
     4: "SGEMM_EINVAL_TRANS", 5: "SGEMM_EINVAL_BATCH", 6: "SGEMM_ELAUNCH", 7: "SGEMM_EDEVICE",
-    8: "SGEMM_EWORKSPACE",
+    8: "SGEMM_EWORKSPACE", 9: "SGEMM_EINVAL_TYPE",
 }
 
 _i64 = ctypes.c_int64
 _int = ctypes.c_int
+_u64 = ctypes.c_uint64
 _vp = ctypes.c_void_p
 
-# Exported symbol -> (restype, argtypes).  Kept in step with include/sgemm_gb300.h.
+# Exported symbol -> (restype, argtypes).  Kept in step with include/*.h.
 SIGNATURES = {
     "sgemm_f32": (_int, [_i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _int, _int, _vp]),
     "sgemm_f32_strided_batched": (_int, [_i64, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _i64,
@@ -91,6 +96,19 @@ SIGNATURES = {
     "sgemm_selftest_wait_timeout": (_int, [_i64, _vp]),
     "sgemm_set_raster_group": (_int, [_int]),
     "sgemm_set_tf32x3_chunk_k": (_int, [_int]),
+    "sgemm_linear": (_int, [_int, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _int, _vp, _vp,
+                            _int, _vp, _i64, _int, _vp, _i64, _vp, _i64, _vp, _u64, _vp]),
+    "sgemm_linear_workspace_size": (_u64, [_int, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _int]),
+    "sgemm_linear_backward": (_int, [_int, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _int, _vp, _i64,
+                                     _vp, _i64, _int, _vp, _i64, _vp, _i64, _vp, _vp, _u64, _vp]),
+    "sgemm_linear_backward_workspace_size": (_u64, [_int, _i64, _i64, _i64, _vp, _i64, _int, _vp,
+                                                    _i64, _vp, _i64, _int]),
+    "sgemm_add_rmsnorm": (_int, [_int, _i64, _i64, _vp, _i64, _vp, _i64, _vp, ctypes.c_float, _vp,
+                                 _i64, _vp, _i64, _vp, _vp, _vp]),
+    "sgemm_add_rmsnorm_backward": (_int, [_int, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp,
+                                          _i64, _vp, _i64, _vp, _vp, _u64, _vp]),
+    "sgemm_add_rmsnorm_backward_workspace_size": (_u64, [_int, _i64, _i64]),
+    "sgemm_quantize_rows": (_int, [_int, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp]),
 }
 
 
@@ -117,6 +135,11 @@ FAST_ENTRIES = ("sgemm_f32", "sgemm_f32_strided_batched", "sgemm_f32_ex",
                 "sgemm_f32_ex_strided_batched", "sgemm_f32_tf32x3_ex", "sgemm_f32_splitk",
                 "sgemm_f32_streamk", "sgemm_f32_tf32x3", "sgemm_f32_tf32x3_strided_batched",
                 "sgemm_f32_tf32", "sgemm_f32_tf32_strided_batched", "sgemm_f32_tf32x3_noalloc")
+# The layer operators' entries (include/sgemm_gb300_layers.h), marshalled the same way.
+LAYER_ENTRIES = ("sgemm_linear", "sgemm_linear_workspace_size", "sgemm_linear_backward",
+                 "sgemm_linear_backward_workspace_size", "sgemm_add_rmsnorm",
+                 "sgemm_add_rmsnorm_backward", "sgemm_add_rmsnorm_backward_workspace_size",
+                 "sgemm_quantize_rows")
 
 
 def library_path() -> str:
@@ -157,7 +180,7 @@ def _bind_calls(lib):
     except ImportError:
         return lib
     _calls.bind({name: ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
-                 for name in FAST_ENTRIES})
+                 for name in FAST_ENTRIES + LAYER_ENTRIES})
     return _calls
 
 
@@ -489,3 +512,77 @@ def matmul(A, B, out=None, stream=None, precision="fp32", workspace=None, alpha=
             fn(M, N, K, A.data_ptr(), lda, B.data_ptr(), ldb, out.data_ptr(), ldc, tA, tB, ws,
                wsb, sp)
     return out
+
+
+def sgemm_linear(dtype, M, N, K, X, ldx, x_scale, W, ldw, transW, w_scale, bias, activation,
+                 residual, ldr, out_dtype, Y, ldy, preact=0, ldp=0, workspace=0, workspace_bytes=0,
+                 stream=0, *, check=True):
+    """Y = act(X op(W) + bias) + residual (see include/sgemm_gb300_layers.h)."""
+    st = _entry().sgemm_linear(dtype, M, N, K, X or 0, ldx, x_scale or 0, W or 0, ldw, transW,
+                               w_scale or 0, bias or 0, activation, residual or 0, ldr, out_dtype,
+                               Y or 0, ldy, preact or 0, ldp, workspace or 0, workspace_bytes,
+                               stream or 0)
+    return _check(st) if check else st
+
+
+def linear_workspace_size(dtype, M, N, K, X, ldx, W, ldw, transW) -> int:
+    return _entry().sgemm_linear_workspace_size(dtype, M, N, K, X or 0, ldx, W or 0, ldw, transW)
+
+
+def sgemm_linear_backward(dtype, M, N, K, dY, lddy, Z, ldz, activation, X, ldx, W, ldw, transW, dX,
+                          lddx, dW, lddw, db, workspace=0, workspace_bytes=0, stream=0, *,
+                          check=True):
+    """Gradients of sgemm_linear (see include/sgemm_gb300_layers.h)."""
+    st = _entry().sgemm_linear_backward(dtype, M, N, K, dY or 0, lddy, Z or 0, ldz, activation,
+                                        X or 0, ldx, W or 0, ldw, transW, dX or 0, lddx, dW or 0,
+                                        lddw, db or 0, workspace or 0, workspace_bytes, stream or 0)
+    return _check(st) if check else st
+
+
+def linear_backward_workspace_size(dtype, M, N, K, dY, lddy, activation, X, ldx, W, ldw,
+                                   transW) -> int:
+    return _entry().sgemm_linear_backward_workspace_size(dtype, M, N, K, dY or 0, lddy, activation,
+                                                         X or 0, ldx, W or 0, ldw, transW)
+
+
+def sgemm_add_rmsnorm(dtype, rows, D, X, ldx, residual, ldr, weight, eps, S, lds, Y, ldy, q_scale=0,
+                      rstd=0, stream=0, *, check=True):
+    """Residual addition and root-mean-square norm (see include/sgemm_gb300_layers.h)."""
+    st = _entry().sgemm_add_rmsnorm(dtype, rows, D, X or 0, ldx, residual or 0, ldr, weight or 0,
+                                    eps, S or 0, lds, Y or 0, ldy, q_scale or 0, rstd or 0,
+                                    stream or 0)
+    return _check(st) if check else st
+
+
+def sgemm_add_rmsnorm_backward(dtype, rows, D, dY, lddy, S, lds, rstd, weight, dS, ldds, dX, lddx,
+                               dweight, workspace=0, workspace_bytes=0, stream=0, *, check=True):
+    """Gradients of sgemm_add_rmsnorm (see include/sgemm_gb300_layers.h)."""
+    st = _entry().sgemm_add_rmsnorm_backward(dtype, rows, D, dY or 0, lddy, S or 0, lds, rstd or 0,
+                                             weight or 0, dS or 0, ldds, dX or 0, lddx,
+                                             dweight or 0, workspace or 0, workspace_bytes,
+                                             stream or 0)
+    return _check(st) if check else st
+
+
+def add_rmsnorm_backward_workspace_size(dtype, rows, D) -> int:
+    return _entry().sgemm_add_rmsnorm_backward_workspace_size(dtype, rows, D)
+
+
+def sgemm_quantize_rows(dtype, rows, D, X, ldx, Q, ldq, scale, stream=0, *, check=True):
+    """8-bit rows with a scale each (see include/sgemm_gb300_layers.h)."""
+    st = _entry().sgemm_quantize_rows(dtype, rows, D, X or 0, ldx, Q or 0, ldq, scale or 0,
+                                      stream or 0)
+    return _check(st) if check else st
+
+
+# The torch-level operators (layers.py), imported at first use: the package
+# itself does not need torch.
+_LAYERS = ("linear", "linear_backward", "add_rmsnorm", "add_rmsnorm_backward", "quantize_rows")
+
+
+def __getattr__(name):
+    if name in _LAYERS:
+        from . import layers
+        globals().update({n: getattr(layers, n) for n in _LAYERS})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

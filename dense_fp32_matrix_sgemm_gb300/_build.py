@@ -99,7 +99,7 @@ def _build_calls(verbose: bool = False):
         if verbose:
             sys.stderr.write("note: no C compiler or Python headers; the binding uses ctypes\n")
         return None
-    newest = max(os.path.getmtime(src), os.path.getmtime(os.path.join(INCLUDE, "sgemm_gb300.h")))
+    newest = max(os.path.getmtime(f) for f in [src, *glob.glob(os.path.join(INCLUDE, "*.h"))])
     if os.path.exists(out) and os.path.getmtime(out) >= newest:
         return out
     cmd = [cc, "-O2", "-std=gnu11", "-shared", "-fPIC", "-Wall", "-I", inc, "-I", INCLUDE, src,

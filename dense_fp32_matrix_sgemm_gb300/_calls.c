@@ -13,6 +13,7 @@
 #include <stdint.h>
 
 #include "sgemm_gb300.h"
+#include "sgemm_gb300_layers.h"
 
 #define P(x) ((void *)(uintptr_t)(x))
 
@@ -28,6 +29,15 @@ static __typeof__(&sgemm_f32_tf32x3_strided_batched) f_sgemm_f32_tf32x3_strided_
 static __typeof__(&sgemm_f32_tf32) f_sgemm_f32_tf32;
 static __typeof__(&sgemm_f32_tf32_strided_batched) f_sgemm_f32_tf32_strided_batched;
 static __typeof__(&sgemm_f32_tf32x3_noalloc) f_sgemm_f32_tf32x3_noalloc;
+static __typeof__(&sgemm_linear) f_sgemm_linear;
+static __typeof__(&sgemm_linear_workspace_size) f_sgemm_linear_workspace_size;
+static __typeof__(&sgemm_linear_backward) f_sgemm_linear_backward;
+static __typeof__(&sgemm_linear_backward_workspace_size) f_sgemm_linear_backward_workspace_size;
+static __typeof__(&sgemm_add_rmsnorm) f_sgemm_add_rmsnorm;
+static __typeof__(&sgemm_add_rmsnorm_backward) f_sgemm_add_rmsnorm_backward;
+static __typeof__(&sgemm_add_rmsnorm_backward_workspace_size)
+    f_sgemm_add_rmsnorm_backward_workspace_size;
+static __typeof__(&sgemm_quantize_rows) f_sgemm_quantize_rows;
 
 /* Not bound yet: raise instead of calling a null pointer. */
 static int unbound(const void *fn) {
@@ -181,6 +191,111 @@ static PyObject *py_sgemm_f32_tf32x3_noalloc(PyObject *self, PyObject *args) {
                                                       tB, P(s)));
 }
 
+/* The layer operators (sgemm_gb300_layers.h), arguments in the C order. */
+static PyObject *py_sgemm_linear(PyObject *self, PyObject *args) {
+    long long M, N, K, ldx, ldw, ldr, ldy, ldp;
+    unsigned long long X, xs, W, wsc, bias, R, Y, Z, ws, wsb, s;
+    int dtype, tW, act, out;
+    (void)self;
+    if (unbound((const void *)f_sgemm_linear)) return NULL;
+    if (!PyArg_ParseTuple(args, "iLLLKLKKLiKKiKLiKLKLKKK", &dtype, &M, &N, &K, &X, &ldx, &xs, &W,
+                          &ldw, &tW, &wsc, &bias, &act, &R, &ldr, &out, &Y, &ldy, &Z, &ldp, &ws,
+                          &wsb, &s))
+        return NULL;
+    return PyLong_FromLong(f_sgemm_linear(dtype, M, N, K, P(X), ldx, P(xs), P(W), ldw, tW, P(wsc),
+                                          P(bias), act, P(R), ldr, out, P(Y), ldy, P(Z), ldp, P(ws),
+                                          (uint64_t)wsb, P(s)));
+}
+
+static PyObject *py_sgemm_linear_workspace_size(PyObject *self, PyObject *args) {
+    long long M, N, K, ldx, ldw;
+    unsigned long long X, W;
+    int dtype, tW;
+    (void)self;
+    if (unbound((const void *)f_sgemm_linear_workspace_size)) return NULL;
+    if (!PyArg_ParseTuple(args, "iLLLKLKLi", &dtype, &M, &N, &K, &X, &ldx, &W, &ldw, &tW))
+        return NULL;
+    return PyLong_FromUnsignedLongLong(
+        f_sgemm_linear_workspace_size(dtype, M, N, K, P(X), ldx, P(W), ldw, tW));
+}
+
+static PyObject *py_sgemm_linear_backward(PyObject *self, PyObject *args) {
+    long long M, N, K, lddy, ldz, ldx, ldw, lddx, lddw;
+    unsigned long long dY, Z, X, W, dX, dW, db, ws, wsb, s;
+    int dtype, act, tW;
+    (void)self;
+    if (unbound((const void *)f_sgemm_linear_backward)) return NULL;
+    if (!PyArg_ParseTuple(args, "iLLLKLKLiKLKLiKLKLKKKK", &dtype, &M, &N, &K, &dY, &lddy, &Z, &ldz,
+                          &act, &X, &ldx, &W, &ldw, &tW, &dX, &lddx, &dW, &lddw, &db, &ws, &wsb,
+                          &s))
+        return NULL;
+    return PyLong_FromLong(f_sgemm_linear_backward(dtype, M, N, K, P(dY), lddy, P(Z), ldz, act, P(X),
+                                                   ldx, P(W), ldw, tW, P(dX), lddx, P(dW), lddw,
+                                                   P(db), P(ws), (uint64_t)wsb, P(s)));
+}
+
+static PyObject *py_sgemm_linear_backward_workspace_size(PyObject *self, PyObject *args) {
+    long long M, N, K, lddy, ldx, ldw;
+    unsigned long long dY, X, W;
+    int dtype, act, tW;
+    (void)self;
+    if (unbound((const void *)f_sgemm_linear_backward_workspace_size)) return NULL;
+    if (!PyArg_ParseTuple(args, "iLLLKLiKLKLi", &dtype, &M, &N, &K, &dY, &lddy, &act, &X, &ldx, &W,
+                          &ldw, &tW))
+        return NULL;
+    return PyLong_FromUnsignedLongLong(f_sgemm_linear_backward_workspace_size(
+        dtype, M, N, K, P(dY), lddy, act, P(X), ldx, P(W), ldw, tW));
+}
+
+static PyObject *py_sgemm_add_rmsnorm(PyObject *self, PyObject *args) {
+    long long rows, D, ldx, ldr, lds, ldy;
+    unsigned long long X, R, w, S, Y, q, rstd, s;
+    float eps;
+    int dtype;
+    (void)self;
+    if (unbound((const void *)f_sgemm_add_rmsnorm)) return NULL;
+    if (!PyArg_ParseTuple(args, "iLLKLKLKfKLKLKKK", &dtype, &rows, &D, &X, &ldx, &R, &ldr, &w, &eps,
+                          &S, &lds, &Y, &ldy, &q, &rstd, &s))
+        return NULL;
+    return PyLong_FromLong(f_sgemm_add_rmsnorm(dtype, rows, D, P(X), ldx, P(R), ldr, P(w), eps, P(S),
+                                               lds, P(Y), ldy, P(q), P(rstd), P(s)));
+}
+
+static PyObject *py_sgemm_add_rmsnorm_backward(PyObject *self, PyObject *args) {
+    long long rows, D, lddy, lds, ldds, lddx;
+    unsigned long long dY, S, rstd, w, dS, dX, dw, ws, wsb, s;
+    int dtype;
+    (void)self;
+    if (unbound((const void *)f_sgemm_add_rmsnorm_backward)) return NULL;
+    if (!PyArg_ParseTuple(args, "iLLKLKLKKKLKLKKKK", &dtype, &rows, &D, &dY, &lddy, &S, &lds, &rstd,
+                          &w, &dS, &ldds, &dX, &lddx, &dw, &ws, &wsb, &s))
+        return NULL;
+    return PyLong_FromLong(f_sgemm_add_rmsnorm_backward(dtype, rows, D, P(dY), lddy, P(S), lds,
+                                                        P(rstd), P(w), P(dS), ldds, P(dX), lddx,
+                                                        P(dw), P(ws), (uint64_t)wsb, P(s)));
+}
+
+static PyObject *py_sgemm_add_rmsnorm_backward_workspace_size(PyObject *self, PyObject *args) {
+    long long rows, D;
+    int dtype;
+    (void)self;
+    if (unbound((const void *)f_sgemm_add_rmsnorm_backward_workspace_size)) return NULL;
+    if (!PyArg_ParseTuple(args, "iLL", &dtype, &rows, &D)) return NULL;
+    return PyLong_FromUnsignedLongLong(f_sgemm_add_rmsnorm_backward_workspace_size(dtype, rows, D));
+}
+
+static PyObject *py_sgemm_quantize_rows(PyObject *self, PyObject *args) {
+    long long rows, D, ldx, ldq;
+    unsigned long long X, Q, scale, s;
+    int dtype;
+    (void)self;
+    if (unbound((const void *)f_sgemm_quantize_rows)) return NULL;
+    if (!PyArg_ParseTuple(args, "iLLKLKLKK", &dtype, &rows, &D, &X, &ldx, &Q, &ldq, &scale, &s))
+        return NULL;
+    return PyLong_FromLong(
+        f_sgemm_quantize_rows(dtype, rows, D, P(X), ldx, P(Q), ldq, P(scale), P(s)));
+}
+
 /* bind({name: address}): the entry points' addresses in the loaded library.
  * Every name above must be present. */
 static PyObject *py_bind(PyObject *self, PyObject *args) {
@@ -210,6 +325,14 @@ static PyObject *py_bind(PyObject *self, PyObject *args) {
     BIND(sgemm_f32_tf32);
     BIND(sgemm_f32_tf32_strided_batched);
     BIND(sgemm_f32_tf32x3_noalloc);
+    BIND(sgemm_linear);
+    BIND(sgemm_linear_workspace_size);
+    BIND(sgemm_linear_backward);
+    BIND(sgemm_linear_backward_workspace_size);
+    BIND(sgemm_add_rmsnorm);
+    BIND(sgemm_add_rmsnorm_backward);
+    BIND(sgemm_add_rmsnorm_backward_workspace_size);
+    BIND(sgemm_quantize_rows);
 #undef BIND
     Py_RETURN_NONE;
 }
@@ -229,6 +352,14 @@ static PyMethodDef methods[] = {
     ENTRY(sgemm_f32_tf32),
     ENTRY(sgemm_f32_tf32_strided_batched),
     ENTRY(sgemm_f32_tf32x3_noalloc),
+    ENTRY(sgemm_linear),
+    ENTRY(sgemm_linear_workspace_size),
+    ENTRY(sgemm_linear_backward),
+    ENTRY(sgemm_linear_backward_workspace_size),
+    ENTRY(sgemm_add_rmsnorm),
+    ENTRY(sgemm_add_rmsnorm_backward),
+    ENTRY(sgemm_add_rmsnorm_backward_workspace_size),
+    ENTRY(sgemm_quantize_rows),
     {NULL, NULL, 0, NULL},
 };
 

@@ -276,6 +276,10 @@ int run_splitk(int64_t M, int64_t N, int64_t K, const float *A, int64_t lda, con
 // translation unit and returns `code`.
 int record_error(int code, const char *msg) { return fail(code, "%s", msg); }
 
+// SGEMM_OK when the current device can run the library's kernels, for other
+// translation units.
+int require_device() { return check_device(); }
+
 // The workspace plan of sgemm_f32_streamk.  A K-contiguous operand (row-major
 // A, B stored transposed) of a large problem is first turned into an
 // M/N-contiguous copy, so the tile kernel sees A^T with row-major B (both
@@ -590,6 +594,7 @@ const char *sgemm_status_string(int status) {
         case SGEMM_ELAUNCH: return "SGEMM_ELAUNCH: kernel launch failed";
         case SGEMM_EDEVICE: return "SGEMM_EDEVICE: no usable sm_103 device";
         case SGEMM_EWORKSPACE: return "SGEMM_EWORKSPACE: workspace missing, misaligned or too small";
+        case SGEMM_EINVAL_TYPE: return "SGEMM_EINVAL_TYPE: element type or activation not supported";
         default: return "unknown sgemm status";
     }
 }

@@ -1,0 +1,328 @@
+// The linear layer of few rows (a decoding step's tokens) on the CUDA cores.
+//
+// z[i,j] = sum_k X[i,k] W[j,k] with M small: every weight is read once and
+// used M times, so HBM bounds it (2 M flops a weight against 4, 2 or 1
+// bytes), and what counts is that enough 16-byte loads are in flight on
+// every SM from the start.  The tensor cores would be idle between loads all
+// the same, and FP32 FMAs (packed in pairs) keep up for the few rows that the
+// launcher sends here.
+//
+// Weights stored N x K (dot form): a warp takes two output features and walks
+// K, each lane with 16-byte pieces of both rows of W and of the MR rows of X
+// (X stays in L1).  Where the features alone would not fill the SMs, K is
+// split over the warps of a CTA and their sums are added through shared
+// memory, in warp order.
+// Weights stored K x N (column form): a lane takes 16 bytes of consecutive
+// features and walks k; K is split over the warps of a CTA and over a cluster
+// of CTAs, and the sums are added through shared and distributed shared
+// memory in rank order.
+// Rows or bases that are not 16-byte aligned take one element an access.
+#include <cstdint>
+#include <type_traits>
+
+#include <cuda_runtime.h>
+
+#include "device_utils.cuh"
+#include "layer_math.cuh"
+#include "layers.h"
+
+namespace sgemm {
+namespace rows {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+
+// 16 bytes (or one element) of T as pairs of floats.
+template <class T, int W>
+struct Piece {
+    static constexpr int PAIRS = W > 1 ? W / 2 : 1;
+};
+
+template <class T, int W>
+__device__ __forceinline__ void load_pairs(const T *p, float2 (&f)[Piece<T, W>::PAIRS]) {
+    if constexpr (W == 1) {
+        f[0] = make_float2(to_f32(*p), 0.f);
+    } else {
+        const Vec<T, W> v = load_vec<T, W>(p);
+#pragma unroll
+        for (int i = 0; i < W / 2; ++i) f[i] = make_float2(to_f32(v.v[2 * i]), to_f32(v.v[2 * i + 1]));
+    }
+}
+template <class T, int W>
+__device__ __forceinline__ void load_pairs_e4m3(const uint8_t *p, float2 (&f)[Piece<T, W>::PAIRS]) {
+    if constexpr (W == 1) {
+        f[0] = make_float2(from_e4m3x2(*p).x, 0.f);
+    } else {
+        const uint4 v = *reinterpret_cast<const uint4 *>(p);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = from_e4m3x2((uint16_t)(w[i] & 0xffffu));
+            f[2 * i + 1] = from_e4m3x2((uint16_t)(w[i] >> 16));
+        }
+    }
+}
+template <>
+__device__ __forceinline__ void load_pairs<uint8_t, 16>(const uint8_t *p, float2 (&f)[8]) {
+    load_pairs_e4m3<uint8_t, 16>(p, f);
+}
+template <>
+__device__ __forceinline__ void load_pairs<uint8_t, 1>(const uint8_t *p, float2 (&f)[1]) {
+    load_pairs_e4m3<uint8_t, 1>(p, f);
+}
+
+struct Args {
+    const void *X, *W;
+    int64_t ldx, ldw;
+    int K;
+    int split;   // dot form: warps of a CTA that share a feature pair's K
+    LayerEpi epi;
+};
+
+// Dot form.  Warp w of the CTA: feature pair w / split, K pieces w % split of
+// split.  Accumulators hold the sums over even and odd positions of the
+// pieces apart (one packed FMA for both).
+template <class T, class O, int W, int MR>
+__global__ void __launch_bounds__(kThreads) dot_kernel(const Args a) {
+    __shared__ float red[kWarps][2 * MR];
+    pdl_trigger();
+    pdl_wait();
+    constexpr int P = Piece<T, W>::PAIRS;
+    constexpr int U = W == 1 ? 4 : MR <= 2 ? 4 : 2;   // pieces in flight a row
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int sub = warp % a.split;
+    const int j0 = 2 * (int)(blockIdx.x * (kWarps / a.split) + warp / a.split);
+    const T *w0 = static_cast<const T *>(a.W) + j0 * a.ldw;
+    const bool two = j0 + 1 < a.epi.N;
+    const T *w1 = two ? w0 + a.ldw : w0;
+    const int groups = (a.epi.M + MR - 1) / MR;
+    for (int g = blockIdx.y; g < groups; g += gridDim.y) {
+        const int m0 = g * MR;
+        float2 acc[2][MR];
+#pragma unroll
+        for (int m = 0; m < MR; ++m) acc[0][m] = acc[1][m] = make_float2(0.f, 0.f);
+        if (j0 < a.epi.N) {
+            const T *x[MR];
+#pragma unroll
+            for (int m = 0; m < MR; ++m)
+                x[m] = static_cast<const T *>(a.X) + min(m0 + m, a.epi.M - 1) * a.ldx;
+            const int step = a.split * 32 * W;
+            int k = (sub * 32 + lane) * W;
+            for (; k + (U - 1) * step < a.K; k += U * step) {
+                float2 f0[U][P], f1[U][P];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    load_pairs<T, W>(w0 + k + u * step, f0[u]);
+                    load_pairs<T, W>(w1 + k + u * step, f1[u]);
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+#pragma unroll
+                    for (int m = 0; m < MR; ++m) {
+                        float2 fx[P];
+                        load_pairs<T, W>(x[m] + k + u * step, fx);
+#pragma unroll
+                        for (int i = 0; i < P; ++i) {
+                            acc[0][m] = __ffma2_rn(f0[u][i], fx[i], acc[0][m]);
+                            acc[1][m] = __ffma2_rn(f1[u][i], fx[i], acc[1][m]);
+                        }
+                    }
+                }
+            }
+            for (; k < a.K; k += step) {
+                float2 f0[P], f1[P];
+                load_pairs<T, W>(w0 + k, f0);
+                load_pairs<T, W>(w1 + k, f1);
+#pragma unroll
+                for (int m = 0; m < MR; ++m) {
+                    float2 fx[P];
+                    load_pairs<T, W>(x[m] + k, fx);
+#pragma unroll
+                    for (int i = 0; i < P; ++i) {
+                        acc[0][m] = __ffma2_rn(f0[i], fx[i], acc[0][m]);
+                        acc[1][m] = __ffma2_rn(f1[i], fx[i], acc[1][m]);
+                    }
+                }
+            }
+        }
+        float v[2 * MR];   // [feature][row]
+#pragma unroll
+        for (int m = 0; m < MR; ++m) {
+            v[m] = acc[0][m].x + acc[0][m].y;
+            v[MR + m] = acc[1][m].x + acc[1][m].y;
+        }
+#pragma unroll
+        for (int i = 0; i < 2 * MR; ++i)
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+        // lane i < 2 MR keeps sum i
+        float mine = 0.f;
+#pragma unroll
+        for (int i = 0; i < 2 * MR; ++i) mine = lane == i ? v[i] : mine;
+        if (a.split > 1) {
+            __syncthreads();   // the previous group's sums have been read
+            if (lane < 2 * MR) red[warp][lane] = mine;
+            __syncthreads();
+            if (sub == 0 && lane < 2 * MR)
+                for (int s = 1; s < a.split; ++s) mine += red[warp + s][lane];
+        }
+        const int row = m0 + lane % MR, col = j0 + lane / MR;
+        if (sub == 0 && lane < 2 * MR && row < a.epi.M && col < a.epi.N)
+            finish1<O>(a.epi, row, col, mine);
+    }
+}
+
+// Column form: CTA (x, y) of a cluster along x of `cluster_size` CTAs: columns
+// [strip * 32 W, ...), k = (rank * 8 + warp) + 8 size * i.
+template <class T, class O, int W, int MR>
+__global__ void __launch_bounds__(kThreads) column_kernel(const Args a) {
+    constexpr int COLS = 32 * W;
+    __shared__ __align__(16) float red[kWarps][MR][COLS];
+    pdl_trigger();
+    pdl_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t rank = cluster_rank(), size = cluster_size();
+    const int strip = (int)(blockIdx.x / size);
+    const int c = strip * COLS + lane * W;
+    const int groups = (a.epi.M + MR - 1) / MR;
+    for (int g = blockIdx.y; g < groups; g += gridDim.y) {
+        const int m0 = g * MR;
+        float acc[MR][W];
+#pragma unroll
+        for (int m = 0; m < MR; ++m)
+#pragma unroll
+            for (int j = 0; j < W; ++j) acc[m][j] = 0.f;
+        if (c < a.epi.N) {
+            const T *w = static_cast<const T *>(a.W) + c;
+            const T *x[MR];
+#pragma unroll
+            for (int m = 0; m < MR; ++m)
+                x[m] = static_cast<const T *>(a.X) + min(m0 + m, a.epi.M - 1) * a.ldx;
+            const int step = kWarps * (int)size;
+            constexpr int U = 4;   // rows of W in flight
+            for (int k = (int)rank * kWarps + warp; k < a.K; k += U * step) {
+                Vec<T, W> vw[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (k + u * step < a.K) vw[u] = load_vec<T, W>(w + (k + u * step) * a.ldw);
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (k + u * step >= a.K) break;
+#pragma unroll
+                    for (int m = 0; m < MR; ++m) {
+                        const float xv = to_f32(x[m][k + u * step]);
+#pragma unroll
+                        for (int j = 0; j < W; ++j)
+                            acc[m][j] = fmaf(xv, to_f32(vw[u].v[j]), acc[m][j]);
+                    }
+                }
+            }
+        }
+        // this CTA's sums into red[0], in warp order
+#pragma unroll
+        for (int m = 0; m < MR; ++m)
+#pragma unroll
+            for (int j = 0; j < W; ++j) red[warp][m][lane * W + j] = acc[m][j];
+        __syncthreads();
+        for (int i = threadIdx.x; i < MR * COLS; i += kThreads) {
+            float s = 0.f;
+#pragma unroll
+            for (int q = 0; q < kWarps; ++q) s += red[q][i / COLS][i % COLS];
+            red[0][i / COLS][i % COLS] = s;
+        }
+        if (size > 1) cluster_sync();
+        else __syncthreads();
+        // each CTA of the cluster finishes a share of the strip
+        for (int i = (int)rank * kThreads + threadIdx.x; i < MR * COLS; i += (int)size * kThreads) {
+            const int m = i / COLS, col = strip * COLS + i % COLS;
+            const float s = size > 1 ? cluster_sum_f32(smem_u32(&red[0][m][i % COLS]), size)
+                                     : red[0][m][i % COLS];
+            if (m0 + m < a.epi.M && col < a.epi.N) finish1<O>(a.epi, m0 + m, col, s);
+        }
+        // red is written again, or the CTA ends, only after every peer has read it
+        if (size > 1) cluster_sync();
+        else __syncthreads();
+    }
+}
+
+template <class K>
+cudaError_t launch(K kernel, dim3 grid, int cluster, const Args &a, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+constexpr int kSms = 152;
+
+template <class T, class O, int W, int MR>
+cudaError_t run(Args a, int transW, cudaStream_t s) {
+    const int groups = (a.epi.M + MR - 1) / MR;
+    const unsigned gy = (unsigned)(groups < 65535 ? groups : 65535);
+    if (transW) {
+        // warps a feature pair: until about 24 warps an SM are busy, each with
+        // at least one piece of K a lane
+        const int64_t pairs = (a.epi.N + 1) / 2;
+        a.split = 1;
+        while (a.split < kWarps && pairs * gy * a.split < kSms * 24 &&
+               (int64_t)a.K > (int64_t)a.split * 32 * W)
+            a.split *= 2;
+        const int64_t per_cta = kWarps / a.split;
+        return launch(dot_kernel<T, O, W, MR>, dim3((unsigned)((pairs + per_cta - 1) / per_cta), gy),
+                      1, a, s);
+    }
+    if constexpr (!std::is_same<T, uint8_t>::value) {
+        const int64_t strips = (a.epi.N + 32 * W - 1) / (32 * W);
+        int size = 1;
+        while (size < 8 && strips * gy * size < kSms * 2 && a.K > size * kWarps * 4) size *= 2;
+        return launch(column_kernel<T, O, W, MR>, dim3((unsigned)(strips * size), gy), size, a, s);
+    }
+    return cudaErrorInvalidValue;
+}
+
+template <class T, class O, int W>
+cudaError_t by_rows(const Args &a, int transW, cudaStream_t s) {
+    if (a.epi.M == 1) return run<T, O, W, 1>(a, transW, s);
+    if (a.epi.M == 2) return run<T, O, W, 2>(a, transW, s);
+    if (a.epi.M <= 4 || sizeof(T) < 4) return run<T, O, W, 4>(a, transW, s);
+    if constexpr (sizeof(T) == 4) return run<T, O, W, 8>(a, transW, s);
+    return cudaErrorInvalidValue;
+}
+
+template <class T, class O>
+cudaError_t by_alignment(const Args &a, int transW, cudaStream_t s) {
+    constexpr int W = 16 / sizeof(T);
+    auto ok = [](const void *p, int64_t ld) {
+        return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * (int64_t)sizeof(T) % 16 == 0;
+    };
+    const bool vec = transW ? ok(a.X, a.ldx) && ok(a.W, a.ldw) && a.K % W == 0
+                            : ok(a.W, a.ldw) && a.epi.N % W == 0;
+    return vec ? by_rows<T, O, W>(a, transW, s) : by_rows<T, O, 1>(a, transW, s);
+}
+
+}  // namespace rows
+
+cudaError_t launch_linear_rows(int in_type, const void *X, int64_t ldx, const void *W, int64_t ldw,
+                               int transW, int K, const LayerEpi &epi, cudaStream_t s) {
+    const rows::Args a = {X, W, ldx, ldw, K, 1, epi};
+    switch (in_type) {
+        case SGEMM_F32: return rows::by_alignment<float, float>(a, transW, s);
+        case SGEMM_BF16: return rows::by_alignment<__nv_bfloat16, __nv_bfloat16>(a, transW, s);
+        case SGEMM_F16: return rows::by_alignment<__half, __half>(a, transW, s);
+        default:
+            return epi.type == SGEMM_BF16 ? rows::by_alignment<uint8_t, __nv_bfloat16>(a, transW, s)
+                                          : rows::by_alignment<uint8_t, __half>(a, transW, s);
+    }
+}
+
+}  // namespace sgemm

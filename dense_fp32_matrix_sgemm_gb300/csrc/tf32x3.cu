@@ -53,12 +53,15 @@
 #include <cstdint>
 #include <cstdio>
 #include <mutex>
+#include <type_traits>
 
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
 #include "gemm_args.h"
+#include "layer_math.cuh"
+#include "layers.h"
 #include "tc_utils.cuh"
 #include "tma_encode.h"
 
@@ -327,6 +330,14 @@ struct Tf32x3Params {
     float *part;            // [split * tail][BM * BN] partial tiles, row-major
 };
 
+// With the layer epilogue instead (its Y is C).  A type of its own, so that
+// the kernels of the plain product keep their parameters and registers.
+struct Tf32x3LayerParams : Tf32x3Params {
+    LayerEpi le;
+};
+template <class PT>
+constexpr bool kLayer = std::is_same<PT, Tf32x3LayerParams>::value;
+
 __device__ __forceinline__ void raster(const Tf32x3Params &p, int bid, int &z, int &tm, int &tn) {
     const int per_batch = p.tiles_m * p.tiles_n;
     z = bid / per_batch;
@@ -350,8 +361,8 @@ __device__ __forceinline__ void raster(const Tf32x3Params &p, int bid, int &z, i
 //   lane 0.  `cc` counts the chunks staged so far (across calls), picks the
 //   buffer and says when to wait for the store two chunks back.
 //   Otherwise: each thread stores its own row, with the epilogue applied.
-template <class CFG>
-__device__ __forceinline__ void store_tile_rows(const Tf32x3Params &p, const CUtensorMap *tmC,
+template <class CFG, class PT>
+__device__ __forceinline__ void store_tile_rows(const PT &p, const CUtensorMap *tmC,
                                                 uint32_t acc, int q, int lane, int z, int m0,
                                                 int n0, uint32_t stage, int &cc) {
     constexpr int BN = CFG::BN, ACC_COLS = CFG::ACC_COLS;
@@ -413,7 +424,14 @@ __device__ __forceinline__ void store_tile_rows(const Tf32x3Params &p, const CUt
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] += w[j];
         }
-        if (row < p.M) {
+        if constexpr (kLayer<PT>) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+                const float w[4] = {v[j], v[j + 1], v[j + 2], v[j + 3]};
+                if (row < p.M && n0 + 32 * c + j < p.N)
+                    finish<float, 4>(p.le, row, n0 + 32 * c + j, w);
+            }
+        } else if (row < p.M) {
             const int col0 = n0 + 32 * c;
             if (!(p.alpha == 1.f && p.beta == 0.f && p.bias == nullptr)) {
 #pragma unroll
@@ -527,13 +545,13 @@ __device__ __forceinline__ void convert_stage(uint8_t *st, int t) {
 
 // tmA / tmB: the operand's planes, or (RAW) its raw rows; tmAlo / tmBlo: the
 // lo-only plane of an operand in RAW but not CONV (unused otherwise).
-template <class CFG, int ACC_BUFS, int RAW, int CONV>
+template <class CFG, int ACC_BUFS, int RAW, int CONV, class PT>
 __global__ void __launch_bounds__(Persist<CFG, ACC_BUFS, RAW, CONV>::THREADS, 1)
 tf32x3_persistent_kernel(const __grid_constant__ CUtensorMap tmA,
                          const __grid_constant__ CUtensorMap tmB,
                          const __grid_constant__ CUtensorMap tmAlo,
                          const __grid_constant__ CUtensorMap tmBlo,
-                         const __grid_constant__ CUtensorMap tmC, const Tf32x3Params p) {
+                         const __grid_constant__ CUtensorMap tmC, const PT p) {
     using P = Persist<CFG, ACC_BUFS, RAW, CONV>;
     constexpr int BK = CFG::BK, STAGES = CFG::STAGES, PLANES = CFG::PLANES;
     constexpr int BN = CFG::BN, ACC_COLS = CFG::ACC_COLS;
@@ -820,8 +838,8 @@ struct Chunked {
 //   Otherwise (C only) the warp reads the block back a row at a time, lane j
 //   taking column j, and stores it with the epilogue: each store is one
 //   128-byte row segment.
-template <int COLS>
-__device__ __forceinline__ void store_running_rows(const Tf32x3Params &p, const CUtensorMap *map,
+template <int COLS, class PT>
+__device__ __forceinline__ void store_running_rows(const PT &p, const CUtensorMap *map,
                                                    bool tma, int tma_n, const float (&run)[COLS],
                                                    int q, int lane, int z, int m0, int n0,
                                                    int rows, int cols, uint32_t stage, int &cc) {
@@ -862,7 +880,9 @@ __device__ __forceinline__ void store_running_rows(const Tf32x3Params &p, const 
                          : "r"(stage + (uint32_t)r * 128u +
                                ((uint32_t)((lane >> 2) ^ (r & 7)) << 4) + cofs)
                          : "memory");
-            if (col < p.N) {
+            if constexpr (kLayer<PT>) {
+                if (col < p.N) finish1<float>(p.le, row0 + r, col, v);
+            } else if (col < p.N) {
                 float *cp = p.C + (int64_t)z * p.strideC + (int64_t)(row0 + r) * p.ldc + col;
                 if (!(p.alpha == 1.f && p.beta == 0.f && p.bias == nullptr)) {
                     const float old = p.beta != 0.f ? *cp : 0.f;
@@ -926,8 +946,8 @@ __device__ __forceinline__ Piece piece_of(const Tf32x3Params &p, int c, int G, i
 // split * V / 8 round trips; the adds go in K order starting from zero.  The
 // launcher takes V = 4 when that still gives a CTA per SM, else V = 1.
 // Launched as a programmatic dependent of the GEMM kernel.
-template <int BN, int V>
-__global__ void __launch_bounds__(256) tf32x3_fixup_kernel(const Tf32x3Params p) {
+template <int BN, int V, class PT>
+__global__ void __launch_bounds__(256) tf32x3_fixup_kernel(const PT p) {
     constexpr int NB = 8 / V;   // segments per batch
     static_assert((BM * BN) % (1024 * V) == 0, "whole float4 groups per CTA");
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -970,6 +990,10 @@ __global__ void __launch_bounds__(256) tf32x3_fixup_kernel(const Tf32x3Params p)
         if (row >= p.M || col >= p.N) continue;
         float *cp = p.C + (int64_t)z * p.strideC + (int64_t)row * p.ldc + col;
         float o[4] = {acc[r].x, acc[r].y, acc[r].z, acc[r].w};
+        if constexpr (kLayer<PT>) {
+            finish<float, 4>(p.le, row, col, o);
+            continue;
+        }
         if (!plain) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -1003,14 +1027,14 @@ __global__ void __launch_bounds__(256) tf32x3_fixup_kernel(const Tf32x3Params p)
 // and the abort word stops all roles.  RAW as in the persistent kernel (no
 // converter warps: chunking applies to K > 256, where operands come from lo
 // planes).
-template <class CFG, int RAW>
+template <class CFG, int RAW, class PT>
 __global__ void __launch_bounds__(Chunked<CFG>::THREADS, 1)
 tf32x3_chunked_kernel(const __grid_constant__ CUtensorMap tmA,
                       const __grid_constant__ CUtensorMap tmB,
                       const __grid_constant__ CUtensorMap tmAlo,
                       const __grid_constant__ CUtensorMap tmBlo,
                       const __grid_constant__ CUtensorMap tmC,
-                      const __grid_constant__ CUtensorMap tmP, const Tf32x3Params p) {
+                      const __grid_constant__ CUtensorMap tmP, const PT p) {
     using P = Chunked<CFG>;
     constexpr int BK = CFG::BK, STAGES = CFG::STAGES, PLANES = CFG::PLANES;
     constexpr int BN = CFG::BN;
@@ -1446,7 +1470,7 @@ size_t plane_bytes(int64_t rows, int64_t K, int64_t batch, int planes) {
 // a raw operand that is not converted gets a lo-only plane and its map in
 // tmAlo / tmBlo (which are left empty otherwise).
 template <class CFG>
-cudaError_t prepare(const GemmArgs &a, bool transA, bool transB, int raw, int conv, void *ws,
+cudaError_t prepare(const GemmArgs &a, bool layer, bool transA, bool transB, int raw, int conv, void *ws,
                     cudaStream_t s, CUtensorMap &tmA, CUtensorMap &tmB, CUtensorMap &tmAlo,
                     CUtensorMap &tmBlo, CUtensorMap &tmC, Tf32x3Params &p) {
     constexpr int PLANES = CFG::PLANES;
@@ -1526,7 +1550,7 @@ cudaError_t prepare(const GemmArgs &a, bool transA, bool transB, int raw, int co
     // tma_c is set.
     tmC = CUtensorMap{};
     const int n4 = a.N / 4 * 4;
-    p.tma_c = p.vec_c && n4 > 0 && plain_epilogue(a) &&
+    p.tma_c = p.vec_c && n4 > 0 && plain_epilogue(a) && !layer &&
               make_c_map(&tmC, a.C, a.M, n4, a.ldc, a.strideC, a.batch);
     p.tma_n = a.N % 4 == 0 ? INT_MAX : n4;
     return cudaSuccess;
@@ -1545,12 +1569,12 @@ cudaError_t ensure_smem(Kern kern, int bytes, PerContext<bool> &configured) {
 }
 
 // One CTA per SM, walking the tiles (see tf32x3_persistent_kernel).
-template <class CFG, int ACC_BUFS, int RAW, int CONV>
-cudaError_t launch_persistent_raw(const GemmArgs &a, bool transA, bool transB, void *ws,
+template <class CFG, int ACC_BUFS, int RAW, int CONV, class PT>
+cudaError_t launch_persistent_raw(const GemmArgs &a, const LayerEpi *le, bool transA, bool transB, void *ws,
                                   cudaStream_t s, CUtensorMap &tmA, CUtensorMap &tmB) {
     using P = Persist<CFG, ACC_BUFS, RAW, CONV>;
     static PerContext<bool> configured;
-    cudaError_t e = ensure_smem(tf32x3_persistent_kernel<CFG, ACC_BUFS, RAW, CONV>, P::SMEM_BYTES,
+    cudaError_t e = ensure_smem(tf32x3_persistent_kernel<CFG, ACC_BUFS, RAW, CONV, PT>, P::SMEM_BYTES,
                                 configured);
     if (e != cudaSuccess) return e;
     int dev = 0, sms = 0;
@@ -1559,9 +1583,11 @@ cudaError_t launch_persistent_raw(const GemmArgs &a, bool transA, bool transB, v
     e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
     CUtensorMap tmC, tmAlo, tmBlo;
-    Tf32x3Params p;
-    e = prepare<CFG>(a, transA, transB, RAW, CONV, ws, s, tmA, tmB, tmAlo, tmBlo, tmC, p);
+    PT p;
+    e = prepare<CFG>(a, kLayer<PT>, transA, transB, RAW, CONV, ws, s, tmA, tmB, tmAlo, tmBlo, tmC,
+                     p);
     if (e != cudaSuccess) return e;
+    if constexpr (kLayer<PT>) p.le = *le;
     const long long tiles = (long long)a.batch * p.tiles_m * p.tiles_n;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(tiles < sms ? tiles : sms));
@@ -1575,7 +1601,7 @@ cudaError_t launch_persistent_raw(const GemmArgs &a, bool transA, bool transB, v
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, tf32x3_persistent_kernel<CFG, ACC_BUFS, RAW, CONV>, tmA, tmB,
+    e = cudaLaunchKernelEx(&cfg, tf32x3_persistent_kernel<CFG, ACC_BUFS, RAW, CONV, PT>, tmA, tmB,
                            tmAlo, tmBlo, tmC, p);
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
@@ -1614,30 +1640,30 @@ constexpr int kChunkMinK = 256;
 // Launches with the runtime choice `conv` (a subset of RAW) of converted
 // operands; a combination the configuration does not provide launches
 // nothing and returns an error (the caller never asks for one).
-template <class CFG, int ACC_BUFS, int RAW>
-cudaError_t launch_conv(const GemmArgs &a, bool transA, bool transB, void *ws, cudaStream_t s,
+template <class CFG, int ACC_BUFS, int RAW, class PT>
+cudaError_t launch_conv(const GemmArgs &a, const LayerEpi *le, bool transA, bool transB, void *ws, cudaStream_t s,
                         CUtensorMap &tmA, CUtensorMap &tmB, int conv) {
     if constexpr (CFG::PLANES == 1) {
         // one term: an operand is raw only when it is rounded in the stage
         if (conv == RAW)
-            return launch_persistent_raw<CFG, ACC_BUFS, RAW, RAW>(a, transA, transB, ws, s, tmA, tmB);
+            return launch_persistent_raw<CFG, ACC_BUFS, RAW, RAW, PT>(a, le, transA, transB, ws, s, tmA, tmB);
     } else if constexpr (CFG::BN == 128) {
         switch (conv) {
             case 0:
-                return launch_persistent_raw<CFG, ACC_BUFS, RAW, 0>(a, transA, transB, ws, s, tmA, tmB);
+                return launch_persistent_raw<CFG, ACC_BUFS, RAW, 0, PT>(a, le, transA, transB, ws, s, tmA, tmB);
             case 1:
                 if constexpr ((RAW & 1) != 0)
-                    return launch_persistent_raw<CFG, ACC_BUFS, RAW, 1>(a, transA, transB, ws, s, tmA,
+                    return launch_persistent_raw<CFG, ACC_BUFS, RAW, 1, PT>(a, le, transA, transB, ws, s, tmA,
                                                                         tmB);
                 break;
             case 2:
                 if constexpr ((RAW & 2) != 0)
-                    return launch_persistent_raw<CFG, ACC_BUFS, RAW, 2>(a, transA, transB, ws, s, tmA,
+                    return launch_persistent_raw<CFG, ACC_BUFS, RAW, 2, PT>(a, le, transA, transB, ws, s, tmA,
                                                                         tmB);
                 break;
             case 3:
                 if constexpr (RAW == 3)
-                    return launch_persistent_raw<CFG, ACC_BUFS, 3, 3>(a, transA, transB, ws, s, tmA, tmB);
+                    return launch_persistent_raw<CFG, ACC_BUFS, 3, 3, PT>(a, le, transA, transB, ws, s, tmA, tmB);
                 break;
             default:
                 break;
@@ -1645,13 +1671,13 @@ cudaError_t launch_conv(const GemmArgs &a, bool transA, bool transB, void *ws, c
     } else {
         // the 256-wide three-term tile (K > 256 only): lo planes, no converters
         if (conv == 0)
-            return launch_persistent_raw<CFG, ACC_BUFS, RAW, 0>(a, transA, transB, ws, s, tmA, tmB);
+            return launch_persistent_raw<CFG, ACC_BUFS, RAW, 0, PT>(a, le, transA, transB, ws, s, tmA, tmB);
     }
     return cudaErrorInvalidValue;
 }
 
-template <class CFG, int ACC_BUFS>
-cudaError_t launch_persistent(const GemmArgs &a, bool transA, bool transB, void *ws,
+template <class CFG, int ACC_BUFS, class PT>
+cudaError_t launch_persistent(const GemmArgs &a, const LayerEpi *le, bool transA, bool transB, void *ws,
                               cudaStream_t s) {
     const int64_t tiles_m = (a.M + BM - 1) / BM, tiles_n = (a.N + CFG::BN - 1) / CFG::BN;
     // converting an operand whose panels `reuse` tiles read
@@ -1680,10 +1706,10 @@ cudaError_t launch_persistent(const GemmArgs &a, bool transA, bool transB, void 
         if ((raw & 2) && convert(tiles_m)) conv |= 2;
     }
     switch (raw) {
-        case 1: return launch_conv<CFG, ACC_BUFS, 1>(a, transA, transB, ws, s, tmA, tmB, conv);
-        case 2: return launch_conv<CFG, ACC_BUFS, 2>(a, transA, transB, ws, s, tmA, tmB, conv);
-        case 3: return launch_conv<CFG, ACC_BUFS, 3>(a, transA, transB, ws, s, tmA, tmB, conv);
-        default: return launch_persistent_raw<CFG, ACC_BUFS, 0, 0>(a, transA, transB, ws, s, tmA, tmB);
+        case 1: return launch_conv<CFG, ACC_BUFS, 1, PT>(a, le, transA, transB, ws, s, tmA, tmB, conv);
+        case 2: return launch_conv<CFG, ACC_BUFS, 2, PT>(a, le, transA, transB, ws, s, tmA, tmB, conv);
+        case 3: return launch_conv<CFG, ACC_BUFS, 3, PT>(a, le, transA, transB, ws, s, tmA, tmB, conv);
+        default: return launch_persistent_raw<CFG, ACC_BUFS, 0, 0, PT>(a, le, transA, transB, ws, s, tmA, tmB);
     }
 }
 
@@ -1725,13 +1751,13 @@ ChunkedPlan chunked_plan_for(const GemmArgs &a, int sms) {
     return chunked_plan(tiles, (a.K + CFG::BK - 1) / CFG::BK, CFG::BN, sms);
 }
 
-template <class CFG, int RAW>
-cudaError_t launch_chunked_raw(const GemmArgs &a, bool transA, bool transB, void *ws,
+template <class CFG, int RAW, class PT>
+cudaError_t launch_chunked_raw(const GemmArgs &a, const LayerEpi *le, bool transA, bool transB, void *ws,
                                size_t ws_bytes, cudaStream_t s, CUtensorMap &tmA,
                                CUtensorMap &tmB) {
     using P = Chunked<CFG>;
     static PerContext<bool> configured;
-    cudaError_t e = ensure_smem(tf32x3_chunked_kernel<CFG, RAW>, P::SMEM_BYTES, configured);
+    cudaError_t e = ensure_smem(tf32x3_chunked_kernel<CFG, RAW, PT>, P::SMEM_BYTES, configured);
     if (e != cudaSuccess) return e;
     int dev = 0, sms = 0;
     e = cudaGetDevice(&dev);
@@ -1739,9 +1765,10 @@ cudaError_t launch_chunked_raw(const GemmArgs &a, bool transA, bool transB, void
     e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
     CUtensorMap tmC, tmAlo, tmBlo;
-    Tf32x3Params p;
-    e = prepare<CFG>(a, transA, transB, RAW, 0, ws, s, tmA, tmB, tmAlo, tmBlo, tmC, p);
+    PT p;
+    e = prepare<CFG>(a, kLayer<PT>, transA, transB, RAW, 0, ws, s, tmA, tmB, tmAlo, tmBlo, tmC, p);
     if (e != cudaSuccess) return e;
+    if constexpr (kLayer<PT>) p.le = *le;
     p.kcb = g_chunk_k.load(std::memory_order_relaxed) / CFG::BK;
     // the partial tiles follow the planes; a workspace without room for them
     // keeps the whole-tile schedule
@@ -1770,7 +1797,7 @@ cudaError_t launch_chunked_raw(const GemmArgs &a, bool transA, bool transB, void
     CUtensorMap tmP = {};
     if (pl.split > 0 && !make_part_map(&tmP, p.part, pl.split * pl.tail, CFG::BN))
         return cudaErrorInvalidValue;
-    e = cudaLaunchKernelEx(&cfg, tf32x3_chunked_kernel<CFG, RAW>, tmA, tmB, tmAlo, tmBlo, tmC, tmP,
+    e = cudaLaunchKernelEx(&cfg, tf32x3_chunked_kernel<CFG, RAW, PT>, tmA, tmB, tmAlo, tmBlo, tmC, tmP,
                            p);
     if (e != cudaSuccess) return e;
     if (pl.split == 0) return cudaGetLastError();
@@ -1779,10 +1806,10 @@ cudaError_t launch_chunked_raw(const GemmArgs &a, bool transA, bool transB, void
     cfg.dynamicSmemBytes = 0;
     if ((long long)pl.tail * (BM * CFG::BN / 4096) >= sms) {
         cfg.gridDim = dim3((unsigned)(BM * CFG::BN / 4096), (unsigned)pl.tail);
-        e = cudaLaunchKernelEx(&cfg, tf32x3_fixup_kernel<CFG::BN, 4>, p);
+        e = cudaLaunchKernelEx(&cfg, tf32x3_fixup_kernel<CFG::BN, 4, PT>, p);
     } else {
         cfg.gridDim = dim3((unsigned)(BM * CFG::BN / 1024), (unsigned)pl.tail);
-        e = cudaLaunchKernelEx(&cfg, tf32x3_fixup_kernel<CFG::BN, 1>, p);
+        e = cudaLaunchKernelEx(&cfg, tf32x3_fixup_kernel<CFG::BN, 1, PT>, p);
     }
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
@@ -1793,8 +1820,8 @@ cudaError_t launch_chunked_raw(const GemmArgs &a, bool transA, bool transB, void
 // sectors, as in the planes (plane_row_floats).  On rows only 16-byte aligned
 // each slice straddles sectors, and the split kernel's planes are the cheaper
 // route (3000 x 2000 x 1500 with row-major A of ld 1500).
-template <class CFG>
-cudaError_t launch_chunked(const GemmArgs &a, bool transA, bool transB, void *ws, size_t ws_bytes,
+template <class CFG, class PT>
+cudaError_t launch_chunked(const GemmArgs &a, const LayerEpi *le, bool transA, bool transB, void *ws, size_t ws_bytes,
                            cudaStream_t s) {
     static_assert(CFG::PLANES == 2, "three terms");
     auto raw_ok = [&](const float *X, int64_t ld, int64_t sX, bool kcontig) {
@@ -1810,10 +1837,10 @@ cudaError_t launch_chunked(const GemmArgs &a, bool transA, bool transB, void *ws
         make_raw_map<CFG>(&tmB, a.B, a.N, a.K, a.ldb, a.strideB, a.batch, CFG::BN))
         raw |= 2;
     switch (raw) {
-        case 1: return launch_chunked_raw<CFG, 1>(a, transA, transB, ws, ws_bytes, s, tmA, tmB);
-        case 2: return launch_chunked_raw<CFG, 2>(a, transA, transB, ws, ws_bytes, s, tmA, tmB);
-        case 3: return launch_chunked_raw<CFG, 3>(a, transA, transB, ws, ws_bytes, s, tmA, tmB);
-        default: return launch_chunked_raw<CFG, 0>(a, transA, transB, ws, ws_bytes, s, tmA, tmB);
+        case 1: return launch_chunked_raw<CFG, 1, PT>(a, le, transA, transB, ws, ws_bytes, s, tmA, tmB);
+        case 2: return launch_chunked_raw<CFG, 2, PT>(a, le, transA, transB, ws, ws_bytes, s, tmA, tmB);
+        case 3: return launch_chunked_raw<CFG, 3, PT>(a, le, transA, transB, ws, ws_bytes, s, tmA, tmB);
+        default: return launch_chunked_raw<CFG, 0, PT>(a, le, transA, transB, ws, ws_bytes, s, tmA, tmB);
     }
 }
 
@@ -1905,18 +1932,55 @@ size_t tf32_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t batch) {
 // kernel (128-wide tiles, converter warps where they pay); longer ones the
 // K-chunked kernel, whose sums are promoted to round-to-nearest fp32 adds
 // every 128 of K, on the tile width the wave count favours.
+namespace {
+
+template <class PT>   // Tf32x3Params, or Tf32x3LayerParams with the layer epilogue `le`
+cudaError_t launch_three_terms(const GemmArgs &a, const LayerEpi *le, bool transA, bool transB,
+                               void *ws, size_t ws_bytes, cudaStream_t s) {
+    if (a.K <= tf32x3::kChunkMinK)
+        return tf32x3::launch_persistent<Tf32x3Narrow, 2, PT>(a, le, transA, transB, ws, s);
+    return tc_wide_tile(a, 3)
+               ? tf32x3::launch_chunked<Tf32x3Wide, PT>(a, le, transA, transB, ws, ws_bytes, s)
+               : tf32x3::launch_chunked<Tf32x3Narrow, PT>(a, le, transA, transB, ws, ws_bytes, s);
+}
+
+}  // namespace
+
 cudaError_t launch_tf32x3(const GemmArgs &a, bool transA, bool transB, void *ws, size_t ws_bytes,
                           cudaStream_t s) {
-    if (a.K <= tf32x3::kChunkMinK)
-        return tf32x3::launch_persistent<Tf32x3Narrow, 2>(a, transA, transB, ws, s);
-    return tc_wide_tile(a, 3)
-               ? tf32x3::launch_chunked<Tf32x3Wide>(a, transA, transB, ws, ws_bytes, s)
-               : tf32x3::launch_chunked<Tf32x3Narrow>(a, transA, transB, ws, ws_bytes, s);
+    return launch_three_terms<tf32x3::Tf32x3Params>(a, nullptr, transA, transB, ws, ws_bytes, s);
+}
+
+cudaError_t launch_linear_tf32x3(const float *X, int64_t ldx, const float *W, int64_t ldw,
+                                 bool transW, int K, const LayerEpi &epi, void *ws,
+                                 size_t ws_bytes, cudaStream_t s) {
+    GemmArgs a = {};
+    a.A = X;
+    a.B = W;
+    a.C = static_cast<float *>(epi.Y);
+    a.lda = ldx;
+    a.ldb = ldw;
+    a.ldc = epi.ldy;
+    a.M = epi.M;
+    a.N = epi.N;
+    a.K = K;
+    a.batch = 1;
+    a.group_m = raster_group();
+    a.alpha = 1.f;
+    // a layer without bias, activation, residual and stored z is the plain
+    // product, whose tiles leave by TMA store
+    const bool plain = epi.act == SGEMM_ACT_NONE && epi.bias == nullptr && epi.R == nullptr &&
+                       epi.Z == nullptr;
+    if (plain)
+        return launch_three_terms<tf32x3::Tf32x3Params>(a, nullptr, false, transW, ws, ws_bytes, s);
+    return launch_three_terms<tf32x3::Tf32x3LayerParams>(a, &epi, false, transW, ws, ws_bytes, s);
 }
 
 cudaError_t launch_tf32(const GemmArgs &a, bool transA, bool transB, void *ws, cudaStream_t s) {
-    return tc_wide_tile(a, 1) ? tf32x3::launch_persistent<Tf32Wide, 2>(a, transA, transB, ws, s)
-                              : tf32x3::launch_persistent<Tf32Narrow, 2>(a, transA, transB, ws, s);
+    using P = tf32x3::Tf32x3Params;
+    return tc_wide_tile(a, 1)
+               ? tf32x3::launch_persistent<Tf32Wide, 2, P>(a, nullptr, transA, transB, ws, s)
+               : tf32x3::launch_persistent<Tf32Narrow, 2, P>(a, nullptr, transA, transB, ws, s);
 }
 
 int set_tf32x3_chunk_k(int chunk_k) {

@@ -73,7 +73,8 @@ typedef enum {
     SGEMM_EINVAL_BATCH = 5,  /* batch < 0, or strideC lets two problems' C overlap */
     SGEMM_ELAUNCH = 6,       /* the kernel launch itself failed */
     SGEMM_EDEVICE = 7,       /* no usable device, or the device is not sm_103 */
-    SGEMM_EWORKSPACE = 8     /* workspace NULL, misaligned or smaller than required */
+    SGEMM_EWORKSPACE = 8,    /* workspace NULL, misaligned or smaller than required */
+    SGEMM_EINVAL_TYPE = 9    /* an element type or activation that the call does not take */
 } sgemm_status;
 
 /*
