@@ -13,6 +13,7 @@ import os
 import shutil
 import subprocess
 import sys
+import threading
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -64,6 +65,16 @@ def build(verbose: bool = False, ptxas_verbose: bool = False, jobs: int | None =
     """Compile every csrc/*.cu for sm_103a and link the shared library."""
     os.makedirs(BUILD, exist_ok=True)
     srcs = _sources()
+    # the torch binding compiles beside the kernels
+    layers_error: list = []
+
+    def build_layers():
+        try:
+            _build_layers(verbose)
+        except Exception as e:   # raised again by the caller's thread
+            layers_error.append(e)
+    layers = threading.Thread(target=build_layers)
+    layers.start()
     jobs = jobs or min(len(srcs), max(1, os.cpu_count() or 1))
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
         results = list(ex.map(lambda s: _compile(s, ptxas_verbose), srcs))
@@ -81,8 +92,44 @@ def build(verbose: bool = False, ptxas_verbose: bool = False, jobs: int | None =
         os.replace(LIB + ".tmp", LIB)
     if verbose:
         sys.stderr.write(f"built {LIB}\n")
+    layers.join()
+    if layers_error:
+        raise layers_error[0]
     _build_calls(verbose)
     return LIB
+
+
+def _build_layers(verbose: bool = False):
+    """Compile _layers.cpp, the torch binding of the layer operators (see that
+    file), next to the library.  Without torch nothing is built: the C ABI and
+    the other calls do not need it."""
+    import importlib.util
+    import sysconfig
+    if importlib.util.find_spec("torch") is None:
+        if verbose:
+            sys.stderr.write("note: no torch; its binding of the layer operators is not built\n")
+        return None
+    src = os.path.join(PKG, "_layers.cpp")
+    out = os.path.join(PKG, "_layers" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
+    newest = max(os.path.getmtime(f) for f in [src, *glob.glob(os.path.join(INCLUDE, "*.h"))])
+    if os.path.exists(out) and os.path.getmtime(out) >= newest:
+        return out
+    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    cmd = [shutil.which("c++") or shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared",
+           "-fPIC", "-Wall", "-I", sysconfig.get_paths()["include"], "-I", INCLUDE,
+           "-isystem", os.path.join(torch_dir, "include"),
+           "-isystem", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(cuda, "include"), src, "-o", out + ".tmp",
+           "-L", os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
+           "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"_layers.cpp did not build:\n{r.stdout}\n{r.stderr}")
+    os.replace(out + ".tmp", out)
+    if verbose:
+        sys.stderr.write(f"built {out}\n")
+    return out
 
 
 def _build_calls(verbose: bool = False):
