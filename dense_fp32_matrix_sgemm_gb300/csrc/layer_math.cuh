@@ -71,8 +71,15 @@ __device__ __forceinline__ void store_vec(T *p, const float (&x)[N]) {
 // ------------------------------------------------------------------ activations
 
 // 1 / (1 + exp(-t)).  exp(-t) overflows to infinity for t below about -88,
-// which gives the limit 0.
-__device__ __forceinline__ float sigmoid(float t) { return 1.f / (1.f + expf(-t)); }
+// which gives the limit 0.  T is the type that the result is rounded to: for
+// the 16-bit types the hardware's exponential and reciprocal (a few units of
+// 2^-23, plus |t| of them in the exponent) are far below its roundoff and take
+// a third of the instructions.
+template <class T>
+__device__ __forceinline__ float sigmoid(float t) {
+    if constexpr (sizeof(T) == 4) return 1.f / (1.f + expf(-t));
+    return __fdividef(1.f, 1.f + __expf(-t));
+}
 
 constexpr float kGeluC = 0.7978845608028654f;   // sqrt(2 / pi)
 constexpr float kGeluK = 0.044715f;
@@ -81,29 +88,55 @@ constexpr float kRsqrt2Pi = 0.3989422804014327f;   // 1 / sqrt(2 pi)
 
 // (1 + tanh u) / 2 = 1 / (1 + exp(-2u)), so the tanh form of GELU is z times
 // a sigmoid: one exponential and no cancellation near tanh u = -1.
+template <class T>
 __device__ __forceinline__ float activate(float z, int act) {
     switch (act) {
         case SGEMM_ACT_RELU: return z < 0.f ? 0.f : z;   // a NaN stays one
-        case SGEMM_ACT_GELU: return z * sigmoid(2.f * kGeluC * (z + kGeluK * z * z * z));
+        case SGEMM_ACT_GELU: return z * sigmoid<T>(2.f * kGeluC * (z + kGeluK * z * z * z));
         case SGEMM_ACT_GELU_ERF: return 0.5f * z * (1.f + erff(z * kSqrtHalf));
-        case SGEMM_ACT_SILU: return z * sigmoid(z);
+        case SGEMM_ACT_SILU: return z * sigmoid<T>(z);
         default: return z;
     }
 }
 
+// act of N values; the choice is made once, outside the loop over them.
+template <class T, int N>
+__device__ __forceinline__ void activate_all(float (&z)[N], int act) {
+    if (act == SGEMM_ACT_NONE) return;
+    switch (act) {
+        case SGEMM_ACT_RELU:
+#pragma unroll
+            for (int j = 0; j < N; ++j) z[j] = activate<T>(z[j], SGEMM_ACT_RELU);
+            break;
+        case SGEMM_ACT_GELU:
+#pragma unroll
+            for (int j = 0; j < N; ++j) z[j] = activate<T>(z[j], SGEMM_ACT_GELU);
+            break;
+        case SGEMM_ACT_GELU_ERF:
+#pragma unroll
+            for (int j = 0; j < N; ++j) z[j] = activate<T>(z[j], SGEMM_ACT_GELU_ERF);
+            break;
+        default:
+#pragma unroll
+            for (int j = 0; j < N; ++j) z[j] = activate<T>(z[j], SGEMM_ACT_SILU);
+            break;
+    }
+}
+
 // d act / dz.  With p = (1 + tanh u) / 2: (1 - tanh^2 u) / 2 = 2 p (1 - p).
+template <class T>
 __device__ __forceinline__ float activate_grad(float z, int act) {
     switch (act) {
         case SGEMM_ACT_RELU: return z > 0.f ? 1.f : 0.f;
         case SGEMM_ACT_GELU: {
             const float z2 = z * z;
-            const float p = sigmoid(2.f * kGeluC * (z + kGeluK * z2 * z));
+            const float p = sigmoid<T>(2.f * kGeluC * (z + kGeluK * z2 * z));
             return p + 2.f * kGeluC * z * p * (1.f - p) * (1.f + 3.f * kGeluK * z2);
         }
         case SGEMM_ACT_GELU_ERF:
             return 0.5f * (1.f + erff(z * kSqrtHalf)) + z * kRsqrt2Pi * expf(-0.5f * z * z);
         case SGEMM_ACT_SILU: {
-            const float p = sigmoid(z);
+            const float p = sigmoid<T>(z);
             return p * (1.f + z * (1.f - p));
         }
         default: return 1.f;
@@ -119,7 +152,7 @@ __device__ __forceinline__ void finish1(const LayerEpi &e, int row, int col, flo
     if (e.sx != nullptr) z *= e.sx[row] * e.sw[col];
     if (e.bias != nullptr) z += to_f32(static_cast<const T *>(e.bias)[col]);
     if (e.Z != nullptr) static_cast<T *>(e.Z)[row * e.ldz + col] = from_f32<T>(z);
-    float y = activate(z, e.act);
+    float y = activate<T>(z, e.act);
     if (e.R != nullptr) y += to_f32(static_cast<const T *>(e.R)[row * e.ldr + col]);
     static_cast<T *>(e.Y)[row * e.ldy + col] = from_f32<T>(y);
 }
@@ -149,15 +182,110 @@ __device__ __forceinline__ void finish(const LayerEpi &e, int row, int col, cons
         for (int j = 0; j < G; ++j) z[j] += to_f32(b.v[j]);
     }
     if (e.Z != nullptr) store_vec<T, G>(static_cast<T *>(e.Z) + row * e.ldz + col, z);
-    float y[G];
-#pragma unroll
-    for (int j = 0; j < G; ++j) y[j] = activate(z[j], e.act);
+    activate_all<T>(z, e.act);
     if (e.R != nullptr) {
         const Vec<T, G> r = load_vec<T, G>(static_cast<const T *>(e.R) + row * e.ldr + col);
 #pragma unroll
-        for (int j = 0; j < G; ++j) y[j] += to_f32(r.v[j]);
+        for (int j = 0; j < G; ++j) z[j] += to_f32(r.v[j]);
     }
-    store_vec<T, G>(static_cast<T *>(e.Y) + row * e.ldy + col, y);
+    store_vec<T, G>(static_cast<T *>(e.Y) + row * e.ldy + col, z);
+}
+
+// 16 values of a 16-bit type as one 32-byte access (aligned to it): a whole
+// sector each lane.
+__device__ __forceinline__ void load_32b(const void *p, uint32_t (&r)[8]) {
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                   "=r"(r[6]), "=r"(r[7])
+                 : "l"(p) : "memory");
+}
+__device__ __forceinline__ void store_32b(void *p, const uint32_t (&r)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                 :: "l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
+                    "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+template <class T>
+__device__ __forceinline__ uint32_t pack2(float a, float b);
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+template <class T>
+__device__ __forceinline__ float2 unpack2(uint32_t x);
+template <>
+__device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t x) {
+    return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+}
+template <>
+__device__ __forceinline__ float2 unpack2<__half>(uint32_t x) {
+    return __half22float2(*reinterpret_cast<const __half2 *>(&x));
+}
+
+// 32 whole columns col .. col + 31 of `row` (16-bit T), every matrix aligned
+// to 16 elements; `z` holds the accumulators on entry.  The residual's loads
+// are issued first.
+template <class T>
+__device__ __forceinline__ void finish32(const LayerEpi &e, int row, int col, float (&z)[32]) {
+    uint32_t r[2][8];
+    if (e.R != nullptr) {
+        const T *p = static_cast<const T *>(e.R) + row * e.ldr + col;
+        load_32b(p, r[0]);
+        load_32b(p + 16, r[1]);
+    }
+    if (e.sx != nullptr) {
+        const float sx = e.sx[row];
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+            const float4 sw = *reinterpret_cast<const float4 *>(e.sw + col + j);
+            z[j] *= sx * sw.x;
+            z[j + 1] *= sx * sw.y;
+            z[j + 2] *= sx * sw.z;
+            z[j + 3] *= sx * sw.w;
+        }
+    }
+    if (e.bias != nullptr) {
+        const T *p = static_cast<const T *>(e.bias) + col;
+#pragma unroll
+        for (int j = 0; j < 32; j += 8) {
+            const uint4 b = *reinterpret_cast<const uint4 *>(p + j);
+            const uint32_t w[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = unpack2<T>(w[i]);
+                z[j + 2 * i] += f.x;
+                z[j + 2 * i + 1] += f.y;
+            }
+        }
+    }
+    auto store = [&](T *p) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = pack2<T>(z[16 * h + 2 * i], z[16 * h + 2 * i + 1]);
+            store_32b(p + 16 * h, w);
+        }
+    };
+    if (e.Z != nullptr) store(static_cast<T *>(e.Z) + row * e.ldz + col);
+    activate_all<T>(z, e.act);
+    if (e.R != nullptr) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float2 f = unpack2<T>(r[h][i]);
+                z[16 * h + 2 * i] += f.x;
+                z[16 * h + 2 * i + 1] += f.y;
+            }
+    }
+    store(static_cast<T *>(e.Y) + row * e.ldy + col);
 }
 
 // ------------------------------------------------------------------ 8-bit rows

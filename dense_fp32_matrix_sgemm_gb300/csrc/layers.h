@@ -18,8 +18,9 @@ __host__ __device__ inline int dtype_size(int t) {
 // What happens to an accumulator on its way to memory:
 //   z = acc * (sx ? sx[row] * sw[col] : 1) + bias[col];  Z = z
 //   Y = act(z) + R
-// All of `type` elements except the scales.  vec: 8 or 4 when every base and
-// leading dimension is aligned to that many elements, else 1.
+// All of `type` elements except the scales.  vec: the most of 16 (16-bit types),
+// 8 (16-bit types), 4 and 1 elements that every base and leading dimension is
+// aligned to.
 struct LayerEpi {
     void *Y, *Z;
     const void *R, *bias;

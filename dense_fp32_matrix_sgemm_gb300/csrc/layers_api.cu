@@ -106,11 +106,14 @@ int vector_width(int type, const LayerEpi &e) {
     const int size = dtype_size(type);
     auto all = [&](int n) {
         const uintptr_t bytes = (uintptr_t)(n * size);
-        return aligned(e.Y, bytes) && e.ldy % n == 0 && aligned(e.bias, bytes) &&
+        // bias and scales: 16-byte accesses at most
+        const uintptr_t few = bytes < 16 ? bytes : 16;
+        return aligned(e.Y, bytes) && e.ldy % n == 0 && aligned(e.bias, few) &&
+               aligned(e.sw, n == 16 ? 16 : 4) &&
                (e.Z == nullptr || (aligned(e.Z, bytes) && e.ldz % n == 0)) &&
                (e.R == nullptr || (aligned(e.R, bytes) && e.ldr % n == 0));
     };
-    return size == 2 && all(8) ? 8 : all(4) ? 4 : 1;
+    return size == 2 && all(16) ? 16 : size == 2 && all(8) ? 8 : all(4) ? 4 : 1;
 }
 
 LayerEpi plain_epi(int type, void *Y, int64_t ldy, int64_t M, int64_t N) {

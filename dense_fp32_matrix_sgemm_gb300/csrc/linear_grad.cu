@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(kThreads) dz_kernel(const DzArgs a) {
 #pragma unroll
                 for (int j = 0; j < W; ++j) {
                     g[j] = to_f32(vy[u].v[j]);
-                    if (a.act != SGEMM_ACT_NONE) g[j] *= activate_grad(to_f32(vz[u].v[j]), a.act);
+                    if (a.act != SGEMM_ACT_NONE) g[j] *= activate_grad<T>(to_f32(vz[u].v[j]), a.act);
                     sum[j] += g[j];
                 }
                 if (a.dZ != nullptr) store_vec<T, W>(dz + row * a.lddz, g);

@@ -6,13 +6,11 @@
 // tcgen05.mma bounds it where all three sizes are large (2 M N K flops), HBM
 // where one of them is small.  A CTA computes 128 x BN tiles with warps in
 // three roles:
-//   warp 0, lane 0: TMA producer: 128 bytes of K of A's and B's rows a stage,
+//   warp 0:         TMA producer: 128 bytes of K of A's and B's rows a stage,
 //                   128-byte swizzle, a ring that runs on across tiles;
-//   warp 1, lane 0: MMA issuer (M128 N=BN, 32 bytes of K an instruction);
+//   warp 1:         MMA issuer (M128 N=BN, 32 bytes of K an instruction);
 //                   warp 1 owns tensor memory;
-//   warps 2-5:      epilogue: TMEM lane quarter warp % 4, 64 columns at a time
-//                   through the warp's own swizzled shared block, so global
-//                   accesses are 16 bytes a lane and whole 128-byte row pieces.
+//   warps 2-9:      epilogue: TMEM lane quarter warp % 4, half of the columns.
 // Operands may be K-major or (16-bit types) M/N-major in memory: the tensor
 // core's descriptors take both, so no operand is transposed.
 //   K-major:  box of 128 bytes of K x rows; 8-row groups 1024 bytes apart.
@@ -45,7 +43,8 @@ namespace sgemm {
 namespace ltc {
 
 constexpr int BM = 128;
-constexpr int kThreads = 192;       // producer, MMA issuer, 4 epilogue warps
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 64 + 32 * kEpiWarps;   // producer, MMA issuer, epilogue
 constexpr int kRowBytes = 128;      // of K in a stage
 constexpr int kBox = 8192;          // MN-major box: 64 k x 128 bytes
 
@@ -54,12 +53,11 @@ struct Shape {
     static constexpr int A_TILE = BM * kRowBytes;
     static constexpr int B_TILE = BN * kRowBytes;
     static constexpr int STAGE = A_TILE + B_TILE;
-    static constexpr int STAGES = 192 * 1024 / STAGE;
-    static constexpr int STAGING = 4 * 8192;   // an epilogue warp's 32 x 64 fp32 block
+    static constexpr int STAGES = 224 * 1024 / STAGE;
     static constexpr int ACCS = SPLIT ? 1 : 2;
     static constexpr int TMEM_COLS = ACCS * BN;
     static constexpr int BARS = 2 * STAGES + 2 * ACCS + 1;
-    static constexpr int SMEM = STAGES * STAGE + STAGING + 1024 + 256;
+    static constexpr int SMEM = STAGES * STAGE + 1024 + 256;
     static_assert(TMEM_COLS >= 32 && TMEM_COLS <= 512, "tensor memory");
     static_assert(BARS * 8 + 8 <= 256, "barrier area");
     static_assert(SMEM <= 227 * 1024, "shared memory budget");
@@ -76,6 +74,45 @@ struct Params {
     int fp8;
     unsigned *error;
 };
+
+// True in one lane of a converged warp.  The producer and the MMA issuer run
+// their loops with the whole warp and let this lane issue, so that the
+// compiler keeps descriptors and coordinates in uniform registers; in loops
+// that a single lane runs it cannot, and an MMA then took about 226 clocks to
+// issue, against the 128 that it runs (4096 x 8192 x 4096: @ISSUE@).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// Position in a ring of N stages: the stage, the parity of its current round,
+// and how many stages have been used so far (up to N).
+template <int N>
+struct Ring {
+    int s = 0, parity = 0, used = 0;
+    __device__ __forceinline__ void next() {
+        if (used < N) ++used;
+        if (++s == N) {
+            s = 0;
+            parity ^= 1;
+        }
+    }
+};
+
+// Waits (bounded) until the latest fill of every used stage has landed: a CTA
+// that gave up does not leave with copies in flight.
+template <int N>
+__device__ __forceinline__ void drain_ring(const Ring<N> &r, uint32_t full0) {
+    for (int s = 0; s < r.used; ++s) {
+        const int parity = s < r.s ? r.parity : r.parity ^ 1;
+        const long long t0 = clock64();
+        while (!tc::mbar_try_wait(full0 + 8 * s, parity) &&
+               clock64() - t0 < tc::kWaitLimitCycles) {
+        }
+    }
+}
 
 // 2-D tiled load of the box at (c0, c1); c0 (innermost) a multiple of 16 bytes.
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void *tmap, uint32_t bar, int c0,
@@ -115,13 +152,6 @@ __device__ __forceinline__ void mma_f8(uint32_t tmem_d, uint64_t adesc, uint64_t
                  : "memory");
 }
 
-__device__ __forceinline__ float4 ld_shared_v4(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
-    return v;
-}
-
 __device__ __forceinline__ void raster(const Params &p, int t, int &tm, int &tn) {
     const int group = p.group_m * p.tiles_n;
     const int g = t / group;
@@ -132,42 +162,36 @@ __device__ __forceinline__ void raster(const Params &p, int t, int &tm, int &tn)
     tn = r / rows;
 }
 
-// Finishes the 32 tile rows of TMEM lane quarter q, all columns.  Each 64
-// columns pass through the warp's block at `stage` (256-byte rows; 16-byte
-// chunk c of row r at c ^ (r & 7)): written a row a lane, read back as four
-// rows an instruction, eight columns a lane.  The lane's two chunks are read
-// in an order that keeps a quarter-warp on distinct banks.
-template <int BN, class O>
+// Finishes COLS columns of the 32 tile rows of TMEM lane quarter q, a row a
+// lane: the accumulators stay in registers from tensor memory to the store.
+// Global accesses are 32 bytes a lane, whole sectors of one row each, so they
+// need no exchange between lanes.  (Turning the tile through shared memory
+// first, for accesses along a row, took 71 us of the 4096 x 8192 outputs of a
+// plain product, and 199 with GELU and stored z, against @FIN@ now.)
+template <int COLS, class O>
 __device__ __forceinline__ void finish_rows(const LayerEpi &e, uint32_t acc, int q, int lane,
-                                            int m0, int n0, uint32_t stage) {
+                                            int m0, int n0) {
     const int row0 = m0 + 32 * q;
     if (row0 >= e.M) return;
+    const int row = row0 + lane;
     const uint32_t lane_base = acc + ((uint32_t)(32 * q) << 16);
 #pragma unroll 1
-    for (int c = 0; c < BN / 64 && n0 + 64 * c < e.N; ++c) {
-        __syncwarp();   // the previous block has been read
+    for (int c = 0; c < COLS / 32 && n0 + 32 * c < e.N; ++c) {
+        const int col = n0 + 32 * c;
+        float v[32];
+        __syncwarp();   // the load is warp-collective
+        tc::tmem_ld_32(lane_base + (uint32_t)(32 * c), v);
+        if (row >= e.M) continue;
+        if (e.vec == 16 && col + 32 <= e.N) {
+            finish32<O>(e, row, col, v);
+        } else {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            float v[32];
-            tc::tmem_ld_32(lane_base + (uint32_t)(64 * c + 32 * h), v);
+            for (int j = 0; j < 32; j += 8) {
+                float w[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                tc::st_shared_v4(stage + (uint32_t)lane * 256u +
-                                     ((uint32_t)((8 * h + j) ^ (lane & 7)) << 4),
-                                 v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-        }
-        __syncwarp();
-        const int l = lane & 7, odd = l >> 2;
-        const int col = n0 + 64 * c + 8 * l;
-#pragma unroll 2
-        for (int i = 0; i < 8; ++i) {
-            const int r = 4 * i + (lane >> 3);
-            const uint32_t base = stage + (uint32_t)r * 256u;
-            const float4 a = ld_shared_v4(base + ((uint32_t)((2 * l + odd) ^ (r & 7)) << 4));
-            const float4 b = ld_shared_v4(base + ((uint32_t)((2 * l + 1 - odd) ^ (r & 7)) << 4));
-            const float4 lo = odd ? b : a, hi = odd ? a : b;
-            const float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-            if (row0 + r < e.M && col < e.N) finish<O, 8>(e, row0 + r, col, v);
+                for (int i = 0; i < 8; ++i) w[i] = v[j + i];
+                if (col + j < e.N) finish<O, 8>(e, row, col + j, w);
+            }
         }
     }
 }
@@ -182,8 +206,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     const uint32_t raw_addr = tc::smem_u32_generic(smem_raw);
     uint8_t *smem = smem_raw + ((1024 - (raw_addr & 1023)) & 1023);
     const uint32_t ring = tc::smem_u32_generic(smem);
-    const uint32_t staging = ring + STAGES * S::STAGE;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + STAGES * S::STAGE + S::STAGING);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + STAGES * S::STAGE);
     const uint32_t full0 = tc::smem_u32_generic(bars);
     const uint32_t empty0 = full0 + 8 * STAGES;
     const uint32_t accf0 = empty0 + 8 * STAGES;   // accumulator b holds a finished tile
@@ -213,7 +236,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         }
         for (int b = 0; b < ACCS; ++b) {
             tc::mbar_init(accf0 + 8 * b, 1);
-            tc::mbar_init(acce0 + 8 * b, 4);   // one arrival an epilogue warp
+            tc::mbar_init(acce0 + 8 * b, kEpiWarps);
         }
         tc::mbar_init(done_bar, 1);
         *abort_flag = 0;
@@ -230,96 +253,99 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     pdl_wait();   // nothing below touches global memory before earlier work has finished
 
     if (warp == 0) {
-        if (lane == 0) {
+        {
             // ---------------- TMA producer
             const int bk = p.fp8 ? 128 : 64;
             const uint32_t tx = (uint32_t)(p.a_bytes + S::B_TILE);
-            long long g = 0;
+            Ring<STAGES> r;
             bool stop = false;
             for (int i = 0; i < ntiles && !stop; ++i) {
                 int tm, tn;
                 raster(p, first + i * stride, tm, tn);
                 const int m0 = tm * BM, n0 = tn * BN;
-                for (int kb = kb0; kb < kb1; ++kb, ++g) {
-                    const int s = (int)(g % STAGES);
-                    if (g >= STAGES &&
-                        !tc::mbar_wait(empty0 + 8 * s, (int)((g / STAGES) & 1) ^ 1, abort_flag)) {
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    bool ok = true;
+                    if (r.used == STAGES)
+                        ok = tc::mbar_wait(empty0 + 8 * r.s, r.parity ^ 1, abort_flag);
+                    if (!__all_sync(0xffffffffu, ok && !*abort_flag)) {
                         stop = true;
                         break;
                     }
-                    if (*abort_flag) {
-                        stop = true;
-                        break;
-                    }
-                    const uint32_t st = ring + s * S::STAGE, fb = full0 + 8 * s;
-                    tc::mbar_arrive_expect_tx(fb, tx);
+                    const uint32_t st = ring + r.s * S::STAGE, fb = full0 + 8 * r.s;
                     const int k0 = kb * bk;
-                    if (p.a_kmajor) {
-                        tma_load_2d(st, &tmA, fb, k0, m0);
-                    } else {
+                    if (elect_one()) {
+                        tc::mbar_arrive_expect_tx(fb, tx);
+                        if (p.a_kmajor) {
+                            tma_load_2d(st, &tmA, fb, k0, m0);
+                        } else {
 #pragma unroll
-                        for (int c = 0; c < BM / 64; ++c)
-                            tma_load_2d(st + c * kBox, &tmA, fb, m0 + 64 * c, k0);
-                    }
-                    if (p.b_kmajor) {
-                        tma_load_2d(st + S::A_TILE, &tmB, fb, k0, n0);
-                    } else {
+                            for (int c = 0; c < BM / 64; ++c)
+                                tma_load_2d(st + c * kBox, &tmA, fb, m0 + 64 * c, k0);
+                        }
+                        if (p.b_kmajor) {
+                            tma_load_2d(st + S::A_TILE, &tmB, fb, k0, n0);
+                        } else {
 #pragma unroll
-                        for (int c = 0; c < BN / 64; ++c)
-                            tma_load_2d(st + S::A_TILE + c * kBox, &tmB, fb, n0 + 64 * c, k0);
+                            for (int c = 0; c < BN / 64; ++c)
+                                tma_load_2d(st + S::A_TILE + c * kBox, &tmB, fb, n0 + 64 * c, k0);
+                        }
                     }
+                    __syncwarp();
+                    r.next();
                 }
             }
-            if (*abort_flag) {
-                // the latest fill of every stage lands before the CTA exits
-                for (long long f = (g > STAGES ? g - STAGES : 0); f < g; ++f) {
-                    const int s = (int)(f % STAGES);
-                    const long long t0 = clock64();
-                    while (!tc::mbar_try_wait(full0 + 8 * s, (int)((f / STAGES) & 1)) &&
-                           clock64() - t0 < tc::kWaitLimitCycles) {
-                    }
-                }
-            }
+            if (*abort_flag) drain_ring(r, full0);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
+        {
             // ---------------- MMA issuer
             const uint64_t astep = p.a_kmajor ? 2 : 128, bstep = p.b_kmajor ? 2 : 128;
-            long long g = 0;
+            Ring<STAGES> r;
             bool stop = false;
             for (int i = 0; i < ntiles && !stop; ++i) {
                 const int b = i % ACCS, u = i / ACCS;
-                if (i >= ACCS && !tc::mbar_wait(acce0 + 8 * b, (u - 1) & 1, abort_flag)) break;
+                bool ok = true;
+                if (i >= ACCS) ok = tc::mbar_wait(acce0 + 8 * b, (u - 1) & 1, abort_flag);
+                if (!__all_sync(0xffffffffu, ok)) break;
                 tc::fence_after_sync();
                 const uint32_t acc = tmem + (uint32_t)(b * BN);
-                for (int kb = 0; kb < nk; ++kb, ++g) {
-                    const int s = (int)(g % STAGES);
-                    if (!tc::mbar_wait(full0 + 8 * s, (int)((g / STAGES) & 1), abort_flag)) {
+                for (int kb = 0; kb < nk; ++kb) {
+                    ok = tc::mbar_wait(full0 + 8 * r.s, r.parity, abort_flag);
+                    if (!__all_sync(0xffffffffu, ok)) {
                         stop = true;
                         break;
                     }
                     tc::fence_after_sync();
-                    const uint32_t st = ring + s * S::STAGE;
+                    const uint32_t st = ring + r.s * S::STAGE;
                     const uint64_t ad = p.a_kmajor ? tc::kmajor_desc<128>(st) : mnmajor_desc(st);
                     const uint64_t bd = p.b_kmajor ? tc::kmajor_desc<128>(st + S::A_TILE)
                                                    : mnmajor_desc(st + S::A_TILE);
+                    if (elect_one()) {
+                        if (p.fp8) {
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        const uint32_t more = (kb | kk) ? 1u : 0u;
-                        if (p.fp8)
-                            mma_f8(acc, ad + kk * astep, bd + kk * bstep, p.idesc, more);
-                        else
-                            mma_f16(acc, ad + kk * astep, bd + kk * bstep, p.idesc, more);
+                            for (int kk = 0; kk < 4; ++kk)
+                                mma_f8(acc, ad + kk * astep, bd + kk * bstep, p.idesc,
+                                       (kb | kk) ? 1u : 0u);
+                        } else {
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                mma_f16(acc, ad + kk * astep, bd + kk * bstep, p.idesc,
+                                        (kb | kk) ? 1u : 0u);
+                        }
+                        tc::mma_commit(empty0 + 8 * r.s);
+                        if (kb + 1 == nk) tc::mma_commit(accf0 + 8 * b);
                     }
-                    tc::mma_commit(empty0 + 8 * s);
+                    __syncwarp();
+                    r.next();
                 }
-                if (!stop) tc::mma_commit(accf0 + 8 * b);
             }
-            tc::mma_commit(done_bar);   // tracks every MMA issued above, also on abort
+            // tracks every MMA issued above, also on abort
+            if (elect_one()) tc::mma_commit(done_bar);
+            __syncwarp();
         }
     } else {
         // ---------------- epilogue
-        const int q = warp & 3;
+        const int q = warp & 3, half = (warp - 2) >> 2;
         for (int i = 0; i < ntiles; ++i) {
             const int b = i % ACCS, u = i / ACCS;
             const bool ok = tc::mbar_wait(accf0 + 8 * b, u & 1, abort_flag);
@@ -337,7 +363,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                 if (tm * BM + 32 * q < p.epi.M) {
                     const int r = 32 * q + lane;
 #pragma unroll 1
-                    for (int c = 0; c < BN / 32; ++c) {
+                    for (int c = half * (BN / 64); c < (half + 1) * (BN / 64); ++c) {
                         float v[32];
                         tc::tmem_ld_32(acc + ((uint32_t)(32 * q) << 16) + (uint32_t)(32 * c), v);
 #pragma unroll
@@ -348,8 +374,8 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                     }
                 }
             } else {
-                finish_rows<BN, O>(p.epi, acc, q, lane, tm * BM, tn * BN,
-                                   staging + (uint32_t)(warp - 2) * 8192u);
+                finish_rows<BN / 2, O>(p.epi, acc + (uint32_t)(half * (BN / 2)), q, lane, tm * BM,
+                                       tn * BN + half * (BN / 2));
             }
             tc::fence_before_sync();   // the TMEM loads above precede the release
             __syncwarp();
@@ -391,6 +417,270 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     }
 }
 
+// ------------------------------------------------------------------ CTA pairs
+
+// 256 x 256 tiles by pairs of CTAs (cta_group::2).  Each CTA of the pair holds
+// 128 rows of A and 128 of B's 256 rows a stage (32 KB) and the 128 rows of
+// the result that are its own, over all 256 columns (two accumulators fill its
+// tensor memory).  One MMA of the even CTA reads both halves, so a CTA takes in
+// 32 KB for the 2 x 128 x 256 x 64 flops of a stage instead of the 48 KB that a
+// 128 x 256 tile of its own needs: at the tensor cores' rate 64 bytes a clock
+// instead of 96, which L2 can deliver.
+// Barriers:
+//   full (in the even CTA): both CTAs' copies complete on it; the even CTA's
+//     producer expects the bytes of both;
+//   empty, accumulator full (one in each CTA): completed in both by the even
+//     CTA's commits;
+//   accumulator empty (in the even CTA): one arrival of each of the pair's
+//     sixteen epilogue warps.
+// Waits are bounded as above.  A CTA whose wait runs out stops; its peer's
+// waits then run out too, the even CTA waits for every copy in flight, and
+// both meet at the closing cluster barrier, so neither leaves while the other
+// may still write to its shared memory.
+struct Pair {
+    static constexpr int BN = 256;
+    static constexpr int A_TILE = BM * kRowBytes;
+    static constexpr int STAGE = 2 * A_TILE;
+    static constexpr int STAGES = 7;
+    static constexpr int BARS = 2 * STAGES + 4 + 1;
+    static constexpr int SMEM = STAGES * STAGE + 1024 + 256;
+    static_assert(BARS * 8 + 8 <= 256, "barrier area");
+    static_assert(SMEM <= 227 * 1024, "shared memory budget");
+};
+
+// The shared::cluster address of `addr` (shared::cta) in the cluster's CTA 0.
+__device__ __forceinline__ uint32_t leader_addr(uint32_t addr) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+    return r;
+}
+
+// As tma_load_2d, into this CTA's shared memory, completing on a barrier in
+// either CTA of the pair (shared::cluster address).
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void *tmap, uint32_t bar,
+                                                 int c0, int c1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];"
+        :: "r"(dst), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c0), "r"(c1)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_f16_pair(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
+                                             uint32_t idesc, uint32_t accumulate) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                 :: "r"(tmem_d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+                 : "memory");
+}
+
+__device__ __forceinline__ void mma_f8_pair(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
+                                            uint32_t idesc, uint32_t accumulate) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+                 :: "r"(tmem_d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+                 : "memory");
+}
+
+// Arrive on the barrier at `bar` in both CTAs once every MMA issued so far by
+// this thread has completed.
+__device__ __forceinline__ void commit_pair(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster"
+                 ".multicast::cluster.b64 [%0], %1;"
+                 :: "r"(bar), "h"((uint16_t)3) : "memory");
+}
+
+__device__ __forceinline__ void arrive_cluster(uint32_t cluster_bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];"
+                 :: "r"(cluster_bar) : "memory");
+}
+
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t slot_smem, uint32_t ncols) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
+                 :: "r"(slot_smem), "r"(ncols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;"
+                 :: "r"(taddr), "r"(ncols) : "memory");
+}
+
+// p.tiles_m counts rows of 256, p.a_bytes is unused.
+template <class O>
+__global__ void __launch_bounds__(kThreads, 1)
+linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                   const Params p) {
+    constexpr int STAGES = Pair::STAGES, ACCS = 2, BN = Pair::BN;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const uint32_t raw_addr = tc::smem_u32_generic(smem_raw);
+    uint8_t *smem = smem_raw + ((1024 - (raw_addr & 1023)) & 1023);
+    const uint32_t ring = tc::smem_u32_generic(smem);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + STAGES * Pair::STAGE);
+    const uint32_t full0 = tc::smem_u32_generic(bars);
+    const uint32_t empty0 = full0 + 8 * STAGES;
+    const uint32_t accf0 = empty0 + 8 * STAGES;
+    const uint32_t acce0 = accf0 + 8 * ACCS;
+    const uint32_t done_bar = acce0 + 8 * ACCS;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + Pair::BARS);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)cluster_rank();
+    const int total = p.tiles_m * p.tiles_n;
+    const int first = (int)blockIdx.x / 2, stride = (int)gridDim.x / 2;
+    const int ntiles = first < total ? (total - 1 - first) / stride + 1 : 0;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            tc::mbar_init(full0 + 8 * s, 1);
+            tc::mbar_init(empty0 + 8 * s, 1);
+        }
+        for (int b = 0; b < ACCS; ++b) {
+            tc::mbar_init(accf0 + 8 * b, 1);
+            tc::mbar_init(acce0 + 8 * b, 2 * kEpiWarps);
+        }
+        tc::mbar_init(done_bar, 1);
+        *abort_flag = 0;
+        tc::fence_barrier_init();
+        tc::tma_prefetch_desc(&tmA);
+        tc::tma_prefetch_desc(&tmB);
+    }
+    if (warp == 1) tmem_alloc_pair(tc::smem_u32_generic(tmem_slot), ACCS * BN);
+    tc::fence_before_sync();
+    __syncthreads();
+    cluster_sync();   // both CTAs' barriers are initialised
+    tc::fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    pdl_trigger();
+    pdl_wait();   // nothing below touches global memory before earlier work has finished
+
+    if (warp == 0) {
+        {
+            // ---------------- TMA producer: this CTA's halves of A and B
+            const int bk = p.fp8 ? 128 : 64;
+            const uint32_t full_leader = leader_addr(full0);
+            Ring<STAGES> r;
+            bool stop = false;
+            for (int i = 0; i < ntiles && !stop; ++i) {
+                int tm, tn;
+                raster(p, first + i * stride, tm, tn);
+                const int m0 = tm * 2 * BM + rank * BM, n0 = tn * BN + rank * (BN / 2);
+                for (int kb = 0; kb < p.kblocks; ++kb) {
+                    bool ok = true;
+                    if (r.used == STAGES)
+                        ok = tc::mbar_wait(empty0 + 8 * r.s, r.parity ^ 1, abort_flag);
+                    if (!__all_sync(0xffffffffu, ok && !*abort_flag)) {
+                        stop = true;
+                        break;
+                    }
+                    const uint32_t st = ring + r.s * Pair::STAGE, fb = full_leader + 8 * r.s;
+                    const int k0 = kb * bk;
+                    if (elect_one()) {
+                        if (rank == 0) tc::mbar_arrive_expect_tx(full0 + 8 * r.s, 2 * Pair::STAGE);
+                        if (p.a_kmajor) {
+                            tma_load_2d_pair(st, &tmA, fb, k0, m0);
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < 2; ++c)
+                                tma_load_2d_pair(st + c * kBox, &tmA, fb, m0 + 64 * c, k0);
+                        }
+                        if (p.b_kmajor) {
+                            tma_load_2d_pair(st + Pair::A_TILE, &tmB, fb, k0, n0);
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < 2; ++c)
+                                tma_load_2d_pair(st + Pair::A_TILE + c * kBox, &tmB, fb,
+                                                 n0 + 64 * c, k0);
+                        }
+                    }
+                    __syncwarp();
+                    r.next();
+                }
+            }
+            // both CTAs' copies, before the pair leaves
+            if (rank == 0 && *abort_flag) drain_ring(r, full0);
+        }
+    } else if (warp == 1) {
+        if (rank == 0) {
+            // ---------------- MMA issuer, for both CTAs
+            const uint64_t astep = p.a_kmajor ? 2 : 128, bstep = p.b_kmajor ? 2 : 128;
+            Ring<STAGES> r;
+            bool stop = false;
+            for (int i = 0; i < ntiles && !stop; ++i) {
+                const int b = i % ACCS, u = i / ACCS;
+                bool ok = true;
+                if (i >= ACCS) ok = tc::mbar_wait(acce0 + 8 * b, (u - 1) & 1, abort_flag);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                tc::fence_after_sync();
+                const uint32_t acc = tmem + (uint32_t)(b * BN);
+                for (int kb = 0; kb < p.kblocks; ++kb) {
+                    ok = tc::mbar_wait(full0 + 8 * r.s, r.parity, abort_flag);
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        stop = true;
+                        break;
+                    }
+                    tc::fence_after_sync();
+                    const uint32_t st = ring + r.s * Pair::STAGE;
+                    const uint64_t ad = p.a_kmajor ? tc::kmajor_desc<128>(st) : mnmajor_desc(st);
+                    const uint64_t bd = p.b_kmajor ? tc::kmajor_desc<128>(st + Pair::A_TILE)
+                                                   : mnmajor_desc(st + Pair::A_TILE);
+                    if (elect_one()) {
+                        if (p.fp8) {
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                mma_f8_pair(acc, ad + kk * astep, bd + kk * bstep, p.idesc,
+                                       (kb | kk) ? 1u : 0u);
+                        } else {
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                mma_f16_pair(acc, ad + kk * astep, bd + kk * bstep, p.idesc,
+                                        (kb | kk) ? 1u : 0u);
+                        }
+                        commit_pair(empty0 + 8 * r.s);
+                        if (kb + 1 == p.kblocks) commit_pair(accf0 + 8 * b);
+                    }
+                    __syncwarp();
+                    r.next();
+                }
+            }
+            // tracks every MMA issued above, also on abort
+            if (elect_one()) commit_pair(done_bar);
+            __syncwarp();
+        }
+    } else {
+        // ---------------- epilogue: this CTA's 128 rows
+        const int q = warp & 3, half = (warp - 2) >> 2;
+        for (int i = 0; i < ntiles; ++i) {
+            const int b = i % ACCS, u = i / ACCS;
+            const bool ok = tc::mbar_wait(accf0 + 8 * b, u & 1, abort_flag);
+            __syncwarp();
+            if (!__all_sync(0xffffffffu, ok && !*abort_flag)) break;
+            tc::fence_after_sync();
+            int tm, tn;
+            raster(p, first + i * stride, tm, tn);
+            finish_rows<BN / 2, O>(p.epi, tmem + (uint32_t)(b * BN + half * (BN / 2)), q, lane,
+                                   tm * 2 * BM + rank * BM, tn * BN + half * (BN / 2));
+            tc::fence_before_sync();   // the TMEM loads above precede the release
+            __syncwarp();
+            if (lane == 0) arrive_cluster(leader_addr(acce0 + 8 * b));
+        }
+    }
+    __syncwarp();
+
+    tc::fence_before_sync();
+    __syncthreads();
+    if (*abort_flag && threadIdx.x == 0 && p.error != nullptr) atomicOr(p.error, 1u);
+    if (warp == 1) {
+        // every MMA issued has completed before TMEM is freed
+        int local_abort = 0;
+        (void)tc::mbar_wait(done_bar, 0, &local_abort);
+        tc::fence_after_sync();
+    }
+    cluster_sync();   // the pair leaves together
+    if (warp == 1) tmem_dealloc_pair(tmem, ACCS * BN);
+}
+
 // ------------------------------------------------------------------ host side
 
 CUtensorMapDataType map_type(int type) {
@@ -414,10 +704,10 @@ bool make_map(CUtensorMap *map, const TcOperand &o, int type, int rows, int K, i
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-uint32_t instruction_desc(int type, int bn, bool a_kmajor, bool b_kmajor) {
+uint32_t instruction_desc(int type, int bm, int bn, bool a_kmajor, bool b_kmajor) {
     const uint32_t fmt = type == SGEMM_BF16 ? 1u : 0u;   // f16 and e4m3: 0
     return (1u << 4) | (fmt << 7) | (fmt << 10) | ((a_kmajor ? 0u : 1u) << 15) |
-           ((b_kmajor ? 0u : 1u) << 16) | ((uint32_t)(bn >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
+           ((b_kmajor ? 0u : 1u) << 16) | ((uint32_t)(bn >> 3) << 17) | ((uint32_t)(bm >> 4) << 24);
 }
 
 template <int BN, class O, bool SPLIT>
@@ -447,7 +737,7 @@ cudaError_t launch(int type, const TcOperand &A, const TcOperand &B, int K, cons
     // whatever the stage held; they are computed and not stored)
     const int a_rows = epi.M < BM ? (epi.M + 7) / 8 * 8 : BM;
     p.a_bytes = A.kmajor ? a_rows * kRowBytes : S::A_TILE;
-    p.idesc = instruction_desc(type, BN, A.kmajor, B.kmajor);
+    p.idesc = instruction_desc(type, BM, BN, A.kmajor, B.kmajor);
     p.fp8 = type == SGEMM_E4M3;
     p.error = device_error_word();
     CUtensorMap tmA, tmB;
@@ -469,6 +759,71 @@ cudaError_t launch(int type, const TcOperand &A, const TcOperand &B, int K, cons
     cfg.attrs = attr;
     cfg.numAttrs = SPLIT ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, linear_tc_kernel<BN, O, SPLIT>, tmA, tmB, p);
+}
+
+// Clusters of two linear_pair_kernel CTAs that the device holds at once (an
+// SM without a partner in its group of SMs holds none).
+template <class O>
+cudaError_t pair_capacity(int &pairs) {
+    static PerContext<int> cached;
+    const unsigned long long ctx = current_context_id();
+    if (cached.get(ctx, pairs)) return cudaSuccess;
+    cudaError_t e = cudaFuncSetAttribute(linear_pair_kernel<O>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, Pair::SMEM);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Pair::SMEM;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(&pairs, linear_pair_kernel<O>, &cfg);
+    if (e != cudaSuccess) return e;
+    if (pairs < 1) return cudaErrorInvalidConfiguration;
+    cached.put(current_context_id(), pairs);
+    return cudaSuccess;
+}
+
+template <class O>
+cudaError_t launch_pair(int type, const TcOperand &A, const TcOperand &B, int K,
+                        const LayerEpi &epi, int pairs, cudaStream_t s) {
+    Params p;
+    p.epi = epi;
+    const int bk = kRowBytes / dtype_size(type);
+    p.kblocks = (K + bk - 1) / bk;
+    p.tiles_m = (epi.M + 2 * BM - 1) / (2 * BM);
+    p.tiles_n = (epi.N + Pair::BN - 1) / Pair::BN;
+    p.group_m = raster_group();
+    p.a_kmajor = A.kmajor;
+    p.b_kmajor = B.kmajor;
+    p.a_bytes = 0;
+    p.idesc = instruction_desc(type, 2 * BM, Pair::BN, A.kmajor, B.kmajor);
+    p.fp8 = type == SGEMM_E4M3;
+    p.error = device_error_word();
+    CUtensorMap tmA, tmB;
+    if (!make_map(&tmA, A, type, epi.M, K, BM) || !make_map(&tmB, B, type, epi.N, K, Pair::BN / 2))
+        return cudaErrorInvalidValue;
+    const long long tiles = (long long)p.tiles_m * p.tiles_n;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs)));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Pair::SMEM;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, linear_pair_kernel<O>, tmA, tmB, p);
 }
 
 template <class O>
@@ -496,10 +851,15 @@ cudaError_t dispatch(int type, const TcOperand &A, const TcOperand &B, int K, co
             return launch<64, O, true>(type, A, B, K, epi, n64, sms, s);
         return launch<128, O, true>(type, A, B, K, epi, n128, sms, s);
     }
-    // waves of one tile an SM; a 256-wide tile costs about 1.7 128-wide ones
-    const double wide = 1.7 * (double)((tiles(256) + sms - 1) / sms);
+    // waves of one tile an SM or a pair; a pair's 256 x 256 tile is four 128 x
+    // 128 ones on two SMs
+    int pairs = 0;
+    e = pair_capacity<O>(pairs);
+    if (e != cudaSuccess) return e;
+    const long long t256 = (long long)((epi.M + 255) / 256) * ((epi.N + 255) / 256);
+    const double wide = 1.4 * (double)((t256 + pairs - 1) / pairs);
     const double narrow = (double)((tiles(128) + sms - 1) / sms);
-    return wide <= narrow ? launch<256, O, false>(type, A, B, K, epi, 1, sms, s)
+    return wide <= narrow ? launch_pair<O>(type, A, B, K, epi, pairs, s)
                           : launch<128, O, false>(type, A, B, K, epi, 1, sms, s);
 }
 

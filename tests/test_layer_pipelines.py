@@ -1,0 +1,140 @@
+"""CPU models of the linear layer's tensor-core pipelines (csrc/linear_tc.cu)
+under random interleavings, with the stage, phase and parity arithmetic of the
+kernels; barriers and the interleaver are those of test_pipeline_protocols.
+
+  * linear_pair_kernel: two CTAs, each with a producer and eight epilogue warps;
+    the even CTA's issuer works for both.  "full" lives in the even CTA and
+    completes with its expectation and both CTAs' copies; "empty" and
+    "accumulator full" exist in each CTA and are completed in both by the
+    issuer's commits; "accumulator empty" takes sixteen arrivals.
+  * linear_tc_kernel's split schedule: every K block of every tile belongs to
+    exactly one CTA of the tile's cluster, and the closing reduction reads every
+    part of every element once.
+"""
+import random
+
+import pytest
+
+from test_pipeline_protocols import Barrier, interleave
+
+
+def pair_pipeline(tiles, kblocks, stages, accs, seed, plant=None):
+    rng = random.Random(seed)
+    full = [Barrier(3, f"full{s}") for s in range(stages)]            # expectation + two copies
+    empty = [[Barrier(1, f"empty{c}.{s}") for s in range(stages)] for c in range(2)]
+    accf = [[Barrier(1, f"accf{c}.{b}") for b in range(accs)] for c in range(2)]
+    acce = [Barrier(16, f"acce{b}") for b in range(accs)]
+    ring = [[None] * stages for _ in range(2)]      # slice held by a stage of a CTA
+    busy = [[0] * stages for _ in range(2)]         # MMAs still to read it
+    acc = [None] * accs                              # tile held by an accumulator
+    readers = [set() for _ in range(accs)]
+    done = []
+
+    def producer(c):
+        g = 0
+        for _ in range(tiles):
+            for _ in range(kblocks):
+                s = g % stages
+                if g >= stages and plant != "no empty wait":
+                    while not empty[c][s].passed(g // stages - 1):
+                        yield
+                assert not busy[c][s], "a stage is refilled while an MMA still reads it"
+                if c == 0:
+                    full[s].arrive()
+                    yield
+                ring[c][s] = g
+                yield
+                full[s].arrive()
+                g += 1
+                yield
+
+    def issuer():
+        g = 0
+        commits = []
+        for i in range(tiles):
+            b, u = i % accs, i // accs
+            if i >= accs and plant != "no drain wait":
+                while not acce[b].passed(u - 1):
+                    yield
+            assert not readers[b], "an accumulator is refilled while it is drained"
+            acc[b] = None
+            for _ in range(kblocks):
+                s = g % stages
+                while not full[s].passed(g // stages + (1 if plant == "full parity" else 0)):
+                    yield
+                for c in range(2):
+                    assert ring[c][s] == g, "an MMA reads another slice"
+                    busy[c][s] = 1
+                yield
+                # the MMA completes, then its commit reaches both CTAs in any order
+                commits = [0, 1]
+                rng.shuffle(commits)
+                for c in range(2):
+                    busy[c][s] = 0
+                for c in commits:
+                    empty[c][s].arrive()
+                    yield
+                g += 1
+            acc[b] = i
+            readers[b] = {(c, q) for c in range(2) for q in range(8)}
+            for c in (0, 1):
+                accf[c][b].arrive()
+                yield
+
+    def epilogue(c, q):
+        for i in range(tiles):
+            b, u = i % accs, i // accs
+            while not accf[c][b].passed(u):
+                yield
+            assert acc[b] == i, "an epilogue warp reads another tile"
+            yield
+            readers[b].discard((c, q))
+            acce[b].arrive()
+            yield
+        done.append((c, q))
+
+    interleave([producer(0), producer(1), issuer()] +
+               [epilogue(c, q) for c in range(2) for q in range(8)], rng)
+    assert len(done) == 16
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_pair_pipeline(seed):
+    rng = random.Random(1000 + seed)
+    pair_pipeline(rng.randint(1, 7), rng.randint(1, 15), 7, 2, seed)
+
+
+@pytest.mark.parametrize("plant", ["no empty wait", "no drain wait", "full parity"])
+def test_pair_pipeline_catches(plant):
+    caught = 0
+    for seed in range(60):
+        try:
+            pair_pipeline(12, 1 if plant == "no drain wait" else 9, 7, 2, seed, plant)
+        except AssertionError:
+            caught += 1
+    assert caught > 0
+
+
+def split_parts(kblocks, size):
+    return [(r * kblocks // size, (r + 1) * kblocks // size) for r in range(size)]
+
+
+@pytest.mark.parametrize("size", [1, 2, 4, 8])
+def test_split_covers_k_once(size):
+    for kblocks in range(size, 70):
+        parts = split_parts(kblocks, size)
+        assert [k for a, b in parts for k in range(a, b)] == list(range(kblocks))
+        assert all(b > a for a, b in parts)     # a part that is empty would never finish
+
+
+@pytest.mark.parametrize("bn,threads", [(64, 320), (128, 320)])
+def test_split_reduction_reads_every_element_once(bn, threads):
+    for rows in (1, 7, 100, 128):
+        for size in (1, 2, 4, 8):
+            seen = set()
+            for rank in range(size):
+                for t in range(threads):
+                    for i in range(rank * threads + t, rows * (bn // 4), size * threads):
+                        assert i not in seen
+                        seen.add(i)
+            assert seen == set(range(rows * (bn // 4)))
