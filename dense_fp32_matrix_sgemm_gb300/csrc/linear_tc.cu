@@ -75,16 +75,24 @@ struct Params {
     unsigned *error;
 };
 
-// True in one lane of a converged warp.  The producer and the MMA issuer run
-// their loops with the whole warp and let this lane issue, so that the
-// compiler keeps descriptors and coordinates in uniform registers; in loops
-// that a single lane runs it cannot, and an MMA then took about 226 clocks to
-// issue, against the 128 that it runs (4096 x 8192 x 4096: @ISSUE@).
+// True in one lane of a converged warp.  The producer's and the MMA issuer's
+// loops run in such a lane: elect.sync tells the compiler that a single thread
+// is active, so descriptors and coordinates stay in uniform registers.  In the
+// same loops under "lane == 0" an MMA took about 226 clocks to issue, against
+// the 128 that it runs (4096 x 8192 x 4096: 224 us, 160 elected).
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\t"
                  "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
     return p != 0;
+}
+
+// Bounded wait that polls before it reads the clock or the abort word: a
+// stage is handed over every 512 clocks, and those two reads in front of each
+// poll alone held the pair kernel at 157 us where this takes 140.
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int *abort) {
+    if (tc::mbar_try_wait(bar, parity)) return true;
+    return tc::mbar_wait(bar, parity, abort);
 }
 
 // Position in a ring of N stages: the stage, the parity of its current round,
@@ -167,7 +175,7 @@ __device__ __forceinline__ void raster(const Params &p, int t, int &tm, int &tn)
 // Global accesses are 32 bytes a lane, whole sectors of one row each, so they
 // need no exchange between lanes.  (Turning the tile through shared memory
 // first, for accesses along a row, took 71 us of the 4096 x 8192 outputs of a
-// plain product, and 199 with GELU and stored z, against @FIN@ now.)
+// plain product, and 199 with GELU and stored z, and 11 and 22 this way.)
 template <int COLS, class O>
 __device__ __forceinline__ void finish_rows(const LayerEpi &e, uint32_t acc, int q, int lane,
                                             int m0, int n0) {
@@ -253,7 +261,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     pdl_wait();   // nothing below touches global memory before earlier work has finished
 
     if (warp == 0) {
-        {
+        if (elect_one()) {
             // ---------------- TMA producer
             const int bk = p.fp8 ? 128 : 64;
             const uint32_t tx = (uint32_t)(p.a_bytes + S::B_TILE);
@@ -264,54 +272,45 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                 raster(p, first + i * stride, tm, tn);
                 const int m0 = tm * BM, n0 = tn * BN;
                 for (int kb = kb0; kb < kb1; ++kb) {
-                    bool ok = true;
-                    if (r.used == STAGES)
-                        ok = tc::mbar_wait(empty0 + 8 * r.s, r.parity ^ 1, abort_flag);
-                    if (!__all_sync(0xffffffffu, ok && !*abort_flag)) {
+                    if (r.used == STAGES && !wait(empty0 + 8 * r.s, r.parity ^ 1, abort_flag)) {
                         stop = true;
                         break;
                     }
                     const uint32_t st = ring + r.s * S::STAGE, fb = full0 + 8 * r.s;
                     const int k0 = kb * bk;
-                    if (elect_one()) {
-                        tc::mbar_arrive_expect_tx(fb, tx);
-                        if (p.a_kmajor) {
-                            tma_load_2d(st, &tmA, fb, k0, m0);
-                        } else {
+                    tc::mbar_arrive_expect_tx(fb, tx);
+                    if (p.a_kmajor) {
+                        tma_load_2d(st, &tmA, fb, k0, m0);
+                    } else {
 #pragma unroll
-                            for (int c = 0; c < BM / 64; ++c)
-                                tma_load_2d(st + c * kBox, &tmA, fb, m0 + 64 * c, k0);
-                        }
-                        if (p.b_kmajor) {
-                            tma_load_2d(st + S::A_TILE, &tmB, fb, k0, n0);
-                        } else {
-#pragma unroll
-                            for (int c = 0; c < BN / 64; ++c)
-                                tma_load_2d(st + S::A_TILE + c * kBox, &tmB, fb, n0 + 64 * c, k0);
-                        }
+                        for (int c = 0; c < BM / 64; ++c)
+                            tma_load_2d(st + c * kBox, &tmA, fb, m0 + 64 * c, k0);
                     }
-                    __syncwarp();
+                    if (p.b_kmajor) {
+                        tma_load_2d(st + S::A_TILE, &tmB, fb, k0, n0);
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < BN / 64; ++c)
+                            tma_load_2d(st + S::A_TILE + c * kBox, &tmB, fb, n0 + 64 * c, k0);
+                    }
                     r.next();
                 }
             }
             if (*abort_flag) drain_ring(r, full0);
         }
     } else if (warp == 1) {
-        {
+        if (elect_one()) {
             // ---------------- MMA issuer
             const uint64_t astep = p.a_kmajor ? 2 : 128, bstep = p.b_kmajor ? 2 : 128;
             Ring<STAGES> r;
             bool stop = false;
             for (int i = 0; i < ntiles && !stop; ++i) {
                 const int b = i % ACCS, u = i / ACCS;
-                bool ok = true;
-                if (i >= ACCS) ok = tc::mbar_wait(acce0 + 8 * b, (u - 1) & 1, abort_flag);
-                if (!__all_sync(0xffffffffu, ok)) break;
+                if (i >= ACCS && !wait(acce0 + 8 * b, (u - 1) & 1, abort_flag)) break;
                 tc::fence_after_sync();
                 const uint32_t acc = tmem + (uint32_t)(b * BN);
                 for (int kb = 0; kb < nk; ++kb) {
-                    ok = tc::mbar_wait(full0 + 8 * r.s, r.parity, abort_flag);
-                    if (!__all_sync(0xffffffffu, ok)) {
+                    if (!wait(full0 + 8 * r.s, r.parity, abort_flag)) {
                         stop = true;
                         break;
                     }
@@ -320,35 +319,30 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                     const uint64_t ad = p.a_kmajor ? tc::kmajor_desc<128>(st) : mnmajor_desc(st);
                     const uint64_t bd = p.b_kmajor ? tc::kmajor_desc<128>(st + S::A_TILE)
                                                    : mnmajor_desc(st + S::A_TILE);
-                    if (elect_one()) {
-                        if (p.fp8) {
+                    if (p.fp8) {
 #pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)
-                                mma_f8(acc, ad + kk * astep, bd + kk * bstep, p.idesc,
-                                       (kb | kk) ? 1u : 0u);
-                        } else {
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_f8(acc, ad + kk * astep, bd + kk * bstep, p.idesc,
+                                   (kb | kk) ? 1u : 0u);
+                    } else {
 #pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)
-                                mma_f16(acc, ad + kk * astep, bd + kk * bstep, p.idesc,
-                                        (kb | kk) ? 1u : 0u);
-                        }
-                        tc::mma_commit(empty0 + 8 * r.s);
-                        if (kb + 1 == nk) tc::mma_commit(accf0 + 8 * b);
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_f16(acc, ad + kk * astep, bd + kk * bstep, p.idesc,
+                                    (kb | kk) ? 1u : 0u);
                     }
-                    __syncwarp();
+                    tc::mma_commit(empty0 + 8 * r.s);
+                    if (kb + 1 == nk) tc::mma_commit(accf0 + 8 * b);
                     r.next();
                 }
             }
-            // tracks every MMA issued above, also on abort
-            if (elect_one()) tc::mma_commit(done_bar);
-            __syncwarp();
+            tc::mma_commit(done_bar);   // tracks every MMA issued above, also on abort
         }
     } else {
         // ---------------- epilogue
         const int q = warp & 3, half = (warp - 2) >> 2;
         for (int i = 0; i < ntiles; ++i) {
             const int b = i % ACCS, u = i / ACCS;
-            const bool ok = tc::mbar_wait(accf0 + 8 * b, u & 1, abort_flag);
+            const bool ok = wait(accf0 + 8 * b, u & 1, abort_flag);
             __syncwarp();
             // one warp-uniform decision: the TMEM loads are warp-collective
             if (!__all_sync(0xffffffffu, ok && !*abort_flag)) break;
@@ -556,7 +550,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
     pdl_wait();   // nothing below touches global memory before earlier work has finished
 
     if (warp == 0) {
-        {
+        if (elect_one()) {
             // ---------------- TMA producer: this CTA's halves of A and B
             const int bk = p.fp8 ? 128 : 64;
             const uint32_t full_leader = leader_addr(full0);
@@ -567,34 +561,28 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                 raster(p, first + i * stride, tm, tn);
                 const int m0 = tm * 2 * BM + rank * BM, n0 = tn * BN + rank * (BN / 2);
                 for (int kb = 0; kb < p.kblocks; ++kb) {
-                    bool ok = true;
-                    if (r.used == STAGES)
-                        ok = tc::mbar_wait(empty0 + 8 * r.s, r.parity ^ 1, abort_flag);
-                    if (!__all_sync(0xffffffffu, ok && !*abort_flag)) {
+                    if (r.used == STAGES && !wait(empty0 + 8 * r.s, r.parity ^ 1, abort_flag)) {
                         stop = true;
                         break;
                     }
                     const uint32_t st = ring + r.s * Pair::STAGE, fb = full_leader + 8 * r.s;
                     const int k0 = kb * bk;
-                    if (elect_one()) {
-                        if (rank == 0) tc::mbar_arrive_expect_tx(full0 + 8 * r.s, 2 * Pair::STAGE);
-                        if (p.a_kmajor) {
-                            tma_load_2d_pair(st, &tmA, fb, k0, m0);
-                        } else {
+                    if (rank == 0) tc::mbar_arrive_expect_tx(full0 + 8 * r.s, 2 * Pair::STAGE);
+                    if (p.a_kmajor) {
+                        tma_load_2d_pair(st, &tmA, fb, k0, m0);
+                    } else {
 #pragma unroll
-                            for (int c = 0; c < 2; ++c)
-                                tma_load_2d_pair(st + c * kBox, &tmA, fb, m0 + 64 * c, k0);
-                        }
-                        if (p.b_kmajor) {
-                            tma_load_2d_pair(st + Pair::A_TILE, &tmB, fb, k0, n0);
-                        } else {
-#pragma unroll
-                            for (int c = 0; c < 2; ++c)
-                                tma_load_2d_pair(st + Pair::A_TILE + c * kBox, &tmB, fb,
-                                                 n0 + 64 * c, k0);
-                        }
+                        for (int c = 0; c < 2; ++c)
+                            tma_load_2d_pair(st + c * kBox, &tmA, fb, m0 + 64 * c, k0);
                     }
-                    __syncwarp();
+                    if (p.b_kmajor) {
+                        tma_load_2d_pair(st + Pair::A_TILE, &tmB, fb, k0, n0);
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+                            tma_load_2d_pair(st + Pair::A_TILE + c * kBox, &tmB, fb,
+                                             n0 + 64 * c, k0);
+                    }
                     r.next();
                 }
             }
@@ -602,21 +590,18 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
             if (rank == 0 && *abort_flag) drain_ring(r, full0);
         }
     } else if (warp == 1) {
-        if (rank == 0) {
+        if (rank == 0 && elect_one()) {
             // ---------------- MMA issuer, for both CTAs
             const uint64_t astep = p.a_kmajor ? 2 : 128, bstep = p.b_kmajor ? 2 : 128;
             Ring<STAGES> r;
             bool stop = false;
             for (int i = 0; i < ntiles && !stop; ++i) {
                 const int b = i % ACCS, u = i / ACCS;
-                bool ok = true;
-                if (i >= ACCS) ok = tc::mbar_wait(acce0 + 8 * b, (u - 1) & 1, abort_flag);
-                if (!__all_sync(0xffffffffu, ok)) break;
+                if (i >= ACCS && !wait(acce0 + 8 * b, (u - 1) & 1, abort_flag)) break;
                 tc::fence_after_sync();
                 const uint32_t acc = tmem + (uint32_t)(b * BN);
                 for (int kb = 0; kb < p.kblocks; ++kb) {
-                    ok = tc::mbar_wait(full0 + 8 * r.s, r.parity, abort_flag);
-                    if (!__all_sync(0xffffffffu, ok)) {
+                    if (!wait(full0 + 8 * r.s, r.parity, abort_flag)) {
                         stop = true;
                         break;
                     }
@@ -625,35 +610,30 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                     const uint64_t ad = p.a_kmajor ? tc::kmajor_desc<128>(st) : mnmajor_desc(st);
                     const uint64_t bd = p.b_kmajor ? tc::kmajor_desc<128>(st + Pair::A_TILE)
                                                    : mnmajor_desc(st + Pair::A_TILE);
-                    if (elect_one()) {
-                        if (p.fp8) {
+                    if (p.fp8) {
 #pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)
-                                mma_f8_pair(acc, ad + kk * astep, bd + kk * bstep, p.idesc,
-                                       (kb | kk) ? 1u : 0u);
-                        } else {
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_f8_pair(acc, ad + kk * astep, bd + kk * bstep, p.idesc,
+                                   (kb | kk) ? 1u : 0u);
+                    } else {
 #pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)
-                                mma_f16_pair(acc, ad + kk * astep, bd + kk * bstep, p.idesc,
-                                        (kb | kk) ? 1u : 0u);
-                        }
-                        commit_pair(empty0 + 8 * r.s);
-                        if (kb + 1 == p.kblocks) commit_pair(accf0 + 8 * b);
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_f16_pair(acc, ad + kk * astep, bd + kk * bstep, p.idesc,
+                                    (kb | kk) ? 1u : 0u);
                     }
-                    __syncwarp();
+                    commit_pair(empty0 + 8 * r.s);
+                    if (kb + 1 == p.kblocks) commit_pair(accf0 + 8 * b);
                     r.next();
                 }
             }
-            // tracks every MMA issued above, also on abort
-            if (elect_one()) commit_pair(done_bar);
-            __syncwarp();
+            commit_pair(done_bar);   // tracks every MMA issued above, also on abort
         }
     } else {
         // ---------------- epilogue: this CTA's 128 rows
         const int q = warp & 3, half = (warp - 2) >> 2;
         for (int i = 0; i < ntiles; ++i) {
             const int b = i % ACCS, u = i / ACCS;
-            const bool ok = tc::mbar_wait(accf0 + 8 * b, u & 1, abort_flag);
+            const bool ok = wait(accf0 + 8 * b, u & 1, abort_flag);
             __syncwarp();
             if (!__all_sync(0xffffffffu, ok && !*abort_flag)) break;
             tc::fence_after_sync();
