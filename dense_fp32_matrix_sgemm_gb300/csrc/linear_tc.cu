@@ -3,29 +3,44 @@
 //
 //   D[row, col] = sum_k A(row, k) B(col, k)
 //
-// tcgen05.mma bounds it where all three sizes are large (2 M N K flops), HBM
-// where one of them is small.  A CTA computes 128 x BN tiles with warps in
-// three roles:
-//   warp 0:         TMA producer: 128 bytes of K of A's and B's rows a stage,
-//                   128-byte swizzle, a ring that runs on across tiles;
-//   warp 1:         MMA issuer (M128 N=BN, 32 bytes of K an instruction);
-//                   warp 1 owns tensor memory;
-//   warps 2-9:      epilogue: TMEM lane quarter warp % 4, half of the columns.
+// tcgen05.mma bounds it where all three sizes are large (2 M N K flops), the
+// bytes that L2 can bring to an SM (about 55 a clock) where the tiles are
+// small, HBM where few rows meet a large W.  A CTA has ten warps in three
+// roles:
+//   warp 0:    TMA producer: 128 bytes of K of A's and B's rows a stage,
+//              128-byte swizzle, a ring that runs on across tiles;
+//   warp 1:    MMA issuer (32 bytes of K an instruction); owns tensor memory;
+//   warps 2-9: epilogue: TMEM lane quarter warp % 4, half of the columns.
 // Operands may be K-major or (16-bit types) M/N-major in memory: the tensor
 // core's descriptors take both, so no operand is transposed.
 //   K-major:  box of 128 bytes of K x rows; 8-row groups 1024 bytes apart.
 //   MN-major: boxes of 64 rows x 64 k; the 64 rows are the 128-byte line, 8
 //             k make a 1024-byte group, the next 64 rows are 8192 bytes on.
+// CTAS = 2: pairs of CTAs (cta_group::2) compute 256 x 256 tiles.  Each CTA
+//   holds 128 of A's rows and 128 of B's 256 a stage (32 KB) and the 128 rows
+//   of the result that are its own.  One MMA of the even CTA reads both halves,
+//   so a CTA takes in 32 KB for 2 x 128 x 256 x 64 flops where a 128 x 256 tile
+//   of its own takes 48 and a 128 x 128 tile 64 for the same: at the tensor
+//   cores' rate 64 bytes a clock instead of 96 and 128.  (4096 x 8192 x 4096:
+//   140 us; 128 x 256 tiles of single CTAs were bound by their operands.)
+// CTAS = 1: 128 x BN tiles, for problems with few rows.
 // Two schedules:
-//   persistent: one CTA an SM walks tiles; two accumulators (2 BN columns), so
-//     a tile's epilogue overlaps the next one's MMAs;
-//   split: problems with fewer tiles than SMs: the CTAs of a cluster take
-//     equal parts of K of one tile, park their sums in their own shared memory
-//     and finish a share of the tile each, adding the parts in rank order
+//   persistent: one CTA an SM walks tiles; two accumulators, so a tile's
+//     epilogue overlaps the next one's MMAs;
+//   SPLIT: problems with fewer tiles than SMs: the CTAs (or pairs) of a cluster
+//     take equal parts of K of one tile, park their sums in their own shared
+//     memory and finish a share of the tile each, adding the parts in K order
 //     through distributed shared memory (no workspace, one launch).
-// Every wait is bounded; one that runs out flags the CTA, all roles drain and
-// the library's device status word is raised.
-#include <climits>
+// Barriers, in each CTA except where noted:
+//   full (even CTA of a pair): the copies of both CTAs complete on it; the
+//     even CTA's producer expects the bytes of both;
+//   empty, accumulator full: completed by the issuer's commits, in both CTAs;
+//   accumulator empty (even CTA): one arrival of each epilogue warp of both.
+// Every wait is bounded.  A CTA whose wait runs out stops; its peer's waits
+// then run out too, the even CTA waits for every copy in flight, and all CTAs
+// of a cluster meet at its closing barrier, so none leaves while another may
+// still write to its shared memory.  The library's device status word is
+// raised.
 #include <cstdint>
 
 #include <cuda.h>
@@ -42,25 +57,27 @@
 namespace sgemm {
 namespace ltc {
 
-constexpr int BM = 128;
+constexpr int BM = 128;             // rows of a CTA's tile
 constexpr int kEpiWarps = 8;
-constexpr int kThreads = 64 + 32 * kEpiWarps;   // producer, MMA issuer, epilogue
+constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr int kRowBytes = 128;      // of K in a stage
 constexpr int kBox = 8192;          // MN-major box: 64 k x 128 bytes
+constexpr int kSmem = 227 * 1024;
 
-template <int BN, bool SPLIT>
+template <int CTAS, int BN, bool SPLIT>
 struct Shape {
+    static constexpr int BROWS = BN / CTAS;   // of B in a CTA
     static constexpr int A_TILE = BM * kRowBytes;
-    static constexpr int B_TILE = BN * kRowBytes;
+    static constexpr int B_TILE = BROWS * kRowBytes;
     static constexpr int STAGE = A_TILE + B_TILE;
-    static constexpr int STAGES = 224 * 1024 / STAGE;
+    static constexpr int STAGING = SPLIT ? 0 : kEpiWarps * 4096;   // an epilogue warp's block
+    static constexpr int STAGES = (kSmem - 1024 - 256 - STAGING) / STAGE;
     static constexpr int ACCS = SPLIT ? 1 : 2;
     static constexpr int TMEM_COLS = ACCS * BN;
     static constexpr int BARS = 2 * STAGES + 2 * ACCS + 1;
-    static constexpr int SMEM = STAGES * STAGE + 1024 + 256;
+    static constexpr int SMEM = STAGES * STAGE + STAGING + 1024 + 256;
     static_assert(TMEM_COLS >= 32 && TMEM_COLS <= 512, "tensor memory");
     static_assert(BARS * 8 + 8 <= 256, "barrier area");
-    static_assert(SMEM <= 227 * 1024, "shared memory budget");
     static_assert(BM * BN * 4 <= STAGES * STAGE, "the split's partial tile fits the ring");
 };
 
@@ -69,9 +86,10 @@ struct Params {
     int kblocks;             // K in stages
     int tiles_m, tiles_n, group_m;
     int a_kmajor, b_kmajor;
-    int a_bytes;             // bytes A's boxes bring to a stage
+    int a_bytes;             // bytes A's boxes bring to a CTA's stage
     uint32_t idesc;
     int fp8;
+    int tma;                 // Y and Z leave by TMA store where whole blocks of 64 columns do
     unsigned *error;
 };
 
@@ -122,14 +140,32 @@ __device__ __forceinline__ void drain_ring(const Ring<N> &r, uint32_t full0) {
     }
 }
 
-// 2-D tiled load of the box at (c0, c1); c0 (innermost) a multiple of 16 bytes.
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const void *tmap, uint32_t bar, int c0,
-                                            int c1) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4}], [%2];"
-        :: "r"(dst), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c0), "r"(c1)
-        : "memory");
+// ------------------------------------------------------------------ PTX
+
+// 2-D tiled load of the box at (c0, c1) into this CTA's shared memory,
+// completing on `bar`: a barrier of this CTA, or (CTAS = 2, a shared::cluster
+// address) of the pair's even CTA.  c0 (innermost) is a multiple of 16 bytes.
+template <int CTAS>
+__device__ __forceinline__ void tma_load(uint32_t dst, const void *tmap, uint32_t bar, int c0,
+                                         int c1) {
+    if constexpr (CTAS == 1)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%3, %4}], [%2];"
+            :: "r"(dst), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c0), "r"(c1)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global"
+            ".mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];"
+            :: "r"(dst), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c0), "r"(c1)
+            : "memory");
+}
+
+__device__ __forceinline__ void tma_store(const void *tmap, uint32_t src, int c0, int c1) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];"
+                 :: "l"(reinterpret_cast<uint64_t>(tmap)), "r"(src), "r"(c0), "r"(c1)
+                 : "memory");
 }
 
 // Descriptor of an MN-major operand tile: 64-row chunks kBox bytes apart
@@ -144,21 +180,95 @@ __device__ __forceinline__ uint64_t mnmajor_desc(uint32_t smem_addr) {
     return d;
 }
 
-__device__ __forceinline__ void mma_f16(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
-                                        uint32_t idesc, uint32_t accumulate) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-                 :: "r"(tmem_d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-                 : "memory");
+template <int CTAS, bool FP8>
+__device__ __forceinline__ void mma(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
+                                    uint32_t idesc, uint32_t accumulate) {
+#define SGEMM_MMA(group, kind)                                                                  \
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"                              \
+                 "tcgen05.mma.cta_group::" group ".kind::" kind " [%0], %1, %2, %3, p;\n\t}"    \
+                 :: "r"(tmem_d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)            \
+                 : "memory")
+    if constexpr (CTAS == 1 && FP8) SGEMM_MMA("1", "f8f6f4");
+    if constexpr (CTAS == 1 && !FP8) SGEMM_MMA("1", "f16");
+    if constexpr (CTAS == 2 && FP8) SGEMM_MMA("2", "f8f6f4");
+    if constexpr (CTAS == 2 && !FP8) SGEMM_MMA("2", "f16");
+#undef SGEMM_MMA
 }
 
-__device__ __forceinline__ void mma_f8(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
-                                       uint32_t idesc, uint32_t accumulate) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
-                 :: "r"(tmem_d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-                 : "memory");
+// Arrive on `bar` (CTAS = 2: in both CTAs of the pair, `mask`) once every MMA
+// issued so far by this thread has completed.
+template <int CTAS>
+__device__ __forceinline__ void commit(uint32_t bar, uint16_t mask) {
+    if constexpr (CTAS == 1)
+        tc::mma_commit(bar);
+    else
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster"
+                     ".multicast::cluster.b64 [%0], %1;" :: "r"(bar), "h"(mask) : "memory");
 }
+
+template <int CTAS>
+__device__ __forceinline__ void tmem_alloc(uint32_t slot_smem, uint32_t ncols) {
+    if constexpr (CTAS == 1) {
+        tc::tmem_alloc(slot_smem, ncols);
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
+                     :: "r"(slot_smem), "r"(ncols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+}
+
+template <int CTAS>
+__device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
+    if constexpr (CTAS == 1)
+        tc::tmem_dealloc(taddr, ncols);
+    else
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;"
+                     :: "r"(taddr), "r"(ncols) : "memory");
+}
+
+// The shared::cluster address of `addr` (shared::cta) in the cluster's CTA `rank`.
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, int rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+
+__device__ __forceinline__ void arrive_cluster(uint32_t cluster_bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];"
+                 :: "r"(cluster_bar) : "memory");
+}
+
+// 64 consecutive columns of this thread's TMEM lane, both loads in flight.
+__device__ __forceinline__ void tmem_ld_64(uint32_t taddr, float (&v)[64]) {
+    uint32_t r[64];
+#define SGEMM_LD32(o)                                                                           \
+    asm volatile(                                                                               \
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "                                               \
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "               \
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, "     \
+        "[%32];"                                                                                \
+        : "=r"(r[o]), "=r"(r[o + 1]), "=r"(r[o + 2]), "=r"(r[o + 3]), "=r"(r[o + 4]),           \
+          "=r"(r[o + 5]), "=r"(r[o + 6]), "=r"(r[o + 7]), "=r"(r[o + 8]), "=r"(r[o + 9]),       \
+          "=r"(r[o + 10]), "=r"(r[o + 11]), "=r"(r[o + 12]), "=r"(r[o + 13]),                   \
+          "=r"(r[o + 14]), "=r"(r[o + 15]), "=r"(r[o + 16]), "=r"(r[o + 17]),                   \
+          "=r"(r[o + 18]), "=r"(r[o + 19]), "=r"(r[o + 20]), "=r"(r[o + 21]),                   \
+          "=r"(r[o + 22]), "=r"(r[o + 23]), "=r"(r[o + 24]), "=r"(r[o + 25]),                   \
+          "=r"(r[o + 26]), "=r"(r[o + 27]), "=r"(r[o + 28]), "=r"(r[o + 29]),                   \
+          "=r"(r[o + 30]), "=r"(r[o + 31])                                                      \
+        : "r"(taddr + o))
+    SGEMM_LD32(0);
+    SGEMM_LD32(32);
+#undef SGEMM_LD32
+    // the registers pass through the wait, so that no use moves above it
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 64; ++i) {
+        asm volatile("" : "+r"(r[i]));
+        v[i] = __uint_as_float(r[i]);
+    }
+}
+
+// ------------------------------------------------------------------ kernel
 
 __device__ __forceinline__ void raster(const Params &p, int t, int &tm, int &tn) {
     const int group = p.group_m * p.tiles_n;
@@ -170,51 +280,142 @@ __device__ __forceinline__ void raster(const Params &p, int t, int &tm, int &tn)
     tn = r / rows;
 }
 
+// 64 values of this lane's row into the warp's staging block (32 rows of 128
+// bytes, 16-byte chunk c of row r at c ^ (r & 7): the TMA 128-byte swizzle,
+// conflict-free for a quarter-warp) and from there by TMA store to (col, row0).
+template <class O>
+__device__ __forceinline__ void store_block(const void *map, uint32_t stage, int lane, int row0,
+                                            int col, const float (&v)[64]) {
+    if (lane == 0) tc::bulk_wait_group_read<0>();   // the previous store has read the block
+    __syncwarp();
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+        const uint32_t a = pack2<O>(v[8 * c], v[8 * c + 1]), b = pack2<O>(v[8 * c + 2], v[8 * c + 3]);
+        const uint32_t d = pack2<O>(v[8 * c + 4], v[8 * c + 5]),
+                       f = pack2<O>(v[8 * c + 6], v[8 * c + 7]);
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                     :: "r"(stage + (uint32_t)lane * 128u + ((uint32_t)(c ^ (lane & 7)) << 4)),
+                        "r"(a), "r"(b), "r"(d), "r"(f) : "memory");
+    }
+    tc::fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+        tma_store(map, stage, col, row0);
+        tc::bulk_commit_group();
+    }
+}
+
 // Finishes COLS columns of the 32 tile rows of TMEM lane quarter q, a row a
-// lane: the accumulators stay in registers from tensor memory to the store.
-// Global accesses are 32 bytes a lane, whole sectors of one row each, so they
-// need no exchange between lanes.  (Turning the tile through shared memory
-// first, for accesses along a row, took 71 us of the 4096 x 8192 outputs of a
-// plain product, and 199 with GELU and stored z, and 11 and 22 this way.)
+// lane, 64 columns at a time: the epilogue runs on the accumulators in
+// registers, whole 128-byte row pieces leave by TMA.  What TMA cannot store
+// (rows that are not 16-byte aligned, the last block of a width that is not a
+// multiple of 64) passes through the staging block in fp32, 32 columns at a
+// time, and is finished a row at a time with a column a lane.
 template <int COLS, class O>
-__device__ __forceinline__ void finish_rows(const LayerEpi &e, uint32_t acc, int q, int lane,
-                                            int m0, int n0) {
+__device__ __forceinline__ void finish_rows(const Params &p, const void *tmY, const void *tmZ,
+                                            uint32_t acc, int q, int lane, int m0, int n0,
+                                            uint32_t stage) {
+    const LayerEpi &e = p.epi;
     const int row0 = m0 + 32 * q;
     if (row0 >= e.M) return;
     const int row = row0 + lane;
     const uint32_t lane_base = acc + ((uint32_t)(32 * q) << 16);
 #pragma unroll 1
-    for (int c = 0; c < COLS / 32 && n0 + 32 * c < e.N; ++c) {
-        const int col = n0 + 32 * c;
-        float v[32];
-        __syncwarp();   // the load is warp-collective
-        tc::tmem_ld_32(lane_base + (uint32_t)(32 * c), v);
-        if (row >= e.M) continue;
-        if (e.vec == 16 && col + 32 <= e.N) {
-            finish32<O>(e, row, col, v);
-        } else {
+    for (int c = 0; c < COLS / 64 && n0 + 64 * c < e.N; ++c) {
+        const int col = n0 + 64 * c;
+        const bool fast = p.tma && col + 64 <= e.N;
+        uint32_t res[4][8];
+        if (fast && e.R != nullptr && row < e.M) {
+            const O *r = static_cast<const O *>(e.R) + row * e.ldr + col;
 #pragma unroll
-            for (int j = 0; j < 32; j += 8) {
-                float w[8];
+            for (int i = 0; i < 4; ++i) load_32b(r + 16 * i, res[i]);
+        }
+        float v[64];
+        __syncwarp();   // the loads are warp-collective
+        tmem_ld_64(lane_base + (uint32_t)(64 * c), v);
+        if (!fast) {
+            const int rows = min(32, e.M - row0);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) w[i] = v[j + i];
-                if (col + j < e.N) finish<O, 8>(e, row, col + j, w);
+            for (int h = 0; h < 2; ++h) {
+                if (lane == 0) tc::bulk_wait_group_read<0>();
+                __syncwarp();   // the block is free
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    tc::st_shared_v4(stage + (uint32_t)lane * 128u +
+                                         ((uint32_t)(j ^ (lane & 7)) << 4),
+                                     v[32 * h + 4 * j], v[32 * h + 4 * j + 1],
+                                     v[32 * h + 4 * j + 2], v[32 * h + 4 * j + 3]);
+                __syncwarp();
+                const int cc = col + 32 * h + lane;
+                if (cc < e.N) {
+#pragma unroll 4
+                    for (int r = 0; r < rows; ++r) {
+                        float x;
+                        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x)
+                                     : "r"(stage + (uint32_t)r * 128u +
+                                           ((uint32_t)((lane >> 2) ^ (r & 7)) << 4) +
+                                           (uint32_t)((lane & 3) * 4)) : "memory");
+                        finish1<O>(e, row0 + r, cc, x);
+                    }
+                }
+                __syncwarp();
+            }
+            continue;
+        }
+        if (e.sx != nullptr) {
+            const float sx = row < e.M ? e.sx[row] : 0.f;
+#pragma unroll
+            for (int j = 0; j < 64; j += 4) {
+                const float4 sw = *reinterpret_cast<const float4 *>(e.sw + col + j);
+                v[j] *= sx * sw.x;
+                v[j + 1] *= sx * sw.y;
+                v[j + 2] *= sx * sw.z;
+                v[j + 3] *= sx * sw.w;
             }
         }
+        if (e.bias != nullptr) {
+            const O *b = static_cast<const O *>(e.bias) + col;
+#pragma unroll
+            for (int j = 0; j < 64; j += 8) {
+                const uint4 u = *reinterpret_cast<const uint4 *>(b + j);
+                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 f = unpack2<O>(w[i]);
+                    v[j + 2 * i] += f.x;
+                    v[j + 2 * i + 1] += f.y;
+                }
+            }
+        }
+        if (e.Z != nullptr) store_block<O>(tmZ, stage, lane, row0, col, v);
+        activate_all<O>(v, e.act);
+        if (e.R != nullptr && row < e.M) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float2 f = unpack2<O>(res[i][j]);
+                    v[16 * i + 2 * j] += f.x;
+                    v[16 * i + 2 * j + 1] += f.y;
+                }
+        }
+        store_block<O>(tmY, stage, lane, row0, col, v);
     }
 }
 
-template <int BN, class O, bool SPLIT>
+template <int CTAS, int BN, class O, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
 linear_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                 const Params p) {
-    using S = Shape<BN, SPLIT>;
+                 const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmZ,
+                 const __grid_constant__ Params p) {
+    using S = Shape<CTAS, BN, SPLIT>;
     constexpr int STAGES = S::STAGES, ACCS = S::ACCS;
+    constexpr bool CLUSTER = CTAS == 2 || SPLIT;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw_addr = tc::smem_u32_generic(smem_raw);
     uint8_t *smem = smem_raw + ((1024 - (raw_addr & 1023)) & 1023);
     const uint32_t ring = tc::smem_u32_generic(smem);
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + STAGES * S::STAGE);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + STAGES * S::STAGE + S::STAGING);
     const uint32_t full0 = tc::smem_u32_generic(bars);
     const uint32_t empty0 = full0 + 8 * STAGES;
     const uint32_t accf0 = empty0 + 8 * STAGES;   // accumulator b holds a finished tile
@@ -224,15 +425,21 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = CLUSTER ? (int)cluster_rank() : 0;
+    const int half = CTAS == 2 ? rank & 1 : 0;      // this CTA's half of the pair's tile
+    const int leader = CTAS == 2 ? rank & ~1 : rank;
+    const uint16_t mask = (uint16_t)(3u << leader);
     // this CTA's tiles first, first + stride, ... and its K blocks of each
     const int total = p.tiles_m * p.tiles_n;
-    int first = (int)blockIdx.x, stride = (int)gridDim.x, kb0 = 0, kb1 = p.kblocks;
+    int first = (int)blockIdx.x / CTAS, stride = (int)gridDim.x / CTAS, kb0 = 0, kb1 = p.kblocks;
+    int parts = 1, part = 0;
     if constexpr (SPLIT) {
-        const int rank = (int)cluster_rank(), size = (int)cluster_size();
-        first = (int)blockIdx.x / size;
+        parts = (int)cluster_size() / CTAS;
+        part = rank / CTAS;
+        first = (int)blockIdx.x / (CTAS * parts);
         stride = total;
-        kb0 = (int)((long long)rank * p.kblocks / size);
-        kb1 = (int)((long long)(rank + 1) * p.kblocks / size);
+        kb0 = (int)((long long)part * p.kblocks / parts);
+        kb1 = (int)((long long)(part + 1) * p.kblocks / parts);
     }
     const int ntiles = first < total ? (total - 1 - first) / stride + 1 : 0;
     const int nk = kb1 - kb0;
@@ -244,17 +451,24 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         }
         for (int b = 0; b < ACCS; ++b) {
             tc::mbar_init(accf0 + 8 * b, 1);
-            tc::mbar_init(acce0 + 8 * b, kEpiWarps);
+            tc::mbar_init(acce0 + 8 * b, CTAS * kEpiWarps);
         }
         tc::mbar_init(done_bar, 1);
         *abort_flag = 0;
         tc::fence_barrier_init();
+    }
+    // a pair's CTAs use one another's barriers: its barrier is passed while
+    // tensor memory is allocated
+    if constexpr (CTAS == 2)
+        asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+    if (warp == 1) tmem_alloc<CTAS>(tc::smem_u32_generic(tmem_slot), S::TMEM_COLS);
+    if (warp == 2 && lane == 0) {
         tc::tma_prefetch_desc(&tmA);
         tc::tma_prefetch_desc(&tmB);
     }
-    if (warp == 1) tc::tmem_alloc(tc::smem_u32_generic(tmem_slot), S::TMEM_COLS);
     tc::fence_before_sync();
     __syncthreads();
+    if constexpr (CTAS == 2) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_slot;
     pdl_trigger();
@@ -262,45 +476,47 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
 
     if (warp == 0) {
         if (elect_one()) {
-            // ---------------- TMA producer
+            // ---------------- TMA producer: this CTA's rows of A and B
             const int bk = p.fp8 ? 128 : 64;
-            const uint32_t tx = (uint32_t)(p.a_bytes + S::B_TILE);
+            const uint32_t tx = (uint32_t)(CTAS * (p.a_bytes + S::B_TILE));
+            const uint32_t fulls = CTAS == 2 ? cluster_addr(full0, leader) : full0;
             Ring<STAGES> r;
             bool stop = false;
             for (int i = 0; i < ntiles && !stop; ++i) {
                 int tm, tn;
                 raster(p, first + i * stride, tm, tn);
-                const int m0 = tm * BM, n0 = tn * BN;
+                const int m0 = (tm * CTAS + half) * BM, n0 = tn * BN + half * S::BROWS;
                 for (int kb = kb0; kb < kb1; ++kb) {
                     if (r.used == STAGES && !wait(empty0 + 8 * r.s, r.parity ^ 1, abort_flag)) {
                         stop = true;
                         break;
                     }
-                    const uint32_t st = ring + r.s * S::STAGE, fb = full0 + 8 * r.s;
+                    const uint32_t st = ring + r.s * S::STAGE, fb = fulls + 8 * r.s;
                     const int k0 = kb * bk;
-                    tc::mbar_arrive_expect_tx(fb, tx);
+                    if (half == 0) tc::mbar_arrive_expect_tx(full0 + 8 * r.s, tx);
                     if (p.a_kmajor) {
-                        tma_load_2d(st, &tmA, fb, k0, m0);
+                        tma_load<CTAS>(st, &tmA, fb, k0, m0);
                     } else {
 #pragma unroll
                         for (int c = 0; c < BM / 64; ++c)
-                            tma_load_2d(st + c * kBox, &tmA, fb, m0 + 64 * c, k0);
+                            tma_load<CTAS>(st + c * kBox, &tmA, fb, m0 + 64 * c, k0);
                     }
                     if (p.b_kmajor) {
-                        tma_load_2d(st + S::A_TILE, &tmB, fb, k0, n0);
+                        tma_load<CTAS>(st + S::A_TILE, &tmB, fb, k0, n0);
                     } else {
 #pragma unroll
-                        for (int c = 0; c < BN / 64; ++c)
-                            tma_load_2d(st + S::A_TILE + c * kBox, &tmB, fb, n0 + 64 * c, k0);
+                        for (int c = 0; c < S::BROWS / 64; ++c)
+                            tma_load<CTAS>(st + S::A_TILE + c * kBox, &tmB, fb, n0 + 64 * c, k0);
                     }
                     r.next();
                 }
             }
-            if (*abort_flag) drain_ring(r, full0);
+            // the copies of both CTAs, before the pair leaves
+            if (half == 0 && *abort_flag) drain_ring(r, full0);
         }
     } else if (warp == 1) {
-        if (elect_one()) {
-            // ---------------- MMA issuer
+        if (half == 0 && elect_one()) {
+            // ---------------- MMA issuer, for the whole pair
             const uint64_t astep = p.a_kmajor ? 2 : 128, bstep = p.b_kmajor ? 2 : 128;
             Ring<STAGES> r;
             bool stop = false;
@@ -322,24 +538,25 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                     if (p.fp8) {
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            mma_f8(acc, ad + kk * astep, bd + kk * bstep, p.idesc,
-                                   (kb | kk) ? 1u : 0u);
+                            mma<CTAS, true>(acc, ad + kk * astep, bd + kk * bstep, p.idesc,
+                                            (kb | kk) ? 1u : 0u);
                     } else {
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            mma_f16(acc, ad + kk * astep, bd + kk * bstep, p.idesc,
-                                    (kb | kk) ? 1u : 0u);
+                            mma<CTAS, false>(acc, ad + kk * astep, bd + kk * bstep, p.idesc,
+                                             (kb | kk) ? 1u : 0u);
                     }
-                    tc::mma_commit(empty0 + 8 * r.s);
-                    if (kb + 1 == nk) tc::mma_commit(accf0 + 8 * b);
+                    commit<CTAS>(empty0 + 8 * r.s, mask);
+                    if (kb + 1 == nk) commit<CTAS>(accf0 + 8 * b, mask);
                     r.next();
                 }
             }
-            tc::mma_commit(done_bar);   // tracks every MMA issued above, also on abort
+            commit<CTAS>(done_bar, mask);   // tracks every MMA issued above, also on abort
         }
     } else {
-        // ---------------- epilogue
-        const int q = warp & 3, half = (warp - 2) >> 2;
+        // ---------------- epilogue: this CTA's rows
+        const int q = warp & 3, side = (warp - 2) >> 2;
+        const uint32_t stage = ring + STAGES * S::STAGE + (uint32_t)(warp - 2) * 4096u;
         for (int i = 0; i < ntiles; ++i) {
             const int b = i % ACCS, u = i / ACCS;
             const bool ok = wait(accf0 + 8 * b, u & 1, abort_flag);
@@ -349,307 +566,78 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             tc::fence_after_sync();
             int tm, tn;
             raster(p, first + i * stride, tm, tn);
-            const uint32_t acc = tmem + (uint32_t)(b * BN);
+            const int m0 = (tm * CTAS + half) * BM;
+            const uint32_t acc = tmem + (uint32_t)(b * BN + side * (BN / 2));
             if constexpr (SPLIT) {
                 // the sums to this CTA's shared memory, over the ring: every
                 // MMA has read its operands.  Row r, 16-byte chunk c at
                 // c ^ (r & 7) of its BN * 4 bytes.
-                if (tm * BM + 32 * q < p.epi.M) {
+                if (m0 + 32 * q < p.epi.M) {
                     const int r = 32 * q + lane;
 #pragma unroll 1
-                    for (int c = half * (BN / 64); c < (half + 1) * (BN / 64); ++c) {
+                    for (int c = 0; c < BN / 64; ++c) {
                         float v[32];
+                        __syncwarp();
                         tc::tmem_ld_32(acc + ((uint32_t)(32 * q) << 16) + (uint32_t)(32 * c), v);
+                        const int c0 = side * (BN / 8) + 8 * c;
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
                             tc::st_shared_v4(ring + (uint32_t)(r * BN * 4) +
-                                                 ((uint32_t)((8 * c + j) ^ (r & 7)) << 4),
+                                                 ((uint32_t)((c0 + j) ^ (r & 7)) << 4),
                                              v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
                     }
                 }
             } else {
-                finish_rows<BN / 2, O>(p.epi, acc + (uint32_t)(half * (BN / 2)), q, lane, tm * BM,
-                                       tn * BN + half * (BN / 2));
+                finish_rows<BN / 2, O>(p, &tmY, &tmZ, acc, q, lane, m0, tn * BN + side * (BN / 2),
+                                       stage);
             }
             tc::fence_before_sync();   // the TMEM loads above precede the release
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(acce0 + 8 * b);
+            if (lane == 0) {
+                if constexpr (CTAS == 2)
+                    arrive_cluster(cluster_addr(acce0 + 8 * b, leader));
+                else
+                    tc::mbar_arrive(acce0 + 8 * b);
+            }
         }
+        if (!SPLIT && lane == 0) tc::bulk_wait_group<0>();   // the stores are done
     }
     __syncwarp();
 
+    tc::fence_before_sync();
+    __syncthreads();
     if constexpr (SPLIT) {
-        // Every CTA of the cluster passes both barriers, an aborted one too
-        // (its share of the tile is then not valid, and the status word says so).
-        const int rank = (int)cluster_rank(), size = (int)cluster_size();
-        __syncthreads();
+        // Every CTA of the cluster passes the barriers, an aborted one too (its
+        // share of the tile is then not valid, and the status word says so).
+        // This CTA's rows are held by the CTAs of its half of every pair.
         cluster_sync();
         int tm, tn;
         raster(p, first, tm, tn);
-        const int rows = min(BM, p.epi.M - tm * BM);
-        for (int i = rank * kThreads + (int)threadIdx.x; i < rows * (BN / 4);
-             i += size * kThreads) {
+        const int m0 = (tm * CTAS + half) * BM;
+        const int rows = min(BM, p.epi.M - m0);
+        for (int i = part * kThreads + (int)threadIdx.x; i < rows * (BN / 4);
+             i += parts * kThreads) {
             const int r = i / (BN / 4), c = i % (BN / 4);
             const int col = tn * BN + 4 * c;
             if (col >= p.epi.N) continue;
-            const float4 s = cluster_sum_f4(
-                ring + (uint32_t)(r * BN * 4) + ((uint32_t)(c ^ (r & 7)) << 4), (uint32_t)size);
-            const float v[4] = {s.x, s.y, s.z, s.w};
-            finish<O, 4>(p.epi, tm * BM + r, col, v);
-        }
-        cluster_sync_relaxed();   // shared memory stays until every peer has read it
-    }
-    tc::fence_before_sync();
-    __syncthreads();
-    if (*abort_flag && threadIdx.x == 0 && p.error != nullptr) atomicOr(p.error, 1u);
-    if (warp == 1) {
-        // every MMA issued has completed before TMEM is freed
-        int local_abort = 0;
-        (void)tc::mbar_wait(done_bar, 0, &local_abort);
-        tc::fence_after_sync();
-        tc::tmem_dealloc(tmem, S::TMEM_COLS);
-    }
-}
-
-// ------------------------------------------------------------------ CTA pairs
-
-// 256 x 256 tiles by pairs of CTAs (cta_group::2).  Each CTA of the pair holds
-// 128 rows of A and 128 of B's 256 rows a stage (32 KB) and the 128 rows of
-// the result that are its own, over all 256 columns (two accumulators fill its
-// tensor memory).  One MMA of the even CTA reads both halves, so a CTA takes in
-// 32 KB for the 2 x 128 x 256 x 64 flops of a stage instead of the 48 KB that a
-// 128 x 256 tile of its own needs: at the tensor cores' rate 64 bytes a clock
-// instead of 96, which L2 can deliver.
-// Barriers:
-//   full (in the even CTA): both CTAs' copies complete on it; the even CTA's
-//     producer expects the bytes of both;
-//   empty, accumulator full (one in each CTA): completed in both by the even
-//     CTA's commits;
-//   accumulator empty (in the even CTA): one arrival of each of the pair's
-//     sixteen epilogue warps.
-// Waits are bounded as above.  A CTA whose wait runs out stops; its peer's
-// waits then run out too, the even CTA waits for every copy in flight, and
-// both meet at the closing cluster barrier, so neither leaves while the other
-// may still write to its shared memory.
-struct Pair {
-    static constexpr int BN = 256;
-    static constexpr int A_TILE = BM * kRowBytes;
-    static constexpr int STAGE = 2 * A_TILE;
-    static constexpr int STAGES = 7;
-    static constexpr int BARS = 2 * STAGES + 4 + 1;
-    static constexpr int SMEM = STAGES * STAGE + 1024 + 256;
-    static_assert(BARS * 8 + 8 <= 256, "barrier area");
-    static_assert(SMEM <= 227 * 1024, "shared memory budget");
-};
-
-// The shared::cluster address of `addr` (shared::cta) in the cluster's CTA 0.
-__device__ __forceinline__ uint32_t leader_addr(uint32_t addr) {
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
-    return r;
-}
-
-// As tma_load_2d, into this CTA's shared memory, completing on a barrier in
-// either CTA of the pair (shared::cluster address).
-__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void *tmap, uint32_t bar,
-                                                 int c0, int c1) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4}], [%2];"
-        :: "r"(dst), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c0), "r"(c1)
-        : "memory");
-}
-
-__device__ __forceinline__ void mma_f16_pair(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
-                                             uint32_t idesc, uint32_t accumulate) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-                 :: "r"(tmem_d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-                 : "memory");
-}
-
-__device__ __forceinline__ void mma_f8_pair(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
-                                            uint32_t idesc, uint32_t accumulate) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
-                 :: "r"(tmem_d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-                 : "memory");
-}
-
-// Arrive on the barrier at `bar` in both CTAs once every MMA issued so far by
-// this thread has completed.
-__device__ __forceinline__ void commit_pair(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster"
-                 ".multicast::cluster.b64 [%0], %1;"
-                 :: "r"(bar), "h"((uint16_t)3) : "memory");
-}
-
-__device__ __forceinline__ void arrive_cluster(uint32_t cluster_bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];"
-                 :: "r"(cluster_bar) : "memory");
-}
-
-__device__ __forceinline__ void tmem_alloc_pair(uint32_t slot_smem, uint32_t ncols) {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
-                 :: "r"(slot_smem), "r"(ncols) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-}
-
-__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;"
-                 :: "r"(taddr), "r"(ncols) : "memory");
-}
-
-// p.tiles_m counts rows of 256, p.a_bytes is unused.
-template <class O>
-__global__ void __launch_bounds__(kThreads, 1)
-linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                   const Params p) {
-    constexpr int STAGES = Pair::STAGES, ACCS = 2, BN = Pair::BN;
-    extern __shared__ __align__(1024) uint8_t smem_raw[];
-    const uint32_t raw_addr = tc::smem_u32_generic(smem_raw);
-    uint8_t *smem = smem_raw + ((1024 - (raw_addr & 1023)) & 1023);
-    const uint32_t ring = tc::smem_u32_generic(smem);
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + STAGES * Pair::STAGE);
-    const uint32_t full0 = tc::smem_u32_generic(bars);
-    const uint32_t empty0 = full0 + 8 * STAGES;
-    const uint32_t accf0 = empty0 + 8 * STAGES;
-    const uint32_t acce0 = accf0 + 8 * ACCS;
-    const uint32_t done_bar = acce0 + 8 * ACCS;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + Pair::BARS);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = (int)cluster_rank();
-    const int total = p.tiles_m * p.tiles_n;
-    const int first = (int)blockIdx.x / 2, stride = (int)gridDim.x / 2;
-    const int ntiles = first < total ? (total - 1 - first) / stride + 1 : 0;
-
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < STAGES; ++s) {
-            tc::mbar_init(full0 + 8 * s, 1);
-            tc::mbar_init(empty0 + 8 * s, 1);
-        }
-        for (int b = 0; b < ACCS; ++b) {
-            tc::mbar_init(accf0 + 8 * b, 1);
-            tc::mbar_init(acce0 + 8 * b, 2 * kEpiWarps);
-        }
-        tc::mbar_init(done_bar, 1);
-        *abort_flag = 0;
-        tc::fence_barrier_init();
-        tc::tma_prefetch_desc(&tmA);
-        tc::tma_prefetch_desc(&tmB);
-    }
-    if (warp == 1) tmem_alloc_pair(tc::smem_u32_generic(tmem_slot), ACCS * BN);
-    tc::fence_before_sync();
-    __syncthreads();
-    cluster_sync();   // both CTAs' barriers are initialised
-    tc::fence_after_sync();
-    const uint32_t tmem = *tmem_slot;
-    pdl_trigger();
-    pdl_wait();   // nothing below touches global memory before earlier work has finished
-
-    if (warp == 0) {
-        if (elect_one()) {
-            // ---------------- TMA producer: this CTA's halves of A and B
-            const int bk = p.fp8 ? 128 : 64;
-            const uint32_t full_leader = leader_addr(full0);
-            Ring<STAGES> r;
-            bool stop = false;
-            for (int i = 0; i < ntiles && !stop; ++i) {
-                int tm, tn;
-                raster(p, first + i * stride, tm, tn);
-                const int m0 = tm * 2 * BM + rank * BM, n0 = tn * BN + rank * (BN / 2);
-                for (int kb = 0; kb < p.kblocks; ++kb) {
-                    if (r.used == STAGES && !wait(empty0 + 8 * r.s, r.parity ^ 1, abort_flag)) {
-                        stop = true;
-                        break;
-                    }
-                    const uint32_t st = ring + r.s * Pair::STAGE, fb = full_leader + 8 * r.s;
-                    const int k0 = kb * bk;
-                    if (rank == 0) tc::mbar_arrive_expect_tx(full0 + 8 * r.s, 2 * Pair::STAGE);
-                    if (p.a_kmajor) {
-                        tma_load_2d_pair(st, &tmA, fb, k0, m0);
-                    } else {
+            const uint32_t at = ring + (uint32_t)(r * BN * 4) + ((uint32_t)(c ^ (r & 7)) << 4);
+            float4 x[8];
 #pragma unroll
-                        for (int c = 0; c < 2; ++c)
-                            tma_load_2d_pair(st + c * kBox, &tmA, fb, m0 + 64 * c, k0);
-                    }
-                    if (p.b_kmajor) {
-                        tma_load_2d_pair(st + Pair::A_TILE, &tmB, fb, k0, n0);
-                    } else {
+            for (int j = 0; j < 8; ++j)
+                if (j < parts) x[j] = ld_cluster_f4(at, (uint32_t)(CTAS * j + half));
+            float v[4] = {x[0].x, x[0].y, x[0].z, x[0].w};
 #pragma unroll
-                        for (int c = 0; c < 2; ++c)
-                            tma_load_2d_pair(st + Pair::A_TILE + c * kBox, &tmB, fb,
-                                             n0 + 64 * c, k0);
-                    }
-                    r.next();
+            for (int j = 1; j < 8; ++j) {
+                if (j < parts) {
+                    v[0] += x[j].x;
+                    v[1] += x[j].y;
+                    v[2] += x[j].z;
+                    v[3] += x[j].w;
                 }
             }
-            // both CTAs' copies, before the pair leaves
-            if (rank == 0 && *abort_flag) drain_ring(r, full0);
-        }
-    } else if (warp == 1) {
-        if (rank == 0 && elect_one()) {
-            // ---------------- MMA issuer, for both CTAs
-            const uint64_t astep = p.a_kmajor ? 2 : 128, bstep = p.b_kmajor ? 2 : 128;
-            Ring<STAGES> r;
-            bool stop = false;
-            for (int i = 0; i < ntiles && !stop; ++i) {
-                const int b = i % ACCS, u = i / ACCS;
-                if (i >= ACCS && !wait(acce0 + 8 * b, (u - 1) & 1, abort_flag)) break;
-                tc::fence_after_sync();
-                const uint32_t acc = tmem + (uint32_t)(b * BN);
-                for (int kb = 0; kb < p.kblocks; ++kb) {
-                    if (!wait(full0 + 8 * r.s, r.parity, abort_flag)) {
-                        stop = true;
-                        break;
-                    }
-                    tc::fence_after_sync();
-                    const uint32_t st = ring + r.s * Pair::STAGE;
-                    const uint64_t ad = p.a_kmajor ? tc::kmajor_desc<128>(st) : mnmajor_desc(st);
-                    const uint64_t bd = p.b_kmajor ? tc::kmajor_desc<128>(st + Pair::A_TILE)
-                                                   : mnmajor_desc(st + Pair::A_TILE);
-                    if (p.fp8) {
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            mma_f8_pair(acc, ad + kk * astep, bd + kk * bstep, p.idesc,
-                                   (kb | kk) ? 1u : 0u);
-                    } else {
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            mma_f16_pair(acc, ad + kk * astep, bd + kk * bstep, p.idesc,
-                                    (kb | kk) ? 1u : 0u);
-                    }
-                    commit_pair(empty0 + 8 * r.s);
-                    if (kb + 1 == p.kblocks) commit_pair(accf0 + 8 * b);
-                    r.next();
-                }
-            }
-            commit_pair(done_bar);   // tracks every MMA issued above, also on abort
-        }
-    } else {
-        // ---------------- epilogue: this CTA's 128 rows
-        const int q = warp & 3, half = (warp - 2) >> 2;
-        for (int i = 0; i < ntiles; ++i) {
-            const int b = i % ACCS, u = i / ACCS;
-            const bool ok = wait(accf0 + 8 * b, u & 1, abort_flag);
-            __syncwarp();
-            if (!__all_sync(0xffffffffu, ok && !*abort_flag)) break;
-            tc::fence_after_sync();
-            int tm, tn;
-            raster(p, first + i * stride, tm, tn);
-            finish_rows<BN / 2, O>(p.epi, tmem + (uint32_t)(b * BN + half * (BN / 2)), q, lane,
-                                   tm * 2 * BM + rank * BM, tn * BN + half * (BN / 2));
-            tc::fence_before_sync();   // the TMEM loads above precede the release
-            __syncwarp();
-            if (lane == 0) arrive_cluster(leader_addr(acce0 + 8 * b));
+            finish<O, 4>(p.epi, m0 + r, col, v);
         }
     }
-    __syncwarp();
-
-    tc::fence_before_sync();
-    __syncthreads();
     if (*abort_flag && threadIdx.x == 0 && p.error != nullptr) atomicOr(p.error, 1u);
     if (warp == 1) {
         // every MMA issued has completed before TMEM is freed
@@ -657,8 +645,8 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
         (void)tc::mbar_wait(done_bar, 0, &local_abort);
         tc::fence_after_sync();
     }
-    cluster_sync();   // the pair leaves together
-    if (warp == 1) tmem_dealloc_pair(tmem, ACCS * BN);
+    if constexpr (CLUSTER) cluster_sync();   // the cluster leaves together
+    if (warp == 1) tmem_dealloc<CTAS>(tmem, S::TMEM_COLS);
 }
 
 // ------------------------------------------------------------------ host side
@@ -669,19 +657,29 @@ CUtensorMapDataType map_type(int type) {
                                : CU_TENSOR_MAP_DATA_TYPE_UINT8;
 }
 
-// K-major: [rows][K] with a box of 128 bytes x box_rows; MN-major: [K][rows]
-// with a box of 64 x 64.
-bool make_map(CUtensorMap *map, const TcOperand &o, int type, int rows, int K, int box_rows) {
+// A rows x cols row-major matrix read or written in boxes of 128 bytes x
+// box_rows, 128-byte swizzle.
+bool make_map(CUtensorMap *map, const void *base, int type, int64_t ld, int cols, int rows,
+              int box_rows, CUtensorMapL2promotion promote) {
     auto fn = tensor_map_encoder();
     if (!fn) return false;
     const int size = dtype_size(type);
-    const cuuint64_t dims[2] = {(cuuint64_t)(o.kmajor ? K : rows), (cuuint64_t)(o.kmajor ? rows : K)};
-    const cuuint64_t strides[1] = {(cuuint64_t)o.ld * size};
-    const cuuint32_t box[2] = {(cuuint32_t)(kRowBytes / size), (cuuint32_t)(o.kmajor ? box_rows : 64)};
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)ld * size};
+    const cuuint32_t box[2] = {(cuuint32_t)(kRowBytes / size), (cuuint32_t)box_rows};
     const cuuint32_t estr[2] = {1, 1};
-    return fn(map, map_type(type), 2, const_cast<void *>(o.base), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return fn(map, map_type(type), 2, const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, promote,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// K-major: [rows][K] with a box of 128 bytes x box_rows; MN-major: [K][rows]
+// with a box of 64 x 64.
+bool operand_map(CUtensorMap *map, const TcOperand &o, int type, int rows, int K, int box_rows) {
+    return o.kmajor ? make_map(map, o.base, type, o.ld, K, rows, box_rows,
+                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B)
+                    : make_map(map, o.base, type, o.ld, rows, K, 64,
+                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
 uint32_t instruction_desc(int type, int bm, int bn, bool a_kmajor, bool b_kmajor) {
@@ -690,16 +688,36 @@ uint32_t instruction_desc(int type, int bm, int bn, bool a_kmajor, bool b_kmajor
            ((b_kmajor ? 0u : 1u) << 16) | ((uint32_t)(bn >> 3) << 17) | ((uint32_t)(bm >> 4) << 24);
 }
 
-template <int BN, class O, bool SPLIT>
+// Launch attributes: programmatic dependent launch and, above 1, a cluster.
+struct Config {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    Config(long long ctas, int smem, int cluster, cudaStream_t s) {
+        cfg.gridDim = dim3((unsigned)ctas);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = s;
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = (unsigned)cluster;
+        attr[1].val.clusterDim.y = 1;
+        attr[1].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = cluster > 1 ? 2 : 1;
+    }
+};
+
+// `parts`: K parts (SPLIT); `most`: CTAs (CTAS = 1) or pairs that run at once.
+template <int CTAS, int BN, class O, bool SPLIT>
 cudaError_t launch(int type, const TcOperand &A, const TcOperand &B, int K, const LayerEpi &epi,
-                   int split, int sms, cudaStream_t s) {
-    using S = Shape<BN, SPLIT>;
+                   int parts, int most, cudaStream_t s) {
+    using S = Shape<CTAS, BN, SPLIT>;
     static PerContext<bool> configured;
-    const unsigned long long ctx = current_context_id();
     bool done = false;
     cudaError_t e;
-    if (!configured.get(ctx, done)) {
-        e = cudaFuncSetAttribute(linear_tc_kernel<BN, O, SPLIT>,
+    if (!configured.get(current_context_id(), done)) {
+        e = cudaFuncSetAttribute(linear_tc_kernel<CTAS, BN, O, SPLIT>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
         if (e != cudaSuccess) return e;
         configured.put(current_context_id(), true);
@@ -708,7 +726,7 @@ cudaError_t launch(int type, const TcOperand &A, const TcOperand &B, int K, cons
     p.epi = epi;
     const int bk = kRowBytes / dtype_size(type);
     p.kblocks = (K + bk - 1) / bk;
-    p.tiles_m = (epi.M + BM - 1) / BM;
+    p.tiles_m = (epi.M + CTAS * BM - 1) / (CTAS * BM);
     p.tiles_n = (epi.N + BN - 1) / BN;
     p.group_m = raster_group();
     p.a_kmajor = A.kmajor;
@@ -717,52 +735,41 @@ cudaError_t launch(int type, const TcOperand &A, const TcOperand &B, int K, cons
     // whatever the stage held; they are computed and not stored)
     const int a_rows = epi.M < BM ? (epi.M + 7) / 8 * 8 : BM;
     p.a_bytes = A.kmajor ? a_rows * kRowBytes : S::A_TILE;
-    p.idesc = instruction_desc(type, BM, BN, A.kmajor, B.kmajor);
+    p.idesc = instruction_desc(type, CTAS * BM, BN, A.kmajor, B.kmajor);
     p.fp8 = type == SGEMM_E4M3;
     p.error = device_error_word();
-    CUtensorMap tmA, tmB;
-    if (!make_map(&tmA, A, type, epi.M, K, a_rows) || !make_map(&tmB, B, type, epi.N, K, BN))
+    CUtensorMap tmA, tmB, tmY = {}, tmZ = {};
+    if (!operand_map(&tmA, A, type, epi.M, K, a_rows) ||
+        !operand_map(&tmB, B, type, epi.N, K, S::BROWS))
         return cudaErrorInvalidValue;
+    // Y and Z by TMA where every matrix of the epilogue is aligned (a store
+    // writes whole 16-byte granules, so only whole blocks inside N are stored)
+    auto out_map = [&](CUtensorMap *map, const void *base, int64_t ld) {
+        return make_map(map, base, epi.type, ld, epi.N, epi.M, 32, CU_TENSOR_MAP_L2_PROMOTION_NONE);
+    };
+    p.tma = !SPLIT && epi.vec == 16 && out_map(&tmY, epi.Y, epi.ldy) &&
+            (epi.Z == nullptr || out_map(&tmZ, epi.Z, epi.ldz));
     const long long tiles = (long long)p.tiles_m * p.tiles_n;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(SPLIT ? tiles * split : tiles < sms ? tiles : sms));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = S::SMEM;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)split;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = SPLIT ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, linear_tc_kernel<BN, O, SPLIT>, tmA, tmB, p);
+    const long long ctas = SPLIT ? tiles * CTAS * parts : CTAS * (tiles < most ? tiles : most);
+    Config c(ctas, S::SMEM, SPLIT ? CTAS * parts : CTAS, s);
+    return cudaLaunchKernelEx(&c.cfg, linear_tc_kernel<CTAS, BN, O, SPLIT>, tmA, tmB, tmY, tmZ, p);
 }
 
-// Clusters of two linear_pair_kernel CTAs that the device holds at once (an
-// SM without a partner in its group of SMs holds none).
+// Pairs of CTAs that the device holds at once (an SM without a partner in its
+// group of SMs holds none).
 template <class O>
 cudaError_t pair_capacity(int &pairs) {
+    using S = Shape<2, 256, false>;
     static PerContext<int> cached;
-    const unsigned long long ctx = current_context_id();
-    if (cached.get(ctx, pairs)) return cudaSuccess;
-    cudaError_t e = cudaFuncSetAttribute(linear_pair_kernel<O>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, Pair::SMEM);
+    if (cached.get(current_context_id(), pairs)) return cudaSuccess;
+    auto kernel = linear_tc_kernel<2, 256, O, false>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         S::SMEM);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = Pair::SMEM;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaOccupancyMaxActiveClusters(&pairs, linear_pair_kernel<O>, &cfg);
+    Config c(2, S::SMEM, 2, nullptr);
+    c.attr[0] = c.attr[1];
+    c.cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(&pairs, kernel, &c.cfg);
     if (e != cudaSuccess) return e;
     if (pairs < 1) return cudaErrorInvalidConfiguration;
     cached.put(current_context_id(), pairs);
@@ -770,49 +777,14 @@ cudaError_t pair_capacity(int &pairs) {
 }
 
 template <class O>
-cudaError_t launch_pair(int type, const TcOperand &A, const TcOperand &B, int K,
-                        const LayerEpi &epi, int pairs, cudaStream_t s) {
-    Params p;
-    p.epi = epi;
-    const int bk = kRowBytes / dtype_size(type);
-    p.kblocks = (K + bk - 1) / bk;
-    p.tiles_m = (epi.M + 2 * BM - 1) / (2 * BM);
-    p.tiles_n = (epi.N + Pair::BN - 1) / Pair::BN;
-    p.group_m = raster_group();
-    p.a_kmajor = A.kmajor;
-    p.b_kmajor = B.kmajor;
-    p.a_bytes = 0;
-    p.idesc = instruction_desc(type, 2 * BM, Pair::BN, A.kmajor, B.kmajor);
-    p.fp8 = type == SGEMM_E4M3;
-    p.error = device_error_word();
-    CUtensorMap tmA, tmB;
-    if (!make_map(&tmA, A, type, epi.M, K, BM) || !make_map(&tmB, B, type, epi.N, K, Pair::BN / 2))
-        return cudaErrorInvalidValue;
-    const long long tiles = (long long)p.tiles_m * p.tiles_n;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs)));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = Pair::SMEM;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = 2;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, linear_pair_kernel<O>, tmA, tmB, p);
-}
-
-template <class O>
 cudaError_t dispatch(int type, const TcOperand &A, const TcOperand &B, int K, const LayerEpi &epi,
                      cudaStream_t s) {
-    int dev = 0, sms = 0;
+    int dev = 0, sms = 0, pairs = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    e = pair_capacity<O>(pairs);
     if (e != cudaSuccess) return e;
     const int bk = kRowBytes / dtype_size(type);
     const int kblocks = (K + bk - 1) / bk;
@@ -828,19 +800,16 @@ cudaError_t dispatch(int type, const TcOperand &A, const TcOperand &B, int K, co
     if (tiles(128) * 2 <= sms) {
         const int n64 = parts(64), n128 = parts(128);
         if (tiles(64) * n64 >= tiles(128) * n128)
-            return launch<64, O, true>(type, A, B, K, epi, n64, sms, s);
-        return launch<128, O, true>(type, A, B, K, epi, n128, sms, s);
+            return launch<1, 64, O, true>(type, A, B, K, epi, n64, sms, s);
+        return launch<1, 128, O, true>(type, A, B, K, epi, n128, sms, s);
     }
     // waves of one tile an SM or a pair; a pair's 256 x 256 tile is four 128 x
     // 128 ones on two SMs
-    int pairs = 0;
-    e = pair_capacity<O>(pairs);
-    if (e != cudaSuccess) return e;
     const long long t256 = (long long)((epi.M + 255) / 256) * ((epi.N + 255) / 256);
     const double wide = 1.4 * (double)((t256 + pairs - 1) / pairs);
     const double narrow = (double)((tiles(128) + sms - 1) / sms);
-    return wide <= narrow ? launch_pair<O>(type, A, B, K, epi, pairs, s)
-                          : launch<128, O, false>(type, A, B, K, epi, 1, sms, s);
+    return wide <= narrow ? launch<2, 256, O, false>(type, A, B, K, epi, 1, pairs, s)
+                          : launch<1, 128, O, false>(type, A, B, K, epi, 1, sms, s);
 }
 
 }  // namespace ltc
