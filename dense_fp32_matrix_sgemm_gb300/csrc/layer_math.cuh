@@ -191,6 +191,88 @@ __device__ __forceinline__ void finish(const LayerEpi &e, int row, int col, cons
     store_vec<T, G>(static_cast<T *>(e.Y) + row * e.ldy + col, z);
 }
 
+// What the epilogue takes for G fixed columns, loaded once for many rows.
+template <class T, int G>
+struct ColumnTerms {
+    float bias[G], sw[G];
+    __device__ __forceinline__ void load(const LayerEpi &e, int col) {
+#pragma unroll
+        for (int j = 0; j < G; ++j) {
+            const bool in = col + j < e.N;
+            bias[j] = in && e.bias != nullptr ? to_f32(static_cast<const T *>(e.bias)[col + j]) : 0.f;
+            sw[j] = in && e.sw != nullptr ? e.sw[col + j] : 1.f;
+        }
+    }
+};
+
+// G columns col .. of one row, as finish; `t` holds the columns' terms.
+template <class T, int G>
+__device__ __forceinline__ void finish_group(const LayerEpi &e, const ColumnTerms<T, G> &t, int row,
+                                             int col, float (&z)[G]) {
+    const bool vec = e.vec >= G && col + G <= e.N;
+    T *y = static_cast<T *>(e.Y) + row * e.ldy + col;
+    float r[G];
+    if (e.R != nullptr) {
+        const T *p = static_cast<const T *>(e.R) + row * e.ldr + col;
+        if (vec) {
+            const Vec<T, G> v = load_vec<T, G>(p);
+#pragma unroll
+            for (int j = 0; j < G; ++j) r[j] = to_f32(v.v[j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < G; ++j) r[j] = col + j < e.N ? to_f32(p[j]) : 0.f;
+        }
+    }
+    const float sx = e.sx != nullptr ? e.sx[row] : 1.f;
+#pragma unroll
+    for (int j = 0; j < G; ++j) z[j] = fmaf(z[j], sx * t.sw[j], t.bias[j]);
+    auto store = [&](T *p) {
+        if (vec) {
+            store_vec<T, G>(p, z);
+        } else {
+#pragma unroll
+            for (int j = 0; j < G; ++j)
+                if (col + j < e.N) p[j] = from_f32<T>(z[j]);
+        }
+    };
+    if (e.Z != nullptr) store(static_cast<T *>(e.Z) + row * e.ldz + col);
+    activate_all<T>(z, e.act);
+    if (e.R != nullptr) {
+#pragma unroll
+        for (int j = 0; j < G; ++j) z[j] += r[j];
+    }
+    store(y);
+}
+
+// One column of R rows from row0 on, the first `rows` of them; the rows'
+// residuals are in flight together.
+template <class T, int R>
+__device__ __forceinline__ void finish_column(const LayerEpi &e, const ColumnTerms<T, 1> &t,
+                                              int row0, int rows, int col, float (&z)[R]) {
+    float r[R];
+    if (e.R != nullptr) {
+        const T *p = static_cast<const T *>(e.R) + row0 * e.ldr + col;
+#pragma unroll
+        for (int i = 0; i < R; ++i) r[i] = i < rows ? to_f32(p[i * e.ldr]) : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const float sx = e.sx != nullptr && i < rows ? e.sx[row0 + i] : 1.f;
+        z[i] = fmaf(z[i], sx * t.sw[0], t.bias[0]);
+    }
+    if (e.Z != nullptr) {
+        T *p = static_cast<T *>(e.Z) + row0 * e.ldz + col;
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            if (i < rows) p[i * e.ldz] = from_f32<T>(z[i]);
+    }
+    activate_all<T>(z, e.act);
+    T *p = static_cast<T *>(e.Y) + row0 * e.ldy + col;
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+        if (i < rows) p[i * e.ldy] = from_f32<T>(e.R != nullptr ? z[i] + r[i] : z[i]);
+}
+
 // 16 values of a 16-bit type as one 32-byte access (aligned to it): a whole
 // sector each lane.
 __device__ __forceinline__ void load_32b(const void *p, uint32_t (&r)[8]) {
@@ -198,12 +280,6 @@ __device__ __forceinline__ void load_32b(const void *p, uint32_t (&r)[8]) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
                    "=r"(r[6]), "=r"(r[7])
                  : "l"(p) : "memory");
-}
-__device__ __forceinline__ void store_32b(void *p, const uint32_t (&r)[8]) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
-                 :: "l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
-                    "r"(r[6]), "r"(r[7])
-                 : "memory");
 }
 template <class T>
 __device__ __forceinline__ uint32_t pack2(float a, float b);
@@ -226,66 +302,6 @@ __device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t x) {
 template <>
 __device__ __forceinline__ float2 unpack2<__half>(uint32_t x) {
     return __half22float2(*reinterpret_cast<const __half2 *>(&x));
-}
-
-// 32 whole columns col .. col + 31 of `row` (16-bit T), every matrix aligned
-// to 16 elements; `z` holds the accumulators on entry.  The residual's loads
-// are issued first.
-template <class T>
-__device__ __forceinline__ void finish32(const LayerEpi &e, int row, int col, float (&z)[32]) {
-    uint32_t r[2][8];
-    if (e.R != nullptr) {
-        const T *p = static_cast<const T *>(e.R) + row * e.ldr + col;
-        load_32b(p, r[0]);
-        load_32b(p + 16, r[1]);
-    }
-    if (e.sx != nullptr) {
-        const float sx = e.sx[row];
-#pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-            const float4 sw = *reinterpret_cast<const float4 *>(e.sw + col + j);
-            z[j] *= sx * sw.x;
-            z[j + 1] *= sx * sw.y;
-            z[j + 2] *= sx * sw.z;
-            z[j + 3] *= sx * sw.w;
-        }
-    }
-    if (e.bias != nullptr) {
-        const T *p = static_cast<const T *>(e.bias) + col;
-#pragma unroll
-        for (int j = 0; j < 32; j += 8) {
-            const uint4 b = *reinterpret_cast<const uint4 *>(p + j);
-            const uint32_t w[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 f = unpack2<T>(w[i]);
-                z[j + 2 * i] += f.x;
-                z[j + 2 * i + 1] += f.y;
-            }
-        }
-    }
-    auto store = [&](T *p) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            uint32_t w[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = pack2<T>(z[16 * h + 2 * i], z[16 * h + 2 * i + 1]);
-            store_32b(p + 16 * h, w);
-        }
-    };
-    if (e.Z != nullptr) store(static_cast<T *>(e.Z) + row * e.ldz + col);
-    activate_all<T>(z, e.act);
-    if (e.R != nullptr) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float2 f = unpack2<T>(r[h][i]);
-                z[16 * h + 2 * i] += f.x;
-                z[16 * h + 2 * i + 1] += f.y;
-            }
-    }
-    store(static_cast<T *>(e.Y) + row * e.ldy + col);
 }
 
 // ------------------------------------------------------------------ 8-bit rows

@@ -233,6 +233,13 @@ __device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, int rank) {
     return r;
 }
 
+__device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
 __device__ __forceinline__ void arrive_cluster(uint32_t cluster_bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];"
                  :: "r"(cluster_bar) : "memory");
@@ -348,14 +355,18 @@ __device__ __forceinline__ void finish_rows(const Params &p, const void *tmY, co
                 __syncwarp();
                 const int cc = col + 32 * h + lane;
                 if (cc < e.N) {
-#pragma unroll 4
-                    for (int r = 0; r < rows; ++r) {
-                        float x;
-                        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x)
-                                     : "r"(stage + (uint32_t)r * 128u +
-                                           ((uint32_t)((lane >> 2) ^ (r & 7)) << 4) +
-                                           (uint32_t)((lane & 3) * 4)) : "memory");
-                        finish1<O>(e, row0 + r, cc, x);
+                    ColumnTerms<O, 1> t;
+                    t.load(e, cc);
+#pragma unroll 1
+                    for (int r = 0; r < rows; r += 8) {
+                        float x[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x[i])
+                                         : "r"(stage + (uint32_t)(r + i) * 128u +
+                                               ((uint32_t)((lane >> 2) ^ i) << 4) +
+                                               (uint32_t)((lane & 3) * 4)) : "memory");
+                        finish_column<O, 8>(e, t, row0 + r, rows - r, cc, x);
                     }
                 }
                 __syncwarp();
@@ -400,6 +411,66 @@ __device__ __forceinline__ void finish_rows(const Params &p, const void *tmY, co
                 }
         }
         store_block<O>(tmY, stage, lane, row0, col, v);
+    }
+}
+
+// This CTA's share of the rows of the tile that PARTS CTAs hold parts of, in
+// their shared memory at `ring` (row r, 16-byte chunk c at c ^ (r & 7) of its
+// BN * 4 bytes).  A lane keeps four columns of each half of the tile and walks
+// rows, so the columns' terms are loaded once and what is left per row is
+// 2 PARTS loads, the sums in K order and two 8-byte stores; the lanes of a load
+// read consecutive chunks (half as many packets between SMs as with eight
+// consecutive columns a lane).  U rows are in flight.  (Four columns a thread
+// at a time, each with its own row and column arithmetic, took 9 us of a
+// 256 x 256 tile where this takes 3.)
+template <int PARTS, int CTAS, int BN, class O>
+__device__ __forceinline__ void join_parts(const LayerEpi &e, uint32_t ring, int part, int half,
+                                           int m0, int n0, int rows) {
+    constexpr int LPR = BN / 8, RPW = 32 / LPR;   // lanes a row, rows a warp
+    constexpr int STEP = kThreads / 32 * RPW * PARTS;
+    constexpr int U = PARTS == 2 ? 4 : PARTS == 8 ? 1 : 2;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int c = lane % LPR;
+    const int col[2] = {n0 + 4 * c, n0 + 4 * (c + LPR)};
+    if (col[0] >= e.N) return;
+    ColumnTerms<O, 4> t[2];
+    t[0].load(e, col[0]);
+    t[1].load(e, col[1]);
+    uint32_t base[PARTS];
+#pragma unroll
+    for (int j = 0; j < PARTS; ++j) base[j] = cluster_addr(ring, CTAS * j + half);
+    for (int r0 = (warp * PARTS + part) * RPW + lane / LPR; r0 < rows; r0 += U * STEP) {
+        float4 x[U][2][PARTS];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int r = r0 + u * STEP;
+            if (r >= rows) break;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t at = (uint32_t)(r * BN * 4) +
+                                    ((uint32_t)((c + h * LPR) ^ (r & 7)) << 4);
+#pragma unroll
+                for (int j = 0; j < PARTS; ++j) x[u][h][j] = ld_cluster_v4(base[j] + at);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int r = r0 + u * STEP;
+            if (r >= rows) break;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float4 s = x[u][h][0];
+#pragma unroll
+                for (int j = 1; j < PARTS; ++j) {
+                    s.x += x[u][h][j].x;
+                    s.y += x[u][h][j].y;
+                    s.z += x[u][h][j].z;
+                    s.w += x[u][h][j].w;
+                }
+                float v[4] = {s.x, s.y, s.z, s.w};
+                if (col[h] < e.N) finish_group<O, 4>(e, t[h], m0 + r, col[h], v);
+            }
+        }
     }
 }
 
@@ -615,28 +686,11 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         raster(p, first, tm, tn);
         const int m0 = (tm * CTAS + half) * BM;
         const int rows = min(BM, p.epi.M - m0);
-        for (int i = part * kThreads + (int)threadIdx.x; i < rows * (BN / 4);
-             i += parts * kThreads) {
-            const int r = i / (BN / 4), c = i % (BN / 4);
-            const int col = tn * BN + 4 * c;
-            if (col >= p.epi.N) continue;
-            const uint32_t at = ring + (uint32_t)(r * BN * 4) + ((uint32_t)(c ^ (r & 7)) << 4);
-            float4 x[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (j < parts) x[j] = ld_cluster_f4(at, (uint32_t)(CTAS * j + half));
-            float v[4] = {x[0].x, x[0].y, x[0].z, x[0].w};
-#pragma unroll
-            for (int j = 1; j < 8; ++j) {
-                if (j < parts) {
-                    v[0] += x[j].x;
-                    v[1] += x[j].y;
-                    v[2] += x[j].z;
-                    v[3] += x[j].w;
-                }
-            }
-            finish<O, 4>(p.epi, m0 + r, col, v);
-        }
+        const int n0 = tn * BN;
+        if (parts == 1) join_parts<1, CTAS, BN, O>(p.epi, ring, part, half, m0, n0, rows);
+        if (parts == 2) join_parts<2, CTAS, BN, O>(p.epi, ring, part, half, m0, n0, rows);
+        if (parts == 4) join_parts<4, CTAS, BN, O>(p.epi, ring, part, half, m0, n0, rows);
+        if (parts == 8) join_parts<8, CTAS, BN, O>(p.epi, ring, part, half, m0, n0, rows);
     }
     if (*abort_flag && threadIdx.x == 0 && p.error != nullptr) atomicOr(p.error, 1u);
     if (warp == 1) {
