@@ -63,6 +63,7 @@ constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr int kRowBytes = 128;      // of K in a stage
 constexpr int kBox = 8192;          // MN-major box: 64 k x 128 bytes
 constexpr int kSmem = 227 * 1024;
+constexpr int kStage = 4096;         // an epilogue warp's blocks of Y and Z, 32 rows x 64 bytes
 
 template <int CTAS, int BN, bool SPLIT>
 struct Shape {
@@ -70,7 +71,7 @@ struct Shape {
     static constexpr int A_TILE = BM * kRowBytes;
     static constexpr int B_TILE = BROWS * kRowBytes;
     static constexpr int STAGE = A_TILE + B_TILE;
-    static constexpr int STAGING = SPLIT ? 0 : kEpiWarps * 4096;   // an epilogue warp's block
+    static constexpr int STAGING = SPLIT ? 0 : kEpiWarps * kStage;   // epilogue warps' blocks
     static constexpr int STAGES = (kSmem - 1024 - 256 - STAGING) / STAGE;
     static constexpr int ACCS = SPLIT ? 1 : 2;
     static constexpr int TMEM_COLS = ACCS * BN;
@@ -89,7 +90,7 @@ struct Params {
     int a_bytes;             // bytes A's boxes bring to a CTA's stage
     uint32_t idesc;
     int fp8;
-    int tma;                 // Y and Z leave by TMA store where whole blocks of 64 columns do
+    int tma;                 // Y and Z leave by TMA store, whole blocks of 32 columns
     unsigned *error;
 };
 
@@ -245,36 +246,6 @@ __device__ __forceinline__ void arrive_cluster(uint32_t cluster_bar) {
                  :: "r"(cluster_bar) : "memory");
 }
 
-// 64 consecutive columns of this thread's TMEM lane, both loads in flight.
-__device__ __forceinline__ void tmem_ld_64(uint32_t taddr, float (&v)[64]) {
-    uint32_t r[64];
-#define SGEMM_LD32(o)                                                                           \
-    asm volatile(                                                                               \
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "                                               \
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "               \
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, "     \
-        "[%32];"                                                                                \
-        : "=r"(r[o]), "=r"(r[o + 1]), "=r"(r[o + 2]), "=r"(r[o + 3]), "=r"(r[o + 4]),           \
-          "=r"(r[o + 5]), "=r"(r[o + 6]), "=r"(r[o + 7]), "=r"(r[o + 8]), "=r"(r[o + 9]),       \
-          "=r"(r[o + 10]), "=r"(r[o + 11]), "=r"(r[o + 12]), "=r"(r[o + 13]),                   \
-          "=r"(r[o + 14]), "=r"(r[o + 15]), "=r"(r[o + 16]), "=r"(r[o + 17]),                   \
-          "=r"(r[o + 18]), "=r"(r[o + 19]), "=r"(r[o + 20]), "=r"(r[o + 21]),                   \
-          "=r"(r[o + 22]), "=r"(r[o + 23]), "=r"(r[o + 24]), "=r"(r[o + 25]),                   \
-          "=r"(r[o + 26]), "=r"(r[o + 27]), "=r"(r[o + 28]), "=r"(r[o + 29]),                   \
-          "=r"(r[o + 30]), "=r"(r[o + 31])                                                      \
-        : "r"(taddr + o))
-    SGEMM_LD32(0);
-    SGEMM_LD32(32);
-#undef SGEMM_LD32
-    // the registers pass through the wait, so that no use moves above it
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < 64; ++i) {
-        asm volatile("" : "+r"(r[i]));
-        v[i] = __uint_as_float(r[i]);
-    }
-}
-
 // ------------------------------------------------------------------ kernel
 
 __device__ __forceinline__ void raster(const Params &p, int t, int &tm, int &tn) {
@@ -287,37 +258,30 @@ __device__ __forceinline__ void raster(const Params &p, int t, int &tm, int &tn)
     tn = r / rows;
 }
 
-// 64 values of this lane's row into the warp's staging block (32 rows of 128
-// bytes, 16-byte chunk c of row r at c ^ (r & 7): the TMA 128-byte swizzle,
-// conflict-free for a quarter-warp) and from there by TMA store to (col, row0).
+// 32 values of this lane's row into a staging block (32 rows of 64 bytes,
+// 16-byte chunk c of row r at c ^ (r >> 1 & 3): the TMA 64-byte swizzle,
+// conflict-free for a quarter-warp).
 template <class O>
-__device__ __forceinline__ void store_block(const void *map, uint32_t stage, int lane, int row0,
-                                            int col, const float (&v)[64]) {
-    if (lane == 0) tc::bulk_wait_group_read<0>();   // the previous store has read the block
-    __syncwarp();
+__device__ __forceinline__ void stage_row(uint32_t block, int lane, const float (&v)[32]) {
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-        const uint32_t a = pack2<O>(v[8 * c], v[8 * c + 1]), b = pack2<O>(v[8 * c + 2], v[8 * c + 3]);
-        const uint32_t d = pack2<O>(v[8 * c + 4], v[8 * c + 5]),
-                       f = pack2<O>(v[8 * c + 6], v[8 * c + 7]);
+    for (int c = 0; c < 4; ++c)
         asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
-                     :: "r"(stage + (uint32_t)lane * 128u + ((uint32_t)(c ^ (lane & 7)) << 4)),
-                        "r"(a), "r"(b), "r"(d), "r"(f) : "memory");
-    }
-    tc::fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) {
-        tma_store(map, stage, col, row0);
-        tc::bulk_commit_group();
-    }
+                     :: "r"(block + (uint32_t)lane * 64u +
+                            ((uint32_t)(c ^ ((lane >> 1) & 3)) << 4)),
+                        "r"(pack2<O>(v[8 * c], v[8 * c + 1])),
+                        "r"(pack2<O>(v[8 * c + 2], v[8 * c + 3])),
+                        "r"(pack2<O>(v[8 * c + 4], v[8 * c + 5])),
+                        "r"(pack2<O>(v[8 * c + 6], v[8 * c + 7])) : "memory");
 }
 
 // Finishes COLS columns of the 32 tile rows of TMEM lane quarter q, a row a
-// lane, 64 columns at a time: the epilogue runs on the accumulators in
-// registers, whole 128-byte row pieces leave by TMA.  What TMA cannot store
-// (rows that are not 16-byte aligned, the last block of a width that is not a
-// multiple of 64) passes through the staging block in fp32, 32 columns at a
-// time, and is finished a row at a time with a column a lane.
+// lane, 32 columns at a time: the epilogue runs on the accumulators in
+// registers, Y and Z leave by TMA as whole 64-byte row pieces.  What TMA cannot
+// store (rows that are not 16-byte aligned, the last block of a width that is
+// not a multiple of 32) passes through the staging block in fp32 and is
+// finished with a column a lane.  The loop is kept rolled: a problem of one
+// tile a CTA runs this code once, and fetching it cold costs more than running
+// it.
 template <int COLS, class O>
 __device__ __forceinline__ void finish_rows(const Params &p, const void *tmY, const void *tmZ,
                                             uint32_t acc, int q, int lane, int m0, int n0,
@@ -326,57 +290,51 @@ __device__ __forceinline__ void finish_rows(const Params &p, const void *tmY, co
     const int row0 = m0 + 32 * q;
     if (row0 >= e.M) return;
     const int row = row0 + lane;
+    const bool in = row < e.M;
     const uint32_t lane_base = acc + ((uint32_t)(32 * q) << 16);
+    const float sx = e.sx != nullptr && in ? e.sx[row] : 1.f;
 #pragma unroll 1
-    for (int c = 0; c < COLS / 64 && n0 + 64 * c < e.N; ++c) {
-        const int col = n0 + 64 * c;
-        const bool fast = p.tma && col + 64 <= e.N;
-        uint32_t res[4][8];
-        if (fast && e.R != nullptr && row < e.M) {
+    for (int c = 0; c < COLS / 32 && n0 + 32 * c < e.N; ++c) {
+        const int col = n0 + 32 * c;
+        const bool fast = p.tma && col + 32 <= e.N;
+        uint32_t res[2][8];
+        if (fast && e.R != nullptr && in) {
             const O *r = static_cast<const O *>(e.R) + row * e.ldr + col;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) load_32b(r + 16 * i, res[i]);
+            load_32b(r, res[0]);
+            load_32b(r + 16, res[1]);
         }
-        float v[64];
-        __syncwarp();   // the loads are warp-collective
-        tmem_ld_64(lane_base + (uint32_t)(64 * c), v);
+        if (lane == 0) tc::bulk_wait_group_read<0>();   // the staging block is free
+        float v[32];
+        __syncwarp();   // the load is warp-collective
+        tc::tmem_ld_32(lane_base + (uint32_t)(32 * c), v);
         if (!fast) {
             const int rows = min(32, e.M - row0);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (lane == 0) tc::bulk_wait_group_read<0>();
-                __syncwarp();   // the block is free
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    tc::st_shared_v4(stage + (uint32_t)lane * 128u +
-                                         ((uint32_t)(j ^ (lane & 7)) << 4),
-                                     v[32 * h + 4 * j], v[32 * h + 4 * j + 1],
-                                     v[32 * h + 4 * j + 2], v[32 * h + 4 * j + 3]);
-                __syncwarp();
-                const int cc = col + 32 * h + lane;
-                if (cc < e.N) {
-                    ColumnTerms<O, 1> t;
-                    t.load(e, cc);
+            for (int j = 0; j < 8; ++j)
+                tc::st_shared_v4(stage + (uint32_t)lane * 128u + ((uint32_t)(j ^ (lane & 7)) << 4),
+                                 v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+            __syncwarp();
+            const int cc = col + lane;
+            if (cc < e.N) {
+                ColumnTerms<O, 1> t;
+                t.load(e, cc);
 #pragma unroll 1
-                    for (int r = 0; r < rows; r += 8) {
-                        float x[8];
+                for (int r = 0; r < rows; r += 8) {
+                    float x[8];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x[i])
-                                         : "r"(stage + (uint32_t)(r + i) * 128u +
-                                               ((uint32_t)((lane >> 2) ^ i) << 4) +
-                                               (uint32_t)((lane & 3) * 4)) : "memory");
-                        finish_column<O, 8>(e, t, row0 + r, rows - r, cc, x);
-                    }
+                    for (int i = 0; i < 8; ++i)
+                        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x[i])
+                                     : "r"(stage + (uint32_t)(r + i) * 128u +
+                                           ((uint32_t)((lane >> 2) ^ i) << 4) +
+                                           (uint32_t)((lane & 3) * 4)) : "memory");
+                    finish_column<O, 8>(e, t, row0 + r, rows - r, cc, x);
                 }
-                __syncwarp();
             }
-            continue;
+            continue;   // (the next block's __syncwarp keeps it from overwriting this one)
         }
         if (e.sx != nullptr) {
-            const float sx = row < e.M ? e.sx[row] : 0.f;
 #pragma unroll
-            for (int j = 0; j < 64; j += 4) {
+            for (int j = 0; j < 32; j += 4) {
                 const float4 sw = *reinterpret_cast<const float4 *>(e.sw + col + j);
                 v[j] *= sx * sw.x;
                 v[j + 1] *= sx * sw.y;
@@ -387,7 +345,7 @@ __device__ __forceinline__ void finish_rows(const Params &p, const void *tmY, co
         if (e.bias != nullptr) {
             const O *b = static_cast<const O *>(e.bias) + col;
 #pragma unroll
-            for (int j = 0; j < 64; j += 8) {
+            for (int j = 0; j < 32; j += 8) {
                 const uint4 u = *reinterpret_cast<const uint4 *>(b + j);
                 const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -398,11 +356,11 @@ __device__ __forceinline__ void finish_rows(const Params &p, const void *tmY, co
                 }
             }
         }
-        if (e.Z != nullptr) store_block<O>(tmZ, stage, lane, row0, col, v);
+        if (e.Z != nullptr) stage_row<O>(stage + 2048u, lane, v);
         activate_all<O>(v, e.act);
-        if (e.R != nullptr && row < e.M) {
+        if (e.R != nullptr && in) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const float2 f = unpack2<O>(res[i][j]);
@@ -410,7 +368,14 @@ __device__ __forceinline__ void finish_rows(const Params &p, const void *tmY, co
                     v[16 * i + 2 * j + 1] += f.y;
                 }
         }
-        store_block<O>(tmY, stage, lane, row0, col, v);
+        stage_row<O>(stage, lane, v);
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            tma_store(tmY, stage, col, row0);
+            if (e.Z != nullptr) tma_store(tmZ, stage + 2048u, col, row0);
+            tc::bulk_commit_group();
+        }
     }
 }
 
@@ -627,7 +592,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     } else {
         // ---------------- epilogue: this CTA's rows
         const int q = warp & 3, side = (warp - 2) >> 2;
-        const uint32_t stage = ring + STAGES * S::STAGE + (uint32_t)(warp - 2) * 4096u;
+        const uint32_t stage = ring + STAGES * S::STAGE + (uint32_t)((warp - 2) * kStage);
         for (int i = 0; i < ntiles; ++i) {
             const int b = i % ACCS, u = i / ACCS;
             const bool ok = wait(accf0 + 8 * b, u & 1, abort_flag);
@@ -671,7 +636,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                     tc::mbar_arrive(acce0 + 8 * b);
             }
         }
-        if (!SPLIT && lane == 0) tc::bulk_wait_group<0>();   // the stores are done
+        if (!SPLIT && lane == 0) tc::bulk_wait_group_read<0>();   // the stores have left
     }
     __syncwarp();
 
@@ -687,14 +652,14 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         const int m0 = (tm * CTAS + half) * BM;
         const int rows = min(BM, p.epi.M - m0);
         const int n0 = tn * BN;
-        if (parts == 1) join_parts<1, CTAS, BN, O>(p.epi, ring, part, half, m0, n0, rows);
         if (parts == 2) join_parts<2, CTAS, BN, O>(p.epi, ring, part, half, m0, n0, rows);
         if (parts == 4) join_parts<4, CTAS, BN, O>(p.epi, ring, part, half, m0, n0, rows);
         if (parts == 8) join_parts<8, CTAS, BN, O>(p.epi, ring, part, half, m0, n0, rows);
     }
     if (*abort_flag && threadIdx.x == 0 && p.error != nullptr) atomicOr(p.error, 1u);
-    if (warp == 1) {
-        // every MMA issued has completed before TMEM is freed
+    if (warp == 1 && *abort_flag) {
+        // every MMA issued has completed before TMEM is freed (otherwise the
+        // epilogue has waited for the last one)
         int local_abort = 0;
         (void)tc::mbar_wait(done_bar, 0, &local_abort);
         tc::fence_after_sync();
@@ -711,28 +676,29 @@ CUtensorMapDataType map_type(int type) {
                                : CU_TENSOR_MAP_DATA_TYPE_UINT8;
 }
 
-// A rows x cols row-major matrix read or written in boxes of 128 bytes x
-// box_rows, 128-byte swizzle.
+// A rows x cols row-major matrix read or written in boxes of box_bytes (128 or
+// 64, with the swizzle of that span) x box_rows.
 bool make_map(CUtensorMap *map, const void *base, int type, int64_t ld, int cols, int rows,
-              int box_rows, CUtensorMapL2promotion promote) {
+              int box_bytes, int box_rows, CUtensorMapL2promotion promote) {
     auto fn = tensor_map_encoder();
     if (!fn) return false;
     const int size = dtype_size(type);
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)ld * size};
-    const cuuint32_t box[2] = {(cuuint32_t)(kRowBytes / size), (cuuint32_t)box_rows};
+    const cuuint32_t box[2] = {(cuuint32_t)(box_bytes / size), (cuuint32_t)box_rows};
     const cuuint32_t estr[2] = {1, 1};
     return fn(map, map_type(type), 2, const_cast<void *>(base), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, promote,
+              CU_TENSOR_MAP_INTERLEAVE_NONE,
+              box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, promote,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // K-major: [rows][K] with a box of 128 bytes x box_rows; MN-major: [K][rows]
 // with a box of 64 x 64.
 bool operand_map(CUtensorMap *map, const TcOperand &o, int type, int rows, int K, int box_rows) {
-    return o.kmajor ? make_map(map, o.base, type, o.ld, K, rows, box_rows,
+    return o.kmajor ? make_map(map, o.base, type, o.ld, K, rows, kRowBytes, box_rows,
                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B)
-                    : make_map(map, o.base, type, o.ld, rows, K, 64,
+                    : make_map(map, o.base, type, o.ld, rows, K, kRowBytes, 64,
                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
@@ -799,7 +765,7 @@ cudaError_t launch(int type, const TcOperand &A, const TcOperand &B, int K, cons
     // Y and Z by TMA where every matrix of the epilogue is aligned (a store
     // writes whole 16-byte granules, so only whole blocks inside N are stored)
     auto out_map = [&](CUtensorMap *map, const void *base, int64_t ld) {
-        return make_map(map, base, epi.type, ld, epi.N, epi.M, 32, CU_TENSOR_MAP_L2_PROMOTION_NONE);
+        return make_map(map, base, epi.type, ld, epi.N, epi.M, 64, 32, CU_TENSOR_MAP_L2_PROMOTION_NONE);
     };
     p.tma = !SPLIT && epi.vec == 16 && out_map(&tmY, epi.Y, epi.ldy) &&
             (epi.Z == nullptr || out_map(&tmZ, epi.Z, epi.ldz));
@@ -853,6 +819,7 @@ cudaError_t dispatch(int type, const TcOperand &A, const TcOperand &B, int K, co
     };
     if (tiles(128) * 2 <= sms) {
         const int n64 = parts(64), n128 = parts(128);
+        if (n64 == 1) return launch<1, 64, O, false>(type, A, B, K, epi, 1, sms, s);
         if (tiles(64) * n64 >= tiles(128) * n128)
             return launch<1, 64, O, true>(type, A, B, K, epi, n64, sms, s);
         return launch<1, 128, O, true>(type, A, B, K, epi, n128, sms, s);
