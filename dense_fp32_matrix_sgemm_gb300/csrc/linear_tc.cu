@@ -51,6 +51,7 @@
 #include "gemm_args.h"
 #include "layer_math.cuh"
 #include "layers.h"
+#include "tc_issue.cuh"
 #include "tc_utils.cuh"
 #include "tma_encode.h"
 
@@ -79,7 +80,7 @@ struct Shape {
     static constexpr int SMEM = STAGES * STAGE + STAGING + 1024 + 256;
     static_assert(TMEM_COLS >= 32 && TMEM_COLS <= 512, "tensor memory");
     static_assert(BARS * 8 + 8 <= 256, "barrier area");
-    static_assert(BM * BN * 4 <= STAGES * STAGE, "the split's partial tile fits the ring");
+    static_assert(!SPLIT || BM * BN * 4 <= STAGES * STAGE, "a part of a tile fits the ring");
 };
 
 struct Params {
@@ -93,53 +94,6 @@ struct Params {
     int tma;                 // Y and Z leave by TMA store, whole blocks of 32 columns
     unsigned *error;
 };
-
-// True in one lane of a converged warp.  The producer's and the MMA issuer's
-// loops run in such a lane: elect.sync tells the compiler that a single thread
-// is active, so descriptors and coordinates stay in uniform registers.  In the
-// same loops under "lane == 0" an MMA took about 226 clocks to issue, against
-// the 128 that it runs (4096 x 8192 x 4096: 224 us, 160 elected).
-__device__ __forceinline__ bool elect_one() {
-    uint32_t p;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\t"
-                 "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-    return p != 0;
-}
-
-// Bounded wait that polls before it reads the clock or the abort word: a
-// stage is handed over every 512 clocks, and those two reads in front of each
-// poll alone held the pair kernel at 157 us where this takes 140.
-__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int *abort) {
-    if (tc::mbar_try_wait(bar, parity)) return true;
-    return tc::mbar_wait(bar, parity, abort);
-}
-
-// Position in a ring of N stages: the stage, the parity of its current round,
-// and how many stages have been used so far (up to N).
-template <int N>
-struct Ring {
-    int s = 0, parity = 0, used = 0;
-    __device__ __forceinline__ void next() {
-        if (used < N) ++used;
-        if (++s == N) {
-            s = 0;
-            parity ^= 1;
-        }
-    }
-};
-
-// Waits (bounded) until the latest fill of every used stage has landed: a CTA
-// that gave up does not leave with copies in flight.
-template <int N>
-__device__ __forceinline__ void drain_ring(const Ring<N> &r, uint32_t full0) {
-    for (int s = 0; s < r.used; ++s) {
-        const int parity = s < r.s ? r.parity : r.parity ^ 1;
-        const long long t0 = clock64();
-        while (!tc::mbar_try_wait(full0 + 8 * s, parity) &&
-               clock64() - t0 < tc::kWaitLimitCycles) {
-        }
-    }
-}
 
 // ------------------------------------------------------------------ PTX
 
@@ -511,19 +465,19 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     pdl_wait();   // nothing below touches global memory before earlier work has finished
 
     if (warp == 0) {
-        if (elect_one()) {
+        if (tc::elect_one()) {
             // ---------------- TMA producer: this CTA's rows of A and B
             const int bk = p.fp8 ? 128 : 64;
             const uint32_t tx = (uint32_t)(CTAS * (p.a_bytes + S::B_TILE));
             const uint32_t fulls = CTAS == 2 ? cluster_addr(full0, leader) : full0;
-            Ring<STAGES> r;
+            tc::Ring<STAGES> r;
             bool stop = false;
             for (int i = 0; i < ntiles && !stop; ++i) {
                 int tm, tn;
                 raster(p, first + i * stride, tm, tn);
                 const int m0 = (tm * CTAS + half) * BM, n0 = tn * BN + half * S::BROWS;
                 for (int kb = kb0; kb < kb1; ++kb) {
-                    if (r.used == STAGES && !wait(empty0 + 8 * r.s, r.parity ^ 1, abort_flag)) {
+                    if (r.used == STAGES && !tc::wait(empty0 + 8 * r.s, r.parity ^ 1, abort_flag)) {
                         stop = true;
                         break;
                     }
@@ -548,21 +502,21 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                 }
             }
             // the copies of both CTAs, before the pair leaves
-            if (half == 0 && *abort_flag) drain_ring(r, full0);
+            if (half == 0 && *abort_flag) tc::drain_ring(r, full0);
         }
     } else if (warp == 1) {
-        if (half == 0 && elect_one()) {
+        if (half == 0 && tc::elect_one()) {
             // ---------------- MMA issuer, for the whole pair
             const uint64_t astep = p.a_kmajor ? 2 : 128, bstep = p.b_kmajor ? 2 : 128;
-            Ring<STAGES> r;
+            tc::Ring<STAGES> r;
             bool stop = false;
             for (int i = 0; i < ntiles && !stop; ++i) {
                 const int b = i % ACCS, u = i / ACCS;
-                if (i >= ACCS && !wait(acce0 + 8 * b, (u - 1) & 1, abort_flag)) break;
+                if (i >= ACCS && !tc::wait(acce0 + 8 * b, (u - 1) & 1, abort_flag)) break;
                 tc::fence_after_sync();
                 const uint32_t acc = tmem + (uint32_t)(b * BN);
                 for (int kb = 0; kb < nk; ++kb) {
-                    if (!wait(full0 + 8 * r.s, r.parity, abort_flag)) {
+                    if (!tc::wait(full0 + 8 * r.s, r.parity, abort_flag)) {
                         stop = true;
                         break;
                     }
@@ -595,7 +549,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         const uint32_t stage = ring + STAGES * S::STAGE + (uint32_t)((warp - 2) * kStage);
         for (int i = 0; i < ntiles; ++i) {
             const int b = i % ACCS, u = i / ACCS;
-            const bool ok = wait(accf0 + 8 * b, u & 1, abort_flag);
+            const bool ok = tc::wait(accf0 + 8 * b, u & 1, abort_flag);
             __syncwarp();
             // one warp-uniform decision: the TMEM loads are warp-collective
             if (!__all_sync(0xffffffffu, ok && !*abort_flag)) break;
@@ -728,7 +682,8 @@ struct Config {
     }
 };
 
-// `parts`: K parts (SPLIT); `most`: CTAs (CTAS = 1) or pairs that run at once.
+// `parts`: K parts (SPLIT); `most`: CTAs (CTAS = 1) or pairs that run at once
+// (persistent).
 template <int CTAS, int BN, class O, bool SPLIT>
 cudaError_t launch(int type, const TcOperand &A, const TcOperand &B, int K, const LayerEpi &epi,
                    int parts, int most, cudaStream_t s) {
@@ -775,62 +730,90 @@ cudaError_t launch(int type, const TcOperand &A, const TcOperand &B, int K, cons
     return cudaLaunchKernelEx(&c.cfg, linear_tc_kernel<CTAS, BN, O, SPLIT>, tmA, tmB, tmY, tmZ, p);
 }
 
-// Pairs of CTAs that the device holds at once (an SM without a partner in its
-// group of SMs holds none).
-template <class O>
-cudaError_t pair_capacity(int &pairs) {
-    using S = Shape<2, 256, false>;
-    static PerContext<int> cached;
-    if (cached.get(current_context_id(), pairs)) return cudaSuccess;
-    auto kernel = linear_tc_kernel<2, 256, O, false>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         S::SMEM);
+// Clusters of 2, 4 and 8 CTAs of these kernels that the device holds at once
+// (on GB300 76, 36 and 15: SMs come in groups that whole clusters do not fill).
+struct Capacity {
+    int sms, clusters[3];
+    int of(int size) const { return size == 1 ? sms : clusters[size == 2 ? 0 : size == 4 ? 1 : 2]; }
+};
+
+cudaError_t capacity(Capacity &cap) {
+    using S = Shape<1, 128, true>;
+    static PerContext<Capacity> cached;
+    if (cached.get(current_context_id(), cap)) return cudaSuccess;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess)
+        e = cudaDeviceGetAttribute(&cap.sms, cudaDevAttrMultiProcessorCount, dev);
+    auto kernel = linear_tc_kernel<1, 128, __nv_bfloat16, true>;
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+    for (int i = 0; i < 3 && e == cudaSuccess; ++i) {
+        Config c(2 << i, S::SMEM, 2 << i, nullptr);
+        c.attr[0] = c.attr[1];
+        c.cfg.numAttrs = 1;
+        e = cudaOccupancyMaxActiveClusters(&cap.clusters[i], kernel, &c.cfg);
+    }
     if (e != cudaSuccess) return e;
-    Config c(2, S::SMEM, 2, nullptr);
-    c.attr[0] = c.attr[1];
-    c.cfg.numAttrs = 1;
-    e = cudaOccupancyMaxActiveClusters(&pairs, kernel, &c.cfg);
-    if (e != cudaSuccess) return e;
-    if (pairs < 1) return cudaErrorInvalidConfiguration;
-    cached.put(current_context_id(), pairs);
+    if (cap.sms < 1 || cap.clusters[0] < 1) return cudaErrorInvalidConfiguration;
+    cached.put(current_context_id(), cap);
     return cudaSuccess;
 }
 
+// The tile and schedule, by their cost in microseconds.  Measured on GB300
+// (graph of 20 calls, bf16, weights out of L2):
+//   a 64- or 128-wide tile of one CTA takes about 0.21 us a stage of K, a 256 x
+//   256 tile of a pair 0.27; what does not depend on K is about 5 us a launch,
+//   6.5 with pairs; joining the parts of a split tile about 1 us and, for 128
+//   rows, 3 more (6 for a pair's tile).
+// The persistent schedules pay the rest once and the stages in waves; a split
+// tile must find all its clusters resident at once.  The choice against the
+// others there, in us: 64 x 1024 x 4096 128-wide in 8 parts 7.4 (whole 18.1, in
+// 4 9.0), 128 x 4096 x 4096 in 4 parts 12.6 (64-wide in 2 13.9, whole 19.5),
+// 256 x 4096 x 4096 in 2 15.8 (19.2), 512 x 4096 x 4096 whole 128-wide 19.9
+// (pairs 23.7, pairs in 2 parts 20.6), 1024 x 2048 x 8192 pairs in 2 28.3
+// (pairs 41.6, 128-wide 36.0), 2048^3 pairs 16.1 (19.9), 1024^3 64-wide 6.9 (7.5;
+// pairs 10.0).
 template <class O>
 cudaError_t dispatch(int type, const TcOperand &A, const TcOperand &B, int K, const LayerEpi &epi,
                      cudaStream_t s) {
-    int dev = 0, sms = 0, pairs = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return e;
-    e = pair_capacity<O>(pairs);
+    Capacity cap;
+    cudaError_t e = capacity(cap);
     if (e != cudaSuccess) return e;
     const int bk = kRowBytes / dtype_size(type);
     const int kblocks = (K + bk - 1) / bk;
-    auto tiles = [&](int bn) {
-        return (long long)((epi.M + BM - 1) / BM) * ((epi.N + bn - 1) / bn);
+    struct {
+        int ctas, bn, parts;
+        double us;
+    } best = {0, 0, 0, 1e30};
+    auto consider = [&](int ctas, int bn, int parts) {
+        const long long tiles = (long long)((epi.M + ctas * BM - 1) / (ctas * BM)) *
+                                ((epi.N + bn - 1) / bn);
+        const int room = cap.of(ctas * parts);
+        if (parts > 1 && (tiles > room || kblocks < 2 * parts)) return;
+        const double stage = ctas == 2 ? 0.27 : 0.21;
+        double us = (double)((tiles + room - 1) / room) * ((kblocks + parts - 1) / parts) * stage +
+                    (ctas == 2 ? 6.5 : 5.0);
+        if (parts > 1)
+            us += 1.0 + (ctas == 2 ? 5.0 : 3.0 * bn / 128) * (epi.M < BM ? epi.M : BM) / BM;
+        if (us < best.us) best = {ctas, bn, parts, us};
     };
-    // parts of K for tiles that leave at least half the SMs idle
-    auto parts = [&](int bn) {
-        int n = 1;
-        while (n < 8 && tiles(bn) * n * 2 <= sms && n * 4 <= kblocks) n *= 2;
-        return n;
-    };
-    if (tiles(128) * 2 <= sms) {
-        const int n64 = parts(64), n128 = parts(128);
-        if (n64 == 1) return launch<1, 64, O, false>(type, A, B, K, epi, 1, sms, s);
-        if (tiles(64) * n64 >= tiles(128) * n128)
-            return launch<1, 64, O, true>(type, A, B, K, epi, n64, sms, s);
-        return launch<1, 128, O, true>(type, A, B, K, epi, n128, sms, s);
+    consider(2, 256, 1);
+    consider(1, 64, 1);
+    consider(1, 128, 1);
+    for (int parts = 2; parts <= 8; parts *= 2) {
+        if (parts <= 4) consider(2, 256, parts);
+        consider(1, 128, parts);
+        consider(1, 64, parts);
     }
-    // waves of one tile an SM or a pair; a pair's 256 x 256 tile is four 128 x
-    // 128 ones on two SMs
-    const long long t256 = (long long)((epi.M + 255) / 256) * ((epi.N + 255) / 256);
-    const double wide = 1.4 * (double)((t256 + pairs - 1) / pairs);
-    const double narrow = (double)((tiles(128) + sms - 1) / sms);
-    return wide <= narrow ? launch<2, 256, O, false>(type, A, B, K, epi, 1, pairs, s)
-                          : launch<1, 128, O, false>(type, A, B, K, epi, 1, sms, s);
+    if (best.parts > 1) {
+        if (best.ctas == 2) return launch<2, 256, O, true>(type, A, B, K, epi, best.parts, 0, s);
+        return best.bn == 128 ? launch<1, 128, O, true>(type, A, B, K, epi, best.parts, 0, s)
+                              : launch<1, 64, O, true>(type, A, B, K, epi, best.parts, 0, s);
+    }
+    if (best.ctas == 2) return launch<2, 256, O, false>(type, A, B, K, epi, 1, cap.of(2), s);
+    return best.bn == 128 ? launch<1, 128, O, false>(type, A, B, K, epi, 1, cap.sms, s)
+                          : launch<1, 64, O, false>(type, A, B, K, epi, 1, cap.sms, s);
 }
 
 }  // namespace ltc

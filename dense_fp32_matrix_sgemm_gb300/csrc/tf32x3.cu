@@ -361,8 +361,8 @@ __device__ __forceinline__ void raster(const Tf32x3Params &p, int bid, int &z, i
 //   lane 0.  `cc` counts the chunks staged so far (across calls), picks the
 //   buffer and says when to wait for the store two chunks back.
 //   Otherwise: each thread stores its own row, with the epilogue applied.
-template <class CFG, class PT>
-__device__ __forceinline__ void store_tile_rows(const PT &p, const CUtensorMap *tmC,
+template <class CFG>
+__device__ __forceinline__ void store_tile_rows(const Tf32x3Params &p, const CUtensorMap *tmC,
                                                 uint32_t acc, int q, int lane, int z, int m0,
                                                 int n0, uint32_t stage, int &cc) {
     constexpr int BN = CFG::BN, ACC_COLS = CFG::ACC_COLS;
@@ -424,14 +424,7 @@ __device__ __forceinline__ void store_tile_rows(const PT &p, const CUtensorMap *
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] += w[j];
         }
-        if constexpr (kLayer<PT>) {
-#pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-                const float w[4] = {v[j], v[j + 1], v[j + 2], v[j + 3]};
-                if (row < p.M && n0 + 32 * c + j < p.N)
-                    finish<float, 4>(p.le, row, n0 + 32 * c + j, w);
-            }
-        } else if (row < p.M) {
+        if (row < p.M) {
             const int col0 = n0 + 32 * c;
             if (!(p.alpha == 1.f && p.beta == 0.f && p.bias == nullptr)) {
 #pragma unroll
@@ -545,13 +538,13 @@ __device__ __forceinline__ void convert_stage(uint8_t *st, int t) {
 
 // tmA / tmB: the operand's planes, or (RAW) its raw rows; tmAlo / tmBlo: the
 // lo-only plane of an operand in RAW but not CONV (unused otherwise).
-template <class CFG, int ACC_BUFS, int RAW, int CONV, class PT>
+template <class CFG, int ACC_BUFS, int RAW, int CONV>
 __global__ void __launch_bounds__(Persist<CFG, ACC_BUFS, RAW, CONV>::THREADS, 1)
 tf32x3_persistent_kernel(const __grid_constant__ CUtensorMap tmA,
                          const __grid_constant__ CUtensorMap tmB,
                          const __grid_constant__ CUtensorMap tmAlo,
                          const __grid_constant__ CUtensorMap tmBlo,
-                         const __grid_constant__ CUtensorMap tmC, const PT p) {
+                         const __grid_constant__ CUtensorMap tmC, const Tf32x3Params p) {
     using P = Persist<CFG, ACC_BUFS, RAW, CONV>;
     constexpr int BK = CFG::BK, STAGES = CFG::STAGES, PLANES = CFG::PLANES;
     constexpr int BN = CFG::BN, ACC_COLS = CFG::ACC_COLS;
@@ -824,6 +817,30 @@ struct Chunked {
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
 };
 
+// The layer epilogue on the first `rows` rows (from row0 on) of a 32 x 32 fp32
+// block that the warp has staged at `stage` (16-byte chunk j of row r at chunk
+// j ^ (r & 7) of its 128 bytes): a column a lane, eight rows at a time, so each
+// access is a 128-byte row segment and eight residual loads are in flight (one
+// row at a time, 2049 x 3071 x 1537 with a residual took 203 us, its plain
+// product 96).
+__device__ __forceinline__ void finish_staged(const LayerEpi &e, uint32_t stage, int lane, int row0,
+                                              int rows, int col) {
+    if (col >= e.N) return;
+    ColumnTerms<float, 1> t;
+    t.load(e, col);
+#pragma unroll 1
+    for (int r = 0; r < rows; r += 8) {
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x[i])
+                         : "r"(stage + (uint32_t)(r + i) * 128u +
+                               ((uint32_t)((lane >> 2) ^ i) << 4) + (uint32_t)((lane & 3) * 4))
+                         : "memory");
+        finish_column<float, 8>(e, t, row0 + r, rows - r, col, x);
+    }
+}
+
 // Stores 32 rows x COLS columns of running sums from the calling warp's
 // threads (thread `lane` holds row m0 + 32q + lane, columns n0 .. n0 + COLS
 // - 1 of a rows x cols matrix), 32 columns at a time through the warp's 4 KB
@@ -870,6 +887,10 @@ __device__ __forceinline__ void store_running_rows(const PT &p, const CUtensorMa
         }
         __syncwarp();
         const int col = n0 + 32 * c + lane;
+        if constexpr (kLayer<PT>) {
+            finish_staged(p.le, stage, lane, row0, min(32, p.M - row0), col);
+            continue;
+        }
         const uint32_t cofs = (uint32_t)((lane & 3) * 4);
         const int rows = min(32, p.M - row0);
 #pragma unroll 1
@@ -880,9 +901,7 @@ __device__ __forceinline__ void store_running_rows(const PT &p, const CUtensorMa
                          : "r"(stage + (uint32_t)r * 128u +
                                ((uint32_t)((lane >> 2) ^ (r & 7)) << 4) + cofs)
                          : "memory");
-            if constexpr (kLayer<PT>) {
-                if (col < p.N) finish1<float>(p.le, row0 + r, col, v);
-            } else if (col < p.N) {
+            if (col < p.N) {
                 float *cp = p.C + (int64_t)z * p.strideC + (int64_t)(row0 + r) * p.ldc + col;
                 if (!(p.alpha == 1.f && p.beta == 0.f && p.bias == nullptr)) {
                     const float old = p.beta != 0.f ? *cp : 0.f;
@@ -1470,8 +1489,8 @@ size_t plane_bytes(int64_t rows, int64_t K, int64_t batch, int planes) {
 // a raw operand that is not converted gets a lo-only plane and its map in
 // tmAlo / tmBlo (which are left empty otherwise).
 template <class CFG>
-cudaError_t prepare(const GemmArgs &a, bool layer, bool transA, bool transB, int raw, int conv, void *ws,
-                    cudaStream_t s, CUtensorMap &tmA, CUtensorMap &tmB, CUtensorMap &tmAlo,
+cudaError_t prepare(const GemmArgs &a, bool layer, bool transA, bool transB, int raw, int conv,
+                    void *ws, cudaStream_t s, CUtensorMap &tmA, CUtensorMap &tmB, CUtensorMap &tmAlo,
                     CUtensorMap &tmBlo, CUtensorMap &tmC, Tf32x3Params &p) {
     constexpr int PLANES = CFG::PLANES;
     const int Kp = plane_row_floats(a.K);
@@ -1569,12 +1588,12 @@ cudaError_t ensure_smem(Kern kern, int bytes, PerContext<bool> &configured) {
 }
 
 // One CTA per SM, walking the tiles (see tf32x3_persistent_kernel).
-template <class CFG, int ACC_BUFS, int RAW, int CONV, class PT>
-cudaError_t launch_persistent_raw(const GemmArgs &a, const LayerEpi *le, bool transA, bool transB, void *ws,
+template <class CFG, int ACC_BUFS, int RAW, int CONV>
+cudaError_t launch_persistent_raw(const GemmArgs &a, bool transA, bool transB, void *ws,
                                   cudaStream_t s, CUtensorMap &tmA, CUtensorMap &tmB) {
     using P = Persist<CFG, ACC_BUFS, RAW, CONV>;
     static PerContext<bool> configured;
-    cudaError_t e = ensure_smem(tf32x3_persistent_kernel<CFG, ACC_BUFS, RAW, CONV, PT>, P::SMEM_BYTES,
+    cudaError_t e = ensure_smem(tf32x3_persistent_kernel<CFG, ACC_BUFS, RAW, CONV>, P::SMEM_BYTES,
                                 configured);
     if (e != cudaSuccess) return e;
     int dev = 0, sms = 0;
@@ -1583,11 +1602,9 @@ cudaError_t launch_persistent_raw(const GemmArgs &a, const LayerEpi *le, bool tr
     e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
     CUtensorMap tmC, tmAlo, tmBlo;
-    PT p;
-    e = prepare<CFG>(a, kLayer<PT>, transA, transB, RAW, CONV, ws, s, tmA, tmB, tmAlo, tmBlo, tmC,
-                     p);
+    Tf32x3Params p;
+    e = prepare<CFG>(a, false, transA, transB, RAW, CONV, ws, s, tmA, tmB, tmAlo, tmBlo, tmC, p);
     if (e != cudaSuccess) return e;
-    if constexpr (kLayer<PT>) p.le = *le;
     const long long tiles = (long long)a.batch * p.tiles_m * p.tiles_n;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(tiles < sms ? tiles : sms));
@@ -1601,7 +1618,7 @@ cudaError_t launch_persistent_raw(const GemmArgs &a, const LayerEpi *le, bool tr
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, tf32x3_persistent_kernel<CFG, ACC_BUFS, RAW, CONV, PT>, tmA, tmB,
+    e = cudaLaunchKernelEx(&cfg, tf32x3_persistent_kernel<CFG, ACC_BUFS, RAW, CONV>, tmA, tmB,
                            tmAlo, tmBlo, tmC, p);
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
@@ -1640,30 +1657,30 @@ constexpr int kChunkMinK = 256;
 // Launches with the runtime choice `conv` (a subset of RAW) of converted
 // operands; a combination the configuration does not provide launches
 // nothing and returns an error (the caller never asks for one).
-template <class CFG, int ACC_BUFS, int RAW, class PT>
-cudaError_t launch_conv(const GemmArgs &a, const LayerEpi *le, bool transA, bool transB, void *ws, cudaStream_t s,
+template <class CFG, int ACC_BUFS, int RAW>
+cudaError_t launch_conv(const GemmArgs &a, bool transA, bool transB, void *ws, cudaStream_t s,
                         CUtensorMap &tmA, CUtensorMap &tmB, int conv) {
     if constexpr (CFG::PLANES == 1) {
         // one term: an operand is raw only when it is rounded in the stage
         if (conv == RAW)
-            return launch_persistent_raw<CFG, ACC_BUFS, RAW, RAW, PT>(a, le, transA, transB, ws, s, tmA, tmB);
+            return launch_persistent_raw<CFG, ACC_BUFS, RAW, RAW>(a, transA, transB, ws, s, tmA, tmB);
     } else if constexpr (CFG::BN == 128) {
         switch (conv) {
             case 0:
-                return launch_persistent_raw<CFG, ACC_BUFS, RAW, 0, PT>(a, le, transA, transB, ws, s, tmA, tmB);
+                return launch_persistent_raw<CFG, ACC_BUFS, RAW, 0>(a, transA, transB, ws, s, tmA, tmB);
             case 1:
                 if constexpr ((RAW & 1) != 0)
-                    return launch_persistent_raw<CFG, ACC_BUFS, RAW, 1, PT>(a, le, transA, transB, ws, s, tmA,
+                    return launch_persistent_raw<CFG, ACC_BUFS, RAW, 1>(a, transA, transB, ws, s, tmA,
                                                                         tmB);
                 break;
             case 2:
                 if constexpr ((RAW & 2) != 0)
-                    return launch_persistent_raw<CFG, ACC_BUFS, RAW, 2, PT>(a, le, transA, transB, ws, s, tmA,
+                    return launch_persistent_raw<CFG, ACC_BUFS, RAW, 2>(a, transA, transB, ws, s, tmA,
                                                                         tmB);
                 break;
             case 3:
                 if constexpr (RAW == 3)
-                    return launch_persistent_raw<CFG, ACC_BUFS, 3, 3, PT>(a, le, transA, transB, ws, s, tmA, tmB);
+                    return launch_persistent_raw<CFG, ACC_BUFS, 3, 3>(a, transA, transB, ws, s, tmA, tmB);
                 break;
             default:
                 break;
@@ -1671,13 +1688,13 @@ cudaError_t launch_conv(const GemmArgs &a, const LayerEpi *le, bool transA, bool
     } else {
         // the 256-wide three-term tile (K > 256 only): lo planes, no converters
         if (conv == 0)
-            return launch_persistent_raw<CFG, ACC_BUFS, RAW, 0, PT>(a, le, transA, transB, ws, s, tmA, tmB);
+            return launch_persistent_raw<CFG, ACC_BUFS, RAW, 0>(a, transA, transB, ws, s, tmA, tmB);
     }
     return cudaErrorInvalidValue;
 }
 
-template <class CFG, int ACC_BUFS, class PT>
-cudaError_t launch_persistent(const GemmArgs &a, const LayerEpi *le, bool transA, bool transB, void *ws,
+template <class CFG, int ACC_BUFS>
+cudaError_t launch_persistent(const GemmArgs &a, bool transA, bool transB, void *ws,
                               cudaStream_t s) {
     const int64_t tiles_m = (a.M + BM - 1) / BM, tiles_n = (a.N + CFG::BN - 1) / CFG::BN;
     // converting an operand whose panels `reuse` tiles read
@@ -1706,10 +1723,10 @@ cudaError_t launch_persistent(const GemmArgs &a, const LayerEpi *le, bool transA
         if ((raw & 2) && convert(tiles_m)) conv |= 2;
     }
     switch (raw) {
-        case 1: return launch_conv<CFG, ACC_BUFS, 1, PT>(a, le, transA, transB, ws, s, tmA, tmB, conv);
-        case 2: return launch_conv<CFG, ACC_BUFS, 2, PT>(a, le, transA, transB, ws, s, tmA, tmB, conv);
-        case 3: return launch_conv<CFG, ACC_BUFS, 3, PT>(a, le, transA, transB, ws, s, tmA, tmB, conv);
-        default: return launch_persistent_raw<CFG, ACC_BUFS, 0, 0, PT>(a, le, transA, transB, ws, s, tmA, tmB);
+        case 1: return launch_conv<CFG, ACC_BUFS, 1>(a, transA, transB, ws, s, tmA, tmB, conv);
+        case 2: return launch_conv<CFG, ACC_BUFS, 2>(a, transA, transB, ws, s, tmA, tmB, conv);
+        case 3: return launch_conv<CFG, ACC_BUFS, 3>(a, transA, transB, ws, s, tmA, tmB, conv);
+        default: return launch_persistent_raw<CFG, ACC_BUFS, 0, 0>(a, transA, transB, ws, s, tmA, tmB);
     }
 }
 
@@ -1752,8 +1769,8 @@ ChunkedPlan chunked_plan_for(const GemmArgs &a, int sms) {
 }
 
 template <class CFG, int RAW, class PT>
-cudaError_t launch_chunked_raw(const GemmArgs &a, const LayerEpi *le, bool transA, bool transB, void *ws,
-                               size_t ws_bytes, cudaStream_t s, CUtensorMap &tmA,
+cudaError_t launch_chunked_raw(const GemmArgs &a, const LayerEpi *le, bool transA, bool transB,
+                               void *ws, size_t ws_bytes, cudaStream_t s, CUtensorMap &tmA,
                                CUtensorMap &tmB) {
     using P = Chunked<CFG>;
     static PerContext<bool> configured;
@@ -1797,8 +1814,8 @@ cudaError_t launch_chunked_raw(const GemmArgs &a, const LayerEpi *le, bool trans
     CUtensorMap tmP = {};
     if (pl.split > 0 && !make_part_map(&tmP, p.part, pl.split * pl.tail, CFG::BN))
         return cudaErrorInvalidValue;
-    e = cudaLaunchKernelEx(&cfg, tf32x3_chunked_kernel<CFG, RAW, PT>, tmA, tmB, tmAlo, tmBlo, tmC, tmP,
-                           p);
+    e = cudaLaunchKernelEx(&cfg, tf32x3_chunked_kernel<CFG, RAW, PT>, tmA, tmB, tmAlo, tmBlo, tmC,
+                           tmP, p);
     if (e != cudaSuccess) return e;
     if (pl.split == 0) return cudaGetLastError();
     // the tail tiles' sums, as a programmatic dependent of the GEMM
@@ -1821,8 +1838,8 @@ cudaError_t launch_chunked_raw(const GemmArgs &a, const LayerEpi *le, bool trans
 // each slice straddles sectors, and the split kernel's planes are the cheaper
 // route (3000 x 2000 x 1500 with row-major A of ld 1500).
 template <class CFG, class PT>
-cudaError_t launch_chunked(const GemmArgs &a, const LayerEpi *le, bool transA, bool transB, void *ws, size_t ws_bytes,
-                           cudaStream_t s) {
+cudaError_t launch_chunked(const GemmArgs &a, const LayerEpi *le, bool transA, bool transB,
+                           void *ws, size_t ws_bytes, cudaStream_t s) {
     static_assert(CFG::PLANES == 2, "three terms");
     auto raw_ok = [&](const float *X, int64_t ld, int64_t sX, bool kcontig) {
         return kcontig && reinterpret_cast<uintptr_t>(X) % 128 == 0 && ld % 32 == 0 &&
@@ -1837,10 +1854,14 @@ cudaError_t launch_chunked(const GemmArgs &a, const LayerEpi *le, bool transA, b
         make_raw_map<CFG>(&tmB, a.B, a.N, a.K, a.ldb, a.strideB, a.batch, CFG::BN))
         raw |= 2;
     switch (raw) {
-        case 1: return launch_chunked_raw<CFG, 1, PT>(a, le, transA, transB, ws, ws_bytes, s, tmA, tmB);
-        case 2: return launch_chunked_raw<CFG, 2, PT>(a, le, transA, transB, ws, ws_bytes, s, tmA, tmB);
-        case 3: return launch_chunked_raw<CFG, 3, PT>(a, le, transA, transB, ws, ws_bytes, s, tmA, tmB);
-        default: return launch_chunked_raw<CFG, 0, PT>(a, le, transA, transB, ws, ws_bytes, s, tmA, tmB);
+        case 1:
+            return launch_chunked_raw<CFG, 1, PT>(a, le, transA, transB, ws, ws_bytes, s, tmA, tmB);
+        case 2:
+            return launch_chunked_raw<CFG, 2, PT>(a, le, transA, transB, ws, ws_bytes, s, tmA, tmB);
+        case 3:
+            return launch_chunked_raw<CFG, 3, PT>(a, le, transA, transB, ws, ws_bytes, s, tmA, tmB);
+        default:
+            return launch_chunked_raw<CFG, 0, PT>(a, le, transA, transB, ws, ws_bytes, s, tmA, tmB);
     }
 }
 
@@ -1935,10 +1956,8 @@ size_t tf32_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t batch) {
 namespace {
 
 template <class PT>   // Tf32x3Params, or Tf32x3LayerParams with the layer epilogue `le`
-cudaError_t launch_three_terms(const GemmArgs &a, const LayerEpi *le, bool transA, bool transB,
-                               void *ws, size_t ws_bytes, cudaStream_t s) {
-    if (a.K <= tf32x3::kChunkMinK)
-        return tf32x3::launch_persistent<Tf32x3Narrow, 2, PT>(a, le, transA, transB, ws, s);
+cudaError_t launch_chunked_tiles(const GemmArgs &a, const LayerEpi *le, bool transA, bool transB,
+                                 void *ws, size_t ws_bytes, cudaStream_t s) {
     return tc_wide_tile(a, 3)
                ? tf32x3::launch_chunked<Tf32x3Wide, PT>(a, le, transA, transB, ws, ws_bytes, s)
                : tf32x3::launch_chunked<Tf32x3Narrow, PT>(a, le, transA, transB, ws, ws_bytes, s);
@@ -1948,9 +1967,14 @@ cudaError_t launch_three_terms(const GemmArgs &a, const LayerEpi *le, bool trans
 
 cudaError_t launch_tf32x3(const GemmArgs &a, bool transA, bool transB, void *ws, size_t ws_bytes,
                           cudaStream_t s) {
-    return launch_three_terms<tf32x3::Tf32x3Params>(a, nullptr, transA, transB, ws, ws_bytes, s);
+    if (a.K <= tf32x3::kChunkMinK)
+        return tf32x3::launch_persistent<Tf32x3Narrow, 2>(a, transA, transB, ws, s);
+    return launch_chunked_tiles<tf32x3::Tf32x3Params>(a, nullptr, transA, transB, ws, ws_bytes, s);
 }
 
+// The layer epilogue is in the K-chunked kernel alone, which takes any K: its
+// running sums are in registers when a tile leaves, so the epilogue runs where
+// no TMEM load (a warp-collective instruction) is near.
 cudaError_t launch_linear_tf32x3(const float *X, int64_t ldx, const float *W, int64_t ldw,
                                  bool transW, int K, const LayerEpi &epi, void *ws,
                                  size_t ws_bytes, cudaStream_t s) {
@@ -1972,15 +1996,14 @@ cudaError_t launch_linear_tf32x3(const float *X, int64_t ldx, const float *W, in
     const bool plain = epi.act == SGEMM_ACT_NONE && epi.bias == nullptr && epi.R == nullptr &&
                        epi.Z == nullptr;
     if (plain)
-        return launch_three_terms<tf32x3::Tf32x3Params>(a, nullptr, false, transW, ws, ws_bytes, s);
-    return launch_three_terms<tf32x3::Tf32x3LayerParams>(a, &epi, false, transW, ws, ws_bytes, s);
+        return launch_tf32x3(a, false, transW, ws, ws_bytes, s);
+    return launch_chunked_tiles<tf32x3::Tf32x3LayerParams>(a, &epi, false, transW, ws, ws_bytes, s);
 }
 
 cudaError_t launch_tf32(const GemmArgs &a, bool transA, bool transB, void *ws, cudaStream_t s) {
-    using P = tf32x3::Tf32x3Params;
     return tc_wide_tile(a, 1)
-               ? tf32x3::launch_persistent<Tf32Wide, 2, P>(a, nullptr, transA, transB, ws, s)
-               : tf32x3::launch_persistent<Tf32Narrow, 2, P>(a, nullptr, transA, transB, ws, s);
+               ? tf32x3::launch_persistent<Tf32Wide, 2>(a, transA, transB, ws, s)
+               : tf32x3::launch_persistent<Tf32Narrow, 2>(a, transA, transB, ws, s);
 }
 
 int set_tf32x3_chunk_k(int chunk_k) {
