@@ -48,6 +48,73 @@ __device__ __forceinline__ __half from_f32<__half>(float x) {
     return __float2half_rn(x);
 }
 
+template <class T>
+__device__ __forceinline__ uint32_t pack2(float a, float b);
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+template <class T>
+__device__ __forceinline__ float2 unpack2(uint32_t x);
+template <>
+__device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t x) {
+    return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+}
+template <>
+__device__ __forceinline__ float2 unpack2<__half>(uint32_t x) {
+    return __half22float2(*reinterpret_cast<const __half2 *>(&x));
+}
+
+// One 16-byte access of W elements (or, W = 1, one element), kept as the words
+// that were loaded: 16-bit values held one to a register cost registers and
+// moves (the norm's backward pass ran at 2.5 TB/s with them).
+template <class T, int W>
+struct Raw {
+    static_assert(W * sizeof(T) == 16, "16-byte accesses");
+    uint4 u;
+    __device__ __forceinline__ void load(const T *p) { u = *reinterpret_cast<const uint4 *>(p); }
+    __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void get(float (&f)[W]) const {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (W == 4) {
+                f[i] = __uint_as_float(w[i]);
+            } else {
+                const float2 v = unpack2<T>(w[i]);
+                f[2 * i] = v.x;
+                f[2 * i + 1] = v.y;
+            }
+        }
+    }
+};
+template <class T>
+struct Raw<T, 1> {
+    T u;
+    __device__ __forceinline__ void load(const T *p) { u = *p; }
+    __device__ __forceinline__ void zero() { u = from_f32<T>(0.f); }
+    __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = to_f32(u); }
+};
+
+// W floats rounded to T and stored as one access.
+template <class T, int W>
+__device__ __forceinline__ void put(T *p, const float (&f)[W]) {
+    if constexpr (W == 1) {
+        *p = from_f32<T>(f[0]);
+    } else if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<float4 *>(p) = make_float4(f[0], f[1], f[2], f[3]);
+    } else {
+        *reinterpret_cast<uint4 *>(p) = make_uint4(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]),
+                                                   pack2<T>(f[4], f[5]), pack2<T>(f[6], f[7]));
+    }
+}
+
 // N consecutive elements as one access of N * sizeof(T) bytes (4, 8 or 16),
 // aligned to its size.
 template <class T, int N>
@@ -281,29 +348,6 @@ __device__ __forceinline__ void load_32b(const void *p, uint32_t (&r)[8]) {
                    "=r"(r[6]), "=r"(r[7])
                  : "l"(p) : "memory");
 }
-template <class T>
-__device__ __forceinline__ uint32_t pack2(float a, float b);
-template <>
-__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&v);
-}
-template <>
-__device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
-    const __half2 v = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&v);
-}
-template <class T>
-__device__ __forceinline__ float2 unpack2(uint32_t x);
-template <>
-__device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t x) {
-    return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
-}
-template <>
-__device__ __forceinline__ float2 unpack2<__half>(uint32_t x) {
-    return __half22float2(*reinterpret_cast<const __half2 *>(&x));
-}
-
 // ------------------------------------------------------------------ 8-bit rows
 
 constexpr float kE4m3Max = 448.f;

@@ -46,13 +46,13 @@ __global__ void __launch_bounds__(kThreads) dz_kernel(const DzArgs a) {
         T *dz = static_cast<T *>(a.dZ) + c;
         constexpr int U = 4;   // rows in flight
         for (int r = r0 + ty; r < r1; r += U * kRowLanes) {
-            Vec<T, W> vy[U], vz[U];
+            Raw<T, W> vy[U], vz[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int row = r + u * kRowLanes;
                 if (row < r1) {
-                    vy[u] = load_vec<T, W>(dy + row * a.lddy);
-                    if (a.act != SGEMM_ACT_NONE) vz[u] = load_vec<T, W>(z + row * a.ldz);
+                    vy[u].load(dy + row * a.lddy);
+                    if (a.act != SGEMM_ACT_NONE) vz[u].load(z + row * a.ldz);
                 }
             }
 #pragma unroll
@@ -60,13 +60,16 @@ __global__ void __launch_bounds__(kThreads) dz_kernel(const DzArgs a) {
                 const int row = r + u * kRowLanes;
                 if (row >= r1) continue;
                 float g[W];
+                vy[u].get(g);
+                if (a.act != SGEMM_ACT_NONE) {
+                    float f[W];
+                    vz[u].get(f);
 #pragma unroll
-                for (int j = 0; j < W; ++j) {
-                    g[j] = to_f32(vy[u].v[j]);
-                    if (a.act != SGEMM_ACT_NONE) g[j] *= activate_grad<T>(to_f32(vz[u].v[j]), a.act);
-                    sum[j] += g[j];
+                    for (int j = 0; j < W; ++j) g[j] *= activate_grad<T>(f[j], a.act);
                 }
-                if (a.dZ != nullptr) store_vec<T, W>(dz + row * a.lddz, g);
+#pragma unroll
+                for (int j = 0; j < W; ++j) sum[j] += g[j];
+                if (a.dZ != nullptr) put<T, W>(dz + row * a.lddz, g);
             }
         }
     }

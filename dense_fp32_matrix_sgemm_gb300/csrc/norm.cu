@@ -16,8 +16,8 @@
 // Rows wider than that are read twice, the second time from L2 (the *_wide
 // kernels); bases or rows that are not 16-byte aligned take W = 1.
 // The weight's gradient sums over rows: every group walks rows with the
-// stride of the grid and keeps its columns' sums in registers, the groups'
-// sums go to the workspace, and one more pass adds them in a fixed order.
+// stride of the grid and keeps its columns' sums in registers, the CTAs' sums
+// go to the workspace, and one more pass adds them in a fixed order.
 #include <cstdint>
 
 #include <cuda_runtime.h>
@@ -59,11 +59,12 @@ __device__ __forceinline__ float2 group_reduce(float sum, float top, float2 *red
 
 // W elements from p, or zeros.
 template <class T, int W>
-__device__ __forceinline__ Vec<T, W> load_or_zero(const T *p, bool in) {
-    Vec<T, W> v;
-    if (in) return load_vec<T, W>(p);
-#pragma unroll
-    for (int i = 0; i < W; ++i) v.v[i] = from_f32<T>(0.f);
+__device__ __forceinline__ Raw<T, W> load_or_zero(const T *p, bool in) {
+    Raw<T, W> v;
+    if (in)
+        v.load(p);
+    else
+        v.zero();
     return v;
 }
 
@@ -100,7 +101,7 @@ __global__ void __launch_bounds__(MAXT) row_kernel(const RowArgs a) {
     const T *x = static_cast<const T *>(a.X) + row * a.ldx;
     const T *r = static_cast<const T *>(a.R) + row * a.ldr;
     const T *w = static_cast<const T *>(a.w);
-    Vec<T, W> vx[NV], vr[NV];
+    Raw<T, W> vx[NV], vr[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (i * blockDim.x + threadIdx.x) * W;
@@ -113,19 +114,22 @@ __global__ void __launch_bounds__(MAXT) row_kernel(const RowArgs a) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (i * blockDim.x + threadIdx.x) * W;
+        vx[i].get(s[i]);
+        if (NORM && a.R != nullptr) {
+            float r[W];
+            vr[i].get(r);
 #pragma unroll
-        for (int j = 0; j < W; ++j) {
-            s[i][j] = to_f32(vx[i].v[j]);
-            if (NORM && a.R != nullptr) s[i][j] += to_f32(vr[i].v[j]);
+            for (int j = 0; j < W; ++j) s[i][j] += r[j];
         }
         if constexpr (NORM) {
             if (a.S != nullptr && live && c < a.D)
-                store_vec<T, W>(static_cast<T *>(a.S) + row * a.lds + c, s[i]);
-            const Vec<T, W> vw = load_or_zero<T, W>(w + c, c < a.D);
+                put<T, W>(static_cast<T *>(a.S) + row * a.lds + c, s[i]);
+            float fw[W];
+            load_or_zero<T, W>(w + c, c < a.D).get(fw);
 #pragma unroll
             for (int j = 0; j < W; ++j) {
                 sum = fmaf(s[i][j], s[i][j], sum);
-                s[i][j] *= to_f32(vw.v[j]);
+                s[i][j] *= fw[j];
             }
         }
         if constexpr (QUANT) {
@@ -162,7 +166,7 @@ __global__ void __launch_bounds__(MAXT) row_kernel(const RowArgs a) {
             float y[W];
 #pragma unroll
             for (int j = 0; j < W; ++j) y[j] = s[i][j] * mul;
-            store_vec<T, W>(out + c, y);
+            put<T, W>(out + c, y);
         }
     }
 }
@@ -233,7 +237,7 @@ __global__ void __launch_bounds__(MAXT) grad_kernel(const GradArgs a) {
     const int64_t group = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     const int64_t groups = (int64_t)gridDim.x * blockDim.y;
     const float inv_d = 1.f / (float)a.D;
-    Vec<T, W> vw[NV];
+    Raw<T, W> vw[NV];
     float dw[NV][W];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -245,28 +249,50 @@ __global__ void __launch_bounds__(MAXT) grad_kernel(const GradArgs a) {
     // every group of the CTA takes as many turns as its first one (barriers)
     const int64_t first = (int64_t)blockIdx.x * blockDim.y;
     const int turns = first < a.rows ? (int)((a.rows - 1 - first) / groups) + 1 : 0;
-    for (int t = 0; t < turns; ++t) {
-        const int64_t row = group + t * groups;
+    // the next row's loads are issued before this row's sums where registers
+    // allow it (CTAs of up to 512 threads)
+    constexpr bool AHEAD = MAXT <= 512;
+    Raw<T, W> ny[NV], ns[NV], nd[NV];
+    float nr = 0.f;
+    auto load_row = [&](int64_t row) {
         const bool live = row < a.rows;
-        Vec<T, W> vy[NV], vs[NV], vd[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * blockDim.x + threadIdx.x) * W;
             const bool in = live && c < a.D;
-            vy[i] = load_or_zero<T, W>(static_cast<const T *>(a.dY) + row * a.lddy + c, in);
-            vs[i] = load_or_zero<T, W>(static_cast<const T *>(a.S) + row * a.lds + c, in);
-            if (a.dS != nullptr)
-                vd[i] = load_or_zero<T, W>(static_cast<const T *>(a.dS) + row * a.ldds + c, in);
+            ny[i] = load_or_zero<T, W>(static_cast<const T *>(a.dY) + row * a.lddy + c, in);
+            ns[i] = load_or_zero<T, W>(static_cast<const T *>(a.S) + row * a.lds + c, in);
+            nd[i] = load_or_zero<T, W>(static_cast<const T *>(a.dS) + row * a.ldds + c,
+                                       in && a.dS != nullptr);
         }
-        const float rstd = live ? a.rstd[row] : 0.f;
+        nr = live ? a.rstd[row] : 0.f;
+    };
+    if (AHEAD && turns > 0) load_row(group);
+    for (int t = 0; t < turns; ++t) {
+        const int64_t row = group + t * groups;
+        const bool live = row < a.rows;
+        if (!AHEAD) load_row(row);
+        Raw<T, W> vy[NV], vs[NV], vd[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            vy[i] = ny[i];
+            vs[i] = ns[i];
+            vd[i] = nd[i];
+        }
+        const float rstd = nr;
+        if (AHEAD && t + 1 < turns) load_row(row + groups);
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
+            float dy[W], s[W], w[W];
+            vy[i].get(dy);
+            vs[i].get(s);
+            vw[i].get(w);
 #pragma unroll
             for (int j = 0; j < W; ++j) {
-                const float dy = to_f32(vy[i].v[j]), s = to_f32(vs[i].v[j]);
-                sum = fmaf(dy * to_f32(vw[i].v[j]), s, sum);
-                dw[i][j] = fmaf(dy * rstd, s, dw[i][j]);
+                const float ys = dy[j] * s[j];
+                sum = fmaf(ys, w[j], sum);
+                dw[i][j] = fmaf(ys, rstd, dw[i][j]);
             }
         }
         // two buffers: a warp may reach the next turn's while another still
@@ -276,23 +302,43 @@ __global__ void __launch_bounds__(MAXT) grad_kernel(const GradArgs a) {
         for (int i = 0; i < NV; ++i) {
             const int c = (i * blockDim.x + threadIdx.x) * W;
             if (!live || c >= a.D) continue;
-            float dx[W];
+            float dy[W], s[W], w[W], ds[W], dx[W];
+            vy[i].get(dy);
+            vs[i].get(s);
+            vw[i].get(w);
+            vd[i].get(ds);
 #pragma unroll
-            for (int j = 0; j < W; ++j) {
-                dx[j] = rstd * fmaf(-k, to_f32(vs[i].v[j]),
-                                    to_f32(vy[i].v[j]) * to_f32(vw[i].v[j]));
-                if (a.dS != nullptr) dx[j] += to_f32(vd[i].v[j]);
-            }
-            store_vec<T, W>(static_cast<T *>(a.dX) + row * a.lddx + c, dx);
+            for (int j = 0; j < W; ++j)
+                dx[j] = fmaf(rstd, fmaf(-k, s[j], dy[j] * w[j]), ds[j]);
+            put<T, W>(static_cast<T *>(a.dX) + row * a.lddx + c, dx);
         }
     }
     if (a.partial == nullptr) return;
+    // one row of partial sums a CTA: its groups' sums are added in their order
+    // (groups share a CTA only up to 256 threads)
+    __shared__ float sums[256 * NV * W];
+    const int width = blockDim.x * NV * W;
+    if (blockDim.y > 1) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < W; ++j)
+                sums[threadIdx.y * width + (i * W + j) * blockDim.x + threadIdx.x] = dw[i][j];
+        __syncthreads();
+        if (threadIdx.y > 0) return;
+        for (int y = 1; y < (int)blockDim.y; ++y)
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int j = 0; j < W; ++j)
+                    dw[i][j] += sums[y * width + (i * W + j) * blockDim.x + threadIdx.x];
+    }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (i * blockDim.x + threadIdx.x) * W;
 #pragma unroll
         for (int j = 0; j < W; ++j)
-            if (c + j < a.D) a.partial[group * a.D + c + j] = dw[i][j];
+            if (c + j < a.D) a.partial[(int64_t)blockIdx.x * a.D + c + j] = dw[i][j];
     }
 }
 
@@ -415,7 +461,10 @@ GradShape grad_shape(int type, int64_t rows, int64_t D, bool vec) {
         g.sh = {kMaxThreads, 1};
     }
     const int64_t need = (rows + g.sh.groups - 1) / g.sh.groups;
-    const int per_sm = g.sh.tpr * g.sh.groups > 512 ? 1 : g.sh.tpr * g.sh.groups > 256 ? 2 : 4;
+    // up to 128 registers a thread: 512 threads an SM, the row of each group and
+    // its next one in flight
+    const int threads = g.sh.tpr * g.sh.groups;
+    const int per_sm = threads > 512 ? 1 : 512 / threads;
     const int64_t most = (int64_t)152 * per_sm;
     g.ctas = (int)(need < most ? need : most);
     return g;
@@ -456,8 +505,7 @@ cudaError_t launch_quantize_rows(int type, int64_t rows, int64_t D, const void *
 int rmsnorm_backward_parts(int type, int64_t rows, int64_t D) {
     const norm::GradShape a = norm::grad_shape(type, rows, D, true);
     const norm::GradShape b = norm::grad_shape(type, rows, D, false);
-    const int pa = a.ctas * a.sh.groups, pb = b.ctas * b.sh.groups;
-    return pa > pb ? pa : pb;
+    return a.ctas > b.ctas ? a.ctas : b.ctas;
 }
 
 cudaError_t launch_add_rmsnorm_backward(int type, int64_t rows, int64_t D, const void *dY,
@@ -476,7 +524,7 @@ cudaError_t launch_add_rmsnorm_backward(int type, int64_t rows, int64_t D, const
                     : type == SGEMM_BF16 ? norm::grad_dispatch<__nv_bfloat16>(a, g, s)
                                          : norm::grad_dispatch<__half>(a, g, s);
     if (e != cudaSuccess || dw == nullptr) return e;
-    return launch_column_sum(type, partial, g.ctas * g.sh.groups, D, dw, s);
+    return launch_column_sum(type, partial, g.ctas, D, dw, s);
 }
 
 }  // namespace sgemm
