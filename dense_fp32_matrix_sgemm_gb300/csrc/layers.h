@@ -51,11 +51,23 @@ cudaError_t launch_linear_tc(int in_type, const TcOperand &A, const TcOperand &B
 cudaError_t launch_linear_rows(int in_type, const void *X, int64_t ldx, const void *W, int64_t ldw,
                                int transW, int K, const LayerEpi &epi, cudaStream_t s);
 
-// f32 on the tensor cores (three TF32 terms) with the layer's epilogue;
-// workspace as launch_tf32x3.  tf32x3.cu.
-cudaError_t launch_linear_tf32x3(const float *X, int64_t ldx, const float *W, int64_t ldw,
-                                 bool transW, int K, const LayerEpi &epi, void *ws,
-                                 size_t ws_bytes, cudaStream_t s);
+// f32 on the tensor cores (linear_f32.cu): every operand as three bf16 planes
+// that sum to it, in the orientation it is stored in.
+struct F32Operand {   // rows x cols as stored, and where its planes go
+    const float *X;
+    int64_t ld, rows, cols;
+    void *planes;
+};
+struct F32Planes {    // planes of a stored rows x cols matrix
+    const void *planes;
+    int64_t rows, cols;
+    bool kmajor;      // cols is the reduction
+};
+size_t f32_planes_bytes(int64_t rows, int64_t cols);
+cudaError_t launch_f32_split(const F32Operand *x, int count, cudaStream_t s);   // one or two
+// D[row, col] = sum_k A(row, k) B(col, k) with the epilogue (float).
+cudaError_t launch_linear_f32(const F32Planes &A, const F32Planes &B, int K, const LayerEpi &epi,
+                              cudaStream_t s);
 
 // Rows of `bytes_per_row` bytes copied to rows `dst_ld` bytes apart (dst
 // 16-byte aligned rows; the gap after each row is not written).

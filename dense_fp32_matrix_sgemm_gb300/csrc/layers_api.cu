@@ -131,7 +131,8 @@ LayerEpi plain_epi(int type, void *Y, int64_t ldy, int64_t M, int64_t N) {
 size_t linear_bytes(int dtype, int64_t M, int64_t N, int64_t K, const void *X, int64_t ldx,
                     const void *W, int64_t ldw, int transW) {
     if (M <= few_rows(dtype) || K == 0) return 0;
-    if (dtype == SGEMM_F32) return tf32x3_workspace_bytes(M, N, K, 1);
+    if (dtype == SGEMM_F32)
+        return f32_planes_bytes(M, K) + f32_planes_bytes(transW ? N : K, transW ? K : N);
     const int size = dtype_size(dtype);
     return copy_bytes(X, ldx, M, K, size) +
            copy_bytes(W, ldw, transW ? N : K, transW ? K : N, size);
@@ -142,8 +143,8 @@ struct BackwardPlan {
     bool dz;                 // dZ is written (else dY is dZ)
     int64_t lddz;
     int parts;
-    size_t dz_bytes, part_bytes, x_bytes, w_bytes, product_bytes;
-    size_t total() const { return dz_bytes + part_bytes + x_bytes + w_bytes + product_bytes; }
+    size_t dz_bytes, part_bytes, x_bytes, w_bytes, g_bytes;   // g: planes of dZ (f32)
+    size_t total() const { return dz_bytes + part_bytes + x_bytes + w_bytes + g_bytes; }
 };
 
 BackwardPlan backward_plan(int dtype, int64_t M, int64_t N, int64_t K, const void *dY, int64_t lddy,
@@ -162,12 +163,9 @@ BackwardPlan backward_plan(int dtype, int64_t M, int64_t N, int64_t K, const voi
     if (db) p.part_bytes = round256((size_t)p.parts * N * sizeof(float));
     if (K == 0) return p;
     if (f32) {
-        if (dx && !dx_rows) p.product_bytes = tf32x3_workspace_bytes(M, K, N, 1);
-        if (dw) {
-            const size_t b = transW ? tf32x3_workspace_bytes(N, K, M, 1)
-                                    : tf32x3_workspace_bytes(K, N, M, 1);
-            if (b > p.product_bytes) p.product_bytes = b;
-        }
+        if (dw) p.x_bytes = f32_planes_bytes(M, K);
+        if (dx && !dx_rows) p.w_bytes = f32_planes_bytes(transW ? N : K, transW ? K : N);
+        if (tc) p.g_bytes = f32_planes_bytes(M, N);
         return p;
     }
     if (dw) p.x_bytes = copy_bytes(X, ldx, M, K, size);
@@ -206,8 +204,7 @@ int linear(int dtype, int64_t M, int64_t N, int64_t K, const void *X, int64_t ld
         return fail(SGEMM_EINVAL_PTR, "x_scale and w_scale are required for e4m3, 4-byte aligned, "
                     "and NULL for the other types");
     const size_t need = linear_bytes(dtype, M, N, K, X, ldx, W, ldw, transW);
-    const size_t least = dtype == SGEMM_F32 && need > 0 ? tf32x3_workspace_min_bytes(M, N, K, 1) : need;
-    CHECK(check_workspace(workspace, workspace_bytes, least));
+    CHECK(check_workspace(workspace, workspace_bytes, need));
     CHECK(require_device());
     LayerEpi epi = {Y, preact, residual, bias, x_scale, w_scale, ldy, ldp, ldr, (int)M, (int)N,
                     activation, out_dtype, 1};
@@ -215,10 +212,16 @@ int linear(int dtype, int64_t M, int64_t N, int64_t K, const void *X, int64_t ld
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (M <= few_rows(dtype) || K == 0)
         return launched(launch_linear_rows(dtype, X, ldx, W, ldw, transW, (int)K, epi, s));
-    if (dtype == SGEMM_F32)
-        return launched(launch_linear_tf32x3(static_cast<const float *>(X), ldx,
-                                             static_cast<const float *>(W), ldw, transW != 0,
-                                             (int)K, epi, workspace, workspace_bytes, s));
+    if (dtype == SGEMM_F32) {
+        const int64_t wr = transW ? N : K, wc = transW ? K : N;
+        char *const wsw = static_cast<char *>(workspace) + f32_planes_bytes(M, K);
+        const F32Operand in[2] = {{static_cast<const float *>(X), ldx, M, K, workspace},
+                                  {static_cast<const float *>(W), ldw, wr, wc, wsw}};
+        const cudaError_t split = launch_f32_split(in, 2, s);
+        if (split != cudaSuccess) return launched(split);
+        return launched(launch_linear_f32({workspace, M, K, true}, {wsw, wr, wc, transW != 0},
+                                          (int)K, epi, s));
+    }
     char *ws = static_cast<char *>(workspace);
     cudaError_t e = place(X, ldx, M, K, size, ws, s);
     if (e == cudaSuccess) e = place(W, ldw, transW ? N : K, transW ? K : N, size, ws, s);
@@ -285,34 +288,24 @@ int linear_backward(int dtype, int64_t M, int64_t N, int64_t K, const void *dY, 
                                plain_epi(dtype, dX, lddx, M, K), s);
     if (e != cudaSuccess) return launched(e);
     if (dtype == SGEMM_F32) {
-        GemmArgs a = {};
-        a.batch = 1;
-        a.group_m = raster_group();
-        a.alpha = 1.f;
-        if (dx && !dx_rows) {
-            a.A = static_cast<const float *>(g);
-            a.lda = ldg;
-            a.B = static_cast<const float *>(W);
-            a.ldb = ldw;
-            a.C = static_cast<float *>(dX);
-            a.ldc = lddx;
-            a.M = (int)M;
-            a.N = (int)K;
-            a.K = (int)N;
-            e = launch_tf32x3(a, false, transW == 0, ws, p.product_bytes, s);
+        // planes of dZ (for both products), X and W
+        char *const wsx = ws, *const wsw = wsx + p.x_bytes, *const wsg = wsw + p.w_bytes;
+        const F32Operand G = {static_cast<const float *>(g), ldg, M, N, wsg};
+        const F32Operand in[3] = {G, {static_cast<const float *>(X), ldx, M, K, wsx},
+                                  {static_cast<const float *>(W), ldw, wrows, wcols, wsw}};
+        const bool tdx = dx && !dx_rows;
+        if (dw) e = launch_f32_split(in, 2, s);
+        if (tdx && e == cudaSuccess) {
+            const F32Operand one[2] = {in[2], G};
+            e = launch_f32_split(one, dw ? 1 : 2, s);
         }
+        if (tdx && e == cudaSuccess)
+            e = launch_linear_f32({wsg, M, N, true}, {wsw, wrows, wcols, transW == 0}, (int)N,
+                                  plain_epi(dtype, dX, lddx, M, K), s);
         if (dw && e == cudaSuccess) {
-            const float *G = static_cast<const float *>(g), *Xf = static_cast<const float *>(X);
-            a.A = transW ? G : Xf;
-            a.lda = transW ? ldg : ldx;
-            a.B = transW ? Xf : G;
-            a.ldb = transW ? ldx : ldg;
-            a.C = static_cast<float *>(dW);
-            a.ldc = lddw;
-            a.M = (int)wrows;
-            a.N = (int)wcols;
-            a.K = (int)M;
-            e = launch_tf32x3(a, true, false, ws, p.product_bytes, s);
+            const F32Planes Gp = {wsg, M, N, false}, Xp = {wsx, M, K, false};
+            e = launch_linear_f32(transW ? Gp : Xp, transW ? Xp : Gp, (int)M,
+                                  plain_epi(dtype, dW, lddw, wrows, wcols), s);
         }
         return launched(e);
     }

@@ -53,15 +53,12 @@
 #include <cstdint>
 #include <cstdio>
 #include <mutex>
-#include <type_traits>
 
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
 #include "gemm_args.h"
-#include "layer_math.cuh"
-#include "layers.h"
 #include "tc_utils.cuh"
 #include "tma_encode.h"
 
@@ -329,14 +326,6 @@ struct Tf32x3Params {
     int tiles_dp, tail, split;
     float *part;            // [split * tail][BM * BN] partial tiles, row-major
 };
-
-// With the layer epilogue instead (its Y is C).  A type of its own, so that
-// the kernels of the plain product keep their parameters and registers.
-struct Tf32x3LayerParams : Tf32x3Params {
-    LayerEpi le;
-};
-template <class PT>
-constexpr bool kLayer = std::is_same<PT, Tf32x3LayerParams>::value;
 
 __device__ __forceinline__ void raster(const Tf32x3Params &p, int bid, int &z, int &tm, int &tn) {
     const int per_batch = p.tiles_m * p.tiles_n;
@@ -817,30 +806,6 @@ struct Chunked {
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
 };
 
-// The layer epilogue on the first `rows` rows (from row0 on) of a 32 x 32 fp32
-// block that the warp has staged at `stage` (16-byte chunk j of row r at chunk
-// j ^ (r & 7) of its 128 bytes): a column a lane, eight rows at a time, so each
-// access is a 128-byte row segment and eight residual loads are in flight (one
-// row at a time, 2049 x 3071 x 1537 with a residual took 203 us, its plain
-// product 96).
-__device__ __forceinline__ void finish_staged(const LayerEpi &e, uint32_t stage, int lane, int row0,
-                                              int rows, int col) {
-    if (col >= e.N) return;
-    ColumnTerms<float, 1> t;
-    t.load(e, col);
-#pragma unroll 1
-    for (int r = 0; r < rows; r += 8) {
-        float x[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x[i])
-                         : "r"(stage + (uint32_t)(r + i) * 128u +
-                               ((uint32_t)((lane >> 2) ^ i) << 4) + (uint32_t)((lane & 3) * 4))
-                         : "memory");
-        finish_column<float, 8>(e, t, row0 + r, rows - r, col, x);
-    }
-}
-
 // Stores 32 rows x COLS columns of running sums from the calling warp's
 // threads (thread `lane` holds row m0 + 32q + lane, columns n0 .. n0 + COLS
 // - 1 of a rows x cols matrix), 32 columns at a time through the warp's 4 KB
@@ -855,8 +820,8 @@ __device__ __forceinline__ void finish_staged(const LayerEpi &e, uint32_t stage,
 //   Otherwise (C only) the warp reads the block back a row at a time, lane j
 //   taking column j, and stores it with the epilogue: each store is one
 //   128-byte row segment.
-template <int COLS, class PT>
-__device__ __forceinline__ void store_running_rows(const PT &p, const CUtensorMap *map,
+template <int COLS>
+__device__ __forceinline__ void store_running_rows(const Tf32x3Params &p, const CUtensorMap *map,
                                                    bool tma, int tma_n, const float (&run)[COLS],
                                                    int q, int lane, int z, int m0, int n0,
                                                    int rows, int cols, uint32_t stage, int &cc) {
@@ -887,10 +852,6 @@ __device__ __forceinline__ void store_running_rows(const PT &p, const CUtensorMa
         }
         __syncwarp();
         const int col = n0 + 32 * c + lane;
-        if constexpr (kLayer<PT>) {
-            finish_staged(p.le, stage, lane, row0, min(32, p.M - row0), col);
-            continue;
-        }
         const uint32_t cofs = (uint32_t)((lane & 3) * 4);
         const int rows = min(32, p.M - row0);
 #pragma unroll 1
@@ -965,8 +926,8 @@ __device__ __forceinline__ Piece piece_of(const Tf32x3Params &p, int c, int G, i
 // split * V / 8 round trips; the adds go in K order starting from zero.  The
 // launcher takes V = 4 when that still gives a CTA per SM, else V = 1.
 // Launched as a programmatic dependent of the GEMM kernel.
-template <int BN, int V, class PT>
-__global__ void __launch_bounds__(256) tf32x3_fixup_kernel(const PT p) {
+template <int BN, int V>
+__global__ void __launch_bounds__(256) tf32x3_fixup_kernel(const Tf32x3Params p) {
     constexpr int NB = 8 / V;   // segments per batch
     static_assert((BM * BN) % (1024 * V) == 0, "whole float4 groups per CTA");
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -1009,10 +970,6 @@ __global__ void __launch_bounds__(256) tf32x3_fixup_kernel(const PT p) {
         if (row >= p.M || col >= p.N) continue;
         float *cp = p.C + (int64_t)z * p.strideC + (int64_t)row * p.ldc + col;
         float o[4] = {acc[r].x, acc[r].y, acc[r].z, acc[r].w};
-        if constexpr (kLayer<PT>) {
-            finish<float, 4>(p.le, row, col, o);
-            continue;
-        }
         if (!plain) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -1046,14 +1003,14 @@ __global__ void __launch_bounds__(256) tf32x3_fixup_kernel(const PT p) {
 // and the abort word stops all roles.  RAW as in the persistent kernel (no
 // converter warps: chunking applies to K > 256, where operands come from lo
 // planes).
-template <class CFG, int RAW, class PT>
+template <class CFG, int RAW>
 __global__ void __launch_bounds__(Chunked<CFG>::THREADS, 1)
 tf32x3_chunked_kernel(const __grid_constant__ CUtensorMap tmA,
                       const __grid_constant__ CUtensorMap tmB,
                       const __grid_constant__ CUtensorMap tmAlo,
                       const __grid_constant__ CUtensorMap tmBlo,
                       const __grid_constant__ CUtensorMap tmC,
-                      const __grid_constant__ CUtensorMap tmP, const PT p) {
+                      const __grid_constant__ CUtensorMap tmP, const Tf32x3Params p) {
     using P = Chunked<CFG>;
     constexpr int BK = CFG::BK, STAGES = CFG::STAGES, PLANES = CFG::PLANES;
     constexpr int BN = CFG::BN;
@@ -1489,8 +1446,8 @@ size_t plane_bytes(int64_t rows, int64_t K, int64_t batch, int planes) {
 // a raw operand that is not converted gets a lo-only plane and its map in
 // tmAlo / tmBlo (which are left empty otherwise).
 template <class CFG>
-cudaError_t prepare(const GemmArgs &a, bool layer, bool transA, bool transB, int raw, int conv,
-                    void *ws, cudaStream_t s, CUtensorMap &tmA, CUtensorMap &tmB, CUtensorMap &tmAlo,
+cudaError_t prepare(const GemmArgs &a, bool transA, bool transB, int raw, int conv, void *ws,
+                    cudaStream_t s, CUtensorMap &tmA, CUtensorMap &tmB, CUtensorMap &tmAlo,
                     CUtensorMap &tmBlo, CUtensorMap &tmC, Tf32x3Params &p) {
     constexpr int PLANES = CFG::PLANES;
     const int Kp = plane_row_floats(a.K);
@@ -1569,7 +1526,7 @@ cudaError_t prepare(const GemmArgs &a, bool layer, bool transA, bool transB, int
     // tma_c is set.
     tmC = CUtensorMap{};
     const int n4 = a.N / 4 * 4;
-    p.tma_c = p.vec_c && n4 > 0 && plain_epilogue(a) && !layer &&
+    p.tma_c = p.vec_c && n4 > 0 && plain_epilogue(a) &&
               make_c_map(&tmC, a.C, a.M, n4, a.ldc, a.strideC, a.batch);
     p.tma_n = a.N % 4 == 0 ? INT_MAX : n4;
     return cudaSuccess;
@@ -1603,7 +1560,7 @@ cudaError_t launch_persistent_raw(const GemmArgs &a, bool transA, bool transB, v
     if (e != cudaSuccess) return e;
     CUtensorMap tmC, tmAlo, tmBlo;
     Tf32x3Params p;
-    e = prepare<CFG>(a, false, transA, transB, RAW, CONV, ws, s, tmA, tmB, tmAlo, tmBlo, tmC, p);
+    e = prepare<CFG>(a, transA, transB, RAW, CONV, ws, s, tmA, tmB, tmAlo, tmBlo, tmC, p);
     if (e != cudaSuccess) return e;
     const long long tiles = (long long)a.batch * p.tiles_m * p.tiles_n;
     cudaLaunchConfig_t cfg = {};
@@ -1768,13 +1725,13 @@ ChunkedPlan chunked_plan_for(const GemmArgs &a, int sms) {
     return chunked_plan(tiles, (a.K + CFG::BK - 1) / CFG::BK, CFG::BN, sms);
 }
 
-template <class CFG, int RAW, class PT>
-cudaError_t launch_chunked_raw(const GemmArgs &a, const LayerEpi *le, bool transA, bool transB,
-                               void *ws, size_t ws_bytes, cudaStream_t s, CUtensorMap &tmA,
+template <class CFG, int RAW>
+cudaError_t launch_chunked_raw(const GemmArgs &a, bool transA, bool transB, void *ws,
+                               size_t ws_bytes, cudaStream_t s, CUtensorMap &tmA,
                                CUtensorMap &tmB) {
     using P = Chunked<CFG>;
     static PerContext<bool> configured;
-    cudaError_t e = ensure_smem(tf32x3_chunked_kernel<CFG, RAW, PT>, P::SMEM_BYTES, configured);
+    cudaError_t e = ensure_smem(tf32x3_chunked_kernel<CFG, RAW>, P::SMEM_BYTES, configured);
     if (e != cudaSuccess) return e;
     int dev = 0, sms = 0;
     e = cudaGetDevice(&dev);
@@ -1782,10 +1739,9 @@ cudaError_t launch_chunked_raw(const GemmArgs &a, const LayerEpi *le, bool trans
     e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
     CUtensorMap tmC, tmAlo, tmBlo;
-    PT p;
-    e = prepare<CFG>(a, kLayer<PT>, transA, transB, RAW, 0, ws, s, tmA, tmB, tmAlo, tmBlo, tmC, p);
+    Tf32x3Params p;
+    e = prepare<CFG>(a, transA, transB, RAW, 0, ws, s, tmA, tmB, tmAlo, tmBlo, tmC, p);
     if (e != cudaSuccess) return e;
-    if constexpr (kLayer<PT>) p.le = *le;
     p.kcb = g_chunk_k.load(std::memory_order_relaxed) / CFG::BK;
     // the partial tiles follow the planes; a workspace without room for them
     // keeps the whole-tile schedule
@@ -1814,8 +1770,8 @@ cudaError_t launch_chunked_raw(const GemmArgs &a, const LayerEpi *le, bool trans
     CUtensorMap tmP = {};
     if (pl.split > 0 && !make_part_map(&tmP, p.part, pl.split * pl.tail, CFG::BN))
         return cudaErrorInvalidValue;
-    e = cudaLaunchKernelEx(&cfg, tf32x3_chunked_kernel<CFG, RAW, PT>, tmA, tmB, tmAlo, tmBlo, tmC,
-                           tmP, p);
+    e = cudaLaunchKernelEx(&cfg, tf32x3_chunked_kernel<CFG, RAW>, tmA, tmB, tmAlo, tmBlo, tmC, tmP,
+                           p);
     if (e != cudaSuccess) return e;
     if (pl.split == 0) return cudaGetLastError();
     // the tail tiles' sums, as a programmatic dependent of the GEMM
@@ -1823,10 +1779,10 @@ cudaError_t launch_chunked_raw(const GemmArgs &a, const LayerEpi *le, bool trans
     cfg.dynamicSmemBytes = 0;
     if ((long long)pl.tail * (BM * CFG::BN / 4096) >= sms) {
         cfg.gridDim = dim3((unsigned)(BM * CFG::BN / 4096), (unsigned)pl.tail);
-        e = cudaLaunchKernelEx(&cfg, tf32x3_fixup_kernel<CFG::BN, 4, PT>, p);
+        e = cudaLaunchKernelEx(&cfg, tf32x3_fixup_kernel<CFG::BN, 4>, p);
     } else {
         cfg.gridDim = dim3((unsigned)(BM * CFG::BN / 1024), (unsigned)pl.tail);
-        e = cudaLaunchKernelEx(&cfg, tf32x3_fixup_kernel<CFG::BN, 1, PT>, p);
+        e = cudaLaunchKernelEx(&cfg, tf32x3_fixup_kernel<CFG::BN, 1>, p);
     }
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
@@ -1837,9 +1793,9 @@ cudaError_t launch_chunked_raw(const GemmArgs &a, const LayerEpi *le, bool trans
 // sectors, as in the planes (plane_row_floats).  On rows only 16-byte aligned
 // each slice straddles sectors, and the split kernel's planes are the cheaper
 // route (3000 x 2000 x 1500 with row-major A of ld 1500).
-template <class CFG, class PT>
-cudaError_t launch_chunked(const GemmArgs &a, const LayerEpi *le, bool transA, bool transB,
-                           void *ws, size_t ws_bytes, cudaStream_t s) {
+template <class CFG>
+cudaError_t launch_chunked(const GemmArgs &a, bool transA, bool transB, void *ws, size_t ws_bytes,
+                           cudaStream_t s) {
     static_assert(CFG::PLANES == 2, "three terms");
     auto raw_ok = [&](const float *X, int64_t ld, int64_t sX, bool kcontig) {
         return kcontig && reinterpret_cast<uintptr_t>(X) % 128 == 0 && ld % 32 == 0 &&
@@ -1854,14 +1810,10 @@ cudaError_t launch_chunked(const GemmArgs &a, const LayerEpi *le, bool transA, b
         make_raw_map<CFG>(&tmB, a.B, a.N, a.K, a.ldb, a.strideB, a.batch, CFG::BN))
         raw |= 2;
     switch (raw) {
-        case 1:
-            return launch_chunked_raw<CFG, 1, PT>(a, le, transA, transB, ws, ws_bytes, s, tmA, tmB);
-        case 2:
-            return launch_chunked_raw<CFG, 2, PT>(a, le, transA, transB, ws, ws_bytes, s, tmA, tmB);
-        case 3:
-            return launch_chunked_raw<CFG, 3, PT>(a, le, transA, transB, ws, ws_bytes, s, tmA, tmB);
-        default:
-            return launch_chunked_raw<CFG, 0, PT>(a, le, transA, transB, ws, ws_bytes, s, tmA, tmB);
+        case 1: return launch_chunked_raw<CFG, 1>(a, transA, transB, ws, ws_bytes, s, tmA, tmB);
+        case 2: return launch_chunked_raw<CFG, 2>(a, transA, transB, ws, ws_bytes, s, tmA, tmB);
+        case 3: return launch_chunked_raw<CFG, 3>(a, transA, transB, ws, ws_bytes, s, tmA, tmB);
+        default: return launch_chunked_raw<CFG, 0>(a, transA, transB, ws, ws_bytes, s, tmA, tmB);
     }
 }
 
@@ -1953,57 +1905,18 @@ size_t tf32_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t batch) {
 // kernel (128-wide tiles, converter warps where they pay); longer ones the
 // K-chunked kernel, whose sums are promoted to round-to-nearest fp32 adds
 // every 128 of K, on the tile width the wave count favours.
-namespace {
-
-template <class PT>   // Tf32x3Params, or Tf32x3LayerParams with the layer epilogue `le`
-cudaError_t launch_chunked_tiles(const GemmArgs &a, const LayerEpi *le, bool transA, bool transB,
-                                 void *ws, size_t ws_bytes, cudaStream_t s) {
-    return tc_wide_tile(a, 3)
-               ? tf32x3::launch_chunked<Tf32x3Wide, PT>(a, le, transA, transB, ws, ws_bytes, s)
-               : tf32x3::launch_chunked<Tf32x3Narrow, PT>(a, le, transA, transB, ws, ws_bytes, s);
-}
-
-}  // namespace
-
 cudaError_t launch_tf32x3(const GemmArgs &a, bool transA, bool transB, void *ws, size_t ws_bytes,
                           cudaStream_t s) {
     if (a.K <= tf32x3::kChunkMinK)
         return tf32x3::launch_persistent<Tf32x3Narrow, 2>(a, transA, transB, ws, s);
-    return launch_chunked_tiles<tf32x3::Tf32x3Params>(a, nullptr, transA, transB, ws, ws_bytes, s);
-}
-
-// The layer epilogue is in the K-chunked kernel alone, which takes any K: its
-// running sums are in registers when a tile leaves, so the epilogue runs where
-// no TMEM load (a warp-collective instruction) is near.
-cudaError_t launch_linear_tf32x3(const float *X, int64_t ldx, const float *W, int64_t ldw,
-                                 bool transW, int K, const LayerEpi &epi, void *ws,
-                                 size_t ws_bytes, cudaStream_t s) {
-    GemmArgs a = {};
-    a.A = X;
-    a.B = W;
-    a.C = static_cast<float *>(epi.Y);
-    a.lda = ldx;
-    a.ldb = ldw;
-    a.ldc = epi.ldy;
-    a.M = epi.M;
-    a.N = epi.N;
-    a.K = K;
-    a.batch = 1;
-    a.group_m = raster_group();
-    a.alpha = 1.f;
-    // a layer without bias, activation, residual and stored z is the plain
-    // product, whose tiles leave by TMA store
-    const bool plain = epi.act == SGEMM_ACT_NONE && epi.bias == nullptr && epi.R == nullptr &&
-                       epi.Z == nullptr;
-    if (plain)
-        return launch_tf32x3(a, false, transW, ws, ws_bytes, s);
-    return launch_chunked_tiles<tf32x3::Tf32x3LayerParams>(a, &epi, false, transW, ws, ws_bytes, s);
+    return tc_wide_tile(a, 3)
+               ? tf32x3::launch_chunked<Tf32x3Wide>(a, transA, transB, ws, ws_bytes, s)
+               : tf32x3::launch_chunked<Tf32x3Narrow>(a, transA, transB, ws, ws_bytes, s);
 }
 
 cudaError_t launch_tf32(const GemmArgs &a, bool transA, bool transB, void *ws, cudaStream_t s) {
-    return tc_wide_tile(a, 1)
-               ? tf32x3::launch_persistent<Tf32Wide, 2>(a, transA, transB, ws, s)
-               : tf32x3::launch_persistent<Tf32Narrow, 2>(a, transA, transB, ws, s);
+    return tc_wide_tile(a, 1) ? tf32x3::launch_persistent<Tf32Wide, 2>(a, transA, transB, ws, s)
+                              : tf32x3::launch_persistent<Tf32Narrow, 2>(a, transA, transB, ws, s);
 }
 
 int set_tf32x3_chunk_k(int chunk_k) {

@@ -104,6 +104,12 @@ def test_pair_pipeline(seed):
     pair_pipeline(rng.randint(1, 7), rng.randint(1, 15), 6, 2, seed)
 
 
+@pytest.mark.parametrize("seed", range(20))
+def test_pair_pipeline_of_single_stages(seed):
+    # linear_f32_kernel: two stages, and an accumulator takes one stage
+    pair_pipeline(random.Random(2000 + seed).randint(1, 40), 1, 2, 2, seed)
+
+
 @pytest.mark.parametrize("plant", ["no empty wait", "no drain wait", "full parity"])
 def test_pair_pipeline_catches(plant):
     caught = 0

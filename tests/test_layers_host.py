@@ -53,7 +53,10 @@ def test_linear_workspace_follows_alignment():
     assert size(E4M3, 32, 16, 129, FAKE, 129, FAKE, 144, 1) == 32 * 256
     assert size(BF16, 4, 16, 7, FAKE, 7, FAKE, 7, 1) == 0             # few rows: any alignment
     assert size(F32, 16, 64, 64, FAKE, 64, FAKE, 64, 1) == 0
-    assert size(F32, 17, 64, 64, FAKE, 64, FAKE, 64, 1) == sg.tf32x3_workspace_size(17, 64, 64, 1)
+    # f32: three bf16 planes of both operands, rows padded to 64 elements
+    assert size(F32, 32, 64, 65, FAKE, 65, FAKE, 65, 1) == 3 * 2 * 128 * (32 + 64)
+    assert size(F32, 32, 64, 65, FAKE, 65, FAKE, 64, 0) == 3 * 2 * 128 * 32 + \
+        (3 * 2 * 64 * 65 + 255) // 256 * 256
     for empty in ((0, 16, 8), (32, 0, 8), (32, 16, 0), (-1, 16, 8)):
         assert size(BF16, *empty, FAKE, 8, FAKE, 8, 1) == 0
 
