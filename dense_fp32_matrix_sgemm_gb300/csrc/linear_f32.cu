@@ -17,7 +17,8 @@
 // takes one stage: the five small terms first, while it is small, then a0 b0
 // (four updates at full size), and the epilogue warps add it to running sums in
 // registers with ordinary fp32 adds while the other accumulator fills.
-// Measured against 64 bits: relative error @ERR@.
+// Relative error against 64 bits, 2049 x
+// 3071 x 1537: 8e-8 (FP32 FMAs 4.2e-7).
 #include <cstdint>
 
 #include <cuda.h>
@@ -54,9 +55,11 @@ struct Params {
     LayerEpi epi;
     int kblocks;
     int tiles_m, tiles_n, group_m;
+    int tile0, tiles;        // this launch's tiles: tile0 .. tile0 + tiles - 1
     int a_kmajor, b_kmajor;
     int a_bytes;        // bytes one plane of A brings to a CTA's stage
     uint32_t idesc;
+    int tma;            // Y leaves by TMA store, whole blocks of 32 columns
     unsigned *error;
 };
 
@@ -73,12 +76,60 @@ __device__ __forceinline__ void tma_load3(uint32_t dst, const void *tmap, uint32
             : "memory");
 }
 
+// 32 whole columns of this lane's row with bias, ReLU and residual, in
+// registers, then out by TMA store through the warp's staging block (the
+// 128-byte swizzle).  The other activations and a stored z take the staged path
+// below: their code, unrolled over a row's registers, would be fetched longer
+// than it runs.
+__device__ __forceinline__ void store_row32(const LayerEpi &e, const void *tmY, uint32_t stage,
+                                            int lane, int row0, int col, float (&v)[32]) {
+    if (e.bias != nullptr) {
+        const float4 *b = reinterpret_cast<const float4 *>(static_cast<const float *>(e.bias) + col);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float4 f = b[j];
+            v[4 * j] += f.x;
+            v[4 * j + 1] += f.y;
+            v[4 * j + 2] += f.z;
+            v[4 * j + 3] += f.w;
+        }
+    }
+    if (e.act == SGEMM_ACT_RELU) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = activate<float>(v[j], SGEMM_ACT_RELU);
+    }
+    if (e.R != nullptr && row0 + lane < e.M) {
+        const float4 *r = reinterpret_cast<const float4 *>(static_cast<const float *>(e.R) +
+                                                           (row0 + lane) * e.ldr + col);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float4 f = r[j];
+            v[4 * j] += f.x;
+            v[4 * j + 1] += f.y;
+            v[4 * j + 2] += f.z;
+            v[4 * j + 3] += f.w;
+        }
+    }
+    if (lane == 0) tc::bulk_wait_group_read<0>();   // the block is free
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        tc::st_shared_v4(stage + (uint32_t)lane * 128u + ((uint32_t)(j ^ (lane & 7)) << 4), v[4 * j],
+                         v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    tc::fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+        tma_store(tmY, stage, col, row0);
+        tc::bulk_commit_group();
+    }
+}
+
 // Roles, barriers and schedules as linear_tc_kernel; "accumulator full" and
 // "empty" are per stage of K instead of per tile, counted across tiles.
 template <int CTAS, int BN, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
 linear_f32_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                  const __grid_constant__ Params p) {
+                  const __grid_constant__ CUtensorMap tmY, const __grid_constant__ Params p) {
     using S = Shape<CTAS, BN, SPLIT>;
     constexpr int STAGES = S::STAGES, SLOTS = S::SLOTS, COLS = BN / 2;
     constexpr bool CLUSTER = CTAS == 2 || SPLIT;
@@ -100,7 +151,7 @@ linear_f32_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
     const int half = CTAS == 2 ? rank & 1 : 0;
     const int leader = CTAS == 2 ? rank & ~1 : rank;
     const uint16_t mask = (uint16_t)(3u << leader);
-    const int total = p.tiles_m * p.tiles_n;
+    const int total = p.tiles;
     int first = (int)blockIdx.x / CTAS, stride = (int)gridDim.x / CTAS, kb0 = 0, kb1 = p.kblocks;
     int parts = 1, part = 0;
     if constexpr (SPLIT) {
@@ -151,7 +202,7 @@ linear_f32_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
             bool stop = false;
             for (int i = 0; i < ntiles && !stop; ++i) {
                 int tm, tn;
-                raster(p.tiles_m, p.tiles_n, p.group_m, first + i * stride, tm, tn);
+                raster(p.tiles_m, p.tiles_n, p.group_m, p.tile0 + first + i * stride, tm, tn);
                 const int m0 = (tm * CTAS + half) * BM, n0 = tn * BN + half * S::BROWS;
                 for (int kb = kb0; kb < kb1; ++kb) {
                     if (r.used == STAGES &&
@@ -267,7 +318,7 @@ linear_f32_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
             }
             if (stop) break;
             int tm, tn;
-            raster(p.tiles_m, p.tiles_n, p.group_m, first + i * stride, tm, tn);
+            raster(p.tiles_m, p.tiles_n, p.group_m, p.tile0 + first + i * stride, tm, tn);
             const int row0 = (tm * CTAS + half) * BM + 32 * q, n0 = tn * BN + side * COLS;
             if (row0 >= p.epi.M) continue;
             if constexpr (SPLIT) {
@@ -284,7 +335,15 @@ linear_f32_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
 #pragma unroll
                 for (int c = 0; c < COLS / 32; ++c) {
                     if (n0 + 32 * c >= p.epi.N) break;
-                    __syncwarp();   // the previous block has been read
+                    if (p.tma && n0 + 32 * c + 32 <= p.epi.N) {
+                        float v[32];
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = run[32 * c + j];
+                        store_row32(p.epi, &tmY, stage, lane, row0, n0 + 32 * c, v);
+                        continue;
+                    }
+                    if (lane == 0) tc::bulk_wait_group_read<0>();
+                    __syncwarp();   // the block is free, the previous one has been read
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
                         tc::st_shared_v4(stage + (uint32_t)lane * 128u +
@@ -297,6 +356,7 @@ linear_f32_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
             }
             __syncwarp();
         }
+        if (!SPLIT && lane == 0) tc::bulk_wait_group_read<0>();   // the stores have left
     }
     __syncwarp();
 
@@ -306,7 +366,7 @@ linear_f32_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
         // every CTA of the cluster passes the barriers, an aborted one too
         cluster_sync();
         int tm, tn;
-        raster(p.tiles_m, p.tiles_n, p.group_m, first, tm, tn);
+        raster(p.tiles_m, p.tiles_n, p.group_m, p.tile0 + first, tm, tn);
         const int m0 = (tm * CTAS + half) * BM;
         const int rows = min(BM, p.epi.M - m0);
         const int n0 = tn * BN;
@@ -351,41 +411,75 @@ __device__ __forceinline__ void split_pair(float x, float y, uint32_t (&w)[3]) {
     w[2] = pack2<__nv_bfloat16>(rx - m.x, ry - m.y);
 }
 
-// CTAs [0, job[0].blocks) take the first operand, the rest the second; 8
-// columns a thread with 16-byte accesses where the rows allow it, else 2.
+// CTAs [0, job[0].blocks) take the first operand, the rest the second.  A warp
+// takes pieces of a row (512 columns with 16-byte accesses, 8 columns a lane
+// each, else 256 columns, 2 a lane), every access of a piece in flight; from
+// piece to piece it steps without a division.
 __global__ void __launch_bounds__(256) split3_kernel(const SplitArgs a) {
     pdl_trigger();
     pdl_wait();
     const int which = (int)blockIdx.x < a.job[0].blocks ? 0 : 1;
     const SplitJob j = which ? a.job[1] : a.job[0];
-    const int64_t block = (int64_t)blockIdx.x - (which ? a.job[0].blocks : 0);
+    const int64_t warp = ((int64_t)blockIdx.x - (which ? a.job[0].blocks : 0)) * 8 +
+                         (threadIdx.x >> 5);
+    const int64_t warps = (int64_t)j.blocks * 8;
+    const int piece = j.vec ? 512 : 256;
+    const int pieces = (j.cols + piece - 1) / piece;
+    const int64_t dr = warps / pieces;
+    const int dc = (int)(warps - dr * pieces);
+    int64_t r = warp / pieces;
+    int pc = (int)(warp - r * pieces);
     const int64_t plane = j.rows * j.ldp;
-    const int w = j.vec ? 8 : 2;
-    const int per_row = (j.cols + w - 1) / w;
-    const int64_t total = j.rows * per_row;
-    for (int64_t i = block * 256 + threadIdx.x; i < total; i += (int64_t)j.blocks * 256) {
-        const int64_t r = i / per_row;
-        const int c = (int)(i - r * per_row) * w;
-        const float *x = j.X + r * j.ld + c;
-        __nv_bfloat16 *out = j.out + r * j.ldp + c;
+    const int lane = threadIdx.x & 31;
+    for (; r < j.rows; r += dr, pc += dc) {
+        if (pc >= pieces) {
+            pc -= pieces;
+            if (++r >= j.rows) break;
+        }
+        const float *x = j.X + r * j.ld;
+        __nv_bfloat16 *out = j.out + r * j.ldp;
         if (j.vec) {   // cols is a multiple of 8
-            const float4 u = __ldg(reinterpret_cast<const float4 *>(x));
-            const float4 v = __ldg(reinterpret_cast<const float4 *>(x) + 1);
-            uint32_t p[4][3];
-            split_pair(u.x, u.y, p[0]);
-            split_pair(u.z, u.w, p[1]);
-            split_pair(v.x, v.y, p[2]);
-            split_pair(v.z, v.w, p[3]);
+            float4 u[2][2];
 #pragma unroll
-            for (int pl = 0; pl < 3; ++pl)
-                *reinterpret_cast<uint4 *>(out + pl * plane) =
-                    make_uint4(p[0][pl], p[1][pl], p[2][pl], p[3][pl]);
+            for (int i = 0; i < 2; ++i) {
+                const int c = pc * 512 + 256 * i + 8 * lane;
+                if (c < j.cols) {
+                    u[i][0] = __ldg(reinterpret_cast<const float4 *>(x + c));
+                    u[i][1] = __ldg(reinterpret_cast<const float4 *>(x + c) + 1);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int c = pc * 512 + 256 * i + 8 * lane;
+                if (c >= j.cols) break;
+                uint32_t p[4][3];
+                split_pair(u[i][0].x, u[i][0].y, p[0]);
+                split_pair(u[i][0].z, u[i][0].w, p[1]);
+                split_pair(u[i][1].x, u[i][1].y, p[2]);
+                split_pair(u[i][1].z, u[i][1].w, p[3]);
+#pragma unroll
+                for (int pl = 0; pl < 3; ++pl)
+                    *reinterpret_cast<uint4 *>(out + pl * plane + c) =
+                        make_uint4(p[0][pl], p[1][pl], p[2][pl], p[3][pl]);
+            }
         } else {
-            uint32_t p[3];
-            split_pair(__ldg(x), c + 1 < j.cols ? __ldg(x + 1) : 0.f, p);
+            float u[4][2];
 #pragma unroll
-            for (int pl = 0; pl < 3; ++pl)   // (the planes' rows are padded to 64)
-                *reinterpret_cast<uint32_t *>(out + pl * plane) = p[pl];
+            for (int i = 0; i < 4; ++i) {
+                const int c = pc * 256 + 64 * i + 2 * lane;
+                u[i][0] = c < j.cols ? __ldg(x + c) : 0.f;
+                u[i][1] = c + 1 < j.cols ? __ldg(x + c + 1) : 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int c = pc * 256 + 64 * i + 2 * lane;
+                if (c >= j.cols) break;
+                uint32_t p[3];
+                split_pair(u[i][0], u[i][1], p);
+#pragma unroll
+                for (int pl = 0; pl < 3; ++pl)   // (the planes' rows are padded to 64)
+                    *reinterpret_cast<uint32_t *>(out + pl * plane + c) = p[pl];
+            }
         }
     }
 }
@@ -412,8 +506,8 @@ bool plane_map(CUtensorMap *map, const void *base, int64_t rows, int64_t cols, i
 }
 
 template <int CTAS, int BN, bool SPLIT>
-cudaError_t launch(const F32Planes &A, const F32Planes &B, int K, const LayerEpi &epi, int parts,
-                   int most, cudaStream_t s) {
+cudaError_t launch(const F32Planes &A, const F32Planes &B, int K, const LayerEpi &epi,
+                   const Piece &piece, cudaStream_t s) {
     using S = Shape<CTAS, BN, SPLIT>;
     static PerContext<bool> configured;
     bool done = false;
@@ -436,14 +530,20 @@ cudaError_t launch(const F32Planes &A, const F32Planes &B, int K, const LayerEpi
     p.a_bytes = A.kmajor ? a_rows * kRowBytes : S::A_TILE;
     p.idesc = instruction_desc(SGEMM_BF16, CTAS * BM, BN, A.kmajor, B.kmajor);
     p.error = device_error_word();
-    CUtensorMap tmA, tmB;
+    CUtensorMap tmA, tmB, tmY = {};
+    p.tma = !SPLIT && epi.vec == 4 && epi.Z == nullptr &&
+            (epi.act == SGEMM_ACT_NONE || epi.act == SGEMM_ACT_RELU) &&
+            make_map(&tmY, epi.Y, SGEMM_F32, epi.ldy, epi.N, epi.M, 128, 32,
+                     CU_TENSOR_MAP_L2_PROMOTION_NONE);
     if (!plane_map(&tmA, A.planes, A.rows, A.cols, A.kmajor ? a_rows : 64) ||
         !plane_map(&tmB, B.planes, B.rows, B.cols, B.kmajor ? S::BROWS : 64))
         return cudaErrorInvalidValue;
-    const long long tiles = (long long)p.tiles_m * p.tiles_n;
-    const long long ctas = SPLIT ? tiles * CTAS * parts : CTAS * (tiles < most ? tiles : most);
-    Config c(ctas, S::SMEM, SPLIT ? CTAS * parts : CTAS, s);
-    return cudaLaunchKernelEx(&c.cfg, linear_f32_kernel<CTAS, BN, SPLIT>, tmA, tmB, p);
+    p.tile0 = piece.tile0;
+    p.tiles = piece.tiles;
+    const long long most = piece.room < piece.tiles ? piece.room : piece.tiles;
+    const long long ctas = CTAS * (SPLIT ? (long long)piece.tiles * piece.parts : most);
+    Config c(ctas, S::SMEM, SPLIT ? CTAS * piece.parts : CTAS, s);
+    return cudaLaunchKernelEx(&c.cfg, linear_f32_kernel<CTAS, BN, SPLIT>, tmA, tmB, tmY, p);
 }
 
 }  // namespace f32
@@ -468,8 +568,8 @@ cudaError_t launch_f32_split(const F32Operand *x, int count, cudaStream_t s) {
         j.cols = (int)x[i].cols;
         j.vec = x[i].cols % 8 == 0 && x[i].ld % 4 == 0 &&
                 reinterpret_cast<uintptr_t>(x[i].X) % 16 == 0;
-        const int w = j.vec ? 8 : 2;
-        const int64_t need = (j.rows * ((j.cols + w - 1) / w) + 255) / 256;
+        const int piece = j.vec ? 512 : 256;
+        const int64_t need = (j.rows * ((j.cols + piece - 1) / piece) + 7) / 8;
         j.blocks = (int)(need < 152 * 16 ? need : 152 * 16);
         blocks += j.blocks;
     }
@@ -485,47 +585,31 @@ cudaError_t launch_f32_split(const F32Operand *x, int count, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, split3_kernel, a);
 }
 
-// The tile and schedule by cost, as linear_tc's; a stage's 24 MMAs take
-// @COST@.
+// The tile and schedule by cost, as linear_tc's; a stage (64 of K, 24 MMAs) takes
+// 0.78, 1.05 and 1.75 us, a pair's launch 9 (4096^3: 474 us with the last 28 of
+// 256 tiles in 2 parts, 514 without, 557 with 128-wide tiles; 2049 x 3071 x 1537
+// 107 128-wide, 119 with pairs).
 cudaError_t launch_linear_f32(const F32Planes &A, const F32Planes &B, int K, const LayerEpi &epi,
                               cudaStream_t s) {
     using namespace ltc;
+    constexpr Costs costs = {{0.78, 1.05, 1.75}, {6.0, 9.0}, {1.5, 3.0, 5.0}};
     Capacity cap;
     cudaError_t e = capacity(cap);
     if (e != cudaSuccess) return e;
-    const int kblocks = (K + f32::kBk - 1) / f32::kBk;
-    struct {
-        int ctas, bn, parts;
-        double us;
-    } best = {0, 0, 0, 1e30};
-    auto consider = [&](int ctas, int bn, int parts) {
-        const long long tiles = (long long)((epi.M + ctas * BM - 1) / (ctas * BM)) *
-                                ((epi.N + bn - 1) / bn);
-        const int room = cap.of(ctas * parts);
-        if (parts > 1 && (tiles > room || kblocks < 2 * parts)) return;
-        const double stage = ctas == 2 ? 1.7 : bn == 128 ? 1.1 : 0.8;
-        double us = (double)((tiles + room - 1) / room) * ((kblocks + parts - 1) / parts) * stage +
-                    (ctas == 2 ? 7.5 : 6.0);
-        if (parts > 1)
-            us += 1.0 + (ctas == 2 ? 5.0 : 3.0 * bn / 128) * (epi.M < BM ? epi.M : BM) / BM;
-        if (us < best.us) best = {ctas, bn, parts, us};
-    };
-    consider(2, 256, 1);
-    consider(1, 64, 1);
-    consider(1, 128, 1);
-    for (int parts = 2; parts <= 8; parts *= 2) {
-        if (parts <= 4) consider(2, 256, parts);
-        consider(1, 128, parts);
-        consider(1, 64, parts);
+    const Plan plan = plan_tiles(epi.M, epi.N, (K + f32::kBk - 1) / f32::kBk, cap, costs);
+    for (int i = 0; i < plan.pieces && e == cudaSuccess; ++i) {
+        const Piece &p = plan.piece[i];
+        if (plan.ctas == 2)
+            e = p.parts > 1 ? f32::launch<2, 256, true>(A, B, K, epi, p, s)
+                            : f32::launch<2, 256, false>(A, B, K, epi, p, s);
+        else if (plan.bn == 128)
+            e = p.parts > 1 ? f32::launch<1, 128, true>(A, B, K, epi, p, s)
+                            : f32::launch<1, 128, false>(A, B, K, epi, p, s);
+        else
+            e = p.parts > 1 ? f32::launch<1, 64, true>(A, B, K, epi, p, s)
+                            : f32::launch<1, 64, false>(A, B, K, epi, p, s);
     }
-    if (best.parts > 1) {
-        if (best.ctas == 2) return f32::launch<2, 256, true>(A, B, K, epi, best.parts, 0, s);
-        return best.bn == 128 ? f32::launch<1, 128, true>(A, B, K, epi, best.parts, 0, s)
-                              : f32::launch<1, 64, true>(A, B, K, epi, best.parts, 0, s);
-    }
-    if (best.ctas == 2) return f32::launch<2, 256, false>(A, B, K, epi, 1, cap.of(2), s);
-    return best.bn == 128 ? f32::launch<1, 128, false>(A, B, K, epi, 1, cap.sms, s)
-                          : f32::launch<1, 64, false>(A, B, K, epi, 1, cap.sms, s);
+    return e;
 }
 
 }  // namespace sgemm

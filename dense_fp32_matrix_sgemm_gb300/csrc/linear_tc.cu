@@ -73,6 +73,7 @@ struct Params {
     LayerEpi epi;
     int kblocks;             // K in stages
     int tiles_m, tiles_n, group_m;
+    int tile0, tiles;        // this launch's tiles: tile0 .. tile0 + tiles - 1
     int a_kmajor, b_kmajor;
     int a_bytes;             // bytes A's boxes bring to a CTA's stage
     uint32_t idesc;
@@ -216,7 +217,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     const int leader = CTAS == 2 ? rank & ~1 : rank;
     const uint16_t mask = (uint16_t)(3u << leader);
     // this CTA's tiles first, first + stride, ... and its K blocks of each
-    const int total = p.tiles_m * p.tiles_n;
+    const int total = p.tiles;
     int first = (int)blockIdx.x / CTAS, stride = (int)gridDim.x / CTAS, kb0 = 0, kb1 = p.kblocks;
     int parts = 1, part = 0;
     if constexpr (SPLIT) {
@@ -270,7 +271,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             bool stop = false;
             for (int i = 0; i < ntiles && !stop; ++i) {
                 int tm, tn;
-                raster(p.tiles_m, p.tiles_n, p.group_m, first + i * stride, tm, tn);
+                raster(p.tiles_m, p.tiles_n, p.group_m, p.tile0 + first + i * stride, tm, tn);
                 const int m0 = (tm * CTAS + half) * BM, n0 = tn * BN + half * S::BROWS;
                 for (int kb = kb0; kb < kb1; ++kb) {
                     if (r.used == STAGES && !tc::wait(empty0 + 8 * r.s, r.parity ^ 1, abort_flag)) {
@@ -351,7 +352,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             if (!__all_sync(0xffffffffu, ok && !*abort_flag)) break;
             tc::fence_after_sync();
             int tm, tn;
-            raster(p.tiles_m, p.tiles_n, p.group_m, first + i * stride, tm, tn);
+            raster(p.tiles_m, p.tiles_n, p.group_m, p.tile0 + first + i * stride, tm, tn);
             const int m0 = (tm * CTAS + half) * BM;
             const uint32_t acc = tmem + (uint32_t)(b * BN + side * (BN / 2));
             if constexpr (SPLIT) {
@@ -398,7 +399,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         // This CTA's rows are held by the CTAs of its half of every pair.
         cluster_sync();
         int tm, tn;
-        raster(p.tiles_m, p.tiles_n, p.group_m, first, tm, tn);
+        raster(p.tiles_m, p.tiles_n, p.group_m, p.tile0 + first, tm, tn);
         const int m0 = (tm * CTAS + half) * BM;
         const int rows = min(BM, p.epi.M - m0);
         const int n0 = tn * BN;
@@ -429,11 +430,9 @@ bool operand_map(CUtensorMap *map, const TcOperand &o, int type, int rows, int K
                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
-// `parts`: K parts (SPLIT); `most`: CTAs (CTAS = 1) or pairs that run at once
-// (persistent).
 template <int CTAS, int BN, class O, bool SPLIT>
 cudaError_t launch(int type, const TcOperand &A, const TcOperand &B, int K, const LayerEpi &epi,
-                   int parts, int most, cudaStream_t s) {
+                   const Piece &piece, cudaStream_t s) {
     using S = Shape<CTAS, BN, SPLIT>;
     static PerContext<bool> configured;
     bool done = false;
@@ -471,9 +470,11 @@ cudaError_t launch(int type, const TcOperand &A, const TcOperand &B, int K, cons
     };
     p.tma = !SPLIT && epi.vec == 16 && out_map(&tmY, epi.Y, epi.ldy) &&
             (epi.Z == nullptr || out_map(&tmZ, epi.Z, epi.ldz));
-    const long long tiles = (long long)p.tiles_m * p.tiles_n;
-    const long long ctas = SPLIT ? tiles * CTAS * parts : CTAS * (tiles < most ? tiles : most);
-    Config c(ctas, S::SMEM, SPLIT ? CTAS * parts : CTAS, s);
+    p.tile0 = piece.tile0;
+    p.tiles = piece.tiles;
+    const long long most = piece.room < piece.tiles ? piece.room : piece.tiles;
+    const long long ctas = CTAS * (SPLIT ? (long long)piece.tiles * piece.parts : most);
+    Config c(ctas, S::SMEM, SPLIT ? CTAS * piece.parts : CTAS, s);
     return cudaLaunchKernelEx(&c.cfg, linear_tc_kernel<CTAS, BN, O, SPLIT>, tmA, tmB, tmY, tmZ, p);
 }
 
@@ -501,19 +502,18 @@ cudaError_t capacity(Capacity &cap) {
 }
 
 // The tile and schedule, by their cost in microseconds.  Measured on GB300
-// (graph of 20 calls, bf16, weights out of L2):
-//   a 64- or 128-wide tile of one CTA takes about 0.21 us a stage of K, a 256 x
-//   256 tile of a pair 0.27; what does not depend on K is about 5 us a launch,
-//   6.5 with pairs; joining the parts of a split tile about 1 us and, for 128
-//   rows, 3 more (6 for a pair's tile).
-// The persistent schedules pay the rest once and the stages in waves; a split
-// tile must find all its clusters resident at once.  The choice against the
-// others there, in us: 64 x 1024 x 4096 128-wide in 8 parts 7.4 (whole 18.1, in
-// 4 9.0), 128 x 4096 x 4096 in 4 parts 12.6 (64-wide in 2 13.9, whole 19.5),
-// 256 x 4096 x 4096 in 2 15.8 (19.2), 512 x 4096 x 4096 whole 128-wide 19.9
-// (pairs 23.7, pairs in 2 parts 20.6), 1024 x 2048 x 8192 pairs in 2 28.3
-// (pairs 41.6, 128-wide 36.0), 2048^3 pairs 16.1 (19.9), 1024^3 64-wide 6.9 (7.5;
-// pairs 10.0).
+// (graph of 20 calls, bf16, weights out of L2): a 64- or 128-wide tile of one
+// CTA takes about 0.21 us a stage of K, a 256 x 256 tile of a pair 0.27; what
+// does not depend on K is about 5 us a launch, 6.5 with pairs; joining the parts
+// of a split tile about 1 us and, for 128 rows, 3 more (5 for a pair's tile).
+// The choice against the others there, in us: 64 x 1024 x 4096 128-wide in 8
+// parts 7.5 (whole 18.1, in 4 9.1), 128 x 4096 x 4096 in 4 parts 12.5 (64-wide in
+// 2 13.8, whole 19.3), 256 x 4096 x 4096 in 2 15.7 (19.5), 512 x 4096 x 4096 whole
+// 128-wide 19.7 (pairs 23.5, pairs in 2 parts 19.9), 1024 x 2048 x 8192 pairs in 2
+// 28.1 (pairs 40.3, 128-wide 34.8), 2048^3 pairs 15.7 (19.8), 1024^3 64-wide 6.8
+// (7.6; pairs 10.0).
+constexpr Costs kCosts = {{0.21, 0.21, 0.27}, {5.0, 6.5}, {1.5, 3.0, 5.0}};
+
 template <class O>
 cudaError_t dispatch(int type, const TcOperand &A, const TcOperand &B, int K, const LayerEpi &epi,
                      cudaStream_t s) {
@@ -521,39 +521,20 @@ cudaError_t dispatch(int type, const TcOperand &A, const TcOperand &B, int K, co
     cudaError_t e = capacity(cap);
     if (e != cudaSuccess) return e;
     const int bk = kRowBytes / dtype_size(type);
-    const int kblocks = (K + bk - 1) / bk;
-    struct {
-        int ctas, bn, parts;
-        double us;
-    } best = {0, 0, 0, 1e30};
-    auto consider = [&](int ctas, int bn, int parts) {
-        const long long tiles = (long long)((epi.M + ctas * BM - 1) / (ctas * BM)) *
-                                ((epi.N + bn - 1) / bn);
-        const int room = cap.of(ctas * parts);
-        if (parts > 1 && (tiles > room || kblocks < 2 * parts)) return;
-        const double stage = ctas == 2 ? 0.27 : 0.21;
-        double us = (double)((tiles + room - 1) / room) * ((kblocks + parts - 1) / parts) * stage +
-                    (ctas == 2 ? 6.5 : 5.0);
-        if (parts > 1)
-            us += 1.0 + (ctas == 2 ? 5.0 : 3.0 * bn / 128) * (epi.M < BM ? epi.M : BM) / BM;
-        if (us < best.us) best = {ctas, bn, parts, us};
-    };
-    consider(2, 256, 1);
-    consider(1, 64, 1);
-    consider(1, 128, 1);
-    for (int parts = 2; parts <= 8; parts *= 2) {
-        if (parts <= 4) consider(2, 256, parts);
-        consider(1, 128, parts);
-        consider(1, 64, parts);
+    const Plan plan = plan_tiles(epi.M, epi.N, (K + bk - 1) / bk, cap, kCosts);
+    for (int i = 0; i < plan.pieces && e == cudaSuccess; ++i) {
+        const Piece &p = plan.piece[i];
+        if (plan.ctas == 2)
+            e = p.parts > 1 ? launch<2, 256, O, true>(type, A, B, K, epi, p, s)
+                            : launch<2, 256, O, false>(type, A, B, K, epi, p, s);
+        else if (plan.bn == 128)
+            e = p.parts > 1 ? launch<1, 128, O, true>(type, A, B, K, epi, p, s)
+                            : launch<1, 128, O, false>(type, A, B, K, epi, p, s);
+        else
+            e = p.parts > 1 ? launch<1, 64, O, true>(type, A, B, K, epi, p, s)
+                            : launch<1, 64, O, false>(type, A, B, K, epi, p, s);
     }
-    if (best.parts > 1) {
-        if (best.ctas == 2) return launch<2, 256, O, true>(type, A, B, K, epi, best.parts, 0, s);
-        return best.bn == 128 ? launch<1, 128, O, true>(type, A, B, K, epi, best.parts, 0, s)
-                              : launch<1, 64, O, true>(type, A, B, K, epi, best.parts, 0, s);
-    }
-    if (best.ctas == 2) return launch<2, 256, O, false>(type, A, B, K, epi, 1, cap.of(2), s);
-    return best.bn == 128 ? launch<1, 128, O, false>(type, A, B, K, epi, 1, cap.sms, s)
-                          : launch<1, 64, O, false>(type, A, B, K, epi, 1, cap.sms, s);
+    return e;
 }
 
 }  // namespace ltc

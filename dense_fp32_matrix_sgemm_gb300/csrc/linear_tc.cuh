@@ -238,6 +238,7 @@ __device__ __forceinline__ void join_parts(const LayerEpi &e, uint32_t ring, int
 inline CUtensorMapDataType map_type(int type) {
     return type == SGEMM_BF16  ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
            : type == SGEMM_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+           : type == SGEMM_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                : CU_TENSOR_MAP_DATA_TYPE_UINT8;
 }
 
@@ -291,6 +292,67 @@ struct Capacity {
     int of(int size) const { return size == 1 ? sms : clusters[size == 2 ? 0 : size == 4 ? 1 : 2]; }
 };
 cudaError_t capacity(Capacity &cap);   // linear_tc.cu
+
+// Consecutive tiles in one launch: `parts` K parts each (1: whole tiles,
+// walked by at most `room` CTAs or pairs).
+struct Piece {
+    int tile0, tiles, parts, room;
+};
+
+// How a product is computed: tiles of ctas * 128 x bn, in one launch, or (pairs)
+// whole waves of tiles in one and the rest split in K in a second.
+struct Plan {
+    int ctas = 0, bn = 0, pieces = 0;
+    Piece piece[2];
+    double us = 1e30;
+};
+
+// Microseconds: `stage` a stage of K of a tile by its width (64, 128, a pair's
+// 256), `fixed` a launch of single CTAs and of pairs, `join` for the parts of a
+// split tile of 128 rows by width, next to 1 us a split launch.
+struct Costs {
+    double stage[3], fixed[2], join[3];
+};
+
+inline Plan plan_tiles(int M, int N, int kblocks, const Capacity &cap, const Costs &cost) {
+    Plan best;
+    const double rows = (M < BM ? M : BM) / (double)BM;
+    // one split launch of `tiles` tiles; negative where it cannot run at once
+    auto split = [&](int ctas, int w, long long tiles, int parts) {
+        if (tiles > cap.of(ctas * parts) || kblocks < 2 * parts) return -1.0;
+        return ((kblocks + parts - 1) / parts) * cost.stage[w] + cost.fixed[ctas - 1] + 1.0 +
+               cost.join[w] * rows;
+    };
+    auto take = [&](double us, int ctas, int bn, Piece a, Piece b, int pieces) {
+        if (us >= best.us) return;
+        best.us = us;
+        best.ctas = ctas;
+        best.bn = bn;
+        best.piece[0] = a;
+        best.piece[1] = b;
+        best.pieces = pieces;
+    };
+    const int widths[3] = {64, 128, 256}, order[3] = {2, 0, 1};
+    for (int w : order) {
+        const int ctas = w == 2 ? 2 : 1, bn = widths[w];
+        const long long all = (long long)((M + ctas * BM - 1) / (ctas * BM)) * ((N + bn - 1) / bn);
+        if (all > 0x7fffffff) continue;
+        const int tiles = (int)all, room = cap.of(ctas);
+        const long long waves = tiles / room;
+        const int tail = (int)(tiles - waves * room);
+        take((double)(waves + (tail > 0)) * kblocks * cost.stage[w] + cost.fixed[ctas - 1], ctas, bn,
+             {0, tiles, 1, room}, {}, 1);
+        for (int parts = 2; parts <= (ctas == 2 ? 4 : 8); parts *= 2) {
+            const double whole = split(ctas, w, tiles, parts);
+            if (whole > 0) take(whole, ctas, bn, {0, tiles, parts, 0}, {}, 1);
+            const double rest = ctas == 2 && waves > 0 && tail > 0 ? split(2, w, tail, parts) : -1;
+            if (rest > 0)
+                take((double)waves * kblocks * cost.stage[w] + cost.fixed[1] + rest, ctas, bn,
+                     {0, tiles - tail, 1, room}, {tiles - tail, tail, parts, 0}, 2);
+        }
+    }
+    return best;
+}
 
 }  // namespace ltc
 }  // namespace sgemm
