@@ -47,7 +47,7 @@ cudaError_t launch_linear_tc(int in_type, const TcOperand &A, const TcOperand &B
                              const LayerEpi &epi, cudaStream_t s);
 
 // The same product of few rows on the CUDA cores, one pass over W; any type
-// and alignment.  linear_rows.cu.
+// and alignment, transW == 1 for the types other than f32.  linear_rows.cu.
 cudaError_t launch_linear_rows(int in_type, const void *X, int64_t ldx, const void *W, int64_t ldw,
                                int transW, int K, const LayerEpi &epi, cudaStream_t s);
 

@@ -77,9 +77,19 @@ int check_workspace(void *ws, uint64_t have, size_t need) {
     return SGEMM_OK;
 }
 
-// Rows up to which a product runs on the CUDA cores (linear_rows.cu) in one
-// pass over the weights.
-int few_rows(int type) { return type == SGEMM_F32 ? 16 : type == SGEMM_E4M3 ? 2 : 4; }
+// Whether a product of M rows runs on the CUDA cores (linear_rows.cu), in one
+// pass over the weights, or on the tensor cores.  Measured with 4096 x 4096
+// weights out of L2, in us, CUDA cores / tensor cores: bf16 1 row 7.9 / 10.5, 2
+// rows 9.0 / 10.5, 4 rows 15.7 / 10.6 (but 512 x 512, 4 rows: 3 / 6, where launch
+// and set-up count); bf16 stored K x N 1 row 24 / 10.5; e4m3 1 row 5.9 / 8.6, 2
+// rows 7.4 / 8.6, 3 rows 8.7 / 8.6; f32, whose planes the tensor cores need
+// written first, 8 rows 25 / 50, 16 rows 45 / 50.
+bool on_cuda_cores(int type, int64_t M, int64_t N, int64_t K, int transW) {
+    if (K == 0) return true;
+    if (type == SGEMM_F32) return M <= 16;
+    if (!transW) return false;
+    return M <= 2 || (type != SGEMM_E4M3 && M <= 4 && N * K <= (1 << 22));
+}
 
 // A tensor-core operand of rows x cols as stored: whether TMA can read it
 // where it lies, and the leading dimension (elements) and bytes of its copy
@@ -130,7 +140,7 @@ LayerEpi plain_epi(int type, void *Y, int64_t ldy, int64_t M, int64_t N) {
 
 size_t linear_bytes(int dtype, int64_t M, int64_t N, int64_t K, const void *X, int64_t ldx,
                     const void *W, int64_t ldw, int transW) {
-    if (M <= few_rows(dtype) || K == 0) return 0;
+    if (on_cuda_cores(dtype, M, N, K, transW)) return 0;
     if (dtype == SGEMM_F32)
         return f32_planes_bytes(M, K) + f32_planes_bytes(transW ? N : K, transW ? K : N);
     const int size = dtype_size(dtype);
@@ -153,7 +163,7 @@ BackwardPlan backward_plan(int dtype, int64_t M, int64_t N, int64_t K, const voi
     BackwardPlan p = {};
     const int size = dtype_size(dtype);
     const bool f32 = dtype == SGEMM_F32;
-    const bool dx_rows = M <= few_rows(dtype);   // dX on the CUDA cores: any alignment
+    const bool dx_rows = on_cuda_cores(dtype, M, K, N, !transW);   // dX: any alignment
     const bool tc = (dx && !dx_rows) || dw;      // a tensor-core product reads dZ
     p.dz = (dx || dw) && K > 0 &&
            (act != SGEMM_ACT_NONE || (!f32 && tc && !tma_ok(dY, lddy, size)));
@@ -210,8 +220,9 @@ int linear(int dtype, int64_t M, int64_t N, int64_t K, const void *X, int64_t ld
                     activation, out_dtype, 1};
     epi.vec = vector_width(out_dtype, epi);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (M <= few_rows(dtype) || K == 0)
-        return launched(launch_linear_rows(dtype, X, ldx, W, ldw, transW, (int)K, epi, s));
+    if (on_cuda_cores(dtype, M, N, K, transW))
+        return launched(launch_linear_rows(dtype, X, ldx, W, ldw, K > 0 ? transW : 1, (int)K, epi,
+                                           s));
     if (dtype == SGEMM_F32) {
         const int64_t wr = transW ? N : K, wc = transW ? K : N;
         char *const wsw = static_cast<char *>(workspace) + f32_planes_bytes(M, K);
@@ -281,7 +292,7 @@ int linear_backward(int dtype, int64_t M, int64_t N, int64_t K, const void *dY, 
     if (e != cudaSuccess) return launched(e);
     const void *g = p.dz ? dZ : dY;
     const int64_t ldg = p.dz ? p.lddz : lddy;
-    const bool dx_rows = M <= few_rows(dtype);
+    const bool dx_rows = on_cuda_cores(dtype, M, K, N, !transW);
     if (dx && dx_rows)
         // reduction over the output features: W's other orientation
         e = launch_linear_rows(dtype, g, ldg, W, ldw, !transW, (int)N,

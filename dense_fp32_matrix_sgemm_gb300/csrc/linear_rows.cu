@@ -7,9 +7,9 @@
 // the same, and FP32 FMAs (packed in pairs) keep up for the few rows that the
 // launcher sends here.
 //
-// Weights stored N x K (dot form): a warp takes two output features and walks
-// K, each lane with 16-byte pieces of both rows of W and of the MR rows of X
-// (X stays in L1).  Where the features alone would not fill the SMs, K is
+// Weights stored N x K (dot form): a warp takes two or four output features and
+// walks K, each lane with 16-byte pieces of their rows of W and of the MR rows of
+// X (X stays in L1).  Where the features alone would not fill the SMs, K is
 // split over the warps of a CTA and their sums are added through shared
 // memory, in warp order.
 // Weights stored K x N (column form): a lane takes 16 bytes of consecutive
@@ -32,44 +32,42 @@ namespace rows {
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 
-// 16 bytes (or one element) of T as pairs of floats.
+// W elements of T loaded as one access (16 bytes, or one element), and their
+// values as pairs of floats.
 template <class T, int W>
 struct Piece {
-    static constexpr int PAIRS = W > 1 ? W / 2 : 1;
-};
-
-template <class T, int W>
-__device__ __forceinline__ void load_pairs(const T *p, float2 (&f)[Piece<T, W>::PAIRS]) {
-    if constexpr (W == 1) {
-        f[0] = make_float2(to_f32(*p), 0.f);
-    } else {
-        const Vec<T, W> v = load_vec<T, W>(p);
+    static constexpr int PAIRS = W / 2;
+    uint4 u;
+    __device__ __forceinline__ void load(const T *p) { u = *reinterpret_cast<const uint4 *>(p); }
+    __device__ __forceinline__ void get(float2 (&f)[PAIRS]) const {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        if constexpr (W == 4) {
+            f[0] = make_float2(__uint_as_float(w[0]), __uint_as_float(w[1]));
+            f[1] = make_float2(__uint_as_float(w[2]), __uint_as_float(w[3]));
+        } else if constexpr (W == 8) {
 #pragma unroll
-        for (int i = 0; i < W / 2; ++i) f[i] = make_float2(to_f32(v.v[2 * i]), to_f32(v.v[2 * i + 1]));
-    }
-}
-template <class T, int W>
-__device__ __forceinline__ void load_pairs_e4m3(const uint8_t *p, float2 (&f)[Piece<T, W>::PAIRS]) {
-    if constexpr (W == 1) {
-        f[0] = make_float2(from_e4m3x2(*p).x, 0.f);
-    } else {
-        const uint4 v = *reinterpret_cast<const uint4 *>(p);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            for (int i = 0; i < 4; ++i) f[i] = unpack2<T>(w[i]);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[2 * i] = from_e4m3x2((uint16_t)(w[i] & 0xffffu));
-            f[2 * i + 1] = from_e4m3x2((uint16_t)(w[i] >> 16));
+            for (int i = 0; i < 4; ++i) {
+                f[2 * i] = from_e4m3x2((uint16_t)(w[i] & 0xffffu));
+                f[2 * i + 1] = from_e4m3x2((uint16_t)(w[i] >> 16));
+            }
         }
     }
-}
-template <>
-__device__ __forceinline__ void load_pairs<uint8_t, 16>(const uint8_t *p, float2 (&f)[8]) {
-    load_pairs_e4m3<uint8_t, 16>(p, f);
-}
-template <>
-__device__ __forceinline__ void load_pairs<uint8_t, 1>(const uint8_t *p, float2 (&f)[1]) {
-    load_pairs_e4m3<uint8_t, 1>(p, f);
-}
+};
+template <class T>
+struct Piece<T, 1> {
+    static constexpr int PAIRS = 1;
+    T u;
+    __device__ __forceinline__ void load(const T *p) { u = *p; }
+    __device__ __forceinline__ void get(float2 (&f)[1]) const {
+        if constexpr (std::is_same<T, uint8_t>::value)
+            f[0] = make_float2(from_e4m3x2(u).x, 0.f);
+        else
+            f[0] = make_float2(to_f32(u), 0.f);
+    }
+};
 
 struct Args {
     const void *X, *W;
@@ -79,102 +77,110 @@ struct Args {
     LayerEpi epi;
 };
 
-// Dot form.  Warp w of the CTA: feature pair w / split, K pieces w % split of
-// split.  Accumulators hold the sums over even and odd positions of the
-// pieces apart (one packed FMA for both).
+// Dot form.  Warp w of the CTA: features j0 .. j0 + F - 1 of group w / split, K
+// pieces w % split of split.  Accumulators hold the sums over even and odd
+// positions of the pieces apart (one packed FMA for both).  F is 4 for 2 to 4
+// rows of f32, where each piece of X is then read from L1 for four features
+// (4096 x 4096 weights, 4 rows: 24.5 -> 16.3 us), else 2 (16-bit, 2 rows: 9.0
+// us, with four 9.8; f32, 8 rows: 25, with four 35, whose 196 registers leave
+// too few warps).
+template <class T, int MR>
+constexpr int kFeatures = sizeof(T) == 4 && (MR == 2 || MR == 4) ? 4 : 2;
+
 template <class T, class O, int W, int MR>
 __global__ void __launch_bounds__(kThreads) dot_kernel(const Args a) {
-    __shared__ float red[kWarps][2 * MR];
+    constexpr int F = kFeatures<T, MR>;
+    constexpr int U = F == 2 && MR <= 2 ? 4 : 2;   // pieces in flight a feature
+    constexpr int P = Piece<T, W>::PAIRS;
+    constexpr int SUMS = F * MR;
+    static_assert(SUMS <= 32, "a sum a lane");
+    __shared__ float red[kWarps][SUMS];
     pdl_trigger();
     pdl_wait();
-    constexpr int P = Piece<T, W>::PAIRS;
-    constexpr int U = W == 1 ? 4 : MR <= 2 ? 4 : 2;   // pieces in flight a row
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int sub = warp % a.split;
-    const int j0 = 2 * (int)(blockIdx.x * (kWarps / a.split) + warp / a.split);
-    const T *w0 = static_cast<const T *>(a.W) + j0 * a.ldw;
-    const bool two = j0 + 1 < a.epi.N;
-    const T *w1 = two ? w0 + a.ldw : w0;
+    const int j0 = F * (int)(blockIdx.x * (kWarps / a.split) + warp / a.split);
+    const T *w[F];
+#pragma unroll
+    for (int f = 0; f < F; ++f)
+        w[f] = static_cast<const T *>(a.W) + (int64_t)min(j0 + f, a.epi.N - 1) * a.ldw;
     const int groups = (a.epi.M + MR - 1) / MR;
     for (int g = blockIdx.y; g < groups; g += gridDim.y) {
         const int m0 = g * MR;
-        float2 acc[2][MR];
+        float2 acc[F][MR];
 #pragma unroll
-        for (int m = 0; m < MR; ++m) acc[0][m] = acc[1][m] = make_float2(0.f, 0.f);
+        for (int f = 0; f < F; ++f)
+#pragma unroll
+            for (int m = 0; m < MR; ++m) acc[f][m] = make_float2(0.f, 0.f);
         if (j0 < a.epi.N) {
             const T *x[MR];
 #pragma unroll
             for (int m = 0; m < MR; ++m)
                 x[m] = static_cast<const T *>(a.X) + min(m0 + m, a.epi.M - 1) * a.ldx;
             const int step = a.split * 32 * W;
-            int k = (sub * 32 + lane) * W;
-            for (; k + (U - 1) * step < a.K; k += U * step) {
-                float2 f0[U][P], f1[U][P];
+            auto use = [&](const Piece<T, W> (&raw)[F], int k) {
+                float2 fw[F][P];
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    load_pairs<T, W>(w0 + k + u * step, f0[u]);
-                    load_pairs<T, W>(w1 + k + u * step, f1[u]);
-                }
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-#pragma unroll
-                    for (int m = 0; m < MR; ++m) {
-                        float2 fx[P];
-                        load_pairs<T, W>(x[m] + k + u * step, fx);
-#pragma unroll
-                        for (int i = 0; i < P; ++i) {
-                            acc[0][m] = __ffma2_rn(f0[u][i], fx[i], acc[0][m]);
-                            acc[1][m] = __ffma2_rn(f1[u][i], fx[i], acc[1][m]);
-                        }
-                    }
-                }
-            }
-            for (; k < a.K; k += step) {
-                float2 f0[P], f1[P];
-                load_pairs<T, W>(w0 + k, f0);
-                load_pairs<T, W>(w1 + k, f1);
+                for (int f = 0; f < F; ++f) raw[f].get(fw[f]);
 #pragma unroll
                 for (int m = 0; m < MR; ++m) {
+                    Piece<T, W> px;
+                    px.load(x[m] + k);
                     float2 fx[P];
-                    load_pairs<T, W>(x[m] + k, fx);
+                    px.get(fx);
 #pragma unroll
-                    for (int i = 0; i < P; ++i) {
-                        acc[0][m] = __ffma2_rn(f0[i], fx[i], acc[0][m]);
-                        acc[1][m] = __ffma2_rn(f1[i], fx[i], acc[1][m]);
-                    }
+                    for (int f = 0; f < F; ++f)
+#pragma unroll
+                        for (int i = 0; i < P; ++i)
+                            acc[f][m] = __ffma2_rn(fw[f][i], fx[i], acc[f][m]);
                 }
+            };
+            int k = (sub * 32 + lane) * W;
+            for (; k + (U - 1) * step < a.K; k += U * step) {
+                Piece<T, W> raw[U][F];
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int f = 0; f < F; ++f) raw[u][f].load(w[f] + k + u * step);
+#pragma unroll
+                for (int u = 0; u < U; ++u) use(raw[u], k + u * step);
+            }
+            for (; k < a.K; k += step) {
+                Piece<T, W> raw[F];
+#pragma unroll
+                for (int f = 0; f < F; ++f) raw[f].load(w[f] + k);
+                use(raw, k);
             }
         }
-        float v[2 * MR];   // [feature][row]
-#pragma unroll
-        for (int m = 0; m < MR; ++m) {
-            v[m] = acc[0][m].x + acc[0][m].y;
-            v[MR + m] = acc[1][m].x + acc[1][m].y;
-        }
-#pragma unroll
-        for (int i = 0; i < 2 * MR; ++i)
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-        // lane i < 2 MR keeps sum i
+        // lane i < SUMS keeps the sum of feature i / MR and row i % MR
         float mine = 0.f;
 #pragma unroll
-        for (int i = 0; i < 2 * MR; ++i) mine = lane == i ? v[i] : mine;
+        for (int f = 0; f < F; ++f)
+#pragma unroll
+            for (int m = 0; m < MR; ++m) {
+                float v = acc[f][m].x + acc[f][m].y;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+                if (lane == f * MR + m) mine = v;
+            }
         if (a.split > 1) {
             __syncthreads();   // the previous group's sums have been read
-            if (lane < 2 * MR) red[warp][lane] = mine;
+            if (lane < SUMS) red[warp][lane] = mine;
             __syncthreads();
-            if (sub == 0 && lane < 2 * MR)
+            if (sub == 0 && lane < SUMS)
                 for (int s = 1; s < a.split; ++s) mine += red[warp + s][lane];
         }
         const int row = m0 + lane % MR, col = j0 + lane / MR;
-        if (sub == 0 && lane < 2 * MR && row < a.epi.M && col < a.epi.N)
+        if (sub == 0 && lane < SUMS && row < a.epi.M && col < a.epi.N)
             finish1<O>(a.epi, row, col, mine);
     }
 }
 
 // Column form: CTA (x, y) of a cluster along x of `cluster_size` CTAs: columns
-// [strip * 32 W, ...), k = (rank * 8 + warp) + 8 size * i.
-template <class T, class O, int W, int MR>
+// [strip * 32 W, ...), k = rank * kWarps + warp + kWarps * size * i.  f32 only: 16-bit weights in this
+// orientation go to the tensor cores, which take it as it is (4096 x 4096, one
+// row: 10.5 us there, 24 here).
+template <int W, int MR>
 __global__ void __launch_bounds__(kThreads) column_kernel(const Args a) {
     constexpr int COLS = 32 * W;
     __shared__ __align__(16) float red[kWarps][MR][COLS];
@@ -193,28 +199,35 @@ __global__ void __launch_bounds__(kThreads) column_kernel(const Args a) {
 #pragma unroll
             for (int j = 0; j < W; ++j) acc[m][j] = 0.f;
         if (c < a.epi.N) {
-            const T *w = static_cast<const T *>(a.W) + c;
-            const T *x[MR];
+            const float *w = static_cast<const float *>(a.W) + c;
+            const float *x[MR];
 #pragma unroll
             for (int m = 0; m < MR; ++m)
-                x[m] = static_cast<const T *>(a.X) + min(m0 + m, a.epi.M - 1) * a.ldx;
+                x[m] = static_cast<const float *>(a.X) + min(m0 + m, a.epi.M - 1) * a.ldx;
             const int step = kWarps * (int)size;
-            constexpr int U = 4;   // rows of W in flight
+            constexpr int U = 4;
             for (int k = (int)rank * kWarps + warp; k < a.K; k += U * step) {
-                Vec<T, W> vw[U];
+                Raw<float, W> vw[U];
+                float vx[U][MR];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int ku = k + u * step;
+                    if (ku < a.K) vw[u].load(w + (int64_t)ku * a.ldw);
+                }
 #pragma unroll
                 for (int u = 0; u < U; ++u)
-                    if (k + u * step < a.K) vw[u] = load_vec<T, W>(w + (k + u * step) * a.ldw);
+#pragma unroll
+                    for (int m = 0; m < MR; ++m) vx[u][m] = x[m][min(k + u * step, a.K - 1)];
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     if (k + u * step >= a.K) break;
+                    float f[W];
+                    vw[u].get(f);
 #pragma unroll
-                    for (int m = 0; m < MR; ++m) {
-                        const float xv = to_f32(x[m][k + u * step]);
+                    for (int m = 0; m < MR; ++m)
 #pragma unroll
                         for (int j = 0; j < W; ++j)
-                            acc[m][j] = fmaf(xv, to_f32(vw[u].v[j]), acc[m][j]);
-                    }
+                            acc[m][j] = fmaf(vx[u][m], f[j], acc[m][j]);
                 }
             }
         }
@@ -222,7 +235,7 @@ __global__ void __launch_bounds__(kThreads) column_kernel(const Args a) {
 #pragma unroll
         for (int m = 0; m < MR; ++m)
 #pragma unroll
-            for (int j = 0; j < W; ++j) red[warp][m][lane * W + j] = acc[m][j];
+            for (int j = 0; j < W; ++j) red[warp][m][j * 32 + lane] = acc[m][j];
         __syncthreads();
         for (int i = threadIdx.x; i < MR * COLS; i += kThreads) {
             float s = 0.f;
@@ -232,12 +245,14 @@ __global__ void __launch_bounds__(kThreads) column_kernel(const Args a) {
         }
         if (size > 1) cluster_sync();
         else __syncthreads();
-        // each CTA of the cluster finishes a share of the strip
-        for (int i = (int)rank * kThreads + threadIdx.x; i < MR * COLS; i += (int)size * kThreads) {
-            const int m = i / COLS, col = strip * COLS + i % COLS;
-            const float s = size > 1 ? cluster_sum_f32(smem_u32(&red[0][m][i % COLS]), size)
-                                     : red[0][m][i % COLS];
-            if (m0 + m < a.epi.M && col < a.epi.N) finish1<O>(a.epi, m0 + m, col, s);
+        // each CTA of the cluster finishes a share of the strip (position p of a
+        // strip is column p % 32 * W + p / 32)
+        for (int i = (int)rank * kThreads + threadIdx.x; i < MR * COLS;
+             i += (int)size * kThreads) {
+            const int m = i / COLS, p = i % COLS, col = strip * COLS + p % 32 * W + p / 32;
+            const float s = size > 1 ? cluster_sum_f32(smem_u32(&red[0][m][p]), size)
+                                     : red[0][m][p];
+            if (m0 + m < a.epi.M && col < a.epi.N) finish1<float>(a.epi, m0 + m, col, s);
         }
         // red is written again, or the CTA ends, only after every peer has read it
         if (size > 1) cluster_sync();
@@ -246,10 +261,10 @@ __global__ void __launch_bounds__(kThreads) column_kernel(const Args a) {
 }
 
 template <class K>
-cudaError_t launch(K kernel, dim3 grid, int cluster, const Args &a, cudaStream_t s) {
+cudaError_t launch(K kernel, dim3 grid, int threads, int cluster, const Args &a, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3((unsigned)threads);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -270,22 +285,24 @@ cudaError_t run(Args a, int transW, cudaStream_t s) {
     const int groups = (a.epi.M + MR - 1) / MR;
     const unsigned gy = (unsigned)(groups < 65535 ? groups : 65535);
     if (transW) {
-        // warps a feature pair: until about 24 warps an SM are busy, each with
-        // at least one piece of K a lane
-        const int64_t pairs = (a.epi.N + 1) / 2;
+        // warps a group of features: until about 24 warps an SM are busy, each
+        // with at least one piece of K a lane
+        constexpr int F = kFeatures<T, MR>;
+        const int64_t sets = (a.epi.N + F - 1) / F;
         a.split = 1;
-        while (a.split < kWarps && pairs * gy * a.split < kSms * 24 &&
+        while (a.split < kWarps && sets * gy * a.split < kSms * 24 &&
                (int64_t)a.K > (int64_t)a.split * 32 * W)
             a.split *= 2;
         const int64_t per_cta = kWarps / a.split;
-        return launch(dot_kernel<T, O, W, MR>, dim3((unsigned)((pairs + per_cta - 1) / per_cta), gy),
-                      1, a, s);
+        return launch(dot_kernel<T, O, W, MR>, dim3((unsigned)((sets + per_cta - 1) / per_cta), gy),
+                      kThreads, 1, a, s);
     }
-    if constexpr (!std::is_same<T, uint8_t>::value) {
+    if constexpr (std::is_same<T, float>::value) {
         const int64_t strips = (a.epi.N + 32 * W - 1) / (32 * W);
         int size = 1;
         while (size < 8 && strips * gy * size < kSms * 2 && a.K > size * kWarps * 4) size *= 2;
-        return launch(column_kernel<T, O, W, MR>, dim3((unsigned)(strips * size), gy), size, a, s);
+        return launch(column_kernel<W, MR>, dim3((unsigned)(strips * size), gy), kThreads, size, a,
+                      s);
     }
     return cudaErrorInvalidValue;
 }
