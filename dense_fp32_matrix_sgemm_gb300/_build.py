@@ -122,7 +122,8 @@ def _build_layers(verbose: bool = False):
            "-isystem", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
            "-isystem", os.path.join(cuda, "include"), src, "-o", out + ".tmp",
            "-L", os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
-           "-lc10_cuda"]
+           "-lc10_cuda",
+           "-ltorch_cuda"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"_layers.cpp did not build:\n{r.stdout}\n{r.stderr}")

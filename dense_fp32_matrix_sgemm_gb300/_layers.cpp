@@ -12,6 +12,7 @@
 
 #include <ATen/ATen.h>
 #include <ATen/core/LegacyTypeDispatch.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -130,6 +131,12 @@ Weight weight(const at::Tensor &w, int64_t k, ScalarType type) {
     value_error("weight must have one unit stride");
 }
 
+// torch's CUDA allocation without its dispatcher (at::empty takes about twice
+// as long).
+at::Tensor fresh(const at::Tensor &like, at::IntArrayRef size, ScalarType type) {
+    return at::detail::empty_cuda(size, type, like.device(), c10::nullopt);
+}
+
 // Scratch memory: the caller's where it is large enough, else torch's.
 struct Scratch {
     at::Tensor own;
@@ -147,15 +154,11 @@ struct Scratch {
                 return;
             }
         }
-        own = at::empty({(int64_t)need}, like.options().dtype(ScalarType::Byte));
+        own = fresh(like, {(int64_t)need}, ScalarType::Byte);
         p = own.data_ptr();
         bytes = need;
     }
 };
-
-at::Tensor fresh(const at::Tensor &like, at::IntArrayRef size, ScalarType type) {
-    return at::empty(size, like.options().dtype(type).requires_grad(false));
-}
 
 void *current_stream(const at::Tensor &t) {
     return c10::cuda::getCurrentCUDAStream(t.get_device()).stream();
