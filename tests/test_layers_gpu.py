@@ -567,3 +567,21 @@ def test_feed_forward_block():
     hq, hs = sg.quantize_rows(hidden)
     got = sg.linear(hq, q2, residual=s, x_scale=hs, w_scale=s2)
     assert float((got.double() - want).norm() / want.norm()) < 0.08
+
+
+@pytest.mark.parametrize("t", ["bf16", "f16"])
+def test_feed_forward_example(t):
+    """The example block learns (a gradient step along the exact gradient lowers
+    this smooth loss), and its 8-bit form stays near it: two roundings of 2^-4
+    relative to 8 bits on the way, averaged by the sums, under 8 %."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "feed_forward.py")
+    spec = importlib.util.spec_from_file_location("feed_forward_example", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    losses, off = example.run(130, 256, 512, 12, TYPES[t])
+    assert all(b < a for a, b in zip(losses, losses[1:])), losses
+    assert losses[-1] < 0.9 * losses[0]
+    assert off < 0.08
