@@ -14,21 +14,6 @@ namespace sgemm {
 
 // ------------------------------------------------------------------ types
 
-template <class T>
-struct TypeOf;
-template <>
-struct TypeOf<float> {
-    static constexpr int id = SGEMM_F32;
-};
-template <>
-struct TypeOf<__nv_bfloat16> {
-    static constexpr int id = SGEMM_BF16;
-};
-template <>
-struct TypeOf<__half> {
-    static constexpr int id = SGEMM_F16;
-};
-
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
@@ -224,40 +209,6 @@ __device__ __forceinline__ void finish1(const LayerEpi &e, int row, int col, flo
     static_cast<T *>(e.Y)[row * e.ldy + col] = from_f32<T>(y);
 }
 
-// Columns col .. col + G - 1 (col a multiple of G, G = 4 or 8) of `row` < M,
-// those below N; one access per matrix where the group is whole and e.vec
-// allows it.
-template <class T, int G>
-__device__ __forceinline__ void finish(const LayerEpi &e, int row, int col, const float (&acc)[G]) {
-    if (e.vec < G || col + G > e.N) {
-#pragma unroll
-        for (int j = 0; j < G; ++j)
-            if (col + j < e.N) finish1<T>(e, row, col + j, acc[j]);
-        return;
-    }
-    float z[G];
-#pragma unroll
-    for (int j = 0; j < G; ++j) z[j] = acc[j];
-    if (e.sx != nullptr) {
-        const float sx = e.sx[row];
-#pragma unroll
-        for (int j = 0; j < G; ++j) z[j] *= sx * e.sw[col + j];
-    }
-    if (e.bias != nullptr) {
-        const Vec<T, G> b = load_vec<T, G>(static_cast<const T *>(e.bias) + col);
-#pragma unroll
-        for (int j = 0; j < G; ++j) z[j] += to_f32(b.v[j]);
-    }
-    if (e.Z != nullptr) store_vec<T, G>(static_cast<T *>(e.Z) + row * e.ldz + col, z);
-    activate_all<T>(z, e.act);
-    if (e.R != nullptr) {
-        const Vec<T, G> r = load_vec<T, G>(static_cast<const T *>(e.R) + row * e.ldr + col);
-#pragma unroll
-        for (int j = 0; j < G; ++j) z[j] += to_f32(r.v[j]);
-    }
-    store_vec<T, G>(static_cast<T *>(e.Y) + row * e.ldy + col, z);
-}
-
 // What the epilogue takes for G fixed columns, loaded once for many rows.
 template <class T, int G>
 struct ColumnTerms {
@@ -272,7 +223,8 @@ struct ColumnTerms {
     }
 };
 
-// G columns col .. of one row, as finish; `t` holds the columns' terms.
+// Columns col .. col + G - 1 of `row` < M, those below N; one access per matrix
+// where the group is whole and e.vec allows it.
 template <class T, int G>
 __device__ __forceinline__ void finish_group(const LayerEpi &e, const ColumnTerms<T, G> &t, int row,
                                              int col, float (&z)[G]) {
@@ -348,6 +300,7 @@ __device__ __forceinline__ void load_32b(const void *p, uint32_t (&r)[8]) {
                    "=r"(r[6]), "=r"(r[7])
                  : "l"(p) : "memory");
 }
+
 // ------------------------------------------------------------------ 8-bit rows
 
 constexpr float kE4m3Max = 448.f;

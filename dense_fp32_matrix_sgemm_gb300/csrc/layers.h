@@ -18,9 +18,8 @@ __host__ __device__ inline int dtype_size(int t) {
 // What happens to an accumulator on its way to memory:
 //   z = acc * (sx ? sx[row] * sw[col] : 1) + bias[col];  Z = z
 //   Y = act(z) + R
-// All of `type` elements except the scales.  vec: the most of 16 (16-bit types),
-// 8 (16-bit types), 4 and 1 elements that every base and leading dimension is
-// aligned to.
+// All of `type` elements except the scales.  vec: the most of 16 (16-bit types
+// only), 4 and 1 elements that every base and leading dimension is aligned to.
 struct LayerEpi {
     void *Y, *Z;
     const void *R, *bias;

@@ -123,7 +123,7 @@ int vector_width(int type, const LayerEpi &e) {
                (e.Z == nullptr || (aligned(e.Z, bytes) && e.ldz % n == 0)) &&
                (e.R == nullptr || (aligned(e.R, bytes) && e.ldr % n == 0));
     };
-    return size == 2 && all(16) ? 16 : size == 2 && all(8) ? 8 : all(4) ? 4 : 1;
+    return size == 2 && all(16) ? 16 : all(4) ? 4 : 1;
 }
 
 LayerEpi plain_epi(int type, void *Y, int64_t ldy, int64_t M, int64_t N) {
