@@ -301,6 +301,36 @@ __device__ __forceinline__ void load_32b(const void *p, uint32_t (&r)[8]) {
                  : "l"(p) : "memory");
 }
 
+// ------------------------------------------------------------------ f32 planes
+
+// Two values as the three planes' pairs.
+__device__ __forceinline__ void split_pair(float x, float y, uint32_t (&w)[3]) {
+    const float x0 = __uint_as_float(__float_as_uint(x) & 0xffff0000u);
+    const float y0 = __uint_as_float(__float_as_uint(y) & 0xffff0000u);
+    const float rx = x - x0, ry = y - y0;   // exact
+    w[0] = (__float_as_uint(x) >> 16) | (__float_as_uint(y) & 0xffff0000u);
+    w[1] = pack2<__nv_bfloat16>(rx, ry);
+    const float2 m = unpack2<__nv_bfloat16>(w[1]);
+    w[2] = pack2<__nv_bfloat16>(rx - m.x, ry - m.y);
+}
+
+// W values into the three planes, `plane` elements apart, at `p`.
+template <int W>
+__device__ __forceinline__ void put_planes(__nv_bfloat16 *p, int64_t plane, const float (&x)[W]) {
+    static_assert(W == 1 || W == 4, "one value or four");
+    uint32_t w[(W + 1) / 2][3];
+#pragma unroll
+    for (int i = 0; i < (W + 1) / 2; ++i)
+        split_pair(x[2 * i], W == 1 ? 0.f : x[(2 * i + 1) % W], w[i]);
+#pragma unroll
+    for (int j = 0; j < 3; ++j) {
+        if constexpr (W == 1)
+            *reinterpret_cast<uint16_t *>(p + j * plane) = (uint16_t)w[0][j];
+        else
+            *reinterpret_cast<uint2 *>(p + j * plane) = make_uint2(w[0][j], w[1][j]);
+    }
+}
+
 // ------------------------------------------------------------------ 8-bit rows
 
 constexpr float kE4m3Max = 448.f;

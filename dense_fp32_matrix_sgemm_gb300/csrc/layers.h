@@ -62,6 +62,7 @@ struct F32Planes {    // planes of a stored rows x cols matrix
     int64_t rows, cols;
     bool kmajor;      // cols is the reduction
 };
+inline int64_t f32_plane_ld(int64_t cols) { return (cols + 63) / 64 * 64; }   // of a plane's rows
 size_t f32_planes_bytes(int64_t rows, int64_t cols);
 cudaError_t launch_f32_split(const F32Operand *x, int count, cudaStream_t s);   // one or two
 // D[row, col] = sum_k A(row, k) B(col, k) with the epilogue (float).
@@ -73,12 +74,13 @@ cudaError_t launch_linear_f32(const F32Planes &A, const F32Planes &B, int K, con
 cudaError_t launch_repack(const void *src, int64_t src_ld_bytes, int64_t rows, int64_t row_bytes,
                           int elem, void *dst, int64_t dst_ld_bytes, cudaStream_t s);
 
-// dZ = dY * act'(Z) (not written when dZ is null) and partial column sums of
-// dZ, `parts` rows of N floats (not formed when partial is null).
+// dZ = dY * act'(Z) (not written when dZ is null; f32 with plane > 0: as planes
+// that many elements apart, rows lddz elements apart) and partial column sums of dZ,
+// `parts` rows of N floats (not formed when partial is null).
 int grad_parts(int64_t M, int64_t N);
 cudaError_t launch_linear_dz(int type, const void *dY, int64_t lddy, const void *Z, int64_t ldz,
-                             int act, int M, int N, void *dZ, int64_t lddz, float *partial,
-                             cudaStream_t s);
+                             int act, int M, int N, void *dZ, int64_t lddz, int64_t plane,
+                             float *partial, cudaStream_t s);
 
 // out[c] = sum over `parts` rows of partial[part][c], added in a fixed order.
 cudaError_t launch_column_sum(int type, const float *partial, int parts, int64_t N, void *out,

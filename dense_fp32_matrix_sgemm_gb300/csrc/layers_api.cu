@@ -151,6 +151,7 @@ size_t linear_bytes(int dtype, int64_t M, int64_t N, int64_t K, const void *X, i
 // Layout of sgemm_linear_backward's workspace.
 struct BackwardPlan {
     bool dz;                 // dZ is written (else dY is dZ)
+    bool planes;             // f32: dZ is written as planes only, by the pass that forms it
     int64_t lddz;
     int parts;
     size_t dz_bytes, part_bytes, x_bytes, w_bytes, g_bytes;   // g: planes of dZ (f32)
@@ -165,7 +166,8 @@ BackwardPlan backward_plan(int dtype, int64_t M, int64_t N, int64_t K, const voi
     const bool f32 = dtype == SGEMM_F32;
     const bool dx_rows = on_cuda_cores(dtype, M, K, N, !transW);   // dX: any alignment
     const bool tc = (dx && !dx_rows) || dw;      // a tensor-core product reads dZ
-    p.dz = (dx || dw) && K > 0 &&
+    p.planes = f32 && K > 0 && tc && !(dx && dx_rows) && (act != SGEMM_ACT_NONE || db);
+    p.dz = !p.planes && (dx || dw) && K > 0 &&
            (act != SGEMM_ACT_NONE || (!f32 && tc && !tma_ok(dY, lddy, size)));
     p.lddz = padded_ld(N, size);
     if (p.dz) p.dz_bytes = round256((size_t)M * p.lddz * size);
@@ -285,9 +287,11 @@ int linear_backward(int dtype, int64_t M, int64_t N, int64_t K, const void *dY, 
     ws += p.dz_bytes;
     float *partial = dbias ? reinterpret_cast<float *>(ws) : nullptr;
     ws += p.part_bytes;
-    if (p.dz || dbias)
-        e = launch_linear_dz(dtype, dY, lddy, Z, ldz, activation, (int)M, (int)N, dZ, p.lddz,
-                             partial, s);
+    char *const wsx = ws, *const wsw = wsx + p.x_bytes, *const wsg = wsw + p.w_bytes;   // f32
+    if (p.dz || p.planes || dbias)
+        e = launch_linear_dz(dtype, dY, lddy, Z, ldz, activation, (int)M, (int)N,
+                             p.planes ? wsg : dZ, p.planes ? f32_plane_ld(N) : p.lddz,
+                             p.planes ? M * f32_plane_ld(N) : 0, partial, s);
     if (dbias && e == cudaSuccess) e = launch_column_sum(dtype, partial, p.parts, N, db, s);
     if (e != cudaSuccess) return launched(e);
     const void *g = p.dz ? dZ : dY;
@@ -299,17 +303,15 @@ int linear_backward(int dtype, int64_t M, int64_t N, int64_t K, const void *dY, 
                                plain_epi(dtype, dX, lddx, M, K), s);
     if (e != cudaSuccess) return launched(e);
     if (dtype == SGEMM_F32) {
-        // planes of dZ (for both products), X and W
-        char *const wsx = ws, *const wsw = wsx + p.x_bytes, *const wsg = wsw + p.w_bytes;
-        const F32Operand G = {static_cast<const float *>(g), ldg, M, N, wsg};
-        const F32Operand in[3] = {G, {static_cast<const float *>(X), ldx, M, K, wsx},
-                                  {static_cast<const float *>(W), ldw, wrows, wcols, wsw}};
+        // planes of dZ (for both products), X and W, two matrices a launch
         const bool tdx = dx && !dx_rows;
-        if (dw) e = launch_f32_split(in, 2, s);
-        if (tdx && e == cudaSuccess) {
-            const F32Operand one[2] = {in[2], G};
-            e = launch_f32_split(one, dw ? 1 : 2, s);
-        }
+        F32Operand in[3];
+        int count = 0;
+        if (dw) in[count++] = {static_cast<const float *>(X), ldx, M, K, wsx};
+        if (tdx) in[count++] = {static_cast<const float *>(W), ldw, wrows, wcols, wsw};
+        if (!p.planes && (tdx || dw)) in[count++] = {static_cast<const float *>(g), ldg, M, N, wsg};
+        for (int i = 0; i < count && e == cudaSuccess; i += 2)
+            e = launch_f32_split(in + i, count - i < 2 ? count - i : 2, s);
         if (tdx && e == cudaSuccess)
             e = launch_linear_f32({wsg, M, N, true}, {wsw, wrows, wcols, transW == 0}, (int)N,
                                   plain_epi(dtype, dX, lddx, M, K), s);

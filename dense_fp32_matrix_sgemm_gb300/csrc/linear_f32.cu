@@ -10,15 +10,26 @@
 // operand is transposed, forward or backward.
 //   split3_kernel writes the three planes of both operands in the orientation
 //     they are stored in (HBM-bound: 4 bytes read, 6 written an element);
-//   linear_f32_kernel is linear_tc_kernel's pipeline on them: a stage holds 64
-//     of K of the six tiles, and its 24 MMAs use each tile two or four times.
+//   linear_f32_kernel is linear_tc_kernel's pipeline on them: a stage is 64 of
+//     K of the six tiles, and its 24 MMAs use each tile two or four times.
+// The ring's slots hold one plane of both operands each, not a whole stage, and
+// the MMAs go through the planes in the order a1 b1, a1 b0, a0 b1, a2 b0, a0 b2,
+// a0 b0: the first ones run when two thirds of a stage have landed, and a single
+// CTA gives plane 1's slot back half-way through (4096^3 in 128-wide tiles: 547
+// -> 523 us; 512 x 4096 x 4096 113 -> 95).  Pairs give all three back at the end,
+// as every commit there goes to both CTAs (464 us; one a plane as it is done
+// 482, whole stages 473).
 // The tensor cores add into their accumulator with a rounding towards zero, so
 // a long sum there would collect errors of one sign.  Here an accumulator
 // takes one stage: the five small terms first, while it is small, then a0 b0
 // (four updates at full size), and the epilogue warps add it to running sums in
-// registers with ordinary fp32 adds while the other accumulator fills.
-// Relative error against 64 bits, 2049 x
-// 3071 x 1537: 8e-8 (FP32 FMAs 4.2e-7).
+// registers with ordinary fp32 adds while the other accumulators fill.
+// Relative error against 64 bits, 2049 x 3071 x 1537: 8e-8 (FP32 FMAs 4.2e-7).
+// 4096^3 runs at 1.77 PFLOP/s of bf16 products, what a long bf16 product runs at
+// under the power limit.  A 128-wide tile of one CTA is bound by shared memory:
+// 24 MMAs read 8 KB each and the copies write 96 KB, 2250 clocks at 128 bytes
+// a clock, against 1536 of MMAs (256 x 128 tiles of pairs, which read less,
+// were no faster: 2049 x 3071 x 1537 104 against 102).
 #include <cstdint>
 
 #include <cuda.h>
@@ -38,17 +49,17 @@ struct Shape {
     static constexpr int BROWS = BN / CTAS;
     static constexpr int A_TILE = BM * kRowBytes;
     static constexpr int B_TILE = BROWS * kRowBytes;
-    static constexpr int STAGE = kPlanes * (A_TILE + B_TILE);
+    static constexpr int PLANE = A_TILE + B_TILE;   // one plane of both operands
     static constexpr int STAGING = SPLIT ? 0 : kEpiWarps * kStage;
-    static constexpr int STAGES = (kSmem - 1024 - 256 - STAGING) / STAGE;
-    static constexpr int SLOTS = 2;   // accumulators, one stage's sum each
+    static constexpr int RING = (kSmem - 1024 - 256 - STAGING) / PLANE;   // planes it holds
+    static constexpr int SLOTS = BN == 256 ? 2 : 4;   // accumulators, one stage's sum each
     static constexpr int TMEM_COLS = SLOTS * BN;
-    static constexpr int BARS = 2 * STAGES + 2 * SLOTS + 1;
-    static constexpr int SMEM = STAGES * STAGE + STAGING + 1024 + 256;
-    static_assert(STAGES >= 2, "a stage loads while another is multiplied");
+    static constexpr int BARS = 2 * RING + 2 * SLOTS + 1;
+    static constexpr int SMEM = RING * PLANE + STAGING + 1024 + 256;
+    static_assert(RING >= 2 * kPlanes, "a stage loads while another is multiplied");
     static_assert(TMEM_COLS <= 512, "tensor memory");
     static_assert(BARS * 8 + 8 <= 256, "barrier area");
-    static_assert(!SPLIT || BM * BN * 4 <= STAGES * STAGE, "a part of a tile fits the ring");
+    static_assert(!SPLIT || BM * BN * 4 <= RING * PLANE, "a part of a tile fits the ring");
 };
 
 struct Params {
@@ -131,16 +142,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 linear_f32_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                   const __grid_constant__ CUtensorMap tmY, const __grid_constant__ Params p) {
     using S = Shape<CTAS, BN, SPLIT>;
-    constexpr int STAGES = S::STAGES, SLOTS = S::SLOTS, COLS = BN / 2;
+    constexpr int RING = S::RING, SLOTS = S::SLOTS, COLS = BN / 2;
     constexpr bool CLUSTER = CTAS == 2 || SPLIT;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw_addr = tc::smem_u32_generic(smem_raw);
     uint8_t *smem = smem_raw + ((1024 - (raw_addr & 1023)) & 1023);
     const uint32_t ring = tc::smem_u32_generic(smem);
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + STAGES * S::STAGE + S::STAGING);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + RING * S::PLANE + S::STAGING);
     const uint32_t full0 = tc::smem_u32_generic(bars);
-    const uint32_t empty0 = full0 + 8 * STAGES;
-    const uint32_t accf0 = empty0 + 8 * STAGES;   // accumulator b holds a finished stage
+    const uint32_t empty0 = full0 + 8 * RING;
+    const uint32_t accf0 = empty0 + 8 * RING;   // accumulator b holds a finished stage
     const uint32_t acce0 = accf0 + 8 * SLOTS;     // accumulator b has been drained
     const uint32_t done_bar = acce0 + 8 * SLOTS;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + S::BARS);
@@ -166,7 +177,7 @@ linear_f32_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
     const int nk = kb1 - kb0;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < STAGES; ++s) {
+        for (int s = 0; s < RING; ++s) {
             tc::mbar_init(full0 + 8 * s, 1);
             tc::mbar_init(empty0 + 8 * s, 1);
         }
@@ -195,45 +206,44 @@ linear_f32_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
 
     if (warp == 0) {
         if (tc::elect_one()) {
-            // ---------------- TMA producer
-            const uint32_t tx = (uint32_t)(CTAS * kPlanes * (p.a_bytes + S::B_TILE));
+            // ---------------- TMA producer: a stage's planes in the issuer's order
+            const uint32_t tx = (uint32_t)(CTAS * (p.a_bytes + S::B_TILE));
             const uint32_t fulls = CTAS == 2 ? cluster_addr(full0, leader) : full0;
-            tc::Ring<STAGES> r;
+            tc::Ring<RING> r;
             bool stop = false;
             for (int i = 0; i < ntiles && !stop; ++i) {
                 int tm, tn;
                 raster(p.tiles_m, p.tiles_n, p.group_m, p.tile0 + first + i * stride, tm, tn);
                 const int m0 = (tm * CTAS + half) * BM, n0 = tn * BN + half * S::BROWS;
-                for (int kb = kb0; kb < kb1; ++kb) {
-                    if (r.used == STAGES &&
-                        !tc::wait(empty0 + 8 * r.s, r.parity ^ 1, abort_flag)) {
-                        stop = true;
-                        break;
-                    }
-                    const uint32_t fb = fulls + 8 * r.s;
+                for (int kb = kb0; kb < kb1 && !stop; ++kb) {
                     const int k0 = kb * kBk;
-                    if (half == 0) tc::mbar_arrive_expect_tx(full0 + 8 * r.s, tx);
+                    constexpr int order[kPlanes] = {1, 0, 2};
 #pragma unroll
-                    for (int pl = 0; pl < kPlanes; ++pl) {
-                        const uint32_t a = ring + r.s * S::STAGE + pl * S::A_TILE;
-                        const uint32_t b = ring + r.s * S::STAGE + kPlanes * S::A_TILE +
-                                           pl * S::B_TILE;
+                    for (int j = 0; j < kPlanes; ++j) {
+                        if (r.used == RING &&
+                            !tc::wait(empty0 + 8 * r.s, r.parity ^ 1, abort_flag)) {
+                            stop = true;
+                            break;
+                        }
+                        const uint32_t fb = fulls + 8 * r.s;
+                        const uint32_t a = ring + r.s * S::PLANE, b = a + S::A_TILE;
+                        if (half == 0) tc::mbar_arrive_expect_tx(full0 + 8 * r.s, tx);
                         if (p.a_kmajor) {
-                            tma_load3<CTAS>(a, &tmA, fb, k0, m0, pl);
+                            tma_load3<CTAS>(a, &tmA, fb, k0, m0, order[j]);
                         } else {
 #pragma unroll
                             for (int c = 0; c < BM / 64; ++c)
-                                tma_load3<CTAS>(a + c * kBox, &tmA, fb, m0 + 64 * c, k0, pl);
+                                tma_load3<CTAS>(a + c * kBox, &tmA, fb, m0 + 64 * c, k0, order[j]);
                         }
                         if (p.b_kmajor) {
-                            tma_load3<CTAS>(b, &tmB, fb, k0, n0, pl);
+                            tma_load3<CTAS>(b, &tmB, fb, k0, n0, order[j]);
                         } else {
 #pragma unroll
                             for (int c = 0; c < S::BROWS / 64; ++c)
-                                tma_load3<CTAS>(b + c * kBox, &tmB, fb, n0 + 64 * c, k0, pl);
+                                tma_load3<CTAS>(b + c * kBox, &tmB, fb, n0 + 64 * c, k0, order[j]);
                         }
+                        r.next();
                     }
-                    r.next();
                 }
             }
             // the copies of both CTAs, before the pair leaves
@@ -243,37 +253,53 @@ linear_f32_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
         if (half == 0 && tc::elect_one()) {
             // ---------------- MMA issuer, for the whole pair
             const uint64_t astep = p.a_kmajor ? 2 : 128, bstep = p.b_kmajor ? 2 : 128;
-            tc::Ring<STAGES> r;
+            tc::Ring<RING> r;
             tc::Ring<SLOTS> q;
             bool stop = false;
+            // the next plane of the ring: its slot, once it has landed
+            auto take = [&](int &slot) {
+                if (!tc::wait(full0 + 8 * r.s, r.parity, abort_flag)) return false;
+                slot = r.s;
+                r.next();
+                tc::fence_after_sync();
+                return true;
+            };
             for (int i = 0; i < ntiles && !stop; ++i) {
                 for (int kb = 0; kb < nk; ++kb) {
-                    if ((q.used == SLOTS &&
-                         !tc::wait(acce0 + 8 * q.s, q.parity ^ 1, abort_flag)) ||
-                        !tc::wait(full0 + 8 * r.s, r.parity, abort_flag)) {
-                        stop = true;
-                        break;
-                    }
-                    tc::fence_after_sync();
                     const uint32_t acc = tmem + (uint32_t)(q.s * BN);
-                    const uint32_t st = ring + r.s * S::STAGE;
-                    // the smallest terms first, a0 b0 last
-                    constexpr int ta[6] = {2, 0, 1, 1, 0, 0}, tb[6] = {0, 2, 1, 0, 1, 0};
-#pragma unroll
-                    for (int t = 0; t < 6; ++t) {
-                        const uint32_t a = st + ta[t] * S::A_TILE;
-                        const uint32_t b = st + kPlanes * S::A_TILE + tb[t] * S::B_TILE;
+                    // A of one slot by B of another
+                    auto term = [&](int sa, int sb, bool fresh) {
+                        const uint32_t a = ring + sa * S::PLANE, b = ring + sb * S::PLANE + S::A_TILE;
                         const uint64_t ad = p.a_kmajor ? tc::kmajor_desc<128>(a) : mnmajor_desc(a);
                         const uint64_t bd = p.b_kmajor ? tc::kmajor_desc<128>(b) : mnmajor_desc(b);
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
                             mma<CTAS, false>(acc, ad + kk * astep, bd + kk * bstep, p.idesc,
-                                             (t | kk) ? 1u : 0u);
+                                             fresh && kk == 0 ? 0u : 1u);
+                    };
+                    int s0, s1, s2;   // slots of the planes
+                    stop = true;
+                    if ((q.used == SLOTS && !tc::wait(acce0 + 8 * q.s, q.parity ^ 1, abort_flag)) ||
+                        !take(s1))
+                        break;
+                    term(s1, s1, true);
+                    if (!take(s0)) break;
+                    term(s1, s0, false);
+                    term(s0, s1, false);
+                    if constexpr (CTAS == 1) commit<1>(empty0 + 8 * s1, mask);
+                    if (!take(s2)) break;
+                    term(s2, s0, false);
+                    term(s0, s2, false);
+                    if constexpr (CTAS == 1) commit<1>(empty0 + 8 * s2, mask);
+                    term(s0, s0, false);
+                    if constexpr (CTAS == 2) {
+                        commit<2>(empty0 + 8 * s1, mask);
+                        commit<2>(empty0 + 8 * s2, mask);
                     }
-                    commit<CTAS>(empty0 + 8 * r.s, mask);
+                    commit<CTAS>(empty0 + 8 * s0, mask);
                     commit<CTAS>(accf0 + 8 * q.s, mask);
-                    r.next();
                     q.next();
+                    stop = false;
                 }
             }
             commit<CTAS>(done_bar, mask);   // tracks every MMA issued above, also on abort
@@ -281,10 +307,14 @@ linear_f32_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
     } else {
         // ---------------- epilogue: this CTA's rows, half of the columns a warp
         const int q = warp & 3, side = (warp - 2) >> 2;
-        const uint32_t stage = ring + STAGES * S::STAGE + (uint32_t)((warp - 2) * kStage);
+        const uint32_t stage = ring + RING * S::PLANE + (uint32_t)((warp - 2) * kStage);
         tc::Ring<SLOTS> slot;
         bool stop = false;
         for (int i = 0; i < ntiles && !stop; ++i) {
+            int tm, tn;
+            raster(p.tiles_m, p.tiles_n, p.group_m, p.tile0 + first + i * stride, tm, tn);
+            const int row0 = (tm * CTAS + half) * BM + 32 * q, n0 = tn * BN + side * COLS;
+            prefetch_residual<float>(p.epi, row0 + lane, n0, COLS);
             float run[COLS];
 #pragma unroll
             for (int j = 0; j < COLS; ++j) run[j] = 0.f;
@@ -317,9 +347,6 @@ linear_f32_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                 slot.next();
             }
             if (stop) break;
-            int tm, tn;
-            raster(p.tiles_m, p.tiles_n, p.group_m, p.tile0 + first + i * stride, tm, tn);
-            const int row0 = (tm * CTAS + half) * BM + 32 * q, n0 = tn * BN + side * COLS;
             if (row0 >= p.epi.M) continue;
             if constexpr (SPLIT) {
                 // the sums to this CTA's shared memory, over the ring (every MMA
@@ -351,7 +378,9 @@ linear_f32_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                                          run[32 * c + 4 * j], run[32 * c + 4 * j + 1],
                                          run[32 * c + 4 * j + 2], run[32 * c + 4 * j + 3]);
                     __syncwarp();
-                    finish_staged<float>(p.epi, stage, lane, row0, rows, n0 + 32 * c + lane);
+                    // (a pair's running sums leave registers for eight rows)
+                    finish_staged<float, BN == 256 ? 8 : 16>(p.epi, stage, lane, row0, rows,
+                                                             n0 + 32 * c + lane);
                 }
             }
             __syncwarp();
@@ -399,17 +428,6 @@ struct SplitJob {
 struct SplitArgs {
     SplitJob job[2];
 };
-
-// Two values as the three planes' pairs.
-__device__ __forceinline__ void split_pair(float x, float y, uint32_t (&w)[3]) {
-    const float x0 = __uint_as_float(__float_as_uint(x) & 0xffff0000u);
-    const float y0 = __uint_as_float(__float_as_uint(y) & 0xffff0000u);
-    const float rx = x - x0, ry = y - y0;   // exact
-    w[0] = (__float_as_uint(x) >> 16) | (__float_as_uint(y) & 0xffff0000u);
-    w[1] = pack2<__nv_bfloat16>(rx, ry);
-    const float2 m = unpack2<__nv_bfloat16>(w[1]);
-    w[2] = pack2<__nv_bfloat16>(rx - m.x, ry - m.y);
-}
 
 // CTAs [0, job[0].blocks) take the first operand, the rest the second.  A warp
 // takes pieces of a row (512 columns with 16-byte accesses, 8 columns a lane
@@ -486,15 +504,13 @@ __global__ void __launch_bounds__(256) split3_kernel(const SplitArgs a) {
 
 // ------------------------------------------------------------------ host side
 
-int64_t plane_ld(int64_t cols) { return (cols + 63) / 64 * 64; }
-
-// Planes as [3][rows][cols], rows plane_ld(cols) apart: boxes as linear_tc's
+// Planes as [3][rows][cols], rows f32_plane_ld(cols) apart: boxes as linear_tc's
 // operands, one plane a load.  The maps end at the operand's own sizes, so the
 // rows past K of an MN-major plane are zeros and not the next plane's.
 bool plane_map(CUtensorMap *map, const void *base, int64_t rows, int64_t cols, int box_rows) {
     auto fn = tensor_map_encoder();
     if (!fn) return false;
-    const int64_t ld = plane_ld(cols);
+    const int64_t ld = f32_plane_ld(cols);
     const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, kPlanes};
     const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)(rows * ld * 2)};
     const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
@@ -550,7 +566,7 @@ cudaError_t launch(const F32Planes &A, const F32Planes &B, int K, const LayerEpi
 }  // namespace ltc
 
 size_t f32_planes_bytes(int64_t rows, int64_t cols) {
-    return ((size_t)ltc::f32::kPlanes * rows * ltc::f32::plane_ld(cols) * 2 + 255) / 256 * 256;
+    return ((size_t)ltc::f32::kPlanes * rows * f32_plane_ld(cols) * 2 + 255) / 256 * 256;
 }
 
 // Planes of one or two matrices, one launch; `out` at 256-byte boundaries.
@@ -563,7 +579,7 @@ cudaError_t launch_f32_split(const F32Operand *x, int count, cudaStream_t s) {
         j.X = x[i].X;
         j.out = static_cast<__nv_bfloat16 *>(x[i].planes);
         j.ld = x[i].ld;
-        j.ldp = plane_ld(x[i].cols);
+        j.ldp = f32_plane_ld(x[i].cols);
         j.rows = x[i].rows;
         j.cols = (int)x[i].cols;
         j.vec = x[i].cols % 8 == 0 && x[i].ld % 4 == 0 &&
@@ -586,30 +602,21 @@ cudaError_t launch_f32_split(const F32Operand *x, int count, cudaStream_t s) {
 }
 
 // The tile and schedule by cost, as linear_tc's; a stage (64 of K, 24 MMAs) takes
-// 0.78, 1.05 and 1.75 us, a pair's launch 9 (4096^3: 474 us with the last 28 of
-// 256 tiles in 2 parts, 514 without, 557 with 128-wide tiles; 2049 x 3071 x 1537
-// 107 128-wide, 119 with pairs).
+// 1.72 us by pairs and 0.78 and 1.05 in 64- and 128-wide tiles, a pair's launch 9
+// (4096^3: 464 us with the last 28 of 256 tiles in 2 parts, 504 without, 523 with
+// 128-wide tiles; 2049 x 3071 x 1537 102 128-wide, 115 with pairs).
 cudaError_t launch_linear_f32(const F32Planes &A, const F32Planes &B, int K, const LayerEpi &epi,
                               cudaStream_t s) {
     using namespace ltc;
-    constexpr Costs costs = {{0.78, 1.05, 1.75}, {6.0, 9.0}, {1.5, 3.0, 5.0}};
+    constexpr Costs costs = {{1.72, 0.78, 1.05}, {5.0, 1.5, 3.0}, {6.0, 9.0}};
     Capacity cap;
     cudaError_t e = capacity(cap);
     if (e != cudaSuccess) return e;
     const Plan plan = plan_tiles(epi.M, epi.N, (K + f32::kBk - 1) / f32::kBk, cap, costs);
-    for (int i = 0; i < plan.pieces && e == cudaSuccess; ++i) {
-        const Piece &p = plan.piece[i];
-        if (plan.ctas == 2)
-            e = p.parts > 1 ? f32::launch<2, 256, true>(A, B, K, epi, p, s)
-                            : f32::launch<2, 256, false>(A, B, K, epi, p, s);
-        else if (plan.bn == 128)
-            e = p.parts > 1 ? f32::launch<1, 128, true>(A, B, K, epi, p, s)
-                            : f32::launch<1, 128, false>(A, B, K, epi, p, s);
-        else
-            e = p.parts > 1 ? f32::launch<1, 64, true>(A, B, K, epi, p, s)
-                            : f32::launch<1, 64, false>(A, B, K, epi, p, s);
-    }
-    return e;
+    return run_plan(plan, [&](auto w, auto split, const Piece &p) {
+        constexpr TileShape t = kShape[w()];
+        return f32::launch<t.ctas, t.bn, split()>(A, B, K, epi, p, s);
+    });
 }
 
 }  // namespace sgemm

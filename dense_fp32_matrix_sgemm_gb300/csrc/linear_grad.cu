@@ -21,15 +21,20 @@ struct DzArgs {
     void *dZ;
     float *partial;
     int64_t lddy, ldz, lddz;
+    int64_t plane;   // f32: dZ is three bf16 planes this many elements apart; 0: dZ itself
     int M, N, act, rows_per_part;
 };
 
 // CTA (x, y): columns [32 W x, ...) of rows [y rows_per_part, ...).  Lane l of
 // a warp holds W consecutive columns, warp r the rows r, r + 8, ...; the
 // columns' sums stay in registers over the rows, the eight warps' sums are
-// added through shared memory in warp order.
+// added through shared memory in warp order.  f32 dZ that only the tensor-core
+// products read is written as their planes (6 bytes an element instead of 4
+// written, 4 read and 6 written).  Four CTAs an SM, which the grid counts on
+// (without the bound 2 or 3 fit: 4096 x 8192 bf16 with the column sums 37.3 us,
+// so 33.8: 201 MB, 6.0 TB/s).
 template <class T, int W>
-__global__ void __launch_bounds__(kThreads) dz_kernel(const DzArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) dz_kernel(const DzArgs a) {
     __shared__ float red[kRowLanes][32 * W];
     pdl_trigger();
     pdl_wait();
@@ -44,7 +49,7 @@ __global__ void __launch_bounds__(kThreads) dz_kernel(const DzArgs a) {
         const T *dy = static_cast<const T *>(a.dY) + c;
         const T *z = static_cast<const T *>(a.Z) + c;
         T *dz = static_cast<T *>(a.dZ) + c;
-        constexpr int U = 4;   // rows in flight
+        constexpr int U = W == 8 ? 3 : 4;   // rows in flight (W = 8: with four, 64 registers spill)
         for (int r = r0 + ty; r < r1; r += U * kRowLanes) {
             Raw<T, W> vy[U], vz[U];
 #pragma unroll
@@ -69,6 +74,13 @@ __global__ void __launch_bounds__(kThreads) dz_kernel(const DzArgs a) {
                 }
 #pragma unroll
                 for (int j = 0; j < W; ++j) sum[j] += g[j];
+                if constexpr (sizeof(T) == 4) {
+                    if (a.plane != 0) {
+                        put_planes<W>(static_cast<__nv_bfloat16 *>(a.dZ) + row * a.lddz + c, a.plane,
+                                      g);
+                        continue;
+                    }
+                }
                 if (a.dZ != nullptr) put<T, W>(dz + row * a.lddz, g);
             }
         }
@@ -168,14 +180,15 @@ int grad_parts(int64_t M, int64_t N) {
 }
 
 cudaError_t launch_linear_dz(int type, const void *dY, int64_t lddy, const void *Z, int64_t ldz,
-                             int act, int M, int N, void *dZ, int64_t lddz, float *partial,
-                             cudaStream_t s) {
+                             int act, int M, int N, void *dZ, int64_t lddz, int64_t plane,
+                             float *partial, cudaStream_t s) {
     const int size = dtype_size(type), w = 16 / size;
     const bool vec = N % w == 0 && grad::aligned16(dY, lddy, size) &&
                      (act == SGEMM_ACT_NONE || grad::aligned16(Z, ldz, size)) &&
-                     grad::aligned16(dZ, lddz, size);
+                     (plane != 0 || grad::aligned16(dZ, lddz, size));
     const int parts = grad_parts(M, N);
-    const grad::DzArgs a = {dY, Z, dZ, partial, lddy, ldz, lddz, M, N, act, (M + parts - 1) / parts};
+    const grad::DzArgs a = {dY,   Z,     dZ, partial, lddy, ldz,
+                            lddz, plane, M,  N,       act,  (M + parts - 1) / parts};
     if (type == SGEMM_F32) return grad::dz_types<float>(a, vec, parts, s);
     if (type == SGEMM_BF16) return grad::dz_types<__nv_bfloat16>(a, vec, parts, s);
     return grad::dz_types<__half>(a, vec, parts, s);

@@ -3,9 +3,11 @@
 //
 //   D[row, col] = sum_k A(row, k) B(col, k)
 //
-// tcgen05.mma bounds it where all three sizes are large (2 M N K flops), the
-// bytes that L2 can bring to an SM (about 55 a clock) where the tiles are
-// small, HBM where few rows meet a large W.  A CTA has ten warps in three
+// tcgen05.mma bounds it where all three sizes are large (2 M N K flops: pairs
+// take 0.27 us a stage of K, what the MMAs alone take at the 1.88 GHz seen under
+// this load), the operands' way from L2 into shared memory (50 to 70 bytes a
+// clock and SM measured with 64- and 128-wide tiles) where the tiles are small,
+// HBM where few rows meet a large W.  A CTA has ten warps in three
 // roles:
 //   warp 0:    TMA producer: 128 bytes of K of A's and B's rows a stage,
 //              128-byte swizzle, a ring that runs on across tiles;
@@ -140,7 +142,7 @@ __device__ __forceinline__ void finish_rows(const Params &p, const void *tmY, co
                 tc::st_shared_v4(stage + (uint32_t)lane * 128u + ((uint32_t)(j ^ (lane & 7)) << 4),
                                  v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
             __syncwarp();
-            finish_staged<O>(e, stage, lane, row0, rows, col + lane);
+            finish_staged<O, 8>(e, stage, lane, row0, rows, col + lane);
             continue;   // (the next block's __syncwarp keeps it from overwriting this one)
         }
         if (e.sx != nullptr) {
@@ -346,14 +348,15 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         const uint32_t stage = ring + STAGES * S::STAGE + (uint32_t)((warp - 2) * kStage);
         for (int i = 0; i < ntiles; ++i) {
             const int b = i % ACCS, u = i / ACCS;
+            int tm, tn;
+            raster(p.tiles_m, p.tiles_n, p.group_m, p.tile0 + first + i * stride, tm, tn);
+            const int m0 = (tm * CTAS + half) * BM, n0 = tn * BN + side * (BN / 2);
+            prefetch_residual<O>(p.epi, m0 + 32 * q + lane, n0, BN / 2);
             const bool ok = tc::wait(accf0 + 8 * b, u & 1, abort_flag);
             __syncwarp();
             // one warp-uniform decision: the TMEM loads are warp-collective
             if (!__all_sync(0xffffffffu, ok && !*abort_flag)) break;
             tc::fence_after_sync();
-            int tm, tn;
-            raster(p.tiles_m, p.tiles_n, p.group_m, p.tile0 + first + i * stride, tm, tn);
-            const int m0 = (tm * CTAS + half) * BM;
             const uint32_t acc = tmem + (uint32_t)(b * BN + side * (BN / 2));
             if constexpr (SPLIT) {
                 // the sums to this CTA's shared memory, over the ring: every
@@ -375,8 +378,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                     }
                 }
             } else {
-                finish_rows<BN / 2, O>(p, &tmY, &tmZ, acc, q, lane, m0, tn * BN + side * (BN / 2),
-                                       stage);
+                finish_rows<BN / 2, O>(p, &tmY, &tmZ, acc, q, lane, m0, n0, stage);
             }
             tc::fence_before_sync();   // the TMEM loads above precede the release
             __syncwarp();
@@ -512,7 +514,7 @@ cudaError_t capacity(Capacity &cap) {
 // 128-wide 19.7 (pairs 23.5, pairs in 2 parts 19.9), 1024 x 2048 x 8192 pairs in 2
 // 28.1 (pairs 40.3, 128-wide 34.8), 2048^3 pairs 15.7 (19.8), 1024^3 64-wide 6.8
 // (7.6; pairs 10.0).
-constexpr Costs kCosts = {{0.21, 0.21, 0.27}, {5.0, 6.5}, {1.5, 3.0, 5.0}};
+constexpr Costs kCosts = {{0.27, 0.21, 0.21}, {5.0, 1.5, 3.0}, {5.0, 6.5}};
 
 template <class O>
 cudaError_t dispatch(int type, const TcOperand &A, const TcOperand &B, int K, const LayerEpi &epi,
@@ -522,19 +524,10 @@ cudaError_t dispatch(int type, const TcOperand &A, const TcOperand &B, int K, co
     if (e != cudaSuccess) return e;
     const int bk = kRowBytes / dtype_size(type);
     const Plan plan = plan_tiles(epi.M, epi.N, (K + bk - 1) / bk, cap, kCosts);
-    for (int i = 0; i < plan.pieces && e == cudaSuccess; ++i) {
-        const Piece &p = plan.piece[i];
-        if (plan.ctas == 2)
-            e = p.parts > 1 ? launch<2, 256, O, true>(type, A, B, K, epi, p, s)
-                            : launch<2, 256, O, false>(type, A, B, K, epi, p, s);
-        else if (plan.bn == 128)
-            e = p.parts > 1 ? launch<1, 128, O, true>(type, A, B, K, epi, p, s)
-                            : launch<1, 128, O, false>(type, A, B, K, epi, p, s);
-        else
-            e = p.parts > 1 ? launch<1, 64, O, true>(type, A, B, K, epi, p, s)
-                            : launch<1, 64, O, false>(type, A, B, K, epi, p, s);
-    }
-    return e;
+    return run_plan(plan, [&](auto w, auto split, const Piece &p) {
+        constexpr TileShape t = kShape[w()];
+        return launch<t.ctas, t.bn, O, split()>(type, A, B, K, epi, p, s);
+    });
 }
 
 }  // namespace ltc

@@ -4,6 +4,7 @@
 #pragma once
 
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -148,28 +149,39 @@ __device__ __forceinline__ void raster(int tiles_m, int tiles_n, int group_m, in
     tn = r / rows;
 }
 
+// Brings a row's piece of the residual into L2 while the tile's product runs: the
+// epilogue waits for HBM otherwise, block after block (2049 x 3071 x 1537 f32 with
+// a residual: 115.7 us, 113.7 so; 8192^3 e4m3 312, 301).
+template <class O>
+__device__ __forceinline__ void prefetch_residual(const LayerEpi &e, int row, int col, int cols) {
+    if (e.R == nullptr || row >= e.M) return;
+    const O *r = static_cast<const O *>(e.R) + row * e.ldr;
+    for (int c = col; c < min(col + cols, e.N); c += 128 / (int)sizeof(O))
+        asm volatile("prefetch.global.L2 [%0];" :: "l"(r + c));
+}
+
 // The epilogue on the first `rows` rows (from row0 on) of a 32 x 32 fp32 block
 // that the warp has staged at `stage` (16-byte chunk j of row r at chunk
-// j ^ (r & 7) of its 128 bytes): a column a lane, eight rows at a time, so each
-// access is a whole row segment and eight residual loads are in flight (one row
+// j ^ (r & 7) of its 128 bytes): a column a lane, U rows (8, 16) at a time, so
+// each access is a whole row segment and U residual loads are in flight (one row
 // at a time, an f32 layer of 2049 x 3071 outputs with a residual took 100 us
-// more than without).
-template <class O>
+// more than without; with eight in flight 114, with sixteen 106).
+template <class O, int U>
 __device__ __forceinline__ void finish_staged(const LayerEpi &e, uint32_t stage, int lane, int row0,
                                               int rows, int col) {
     if (col >= e.N) return;
     ColumnTerms<O, 1> t;
     t.load(e, col);
 #pragma unroll 1
-    for (int r = 0; r < rows; r += 8) {
-        float x[8];
+    for (int r = 0; r < rows; r += U) {
+        float x[U];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < U; ++i)
             asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x[i])
                          : "r"(stage + (uint32_t)(r + i) * 128u +
-                               ((uint32_t)((lane >> 2) ^ i) << 4) + (uint32_t)((lane & 3) * 4))
+                               ((uint32_t)((lane >> 2) ^ (i & 7)) << 4) + (uint32_t)((lane & 3) * 4))
                          : "memory");
-        finish_column<O, 8>(e, t, row0 + r, rows - r, col, x);
+        finish_column<O, U>(e, t, row0 + r, rows - r, col, x);
     }
 }
 
@@ -299,59 +311,84 @@ struct Piece {
     int tile0, tiles, parts, room;
 };
 
-// How a product is computed: tiles of ctas * 128 x bn, in one launch, or (pairs)
-// whole waves of tiles in one and the rest split in K in a second.
+// Tiles of ctas * 128 x bn that the kernels are built for.
+struct TileShape {
+    int ctas, bn;
+};
+constexpr int kShapes = 3;
+constexpr TileShape kShape[kShapes] = {{2, 256}, {1, 64}, {1, 128}};
+
+// How a product is computed: tiles of one shape, in one launch, or (pairs) whole
+// waves of tiles in one and the rest split in K in a second.
 struct Plan {
-    int ctas = 0, bn = 0, pieces = 0;
+    TileShape shape = {};
+    int pieces = 0;
     Piece piece[2];
     double us = 1e30;
 };
 
-// Microseconds: `stage` a stage of K of a tile by its width (64, 128, a pair's
-// 256), `fixed` a launch of single CTAs and of pairs, `join` for the parts of a
-// split tile of 128 rows by width, next to 1 us a split launch.
+// Microseconds, by shape: `stage` a stage of K of a tile, `join` for the parts of
+// a split tile of 128 rows (next to 1 us a split launch); `fixed` a launch of
+// single CTAs and of pairs.
 struct Costs {
-    double stage[3], fixed[2], join[3];
+    double stage[kShapes], join[kShapes], fixed[2];
 };
 
 inline Plan plan_tiles(int M, int N, int kblocks, const Capacity &cap, const Costs &cost) {
     Plan best;
     const double rows = (M < BM ? M : BM) / (double)BM;
     // one split launch of `tiles` tiles; negative where it cannot run at once
-    auto split = [&](int ctas, int w, long long tiles, int parts) {
+    auto split = [&](int w, long long tiles, int parts) {
+        const int ctas = kShape[w].ctas;
         if (tiles > cap.of(ctas * parts) || kblocks < 2 * parts) return -1.0;
         return ((kblocks + parts - 1) / parts) * cost.stage[w] + cost.fixed[ctas - 1] + 1.0 +
                cost.join[w] * rows;
     };
-    auto take = [&](double us, int ctas, int bn, Piece a, Piece b, int pieces) {
+    auto take = [&](double us, int w, Piece a, Piece b, int pieces) {
         if (us >= best.us) return;
         best.us = us;
-        best.ctas = ctas;
-        best.bn = bn;
+        best.shape = kShape[w];
         best.piece[0] = a;
         best.piece[1] = b;
         best.pieces = pieces;
     };
-    const int widths[3] = {64, 128, 256}, order[3] = {2, 0, 1};
-    for (int w : order) {
-        const int ctas = w == 2 ? 2 : 1, bn = widths[w];
+    for (int w = 0; w < kShapes; ++w) {
+        const int ctas = kShape[w].ctas, bn = kShape[w].bn;
         const long long all = (long long)((M + ctas * BM - 1) / (ctas * BM)) * ((N + bn - 1) / bn);
         if (all > 0x7fffffff) continue;
         const int tiles = (int)all, room = cap.of(ctas);
         const long long waves = tiles / room;
         const int tail = (int)(tiles - waves * room);
-        take((double)(waves + (tail > 0)) * kblocks * cost.stage[w] + cost.fixed[ctas - 1], ctas, bn,
+        take((double)(waves + (tail > 0)) * kblocks * cost.stage[w] + cost.fixed[ctas - 1], w,
              {0, tiles, 1, room}, {}, 1);
         for (int parts = 2; parts <= (ctas == 2 ? 4 : 8); parts *= 2) {
-            const double whole = split(ctas, w, tiles, parts);
-            if (whole > 0) take(whole, ctas, bn, {0, tiles, parts, 0}, {}, 1);
-            const double rest = ctas == 2 && waves > 0 && tail > 0 ? split(2, w, tail, parts) : -1;
+            const double whole = split(w, tiles, parts);
+            if (whole > 0) take(whole, w, {0, tiles, parts, 0}, {}, 1);
+            const double rest = ctas == 2 && waves > 0 && tail > 0 ? split(w, tail, parts) : -1;
             if (rest > 0)
-                take((double)waves * kblocks * cost.stage[w] + cost.fixed[1] + rest, ctas, bn,
+                take((double)waves * kblocks * cost.stage[w] + cost.fixed[1] + rest, w,
                      {0, tiles - tail, 1, room}, {tiles - tail, tail, parts, 0}, 2);
         }
     }
     return best;
+}
+
+// launch(shape constant, split constant, piece) for every piece of the plan.
+template <class F>
+cudaError_t run_plan(const Plan &plan, F &&launch) {
+    using Yes = std::true_type;
+    using No = std::false_type;
+    cudaError_t e = cudaSuccess;
+    for (int i = 0; i < plan.pieces && e == cudaSuccess; ++i) {
+        const Piece &p = plan.piece[i];
+        auto shaped = [&](auto w) {
+            return p.parts > 1 ? launch(w, Yes(), p) : launch(w, No(), p);
+        };
+        e = plan.shape.bn == 256  ? shaped(std::integral_constant<int, 0>())
+            : plan.shape.bn == 64 ? shaped(std::integral_constant<int, 1>())
+                                  : shaped(std::integral_constant<int, 2>());
+    }
+    return e;
 }
 
 }  // namespace ltc
