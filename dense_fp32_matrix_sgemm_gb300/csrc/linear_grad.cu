@@ -111,8 +111,17 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const float *partial, 
     const int64_t c = (int64_t)blockIdx.x * 32 + lane;
     float v = 0.f;
     if (c < N) {
-#pragma unroll 4
-        for (int p = ty; p < parts; p += 32) v += partial[p * N + c];
+        constexpr int U = 10;   // rows in flight; up to 320 parts in one go
+        for (int p0 = ty; p0 < parts; p0 += 32 * U) {
+            float x[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int p = p0 + 32 * u;
+                x[u] = p < parts ? partial[p * N + c] : 0.f;
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) v += x[u];
+        }
     }
     red[ty][lane] = v;
     __syncthreads();

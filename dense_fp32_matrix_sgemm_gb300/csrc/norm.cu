@@ -315,8 +315,8 @@ __global__ void __launch_bounds__(MAXT) grad_kernel(const GradArgs a) {
     }
     if (a.partial == nullptr) return;
     // one row of partial sums a CTA: its groups' sums are added in their order
-    // (groups share a CTA only up to 256 threads)
-    __shared__ float sums[256 * NV * W];
+    // (groups share a CTA only up to 512 threads)
+    __shared__ float sums[512 * NV * W];
     const int width = blockDim.x * NV * W;
     if (blockDim.y > 1) {
 #pragma unroll
@@ -460,6 +460,7 @@ GradShape grad_shape(int type, int64_t rows, int64_t D, bool vec) {
         g.nv = 0;
         g.sh = {kMaxThreads, 1};
     }
+    if (g.sh.tpr <= 256) g.sh.groups = 512 / g.sh.tpr;
     const int64_t need = (rows + g.sh.groups - 1) / g.sh.groups;
     // up to 128 registers a thread: 512 threads an SM, the row of each group and
     // its next one in flight

@@ -176,6 +176,18 @@ def test_linear_strides_and_offsets(m, pad, offset, t):
         run_linear(m, 345, 201, t, "none", pad=pad, offset=offset, w_kn=True)
 
 
+# long sums: pairs' tiles with K split over two pairs, and whole waves of pairs'
+# tiles followed by a second launch that splits the rest
+@pytest.mark.parametrize("m,n,k,t", [(1024, 2048, 8192, "f32"), (1000, 2050, 8200, "bf16"),
+                                     (1024, 2048, 8192, "f16"), (1020, 2040, 16400, "e4m3"),
+                                     (2560, 2560, 2600, "f32"), (2500, 2540, 8008, "bf16"),
+                                     (2560, 2560, 16000, "e4m3")])
+def test_linear_long_sums(m, n, k, t):
+    run_linear(m, n, k, t, "gelu", bias=True, residual=True, preact=True)
+    if t != "e4m3":
+        run_linear(m, n, k, t, "relu", bias=True, residual=True, w_kn=True)
+
+
 def test_linear_e4m3_to_f16():
     run_linear(2, 96, 256, "e4m3", "silu", bias=True, out_dtype=torch.float16)
     run_linear(200, 500, 256, "e4m3", "silu", bias=True, residual=True, out_dtype=torch.float16)
@@ -328,6 +340,25 @@ def test_linear_backward_parts():
     assert torch.equal(a[0], dx) and a[1] is None and a[2] is None
     assert torch.equal(b[1], dw) and b[0] is None
     assert torch.equal(c[2], db) and c[1] is None
+
+
+@pytest.mark.parametrize("t", ["f32", "f16"])
+@pytest.mark.parametrize("name", ["none", "silu"])
+@pytest.mark.parametrize("m,n,k", [(9, 77, 130), (96, 64, 80), (301, 259, 130)])
+def test_linear_backward_parts_give_the_same_bits(m, n, k, name, t):
+    # what dZ is written as, and by which pass, follows from what is asked for
+    g = gen(23)
+    dy, x, w, z = (normal(g, *s, dtype=TYPES[t]) for s in ((m, n), (m, k), (n, k), (m, n)))
+    z = z if name != "none" else None
+    full = sg.linear_backward(dy, x, w, z, activation=name)
+    for need in range(1, 8):
+        some = sg.linear_backward(dy, x, w, z, activation=name, need_dx=bool(need & 1),
+                                  need_dw=bool(need & 2), need_db=bool(need & 4))
+        for i in range(3):
+            if need >> i & 1:
+                assert torch.equal(some[i], full[i]), (need, i)
+            else:
+                assert some[i] is None
 
 
 @pytest.mark.parametrize("t", ["f32", "bf16"])
