@@ -100,6 +100,11 @@ __device__ __forceinline__ void put(T *p, const float (&f)[W]) {
     }
 }
 
+// Asks for the 128-byte line of p in L2.
+__device__ __forceinline__ void prefetch_l2(const void *p) {
+    asm volatile("prefetch.global.L2 [%0];" :: "l"(p));
+}
+
 // N consecutive elements as one access of N * sizeof(T) bytes (4, 8 or 16),
 // aligned to its size.
 template <class T, int N>

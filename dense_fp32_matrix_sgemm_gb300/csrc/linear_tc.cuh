@@ -157,7 +157,7 @@ __device__ __forceinline__ void prefetch_residual(const LayerEpi &e, int row, in
     if (e.R == nullptr || row >= e.M) return;
     const O *r = static_cast<const O *>(e.R) + row * e.ldr;
     for (int c = col; c < min(col + cols, e.N); c += 128 / (int)sizeof(O))
-        asm volatile("prefetch.global.L2 [%0];" :: "l"(r + c));
+        prefetch_l2(r + c);
 }
 
 // The epilogue on the first `rows` rows (from row0 on) of a 32 x 32 fp32 block

@@ -254,6 +254,10 @@ __global__ void __launch_bounds__(MAXT) grad_kernel(const GradArgs a) {
     constexpr bool AHEAD = MAXT <= 512;
     Raw<T, W> ny[NV], ns[NV], nd[NV];
     float nr = 0.f;
+    auto load_ds = [&](int64_t row, int c) {
+        return load_or_zero<T, W>(static_cast<const T *>(a.dS) + row * a.ldds + c,
+                                  row < a.rows && c < a.D && a.dS != nullptr);
+    };
     auto load_row = [&](int64_t row) {
         const bool live = row < a.rows;
 #pragma unroll
@@ -262,22 +266,39 @@ __global__ void __launch_bounds__(MAXT) grad_kernel(const GradArgs a) {
             const bool in = live && c < a.D;
             ny[i] = load_or_zero<T, W>(static_cast<const T *>(a.dY) + row * a.lddy + c, in);
             ns[i] = load_or_zero<T, W>(static_cast<const T *>(a.S) + row * a.lds + c, in);
-            nd[i] = load_or_zero<T, W>(static_cast<const T *>(a.dS) + row * a.ldds + c,
-                                       in && a.dS != nullptr);
+            if (AHEAD) nd[i] = load_ds(row, c);
         }
         nr = live ? a.rstd[row] : 0.f;
+    };
+    // where they do not, the next row is brought to L2 in the meantime, a lane a
+    // 128-byte line (2048 x 16384 bf16: 88 -> 73 us), and dS is read only when dX is
+    // formed, which leaves fewer registers to spill (70)
+    auto prefetch_row = [&](int64_t row) {
+        constexpr int LANES = W > 1 ? 128 / (W * (int)sizeof(T)) : 32;
+        if (row >= a.rows || threadIdx.x % LANES != 0) return;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * blockDim.x + threadIdx.x) * W;
+            if (c >= a.D) continue;
+            prefetch_l2(static_cast<const T *>(a.dY) + row * a.lddy + c);
+            prefetch_l2(static_cast<const T *>(a.S) + row * a.lds + c);
+            if (a.dS != nullptr) prefetch_l2(static_cast<const T *>(a.dS) + row * a.ldds + c);
+        }
     };
     if (AHEAD && turns > 0) load_row(group);
     for (int t = 0; t < turns; ++t) {
         const int64_t row = group + t * groups;
         const bool live = row < a.rows;
-        if (!AHEAD) load_row(row);
+        if (!AHEAD) {
+            load_row(row);
+            if (t + 1 < turns) prefetch_row(row + groups);
+        }
         Raw<T, W> vy[NV], vs[NV], vd[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             vy[i] = ny[i];
             vs[i] = ns[i];
-            vd[i] = nd[i];
+            if (AHEAD) vd[i] = nd[i];
         }
         const float rstd = nr;
         if (AHEAD && t + 1 < turns) load_row(row + groups);
@@ -306,7 +327,7 @@ __global__ void __launch_bounds__(MAXT) grad_kernel(const GradArgs a) {
             vy[i].get(dy);
             vs[i].get(s);
             vw[i].get(w);
-            vd[i].get(ds);
+            (AHEAD ? vd[i] : load_ds(row, c)).get(ds);
 #pragma unroll
             for (int j = 0; j < W; ++j)
                 dx[j] = fmaf(rstd, fmaf(-k, s[j], dy[j] * w[j]), ds[j]);
@@ -460,7 +481,10 @@ GradShape grad_shape(int type, int64_t rows, int64_t D, bool vec) {
         g.nv = 0;
         g.sh = {kMaxThreads, 1};
     }
-    if (g.sh.tpr <= 256) g.sh.groups = 512 / g.sh.tpr;
+    // one CTA of 512 threads an SM has half the partial sums to write and add of two
+    // of 256 (8192 x 4096 bf16: 48.8 -> 47.1 us); its groups wait for one another
+    // (4096 x 1024: 7.9 -> 8.3), so only where each takes eight turns or more
+    if (g.sh.tpr <= 256 && rows >= 152 * 8 * (512 / g.sh.tpr)) g.sh.groups = 512 / g.sh.tpr;
     const int64_t need = (rows + g.sh.groups - 1) / g.sh.groups;
     // up to 128 registers a thread: 512 threads an SM, the row of each group and
     // its next one in flight
