@@ -608,13 +608,14 @@ cudaError_t launch_f32_split(const F32Operand *x, int count, cudaStream_t s) {
 cudaError_t launch_linear_f32(const F32Planes &A, const F32Planes &B, int K, const LayerEpi &epi,
                               cudaStream_t s) {
     using namespace ltc;
-    constexpr Costs costs = {{1.72, 0.78, 1.05}, {5.0, 1.5, 3.0}, {6.0, 9.0}};
+    constexpr Costs costs = {{{2, 256}, {1, 64}, {1, 128}}, {1.72, 0.78, 1.05}, {9.0, 6.0, 6.0},
+                             {5.0, 1.5, 3.0}};
     Capacity cap;
     cudaError_t e = capacity(cap);
     if (e != cudaSuccess) return e;
     const Plan plan = plan_tiles(epi.M, epi.N, (K + f32::kBk - 1) / f32::kBk, cap, costs);
     return run_plan(plan, [&](auto w, auto split, const Piece &p) {
-        constexpr TileShape t = kShape[w()];
+        constexpr TileShape t = costs.shape[w()];
         return f32::launch<t.ctas, t.bn, split()>(A, B, K, epi, p, s);
     });
 }

@@ -3,16 +3,21 @@
 //
 //   D[row, col] = sum_k A(row, k) B(col, k)
 //
-// tcgen05.mma bounds it where all three sizes are large (2 M N K flops: pairs
-// take 0.27 us a stage of K, what the MMAs alone take at the 1.88 GHz seen under
-// this load), the operands' way from L2 into shared memory (50 to 70 bytes a
-// clock and SM measured with 64- and 128-wide tiles) where the tiles are small,
-// HBM where few rows meet a large W.  A CTA has ten warps in three
-// roles:
-//   warp 0:    TMA producer: 128 bytes of K of A's and B's rows a stage,
-//              128-byte swizzle, a ring that runs on across tiles;
+// tcgen05.mma bounds it where all three sizes are large (2 M N K flops: pairs'
+// 256 x 256 tiles take 0.27 us per 128 bytes of K, what the MMAs alone take at
+// the 1.88 GHz seen under this load), the operands' way from L2 into shared
+// memory where the tiles are small, HBM where few rows meet a large W.  A CTA
+// has ten warps in three roles:
+//   warp 0:    TMA producer: KS times 128 bytes of K of A's and B's rows a
+//              stage, 128-byte swizzle, a ring that runs on across tiles;
 //   warp 1:    MMA issuer (32 bytes of K an instruction); owns tensor memory;
 //   warps 2-9: epilogue: TMEM lane quarter warp % 4, half of the columns.
+// One thread issues each role's work, and handing a stage over costs it about
+// 100 clocks for the wait, 40 to 65 for the expected bytes, 65 a copy, 60 to 105
+// a commit: 330 clocks in the producer and as many in the issuer, whatever the
+// stage holds.  That is hidden by the 512 clocks of the 256 x 256 tiles' MMAs, not
+// by smaller tiles' 128 to 256, so their stages hold two times 128 bytes of K
+// (4096 x 8192 x 4096 in 64-wide tiles 417 -> 290 us, in 256 x 128 200 -> 170).
 // Operands may be K-major or (16-bit types) M/N-major in memory: the tensor
 // core's descriptors take both, so no operand is transposed.
 //   K-major:  box of 128 bytes of K x rows; 8-row groups 1024 bytes apart.
@@ -24,8 +29,10 @@
 //   so a CTA takes in 32 KB for 2 x 128 x 256 x 64 flops where a 128 x 256 tile
 //   of its own takes 48 and a 128 x 128 tile 64 for the same: at the tensor
 //   cores' rate 64 bytes a clock instead of 96 and 128.  (4096 x 8192 x 4096:
-//   140 us; 128 x 256 tiles of single CTAs were bound by their operands.)
-// CTAS = 1: 128 x BN tiles, for problems with few rows.
+//   140 us.)  Pairs' 256 x 128 tiles take 96 bytes a clock, where 128 x 128 tiles
+//   of single CTAs would take 128 (they were: 512 x 4096 x 4096 19.4 us, the
+//   pairs' 16.8).
+// CTAS = 1: 128 x 64 tiles, for problems with few rows or few tiles.
 // Two schedules:
 //   persistent: one CTA an SM walks tiles; two accumulators, so a tile's
 //     epilogue overlaps the next one's MMAs;
@@ -59,7 +66,9 @@ struct Shape {
     static constexpr int BROWS = BN / CTAS;   // of B in a CTA
     static constexpr int A_TILE = BM * kRowBytes;
     static constexpr int B_TILE = BROWS * kRowBytes;
-    static constexpr int STAGE = A_TILE + B_TILE;
+    static constexpr int KS = BN == 256 ? 1 : 2;   // kRowBytes of K in a stage
+    static constexpr int SUB = A_TILE + B_TILE;
+    static constexpr int STAGE = KS * SUB;
     static constexpr int STAGING = SPLIT ? 0 : kEpiWarps * kStage;   // epilogue warps' blocks
     static constexpr int STAGES = (kSmem - 1024 - 256 - STAGING) / STAGE;
     static constexpr int ACCS = SPLIT ? 1 : 2;
@@ -213,7 +222,8 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + S::BARS);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // (broadcast: the compiler then knows that a warp takes one role as a whole)
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int rank = CLUSTER ? (int)cluster_rank() : 0;
     const int half = CTAS == 2 ? rank & 1 : 0;      // this CTA's half of the pair's tile
     const int leader = CTAS == 2 ? rank & ~1 : rank;
@@ -275,27 +285,33 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                 int tm, tn;
                 raster(p.tiles_m, p.tiles_n, p.group_m, p.tile0 + first + i * stride, tm, tn);
                 const int m0 = (tm * CTAS + half) * BM, n0 = tn * BN + half * S::BROWS;
-                for (int kb = kb0; kb < kb1; ++kb) {
+                for (int kb = kb0; kb < kb1; kb += S::KS) {
                     if (r.used == STAGES && !tc::wait(empty0 + 8 * r.s, r.parity ^ 1, abort_flag)) {
                         stop = true;
                         break;
                     }
-                    const uint32_t st = ring + r.s * S::STAGE, fb = fulls + 8 * r.s;
-                    const int k0 = kb * bk;
-                    if (half == 0) tc::mbar_arrive_expect_tx(full0 + 8 * r.s, tx);
-                    if (p.a_kmajor) {
-                        tma_load<CTAS>(st, &tmA, fb, k0, m0);
-                    } else {
+                    const uint32_t fb = fulls + 8 * r.s;
+                    const int subs = min(S::KS, kb1 - kb);
+                    if (half == 0) tc::mbar_arrive_expect_tx(full0 + 8 * r.s, tx * subs);
 #pragma unroll
-                        for (int c = 0; c < BM / 64; ++c)
-                            tma_load<CTAS>(st + c * kBox, &tmA, fb, m0 + 64 * c, k0);
-                    }
-                    if (p.b_kmajor) {
-                        tma_load<CTAS>(st + S::A_TILE, &tmB, fb, k0, n0);
-                    } else {
+                    for (int j = 0; j < S::KS; ++j) {
+                        if (j >= subs) break;
+                        const uint32_t st = ring + r.s * S::STAGE + j * S::SUB;
+                        const int k0 = (kb + j) * bk;
+                        if (p.a_kmajor) {
+                            tma_load<CTAS>(st, &tmA, fb, k0, m0);
+                        } else {
 #pragma unroll
-                        for (int c = 0; c < S::BROWS / 64; ++c)
-                            tma_load<CTAS>(st + S::A_TILE + c * kBox, &tmB, fb, n0 + 64 * c, k0);
+                            for (int c = 0; c < BM / 64; ++c)
+                                tma_load<CTAS>(st + c * kBox, &tmA, fb, m0 + 64 * c, k0);
+                        }
+                        if (p.b_kmajor) {
+                            tma_load<CTAS>(st + S::A_TILE, &tmB, fb, k0, n0);
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < S::BROWS / 64; ++c)
+                                tma_load<CTAS>(st + S::A_TILE + c * kBox, &tmB, fb, n0 + 64 * c, k0);
+                        }
                     }
                     r.next();
                 }
@@ -314,29 +330,33 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                 if (i >= ACCS && !tc::wait(acce0 + 8 * b, (u - 1) & 1, abort_flag)) break;
                 tc::fence_after_sync();
                 const uint32_t acc = tmem + (uint32_t)(b * BN);
-                for (int kb = 0; kb < nk; ++kb) {
+                for (int kb = 0; kb < nk; kb += S::KS) {
                     if (!tc::wait(full0 + 8 * r.s, r.parity, abort_flag)) {
                         stop = true;
                         break;
                     }
                     tc::fence_after_sync();
-                    const uint32_t st = ring + r.s * S::STAGE;
-                    const uint64_t ad = p.a_kmajor ? tc::kmajor_desc<128>(st) : mnmajor_desc(st);
-                    const uint64_t bd = p.b_kmajor ? tc::kmajor_desc<128>(st + S::A_TILE)
-                                                   : mnmajor_desc(st + S::A_TILE);
-                    if (p.fp8) {
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            mma<CTAS, true>(acc, ad + kk * astep, bd + kk * bstep, p.idesc,
-                                            (kb | kk) ? 1u : 0u);
-                    } else {
+                    for (int j = 0; j < S::KS; ++j) {
+                        if (kb + j >= nk) break;
+                        const uint32_t st = ring + r.s * S::STAGE + j * S::SUB;
+                        const uint64_t ad = p.a_kmajor ? tc::kmajor_desc<128>(st) : mnmajor_desc(st);
+                        const uint64_t bd = p.b_kmajor ? tc::kmajor_desc<128>(st + S::A_TILE)
+                                                       : mnmajor_desc(st + S::A_TILE);
+                        if (p.fp8) {
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            mma<CTAS, false>(acc, ad + kk * astep, bd + kk * bstep, p.idesc,
-                                             (kb | kk) ? 1u : 0u);
+                            for (int kk = 0; kk < 4; ++kk)
+                                mma<CTAS, true>(acc, ad + kk * astep, bd + kk * bstep, p.idesc,
+                                                (kb | j | kk) ? 1u : 0u);
+                        } else {
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                mma<CTAS, false>(acc, ad + kk * astep, bd + kk * bstep, p.idesc,
+                                                 (kb | j | kk) ? 1u : 0u);
+                        }
                     }
                     commit<CTAS>(empty0 + 8 * r.s, mask);
-                    if (kb + 1 == nk) commit<CTAS>(accf0 + 8 * b, mask);
+                    if (kb + S::KS >= nk) commit<CTAS>(accf0 + 8 * b, mask);
                     r.next();
                 }
             }
@@ -481,14 +501,14 @@ cudaError_t launch(int type, const TcOperand &A, const TcOperand &B, int K, cons
 }
 
 cudaError_t capacity(Capacity &cap) {
-    using S = Shape<1, 128, true>;
+    using S = Shape<2, 256, true>;
     static PerContext<Capacity> cached;
     if (cached.get(current_context_id(), cap)) return cudaSuccess;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess)
         e = cudaDeviceGetAttribute(&cap.sms, cudaDevAttrMultiProcessorCount, dev);
-    auto kernel = linear_tc_kernel<1, 128, __nv_bfloat16, true>;
+    auto kernel = linear_tc_kernel<2, 256, __nv_bfloat16, true>;
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
     for (int i = 0; i < 3 && e == cudaSuccess; ++i) {
@@ -504,17 +524,20 @@ cudaError_t capacity(Capacity &cap) {
 }
 
 // The tile and schedule, by their cost in microseconds.  Measured on GB300
-// (graph of 20 calls, bf16, weights out of L2): a 64- or 128-wide tile of one
-// CTA takes about 0.21 us a stage of K, a 256 x 256 tile of a pair 0.27; what
-// does not depend on K is about 5 us a launch, 6.5 with pairs; joining the parts
-// of a split tile about 1 us and, for 128 rows, 3 more (5 for a pair's tile).
-// The choice against the others there, in us: 64 x 1024 x 4096 128-wide in 8
-// parts 7.5 (whole 18.1, in 4 9.1), 128 x 4096 x 4096 in 4 parts 12.5 (64-wide in
-// 2 13.8, whole 19.3), 256 x 4096 x 4096 in 2 15.7 (19.5), 512 x 4096 x 4096 whole
-// 128-wide 19.7 (pairs 23.5, pairs in 2 parts 19.9), 1024 x 2048 x 8192 pairs in 2
-// 28.1 (pairs 40.3, 128-wide 34.8), 2048^3 pairs 15.7 (19.8), 1024^3 64-wide 6.8
-// (7.6; pairs 10.0).
-constexpr Costs kCosts = {{0.27, 0.21, 0.21}, {5.0, 1.5, 3.0}, {5.0, 6.5}};
+// (graph of 20 calls, bf16, weights out of L2): 128 bytes of K of a pair's
+// 256-wide tile take 0.27 us, of its 128-wide tile 0.16 to 0.18, of a single CTA's
+// 64-wide tile 0.15 to 0.17; what does not depend on K is 6.5, 5.5 and 4.5 us a
+// launch; joining the parts of a split tile 1 us and, for 128 rows, 5, 3 and 1.5
+// more.  The choice against the others there, in us:
+//   64 x 1024 x 4096: 64-wide in 8 or 4 parts 7.5 (whole 12.4, pairs 13.4, 21.6);
+//   128 x 4096 x 4096: 64-wide in 2 12.0 (whole 14.4, 128-wide in 2 14.3);
+//   256 x 4096 x 4096: 64-wide 14.5 (128-wide in 2 14.7, whole 16.6);
+//   512 x 4096 x 4096: 128-wide 16.8 (256-wide 23.1, in 2 19.8, 64-wide 24.2);
+//   1024 x 2048 x 8192: 128-wide or 256-wide in 2 27.8 (256-wide 39.6);
+//   2048^3: 256-wide 15.1 (128-wide 16.1); 1024^3: 64-wide 5.8 (6.8, 9.5);
+//   4096 x 4096 x 8192: 256-wide, the last 28 of 256 tiles in 2 parts 151.9 (155.2).
+constexpr Costs kCosts = {{{2, 256}, {2, 128}, {1, 64}}, {0.27, 0.165, 0.15}, {6.5, 5.5, 4.5},
+                          {5.0, 3.0, 1.5}};
 
 template <class O>
 cudaError_t dispatch(int type, const TcOperand &A, const TcOperand &B, int K, const LayerEpi &epi,
@@ -525,7 +548,7 @@ cudaError_t dispatch(int type, const TcOperand &A, const TcOperand &B, int K, co
     const int bk = kRowBytes / dtype_size(type);
     const Plan plan = plan_tiles(epi.M, epi.N, (K + bk - 1) / bk, cap, kCosts);
     return run_plan(plan, [&](auto w, auto split, const Piece &p) {
-        constexpr TileShape t = kShape[w()];
+        constexpr TileShape t = kCosts.shape[w()];
         return launch<t.ctas, t.bn, O, split()>(type, A, B, K, epi, p, s);
     });
 }

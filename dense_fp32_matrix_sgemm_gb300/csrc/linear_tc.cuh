@@ -311,27 +311,27 @@ struct Piece {
     int tile0, tiles, parts, room;
 };
 
-// Tiles of ctas * 128 x bn that the kernels are built for.
+// Tiles of ctas * 128 x bn; a kernel is built for three shapes.
 struct TileShape {
     int ctas, bn;
 };
 constexpr int kShapes = 3;
-constexpr TileShape kShape[kShapes] = {{2, 256}, {1, 64}, {1, 128}};
 
 // How a product is computed: tiles of one shape, in one launch, or (pairs) whole
 // waves of tiles in one and the rest split in K in a second.
 struct Plan {
-    TileShape shape = {};
+    int shape = 0;
     int pieces = 0;
     Piece piece[2];
     double us = 1e30;
 };
 
-// Microseconds, by shape: `stage` a stage of K of a tile, `join` for the parts of
-// a split tile of 128 rows (next to 1 us a split launch); `fixed` a launch of
-// single CTAs and of pairs.
+// The shapes and, in microseconds, what 128 bytes (f32: 64) of K of a tile take,
+// what a launch takes besides, and the joining of the parts of a split tile of 128
+// rows (next to 1 us a split launch).
 struct Costs {
-    double stage[kShapes], join[kShapes], fixed[2];
+    TileShape shape[kShapes];
+    double stage[kShapes], fixed[kShapes], join[kShapes];
 };
 
 inline Plan plan_tiles(int M, int N, int kblocks, const Capacity &cap, const Costs &cost) {
@@ -339,41 +339,41 @@ inline Plan plan_tiles(int M, int N, int kblocks, const Capacity &cap, const Cos
     const double rows = (M < BM ? M : BM) / (double)BM;
     // one split launch of `tiles` tiles; negative where it cannot run at once
     auto split = [&](int w, long long tiles, int parts) {
-        const int ctas = kShape[w].ctas;
+        const int ctas = cost.shape[w].ctas;
         if (tiles > cap.of(ctas * parts) || kblocks < 2 * parts) return -1.0;
-        return ((kblocks + parts - 1) / parts) * cost.stage[w] + cost.fixed[ctas - 1] + 1.0 +
+        return ((kblocks + parts - 1) / parts) * cost.stage[w] + cost.fixed[w] + 1.0 +
                cost.join[w] * rows;
     };
     auto take = [&](double us, int w, Piece a, Piece b, int pieces) {
         if (us >= best.us) return;
         best.us = us;
-        best.shape = kShape[w];
+        best.shape = w;
         best.piece[0] = a;
         best.piece[1] = b;
         best.pieces = pieces;
     };
     for (int w = 0; w < kShapes; ++w) {
-        const int ctas = kShape[w].ctas, bn = kShape[w].bn;
+        const int ctas = cost.shape[w].ctas, bn = cost.shape[w].bn;
         const long long all = (long long)((M + ctas * BM - 1) / (ctas * BM)) * ((N + bn - 1) / bn);
         if (all > 0x7fffffff) continue;
         const int tiles = (int)all, room = cap.of(ctas);
         const long long waves = tiles / room;
         const int tail = (int)(tiles - waves * room);
-        take((double)(waves + (tail > 0)) * kblocks * cost.stage[w] + cost.fixed[ctas - 1], w,
+        take((double)(waves + (tail > 0)) * kblocks * cost.stage[w] + cost.fixed[w], w,
              {0, tiles, 1, room}, {}, 1);
         for (int parts = 2; parts <= (ctas == 2 ? 4 : 8); parts *= 2) {
             const double whole = split(w, tiles, parts);
             if (whole > 0) take(whole, w, {0, tiles, parts, 0}, {}, 1);
             const double rest = ctas == 2 && waves > 0 && tail > 0 ? split(w, tail, parts) : -1;
             if (rest > 0)
-                take((double)waves * kblocks * cost.stage[w] + cost.fixed[1] + rest, w,
+                take((double)waves * kblocks * cost.stage[w] + cost.fixed[w] + rest, w,
                      {0, tiles - tail, 1, room}, {tiles - tail, tail, parts, 0}, 2);
         }
     }
     return best;
 }
 
-// launch(shape constant, split constant, piece) for every piece of the plan.
+// launch(shape's index, split) as constants with the piece, for every piece of the plan.
 template <class F>
 cudaError_t run_plan(const Plan &plan, F &&launch) {
     using Yes = std::true_type;
@@ -384,9 +384,9 @@ cudaError_t run_plan(const Plan &plan, F &&launch) {
         auto shaped = [&](auto w) {
             return p.parts > 1 ? launch(w, Yes(), p) : launch(w, No(), p);
         };
-        e = plan.shape.bn == 256  ? shaped(std::integral_constant<int, 0>())
-            : plan.shape.bn == 64 ? shaped(std::integral_constant<int, 1>())
-                                  : shaped(std::integral_constant<int, 2>());
+        e = plan.shape == 0   ? shaped(std::integral_constant<int, 0>())
+            : plan.shape == 1 ? shaped(std::integral_constant<int, 1>())
+                              : shaped(std::integral_constant<int, 2>());
     }
     return e;
 }
