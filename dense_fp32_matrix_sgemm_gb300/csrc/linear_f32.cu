@@ -157,7 +157,7 @@ linear_f32_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + S::BARS);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int rank = CLUSTER ? (int)cluster_rank() : 0;
     const int half = CTAS == 2 ? rank & 1 : 0;
     const int leader = CTAS == 2 ? rank & ~1 : rank;
