@@ -7,12 +7,15 @@
 // the same, and FP32 FMAs (packed in pairs) keep up for the few rows that the
 // launcher sends here.
 //
+// Measured with weights out of L2: 4096 x 4096 bf16, one row 7.8 us (33.6 MB, 4.3
+// TB/s, launch included); 8192 x 4096 under a profiler DRAM runs at 52 %, so the
+// start of the loads and the launch, not their number, are what is left.
 // Weights stored N x K (dot form): a warp takes two or four output features and
 // walks K, each lane with 16-byte pieces of their rows of W and of the MR rows of
 // X (X stays in L1).  Where the features alone would not fill the SMs, K is
 // split over the warps of a CTA and their sums are added through shared
 // memory, in warp order.
-// Weights stored K x N (column form): a lane takes 16 bytes of consecutive
+// f32 weights stored K x N (column form): a lane takes 16 bytes of consecutive
 // features and walks k; K is split over the warps of a CTA and over a cluster
 // of CTAs, and the sums are added through shared and distributed shared
 // memory in rank order.
