@@ -8,6 +8,7 @@
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include "device_utils.cuh"
 #include "layers.h"
 
 namespace sgemm {
@@ -123,6 +124,24 @@ __device__ __forceinline__ void store_vec(T *p, const float (&x)[N]) {
 #pragma unroll
     for (int i = 0; i < N; ++i) r.v[i] = from_f32<T>(x[i]);
     *reinterpret_cast<Vec<T, N> *>(p) = r;
+}
+
+// ------------------------------------------------------------------ launches
+
+// Launches of one call that do not read one another's results (the pieces of a
+// plan, the gradients' two products, ...) form a chain, in which a later one fills the
+// SMs that the ones before it leave.  The first (kChainNext alone) waits for
+// earlier work as ever, and lets the next one start only after that wait: where
+// the next one runs, all earlier work is complete.  The others (kChainPrev) do not
+// wait at their start but before they end, so that each launch completes after the
+// ones before it and the work behind the last one waits for all of them.
+__device__ __forceinline__ void chain_begin(int chain) {
+    if (!(chain & kChainNext)) pdl_trigger();
+    if (!(chain & kChainPrev)) pdl_wait();
+    if (chain & kChainNext) pdl_trigger();
+}
+__device__ __forceinline__ void chain_end(int chain) {
+    if (chain & kChainPrev) pdl_wait();
 }
 
 // ------------------------------------------------------------------ activations

@@ -15,6 +15,11 @@ __host__ __device__ inline int dtype_size(int t) {
     return t == SGEMM_F32 ? 4 : t == SGEMM_E4M3 ? 1 : 2;
 }
 
+// Place of a launch among launches of a call that do not read one another's results:
+// after, before such a launch (chain_begin in layer_math.cuh), and with half of the
+// SMs for each of two products.
+enum { kChainPrev = 1, kChainNext = 2, kChainHalf = 4 };
+
 // What happens to an accumulator on its way to memory:
 //   z = acc * (sx ? sx[row] * sw[col] : 1) + bias[col];  Z = z
 //   Y = act(z) + R
@@ -39,11 +44,19 @@ struct TcOperand {
     bool kmajor;
 };
 
+// A product's sizes as launch_linear_tc and launch_linear_f32 take them.
+struct ProductSize {
+    int M, N, K;
+};
+// Whether two products of a chain are better run side by side than in turn.
+bool linear_tc_side_by_side(int in_type, const ProductSize &a, const ProductSize &b);
+bool linear_f32_side_by_side(const ProductSize &a, const ProductSize &b);
+
 // D[row, col] = sum_k A(row, k) B(col, k) with the epilogue, 16-bit operands
 // of one type (SGEMM_BF16, SGEMM_F16) or SGEMM_E4M3 (K-major only), every
 // operand's base and rows 16-byte aligned.  linear_tc.cu.
 cudaError_t launch_linear_tc(int in_type, const TcOperand &A, const TcOperand &B, int K,
-                             const LayerEpi &epi, cudaStream_t s);
+                             const LayerEpi &epi, int chain, cudaStream_t s);
 
 // The same product of few rows on the CUDA cores, one pass over W; any type
 // and alignment, transW == 1 for the types other than f32.  linear_rows.cu.
@@ -64,10 +77,10 @@ struct F32Planes {    // planes of a stored rows x cols matrix
 };
 inline int64_t f32_plane_ld(int64_t cols) { return (cols + 63) / 64 * 64; }   // of a plane's rows
 size_t f32_planes_bytes(int64_t rows, int64_t cols);
-cudaError_t launch_f32_split(const F32Operand *x, int count, cudaStream_t s);   // one or two
+cudaError_t launch_f32_split(const F32Operand *x, int count, int chain, cudaStream_t s);   // one or two
 // D[row, col] = sum_k A(row, k) B(col, k) with the epilogue (float).
 cudaError_t launch_linear_f32(const F32Planes &A, const F32Planes &B, int K, const LayerEpi &epi,
-                              cudaStream_t s);
+                              int chain, cudaStream_t s);
 
 // Rows of `bytes_per_row` bytes copied to rows `dst_ld` bytes apart (dst
 // 16-byte aligned rows; the gap after each row is not written).
@@ -80,11 +93,11 @@ cudaError_t launch_repack(const void *src, int64_t src_ld_bytes, int64_t rows, i
 int grad_parts(int64_t M, int64_t N);
 cudaError_t launch_linear_dz(int type, const void *dY, int64_t lddy, const void *Z, int64_t ldz,
                              int act, int M, int N, void *dZ, int64_t lddz, int64_t plane,
-                             float *partial, cudaStream_t s);
+                             float *partial, int chain, cudaStream_t s);
 
 // out[c] = sum over `parts` rows of partial[part][c], added in a fixed order.
 cudaError_t launch_column_sum(int type, const float *partial, int parts, int64_t N, void *out,
-                              cudaStream_t s);
+                              int chain, cudaStream_t s);
 
 // norm.cu
 cudaError_t launch_add_rmsnorm(int type, int64_t rows, int64_t D, const void *X, int64_t ldx,

@@ -230,16 +230,17 @@ int linear(int dtype, int64_t M, int64_t N, int64_t K, const void *X, int64_t ld
         char *const wsw = static_cast<char *>(workspace) + f32_planes_bytes(M, K);
         const F32Operand in[2] = {{static_cast<const float *>(X), ldx, M, K, workspace},
                                   {static_cast<const float *>(W), ldw, wr, wc, wsw}};
-        const cudaError_t split = launch_f32_split(in, 2, s);
+        const cudaError_t split = launch_f32_split(in, 2, 0, s);
         if (split != cudaSuccess) return launched(split);
         return launched(launch_linear_f32({workspace, M, K, true}, {wsw, wr, wc, transW != 0},
-                                          (int)K, epi, s));
+                                          (int)K, epi, 0, s));
     }
     char *ws = static_cast<char *>(workspace);
     cudaError_t e = place(X, ldx, M, K, size, ws, s);
     if (e == cudaSuccess) e = place(W, ldw, transW ? N : K, transW ? K : N, size, ws, s);
     if (e != cudaSuccess) return launched(e);
-    return launched(launch_linear_tc(dtype, {X, ldx, true}, {W, ldw, transW != 0}, (int)K, epi, s));
+    return launched(launch_linear_tc(dtype, {X, ldx, true}, {W, ldw, transW != 0}, (int)K, epi, 0,
+                                     s));
 }
 
 int linear_backward(int dtype, int64_t M, int64_t N, int64_t K, const void *dY, int64_t lddy,
@@ -288,53 +289,72 @@ int linear_backward(int dtype, int64_t M, int64_t N, int64_t K, const void *dY, 
     float *partial = dbias ? reinterpret_cast<float *>(ws) : nullptr;
     ws += p.part_bytes;
     char *const wsx = ws, *const wsw = wsx + p.x_bytes, *const wsg = wsw + p.w_bytes;   // f32
+    const bool dx_rows = on_cuda_cores(dtype, M, K, N, !transW);
+    const bool tdx = dx && !dx_rows;
+    // what does not wait for what: the planes of X and W for the pass over dZ, the
+    // two products and, behind a product, the bias gradient's last sum (500 x 777 x
+    // 1001 f32: 31.5 us with every launch after the one before it, 22.8 so; 512 x
+    // 1024 x 1024 bf16 14.3 and 11.9)
+    const int split_at = p.planes ? kChainPrev : 0;
+    const bool sum_last = tdx || dw;
     if (p.dz || p.planes || dbias)
         e = launch_linear_dz(dtype, dY, lddy, Z, ldz, activation, (int)M, (int)N,
                              p.planes ? wsg : dZ, p.planes ? f32_plane_ld(N) : p.lddz,
-                             p.planes ? M * f32_plane_ld(N) : 0, partial, s);
-    if (dbias && e == cudaSuccess) e = launch_column_sum(dtype, partial, p.parts, N, db, s);
+                             p.planes ? M * f32_plane_ld(N) : 0, partial,
+                             p.planes ? kChainNext : 0, s);
+    if (dbias && !sum_last && e == cudaSuccess)
+        e = launch_column_sum(dtype, partial, p.parts, N, db, 0, s);
     if (e != cudaSuccess) return launched(e);
     const void *g = p.dz ? dZ : dY;
     const int64_t ldg = p.dz ? p.lddz : lddy;
-    const bool dx_rows = on_cuda_cores(dtype, M, K, N, !transW);
     if (dx && dx_rows)
         // reduction over the output features: W's other orientation
         e = launch_linear_rows(dtype, g, ldg, W, ldw, !transW, (int)N,
                                plain_epi(dtype, dX, lddx, M, K), s);
     if (e != cudaSuccess) return launched(e);
+    int before = dw || dbias ? kChainNext : 0;
+    int after = (tdx ? kChainPrev : 0) | (dbias ? kChainNext : 0);
+    if (tdx && dw) {
+        const ProductSize a = {(int)M, (int)K, (int)N}, b = {(int)wrows, (int)wcols, (int)M};
+        if (dtype == SGEMM_F32 ? linear_f32_side_by_side(a, b)
+                               : linear_tc_side_by_side(dtype, a, b)) {
+            before |= kChainHalf;
+            after |= kChainHalf;
+        }
+    }
     if (dtype == SGEMM_F32) {
         // planes of dZ (for both products), X and W, two matrices a launch
-        const bool tdx = dx && !dx_rows;
         F32Operand in[3];
         int count = 0;
         if (dw) in[count++] = {static_cast<const float *>(X), ldx, M, K, wsx};
         if (tdx) in[count++] = {static_cast<const float *>(W), ldw, wrows, wcols, wsw};
         if (!p.planes && (tdx || dw)) in[count++] = {static_cast<const float *>(g), ldg, M, N, wsg};
         for (int i = 0; i < count && e == cudaSuccess; i += 2)
-            e = launch_f32_split(in + i, count - i < 2 ? count - i : 2, s);
+            e = launch_f32_split(in + i, count - i < 2 ? count - i : 2, split_at, s);
         if (tdx && e == cudaSuccess)
             e = launch_linear_f32({wsg, M, N, true}, {wsw, wrows, wcols, transW == 0}, (int)N,
-                                  plain_epi(dtype, dX, lddx, M, K), s);
+                                  plain_epi(dtype, dX, lddx, M, K), before, s);
         if (dw && e == cudaSuccess) {
             const F32Planes Gp = {wsg, M, N, false}, Xp = {wsx, M, K, false};
             e = launch_linear_f32(transW ? Gp : Xp, transW ? Xp : Gp, (int)M,
-                                  plain_epi(dtype, dW, lddw, wrows, wcols), s);
+                                  plain_epi(dtype, dW, lddw, wrows, wcols), after, s);
         }
+        if (dbias && sum_last && e == cudaSuccess)
+            e = launch_column_sum(dtype, partial, p.parts, N, db, kChainPrev, s);
         return launched(e);
     }
-    if (dx && !dx_rows) {
-        e = place(W, ldw, wrows, wcols, size, ws, s);
-        if (e == cudaSuccess)
-            e = launch_linear_tc(dtype, {g, ldg, true}, {W, ldw, transW == 0}, (int)N,
-                                 plain_epi(dtype, dX, lddx, M, K), s);
-    }
+    if (tdx) e = place(W, ldw, wrows, wcols, size, ws, s);
+    if (dw && e == cudaSuccess) e = place(X, ldx, M, K, size, ws, s);
+    if (tdx && e == cudaSuccess)
+        e = launch_linear_tc(dtype, {g, ldg, true}, {W, ldw, transW == 0}, (int)N,
+                             plain_epi(dtype, dX, lddx, M, K), before, s);
     if (dw && e == cudaSuccess) {
-        e = place(X, ldx, M, K, size, ws, s);
         const TcOperand G = {g, ldg, false}, Xo = {X, ldx, false};
-        if (e == cudaSuccess)
-            e = launch_linear_tc(dtype, transW ? G : Xo, transW ? Xo : G, (int)M,
-                                 plain_epi(dtype, dW, lddw, wrows, wcols), s);
+        e = launch_linear_tc(dtype, transW ? G : Xo, transW ? Xo : G, (int)M,
+                             plain_epi(dtype, dW, lddw, wrows, wcols), after, s);
     }
+    if (dbias && sum_last && e == cudaSuccess)
+        e = launch_column_sum(dtype, partial, p.parts, N, db, kChainPrev, s);
     return launched(e);
 }
 

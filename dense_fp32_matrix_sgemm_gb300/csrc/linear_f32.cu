@@ -67,6 +67,7 @@ struct Params {
     int kblocks;
     int tiles_m, tiles_n, group_m;
     int tile0, tiles;        // this launch's tiles: tile0 .. tile0 + tiles - 1
+    int chain;
     int a_kmajor, b_kmajor;
     int a_bytes;        // bytes one plane of A brings to a CTA's stage
     uint32_t idesc;
@@ -201,8 +202,7 @@ linear_f32_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
     if constexpr (CTAS == 2) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_slot;
-    pdl_trigger();
-    pdl_wait();   // nothing below touches global memory before the planes are complete
+    chain_begin(p.chain);   // nothing below touches global memory before the planes are complete
 
     if (warp == 0) {
         if (tc::elect_one()) {
@@ -414,6 +414,7 @@ linear_f32_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
     }
     if constexpr (CLUSTER) cluster_sync();   // the cluster leaves together
     if (warp == 1) tmem_dealloc<CTAS>(tmem, S::TMEM_COLS);
+    chain_end(p.chain);
 }
 
 // ------------------------------------------------------------------ split
@@ -427,6 +428,7 @@ struct SplitJob {
 };
 struct SplitArgs {
     SplitJob job[2];
+    int chain;
 };
 
 // CTAs [0, job[0].blocks) take the first operand, the rest the second.  A warp
@@ -434,8 +436,7 @@ struct SplitArgs {
 // each, else 256 columns, 2 a lane), every access of a piece in flight; from
 // piece to piece it steps without a division.
 __global__ void __launch_bounds__(256) split3_kernel(const SplitArgs a) {
-    pdl_trigger();
-    pdl_wait();
+    chain_begin(a.chain);
     const int which = (int)blockIdx.x < a.job[0].blocks ? 0 : 1;
     const SplitJob j = which ? a.job[1] : a.job[0];
     const int64_t warp = ((int64_t)blockIdx.x - (which ? a.job[0].blocks : 0)) * 8 +
@@ -500,6 +501,7 @@ __global__ void __launch_bounds__(256) split3_kernel(const SplitArgs a) {
             }
         }
     }
+    chain_end(a.chain);
 }
 
 // ------------------------------------------------------------------ host side
@@ -523,7 +525,7 @@ bool plane_map(CUtensorMap *map, const void *base, int64_t rows, int64_t cols, i
 
 template <int CTAS, int BN, bool SPLIT>
 cudaError_t launch(const F32Planes &A, const F32Planes &B, int K, const LayerEpi &epi,
-                   const Piece &piece, cudaStream_t s) {
+                   const Piece &piece, int chain, cudaStream_t s) {
     using S = Shape<CTAS, BN, SPLIT>;
     static PerContext<bool> configured;
     bool done = false;
@@ -554,6 +556,7 @@ cudaError_t launch(const F32Planes &A, const F32Planes &B, int K, const LayerEpi
     if (!plane_map(&tmA, A.planes, A.rows, A.cols, A.kmajor ? a_rows : 64) ||
         !plane_map(&tmB, B.planes, B.rows, B.cols, B.kmajor ? S::BROWS : 64))
         return cudaErrorInvalidValue;
+    p.chain = chain;
     p.tile0 = piece.tile0;
     p.tiles = piece.tiles;
     const long long most = piece.room < piece.tiles ? piece.room : piece.tiles;
@@ -570,9 +573,10 @@ size_t f32_planes_bytes(int64_t rows, int64_t cols) {
 }
 
 // Planes of one or two matrices, one launch; `out` at 256-byte boundaries.
-cudaError_t launch_f32_split(const F32Operand *x, int count, cudaStream_t s) {
+cudaError_t launch_f32_split(const F32Operand *x, int count, int chain, cudaStream_t s) {
     using namespace ltc::f32;
     SplitArgs a = {};
+    a.chain = chain;
     int blocks = 0;
     for (int i = 0; i < count; ++i) {
         SplitJob &j = a.job[i];
@@ -605,18 +609,26 @@ cudaError_t launch_f32_split(const F32Operand *x, int count, cudaStream_t s) {
 // 1.72 us by pairs and 0.78 and 1.05 in 64- and 128-wide tiles, a pair's launch 9
 // (4096^3: 464 us with the last 28 of 256 tiles in 2 parts, 504 without, 523 with
 // 128-wide tiles; 2049 x 3071 x 1537 102 128-wide, 115 with pairs).
+constexpr ltc::Costs kF32Costs = {{{2, 256}, {1, 64}, {1, 128}}, {1.72, 0.78, 1.05}, {9.0, 6.0, 6.0},
+                                  {5.0, 1.5, 3.0}};
+
+bool linear_f32_side_by_side(const ProductSize &a, const ProductSize &b) {
+    ltc::Capacity cap;
+    return ltc::capacity(cap) == cudaSuccess &&
+           ltc::side_by_side(a, b, ltc::f32::kBk, cap, kF32Costs);
+}
+
 cudaError_t launch_linear_f32(const F32Planes &A, const F32Planes &B, int K, const LayerEpi &epi,
-                              cudaStream_t s) {
+                              int chain, cudaStream_t s) {
     using namespace ltc;
-    constexpr Costs costs = {{{2, 256}, {1, 64}, {1, 128}}, {1.72, 0.78, 1.05}, {9.0, 6.0, 6.0},
-                             {5.0, 1.5, 3.0}};
     Capacity cap;
     cudaError_t e = capacity(cap);
     if (e != cudaSuccess) return e;
-    const Plan plan = plan_tiles(epi.M, epi.N, (K + f32::kBk - 1) / f32::kBk, cap, costs);
-    return run_plan(plan, [&](auto w, auto split, const Piece &p) {
-        constexpr TileShape t = costs.shape[w()];
-        return f32::launch<t.ctas, t.bn, split()>(A, B, K, epi, p, s);
+    if (chain & kChainHalf) cap = cap.half();
+    const Plan plan = plan_tiles(epi.M, epi.N, (K + f32::kBk - 1) / f32::kBk, cap, kF32Costs);
+    return run_plan(plan, chain, [&](auto w, auto split, const Piece &p, int at) {
+        constexpr TileShape t = kF32Costs.shape[w()];
+        return f32::launch<t.ctas, t.bn, split()>(A, B, K, epi, p, at, s);
     });
 }
 

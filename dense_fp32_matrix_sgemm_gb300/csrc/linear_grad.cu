@@ -23,6 +23,7 @@ struct DzArgs {
     int64_t lddy, ldz, lddz;
     int64_t plane;   // f32: dZ is three bf16 planes this many elements apart; 0: dZ itself
     int M, N, act, rows_per_part;
+    int chain;
 };
 
 // CTA (x, y): columns [32 W x, ...) of rows [y rows_per_part, ...).  Lane l of
@@ -36,8 +37,7 @@ struct DzArgs {
 template <class T, int W>
 __global__ void __launch_bounds__(kThreads, 4) dz_kernel(const DzArgs a) {
     __shared__ float red[kRowLanes][32 * W];
-    pdl_trigger();
-    pdl_wait();
+    chain_begin(a.chain);
     const int lane = threadIdx.x & 31, ty = threadIdx.x >> 5;
     const int c = (int)(blockIdx.x * 32 + lane) * W;
     const int r0 = (int)blockIdx.y * a.rows_per_part;
@@ -103,10 +103,9 @@ __global__ void __launch_bounds__(kThreads, 4) dz_kernel(const DzArgs a) {
 // partial sums, then the 32 sums are added in order.
 template <class T>
 __global__ void __launch_bounds__(1024) column_sum_kernel(const float *partial, int parts,
-                                                          int64_t N, T *out) {
+                                                          int64_t N, T *out, int chain) {
     __shared__ float red[32][33];
-    pdl_trigger();
-    pdl_wait();
+    chain_begin(chain);
     const int lane = threadIdx.x & 31, ty = threadIdx.x >> 5;
     const int64_t c = (int64_t)blockIdx.x * 32 + lane;
     float v = 0.f;
@@ -131,6 +130,7 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const float *partial, 
         for (int r = 0; r < 32; ++r) s += red[r][lane];
         out[c] = from_f32<T>(s);
     }
+    chain_end(chain);
 }
 
 // Row copy in words of U bytes (the largest that source and rows allow).
@@ -190,30 +190,30 @@ int grad_parts(int64_t M, int64_t N) {
 
 cudaError_t launch_linear_dz(int type, const void *dY, int64_t lddy, const void *Z, int64_t ldz,
                              int act, int M, int N, void *dZ, int64_t lddz, int64_t plane,
-                             float *partial, cudaStream_t s) {
+                             float *partial, int chain, cudaStream_t s) {
     const int size = dtype_size(type), w = 16 / size;
     const bool vec = N % w == 0 && grad::aligned16(dY, lddy, size) &&
                      (act == SGEMM_ACT_NONE || grad::aligned16(Z, ldz, size)) &&
                      (plane != 0 || grad::aligned16(dZ, lddz, size));
     const int parts = grad_parts(M, N);
     const grad::DzArgs a = {dY,   Z,     dZ, partial, lddy, ldz,
-                            lddz, plane, M,  N,       act,  (M + parts - 1) / parts};
+                            lddz, plane, M,  N,       act,  (M + parts - 1) / parts, chain};
     if (type == SGEMM_F32) return grad::dz_types<float>(a, vec, parts, s);
     if (type == SGEMM_BF16) return grad::dz_types<__nv_bfloat16>(a, vec, parts, s);
     return grad::dz_types<__half>(a, vec, parts, s);
 }
 
 cudaError_t launch_column_sum(int type, const float *partial, int parts, int64_t N, void *out,
-                              cudaStream_t s) {
+                              int chain, cudaStream_t s) {
     const dim3 grid((unsigned)((N + 31) / 32));
     if (type == SGEMM_F32)
         return grad::launch(grad::column_sum_kernel<float>, grid, 1024, s, partial, parts, N,
-                            static_cast<float *>(out));
+                            static_cast<float *>(out), chain);
     if (type == SGEMM_BF16)
         return grad::launch(grad::column_sum_kernel<__nv_bfloat16>, grid, 1024, s, partial, parts,
-                            N, static_cast<__nv_bfloat16 *>(out));
+                            N, static_cast<__nv_bfloat16 *>(out), chain);
     return grad::launch(grad::column_sum_kernel<__half>, grid, 1024, s, partial, parts, N,
-                        static_cast<__half *>(out));
+                        static_cast<__half *>(out), chain);
 }
 
 cudaError_t launch_repack(const void *src, int64_t src_ld_bytes, int64_t rows, int64_t row_bytes,

@@ -85,6 +85,7 @@ struct Params {
     int kblocks;             // K in stages
     int tiles_m, tiles_n, group_m;
     int tile0, tiles;        // this launch's tiles: tile0 .. tile0 + tiles - 1
+    int chain;
     int a_kmajor, b_kmajor;
     int a_bytes;             // bytes A's boxes bring to a CTA's stage
     uint32_t idesc;
@@ -270,8 +271,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     if constexpr (CTAS == 2) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_slot;
-    pdl_trigger();
-    pdl_wait();   // nothing below touches global memory before earlier work has finished
+    chain_begin(p.chain);   // nothing below touches global memory before earlier work has finished
 
     if (warp == 0) {
         if (tc::elect_one()) {
@@ -439,6 +439,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     }
     if constexpr (CLUSTER) cluster_sync();   // the cluster leaves together
     if (warp == 1) tmem_dealloc<CTAS>(tmem, S::TMEM_COLS);
+    chain_end(p.chain);
 }
 
 // ------------------------------------------------------------------ host side
@@ -454,7 +455,7 @@ bool operand_map(CUtensorMap *map, const TcOperand &o, int type, int rows, int K
 
 template <int CTAS, int BN, class O, bool SPLIT>
 cudaError_t launch(int type, const TcOperand &A, const TcOperand &B, int K, const LayerEpi &epi,
-                   const Piece &piece, cudaStream_t s) {
+                   const Piece &piece, int chain, cudaStream_t s) {
     using S = Shape<CTAS, BN, SPLIT>;
     static PerContext<bool> configured;
     bool done = false;
@@ -492,6 +493,7 @@ cudaError_t launch(int type, const TcOperand &A, const TcOperand &B, int K, cons
     };
     p.tma = !SPLIT && epi.vec == 16 && out_map(&tmY, epi.Y, epi.ldy) &&
             (epi.Z == nullptr || out_map(&tmZ, epi.Z, epi.ldz));
+    p.chain = chain;
     p.tile0 = piece.tile0;
     p.tiles = piece.tiles;
     const long long most = piece.room < piece.tiles ? piece.room : piece.tiles;
@@ -541,24 +543,31 @@ constexpr Costs kCosts = {{{2, 256}, {2, 128}, {1, 64}}, {0.27, 0.165, 0.15}, {6
 
 template <class O>
 cudaError_t dispatch(int type, const TcOperand &A, const TcOperand &B, int K, const LayerEpi &epi,
-                     cudaStream_t s) {
+                     int chain, cudaStream_t s) {
     Capacity cap;
     cudaError_t e = capacity(cap);
     if (e != cudaSuccess) return e;
     const int bk = kRowBytes / dtype_size(type);
+    if (chain & kChainHalf) cap = cap.half();
     const Plan plan = plan_tiles(epi.M, epi.N, (K + bk - 1) / bk, cap, kCosts);
-    return run_plan(plan, [&](auto w, auto split, const Piece &p) {
+    return run_plan(plan, chain, [&](auto w, auto split, const Piece &p, int at) {
         constexpr TileShape t = kCosts.shape[w()];
-        return launch<t.ctas, t.bn, O, split()>(type, A, B, K, epi, p, s);
+        return launch<t.ctas, t.bn, O, split()>(type, A, B, K, epi, p, at, s);
     });
 }
 
 }  // namespace ltc
 
+bool linear_tc_side_by_side(int in_type, const ProductSize &a, const ProductSize &b) {
+    ltc::Capacity cap;
+    return ltc::capacity(cap) == cudaSuccess &&
+           ltc::side_by_side(a, b, ltc::kRowBytes / dtype_size(in_type), cap, ltc::kCosts);
+}
+
 cudaError_t launch_linear_tc(int in_type, const TcOperand &A, const TcOperand &B, int K,
-                             const LayerEpi &epi, cudaStream_t s) {
-    return epi.type == SGEMM_BF16 ? ltc::dispatch<__nv_bfloat16>(in_type, A, B, K, epi, s)
-                                  : ltc::dispatch<__half>(in_type, A, B, K, epi, s);
+                             const LayerEpi &epi, int chain, cudaStream_t s) {
+    return epi.type == SGEMM_BF16 ? ltc::dispatch<__nv_bfloat16>(in_type, A, B, K, epi, chain, s)
+                                  : ltc::dispatch<__half>(in_type, A, B, K, epi, chain, s);
 }
 
 }  // namespace sgemm

@@ -302,6 +302,7 @@ struct Config {
 struct Capacity {
     int sms, clusters[3];
     int of(int size) const { return size == 1 ? sms : clusters[size == 2 ? 0 : size == 4 ? 1 : 2]; }
+    Capacity half() const { return {sms / 2, {clusters[0] / 2, clusters[1] / 2, clusters[2] / 2}}; }
 };
 cudaError_t capacity(Capacity &cap);   // linear_tc.cu
 
@@ -373,16 +374,34 @@ inline Plan plan_tiles(int M, int N, int kblocks, const Capacity &cap, const Cos
     return best;
 }
 
-// launch(shape's index, split) as constants with the piece, for every piece of the plan.
+// Two products that each leave SMs idle take the time of the longer one when
+// each is planned for half of the SMs; in turn, the second one's start is hidden
+// by the first (about 4 us).  (Gradients of 500 x 777 x 1001 f32: 31.5 us in turn, 27.2 so; 1024 x 2048 x 2048
+// bf16 27.9 and 23.7.)
+inline bool side_by_side(const ProductSize &a, const ProductSize &b, int k_stage,
+                         const Capacity &cap, const Costs &cost) {
+    auto us = [&](const ProductSize &p, const Capacity &c) {
+        return plan_tiles(p.M, p.N, (p.K + k_stage - 1) / k_stage, c, cost).us;
+    };
+    const Capacity half = cap.half();
+    if (half.clusters[0] < 1) return false;
+    const double ha = us(a, half), hb = us(b, half);
+    return (ha > hb ? ha : hb) < us(a, cap) + us(b, cap) - 4.0;
+}
+
+// launch(shape's index, split) as constants with the piece and its place in the
+// chain, for every piece of the plan.
 template <class F>
-cudaError_t run_plan(const Plan &plan, F &&launch) {
+cudaError_t run_plan(const Plan &plan, int chain, F &&launch) {
     using Yes = std::true_type;
     using No = std::false_type;
     cudaError_t e = cudaSuccess;
     for (int i = 0; i < plan.pieces && e == cudaSuccess; ++i) {
         const Piece &p = plan.piece[i];
         auto shaped = [&](auto w) {
-            return p.parts > 1 ? launch(w, Yes(), p) : launch(w, No(), p);
+            const int at = (i > 0 ? kChainPrev : chain & kChainPrev) |
+                           (i + 1 < plan.pieces ? kChainNext : chain & kChainNext);
+            return p.parts > 1 ? launch(w, Yes(), p, at) : launch(w, No(), p, at);
         };
         e = plan.shape == 0   ? shaped(std::integral_constant<int, 0>())
             : plan.shape == 1 ? shaped(std::integral_constant<int, 1>())

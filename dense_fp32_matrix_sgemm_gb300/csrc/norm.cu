@@ -553,7 +553,7 @@ cudaError_t launch_add_rmsnorm_backward(int type, int64_t rows, int64_t D, const
                     : type == SGEMM_BF16 ? norm::grad_dispatch<__nv_bfloat16>(a, g, s)
                                          : norm::grad_dispatch<__half>(a, g, s);
     if (e != cudaSuccess || dw == nullptr) return e;
-    return launch_column_sum(type, partial, g.ctas, D, dw, s);
+    return launch_column_sum(type, partial, g.ctas, D, dw, 0, s);
 }
 
 }  // namespace sgemm

@@ -361,6 +361,32 @@ def test_linear_backward_parts_give_the_same_bits(m, n, k, name, t):
                 assert some[i] is None
 
 
+@pytest.mark.parametrize("m,n,k,t", [(500, 777, 301, "f32"), (300, 264, 520, "bf16"), (1030, 520, 777, "f16"),
+                                     (2560, 2560, 2600, "f32"), (2500, 2540, 8008, "bf16")])
+def test_products_back_to_back_give_the_same_bits(m, n, k, t):
+    # launches that overlap one another's ends: every call reads what the one
+    # before it wrote, in the same memory, without waiting on the host
+    g, dtype = gen(31), TYPES[t]
+    x, w, z, dy = (normal(g, *s, dtype=dtype, std=std) for s, std in
+                   (((m, k), 1), ((n, k), k ** -0.5), ((m, n), 1), ((m, n), 0.05)))
+
+    def chain(wait):
+        a, b, d, out = x.clone(), w.clone(), dy.clone(), []
+        for _ in range(6):
+            da, db, dbias = sg.linear_backward(d, a, b, z, activation="gelu")
+            wait()
+            y = sg.linear(da, b, residual=d, out=d)
+            wait()
+            d = sg.linear(a, db, activation="silu").mul_(1e-3).add_(y, alpha=0.1)
+            wait()
+            out += [da, db, dbias, y.clone(), d.clone()]
+        return out
+    apart = chain(torch.cuda.synchronize)
+    for _ in range(3):
+        for i, (p, q) in enumerate(zip(chain(lambda: None), apart)):
+            assert torch.equal(p, q), i
+
+
 @pytest.mark.parametrize("t", ["f32", "bf16"])
 def test_linear_backward_empty(t):
     d = TYPES[t]
