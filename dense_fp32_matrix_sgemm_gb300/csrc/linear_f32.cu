@@ -16,20 +16,18 @@
 // the MMAs go through the planes in the order a1 b1, a1 b0, a0 b1, a2 b0, a0 b2,
 // a0 b0: the first ones run when two thirds of a stage have landed, and a single
 // CTA gives plane 1's slot back half-way through (4096^3 in 128-wide tiles: 547
-// -> 523 us; 512 x 4096 x 4096 113 -> 95).  Pairs give all three back at the end,
-// as every commit there goes to both CTAs (464 us; one a plane as it is done
-// 482, whole stages 473).
+// -> 523 us).  Pairs give all three back at the end, as every commit there goes to
+// both CTAs (4096^3 464 us; one a plane as it is done 482, whole stages 473).
 // The tensor cores add into their accumulator with a rounding towards zero, so
 // a long sum there would collect errors of one sign.  Here an accumulator
 // takes one stage: the five small terms first, while it is small, then a0 b0
 // (four updates at full size), and the epilogue warps add it to running sums in
 // registers with ordinary fp32 adds while the other accumulators fill.
 // Relative error against 64 bits, 2049 x 3071 x 1537: 8e-8 (FP32 FMAs 4.2e-7).
-// 4096^3 runs at 1.77 PFLOP/s of bf16 products, what a long bf16 product runs at
-// under the power limit.  A 128-wide tile of one CTA is bound by shared memory:
-// 24 MMAs read 8 KB each and the copies write 96 KB, 2250 clocks at 128 bytes
-// a clock, against 1536 of MMAs (256 x 128 tiles of pairs, which read less,
-// were no faster: 2049 x 3071 x 1537 104 against 102).
+// 4096^3 runs at 1.84 PFLOP/s of bf16 products, what a long bf16 product runs at
+// under the power limit.  128 x 128 tiles of single CTAs are bound by shared memory
+// (24 MMAs read 8 KB each and the copies write 96 KB, 2250 clocks at 128 bytes a
+// clock against 1536 of MMAs), so they are left to problems of few rows.
 #include <cstdint>
 
 #include <cuda.h>
@@ -606,11 +604,15 @@ cudaError_t launch_f32_split(const F32Operand *x, int count, int chain, cudaStre
 }
 
 // The tile and schedule by cost, as linear_tc's; a stage (64 of K, 24 MMAs) takes
-// 1.72 us by pairs and 0.78 and 1.05 in 64- and 128-wide tiles, a pair's launch 9
-// (4096^3: 464 us with the last 28 of 256 tiles in 2 parts, 504 without, 523 with
-// 128-wide tiles; 2049 x 3071 x 1537 102 128-wide, 115 with pairs).
-constexpr ltc::Costs kF32Costs = {{{2, 256}, {1, 64}, {1, 128}}, {1.72, 0.78, 1.05}, {9.0, 6.0, 6.0},
-                                  {5.0, 1.5, 3.0}};
+// 1.6 to 1.8 us in pairs' 256-wide tiles, 0.86 to 0.98 in their 128-wide ones, and
+// in single CTAs' 64- and 128-wide tiles 0.78 and 1.05 (those for few rows).  The
+// choice against the others, us:
+//   4096^3: 256-wide with the last 28 of 256 tiles in 2 parts 449 (whole 490,
+//     128-wide pairs 460, single CTAs 514);
+//   2049 x 3071 x 1537: 128-wide pairs 89 (256-wide 114, single CTAs 102);
+//   64 x 4096 x 4096: 128-wide single CTAs in 4 parts 48 (64-wide in 2 56, pairs 57).
+constexpr ltc::Costs<4> kF32Costs = {{{2, 256}, {2, 128}, {1, 64}, {1, 128}}, {1.66, 0.89, 0.78, 1.05},
+                                     {8.5, 8.0, 6.0, 6.0}, {5.0, 3.0, 1.5, 3.0}};
 
 bool linear_f32_side_by_side(const ProductSize &a, const ProductSize &b) {
     ltc::Capacity cap;
@@ -626,7 +628,7 @@ cudaError_t launch_linear_f32(const F32Planes &A, const F32Planes &B, int K, con
     if (e != cudaSuccess) return e;
     if (chain & kChainHalf) cap = cap.half();
     const Plan plan = plan_tiles(epi.M, epi.N, (K + f32::kBk - 1) / f32::kBk, cap, kF32Costs);
-    return run_plan(plan, chain, [&](auto w, auto split, const Piece &p, int at) {
+    return run_plan(kF32Costs, plan, chain, [&](auto w, auto split, const Piece &p, int at) {
         constexpr TileShape t = kF32Costs.shape[w()];
         return f32::launch<t.ctas, t.bn, split()>(A, B, K, epi, p, at, s);
     });

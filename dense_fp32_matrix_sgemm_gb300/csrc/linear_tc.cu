@@ -538,8 +538,8 @@ cudaError_t capacity(Capacity &cap) {
 //   1024 x 2048 x 8192: 128-wide or 256-wide in 2 27.8 (256-wide 39.6);
 //   2048^3: 256-wide 15.1 (128-wide 16.1); 1024^3: 64-wide 5.8 (6.8, 9.5);
 //   4096 x 4096 x 8192: 256-wide, the last 28 of 256 tiles in 2 parts 151.9 (155.2).
-constexpr Costs kCosts = {{{2, 256}, {2, 128}, {1, 64}}, {0.27, 0.165, 0.15}, {6.5, 5.5, 4.5},
-                          {5.0, 3.0, 1.5}};
+constexpr Costs<3> kCosts = {{{2, 256}, {2, 128}, {1, 64}}, {0.27, 0.165, 0.15}, {6.5, 5.5, 4.5},
+                             {5.0, 3.0, 1.5}};
 
 template <class O>
 cudaError_t dispatch(int type, const TcOperand &A, const TcOperand &B, int K, const LayerEpi &epi,
@@ -550,7 +550,7 @@ cudaError_t dispatch(int type, const TcOperand &A, const TcOperand &B, int K, co
     const int bk = kRowBytes / dtype_size(type);
     if (chain & kChainHalf) cap = cap.half();
     const Plan plan = plan_tiles(epi.M, epi.N, (K + bk - 1) / bk, cap, kCosts);
-    return run_plan(plan, chain, [&](auto w, auto split, const Piece &p, int at) {
+    return run_plan(kCosts, plan, chain, [&](auto w, auto split, const Piece &p, int at) {
         constexpr TileShape t = kCosts.shape[w()];
         return launch<t.ctas, t.bn, O, split()>(type, A, B, K, epi, p, at, s);
     });

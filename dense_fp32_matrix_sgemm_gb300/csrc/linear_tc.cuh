@@ -129,8 +129,11 @@ __device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
     return v;
 }
 
+// Arrival on another CTA's barrier that publishes no memory: it says that this
+// warp's loads from tensor memory have completed (each waits for its data).  With
+// .release the warp first waits for all it has written and read, about 1700 clocks.
 __device__ __forceinline__ void arrive_cluster(uint32_t cluster_bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];"
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];"
                  :: "r"(cluster_bar) : "memory");
 }
 
@@ -312,11 +315,10 @@ struct Piece {
     int tile0, tiles, parts, room;
 };
 
-// Tiles of ctas * 128 x bn; a kernel is built for three shapes.
+// Tiles of ctas * 128 x bn; a kernel is built for a few shapes.
 struct TileShape {
     int ctas, bn;
 };
-constexpr int kShapes = 3;
 
 // How a product is computed: tiles of one shape, in one launch, or (pairs) whole
 // waves of tiles in one and the rest split in K in a second.
@@ -330,12 +332,14 @@ struct Plan {
 // The shapes and, in microseconds, what 128 bytes (f32: 64) of K of a tile take,
 // what a launch takes besides, and the joining of the parts of a split tile of 128
 // rows (next to 1 us a split launch).
+template <int SHAPES>
 struct Costs {
-    TileShape shape[kShapes];
-    double stage[kShapes], fixed[kShapes], join[kShapes];
+    TileShape shape[SHAPES];
+    double stage[SHAPES], fixed[SHAPES], join[SHAPES];
 };
 
-inline Plan plan_tiles(int M, int N, int kblocks, const Capacity &cap, const Costs &cost) {
+template <int SHAPES>
+Plan plan_tiles(int M, int N, int kblocks, const Capacity &cap, const Costs<SHAPES> &cost) {
     Plan best;
     const double rows = (M < BM ? M : BM) / (double)BM;
     // one split launch of `tiles` tiles; negative where it cannot run at once
@@ -353,7 +357,7 @@ inline Plan plan_tiles(int M, int N, int kblocks, const Capacity &cap, const Cos
         best.piece[1] = b;
         best.pieces = pieces;
     };
-    for (int w = 0; w < kShapes; ++w) {
+    for (int w = 0; w < SHAPES; ++w) {
         const int ctas = cost.shape[w].ctas, bn = cost.shape[w].bn;
         const long long all = (long long)((M + ctas * BM - 1) / (ctas * BM)) * ((N + bn - 1) / bn);
         if (all > 0x7fffffff) continue;
@@ -378,8 +382,9 @@ inline Plan plan_tiles(int M, int N, int kblocks, const Capacity &cap, const Cos
 // each is planned for half of the SMs; in turn, the second one's start is hidden
 // by the first (about 4 us).  (Gradients of 500 x 777 x 1001 f32: 31.5 us in turn, 27.2 so; 1024 x 2048 x 2048
 // bf16 27.9 and 23.7.)
-inline bool side_by_side(const ProductSize &a, const ProductSize &b, int k_stage,
-                         const Capacity &cap, const Costs &cost) {
+template <int SHAPES>
+bool side_by_side(const ProductSize &a, const ProductSize &b, int k_stage, const Capacity &cap,
+                  const Costs<SHAPES> &cost) {
     auto us = [&](const ProductSize &p, const Capacity &c) {
         return plan_tiles(p.M, p.N, (p.K + k_stage - 1) / k_stage, c, cost).us;
     };
@@ -389,23 +394,28 @@ inline bool side_by_side(const ProductSize &a, const ProductSize &b, int k_stage
     return (ha > hb ? ha : hb) < us(a, cap) + us(b, cap) - 4.0;
 }
 
-// launch(shape's index, split) as constants with the piece and its place in the
-// chain, for every piece of the plan.
-template <class F>
-cudaError_t run_plan(const Plan &plan, int chain, F &&launch) {
-    using Yes = std::true_type;
-    using No = std::false_type;
+// f(w as a constant).
+template <int W, int SHAPES, class F>
+cudaError_t with_shape(int w, F &&f) {
+    if constexpr (W < SHAPES)
+        return w == W ? f(std::integral_constant<int, W>()) : with_shape<W + 1, SHAPES>(w, f);
+    else
+        return cudaErrorInvalidValue;
+}
+
+// launch(shape's index and split as constants, the piece, its place in the chain)
+// for every piece of the plan.
+template <int SHAPES, class F>
+cudaError_t run_plan(const Costs<SHAPES> &, const Plan &plan, int chain, F &&launch) {
     cudaError_t e = cudaSuccess;
     for (int i = 0; i < plan.pieces && e == cudaSuccess; ++i) {
         const Piece &p = plan.piece[i];
-        auto shaped = [&](auto w) {
-            const int at = (i > 0 ? kChainPrev : chain & kChainPrev) |
-                           (i + 1 < plan.pieces ? kChainNext : chain & kChainNext);
-            return p.parts > 1 ? launch(w, Yes(), p, at) : launch(w, No(), p, at);
-        };
-        e = plan.shape == 0   ? shaped(std::integral_constant<int, 0>())
-            : plan.shape == 1 ? shaped(std::integral_constant<int, 1>())
-                              : shaped(std::integral_constant<int, 2>());
+        const int at = (i > 0 ? kChainPrev : chain & kChainPrev) |
+                       (i + 1 < plan.pieces ? kChainNext : chain & kChainNext);
+        e = with_shape<0, SHAPES>(plan.shape, [&](auto w) {
+            return p.parts > 1 ? launch(w, std::true_type(), p, at)
+                               : launch(w, std::false_type(), p, at);
+        });
     }
     return e;
 }
