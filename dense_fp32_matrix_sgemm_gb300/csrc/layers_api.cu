@@ -79,16 +79,17 @@ int check_workspace(void *ws, uint64_t have, size_t need) {
 
 // Whether a product of M rows runs on the CUDA cores (linear_rows.cu), in one
 // pass over the weights, or on the tensor cores.  Measured with 4096 x 4096
-// weights out of L2, in us, CUDA cores / tensor cores: bf16 1 row 7.9 / 10.5, 2
-// rows 9.0 / 10.5, 4 rows 15.7 / 10.6 (but 512 x 512, 4 rows: 3 / 6, where launch
-// and set-up count); bf16 stored K x N 1 row 24 / 10.5; e4m3 1 row 5.9 / 8.6, 2
-// rows 7.4 / 8.6, 3 rows 8.7 / 8.6; f32, whose planes the tensor cores need
-// written first, 8 rows 25 / 50, 16 rows 45 / 50.
+// weights out of L2, in us, CUDA cores / tensor cores: bf16 1 row 7.9 / 11, 2 rows
+// 8.4 / 11, 4 rows 15.7 / 11; bf16 stored K x N 1 row 24 / 11; e4m3 1 row 5.9 / 8.2,
+// 2 rows 9.0 / 8.2; with 1024 x 4096 weights, where launch and set-up count, bf16 4
+// rows 5.9 / 7.4, e4m3 2 rows 3.9 / 5.6; f32, whose planes the tensor cores need
+// written first, 8 rows 25 / 48, 16 rows 45 / 48.
 bool on_cuda_cores(int type, int64_t M, int64_t N, int64_t K, int transW) {
     if (K == 0) return true;
     if (type == SGEMM_F32) return M <= 16;
     if (!transW) return false;
-    return M <= 2 || (type != SGEMM_E4M3 && M <= 4 && N * K <= (1 << 22));
+    const int most = type == SGEMM_E4M3 ? 1 : 2;
+    return M <= (N * K <= (1 << 22) ? 2 * most : most);
 }
 
 // A tensor-core operand of rows x cols as stored: whether TMA can read it

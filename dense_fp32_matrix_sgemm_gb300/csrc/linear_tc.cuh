@@ -51,6 +51,12 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const void *tmap, uint32_
             : "memory");
 }
 
+// Asks for the box at (c0, c1) in L2.
+__device__ __forceinline__ void tma_prefetch(const void *tmap, int c0, int c1) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];"
+                 :: "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1) : "memory");
+}
+
 __device__ __forceinline__ void tma_store(const void *tmap, uint32_t src, int c0, int c1) {
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];"
                  :: "l"(reinterpret_cast<uint64_t>(tmap)), "r"(src), "r"(c0), "r"(c1)

@@ -188,6 +188,13 @@ def test_linear_long_sums(m, n, k, t):
         run_linear(m, n, k, t, "relu", bias=True, residual=True, w_kn=True)
 
 
+@pytest.mark.parametrize("t", ["bf16", "e4m3"])
+@pytest.mark.parametrize("m", [1, 2, 3, 4, 5])
+@pytest.mark.parametrize("n,k", [(2048, 2048), (2056, 2064), (2050, 2051)])
+def test_linear_few_rows_of_either_kernel(n, k, m, t):
+    run_linear(m, n, k, t, "silu", bias=True, residual=True, preact=True)
+
+
 def test_linear_e4m3_to_f16():
     run_linear(2, 96, 256, "e4m3", "silu", bias=True, out_dtype=torch.float16)
     run_linear(200, 500, 256, "e4m3", "silu", bias=True, residual=True, out_dtype=torch.float16)
