@@ -146,15 +146,25 @@ __device__ __forceinline__ void chain_end(int chain) {
 
 // ------------------------------------------------------------------ activations
 
-// 1 / (1 + exp(-t)).  exp(-t) overflows to infinity for t below about -88,
-// which gives the limit 0.  T is the type that the result is rounded to: for
-// the 16-bit types the hardware's exponential and reciprocal (a few units of
-// 2^-23, plus |t| of them in the exponent) are far below its roundoff and take
-// a third of the instructions.
+// 1 / (1 + 2^m) by the hardware's power of two and reciprocal (each within a few
+// units of 2^-23; results below 2^-126 become 0).  2^m overflows to infinity for
+// large m, which gives the limit 0.
+__device__ __forceinline__ float sigmoid_of_power(float m) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(m));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return r;
+}
+
+constexpr float kLog2E = 1.4426950408889634f;
+
+// 1 / (1 + exp(-t)).  T is the type that the result is rounded to: for the 16-bit
+// types the hardware's approximations (and |t| units of 2^-23 in the exponent) are
+// far below its roundoff and take a third of the instructions.
 template <class T>
 __device__ __forceinline__ float sigmoid(float t) {
     if constexpr (sizeof(T) == 4) return 1.f / (1.f + expf(-t));
-    return __fdividef(1.f, 1.f + __expf(-t));
+    return sigmoid_of_power(-kLog2E * t);
 }
 
 constexpr float kGeluC = 0.7978845608028654f;   // sqrt(2 / pi)
@@ -168,7 +178,12 @@ template <class T>
 __device__ __forceinline__ float activate(float z, int act) {
     switch (act) {
         case SGEMM_ACT_RELU: return z < 0.f ? 0.f : z;   // a NaN stays one
-        case SGEMM_ACT_GELU: return z * sigmoid<T>(2.f * kGeluC * (z + kGeluK * z * z * z));
+        case SGEMM_ACT_GELU:
+            if constexpr (sizeof(T) == 4)
+                return z * sigmoid<T>(2.f * kGeluC * (z + kGeluK * z * z * z));
+            else   // the same with the constants multiplied out
+                return z * sigmoid_of_power(z * fmaf(z * z, -2.f * kGeluC * kGeluK * kLog2E,
+                                                     -2.f * kGeluC * kLog2E));
         case SGEMM_ACT_GELU_ERF: return 0.5f * z * (1.f + erff(z * kSqrtHalf));
         case SGEMM_ACT_SILU: return z * sigmoid<T>(z);
         default: return z;
@@ -206,7 +221,12 @@ __device__ __forceinline__ float activate_grad(float z, int act) {
         case SGEMM_ACT_RELU: return z > 0.f ? 1.f : 0.f;
         case SGEMM_ACT_GELU: {
             const float z2 = z * z;
-            const float p = sigmoid<T>(2.f * kGeluC * (z + kGeluK * z2 * z));
+            float p;
+            if constexpr (sizeof(T) == 4)
+                p = sigmoid<T>(2.f * kGeluC * (z + kGeluK * z2 * z));
+            else
+                p = sigmoid_of_power(z * fmaf(z2, -2.f * kGeluC * kGeluK * kLog2E,
+                                              -2.f * kGeluC * kLog2E));
             return p + 2.f * kGeluC * z * p * (1.f - p) * (1.f + 3.f * kGeluK * z2);
         }
         case SGEMM_ACT_GELU_ERF:
