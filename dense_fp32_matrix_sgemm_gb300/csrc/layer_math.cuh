@@ -221,13 +221,15 @@ __device__ __forceinline__ float activate_grad(float z, int act) {
         case SGEMM_ACT_RELU: return z > 0.f ? 1.f : 0.f;
         case SGEMM_ACT_GELU: {
             const float z2 = z * z;
-            float p;
-            if constexpr (sizeof(T) == 4)
-                p = sigmoid<T>(2.f * kGeluC * (z + kGeluK * z2 * z));
-            else
-                p = sigmoid_of_power(z * fmaf(z2, -2.f * kGeluC * kGeluK * kLog2E,
-                                              -2.f * kGeluC * kLog2E));
-            return p + 2.f * kGeluC * z * p * (1.f - p) * (1.f + 3.f * kGeluK * z2);
+            if constexpr (sizeof(T) == 4) {
+                const float p = sigmoid<T>(2.f * kGeluC * (z + kGeluK * z2 * z));
+                return p + 2.f * kGeluC * z * p * (1.f - p) * (1.f + 3.f * kGeluK * z2);
+            } else {   // the same with the constants multiplied out
+                const float p = sigmoid_of_power(z * fmaf(z2, -2.f * kGeluC * kGeluK * kLog2E,
+                                                          -2.f * kGeluC * kLog2E));
+                const float q = z * fmaf(z2, 6.f * kGeluC * kGeluK, 2.f * kGeluC);
+                return fmaf(q, fmaf(-p, p, p), p);
+            }
         }
         case SGEMM_ACT_GELU_ERF:
             return 0.5f * (1.f + erff(z * kSqrtHalf)) + z * kRsqrt2Pi * expf(-0.5f * z * z);

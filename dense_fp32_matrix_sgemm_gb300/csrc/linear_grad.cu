@@ -32,8 +32,9 @@ struct DzArgs {
 // added through shared memory in warp order.  f32 dZ that only the tensor-core
 // products read is written as their planes (6 bytes an element instead of 4
 // written, 4 read and 6 written).  Four CTAs an SM, which the grid counts on
-// (without the bound 2 or 3 fit: 4096 x 8192 bf16 with the column sums 37.3 us,
-// so 33.8, with the activations as they are now 31: 201 MB, 6.5 TB/s).
+// (without the bound 2 or 3 fit: 4096 x 8192 bf16, GELU, the column sums alone 37.3
+// us, so 33.8, and 28.8 with the gradient's constants multiplied out; with dZ
+// written 33, 201 MB at 6.0 TB/s).
 template <class T, int W>
 __global__ void __launch_bounds__(kThreads, 4) dz_kernel(const DzArgs a) {
     __shared__ float red[kRowLanes][32 * W];
