@@ -413,6 +413,7 @@ cudaError_t with_shape(int w, F &&f) {
 // for every piece of the plan.
 template <int SHAPES, class F>
 cudaError_t run_plan(const Costs<SHAPES> &, const Plan &plan, int chain, F &&launch) {
+    if (plan.pieces == 0) return cudaErrorInvalidConfiguration;   // more than 2^31 tiles
     cudaError_t e = cudaSuccess;
     for (int i = 0; i < plan.pieces && e == cudaSuccess; ++i) {
         const Piece &p = plan.piece[i];

@@ -394,6 +394,33 @@ def test_products_back_to_back_give_the_same_bits(m, n, k, t):
             assert torch.equal(p, q), i
 
 
+@pytest.mark.parametrize("m,n,k,t", [(500, 777, 301, "f32"), (1024, 520, 776, "bf16")])
+def test_linear_backward_in_a_graph_and_on_another_stream(m, n, k, t):
+    g, dtype = gen(37), TYPES[t]
+    x, w, z, dy = (normal(g, *s, dtype=dtype) for s in ((m, k), (n, k), (m, n), (m, n)))
+    call = lambda **kw: sg.linear_backward(dy, x, w, z, activation="silu", **kw)  # noqa: E731
+    first = call()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    other = call(stream=side)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(first, other))
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        out = [call() for _ in range(3)]      # launches of one call behind another's
+        back = sg.linear(out[-1][0], out[-1][1])
+    dy.mul_(0.5)
+    x.mul_(2)
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    want = call()
+    for got in out:
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert torch.equal(back, sg.linear(want[0], want[1]))
+
+
 @pytest.mark.parametrize("t", ["f32", "bf16"])
 def test_linear_backward_empty(t):
     d = TYPES[t]
