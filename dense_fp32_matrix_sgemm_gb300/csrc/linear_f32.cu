@@ -430,9 +430,10 @@ struct SplitArgs {
 };
 
 // CTAs [0, job[0].blocks) take the first operand, the rest the second.  A warp
-// takes pieces of a row (512 columns with 16-byte accesses, 8 columns a lane
-// each, else 256 columns, 2 a lane), every access of a piece in flight; from
-// piece to piece it steps without a division.
+// takes pieces of 512 columns of a row, every load of a piece in flight: 16-byte
+// loads of 8 columns a lane, or (rows that are not aligned) single ones of 4, which
+// store 8 bytes a plane (2049 x 3071 x 1537: with 2 columns a lane the layer took
+// 89 us, so 86).  From piece to piece it steps without a division.
 __global__ void __launch_bounds__(256) split3_kernel(const SplitArgs a) {
     chain_begin(a.chain);
     const int which = (int)blockIdx.x < a.job[0].blocks ? 0 : 1;
@@ -440,8 +441,7 @@ __global__ void __launch_bounds__(256) split3_kernel(const SplitArgs a) {
     const int64_t warp = ((int64_t)blockIdx.x - (which ? a.job[0].blocks : 0)) * 8 +
                          (threadIdx.x >> 5);
     const int64_t warps = (int64_t)j.blocks * 8;
-    const int piece = j.vec ? 512 : 256;
-    const int pieces = (j.cols + piece - 1) / piece;
+    const int pieces = (j.cols + 511) / 512;
     const int64_t dr = warps / pieces;
     const int dc = (int)(warps - dr * pieces);
     int64_t r = warp / pieces;
@@ -480,22 +480,23 @@ __global__ void __launch_bounds__(256) split3_kernel(const SplitArgs a) {
                         make_uint4(p[0][pl], p[1][pl], p[2][pl], p[3][pl]);
             }
         } else {
-            float u[4][2];
+            float u[4][4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int c = pc * 256 + 64 * i + 2 * lane;
-                u[i][0] = c < j.cols ? __ldg(x + c) : 0.f;
-                u[i][1] = c + 1 < j.cols ? __ldg(x + c + 1) : 0.f;
+                const int c = pc * 512 + 128 * i + 4 * lane;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) u[i][k] = c + k < j.cols ? __ldg(x + c + k) : 0.f;
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int c = pc * 256 + 64 * i + 2 * lane;
+                const int c = pc * 512 + 128 * i + 4 * lane;
                 if (c >= j.cols) break;
-                uint32_t p[3];
-                split_pair(u[i][0], u[i][1], p);
+                uint32_t p[2][3];
+                split_pair(u[i][0], u[i][1], p[0]);
+                split_pair(u[i][2], u[i][3], p[1]);
 #pragma unroll
                 for (int pl = 0; pl < 3; ++pl)   // (the planes' rows are padded to 64)
-                    *reinterpret_cast<uint32_t *>(out + pl * plane + c) = p[pl];
+                    *reinterpret_cast<uint2 *>(out + pl * plane + c) = make_uint2(p[0][pl], p[1][pl]);
             }
         }
     }
@@ -586,8 +587,7 @@ cudaError_t launch_f32_split(const F32Operand *x, int count, int chain, cudaStre
         j.cols = (int)x[i].cols;
         j.vec = x[i].cols % 8 == 0 && x[i].ld % 4 == 0 &&
                 reinterpret_cast<uintptr_t>(x[i].X) % 16 == 0;
-        const int piece = j.vec ? 512 : 256;
-        const int64_t need = (j.rows * ((j.cols + piece - 1) / piece) + 7) / 8;
+        const int64_t need = (j.rows * ((j.cols + 511) / 512) + 7) / 8;
         j.blocks = (int)(need < 152 * 16 ? need : 152 * 16);
         blocks += j.blocks;
     }
@@ -609,7 +609,7 @@ cudaError_t launch_f32_split(const F32Operand *x, int count, int chain, cudaStre
 // choice against the others, us:
 //   4096^3: 256-wide with the last 28 of 256 tiles in 2 parts 449 (whole 490,
 //     128-wide pairs 460, single CTAs 514);
-//   2049 x 3071 x 1537: 128-wide pairs 89 (256-wide 114, single CTAs 102);
+//   2049 x 3071 x 1537: 128-wide pairs 86 (256-wide 110, single CTAs 98);
 //   64 x 4096 x 4096: 128-wide single CTAs in 4 parts 48 (64-wide in 2 56, pairs 57).
 constexpr ltc::Costs<4> kF32Costs = {{{2, 256}, {2, 128}, {1, 64}, {1, 128}}, {1.66, 0.89, 0.78, 1.05},
                                      {8.5, 8.0, 6.0, 6.0}, {5.0, 3.0, 1.5, 3.0}};
