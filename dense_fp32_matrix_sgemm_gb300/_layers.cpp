@@ -13,6 +13,7 @@
 #include <ATen/ATen.h>
 #include <ATen/core/LegacyTypeDispatch.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -72,15 +73,24 @@ int operand_type(const at::Tensor &t, const char *name, bool e4m3) {
     return c;
 }
 
+// Every tensor of a call is on the device of its first one, `like`: the call runs
+// there (CUDAGuard in each entry), whatever device is current.
+void same_device(const at::Tensor &t, const at::Tensor &like, const char *name) {
+    if (t.device() != like.device())
+        value_error(std::string(name) + " is on " + t.device().str() + ", the call's first tensor on " +
+                    like.device().str());
+}
+
 // Pointer and leading dimension of a 2-D CUDA tensor with contiguous rows.
 struct Mat {
     void *p = nullptr;
     int64_t ld = 0;
 };
-Mat matrix(const at::Tensor &t, const char *name, ScalarType type, int64_t rows = -1,
-           int64_t cols = -1) {
+Mat matrix(const at::Tensor &t, const char *name, const at::Tensor &like, ScalarType type,
+           int64_t rows = -1, int64_t cols = -1) {
     if (!t.is_cuda() || t.dim() != 2 || t.scalar_type() != type)
         type_error(std::string(name) + " must be a 2-D CUDA tensor of " + c10::toString(type));
+    same_device(t, like, name);
     const int64_t r = t.size(0), c = t.size(1);
     if (rows >= 0 && (r != rows || c != cols))
         value_error(std::string(name) + " has shape (" + std::to_string(r) + ", " +
@@ -92,21 +102,24 @@ Mat matrix(const at::Tensor &t, const char *name, ScalarType type, int64_t rows 
     const int64_t ld = r > 1 ? sr : c;
     return {t.data_ptr(), ld > 1 ? ld : 1};
 }
-Mat optional_matrix(PyObject *o, const char *name, ScalarType type, int64_t rows, int64_t cols) {
-    return present(o) ? matrix(tensor(o, name), name, type, rows, cols) : Mat{};
+Mat optional_matrix(PyObject *o, const char *name, const at::Tensor &like, ScalarType type,
+                    int64_t rows, int64_t cols) {
+    return present(o) ? matrix(tensor(o, name), name, like, type, rows, cols) : Mat{};
 }
 
 // Pointer of a contiguous vector of n elements.
-void *vector(PyObject *o, const char *name, ScalarType type, int64_t n) {
+void *vector(PyObject *o, const char *name, const at::Tensor &like, ScalarType type, int64_t n) {
     const at::Tensor &t = tensor(o, name);
     if (!t.is_cuda() || t.scalar_type() != type || t.dim() != 1 || t.size(0) != n ||
         (n > 1 && t.stride(0) != 1))
         value_error(std::string(name) + " must be a contiguous " + c10::toString(type) +
                     " CUDA tensor of " + std::to_string(n) + " elements");
+    same_device(t, like, name);
     return t.data_ptr();
 }
-void *optional_vector(PyObject *o, const char *name, ScalarType type, int64_t n) {
-    return present(o) ? vector(o, name, type, n) : nullptr;
+void *optional_vector(PyObject *o, const char *name, const at::Tensor &like, ScalarType type,
+                      int64_t n) {
+    return present(o) ? vector(o, name, like, type, n) : nullptr;
 }
 
 // An (N, K) weight stored by rows (trans 1) or as the transposed view of a
@@ -116,9 +129,10 @@ struct Weight {
     int64_t n, ld;
     int trans;
 };
-Weight weight(const at::Tensor &w, int64_t k, ScalarType type) {
+Weight weight(const at::Tensor &w, const at::Tensor &like, int64_t k, ScalarType type) {
     if (!w.is_cuda() || w.dim() != 2 || w.scalar_type() != type)
         type_error(std::string("weight must be a 2-D CUDA tensor of ") + c10::toString(type));
+    same_device(w, like, "weight");
     const int64_t n = w.size(0), sr = w.stride(0), sc = w.stride(1);
     if (w.size(1) != k)
         value_error("weight has " + std::to_string(w.size(1)) + " input features, expected " +
@@ -148,6 +162,7 @@ struct Scratch {
             const at::Tensor &t = tensor(given, "workspace");
             if (!t.is_cuda() || t.scalar_type() != ScalarType::Byte || !t.is_contiguous())
                 type_error("workspace must be a contiguous uint8 CUDA tensor");
+            same_device(t, like, "workspace");
             if ((uint64_t)t.numel() >= need && reinterpret_cast<uintptr_t>(t.data_ptr()) % 256 == 0) {
                 p = t.data_ptr();
                 bytes = (uint64_t)t.numel();
@@ -202,9 +217,10 @@ PyObject *linear(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
     return guarded([&]() -> PyObject * {
         const at::Tensor &x = tensor(a[0], "x");
         const int type = operand_type(x, "x", true);
-        const Mat X = matrix(x, "x", x.scalar_type());
+        const Mat X = matrix(x, "x", x, x.scalar_type());
+        const c10::cuda::CUDAGuard device(x.device());
         const int64_t m = x.size(0), k = x.size(1);
-        const Weight W = weight(tensor(a[1], "weight"), k, x.scalar_type());
+        const Weight W = weight(tensor(a[1], "weight"), x, k, x.scalar_type());
         ScalarType out_type = x.scalar_type();
         if (type == SGEMM_E4M3) {
             out_type = flag(a[7]) ? ScalarType::Half : ScalarType::BFloat16;
@@ -218,7 +234,7 @@ PyObject *linear(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
         at::Tensor y, z;
         Mat Y, Z;
         if (present(a[9])) {
-            Y = matrix(tensor(a[9], "out"), "out", out_type, m, W.n);
+            Y = matrix(tensor(a[9], "out"), "out", x, out_type, m, W.n);
         } else {
             y = fresh(x, {m, W.n}, out_type);
             Y = {y.data_ptr(), std::max<int64_t>(W.n, 1)};
@@ -228,10 +244,10 @@ PyObject *linear(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
             z = fresh(x, {m, W.n}, out_type);
             Z = {z.data_ptr(), std::max<int64_t>(W.n, 1)};
         }
-        const Mat R = optional_matrix(a[4], "residual", out_type, m, W.n);
-        void *xs = optional_vector(a[5], "x_scale", ScalarType::Float, m);
-        void *ws = optional_vector(a[6], "w_scale", ScalarType::Float, W.n);
-        void *bias = optional_vector(a[2], "bias", out_type, W.n);
+        const Mat R = optional_matrix(a[4], "residual", x, out_type, m, W.n);
+        void *xs = optional_vector(a[5], "x_scale", x, ScalarType::Float, m);
+        void *ws = optional_vector(a[6], "w_scale", x, ScalarType::Float, W.n);
+        void *bias = optional_vector(a[2], "bias", x, out_type, W.n);
         const Scratch s(a[10], f_linear_ws(type, m, W.n, k, X.p, X.ld, W.p, W.ld, W.trans), x);
         check_status(f_linear(type, m, W.n, k, X.p, X.ld, (const float *)xs, W.p, W.ld, W.trans,
                               (const float *)ws, bias, act, R.p, R.ld, type_code(out_type), Y.p,
@@ -254,18 +270,20 @@ PyObject *linear_backward(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
         const at::Tensor &dy = tensor(a[0], "dy"), &x = tensor(a[1], "x");
         const ScalarType t = dy.scalar_type();
         const int type = operand_type(dy, "dy", false);
-        const Mat G = matrix(dy, "dy", t), X = matrix(x, "x", t);
+        const Mat G = matrix(dy, "dy", dy, t), X = matrix(x, "x", dy, t);
+        const c10::cuda::CUDAGuard device(dy.device());
         const int64_t m = dy.size(0), n = dy.size(1), k = x.size(1);
         if (x.size(0) != m)
             value_error("x has " + std::to_string(x.size(0)) + " rows, dy " + std::to_string(m));
-        const Weight W = weight(tensor(a[2], "weight"), k, t);
+        const Weight W = weight(tensor(a[2], "weight"), dy, k, t);
         if (W.n != n)
             value_error("weight has " + std::to_string(W.n) + " output features, dy " +
                         std::to_string(n));
         const int act = (int)PyLong_AsLong(a[4]);
         if (act != SGEMM_ACT_NONE && !present(a[3]))
             value_error("this activation's gradient needs preact");
-        const Mat Z = act != SGEMM_ACT_NONE ? optional_matrix(a[3], "preact", t, m, n) : Mat{};
+        const Mat Z =
+            act != SGEMM_ACT_NONE ? optional_matrix(a[3], "preact", dy, t, m, n) : Mat{};
         at::Tensor dx, dw, db;
         if (flag(a[5])) dx = fresh(dy, {m, k}, t);
         if (flag(a[6])) dw = W.trans ? fresh(dy, {n, k}, t) : fresh(dy, {k, n}, t);
@@ -292,10 +310,11 @@ PyObject *add_rmsnorm(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
         const at::Tensor &x = tensor(a[0], "x");
         const ScalarType t = x.scalar_type();
         const int type = operand_type(x, "x", false);
-        const Mat X = matrix(x, "x", t);
+        const Mat X = matrix(x, "x", x, t);
+        const c10::cuda::CUDAGuard device(x.device());
         const int64_t rows = x.size(0), d = x.size(1), ld = std::max<int64_t>(d, 1);
-        void *w = vector(a[1], "weight", t, d);
-        const Mat R = optional_matrix(a[2], "residual", t, rows, d);
+        void *w = vector(a[1], "weight", x, t, d);
+        const Mat R = optional_matrix(a[2], "residual", x, t, rows, d);
         const double eps = PyFloat_AsDouble(a[3]);
         if (PyErr_Occurred()) throw Raised{};
         const bool quantize = flag(a[4]);
@@ -329,12 +348,13 @@ PyObject *add_rmsnorm_backward(PyObject *, PyObject *const *a, Py_ssize_t n_args
         const at::Tensor &dy = tensor(a[0], "dy");
         const ScalarType t = dy.scalar_type();
         const int type = operand_type(dy, "dy", false);
-        const Mat G = matrix(dy, "dy", t);
+        const Mat G = matrix(dy, "dy", dy, t);
+        const c10::cuda::CUDAGuard device(dy.device());
         const int64_t rows = dy.size(0), d = dy.size(1);
-        const Mat S = matrix(tensor(a[1], "s"), "s", t, rows, d);
-        const Mat D = optional_matrix(a[4], "ds", t, rows, d);
-        void *rstd = vector(a[2], "rstd", ScalarType::Float, rows);
-        void *w = vector(a[3], "weight", t, d);
+        const Mat S = matrix(tensor(a[1], "s"), "s", dy, t, rows, d);
+        const Mat D = optional_matrix(a[4], "ds", dy, t, rows, d);
+        void *rstd = vector(a[2], "rstd", dy, ScalarType::Float, rows);
+        void *w = vector(a[3], "weight", dy, t, d);
         const bool need = flag(a[5]);
         at::Tensor dx = fresh(dy, {rows, d}, t), dw;
         if (need) dw = fresh(dy, {d}, t);
@@ -354,7 +374,8 @@ PyObject *quantize_rows(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
     return guarded([&]() -> PyObject * {
         const at::Tensor &x = tensor(a[0], "x");
         const int type = operand_type(x, "x", false);
-        const Mat X = matrix(x, "x", x.scalar_type());
+        const Mat X = matrix(x, "x", x, x.scalar_type());
+        const c10::cuda::CUDAGuard device(x.device());
         const int64_t rows = x.size(0), d = x.size(1);
         at::Tensor q = fresh(x, {rows, d}, ScalarType::Float8_e4m3fn);
         at::Tensor scale = fresh(x, {rows}, ScalarType::Float);
@@ -363,6 +384,15 @@ PyObject *quantize_rows(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
                                      current_stream(x)));
         return Py_BuildValue("(NN)", THPVariable_Wrap(std::move(q)),
                              THPVariable_Wrap(std::move(scale)));
+    });
+}
+
+// t, like: what every entry asks of its tensors' devices
+PyObject *check_device(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
+    if (!arity(n_args, 2)) return nullptr;
+    return guarded([&]() -> PyObject * {
+        same_device(tensor(a[0], "t"), tensor(a[1], "like"), "t");
+        return none();
     });
 }
 
@@ -405,6 +435,7 @@ PyMethodDef methods[] = {
     ENTRY(add_rmsnorm),
     ENTRY(add_rmsnorm_backward),
     ENTRY(quantize_rows),
+    ENTRY(check_device),
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_layers", "The layer operators on torch tensors", -1,

@@ -9,7 +9,8 @@ enqueues the library's kernels (the C ABI of include/sgemm_gb300_layers.h) on
 ``stream`` (default: torch's current stream; outputs and scratch memory are
 allocated for the stream the call runs on).  Nothing synchronises.  Matrices
 are 2-D with a unit column stride and any row stride; a weight may also be the
-transposed view of one.  The checks and the call itself are in ``_layers``, a
+transposed view of one.  All tensors of a call, its workspace and its stream are
+of one device, and the call runs there whatever device is current.  The checks and the call itself are in ``_layers``, a
 C++ extension built beside the library; there is no other route.
 """
 from __future__ import annotations
@@ -46,6 +47,8 @@ def _on(stream, like):
     in that stream's order."""
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=like.device)
+    elif stream.device != like.device:
+        raise ValueError(f"stream is of {stream.device}, the call's first tensor on {like.device}")
     return torch.cuda.stream(stream)
 
 

@@ -1,0 +1,45 @@
+"""The layer operators on the GPU where they can go wrong: empty rows, the
+activations' tails and limits, special values, devices, overlapping launches."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+import dense_fp32_matrix_sgemm_gb300 as sg  # noqa: E402
+
+TYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def no_pipeline_errors():
+    sg.device_status(reset=True)
+    yield
+    assert sg.device_status(reset=True) == 0
+
+
+# ------------------------------------------------------------------ devices
+
+
+def test_operands_on_the_host_are_refused():
+    # (of two GPUs' tensors: the host tests' comparison, which every operand goes through)
+    x, w = torch.ones(4, 8, device="cuda"), torch.ones(16, 8, device="cuda")
+    v, rstd = torch.ones(8, device="cuda"), torch.ones(4, device="cuda")
+    host = lambda t: t.cpu()  # noqa: E731
+    for call in (lambda: sg.linear(x, host(w)), lambda: sg.linear(x, w, host(v.repeat(2))),
+                 lambda: sg.linear(x, w, residual=host(x @ w.t())),
+                 lambda: sg.linear(x, w, out=host(x @ w.t())),
+                 lambda: sg.linear(torch.ones(32, 8, device="cuda"), w,
+                                   workspace=torch.zeros(1 << 20, dtype=torch.uint8)),
+                 lambda: sg.linear_backward(x @ w.t(), host(x), w),
+                 lambda: sg.add_rmsnorm(x, host(v)), lambda: sg.add_rmsnorm(x, v, host(x)),
+                 lambda: sg.add_rmsnorm_backward(x, x, host(rstd), v),
+                 lambda: sg.add_rmsnorm_backward(x, host(x), rstd, v)):
+        with pytest.raises((TypeError, ValueError)):
+            call()
+    torch.cuda.synchronize()
+
+
+def test_calls_leave_the_current_device():
+    at = torch.cuda.current_device()
+    sg.quantize_rows(torch.ones(4, 8, device="cuda"))
+    assert torch.cuda.current_device() == at

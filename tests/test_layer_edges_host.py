@@ -1,0 +1,41 @@
+"""The layer operators' torch binding and build, without a GPU: devices, what the
+package needs to be imported, and when the binding is built."""
+import pytest
+
+import dense_fp32_matrix_sgemm_gb300 as sg
+from dense_fp32_matrix_sgemm_gb300 import _build
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    _build.build()
+    return sg.load_library()
+
+
+# ------------------------------------------------------------------ devices
+
+
+def test_tensors_of_different_devices_are_refused():
+    # the comparison that every entry makes of its tensors, on devices that
+    # exist everywhere
+    torch = pytest.importorskip("torch")
+    from dense_fp32_matrix_sgemm_gb300.layers import _layers
+    a, b = torch.zeros(2, 2), torch.zeros(2, 2, device="meta")
+    assert _layers.check_device(a, a.t()) is None
+    with pytest.raises(ValueError, match="t is on meta.*first tensor on cpu"):
+        _layers.check_device(b, a)
+    with pytest.raises(TypeError):
+        _layers.check_device(None, a)
+
+
+def test_a_stream_of_another_device_is_refused():
+    torch = pytest.importorskip("torch")
+
+    class Stream:
+        cuda_stream, device = 0, torch.device("cuda", 1)
+
+    class Tensor:
+        device = torch.device("cuda", 0)
+
+    with pytest.raises(ValueError, match="stream is of cuda:1"):
+        sg.quantize_rows(Tensor(), stream=Stream())
