@@ -411,13 +411,14 @@ int sgemm_add_rmsnorm(int dtype, int64_t rows, int64_t D, const void *X, int64_t
                       int64_t lds, void *Y, int64_t ldy, float *q_scale, float *rstd, void *stream) {
     using namespace sgemm;
     CHECK(check_norm(dtype, rows, D));
-    if (rows == 0 || D == 0) return SGEMM_OK;
+    // (rows of no elements have a scale and a reciprocal root all the same)
+    if (rows == 0 || (D == 0 && q_scale == nullptr && rstd == nullptr)) return SGEMM_OK;
     const int size = dtype_size(dtype);
-    CHECK(check_matrix("X", X, ldx, D, size, true));
+    CHECK(check_matrix("X", X, ldx, D, size, D > 0));
     CHECK(check_matrix("residual", residual, ldr, D, size, false));
     CHECK(check_matrix("S", S, lds, D, size, false));
-    CHECK(check_matrix("Y", Y, ldy, D, q_scale != nullptr ? 1 : size, true));
-    CHECK(check_matrix("weight", weight, D, D, size, true));
+    CHECK(check_matrix("Y", Y, ldy, D, q_scale != nullptr ? 1 : size, D > 0));
+    CHECK(check_matrix("weight", weight, D > 1 ? D : 1, D, size, D > 0));
     if (!aligned(q_scale, 4) || !aligned(rstd, 4))
         return fail(SGEMM_EINVAL_PTR, "q_scale or rstd is not 4-byte aligned");
     CHECK(require_device());
@@ -464,9 +465,9 @@ int sgemm_quantize_rows(int dtype, int64_t rows, int64_t D, const void *X, int64
                         int64_t ldq, float *scale, void *stream) {
     using namespace sgemm;
     CHECK(check_norm(dtype, rows, D));
-    if (rows == 0 || D == 0) return SGEMM_OK;
-    CHECK(check_matrix("X", X, ldx, D, dtype_size(dtype), true));
-    CHECK(check_matrix("Q", Q, ldq, D, 1, true));
+    if (rows == 0) return SGEMM_OK;
+    CHECK(check_matrix("X", X, ldx, D, dtype_size(dtype), D > 0));
+    CHECK(check_matrix("Q", Q, ldq, D, 1, D > 0));
     CHECK(check_matrix("scale", scale, 1, 1, 4, true));
     CHECK(require_device());
     return launched(launch_quantize_rows(dtype, rows, D, X, ldx, Q, ldq, scale,

@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(MAXT) row_kernel(const RowArgs a) {
     const float2 t = group_reduce(sum, top, red);
     float mul = 1.f;
     if constexpr (NORM) {
-        mul = 1.f / sqrtf(t.x / (float)a.D + a.eps);
+        mul = 1.f / sqrtf(t.x / (float)max(a.D, 1) + a.eps);   // (no elements: a mean of 0)
         if (a.rstd != nullptr && live && threadIdx.x == 0) a.rstd[row] = mul;
     }
     if constexpr (QUANT) {
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kMaxThreads) row_wide_kernel(const RowArgs a) 
     const float2 t = group_reduce(sum, top, red);
     float mul = 1.f;
     if constexpr (NORM) {
-        mul = 1.f / sqrtf(t.x / (float)a.D + a.eps);
+        mul = 1.f / sqrtf(t.x / (float)max(a.D, 1) + a.eps);   // (no elements: a mean of 0)
         if (a.rstd != nullptr && threadIdx.x == 0) a.rstd[row] = mul;
     }
     float inv = 1.f;

@@ -127,7 +127,8 @@ uint64_t sgemm_linear_backward_workspace_size(int dtype, int64_t M, int64_t N, i
  *            so that y is about Y * q_scale.
  *   rstd     NULL, or `rows` floats.
  * A NaN or infinity makes its own row's values as the formula gives them and
- * touches no other row.
+ * touches no other row.  Rows of no elements (D == 0) have the statistics of
+ * a row of zeros: q_scale = 1e-30 / 448, rstd = eps^(-1/2).
  */
 int sgemm_add_rmsnorm(int dtype, int64_t rows, int64_t D, const void *X, int64_t ldx,
                       const void *residual, int64_t ldr, const void *weight, float eps,
@@ -154,7 +155,10 @@ uint64_t sgemm_add_rmsnorm_backward_workspace_size(int dtype, int64_t rows, int6
 /*
  * Every row of X (rows x D of dtype SGEMM_F32, SGEMM_BF16 or SGEMM_F16) as
  * 8-bit codes with one scale: a = max(max_d |x|, 1e-30), scale = a / 448,
- * Q = x (448 / a) rounded to nearest even (SGEMM_E4M3, ldq >= D).
+ * Q = x (448 / a) rounded to nearest even (SGEMM_E4M3, ldq >= D).  A NaN or
+ * infinity reaches its row's a: that row's scale and codes are as the formula
+ * gives them, no other row's change.
+ * Rows of no elements (D == 0) have the scale of a row of zeros.
  */
 int sgemm_quantize_rows(int dtype, int64_t rows, int64_t D, const void *X, int64_t ldx,
                         void *Q, int64_t ldq, float *scale, void *stream);

@@ -43,3 +43,34 @@ def test_calls_leave_the_current_device():
     at = torch.cuda.current_device()
     sg.quantize_rows(torch.ones(4, 8, device="cuda"))
     assert torch.cuda.current_device() == at
+
+
+# ------------------------------------------------------------------ rows of no elements
+
+
+def poisoned(*shape):
+    """The allocator's next block of this size holds NaN."""
+    t = torch.full(shape, float("nan"), device="cuda")
+    del t
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("rows", [1, 4, 700])
+def test_rows_of_no_elements_have_scales(rows, t):
+    # 1e-30 / 448 and eps^(-1/2), each formed in fp32 with two roundings at most
+    x = torch.empty(rows, 0, dtype=TYPES[t], device="cuda")
+    w = torch.empty(0, dtype=TYPES[t], device="cuda")
+    ones = torch.ones(rows, dtype=torch.float64)
+    poisoned(rows)
+    q, scale = sg.quantize_rows(x)
+    assert q.shape == (rows, 0) and q.dtype == torch.float8_e4m3fn
+    torch.testing.assert_close(scale.cpu().double(), ones * (1e-30 / 448), rtol=2.0 ** -22, atol=0)
+    for residual in (None, x.clone()):
+        poisoned(rows)
+        y, s, rstd = sg.add_rmsnorm(x, w, residual, eps=0.25)
+        assert y.shape == s.shape == (rows, 0)
+        assert torch.equal(rstd.cpu().double(), 2 * ones)
+        poisoned(rows)
+        q, scale, s, rstd = sg.add_rmsnorm(x, w, residual, eps=0.25, quantize=True)
+        torch.testing.assert_close(scale.cpu().double(), ones * (1e-30 / 448), rtol=2.0 ** -22, atol=0)
+        assert torch.equal(rstd.cpu().double(), 2 * ones)

@@ -39,3 +39,17 @@ def test_a_stream_of_another_device_is_refused():
 
     with pytest.raises(ValueError, match="stream is of cuda:1"):
         sg.quantize_rows(Tensor(), stream=Stream())
+
+
+# ------------------------------------------------------------------ rows of no elements
+
+
+def test_rows_of_no_elements_are_checked_like_others():
+    fake = 0x100000
+    assert sg.sgemm_quantize_rows(0, 4, 0, 0, 1, 0, 1, 0, check=False) == 3          # scale
+    assert sg.sgemm_quantize_rows(0, 4, 0, 0, 1, 0, 1, fake + 2, check=False) == 3
+    assert sg.sgemm_add_rmsnorm(0, 4, 0, 0, 1, 0, 1, 0, 1e-6, 0, 1, 0, 1, q_scale=fake + 1,
+                                check=False) == 3
+    assert sg.sgemm_add_rmsnorm(0, 4, 0, 0, 1, 0, 1, 0, 1e-6, 0, 1, 0, 1, rstd=fake + 1,
+                                check=False) == 3
+    assert sg.sgemm_add_rmsnorm(0, 4, 0, 0, 1, 0, 1, 0, 1e-6, 0, 1, 0, 1, check=False) == 0
