@@ -221,6 +221,7 @@ int linear(int dtype, int64_t M, int64_t N, int64_t K, const void *X, int64_t ld
     CHECK(require_device());
     LayerEpi epi = {Y, preact, residual, bias, x_scale, w_scale, ldy, ldp, ldr, (int)M, (int)N,
                     activation, out_dtype, 1};
+    if (K == 0) epi.sx = epi.sw = nullptr;   // an empty sum is 0 in any unit, a NaN's too
     epi.vec = vector_width(out_dtype, epi);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (on_cuda_cores(dtype, M, N, K, transW))

@@ -67,7 +67,8 @@ typedef enum {
  * its own feature's; in f32 on the tensor cores an infinity gives NaN where the
  * formula's sum would be infinite (its terms are formed from the difference of
  * infinities).  Y and preact overlap neither X nor W.
- * M == 0 or N == 0 does nothing; K == 0 gives act(bias) + residual.
+ * M == 0 or N == 0 does nothing; K == 0 gives act(bias) + residual, whatever
+ * the scales.
  *   workspace   caller-owned device memory of at least
  *               sgemm_linear_workspace_size(...) bytes for the same
  *               arguments, 256-byte aligned, not used by other work while

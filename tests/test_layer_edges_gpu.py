@@ -74,3 +74,22 @@ def test_rows_of_no_elements_have_scales(rows, t):
         q, scale, s, rstd = sg.add_rmsnorm(x, w, residual, eps=0.25, quantize=True)
         torch.testing.assert_close(scale.cpu().double(), ones * (1e-30 / 448), rtol=2.0 ** -22, atol=0)
         assert torch.equal(rstd.cpu().double(), 2 * ones)
+
+
+@pytest.mark.parametrize("out", ["bf16", "f16"])
+@pytest.mark.parametrize("m", [1, 9, 300])
+def test_linear_e4m3_without_inputs(m, out):
+    # K = 0: act(bias) + residual, two exact terms and one rounding, whatever the scales hold
+    d = TYPES[out]
+    x, w = (torch.empty(r, 0, dtype=torch.float8_e4m3fn, device="cuda") for r in (m, 130))
+    b = torch.linspace(-3, 3, 130, device="cuda").to(d)
+    r = torch.linspace(-1, 1, m * 130, device="cuda").view(m, 130).to(d)
+    want = (b.double().clamp(min=0) + r.double()).float().to(d)
+    for value in (float("nan"), float("inf"), 1.0):
+        xs, ws = (torch.full((n,), value, device="cuda") for n in (m, 130))
+        assert torch.equal(sg.linear(x, w, b, activation="relu", residual=r, x_scale=xs, w_scale=ws,
+                                     out_dtype=d), want)
+    xs = sg.quantize_rows(torch.empty(m, 0, device="cuda"))[1]
+    ws = sg.quantize_rows(torch.empty(130, 0, device="cuda"))[1]
+    assert torch.equal(sg.linear(x, w, b, activation="relu", residual=r, x_scale=xs, w_scale=ws,
+                                 out_dtype=d), want)
