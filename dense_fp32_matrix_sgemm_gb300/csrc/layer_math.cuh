@@ -214,12 +214,23 @@ __device__ __forceinline__ void activate_all(float (&z)[N], int act) {
     }
 }
 
-// d act / dz.  With p = (1 + tanh u) / 2: (1 - tanh^2 u) / 2 = 2 p (1 - p).
+// z held to -limit .. limit; a NaN stays one.
+__device__ __forceinline__ float hold(float z, float limit) {
+    float r;
+    asm("min.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(r) : "f"(z), "f"(limit));
+    return r;
+}
+
+// d act / dz.  With p = (1 + tanh u) / 2: (1 - tanh^2 u) / 2 = 2 p (1 - p).  z is held
+// to where the slope has become exactly 0 or 1 in fp32 (p(1 - p) and the density are
+// 0 there): beyond, a term that grows with z would meet that 0 as an infinity and
+// give NaN (tanh form in 16 bits from |z| = 1.2e13 on, an infinite stored z in all).
 template <class T>
 __device__ __forceinline__ float activate_grad(float z, int act) {
     switch (act) {
         case SGEMM_ACT_RELU: return z > 0.f ? 1.f : 0.f;
         case SGEMM_ACT_GELU: {
+            z = hold(z, 16.f);   // the sigmoid's argument there: 318
             const float z2 = z * z;
             if constexpr (sizeof(T) == 4) {
                 const float p = sigmoid<T>(2.f * kGeluC * (z + kGeluK * z2 * z));
@@ -232,8 +243,10 @@ __device__ __forceinline__ float activate_grad(float z, int act) {
             }
         }
         case SGEMM_ACT_GELU_ERF:
+            z = hold(z, 32.f);   // the density's exponent there: -512
             return 0.5f * (1.f + erff(z * kSqrtHalf)) + z * kRsqrt2Pi * expf(-0.5f * z * z);
         case SGEMM_ACT_SILU: {
+            z = hold(z, 256.f);
             const float p = sigmoid<T>(z);
             return p * (1.f + z * (1.f - p));
         }

@@ -98,7 +98,8 @@ uint64_t sgemm_linear_workspace_size(int dtype, int64_t M, int64_t N, int64_t K,
  * not read, and may be NULL, for SGEMM_ACT_NONE.  dtype is the type of every
  * matrix: SGEMM_F32, SGEMM_BF16 or SGEMM_F16.  For the 16-bit types dZ enters
  * the two products rounded to the type (db is summed from the unrounded
- * values).  X is read for dW only, W for dX only.  No output overlaps an
+ * values).  Where z is infinite, act' is its limit, 0 or 1.  X is read for dW
+ * only, W for dX only.  No output overlaps an
  * input or another output.
  */
 int sgemm_linear_backward(int dtype, int64_t M, int64_t N, int64_t K,

@@ -93,3 +93,44 @@ def test_linear_e4m3_without_inputs(m, out):
     ws = sg.quantize_rows(torch.empty(130, 0, device="cuda"))[1]
     assert torch.equal(sg.linear(x, w, b, activation="relu", residual=r, x_scale=xs, w_scale=ws,
                                  out_dtype=d), want)
+
+
+# ------------------------------------------------------------------ activations
+
+
+def slopes(z, name):
+    """act'(z) by the bias gradient of one row with dY = 1."""
+    z = z.view(1, -1)
+    x, w = (torch.zeros(n, 1, dtype=z.dtype, device="cuda") for n in (1, z.shape[1]))
+    return sg.linear_backward(torch.ones_like(z), x, w, z, activation=name, need_dx=False,
+                              need_dw=False)[2]
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("name", ["relu", "gelu", "gelu_erf", "silu"])
+def test_slopes_at_large_and_infinite_z(name, t):
+    # exactly 0 or 1: the exponentials in them are below 2^-149 or their complements
+    big = [300.0, 65504.0, float("inf")] + ([] if t == "f16" else [1e13, 1e14, 2e19, 1e30, 3e38])
+    for n in (len(big), 8 * len(big), 8 * len(big) + 1):     # single elements, 16-byte accesses
+        z = torch.tensor(big * 9, device="cuda")[:n].to(TYPES[t])
+        assert torch.equal(slopes(z, name).float(), torch.ones(n, device="cuda"))
+        assert torch.equal(slopes(-z, name).float().abs(), torch.zeros(n, device="cuda"))
+    if name != "relu":
+        assert torch.isnan(slopes(torch.full((17,), float("nan"), device="cuda", dtype=TYPES[t]),
+                                  name)).all()
+
+
+@pytest.mark.parametrize("t", TYPES)
+def test_gradients_where_the_stored_z_has_overflowed(t):
+    # an infinite z in one place changes nothing but that place's slope
+    d, inf = TYPES[t], float("inf")
+    g = torch.Generator(device="cuda").manual_seed(5)
+    dy, z, x, w = (torch.randn(*s, generator=g, device="cuda").to(d)
+                   for s in ((40, 64), (40, 64), (40, 72), (64, 72)))
+    z[3, 5], z[7, 9] = inf, -inf
+    for name in ("gelu", "gelu_erf", "silu"):
+        got = sg.linear_backward(dy, x, w, z, activation=name)
+        near = z.clone()
+        near[3, 5], near[7, 9] = 300.0, -300.0    # slopes 1 and 0 to the last bit
+        for a, b in zip(got, sg.linear_backward(dy, x, w, near, activation=name)):
+            assert torch.equal(a, b)
