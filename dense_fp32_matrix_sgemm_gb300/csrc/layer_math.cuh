@@ -146,6 +146,8 @@ __device__ __forceinline__ void chain_end(int chain) {
 
 // ------------------------------------------------------------------ activations
 
+constexpr float kLog2E = 1.4426950408889634f;
+
 // 1 / (1 + 2^m) by the hardware's power of two and reciprocal (each within a few
 // units of 2^-23; results below 2^-126 become 0).  2^m overflows to infinity for
 // large m, which gives the limit 0.
@@ -155,8 +157,6 @@ __device__ __forceinline__ float sigmoid_of_power(float m) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
     return r;
 }
-
-constexpr float kLog2E = 1.4426950408889634f;
 
 // 1 / (1 + exp(-t)).  T is the type that the result is rounded to: for the 16-bit
 // types the hardware's approximations (and |t| units of 2^-23 in the exponent) are
@@ -172,6 +172,37 @@ constexpr float kGeluK = 0.044715f;
 constexpr float kSqrtHalf = 0.7071067811865476f;
 constexpr float kRsqrt2Pi = 0.3989422804014327f;   // 1 / sqrt(2 pi)
 
+// The normal distribution's Phi(z) = erfc(-z / sqrt 2) / 2 (1 + erf would lose 4 % of
+// it to rounding at z = -5 and all of it from -5.7 on), and 2^15 exp(-z^2/2).  For
+// the 16-bit types, with u = |z| and t = 1 / (1 + 0.36 u),
+//   Phi(-u) = exp(-u^2/2) t P(t)
+// where P, of degree 6, is a least-maximum fit to the smooth rest (over 0 <= u <= 15
+// relative error 1.1e-6, 1.3e-6 as evaluated), Phi(u) = 1 - Phi(-u).  (Column sums
+// of 4096 x 8192 bf16: 35 us, 78 with erfcf and expf.)  The factor 2^15 keeps
+// exp(-z^2/2) normal as far as z Phi(z) is a bf16 number.
+constexpr float kTail = 0x1p-15f;
+template <class T>
+__device__ __forceinline__ float normal_cdf(float z, float &density) {
+    if constexpr (sizeof(T) == 4) {
+        density = expf(-0.5f * z * z);
+        return 0.5f * erfcf(-z * kSqrtHalf);
+    }
+    const float u = fabsf(z);
+    float t;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(fmaf(0.36f, u, 1.f)));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(density)
+        : "f"(fmaf(u * (-0.5f * kLog2E), u, 15.f)));
+    float p = 0.0465225801f * kTail;
+    p = fmaf(p, t, -0.177935556f * kTail);
+    p = fmaf(p, t, 0.178465992f * kTail);
+    p = fmaf(p, t, 0.0282577164f * kTail);
+    p = fmaf(p, t, 0.139098883f * kTail);
+    p = fmaf(p, t, 0.141884699f * kTail);
+    p = fmaf(p, t, 0.143705189f * kTail);
+    const float h = density * (t * p);
+    return z < 0.f ? h : 1.f - h;
+}
+
 // (1 + tanh u) / 2 = 1 / (1 + exp(-2u)), so the tanh form of GELU is z times
 // a sigmoid: one exponential and no cancellation near tanh u = -1.
 template <class T>
@@ -184,7 +215,10 @@ __device__ __forceinline__ float activate(float z, int act) {
             else   // the same with the constants multiplied out
                 return z * sigmoid_of_power(z * fmaf(z * z, -2.f * kGeluC * kGeluK * kLog2E,
                                                      -2.f * kGeluC * kLog2E));
-        case SGEMM_ACT_GELU_ERF: return 0.5f * z * (1.f + erff(z * kSqrtHalf));
+        case SGEMM_ACT_GELU_ERF: {
+            float e;
+            return z * normal_cdf<T>(z, e);
+        }
         case SGEMM_ACT_SILU: return z * sigmoid<T>(z);
         default: return z;
     }
@@ -242,9 +276,12 @@ __device__ __forceinline__ float activate_grad(float z, int act) {
                 return fmaf(q, fmaf(-p, p, p), p);
             }
         }
-        case SGEMM_ACT_GELU_ERF:
+        case SGEMM_ACT_GELU_ERF: {
             z = hold(z, 32.f);   // the density's exponent there: -512
-            return 0.5f * (1.f + erff(z * kSqrtHalf)) + z * kRsqrt2Pi * expf(-0.5f * z * z);
+            float e;
+            const float p = normal_cdf<T>(z, e);
+            return fmaf(z * (kRsqrt2Pi * (sizeof(T) == 4 ? 1.f : kTail)), e, p);
+        }
         case SGEMM_ACT_SILU: {
             z = hold(z, 256.f);
             const float p = sigmoid<T>(z);

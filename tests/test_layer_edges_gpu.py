@@ -134,3 +134,45 @@ def test_gradients_where_the_stored_z_has_overflowed(t):
         near[3, 5], near[7, 9] = 300.0, -300.0    # slopes 1 and 0 to the last bit
         for a, b in zip(got, sg.linear_backward(dy, x, w, near, activation=name)):
             assert torch.equal(a, b)
+
+
+UNIT = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}
+STEP = {torch.float32: 2.0 ** -149, torch.bfloat16: 2.0 ** -133, torch.float16: 2.0 ** -24}   # smallest
+
+
+def values(z, name, m):
+    """act(z) in m rows, z coming in as the bias (m > 16: on the tensor cores)."""
+    x, w = (torch.zeros(n, 64, dtype=z.dtype, device="cuda") for n in (m, z.numel()))
+    return sg.linear(x, w, z, activation=name)
+
+
+def within(got, want, rel, what):
+    """rel of the value and half a step of the type's smallest values (rounding
+    there is absolute), both of them per element."""
+    err = (got.double() - want).abs()
+    tol = rel * want.abs() + 0.75 * STEP[got.dtype]
+    assert (err <= tol).all(), (what, float((err / tol).max()), int((err / tol).argmax()))
+
+
+@pytest.mark.parametrize("t", TYPES)
+def test_erf_gelu_keeps_its_relative_accuracy(t):
+    """z Phi(z) and Phi(z) + z phi(z) for z in [-12, 12] against erfc in 64 bits.
+    Phi's argument z / sqrt 2, or z^2 / 2 in an exponent, carries 1.5 roundings of
+    2^-24, which the tail magnifies by at most z^2 + 2; the functions called err by 4
+    units of 2^-23 at most, the products and sums by 2^-24 each: 16 2^-24 together;
+    the 16-bit types' own form adds the fit's 1.3e-6 and two hardware functions of
+    2^-22 each: 32 2^-24.  The slope's two terms have either sign: their sizes
+    count."""
+    d = TYPES[t]
+    z = torch.linspace(-12, 12, 4001, dtype=torch.float64).to(d)
+    z = z[: 4000 if t == "f32" else 4001].cuda()
+    zd = z.double()
+    phi = torch.exp(-0.5 * zd * zd) * 0.3989422804014326779
+    Phi = 0.5 * torch.special.erfc(-zd * 0.70710678118654752440)
+    rel = (1.5 * (zd * zd + 2) + 16 + (0 if t == "f32" else 32)) * 2.0 ** -24
+    for m in (1, 200):
+        y = values(z, "gelu_erf", m)
+        within(y, (zd * Phi).expand(m, -1), (rel + UNIT[d]).expand(m, -1), f"value, {m} rows")
+    want, size = Phi + zd * phi, Phi + zd.abs() * phi
+    err = (slopes(z, "gelu_erf").double() - want).abs()
+    assert (err <= rel * size + UNIT[d] * want.abs() + 0.75 * STEP[d]).all(), float(err.max())
