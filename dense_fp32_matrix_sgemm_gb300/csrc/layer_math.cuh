@@ -148,23 +148,31 @@ __device__ __forceinline__ void chain_end(int chain) {
 
 constexpr float kLog2E = 1.4426950408889634f;
 
-// 1 / (1 + 2^m) by the hardware's power of two and reciprocal (each within a few
-// units of 2^-23; results below 2^-126 become 0).  2^m overflows to infinity for
-// large m, which gives the limit 0.
-__device__ __forceinline__ float sigmoid_of_power(float m) {
+// 1 / (1 + 2^(a b)) by the hardware's power of two and reciprocal (each within a
+// few units of 2^-23), formed as 2^-18 / (2^-18 + 2^(a b - 18)): the reciprocal, whose
+// results below 2^-126 become 0, is then normal down to a quotient of 2^-144, from
+// where on z times it, and the slopes' largest factor (260, tanh form) times it, are
+// 0 in bf16 too.  (Without the factor SiLU was 0 from z = -88 on, where bf16 has
+// values down to z = -98.)
+constexpr float kTailBits = 18.f, kTail = 0x1p-18f;
+__device__ __forceinline__ float sigmoid_of_power(float a, float b) {
     float e, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(m));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
-    return r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fmaf(a, b, -kTailBits)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(kTail + e));
+    return r * kTail;
 }
 
 // 1 / (1 + exp(-t)).  T is the type that the result is rounded to: for the 16-bit
 // types the hardware's approximations (and |t| units of 2^-23 in the exponent) are
-// far below its roundoff and take a third of the instructions.
+// far below its roundoff and take a third of the instructions.  (f32: exp(-|t|), as
+// exp(-t) overflows at t = -88.7, where the result is still 3e-39.)
 template <class T>
 __device__ __forceinline__ float sigmoid(float t) {
-    if constexpr (sizeof(T) == 4) return 1.f / (1.f + expf(-t));
-    return sigmoid_of_power(-kLog2E * t);
+    if constexpr (sizeof(T) == 4) {
+        const float e = expf(-fabsf(t));
+        return (t < 0.f ? e : 1.f) / (1.f + e);
+    }
+    return sigmoid_of_power(t, -kLog2E);
 }
 
 constexpr float kGeluC = 0.7978845608028654f;   // sqrt(2 / pi)
@@ -173,14 +181,13 @@ constexpr float kSqrtHalf = 0.7071067811865476f;
 constexpr float kRsqrt2Pi = 0.3989422804014327f;   // 1 / sqrt(2 pi)
 
 // The normal distribution's Phi(z) = erfc(-z / sqrt 2) / 2 (1 + erf would lose 4 % of
-// it to rounding at z = -5 and all of it from -5.7 on), and 2^15 exp(-z^2/2).  For
-// the 16-bit types, with u = |z| and t = 1 / (1 + 0.36 u),
+// it to rounding at z = -5 and all of it from -5.7 on), and the `density`
+// exp(-z^2/2), 2^18 times it for the 16-bit types.  For those, with u = |z| and t = 1 / (1 + 0.36 u),
 //   Phi(-u) = exp(-u^2/2) t P(t)
 // where P, of degree 6, is a least-maximum fit to the smooth rest (over 0 <= u <= 15
 // relative error 1.1e-6, 1.3e-6 as evaluated), Phi(u) = 1 - Phi(-u).  (Column sums
-// of 4096 x 8192 bf16: 35 us, 78 with erfcf and expf.)  The factor 2^15 keeps
+// of 4096 x 8192 bf16: 35 us, 78 with erfcf and expf.)  The factor 2^18 keeps
 // exp(-z^2/2) normal as far as z Phi(z) is a bf16 number.
-constexpr float kTail = 0x1p-15f;
 template <class T>
 __device__ __forceinline__ float normal_cdf(float z, float &density) {
     if constexpr (sizeof(T) == 4) {
@@ -191,7 +198,7 @@ __device__ __forceinline__ float normal_cdf(float z, float &density) {
     float t;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(fmaf(0.36f, u, 1.f)));
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(density)
-        : "f"(fmaf(u * (-0.5f * kLog2E), u, 15.f)));
+        : "f"(fmaf(u * (-0.5f * kLog2E), u, kTailBits)));
     float p = 0.0465225801f * kTail;
     p = fmaf(p, t, -0.177935556f * kTail);
     p = fmaf(p, t, 0.178465992f * kTail);
@@ -213,8 +220,8 @@ __device__ __forceinline__ float activate(float z, int act) {
             if constexpr (sizeof(T) == 4)
                 return z * sigmoid<T>(2.f * kGeluC * (z + kGeluK * z * z * z));
             else   // the same with the constants multiplied out
-                return z * sigmoid_of_power(z * fmaf(z * z, -2.f * kGeluC * kGeluK * kLog2E,
-                                                     -2.f * kGeluC * kLog2E));
+                return z * sigmoid_of_power(z, fmaf(z * z, -2.f * kGeluC * kGeluK * kLog2E,
+                                                    -2.f * kGeluC * kLog2E));
         case SGEMM_ACT_GELU_ERF: {
             float e;
             return z * normal_cdf<T>(z, e);
@@ -270,8 +277,8 @@ __device__ __forceinline__ float activate_grad(float z, int act) {
                 const float p = sigmoid<T>(2.f * kGeluC * (z + kGeluK * z2 * z));
                 return p + 2.f * kGeluC * z * p * (1.f - p) * (1.f + 3.f * kGeluK * z2);
             } else {   // the same with the constants multiplied out
-                const float p = sigmoid_of_power(z * fmaf(z2, -2.f * kGeluC * kGeluK * kLog2E,
-                                                          -2.f * kGeluC * kLog2E));
+                const float p = sigmoid_of_power(z, fmaf(z2, -2.f * kGeluC * kGeluK * kLog2E,
+                                                         -2.f * kGeluC * kLog2E));
                 const float q = z * fmaf(z2, 6.f * kGeluC * kGeluK, 2.f * kGeluC);
                 return fmaf(q, fmaf(-p, p, p), p);
             }

@@ -176,3 +176,32 @@ def test_erf_gelu_keeps_its_relative_accuracy(t):
     want, size = Phi + zd * phi, Phi + zd.abs() * phi
     err = (slopes(z, "gelu_erf").double() - want).abs()
     assert (err <= rel * size + UNIT[d] * want.abs() + 0.75 * STEP[d]).all(), float(err.max())
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("name,low", [("silu", -104.0), ("gelu", -12.0)])
+def test_activations_in_the_far_tail(name, low, t):
+    """z p(z) and its slope, p = 1 / (1 + exp(-v)), where p is near or below the
+    smallest normal number (2^-126), against 64 bits.  v = z, or 2 sqrt(2/pi) (z +
+    0.044715 z^3) with 5 roundings, enters an exponential: (6 |v| + 16) 2^-24 relative.
+    A p below 2^-126 has an absolute error of up to 2^-149 in fp32, which z, or the
+    slope's factor f, multiplies."""
+    d = TYPES[t]
+    z = torch.linspace(low, 0.75 * low, 801, dtype=torch.float64).to(d)
+    z = z[: 800 if t == "f32" else 801].cuda()
+    zd = z.double()
+    if name == "silu":
+        v, dv = zd, torch.ones_like(zd)
+    else:
+        c = (8 / torch.pi) ** 0.5
+        v, dv = c * (zd + 0.044715 * zd ** 3), c * (1 + 3 * 0.044715 * zd ** 2)
+    p = torch.exp(v) / (1 + torch.exp(v))
+    f = 1 + zd * dv * (1 - p)
+    rel = (6 * v.abs() + 16) * 2.0 ** -24 + UNIT[d]
+    for m in (1, 200):
+        y = values(z, name, m)
+        err, tol = (y.double() - zd * p).abs(), rel * (zd * p).abs() + 2.0 ** -149 * zd.abs()
+        assert (err <= tol + 0.75 * STEP[d]).all(), (m, float((err / tol).max()))
+    err = (slopes(z, name).double() - p * f).abs()
+    tol = rel * p * (1 + (zd * dv).abs()) + 2.0 ** -149 * f.abs()
+    assert (err <= tol + 0.75 * STEP[d]).all(), float((err / tol).max())
