@@ -240,7 +240,6 @@ __global__ void __launch_bounds__(MAXT) grad_kernel(const GradArgs a) {
     pdl_wait();
     const int64_t group = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     const int64_t groups = (int64_t)gridDim.x * blockDim.y;
-    const float inv_d = 1.f / (float)a.D;
     Raw<T, W> vw[NV];
     float dw[NV][W];
 #pragma unroll
@@ -322,7 +321,8 @@ __global__ void __launch_bounds__(MAXT) grad_kernel(const GradArgs a) {
         }
         // two buffers: a warp may reach the next turn's while another still
         // reads this one's, not the one after (that takes the next barrier)
-        const float k = group_reduce(sum, 0.f, red[t & 1]).x * inv_d * rstd * rstd;
+        // (the mean by a division: a rounded 1 / D would double its error)
+        const float k = group_reduce(sum, 0.f, red[t & 1]).x / (float)a.D * rstd * rstd;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * blockDim.x + threadIdx.x) * W;

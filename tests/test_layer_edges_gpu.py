@@ -205,3 +205,18 @@ def test_activations_in_the_far_tail(name, low, t):
     err = (slopes(z, name).double() - p * f).abs()
     tol = rel * p * (1 + (zd * dv).abs()) + 2.0 ** -149 * f.abs()
     assert (err <= tol + 0.75 * STEP[d]).all(), float((err / tol).max())
+
+
+# ------------------------------------------------------------------ norm gradient
+
+
+@pytest.mark.parametrize("t", TYPES)
+def test_norm_gradient_of_constant_rows_is_zero(t):
+    """dY = s = w = rstd = 1: dX = 1 - mean(1).  Sums of D ones are exact in any
+    order up to 2^24, so is D / D; D times a rounded 1 / D is not always 1 (here for
+    several of the widths, both kernels)."""
+    for d in (1, 3, 41, 47, 49, 61, 82, 83, 98, 97, 103, 328, 1001, 1312, 2048, 4099, 6150, 9001, 40000):
+        one = torch.ones(5, d, dtype=TYPES[t], device="cuda")
+        dx, dw = sg.add_rmsnorm_backward(one, one, torch.ones(5, device="cuda"), one[0].contiguous())
+        assert not dx.any(), d
+        assert torch.equal(dw, 5 * one[0]), d
