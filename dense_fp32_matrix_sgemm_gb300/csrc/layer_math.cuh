@@ -132,13 +132,24 @@ __device__ __forceinline__ void store_vec(T *p, const float (&x)[N]) {
 // plan, the gradients' two products, ...) form a chain, in which a later one fills the
 // SMs that the ones before it leave.  The first (kChainNext alone) waits for
 // earlier work as ever, and lets the next one start only after that wait: where
-// the next one runs, all earlier work is complete.  The others (kChainPrev) do not
-// wait at their start but before they end, so that each launch completes after the
-// ones before it and the work behind the last one waits for all of them.
+// the next one runs, all earlier work has completed.  The others (kChainPrev) do
+// not wait at their start but before they end, so that each launch completes after
+// the ones before it and the work behind the last one waits for all of them.
+// That earlier work has completed says where its results are (L2, at the latest
+// when it ended), not that this launch's loads look there: only a launch's own wait
+// promises that, and an L1 may hold the same addresses as an earlier call left them
+// (workspaces are used again).  So a launch with kChainPrev takes what earlier work
+// wrote from L2: by TMA, by __ldcg, or by plain loads after chain_fence, which leaves
+// nothing older in the SM's L1; never through the read-only path (__ldg).
 __device__ __forceinline__ void chain_begin(int chain) {
     if (!(chain & kChainNext)) pdl_trigger();
     if (!(chain & kChainPrev)) pdl_wait();
     if (chain & kChainNext) pdl_trigger();
+}
+// (about a microsecond where a launch starts with it, as the planes' does: gradients
+// of 500 x 777 x 1001 f32 23.6 us, without it 22.5)
+__device__ __forceinline__ void chain_fence(int chain) {
+    if (chain & kChainPrev) asm volatile("fence.acq_rel.gpu;" ::: "memory");
 }
 __device__ __forceinline__ void chain_end(int chain) {
     if (chain & kChainPrev) pdl_wait();

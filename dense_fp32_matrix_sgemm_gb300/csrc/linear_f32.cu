@@ -304,6 +304,7 @@ linear_f32_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
         }
     } else {
         // ---------------- epilogue: this CTA's rows, half of the columns a warp
+        if (p.epi.bias != nullptr || p.epi.R != nullptr) chain_fence(p.chain);
         const int q = warp & 3, side = (warp - 2) >> 2;
         const uint32_t stage = ring + RING * S::PLANE + (uint32_t)((warp - 2) * kStage);
         tc::Ring<SLOTS> slot;
@@ -433,9 +434,12 @@ struct SplitArgs {
 // takes pieces of 512 columns of a row, every load of a piece in flight: 16-byte
 // loads of 8 columns a lane, or (rows that are not aligned) single ones of 4, which
 // store 8 bytes a plane (2049 x 3071 x 1537: with 2 columns a lane the layer took
-// 89 us, so 86).  From piece to piece it steps without a division.
+// 89 us, so 86).  From piece to piece it steps without a division.  A lane's
+// loads share their sectors through L1, hence the fence (chain_begin; from L2 alone
+// 2049 x 3071 x 1537 takes 107 us, 2560 x 2560 x 2600 149 for 143).
 __global__ void __launch_bounds__(256) split3_kernel(const SplitArgs a) {
     chain_begin(a.chain);
+    chain_fence(a.chain);
     const int which = (int)blockIdx.x < a.job[0].blocks ? 0 : 1;
     const SplitJob j = which ? a.job[1] : a.job[0];
     const int64_t warp = ((int64_t)blockIdx.x - (which ? a.job[0].blocks : 0)) * 8 +
@@ -461,8 +465,8 @@ __global__ void __launch_bounds__(256) split3_kernel(const SplitArgs a) {
             for (int i = 0; i < 2; ++i) {
                 const int c = pc * 512 + 256 * i + 8 * lane;
                 if (c < j.cols) {
-                    u[i][0] = __ldg(reinterpret_cast<const float4 *>(x + c));
-                    u[i][1] = __ldg(reinterpret_cast<const float4 *>(x + c) + 1);
+                    u[i][0] = *reinterpret_cast<const float4 *>(x + c);
+                    u[i][1] = *(reinterpret_cast<const float4 *>(x + c) + 1);
                 }
             }
 #pragma unroll
@@ -485,7 +489,7 @@ __global__ void __launch_bounds__(256) split3_kernel(const SplitArgs a) {
             for (int i = 0; i < 4; ++i) {
                 const int c = pc * 512 + 128 * i + 4 * lane;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) u[i][k] = c + k < j.cols ? __ldg(x + c + k) : 0.f;
+                for (int k = 0; k < 4; ++k) u[i][k] = c + k < j.cols ? x[c + k] : 0.f;
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {

@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const float *partial, 
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int p = p0 + 32 * u;
-                x[u] = p < parts ? partial[p * N + c] : 0.f;
+                x[u] = p < parts ? __ldcg(partial + p * N + c) : 0.f;   // (see chain_begin)
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) v += x[u];

@@ -381,6 +381,8 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         }
     } else {
         // ---------------- epilogue: this CTA's rows
+        if (p.epi.bias != nullptr || p.epi.R != nullptr || p.epi.sx != nullptr)
+            chain_fence(p.chain);   // they are read through L1
         const int q = warp & 3, side = (warp - 2) >> 2;
         const uint32_t stage = ring + STAGES * S::STAGE + (uint32_t)((warp - 2) * kStage);
         for (int i = 0; i < ntiles; ++i) {
