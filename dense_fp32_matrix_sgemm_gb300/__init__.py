@@ -33,8 +33,7 @@ __all__ = ["SgemmError", "SgemmUnavailable", "load_library", "library_path",
            "set_tf32x3_chunk_k", "marshalling", "sgemm_linear", "sgemm_linear_backward",
            "sgemm_add_rmsnorm", "sgemm_add_rmsnorm_backward", "sgemm_quantize_rows",
            "linear_workspace_size", "linear_backward_workspace_size",
-           "add_rmsnorm_backward_workspace_size", "linear", "linear_backward", "add_rmsnorm",
-           "add_rmsnorm_backward", "quantize_rows"]
+           "add_rmsnorm_backward_workspace_size"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "libsgemm_gb300.so")
@@ -575,8 +574,8 @@ def sgemm_quantize_rows(dtype, rows, D, X, ldx, Q, ldq, scale, stream=0, *, chec
     return _check(st) if check else st
 
 
-# The torch-level operators (layers.py), imported at first use: the package
-# itself does not need torch.
+# The torch-level operators (layers.py), imported at first use and not in __all__:
+# the package itself does not need torch.
 _LAYERS = ("linear", "linear_backward", "add_rmsnorm", "add_rmsnorm_backward", "quantize_rows")
 
 

@@ -53,3 +53,34 @@ def test_rows_of_no_elements_are_checked_like_others():
     assert sg.sgemm_add_rmsnorm(0, 4, 0, 0, 1, 0, 1, 0, 1e-6, 0, 1, 0, 1, rstd=fake + 1,
                                 check=False) == 3
     assert sg.sgemm_add_rmsnorm(0, 4, 0, 0, 1, 0, 1, 0, 1e-6, 0, 1, 0, 1, check=False) == 0
+
+
+# ------------------------------------------------------------------ imports
+
+
+def test_star_import_needs_no_torch():
+    # torch hidden, and the binding's module with it
+    import os
+    import subprocess
+    import sys
+    code = ("import sys\n"
+            "sys.modules['torch'] = None\n"
+            "from dense_fp32_matrix_sgemm_gb300 import *\n"
+            "import dense_fp32_matrix_sgemm_gb300 as sg\n"
+            "assert all(hasattr(sg, n) for n in sg.__all__)\n"
+            "assert sgemm_linear and matmul and load_library\n"
+            "try:\n"
+            "    sg.linear\n"
+            "except ImportError:\n"
+            "    print('fine')\n")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.stdout == "fine\n", r.stderr
+
+
+def test_the_torch_functions_are_attributes():
+    pytest.importorskip("torch")
+    for name in ("linear", "linear_backward", "add_rmsnorm", "add_rmsnorm_backward", "quantize_rows"):
+        assert callable(getattr(sg, name))
+    with pytest.raises(AttributeError):
+        sg.no_such_operator
