@@ -66,14 +66,7 @@ def build(verbose: bool = False, ptxas_verbose: bool = False, jobs: int | None =
     os.makedirs(BUILD, exist_ok=True)
     srcs = _sources()
     # the torch binding compiles beside the kernels
-    layers_error: list = []
-
-    def build_layers():
-        try:
-            _build_layers(verbose)
-        except Exception as e:   # raised again by the caller's thread
-            layers_error.append(e)
-    layers = threading.Thread(target=build_layers)
+    layers = threading.Thread(target=_build_layers, args=(verbose,))
     layers.start()
     jobs = jobs or min(len(srcs), max(1, os.cpu_count() or 1))
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
@@ -92,17 +85,16 @@ def build(verbose: bool = False, ptxas_verbose: bool = False, jobs: int | None =
         os.replace(LIB + ".tmp", LIB)
     if verbose:
         sys.stderr.write(f"built {LIB}\n")
-    layers.join()
-    if layers_error:
-        raise layers_error[0]
     _build_calls(verbose)
+    layers.join()
     return LIB
 
 
 def _build_layers(verbose: bool = False):
     """Compile _layers.cpp, the torch binding of the layer operators (see that
-    file), next to the library.  Without torch nothing is built: the C ABI and
-    the other calls do not need it."""
+    file), next to the library.  Without a torch that it can be built against
+    nothing is built, and a note says why: the C ABI and the other calls do not
+    need it, and layers.py raises SgemmUnavailable."""
     import importlib.util
     import sysconfig
     if importlib.util.find_spec("torch") is None:
@@ -124,9 +116,17 @@ def _build_layers(verbose: bool = False):
            "-L", os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
            "-lc10_cuda",
            "-ltorch_cuda"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"_layers.cpp did not build:\n{r.stdout}\n{r.stderr}")
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        failed = f"{r.stdout}\n{r.stderr}" if r.returncode != 0 else ""
+    except OSError as e:
+        failed = str(e)
+    if failed:
+        if os.path.exists(out):
+            os.remove(out)   # of older sources or another torch
+        sys.stderr.write("note: the torch binding of the layer operators (_layers.cpp) does not build "
+                         f"against {torch_dir}; everything else does:\n{failed}\n")
+        return None
     os.replace(out + ".tmp", out)
     if verbose:
         sys.stderr.write(f"built {out}\n")

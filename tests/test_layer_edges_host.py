@@ -84,3 +84,51 @@ def test_the_torch_functions_are_attributes():
         assert callable(getattr(sg, name))
     with pytest.raises(AttributeError):
         sg.no_such_operator
+
+
+# ------------------------------------------------------------------ build
+
+
+@pytest.fixture
+def scratch_build(tmp_path, monkeypatch):
+    """_build on a copy of the binding's source, with a compiler that records its
+    calls: `state` holds its exit status and the commands it got."""
+    import shutil
+    import types
+    pytest.importorskip("torch")
+    shutil.copy(_build.PKG + "/_layers.cpp", tmp_path)
+    monkeypatch.setattr(_build, "PKG", str(tmp_path))
+    monkeypatch.setattr(_build, "BUILD", str(tmp_path / "build"))
+    (tmp_path / "build").mkdir()
+    state = types.SimpleNamespace(status=0, commands=[], dir=tmp_path)
+
+    def run(cmd, **kw):
+        if state.status is None:
+            raise FileNotFoundError("no compiler")
+        state.commands.append(cmd)
+        if state.status == 0:
+            with open(cmd[cmd.index("-o") + 1], "w") as f:
+                f.write("built")
+        return types.SimpleNamespace(returncode=state.status, stdout="", stderr="cannot find -ltorch_cuda")
+
+    monkeypatch.setattr(_build.subprocess, "run", run)
+    return state
+
+
+@pytest.mark.parametrize("status", [1, None])
+def test_a_binding_that_cannot_be_built_is_a_note(scratch_build, capsys, status):
+    # a torch without CUDA libraries, or no C++ compiler
+    built = _build._build_layers()
+    assert built is not None
+    scratch_build.status = status
+    _touch(scratch_build.dir / "_layers.cpp")
+    assert _build._build_layers() is None
+    assert "does not build" in capsys.readouterr().err
+    import os
+    assert not os.path.exists(built)     # what was built from the older source is gone
+
+
+def _touch(path):
+    import os
+    import time
+    os.utime(path, (time.time() + 100,) * 2)
