@@ -104,9 +104,21 @@ def _build_layers(verbose: bool = False):
     src = os.path.join(PKG, "_layers.cpp")
     out = os.path.join(PKG, "_layers" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
     newest = max(os.path.getmtime(f) for f in [src, *glob.glob(os.path.join(INCLUDE, "*.h"))])
-    if os.path.exists(out) and os.path.getmtime(out) >= newest:
-        return out
     torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    # which torch it was built against (its C++ interface changes between versions)
+    try:
+        with open(os.path.join(torch_dir, "version.py")) as f:
+            torch_is = f"{torch_dir}\n{f.read()}"
+    except OSError:
+        torch_is = torch_dir
+    stamp = os.path.join(BUILD, os.path.basename(out) + ".torch")
+    try:
+        with open(stamp) as f:
+            same_torch = f.read() == torch_is
+    except OSError:
+        same_torch = False
+    if same_torch and os.path.exists(out) and os.path.getmtime(out) >= newest:
+        return out
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     cmd = [shutil.which("c++") or shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared",
            "-fPIC", "-Wall", "-I", sysconfig.get_paths()["include"], "-I", INCLUDE,
@@ -128,6 +140,8 @@ def _build_layers(verbose: bool = False):
                          f"against {torch_dir}; everything else does:\n{failed}\n")
         return None
     os.replace(out + ".tmp", out)
+    with open(stamp, "w") as f:
+        f.write(torch_is)
     if verbose:
         sys.stderr.write(f"built {out}\n")
     return out

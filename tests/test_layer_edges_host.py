@@ -128,6 +128,24 @@ def test_a_binding_that_cannot_be_built_is_a_note(scratch_build, capsys, status)
     assert not os.path.exists(built)     # what was built from the older source is gone
 
 
+def test_the_binding_is_rebuilt_for_another_torch(scratch_build, tmp_path, monkeypatch):
+    import importlib.util
+    import types
+    torch_dir = tmp_path / "torch"
+    torch_dir.mkdir()
+    (torch_dir / "version.py").write_text("__version__ = '1'\n")
+    monkeypatch.setattr(importlib.util, "find_spec",
+                        lambda name: types.SimpleNamespace(origin=str(torch_dir / "__init__.py")))
+    built = _build._build_layers()
+    assert len(scratch_build.commands) == 1
+    assert _build._build_layers() == built and len(scratch_build.commands) == 1
+    (torch_dir / "version.py").write_text("__version__ = '2'\n")
+    import os
+    os.utime(torch_dir / "version.py", (0, 0))      # an archive's old file times
+    assert _build._build_layers() == built and len(scratch_build.commands) == 2
+    assert _build._build_layers() == built and len(scratch_build.commands) == 2
+
+
 def _touch(path):
     import os
     import time
