@@ -254,6 +254,9 @@ PyObject *linear(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
                               Y.ld, Z.p, Z.ld, s.p, s.bytes, current_stream(x)));
         PyObject *py;
         if (present(a[9])) {
+            // written in place: autograd then sees that what it saved has changed
+            const at::Tensor &out = tensor(a[9], "out");
+            if (!out.is_inference()) out.unsafeGetTensorImpl()->bump_version();
             py = a[9];
             Py_INCREF(py);
         } else {

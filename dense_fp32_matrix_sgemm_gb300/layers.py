@@ -7,7 +7,10 @@ scale each), its gradients ``add_rmsnorm_backward``, and ``quantize_rows``.
 Each call checks its tensors, allocates the outputs with torch's allocator and
 enqueues the library's kernels (the C ABI of include/sgemm_gb300_layers.h) on
 ``stream`` (default: torch's current stream; outputs and scratch memory are
-allocated for the stream the call runs on).  Nothing synchronises.  Matrices
+allocated for the stream the call runs on).  Nothing synchronises.  No gradient is
+recorded: results of tensors that require one do not (the ``_backward`` functions
+are the gradients, for a torch.autograd.Function or a training loop of one's own,
+as examples/feed_forward.py has).  Matrices
 are 2-D with a unit column stride and any row stride; a weight may also be the
 transposed view of one.  All tensors of a call, its workspace and its stream are
 of one device, and the call runs there whatever device is current.  The checks and the call itself are in ``_layers``, a
@@ -59,7 +62,8 @@ def linear(x, weight, bias=None, *, activation="none", residual=None, x_scale=No
     float32 (FP32 accuracy), bfloat16, float16, or float8_e4m3fn with
     ``x_scale`` (M) and ``w_scale`` (N) float32 (as ``add_rmsnorm`` and
     ``quantize_rows`` make them) and a bfloat16 (default) or float16 result.
-    bias, residual and out have the result's type; out may be residual.
+    bias, residual and out have the result's type; out may be residual and overlaps
+    nothing else that the call reads.
     ``save_preact=True`` returns (y, z) with z the rounded pre-activation that
     ``linear_backward`` takes.  ``workspace``: a CUDA uint8 tensor, used where
     the call needs scratch memory and it is large enough."""

@@ -220,3 +220,30 @@ def test_norm_gradient_of_constant_rows_is_zero(t):
         dx, dw = sg.add_rmsnorm_backward(one, one, torch.ones(5, device="cuda"), one[0].contiguous())
         assert not dx.any(), d
         assert torch.equal(dw, 5 * one[0]), d
+
+
+# ------------------------------------------------------------------ torch
+
+
+def test_out_counts_as_changed_in_place():
+    x, w = torch.ones(4, 8, device="cuda"), torch.ones(16, 8, device="cuda")
+    r = torch.ones(4, 16, device="cuda")
+    before = r._version
+    sg.linear(x, w, residual=r, out=r)
+    assert r._version == before + 1
+    # so a product's backward that saved it is refused, as after any change in place
+    p = torch.ones(16, 4, device="cuda", requires_grad=True)
+    y = (r @ p).sum()
+    sg.linear(x, w, out=r)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+    with torch.inference_mode():
+        o = torch.empty(4, 16, device="cuda")
+        assert torch.equal(sg.linear(x, w, out=o), torch.full((4, 16), 8.0, device="cuda"))
+
+
+def test_results_record_no_gradient():
+    x = torch.ones(4, 8, device="cuda", requires_grad=True)
+    w = torch.ones(16, 8, device="cuda", requires_grad=True)
+    assert not sg.linear(x, w).requires_grad
+    assert not any(t.requires_grad for t in sg.add_rmsnorm(x, w[0].detach(), x))
