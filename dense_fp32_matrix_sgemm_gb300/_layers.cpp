@@ -30,6 +30,7 @@ decltype(&sgemm_add_rmsnorm_backward) f_add_rmsnorm_backward;
 decltype(&sgemm_add_rmsnorm_backward_workspace_size) f_add_rmsnorm_backward_ws;
 decltype(&sgemm_quantize_rows) f_quantize_rows;
 PyObject *py_raise;   // called with a nonzero status; raises
+PyObject *py_out_of_memory;   // torch.OutOfMemoryError
 
 // An exception of the C++ side that names the Python type to raise.
 struct Refusal {
@@ -196,6 +197,8 @@ PyObject *guarded(F body) {
     } catch (const Refusal &r) {
         PyErr_SetString(r.type, r.what.c_str());
     } catch (const Raised &) {
+    } catch (const c10::OutOfMemoryError &e) {   // the type that torch's own calls raise
+        PyErr_SetString(py_out_of_memory, e.what_without_backtrace());
     } catch (const std::exception &e) {
         PyErr_SetString(PyExc_RuntimeError, e.what());
     } catch (...) {
@@ -399,11 +402,13 @@ PyObject *check_device(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
     });
 }
 
-// bind({name: address}, raise): the loaded library's entry points, and what
-// to call with a nonzero status.
+// bind({name: address}, raise, out_of_memory): the loaded library's entry points,
+// what to call with a nonzero status, and the type to raise when torch's allocator
+// has no memory left.
 PyObject *bind(PyObject *, PyObject *args) {
-    PyObject *table, *raise;
-    if (!PyArg_ParseTuple(args, "O!O", &PyDict_Type, &table, &raise)) return nullptr;
+    PyObject *table, *raise, *out_of_memory;
+    if (!PyArg_ParseTuple(args, "O!OO", &PyDict_Type, &table, &raise, &out_of_memory))
+        return nullptr;
 #define BIND(name, f)                                                                           \
     do {                                                                                       \
         PyObject *v = PyDict_GetItemString(table, #name);                                      \
@@ -425,7 +430,9 @@ PyObject *bind(PyObject *, PyObject *args) {
     BIND(sgemm_quantize_rows, f_quantize_rows);
 #undef BIND
     Py_INCREF(raise);
+    Py_INCREF(out_of_memory);
     py_raise = raise;
+    py_out_of_memory = out_of_memory;
     return none();
 }
 

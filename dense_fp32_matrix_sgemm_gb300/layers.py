@@ -32,7 +32,7 @@ except ImportError as e:
         f"the torch binding of the layer operators is not built or does not load ({e}); run "
         "__graft_entry__.build() or python -m dense_fp32_matrix_sgemm_gb300._build") from e
 _layers.bind({name: ctypes.cast(getattr(_lib, name), ctypes.c_void_p).value
-              for name in _sg.LAYER_ENTRIES}, _sg._check)
+              for name in _sg.LAYER_ENTRIES}, _sg._check, torch.OutOfMemoryError)
 
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_erf": 3, "silu": 4}
 

@@ -247,3 +247,16 @@ def test_results_record_no_gradient():
     w = torch.ones(16, 8, device="cuda", requires_grad=True)
     assert not sg.linear(x, w).requires_grad
     assert not any(t.requires_grad for t in sg.add_rmsnorm(x, w[0].detach(), x))
+
+
+def test_memory_running_out_is_torchs_error():
+    # (refused by torch's allocator at the limit set here, before the device is asked)
+    x, w = (torch.ones(1 << 15, 1, device="cuda") for _ in range(2))
+    torch.cuda.empty_cache()
+    torch.cuda.set_per_process_memory_fraction(0.01)
+    try:
+        with pytest.raises(torch.OutOfMemoryError):
+            sg.linear(x, w)      # 4 GB
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    assert torch.equal(sg.linear(x[:4], w[:8]), torch.ones(4, 8, device="cuda"))
