@@ -185,7 +185,12 @@ PyObject *none() {
     return Py_None;
 }
 
-bool flag(PyObject *o) { return o == Py_True || (o != Py_False && PyObject_IsTrue(o) == 1); }
+bool flag(PyObject *o) {
+    if (o == Py_True || o == Py_False) return o == Py_True;
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) throw Raised{};   // an object without a truth value
+    return v == 1;
+}
 
 // Runs `body`, turning C++ exceptions into Python ones.
 template <class F>

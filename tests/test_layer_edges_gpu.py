@@ -260,3 +260,18 @@ def test_memory_running_out_is_torchs_error():
     finally:
         torch.cuda.set_per_process_memory_fraction(1.0)
     assert torch.equal(sg.linear(x[:4], w[:8]), torch.ones(4, 8, device="cuda"))
+
+
+def test_an_argument_without_a_truth_value_is_its_own_error():
+    x, w = torch.ones(4, 8, device="cuda"), torch.ones(16, 8, device="cuda")
+
+    class Undecided:
+        def __bool__(self):
+            raise ValueError("neither")
+
+    for call in (lambda u: sg.linear(x, w, save_preact=u), lambda u: sg.add_rmsnorm(x, w[0], quantize=u),
+                 lambda u: sg.linear_backward(x @ w.t(), x, w, need_db=u),
+                 lambda u: sg.add_rmsnorm_backward(x, x, x[:, 0].contiguous(), w[0], need_dweight=u)):
+        with pytest.raises(ValueError, match="neither"):
+            call(Undecided())
+    assert sg.linear(x, w, save_preact=1)[1].shape == (4, 16)
