@@ -275,3 +275,80 @@ def test_an_argument_without_a_truth_value_is_its_own_error():
         with pytest.raises(ValueError, match="neither"):
             call(Undecided())
     assert sg.linear(x, w, save_preact=1)[1].shape == (4, 16)
+
+
+# ------------------------------------------------------------------ special values
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("d", [256, 257, 40000])
+def test_quantize_rows_special_rows(d, t):
+    # a = max |x|: a NaN makes scale and codes NaN; an infinity makes the scale
+    # infinite, 448 / a 0, its own code NaN (inf 0) and the others 0
+    x = torch.randn(6, d, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda").to(TYPES[t])
+    clean_q, clean_scale = sg.quantize_rows(x)
+    x[1, d - 1], x[2, 0], x[3, 5] = float("nan"), float("inf"), -float("inf")
+    q, scale = sg.quantize_rows(x)
+    f = q.float()
+    assert torch.isnan(scale[1]) and torch.isnan(f[1]).all()
+    for row, col in ((2, 0), (3, 5)):
+        assert torch.isinf(scale[row]) and scale[row] > 0
+        assert torch.isnan(f[row, col])
+        f[row, col] = 0
+        assert not f[row].any()
+    for row in (0, 4, 5):
+        assert torch.equal(q[row].view(torch.uint8), clean_q[row].view(torch.uint8))
+        assert torch.equal(scale[row], clean_scale[row])
+
+
+@pytest.mark.parametrize("w_kn", [False, True])
+@pytest.mark.parametrize("m", [1, 8, 16, 17, 200])
+def test_linear_f32_infinities(m, w_kn):
+    """An infinity in X reaches its own row, one in W its own feature, all of their
+    values non-finite and nobody else's changed; up to 16 rows (FP32 FMAs) they are
+    the formula's infinities, above (differences of infinities) they may be NaN."""
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x, w = torch.randn(m, 96, generator=g, device="cuda"), torch.randn(130, 96, generator=g, device="cuda")
+    make = (lambda w: w.t().contiguous().t()) if w_kn else (lambda w: w)
+    clean = sg.linear(x, make(w))
+    bad = x.clone()
+    bad[m // 2, 7] = float("inf")
+    y = sg.linear(bad, make(w))
+    rest = torch.arange(m, device="cuda") != m // 2
+    assert torch.equal(y[rest], clean[rest]) and not torch.isfinite(y[m // 2]).any()
+    if m <= 16:
+        assert torch.equal(y[m // 2], torch.where(w[:, 7] > 0, float("inf"), -float("inf")))
+    bad = w.clone()
+    bad[50, 3] = -float("inf")
+    y = sg.linear(x, make(bad))
+    rest = torch.arange(130, device="cuda") != 50
+    assert torch.equal(y[:, rest], clean[:, rest]) and not torch.isfinite(y[:, 50]).any()
+    if m <= 16:
+        assert torch.equal(y[:, 50], torch.where(x[:, 3] > 0, -float("inf"), float("inf")))
+
+
+@pytest.mark.parametrize("m", [1, 2, 3, 40, 300])
+@pytest.mark.parametrize("k", [200, 201, 208])
+@pytest.mark.parametrize("pad,offset", [(0, 0), (3, 1), (8, 0), (16, 8)])
+def test_linear_e4m3_to_f16_of_any_alignment(pad, offset, k, m):
+    """Codes and scales whose products and sums are exact in fp32 (codes of -2 .. 2,
+    scales of powers of two): one rounding to f16, the same bits as torch's."""
+    g = torch.Generator(device="cuda").manual_seed(k + m)
+    n = 131
+
+    def strided(t):
+        buf = torch.full((t.shape[0] * (t.shape[1] + pad) + offset,), 0x7f if t.element_size() == 1 else 0,
+                         dtype=torch.uint8 if t.element_size() == 1 else t.dtype, device="cuda")
+        v = buf[offset:].view(t.shape[0], t.shape[1] + pad)[:, :t.shape[1]]
+        v.copy_(t.view(torch.uint8) if t.element_size() == 1 else t)
+        return v.view(t.dtype)
+
+    x, w = (torch.randint(-2, 3, s, generator=g, device="cuda").float().to(torch.float8_e4m3fn)
+            for s in ((m, k), (n, k)))
+    xs, ws = (2.0 ** torch.randint(-3, 2, (s,), generator=g, device="cuda").float() for s in (m, n))
+    r = strided(torch.randint(-8, 9, (m, n), generator=g, device="cuda").half())
+    out = strided(torch.zeros(m, n, dtype=torch.float16, device="cuda"))
+    y = sg.linear(strided(x), strided(w), activation="relu", residual=r, x_scale=xs, w_scale=ws,
+                  out_dtype=torch.float16, out=out)
+    z = (x.double() @ w.double().t()) * xs.double()[:, None] * ws.double()
+    assert torch.equal(y, (z.clamp(min=0) + r.double()).float().half())
