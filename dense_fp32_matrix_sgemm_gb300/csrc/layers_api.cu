@@ -78,12 +78,18 @@ int check_workspace(void *ws, uint64_t have, size_t need) {
 }
 
 // Whether a product of M rows runs on the CUDA cores (linear_rows.cu), in one
-// pass over the weights, or on the tensor cores.  Measured with 4096 x 4096
-// weights out of L2, in us, CUDA cores / tensor cores: bf16 1 row 7.9 / 11, 2 rows
-// 8.4 / 11, 4 rows 15.7 / 11; bf16 stored K x N 1 row 24 / 11; e4m3 1 row 5.9 / 8.2,
-// 2 rows 9.0 / 8.2; with 1024 x 4096 weights, where launch and set-up count, bf16 4
-// rows 5.9 / 7.4, e4m3 2 rows 3.9 / 5.6; f32, whose planes the tensor cores need
-// written first, 8 rows 25 / 48, 16 rows 45 / 48.
+// pass over the weights, or on the tensor cores.  Measured in a graph with the
+// weights out of L2, in us, CUDA cores / tensor cores:
+//   weights N x K    512x1024   1024x2048  1024x4096  1536x4096  2048x4096  4096x4096
+//   bf16, 1 row      2.1 / 4.5  3.0 / 5.8  3.8 / 7.1  5.4 / 7.8  5.2 / 8.0  8.2 / 11.0
+//   2 rows           2.2 / 4.4  3.0 / 5.7  3.9 / 7.1  6.0 / 7.8  5.4 / 8.0  8.4 / 11.2
+//   4 rows           2.5 / 4.5  4.3 / 5.9  6.4 / 7.1  6.9 / 7.8  9.3 / 8.1  15.0 / 11.2
+//   e4m3, 1 row      2.1 / 4.0  2.9 / 4.8  3.3 / 5.8  5.2 / 6.2  4.2 / 6.6  5.8 / 8.1
+//   2 rows           2.2 / 4.0  2.8 / 4.8  4.4 / 5.9  5.4 / 6.3  6.3 / 6.7  9.0 / 8.3
+// (4096 x 1024 much as 1024 x 4096.)  For the rows that the rule turns on, the sides
+// come within 16 % of one another between 2^22 and 2^23 weights.  bf16 stored K x N,
+// 4096 x 4096, 1 row: 24 / 11.  f32, whose planes the tensor cores need written
+// first: 8 rows 25 / 48, 16 rows 45 / 48.
 bool on_cuda_cores(int type, int64_t M, int64_t N, int64_t K, int transW) {
     if (K == 0) return true;
     if (type == SGEMM_F32) return M <= 16;

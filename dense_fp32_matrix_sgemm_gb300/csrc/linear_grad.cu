@@ -33,8 +33,9 @@ struct DzArgs {
 // products read is written as their planes (6 bytes an element instead of 4
 // written, 4 read and 6 written).  Four CTAs an SM, which the grid counts on
 // (without the bound 2 or 3 fit: 4096 x 8192 bf16, GELU, the column sums alone 37.3
-// us, so 33.8, and 28.8 with the gradient's constants multiplied out; with dZ
-// written 33, 201 MB at 6.0 TB/s).
+// us, so 33.8, and 28.5 with the gradient's constants multiplied out; 30.8 with
+// slopes that are right to the ends of z's range; with dZ written 35, 201 MB at
+// 5.7 TB/s).
 template <class T, int W>
 __global__ void __launch_bounds__(kThreads, 4) dz_kernel(const DzArgs a) {
     __shared__ float red[kRowLanes][32 * W];

@@ -7,9 +7,11 @@
 // the same, and FP32 FMAs (packed in pairs) keep up for the few rows that the
 // launcher sends here.
 //
-// Measured with weights out of L2: 4096 x 4096 bf16, one row 7.8 us (33.6 MB, 4.3
-// TB/s, launch included); 8192 x 4096 under a profiler DRAM runs at 52 %, so the
-// start of the loads and the launch, not their number, are what is left.
+// Measured in a graph with weights out of L2, one row, K = 4096, 1024 to 32768
+// features: bf16 3.1 us and the bytes at 6.5 TB/s (4096: 8.2 us, 4.1 TB/s; 8192: 13.7;
+// 32768: 43.3, 6.2 TB/s), so a launch's start is what is left there; e4m3 2.5 us and
+// the bytes at 5.3 TB/s (4096: 5.7; 32768: 27.8, 4.8 TB/s), where the codes'
+// conversion costs instructions too.
 // Weights stored N x K (dot form): a warp takes two or four output features and
 // walks K, each lane with 16-byte pieces of their rows of W and of the MR rows of
 // X (X stays in L1).  Where the features alone would not fill the SMs, K is

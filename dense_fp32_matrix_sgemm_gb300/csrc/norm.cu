@@ -274,8 +274,8 @@ __global__ void __launch_bounds__(MAXT) grad_kernel(const GradArgs a) {
         nr = live ? a.rstd[row] : 0.f;
     };
     // where they do not, the next row is brought to L2 in the meantime, a lane a
-    // 128-byte line (2048 x 16384 bf16: 88 -> 73 us), and dS is read only when dX is
-    // formed, which leaves fewer registers to spill (70)
+    // 128-byte line (2048 x 16384 bf16 without dS: 88 -> 73 us), and dS is read only
+    // when dX is formed, which leaves fewer registers to spill (70; now 66, with dS 75)
     auto prefetch_row = [&](int64_t row) {
         constexpr int LANES = W > 1 ? 128 / (W * (int)sizeof(T)) : 32;
         if (row >= a.rows || threadIdx.x % LANES != 0) return;

@@ -59,7 +59,8 @@ def linear(x, weight, bias=None, *, activation="none", residual=None, x_scale=No
            out_dtype=None, save_preact=False, out=None, workspace=None, stream=None):
     """act(x @ weight.T + bias) + residual, x (M, K), weight (N, K).
 
-    float32 (FP32 accuracy), bfloat16, float16, or float8_e4m3fn with
+    float32 (FP32 accuracy; beyond 16 rows an infinity in x or weight may give NaN
+    where the sum is infinite), bfloat16, float16, or float8_e4m3fn with
     ``x_scale`` (M) and ``w_scale`` (N) float32 (as ``add_rmsnorm`` and
     ``quantize_rows`` make them) and a bfloat16 (default) or float16 result.
     bias, residual and out have the result's type; out may be residual and overlaps
@@ -99,7 +100,8 @@ def add_rmsnorm(x, weight, residual=None, *, eps=1e-6, quantize=False, stream=No
     Returns (y, s, rstd), or with ``quantize`` (q, scale, s, rstd): q
     float8_e4m3fn and scale float32 a row, y about q * scale[:, None].  Without
     a residual s is x itself.  x (rows, D) float32, bfloat16 or float16; rstd
-    float32, for ``add_rmsnorm_backward``."""
+    float32, for ``add_rmsnorm_backward``.  Rows of no elements have the statistics
+    of a row of zeros."""
     if stream is not None:
         with _on(stream, x):
             return add_rmsnorm(x, weight, residual, eps=eps, quantize=quantize)
