@@ -61,8 +61,9 @@ typedef enum {
  *   preact      NULL, or M x N values (ldp >= N) that receive z rounded to
  *               out_dtype (for sgemm_linear_backward); it overlaps nothing.
  * SGEMM_E4M3 takes transW == 1 only.  f32 products are formed on the tensor
- * cores from operands written as three bf16 terms each (FP32 accuracy), or by
- * FP32 FMAs for up to 16 rows; 16- and 8-bit products are exact and summed in
+ * cores from operands written as three bf16 terms each (FP32 accuracy; elements
+ * below 2^-110 are held to 2^-134, half a bf16's smallest step), or by FP32 FMAs
+ * for up to 16 rows; 16- and 8-bit products are exact and summed in
  * fp32.  A NaN or infinity in X makes its own row's values non-finite, one in W
  * its own feature's; in f32 on the tensor cores an infinity gives NaN where the
  * formula's sum would be infinite (its terms are formed from the difference of

@@ -352,3 +352,23 @@ def test_linear_e4m3_to_f16_of_any_alignment(pad, offset, k, m):
                   out_dtype=torch.float16, out=out)
     z = (x.double() @ w.double().t()) * xs.double()[:, None] * ws.double()
     assert torch.equal(y, (z.clamp(min=0) + r.double()).float().half())
+
+
+@pytest.mark.parametrize("e", [-108, -113, -119, -125])
+@pytest.mark.parametrize("m", [16, 64])
+def test_linear_f32_of_tiny_elements(m, e):
+    """Elements of 2^e, normal f32 numbers.  By FP32 FMAs, K = 256 updates of half a
+    unit of the sum of sizes S; on the tensor cores 64 2^-23 / 4 + 2^-19 of S as for
+    any f32 product, and every tiny element to 2^-134."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(m, 256, generator=g, device="cuda").clamp(-4, 4)
+    w = torch.randn(130, 256, generator=g, device="cuda")
+    tiny = torch.ldexp(x, torch.tensor(e, device="cuda"))
+    want, S = tiny.double() @ w.double().t(), tiny.double().abs() @ w.double().abs().t()
+    tol = (256 * 2.0 ** -24 if m <= 16 else 2.0 ** -19 + (64 + 32) * 2.0 ** -25) * S
+    if m > 16:
+        tol = tol + 2.0 ** -134 * w.double().abs().sum(1)
+    assert ((sg.linear(tiny, w).double() - want).abs() <= tol + 2.0 ** -149 * 256).all()
+    if m > 16:      # the same of a weight
+        y = sg.linear(w, tiny).double()
+        assert ((y - want.t()).abs() <= tol.t() + 2.0 ** -149 * 256).all()
