@@ -33,7 +33,11 @@ __all__ = ["SgemmError", "SgemmUnavailable", "load_library", "library_path",
            "set_tf32x3_chunk_k", "marshalling", "sgemm_linear", "sgemm_linear_backward",
            "sgemm_add_rmsnorm", "sgemm_add_rmsnorm_backward", "sgemm_quantize_rows",
            "linear_workspace_size", "linear_backward_workspace_size",
-           "add_rmsnorm_backward_workspace_size"]
+           "add_rmsnorm_backward_workspace_size", "sgemm_gated_linear",
+           "sgemm_gated_linear_backward", "sgemm_add_layernorm", "sgemm_add_layernorm_backward",
+           "sgemm_clip_grad_norm", "gated_linear_workspace_size",
+           "gated_linear_backward_workspace_size", "add_layernorm_backward_workspace_size",
+           "clip_grad_norm_workspace_size"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "libsgemm_gb300.so")
@@ -108,6 +112,24 @@ SIGNATURES = {
                                           _i64, _vp, _i64, _vp, _vp, _u64, _vp]),
     "sgemm_add_rmsnorm_backward_workspace_size": (_u64, [_int, _i64, _i64]),
     "sgemm_quantize_rows": (_int, [_int, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp]),
+    "sgemm_gated_linear": (_int, [_int, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _vp, _i64,
+                                  _vp, _int, _vp, _vp, _int, _int, _vp, _i64, _vp, _i64, _vp, _i64,
+                                  _vp, _u64, _vp]),
+    "sgemm_gated_linear_workspace_size": (_u64, [_int, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp,
+                                                 _i64, _int]),
+    "sgemm_gated_linear_backward": (_int, [_int, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64,
+                                           _int, _vp, _i64, _vp, _i64, _vp, _i64, _int, _vp, _i64,
+                                           _vp, _i64, _vp, _i64, _vp, _vp, _vp, _u64, _vp]),
+    "sgemm_gated_linear_backward_workspace_size": (_u64, [_int, _i64, _i64, _i64, _vp, _i64, _vp,
+                                                          _i64, _vp, _i64, _int]),
+    "sgemm_add_layernorm": (_int, [_int, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, ctypes.c_float,
+                                   _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp]),
+    "sgemm_add_layernorm_backward": (_int, [_int, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp,
+                                            _vp, _i64, _vp, _i64, _vp, _vp, _vp, _u64, _vp]),
+    "sgemm_add_layernorm_backward_workspace_size": (_u64, [_int, _i64, _i64]),
+    "sgemm_clip_grad_norm": (_int, [_i64, _vp, _vp, _vp, _vp, ctypes.c_float, ctypes.c_float, _vp,
+                                    _vp, _u64, _vp]),
+    "sgemm_clip_grad_norm_workspace_size": (_u64, [_i64, _vp, _vp]),
 }
 
 
@@ -139,6 +161,13 @@ LAYER_ENTRIES = ("sgemm_linear", "sgemm_linear_workspace_size", "sgemm_linear_ba
                  "sgemm_linear_backward_workspace_size", "sgemm_add_rmsnorm",
                  "sgemm_add_rmsnorm_backward", "sgemm_add_rmsnorm_backward_workspace_size",
                  "sgemm_quantize_rows")
+# The gated block's entries (include/sgemm_gb300_block.h): through ctypes here; torch tensors
+# reach them through the _layers extension.
+BLOCK_ENTRIES = ("sgemm_gated_linear", "sgemm_gated_linear_workspace_size",
+                 "sgemm_gated_linear_backward", "sgemm_gated_linear_backward_workspace_size",
+                 "sgemm_add_layernorm", "sgemm_add_layernorm_backward",
+                 "sgemm_add_layernorm_backward_workspace_size", "sgemm_clip_grad_norm",
+                 "sgemm_clip_grad_norm_workspace_size")
 
 
 def library_path() -> str:
@@ -574,9 +603,92 @@ def sgemm_quantize_rows(dtype, rows, D, X, ldx, Q, ldq, scale, stream=0, *, chec
     return _check(st) if check else st
 
 
+def sgemm_gated_linear(dtype, M, N, K, X, ldx, x_scale, Wg, ldwg, gate_scale, Wu, ldwu, up_scale,
+                       transW, bias_gate, bias_up, activation, out_dtype, H, ldh, preact_gate=0,
+                       ldpg=0, preact_up=0, ldpu=0, workspace=0, workspace_bytes=0, stream=0, *,
+                       check=True):
+    """H = act(X op(Wg) + bias_gate) (X op(Wu) + bias_up) (see include/sgemm_gb300_block.h)."""
+    st = load_library().sgemm_gated_linear(
+        dtype, M, N, K, X, ldx, x_scale, Wg, ldwg, gate_scale, Wu, ldwu, up_scale, transW,
+        bias_gate, bias_up, activation, out_dtype, H, ldh, preact_gate, ldpg, preact_up, ldpu,
+        workspace, workspace_bytes, stream)
+    return _check(st) if check else st
+
+
+def gated_linear_workspace_size(dtype, M, N, K, X, ldx, Wg, ldwg, Wu, ldwu, transW) -> int:
+    return load_library().sgemm_gated_linear_workspace_size(dtype, M, N, K, X, ldx, Wg, ldwg, Wu,
+                                                            ldwu, transW)
+
+
+def sgemm_gated_linear_backward(dtype, M, N, K, dH, lddh, Zg, ldzg, Zu, ldzu, activation, X, ldx,
+                                Wg, ldwg, Wu, ldwu, transW, dX, lddx, dWg, lddwg, dWu, lddwu,
+                                db_gate, db_up, workspace=0, workspace_bytes=0, stream=0, *,
+                                check=True):
+    """Gradients of sgemm_gated_linear (see include/sgemm_gb300_block.h)."""
+    st = load_library().sgemm_gated_linear_backward(
+        dtype, M, N, K, dH, lddh, Zg, ldzg, Zu, ldzu, activation, X, ldx, Wg, ldwg, Wu, ldwu,
+        transW, dX, lddx, dWg, lddwg, dWu, lddwu, db_gate, db_up, workspace, workspace_bytes,
+        stream)
+    return _check(st) if check else st
+
+
+def gated_linear_backward_workspace_size(dtype, M, N, K, X, ldx, Wg, ldwg, Wu, ldwu,
+                                         transW) -> int:
+    return load_library().sgemm_gated_linear_backward_workspace_size(dtype, M, N, K, X, ldx, Wg,
+                                                                     ldwg, Wu, ldwu, transW)
+
+
+def sgemm_add_layernorm(dtype, rows, D, X, ldx, residual, ldr, weight, bias, eps, S, lds, Y, ldy,
+                        q_scale=0, mean=0, rstd=0, stream=0, *, check=True):
+    """Residual addition and layer norm (see include/sgemm_gb300_block.h)."""
+    st = load_library().sgemm_add_layernorm(dtype, rows, D, X, ldx, residual, ldr, weight, bias,
+                                            eps, S, lds, Y, ldy, q_scale, mean, rstd, stream)
+    return _check(st) if check else st
+
+
+def sgemm_add_layernorm_backward(dtype, rows, D, dY, lddy, S, lds, mean, rstd, weight, dS, ldds, dX,
+                                 lddx, dweight, dbias, workspace=0, workspace_bytes=0, stream=0, *,
+                                 check=True):
+    """Gradients of sgemm_add_layernorm (see include/sgemm_gb300_block.h)."""
+    st = load_library().sgemm_add_layernorm_backward(
+        dtype, rows, D, dY, lddy, S, lds, mean, rstd, weight, dS, ldds, dX, lddx, dweight, dbias,
+        workspace, workspace_bytes, stream)
+    return _check(st) if check else st
+
+
+def add_layernorm_backward_workspace_size(dtype, rows, D) -> int:
+    return load_library().sgemm_add_layernorm_backward_workspace_size(dtype, rows, D)
+
+
+def _host_arrays(dtypes, sizes, *pointers):
+    """The C arrays of a list of tensors (kept alive by the caller); None stays a null pointer."""
+    n = len(sizes)
+    if len(dtypes) != n or any(p is not None and len(p) != n for p in pointers):
+        raise ValueError("dtypes, sizes and pointers must be of one length")
+    return ((_int * n)(*dtypes), (_i64 * n)(*sizes),
+            *(None if p is None else (_vp * n)(*p) for p in pointers))
+
+
+def sgemm_clip_grad_norm(dtypes, sizes, X, Y, max_norm, eps, norm, workspace=0, workspace_bytes=0,
+                         stream=0, *, check=True):
+    """Common norm of a list of tensors, and the tensors scaled to at most max_norm (see
+    include/sgemm_gb300_block.h).  dtypes, sizes, X and Y are sequences (Y may be None)."""
+    t, n, x, y = _host_arrays(dtypes, sizes, X, Y)
+    st = load_library().sgemm_clip_grad_norm(len(sizes), t, n, x, y, max_norm, eps, norm, workspace,
+                                             workspace_bytes, stream)
+    return _check(st) if check else st
+
+
+def clip_grad_norm_workspace_size(dtypes, sizes) -> int:
+    return load_library().sgemm_clip_grad_norm_workspace_size(len(sizes),
+                                                              *_host_arrays(dtypes, sizes))
+
+
 # The torch-level operators (layers.py), imported at first use and not in __all__:
 # the package itself does not need torch.
-_LAYERS = ("linear", "linear_backward", "add_rmsnorm", "add_rmsnorm_backward", "quantize_rows")
+_LAYERS = ("linear", "linear_backward", "add_rmsnorm", "add_rmsnorm_backward", "quantize_rows",
+           "gated_linear", "gated_linear_backward", "add_layernorm", "add_layernorm_backward",
+           "grad_norm", "clip_grad_norm")
 
 
 def __getattr__(name):

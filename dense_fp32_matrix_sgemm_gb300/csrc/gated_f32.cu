@@ -1,0 +1,133 @@
+// The gated layer and the sum of two products in f32 on the bf16 tensor cores:
+// linear_f32_body (linear_f32_kernel.cuh) in its two other forms, as gated_tc.cu has them
+// for the 16- and 8-bit types.  The running sums of a gate and of its factor are in the
+// same lane's registers; both leave through the warp's staging block 16 outputs at a
+// time, a column a lane, as unrolled activations of whole rows would be fetched longer
+// than they run.
+#include <cstdint>
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "linear_f32_kernel.cuh"
+
+namespace sgemm {
+namespace ltc {
+namespace f32 {
+
+template <int CTAS, int BN, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, 1)
+gated_f32_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmG,
+                 const __grid_constant__ CUtensorMap tmU,
+                 const __grid_constant__ Params<GatedEpi> p) {
+    linear_f32_body<kGated, CTAS, BN, SPLIT>({&tmX, &tmX, &tmG, &tmU, &tmX, &tmX, &tmX}, p);
+}
+
+template <int CTAS, int BN, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, 1)
+sum_f32_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA2,
+               const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmB2,
+               const __grid_constant__ CUtensorMap tmY,
+               const __grid_constant__ Params<LayerEpi> p) {
+    linear_f32_body<kSum, CTAS, BN, SPLIT>({&tmA, &tmA2, &tmB, &tmB2, &tmY, &tmY, &tmY}, p);
+}
+
+template <int CTAS, int BN, bool SPLIT>
+cudaError_t launch_gated(const F32Planes &X, const F32Planes &Wg, const F32Planes &Wu, int K,
+                         const GatedEpi &epi, const Piece &piece, int chain, cudaStream_t s) {
+    using S = Shape<CTAS, BN, SPLIT>;
+    constexpr int OUT = BN / 2;
+    static PerContext<bool> configured;
+    bool done = false;
+    cudaError_t e;
+    if (!configured.get(current_context_id(), done)) {
+        e = cudaFuncSetAttribute(gated_f32_kernel<CTAS, BN, SPLIT>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+        if (e != cudaSuccess) return e;
+        configured.put(current_context_id(), true);
+    }
+    if (OUT < 64 && !Wg.kmajor) return cudaErrorInvalidValue;
+    Params<GatedEpi> p;
+    p.epi = epi;
+    const int a_rows = fill_params<CTAS, BN>(p, epi.M, 2 * epi.N, K, X.kmajor, Wg.kmajor, piece,
+                                             chain);
+    CUtensorMap tmX, tmG, tmU;
+    if (!plane_map(&tmX, X.planes, X.rows, X.cols, X.kmajor ? a_rows : 64) ||
+        !plane_map(&tmG, Wg.planes, Wg.rows, Wg.cols, Wg.kmajor ? OUT : 64) ||
+        !plane_map(&tmU, Wu.planes, Wu.rows, Wu.cols, Wu.kmajor ? OUT : 64))
+        return cudaErrorInvalidValue;
+    Config c(ctas_of<CTAS, SPLIT>(piece), S::SMEM, SPLIT ? CTAS * piece.parts : CTAS, s);
+    return cudaLaunchKernelEx(&c.cfg, gated_f32_kernel<CTAS, BN, SPLIT>, tmX, tmG, tmU, p);
+}
+
+template <int CTAS, int BN, bool SPLIT>
+cudaError_t launch_sum(const F32Planes (&A)[2], const F32Planes (&B)[2], int K, const LayerEpi &epi,
+                       const Piece &piece, int chain, cudaStream_t s) {
+    using S = Shape<CTAS, BN, SPLIT>;
+    static PerContext<bool> configured;
+    bool done = false;
+    cudaError_t e;
+    if (!configured.get(current_context_id(), done)) {
+        e = cudaFuncSetAttribute(sum_f32_kernel<CTAS, BN, SPLIT>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+        if (e != cudaSuccess) return e;
+        configured.put(current_context_id(), true);
+    }
+    Params<LayerEpi> p;
+    p.epi = epi;
+    const int a_rows = fill_params<CTAS, BN>(p, epi.M, epi.N, K, A[0].kmajor, B[0].kmajor, piece,
+                                             chain);
+    p.kblocks = 2 * p.kblocks1;
+    CUtensorMap tmA[2], tmB[2], tmY = {};
+    p.tma = !SPLIT && stores_by_tma(epi, &tmY);
+    for (int i = 0; i < 2; ++i)
+        if (!plane_map(&tmA[i], A[i].planes, A[i].rows, A[i].cols, A[i].kmajor ? a_rows : 64) ||
+            !plane_map(&tmB[i], B[i].planes, B[i].rows, B[i].cols, B[i].kmajor ? S::BROWS : 64))
+            return cudaErrorInvalidValue;
+    Config c(ctas_of<CTAS, SPLIT>(piece), S::SMEM, SPLIT ? CTAS * piece.parts : CTAS, s);
+    return cudaLaunchKernelEx(&c.cfg, sum_f32_kernel<CTAS, BN, SPLIT>, tmA[0], tmA[1], tmB[0],
+                              tmB[1], tmY, p);
+}
+
+// The shapes of weights stored K x N: no 64-wide tile (32 features of each weight).
+constexpr Costs<3> kByInput = {{{2, 256}, {2, 128}, {1, 128}}, {1.66, 0.89, 1.05}, {8.5, 8.0, 6.0},
+                               {5.0, 3.0, 3.0}};
+
+}  // namespace f32
+}  // namespace ltc
+
+cudaError_t launch_gated_f32(const F32Planes &X, const F32Planes &Wg, const F32Planes &Wu, int K,
+                             const GatedEpi &epi, cudaStream_t s) {
+    using namespace ltc;
+    Capacity cap;
+    cudaError_t e = capacity(cap);
+    if (e != cudaSuccess) return e;
+    const int kblocks = (K + f32::kBk - 1) / f32::kBk;
+    if (Wg.kmajor) {
+        const Plan plan = plan_tiles(epi.M, 2 * epi.N, kblocks, cap, f32::kCosts);
+        return run_plan(f32::kCosts, plan, 0, [&](auto w, auto split, const Piece &p, int at) {
+            constexpr TileShape t = f32::kCosts.shape[w()];
+            return f32::launch_gated<t.ctas, t.bn, split()>(X, Wg, Wu, K, epi, p, at, s);
+        });
+    }
+    const Plan plan = plan_tiles(epi.M, 2 * epi.N, kblocks, cap, f32::kByInput);
+    return run_plan(f32::kByInput, plan, 0, [&](auto w, auto split, const Piece &p, int at) {
+        constexpr TileShape t = f32::kByInput.shape[w()];
+        return f32::launch_gated<t.ctas, t.bn, split()>(X, Wg, Wu, K, epi, p, at, s);
+    });
+}
+
+cudaError_t launch_sum_f32(const F32Planes (&A)[2], const F32Planes (&B)[2], int K,
+                           const LayerEpi &epi, int chain, cudaStream_t s) {
+    using namespace ltc;
+    Capacity cap;
+    cudaError_t e = capacity(cap);
+    if (e != cudaSuccess) return e;
+    const Plan plan = plan_tiles(epi.M, epi.N, 2 * ((K + f32::kBk - 1) / f32::kBk), cap, f32::kCosts);
+    return run_plan(f32::kCosts, plan, chain, [&](auto w, auto split, const Piece &p, int at) {
+        constexpr TileShape t = f32::kCosts.shape[w()];
+        return f32::launch_sum<t.ctas, t.bn, split()>(A, B, K, epi, p, at, s);
+    });
+}
+
+}  // namespace sgemm

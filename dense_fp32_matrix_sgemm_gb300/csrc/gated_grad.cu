@@ -1,0 +1,209 @@
+// What the gated layer's gradients need around the products: from dH and the stored
+// pre-activations,
+//   dZg = dH Zu act'(Zg),   dZu = dH act(Zg),
+// with both bias gradients' column sums in the same pass, and the sum of two outputs'
+// partial rows.  HBM bounds both: three reads and two writes an element (f32: two times
+// three planes of 2 bytes written), each in 16-byte accesses.
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+#include "device_utils.cuh"
+#include "layer_math.cuh"
+#include "layers.h"
+
+namespace sgemm {
+namespace gated {
+
+constexpr int kThreads = 256;   // 32 column lanes x 8 row lanes
+constexpr int kRowLanes = 8;
+
+struct DzArgs {
+    const void *dH, *Zg, *Zu;
+    void *dZg, *dZu;
+    float *partial;
+    int64_t lddh, ldzg, ldzu, lddz;
+    int64_t plane;   // f32: three bf16 planes this many elements apart; 0: dZ itself
+    int M, N, act, rows_per_part;
+    int chain;
+};
+
+// CTA (x, y): columns [32 W x, ...) of rows [y rows_per_part, ...), as dz_kernel.
+template <class T, int W>
+__global__ void __launch_bounds__(kThreads, 3) gated_dz_kernel(const DzArgs a) {
+    __shared__ float red[kRowLanes][32 * W];
+    chain_begin(a.chain);
+    const int lane = threadIdx.x & 31, ty = threadIdx.x >> 5;
+    const int c = (int)(blockIdx.x * 32 + lane) * W;
+    const int r0 = (int)blockIdx.y * a.rows_per_part;
+    const int r1 = min(a.M, r0 + a.rows_per_part);
+    float sum[2][W];
+#pragma unroll
+    for (int j = 0; j < W; ++j) sum[0][j] = sum[1][j] = 0.f;
+    if (c < a.N) {
+        const T *dh = static_cast<const T *>(a.dH) + c;
+        const T *zg = static_cast<const T *>(a.Zg) + c;
+        const T *zu = static_cast<const T *>(a.Zu) + c;
+        auto store = [&](void *base, int row, const float (&x)[W]) {
+            if constexpr (sizeof(T) == 4) {
+                if (a.plane != 0) {
+                    put_planes<W>(static_cast<__nv_bfloat16 *>(base) + row * a.lddz + c, a.plane, x);
+                    return;
+                }
+            }
+            put<T, W>(static_cast<T *>(base) + row * a.lddz + c, x);
+        };
+        constexpr int U = 2;   // rows in flight
+        for (int r = r0 + ty; r < r1; r += U * kRowLanes) {
+            Raw<T, W> vh[U], vg[U], vu[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int row = r + u * kRowLanes;
+                if (row < r1) {
+                    vh[u].load(dh + row * a.lddh);
+                    vg[u].load(zg + row * a.ldzg);
+                    vu[u].load(zu + row * a.ldzu);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int row = r + u * kRowLanes;
+                if (row >= r1) continue;
+                float h[W], g[W], f[W];
+                vh[u].get(h);
+                vg[u].get(g);
+                vu[u].get(f);
+#pragma unroll
+                for (int j = 0; j < W; ++j) f[j] *= h[j] * activate_grad<T>(g[j], a.act);
+                activate_all<T>(g, a.act);
+#pragma unroll
+                for (int j = 0; j < W; ++j) {
+                    g[j] *= h[j];
+                    sum[0][j] += f[j];
+                    sum[1][j] += g[j];
+                }
+                if (a.dZg != nullptr) {
+                    store(a.dZg, row, f);
+                    store(a.dZu, row, g);
+                }
+            }
+        }
+    }
+    if (a.partial == nullptr) return;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        if (k > 0) __syncthreads();   // the gate's sums have been read
+#pragma unroll
+        for (int j = 0; j < W; ++j) red[ty][lane * W + j] = sum[k][j];
+        __syncthreads();
+        for (int i = threadIdx.x; i < 32 * W; i += kThreads) {
+            const int col = (int)blockIdx.x * 32 * W + i;
+            if (col >= a.N) break;
+            float v = 0.f;
+#pragma unroll
+            for (int r = 0; r < kRowLanes; ++r) v += red[r][i];
+            a.partial[((int64_t)blockIdx.y * 2 + k) * a.N + col] = v;
+        }
+    }
+}
+
+// 32 columns a CTA, 32 row lanes, as column_sum_kernel; blockIdx.y: which output.
+template <class T>
+__global__ void __launch_bounds__(1024) column_sum2_kernel(const float *partial, int parts,
+                                                           int64_t N, T *out, T *out2, int chain) {
+    __shared__ float red[32][33];
+    chain_begin(chain);
+    const int lane = threadIdx.x & 31, ty = threadIdx.x >> 5;
+    const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+    T *const to = blockIdx.y == 0 ? out : out2;
+    if (to != nullptr) {
+        const float *from = partial + blockIdx.y * N;
+        float v = 0.f;
+        if (c < N) {
+            constexpr int U = 10;   // rows in flight; up to 320 parts in one go
+            for (int p0 = ty; p0 < parts; p0 += 32 * U) {
+                float x[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int p = p0 + 32 * u;
+                    x[u] = p < parts ? __ldcg(from + 2 * p * N + c) : 0.f;   // (see chain_begin)
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) v += x[u];
+            }
+        }
+        red[ty][lane] = v;
+        __syncthreads();
+        if (ty == 0 && c < N) {
+            float s = 0.f;
+#pragma unroll
+            for (int r = 0; r < 32; ++r) s += red[r][lane];
+            to[c] = from_f32<T>(s);
+        }
+    }
+    chain_end(chain);
+}
+
+bool aligned16(const void *p, int64_t ld, int size) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * size % 16 == 0;
+}
+
+template <class... P, class... A>
+cudaError_t launch(void (*kernel)(P...), dim3 grid, int block, cudaStream_t s, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)block);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
+template <class T>
+cudaError_t dz_types(const DzArgs &a, bool vec, int parts, cudaStream_t s) {
+    constexpr int W = 16 / sizeof(T);
+    const int strip = 32 * (vec ? W : 1);
+    const dim3 grid((unsigned)((a.N + strip - 1) / strip), (unsigned)parts);
+    return vec ? launch(gated_dz_kernel<T, W>, grid, kThreads, s, a)
+               : launch(gated_dz_kernel<T, 1>, grid, kThreads, s, a);
+}
+
+}  // namespace gated
+
+cudaError_t launch_gated_dz(int type, const void *dH, int64_t lddh, const void *Zg, int64_t ldzg,
+                            const void *Zu, int64_t ldzu, int act, int M, int N, void *dZg,
+                            void *dZu, int64_t lddz, int64_t plane, float *partial, int chain,
+                            cudaStream_t s) {
+    using gated::aligned16;
+    const int size = dtype_size(type), w = 16 / size;
+    const bool vec = N % w == 0 && aligned16(dH, lddh, size) && aligned16(Zg, ldzg, size) &&
+                     aligned16(Zu, ldzu, size) &&
+                     (plane != 0 || dZg == nullptr ||
+                      (aligned16(dZg, lddz, size) && aligned16(dZu, lddz, size)));
+    const int parts = grad_parts(M, N);
+    const gated::DzArgs a = {dH,   Zg,   Zu,    dZg, dZu, partial, lddh,
+                             ldzg, ldzu, lddz, plane, M,  N,   act,     (M + parts - 1) / parts,
+                             chain};
+    if (type == SGEMM_F32) return gated::dz_types<float>(a, vec, parts, s);
+    if (type == SGEMM_BF16) return gated::dz_types<__nv_bfloat16>(a, vec, parts, s);
+    return gated::dz_types<__half>(a, vec, parts, s);
+}
+
+cudaError_t launch_column_sum2(int type, const float *partial, int parts, int64_t N, void *out,
+                               void *out2, int chain, cudaStream_t s) {
+    const dim3 grid((unsigned)((N + 31) / 32), 2);
+    if (type == SGEMM_F32)
+        return gated::launch(gated::column_sum2_kernel<float>, grid, 1024, s, partial, parts, N,
+                             static_cast<float *>(out), static_cast<float *>(out2), chain);
+    if (type == SGEMM_BF16)
+        return gated::launch(gated::column_sum2_kernel<__nv_bfloat16>, grid, 1024, s, partial,
+                             parts, N, static_cast<__nv_bfloat16 *>(out),
+                             static_cast<__nv_bfloat16 *>(out2), chain);
+    return gated::launch(gated::column_sum2_kernel<__half>, grid, 1024, s, partial, parts, N,
+                         static_cast<__half *>(out), static_cast<__half *>(out2), chain);
+}
+
+}  // namespace sgemm

@@ -406,6 +406,70 @@ __device__ __forceinline__ void finish_column(const LayerEpi &e, const ColumnTer
         if (i < rows) p[i * e.ldy] = from_f32<T>(e.R != nullptr ? z[i] + r[i] : z[i]);
 }
 
+// ------------------------------------------------------------------ gated epilogue
+
+// One output of the gated layer.
+template <class T>
+__device__ __forceinline__ void finish_gated1(const GatedEpi &e, int row, int col, float g,
+                                              float u) {
+    if (e.sx != nullptr) {
+        const float sx = e.sx[row];
+        g *= sx * e.sg[col];
+        u *= sx * e.su[col];
+    }
+    if (e.bg != nullptr) g += to_f32(static_cast<const T *>(e.bg)[col]);
+    if (e.bu != nullptr) u += to_f32(static_cast<const T *>(e.bu)[col]);
+    if (e.Zg != nullptr) static_cast<T *>(e.Zg)[row * e.ldg + col] = from_f32<T>(g);
+    if (e.Zu != nullptr) static_cast<T *>(e.Zu)[row * e.ldu + col] = from_f32<T>(u);
+    static_cast<T *>(e.H)[row * e.ldh + col] = from_f32<T>(activate<T>(g, e.act) * u);
+}
+
+// What it takes for G fixed columns.
+template <class T, int G>
+struct GatedTerms {
+    float bg[G], bu[G], sg[G], su[G];
+    __device__ __forceinline__ void load(const GatedEpi &e, int col) {
+#pragma unroll
+        for (int j = 0; j < G; ++j) {
+            const bool in = col + j < e.N;
+            bg[j] = in && e.bg != nullptr ? to_f32(static_cast<const T *>(e.bg)[col + j]) : 0.f;
+            bu[j] = in && e.bu != nullptr ? to_f32(static_cast<const T *>(e.bu)[col + j]) : 0.f;
+            sg[j] = in && e.sg != nullptr ? e.sg[col + j] : 1.f;
+            su[j] = in && e.su != nullptr ? e.su[col + j] : 1.f;
+        }
+    }
+};
+
+// Columns col .. col + G - 1 of `row` < M, those below N.
+template <class T, int G>
+__device__ __forceinline__ void finish_gated_group(const GatedEpi &e, const GatedTerms<T, G> &t,
+                                                   int row, int col, float (&g)[G],
+                                                   float (&u)[G]) {
+    const bool vec = e.vec >= G && col + G <= e.N;
+    const float sx = e.sx != nullptr ? e.sx[row] : 1.f;
+#pragma unroll
+    for (int j = 0; j < G; ++j) {
+        g[j] = fmaf(g[j], sx * t.sg[j], t.bg[j]);
+        u[j] = fmaf(u[j], sx * t.su[j], t.bu[j]);
+    }
+    auto store = [&](void *base, int64_t ld, const float (&x)[G]) {
+        T *p = static_cast<T *>(base) + row * ld + col;
+        if (vec) {
+            store_vec<T, G>(p, x);
+        } else {
+#pragma unroll
+            for (int j = 0; j < G; ++j)
+                if (col + j < e.N) p[j] = from_f32<T>(x[j]);
+        }
+    };
+    if (e.Zg != nullptr) store(e.Zg, e.ldg, g);
+    if (e.Zu != nullptr) store(e.Zu, e.ldu, u);
+    activate_all<T>(g, e.act);
+#pragma unroll
+    for (int j = 0; j < G; ++j) g[j] *= u[j];
+    store(e.H, e.ldh, g);
+}
+
 // 16 values of a 16-bit type as one 32-byte access (aligned to it): a whole
 // sector each lane.
 __device__ __forceinline__ void load_32b(const void *p, uint32_t (&r)[8]) {

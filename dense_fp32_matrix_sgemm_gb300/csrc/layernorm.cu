@@ -1,0 +1,515 @@
+// Layer norm with the residual's addition, in the input's type or as 8-bit rows with a
+// scale, and its gradients.
+//
+//   s = x + r,  m = mean s,  rstd = (mean (s - m)^2 + eps)^(-1/2),  n = (s - m) rstd,  y = n w + b
+//   g = dy w,   dx = ds + rstd (g - mean g - n mean(g n)),  dw = sum_rows dy n,  db = sum_rows dy
+//
+// HBM bounds them as it bounds the root-mean-square norm, and the row groups, accesses and
+// launches are norm.cu's: a row is read once into registers (fp32), and written from there.
+// The statistics are formed from differences, not from sums of squares (which would lose a
+// large mean's digits): first the mean, then the sums of s - m and of its square, where the
+// first corrects both for the mean's own rounding.  That is two reductions across the group; the 8-bit output's largest |y| is
+// a third, as the bias keeps it from being formed before rstd is known.
+// The gradients' two row sums go through one reduction; the sums over rows of dw and db stay
+// in registers over a group's rows, go to the workspace a row a CTA, and are added in a fixed
+// order by one more pass.
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+#include "device_utils.cuh"
+#include "layer_math.cuh"
+#include "layers.h"
+#include "row_reduce.cuh"
+
+namespace sgemm {
+namespace norm {
+namespace {
+
+// Sums of a and b over the CTA's row group, the same in each of its threads.  red: 32 float2
+// of shared memory that nothing else uses until two barriers later.
+__device__ __forceinline__ float2 group_sum2(float a, float b, float2 *red) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        a += __shfl_xor_sync(0xffffffffu, a, o);
+        b += __shfl_xor_sync(0xffffffffu, b, o);
+    }
+    const int warps = blockDim.x >> 5;   // of one group
+    if (warps == 1) return make_float2(a, b);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float2 *mine = red + threadIdx.y * warps;
+    if (lane == 0) mine[warp] = make_float2(a, b);
+    __syncthreads();
+    const float2 p = lane < warps ? mine[lane] : make_float2(0.f, 0.f);
+    a = p.x;
+    b = p.y;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        a += __shfl_xor_sync(0xffffffffu, a, o);
+        b += __shfl_xor_sync(0xffffffffu, b, o);
+    }
+    return make_float2(a, b);
+}
+
+struct LayerRowArgs {
+    const void *X, *R, *w, *b;
+    void *S, *Y;
+    int64_t ldx, ldr, lds, ldy, rows;
+    float *q_scale, *mean, *rstd;
+    float eps;
+    int D;
+};
+
+// QUANT: 8-bit output.
+template <class T, int W, int NV, int MAXT, bool QUANT>
+__global__ void __launch_bounds__(MAXT) layer_row_kernel(const LayerRowArgs a) {
+    __shared__ float2 red[3][32];
+    pdl_trigger();
+    pdl_wait();
+    const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    const bool live = row < a.rows;
+    const T *x = static_cast<const T *>(a.X) + row * a.ldx;
+    const T *r = static_cast<const T *>(a.R) + row * a.ldr;
+    const T *w = static_cast<const T *>(a.w);
+    const T *b = static_cast<const T *>(a.b);
+    Raw<T, W> vx[NV], vr[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * blockDim.x + threadIdx.x) * W;
+        const bool in = live && c < a.D;
+        vx[i] = load_or_zero<T, W>(x + c, in);
+        if (a.R != nullptr) vr[i] = load_or_zero<T, W>(r + c, in);
+    }
+    float s[NV][W];
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * blockDim.x + threadIdx.x) * W;
+        vx[i].get(s[i]);
+        if (a.R != nullptr) {
+            float r[W];
+            vr[i].get(r);
+#pragma unroll
+            for (int j = 0; j < W; ++j) s[i][j] += r[j];
+        }
+        if (a.S != nullptr && live && c < a.D)
+            put<T, W>(static_cast<T *>(a.S) + row * a.lds + c, s[i]);
+#pragma unroll
+        for (int j = 0; j < W; ++j) sum += s[i][j];
+    }
+    const float width = (float)max(a.D, 1);   // (no elements: a mean and a variance of 0)
+    const float first = group_sum2(sum, 0.f, red[0]).x / width;
+    float off = 0.f, square = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * blockDim.x + threadIdx.x) * W;
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+            s[i][j] = c < a.D ? s[i][j] - first : 0.f;
+            off += s[i][j];
+            square = fmaf(s[i][j], s[i][j], square);
+        }
+    }
+    const float2 t = group_sum2(off, square, red[1]);
+    const float shift = t.x / width;
+    const float rstd = 1.f / sqrtf(max_nan(t.y / width - shift * shift, 0.f) + a.eps);
+    if (live && threadIdx.x == 0) {
+        if (a.mean != nullptr) a.mean[row] = isinf(first) ? first : first + shift;
+        if (a.rstd != nullptr) a.rstd[row] = rstd;
+    }
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * blockDim.x + threadIdx.x) * W;
+        const bool in = c < a.D;
+        float fw[W], fb[W];
+        load_or_zero<T, W>(w + c, in).get(fw);
+        load_or_zero<T, W>(b + c, in && b != nullptr).get(fb);
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+            s[i][j] = fmaf((s[i][j] - shift) * rstd, fw[j], fb[j]);
+            if (QUANT && in) top = max_nan(top, fabsf(s[i][j]));
+        }
+        if (!QUANT && live && in) put<T, W>(static_cast<T *>(a.Y) + row * a.ldy + c, s[i]);
+    }
+    if constexpr (QUANT) {
+        const float amax = max_nan(group_reduce(0.f, top, red[2]).y, kAmaxFloor);
+        if (live && threadIdx.x == 0) a.q_scale[row] = amax / kE4m3Max;
+        const float inv = kE4m3Max / amax;
+        uint8_t *q = static_cast<uint8_t *>(a.Y) + row * a.ldy;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * blockDim.x + threadIdx.x) * W;
+            if (!live || c >= a.D) continue;
+#pragma unroll
+            for (int j = 0; j < W; ++j) s[i][j] *= inv;
+            store_codes<W>(q + c, s[i]);
+        }
+    }
+}
+
+// Rows wider than a group's registers: one CTA a row, read again (from L2) for each sum and
+// for the output.  S may be X or R: it is written in the last pass, each element after the
+// same thread has read it.
+template <class T, bool QUANT>
+__global__ void __launch_bounds__(kMaxThreads) layer_row_wide_kernel(const LayerRowArgs a) {
+    __shared__ float2 red[3][32];
+    pdl_trigger();
+    pdl_wait();
+    const int64_t row = blockIdx.x;
+    const T *x = static_cast<const T *>(a.X) + row * a.ldx;
+    const T *r = a.R != nullptr ? static_cast<const T *>(a.R) + row * a.ldr : nullptr;
+    const T *w = static_cast<const T *>(a.w);
+    const T *b = static_cast<const T *>(a.b);
+    auto value = [&](int c) { return to_f32(x[c]) + (r != nullptr ? to_f32(r[c]) : 0.f); };
+    float sum = 0.f;
+    for (int c = threadIdx.x; c < a.D; c += blockDim.x) sum += value(c);
+    const float width = (float)max(a.D, 1);
+    const float first = group_sum2(sum, 0.f, red[0]).x / width;
+    float off = 0.f, square = 0.f;
+    for (int c = threadIdx.x; c < a.D; c += blockDim.x) {
+        const float s = value(c) - first;
+        off += s;
+        square = fmaf(s, s, square);
+    }
+    const float2 t = group_sum2(off, square, red[1]);
+    const float shift = t.x / width;
+    const float rstd = 1.f / sqrtf(max_nan(t.y / width - shift * shift, 0.f) + a.eps);
+    if (threadIdx.x == 0) {
+        if (a.mean != nullptr) a.mean[row] = isinf(first) ? first : first + shift;
+        if (a.rstd != nullptr) a.rstd[row] = rstd;
+    }
+    auto output = [&](int c, float s) {
+        return fmaf((s - first - shift) * rstd, to_f32(w[c]), b != nullptr ? to_f32(b[c]) : 0.f);
+    };
+    float inv = 1.f;
+    if constexpr (QUANT) {
+        float top = 0.f;
+        for (int c = threadIdx.x; c < a.D; c += blockDim.x)
+            top = max_nan(top, fabsf(output(c, value(c))));
+        const float amax = max_nan(group_reduce(0.f, top, red[2]).y, kAmaxFloor);
+        if (threadIdx.x == 0) a.q_scale[row] = amax / kE4m3Max;
+        inv = kE4m3Max / amax;
+    }
+    for (int c = threadIdx.x; c < a.D; c += blockDim.x) {
+        const float s = value(c);
+        if (a.S != nullptr) static_cast<T *>(a.S)[row * a.lds + c] = from_f32<T>(s);
+        const float y = output(c, s);
+        if constexpr (QUANT)
+            static_cast<uint8_t *>(a.Y)[row * a.ldy + c] = to_e4m3(y * inv);
+        else
+            static_cast<T *>(a.Y)[row * a.ldy + c] = from_f32<T>(y);
+    }
+}
+
+struct LayerGradArgs {
+    const void *dY, *S, *w, *dS;
+    void *dX;
+    const float *mean, *rstd;
+    float *partial;   // rows of 2 D floats: dw's, then db's
+    int64_t lddy, lds, ldds, lddx, rows;
+    int D;
+};
+
+template <class T, int W, int NV, int MAXT>
+__global__ void __launch_bounds__(MAXT) layer_grad_kernel(const LayerGradArgs a) {
+    __shared__ float2 red[2][32];
+    pdl_trigger();
+    pdl_wait();
+    const int64_t group = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    const int64_t groups = (int64_t)gridDim.x * blockDim.y;
+    Raw<T, W> vw[NV];
+    float dw[NV][W], db[NV][W];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * blockDim.x + threadIdx.x) * W;
+        vw[i] = load_or_zero<T, W>(static_cast<const T *>(a.w) + c, c < a.D);
+#pragma unroll
+        for (int j = 0; j < W; ++j) dw[i][j] = db[i][j] = 0.f;
+    }
+    // every group of the CTA takes as many turns as its first one (barriers)
+    const int64_t first = (int64_t)blockIdx.x * blockDim.y;
+    const int turns = first < a.rows ? (int)((a.rows - 1 - first) / groups) + 1 : 0;
+    // the next row's loads are issued before this row's sums where registers allow it
+    constexpr bool AHEAD = MAXT <= 512;
+    Raw<T, W> ny[NV], ns[NV];
+    float nm = 0.f, nr = 0.f;
+    auto load_ds = [&](int64_t row, int c) {
+        return load_or_zero<T, W>(static_cast<const T *>(a.dS) + row * a.ldds + c,
+                                  row < a.rows && c < a.D && a.dS != nullptr);
+    };
+    auto load_row = [&](int64_t row) {
+        const bool live = row < a.rows;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * blockDim.x + threadIdx.x) * W;
+            const bool in = live && c < a.D;
+            ny[i] = load_or_zero<T, W>(static_cast<const T *>(a.dY) + row * a.lddy + c, in);
+            ns[i] = load_or_zero<T, W>(static_cast<const T *>(a.S) + row * a.lds + c, in);
+        }
+        nm = live ? a.mean[row] : 0.f;
+        nr = live ? a.rstd[row] : 0.f;
+    };
+    // where they do not, it is brought to L2 in the meantime, a lane a 128-byte line
+    auto prefetch_row = [&](int64_t row) {
+        constexpr int LANES = W > 1 ? 128 / (W * (int)sizeof(T)) : 32;
+        if (row >= a.rows || threadIdx.x % LANES != 0) return;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * blockDim.x + threadIdx.x) * W;
+            if (c >= a.D) continue;
+            prefetch_l2(static_cast<const T *>(a.dY) + row * a.lddy + c);
+            prefetch_l2(static_cast<const T *>(a.S) + row * a.lds + c);
+            if (a.dS != nullptr) prefetch_l2(static_cast<const T *>(a.dS) + row * a.ldds + c);
+        }
+    };
+    if (AHEAD && turns > 0) load_row(group);
+    for (int t = 0; t < turns; ++t) {
+        const int64_t row = group + t * groups;
+        const bool live = row < a.rows;
+        if (!AHEAD) {
+            load_row(row);
+            if (t + 1 < turns) prefetch_row(row + groups);
+        }
+        Raw<T, W> vy[NV], vs[NV], vd[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            vy[i] = ny[i];
+            vs[i] = ns[i];
+            if (AHEAD) vd[i] = load_ds(row, (i * blockDim.x + threadIdx.x) * W);
+        }
+        const float mean = nm, rstd = nr;
+        if (AHEAD && t + 1 < turns) load_row(row + groups);
+        float sg = 0.f, sgn = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float dy[W], s[W], w[W];
+            vy[i].get(dy);
+            vs[i].get(s);
+            vw[i].get(w);
+#pragma unroll
+            for (int j = 0; j < W; ++j) {
+                const float n = (s[j] - mean) * rstd, g = dy[j] * w[j];
+                sg += g;
+                sgn = fmaf(g, n, sgn);
+                dw[i][j] = fmaf(dy[j], n, dw[i][j]);
+                db[i][j] += dy[j];
+            }
+        }
+        // two buffers: a warp may reach the next turn's while another still reads this
+        // one's, not the one after (that takes the next barrier)
+        const float2 k = group_sum2(sg, sgn, red[t & 1]);
+        const float kg = k.x / (float)a.D, kn = k.y / (float)a.D;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * blockDim.x + threadIdx.x) * W;
+            if (!live || c >= a.D) continue;
+            float dy[W], s[W], w[W], ds[W], dx[W];
+            vy[i].get(dy);
+            vs[i].get(s);
+            vw[i].get(w);
+            (AHEAD ? vd[i] : load_ds(row, c)).get(ds);
+#pragma unroll
+            for (int j = 0; j < W; ++j) {
+                const float n = (s[j] - mean) * rstd;
+                dx[j] = fmaf(rstd, fmaf(-n, kn, fmaf(dy[j], w[j], -kg)), ds[j]);
+            }
+            put<T, W>(static_cast<T *>(a.dX) + row * a.lddx + c, dx);
+        }
+    }
+    if (a.partial == nullptr) return;
+    // one row of partial sums a CTA: its groups' sums are added in their order (groups share a
+    // CTA only up to 512 threads)
+    __shared__ float sums[512 * NV * W];
+    const int width = blockDim.x * NV * W;
+    auto join = [&](float (&d)[NV][W]) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < W; ++j)
+                sums[threadIdx.y * width + (i * W + j) * blockDim.x + threadIdx.x] = d[i][j];
+        __syncthreads();
+        if (threadIdx.y == 0)
+            for (int y = 1; y < (int)blockDim.y; ++y)
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+#pragma unroll
+                    for (int j = 0; j < W; ++j)
+                        d[i][j] += sums[y * width + (i * W + j) * blockDim.x + threadIdx.x];
+        __syncthreads();
+    };
+    if (blockDim.y > 1) {
+        join(dw);
+        join(db);
+        if (threadIdx.y > 0) return;
+    }
+    float *to = a.partial + (int64_t)blockIdx.x * 2 * a.D;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * blockDim.x + threadIdx.x) * W;
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+            if (c + j < a.D) {
+                to[c + j] = dw[i][j];
+                to[a.D + c + j] = db[i][j];
+            }
+    }
+}
+
+// Rows wider than a group's registers: the CTA reads each of its rows twice and keeps its
+// columns' sums in its own row of the workspace.
+template <class T>
+__global__ void __launch_bounds__(kMaxThreads) layer_grad_wide_kernel(const LayerGradArgs a) {
+    __shared__ float2 red[2][32];
+    pdl_trigger();
+    pdl_wait();
+    const T *w = static_cast<const T *>(a.w);
+    float *part = a.partial != nullptr ? a.partial + (int64_t)blockIdx.x * 2 * a.D : nullptr;
+    int t = 0;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, ++t) {
+        const T *dy = static_cast<const T *>(a.dY) + row * a.lddy;
+        const T *s = static_cast<const T *>(a.S) + row * a.lds;
+        const float mean = a.mean[row], rstd = a.rstd[row];
+        float sg = 0.f, sgn = 0.f;
+        for (int c = threadIdx.x; c < a.D; c += blockDim.x) {
+            const float g = to_f32(dy[c]) * to_f32(w[c]);
+            sg += g;
+            sgn = fmaf(g, (to_f32(s[c]) - mean) * rstd, sgn);
+        }
+        const float2 k = group_sum2(sg, sgn, red[t & 1]);
+        const float kg = k.x / (float)a.D, kn = k.y / (float)a.D;
+        for (int c = threadIdx.x; c < a.D; c += blockDim.x) {
+            const float y = to_f32(dy[c]), n = (to_f32(s[c]) - mean) * rstd;
+            float dx = rstd * fmaf(-n, kn, fmaf(y, to_f32(w[c]), -kg));
+            if (a.dS != nullptr) dx += to_f32(static_cast<const T *>(a.dS)[row * a.ldds + c]);
+            if (part != nullptr) {
+                part[c] = fmaf(y, n, t > 0 ? part[c] : 0.f);
+                part[a.D + c] = y + (t > 0 ? part[a.D + c] : 0.f);
+            }
+            static_cast<T *>(a.dX)[row * a.lddx + c] = from_f32<T>(dx);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ host side
+
+template <class T, int W, int NV, bool QUANT>
+cudaError_t launch_row(const LayerRowArgs &a, Shape sh, cudaStream_t s) {
+    const dim3 grid((unsigned)((a.rows + sh.groups - 1) / sh.groups));
+    const dim3 block((unsigned)sh.tpr, (unsigned)sh.groups);
+    if (sh.tpr <= 512) return launch(layer_row_kernel<T, W, NV, 512, QUANT>, grid, block, a, s);
+    return launch(layer_row_kernel<T, W, NV, kMaxThreads, QUANT>, grid, block, a, s);
+}
+
+template <class T, bool QUANT>
+cudaError_t row_dispatch(const LayerRowArgs &a, bool vec, cudaStream_t s) {
+    constexpr int W = 16 / sizeof(T);
+    if (vec) {
+        const int64_t n = a.D / W;
+        Shape sh = shape_for(n, 1);
+        // few rows: as many threads as possible on each, for its latency
+        if (sh.tpr > 0 && a.rows <= 304) return launch_row<T, W, 1, QUANT>(a, sh, s);
+        sh = shape_for(n, 4);
+        if (sh.tpr > 0) return launch_row<T, W, 4, QUANT>(a, sh, s);
+    } else {
+        const Shape sh = shape_for(a.D, 8);
+        if (sh.tpr > 0) return launch_row<T, 1, 8, QUANT>(a, sh, s);
+    }
+    return launch(layer_row_wide_kernel<T, QUANT>, dim3((unsigned)a.rows), dim3(kMaxThreads), a, s);
+}
+
+template <bool QUANT>
+cudaError_t row_types(int type, const LayerRowArgs &a, cudaStream_t s) {
+    const int size = dtype_size(type), w = 16 / size;
+    const bool vec = a.D % w == 0 && aligned16(a.X, a.ldx, size) && aligned16(a.R, a.ldr, size) &&
+                     aligned16(a.w, 0, size) && aligned16(a.b, 0, size) &&
+                     aligned16(a.S, a.lds, size) &&
+                     (QUANT ? reinterpret_cast<uintptr_t>(a.Y) % 8 == 0 && a.ldy % 8 == 0
+                            : aligned16(a.Y, a.ldy, size));
+    if (type == SGEMM_F32) return row_dispatch<float, QUANT>(a, vec, s);
+    if (type == SGEMM_BF16) return row_dispatch<__nv_bfloat16, QUANT>(a, vec, s);
+    return row_dispatch<__half, QUANT>(a, vec, s);
+}
+
+// The backward pass's row groups: as many CTAs as the SMs hold at once, at most one group
+// a row.
+struct GradShape {
+    int w, nv;      // elements an access, accesses a thread; nv 0: the wide kernel
+    Shape sh;
+    int ctas;
+};
+GradShape grad_shape(int type, int64_t rows, int64_t D, bool vec) {
+    GradShape g;
+    g.w = vec ? 16 / dtype_size(type) : 1;
+    const int64_t n = (D + g.w - 1) / g.w;
+    g.nv = vec ? 2 : 8;
+    g.sh = shape_for(n, g.nv);
+    if (g.sh.tpr == 0) {
+        g.nv = 0;
+        g.sh = {kMaxThreads, 1};
+    }
+    // one CTA of 512 threads an SM has half the partial sums of two of 256; its groups wait
+    // for one another, so only where each takes eight turns or more (as in norm.cu)
+    if (g.sh.tpr <= 256 && rows >= 152 * 8 * (512 / g.sh.tpr)) g.sh.groups = 512 / g.sh.tpr;
+    const int64_t need = (rows + g.sh.groups - 1) / g.sh.groups;
+    const int threads = g.sh.tpr * g.sh.groups;
+    const int per_sm = threads > 512 ? 1 : 512 / threads;
+    const int64_t most = (int64_t)152 * per_sm;
+    g.ctas = (int)(need < most ? need : most);
+    return g;
+}
+
+template <class T>
+cudaError_t grad_dispatch(const LayerGradArgs &a, const GradShape &g, cudaStream_t s) {
+    constexpr int W = 16 / sizeof(T);
+    const dim3 grid((unsigned)g.ctas), block((unsigned)g.sh.tpr, (unsigned)g.sh.groups);
+    if (g.nv == 0) return launch(layer_grad_wide_kernel<T>, grid, block, a, s);
+    if (g.w == 1)
+        return g.sh.tpr <= 512 ? launch(layer_grad_kernel<T, 1, 8, 512>, grid, block, a, s)
+                               : launch(layer_grad_kernel<T, 1, 8, kMaxThreads>, grid, block, a, s);
+    return g.sh.tpr <= 512 ? launch(layer_grad_kernel<T, W, 2, 512>, grid, block, a, s)
+                           : launch(layer_grad_kernel<T, W, 2, kMaxThreads>, grid, block, a, s);
+}
+
+}  // namespace
+}  // namespace norm
+
+cudaError_t launch_add_layernorm(int type, int64_t rows, int64_t D, const void *X, int64_t ldx,
+                                 const void *R, int64_t ldr, const void *w, const void *b,
+                                 float eps, void *S, int64_t lds, void *Y, int64_t ldy,
+                                 float *q_scale, float *mean, float *rstd, cudaStream_t s) {
+    const norm::LayerRowArgs a = {X,   R,   w,   b,    S,       Y,    ldx,  ldr,
+                                  lds, ldy, rows, q_scale, mean, rstd, eps, (int)D};
+    return q_scale != nullptr ? norm::row_types<true>(type, a, s)
+                              : norm::row_types<false>(type, a, s);
+}
+
+// Rows of partial sums, the larger of the aligned and the unaligned plan (the caller's
+// pointers decide which one runs).
+int layernorm_backward_parts(int type, int64_t rows, int64_t D) {
+    const norm::GradShape a = norm::grad_shape(type, rows, D, true);
+    const norm::GradShape b = norm::grad_shape(type, rows, D, false);
+    return a.ctas > b.ctas ? a.ctas : b.ctas;
+}
+
+cudaError_t launch_add_layernorm_backward(int type, int64_t rows, int64_t D, const void *dY,
+                                          int64_t lddy, const void *S, int64_t lds,
+                                          const float *mean, const float *rstd, const void *w,
+                                          const void *dS, int64_t ldds, void *dX, int64_t lddx,
+                                          void *dw, void *db, float *partial, cudaStream_t s) {
+    const int size = dtype_size(type), width = 16 / size;
+    const bool vec = D % width == 0 && norm::aligned16(dY, lddy, size) &&
+                     norm::aligned16(S, lds, size) && norm::aligned16(w, 0, size) &&
+                     norm::aligned16(dS, ldds, size) && norm::aligned16(dX, lddx, size);
+    const norm::GradShape g = norm::grad_shape(type, rows, D, vec);
+    const bool sums = dw != nullptr || db != nullptr;
+    const norm::LayerGradArgs a = {dY,   S,    w,    dS,   dX,   mean, rstd, sums ? partial : nullptr,
+                                   lddy, lds, ldds, lddx, rows, (int)D};
+    cudaError_t e = type == SGEMM_F32    ? norm::grad_dispatch<float>(a, g, s)
+                    : type == SGEMM_BF16 ? norm::grad_dispatch<__nv_bfloat16>(a, g, s)
+                                         : norm::grad_dispatch<__half>(a, g, s);
+    if (e != cudaSuccess || !sums) return e;
+    return launch_column_sum2(type, partial, g.ctas, D, dw, db, 0, s);
+}
+
+}  // namespace sgemm

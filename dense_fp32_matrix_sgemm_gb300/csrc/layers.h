@@ -15,6 +15,9 @@ __host__ __device__ inline int dtype_size(int t) {
     return t == SGEMM_F32 ? 4 : t == SGEMM_E4M3 ? 1 : 2;
 }
 
+// Whether a product of M rows runs on the CUDA cores (linear_rows.cu).  layers_api.cu.
+bool on_cuda_cores(int type, int64_t M, int64_t N, int64_t K, int transW);
+
 // Place of a launch among launches of a call that do not read one another's results:
 // after, before such a launch (chain_begin in layer_math.cuh), and with half of the
 // SMs for each of two products.
@@ -36,6 +39,22 @@ struct LayerEpi {
     int vec;
 };
 
+// What happens to the two accumulators of a gated layer:
+//   z = acc * (sx ? sx[row] * s[col] : 1) + b[col] for the gate (g) and its factor (u)
+//   H = act(zg) zu;  Zg = zg, Zu = zu where they are kept
+// vec: 8 (16-bit types only: 16-byte accesses), 4 or 1 elements that every base and
+// leading dimension is aligned to.
+struct GatedEpi {
+    void *H, *Zg, *Zu;
+    const void *bg, *bu;
+    const float *sx, *sg, *su;
+    int64_t ldh, ldg, ldu;
+    int M, N;
+    int act;
+    int type;
+    int vec;
+};
+
 // One operand of the tensor-core product: P (reduction) x rows as stored.
 // kmajor: element (row, k) at base[row*ld + k], else at base[k*ld + row].
 struct TcOperand {
@@ -48,6 +67,19 @@ struct TcOperand {
 struct ProductSize {
     int M, N, K;
 };
+// (gated_tc.cu, gated_f32.cu)  H = act(X Wg^T + bg) (X Wu^T + bu), operands as
+// launch_linear_tc takes them; both weights stored in one order.
+cudaError_t launch_gated_tc(int in_type, const TcOperand &X, const TcOperand &Wg,
+                            const TcOperand &Wu, int K, const GatedEpi &epi, cudaStream_t s);
+// D = A1 B1^T + A2 B2^T, each reduction K long.
+cudaError_t launch_sum_tc(int in_type, const TcOperand (&A)[2], const TcOperand (&B)[2], int K,
+                          const LayerEpi &epi, int chain, cudaStream_t s);
+// The gated product of few rows on the CUDA cores, one pass over both weights; any type and
+// alignment, weights stored by output features.  linear_rows.cu.
+cudaError_t launch_gated_rows(int in_type, const void *X, int64_t ldx, const void *Wg, int64_t ldwg,
+                              const void *Wu, int64_t ldwu, int K, const GatedEpi &epi,
+                              cudaStream_t s);
+
 // Whether two products of a chain are better run side by side than in turn.
 bool linear_tc_side_by_side(int in_type, const ProductSize &a, const ProductSize &b);
 bool linear_f32_side_by_side(const ProductSize &a, const ProductSize &b);
@@ -77,10 +109,14 @@ struct F32Planes {    // planes of a stored rows x cols matrix
 };
 inline int64_t f32_plane_ld(int64_t cols) { return (cols + 63) / 64 * 64; }   // of a plane's rows
 size_t f32_planes_bytes(int64_t rows, int64_t cols);
-cudaError_t launch_f32_split(const F32Operand *x, int count, int chain, cudaStream_t s);   // one or two
+cudaError_t launch_f32_split(const F32Operand *x, int count, int chain, cudaStream_t s);   // one to three
 // D[row, col] = sum_k A(row, k) B(col, k) with the epilogue (float).
 cudaError_t launch_linear_f32(const F32Planes &A, const F32Planes &B, int K, const LayerEpi &epi,
                               int chain, cudaStream_t s);
+cudaError_t launch_gated_f32(const F32Planes &X, const F32Planes &Wg, const F32Planes &Wu, int K,
+                             const GatedEpi &epi, cudaStream_t s);
+cudaError_t launch_sum_f32(const F32Planes (&A)[2], const F32Planes (&B)[2], int K,
+                           const LayerEpi &epi, int chain, cudaStream_t s);
 
 // Rows of `bytes_per_row` bytes copied to rows `dst_ld` bytes apart (dst
 // 16-byte aligned rows; the gap after each row is not written).
@@ -99,6 +135,17 @@ cudaError_t launch_linear_dz(int type, const void *dY, int64_t lddy, const void 
 cudaError_t launch_column_sum(int type, const float *partial, int parts, int64_t N, void *out,
                               int chain, cudaStream_t s);
 
+// The gated layer's dZg = dH Zu act'(Zg) and dZu = dH act(Zg) (f32 with plane > 0: as
+// planes) with partial column sums of both, `parts` (grad_parts) rows of 2 N floats.  gated_grad.cu
+cudaError_t launch_gated_dz(int type, const void *dH, int64_t lddh, const void *Zg, int64_t ldzg,
+                            const void *Zu, int64_t ldzu, int act, int M, int N, void *dZg,
+                            void *dZu, int64_t lddz, int64_t plane, float *partial, int chain,
+                            cudaStream_t s);
+// out[c] and out2[c] = sums over `parts` rows of partial[part][c] and partial[part][N + c],
+// added in a fixed order; either output may be null.
+cudaError_t launch_column_sum2(int type, const float *partial, int parts, int64_t N, void *out,
+                               void *out2, int chain, cudaStream_t s);
+
 // norm.cu
 cudaError_t launch_add_rmsnorm(int type, int64_t rows, int64_t D, const void *X, int64_t ldx,
                                const void *R, int64_t ldr, const void *w, float eps, void *S,
@@ -112,5 +159,23 @@ cudaError_t launch_add_rmsnorm_backward(int type, int64_t rows, int64_t D, const
                                         const float *rstd, const void *w, const void *dS,
                                         int64_t ldds, void *dX, int64_t lddx, void *dw,
                                         float *partial, cudaStream_t s);
+
+// layernorm.cu
+cudaError_t launch_add_layernorm(int type, int64_t rows, int64_t D, const void *X, int64_t ldx,
+                                 const void *R, int64_t ldr, const void *w, const void *b,
+                                 float eps, void *S, int64_t lds, void *Y, int64_t ldy,
+                                 float *q_scale, float *mean, float *rstd, cudaStream_t s);
+int layernorm_backward_parts(int type, int64_t rows, int64_t D);
+cudaError_t launch_add_layernorm_backward(int type, int64_t rows, int64_t D, const void *dY,
+                                          int64_t lddy, const void *S, int64_t lds,
+                                          const float *mean, const float *rstd, const void *w,
+                                          const void *dS, int64_t ldds, void *dX, int64_t lddx,
+                                          void *dw, void *db, float *partial, cudaStream_t s);
+
+// grad_clip.cu: Y null: the norm alone
+size_t grad_clip_bytes(int64_t count, const int *types, const int64_t *sizes);
+cudaError_t launch_grad_clip(int64_t count, const int *types, const int64_t *sizes,
+                             const void *const *X, void *const *Y, float max_norm, float eps,
+                             float *norm, double *partial, cudaStream_t s);
 
 }  // namespace sgemm

@@ -22,6 +22,8 @@
 // of CTAs, and the sums are added through shared and distributed shared
 // memory in rank order.
 // Rows or bases that are not 16-byte aligned take one element an access.
+// The gated layer of few rows is the dot form on both weights (weights stored K x N
+// are left to the tensor cores in every type).
 #include <cstdint>
 #include <type_traits>
 
@@ -74,12 +76,13 @@ struct Piece<T, 1> {
     }
 };
 
+template <class E>
 struct Args {
-    const void *X, *W;
-    int64_t ldx, ldw;
+    const void *X, *W, *W2;   // W2: the gated layer's second weight
+    int64_t ldx, ldw, ldw2;
     int K;
     int split;   // dot form: warps of a CTA that share a feature pair's K
-    LayerEpi epi;
+    E epi;
 };
 
 // Dot form.  Warp w of the CTA: features j0 .. j0 + F - 1 of group w / split, K
@@ -92,9 +95,13 @@ struct Args {
 template <class T, int MR>
 constexpr int kFeatures = sizeof(T) == 4 && (MR == 2 || MR == 4) ? 4 : 2;
 
-template <class T, class O, int W, int MR>
-__global__ void __launch_bounds__(kThreads) dot_kernel(const Args a) {
+// The gated layer's warps take a gate's and its factor's rows instead of two features
+// of one weight (or two of each), so that both sums of an output end in one warp.
+template <class T, class O, int W, int MR, class E>
+__global__ void __launch_bounds__(kThreads) dot_kernel(const Args<E> a) {
+    constexpr bool GATED = std::is_same<E, GatedEpi>::value;
     constexpr int F = kFeatures<T, MR>;
+    constexpr int OUT = GATED ? F / 2 : F;         // output columns
     constexpr int U = F == 2 && MR <= 2 ? 4 : 2;   // pieces in flight a feature
     constexpr int P = Piece<T, W>::PAIRS;
     constexpr int SUMS = F * MR;
@@ -104,11 +111,14 @@ __global__ void __launch_bounds__(kThreads) dot_kernel(const Args a) {
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int sub = warp % a.split;
-    const int j0 = F * (int)(blockIdx.x * (kWarps / a.split) + warp / a.split);
+    const int j0 = OUT * (int)(blockIdx.x * (kWarps / a.split) + warp / a.split);
     const T *w[F];
 #pragma unroll
-    for (int f = 0; f < F; ++f)
-        w[f] = static_cast<const T *>(a.W) + (int64_t)min(j0 + f, a.epi.N - 1) * a.ldw;
+    for (int f = 0; f < F; ++f) {
+        const int64_t j = min(j0 + f % OUT, a.epi.N - 1);
+        w[f] = f < OUT ? static_cast<const T *>(a.W) + j * a.ldw
+                       : static_cast<const T *>(a.W2) + j * a.ldw2;
+    }
     const int groups = (a.epi.M + MR - 1) / MR;
     for (int g = blockIdx.y; g < groups; g += gridDim.y) {
         const int m0 = g * MR;
@@ -176,8 +186,13 @@ __global__ void __launch_bounds__(kThreads) dot_kernel(const Args a) {
                 for (int s = 1; s < a.split; ++s) mine += red[warp + s][lane];
         }
         const int row = m0 + lane % MR, col = j0 + lane / MR;
-        if (sub == 0 && lane < SUMS && row < a.epi.M && col < a.epi.N)
+        if constexpr (GATED) {
+            const float factor = __shfl_sync(0xffffffffu, mine, (lane + OUT * MR) & 31);
+            if (sub == 0 && lane < OUT * MR && row < a.epi.M && col < a.epi.N)
+                finish_gated1<O>(a.epi, row, col, mine, factor);
+        } else if (sub == 0 && lane < SUMS && row < a.epi.M && col < a.epi.N) {
             finish1<O>(a.epi, row, col, mine);
+        }
     }
 }
 
@@ -186,7 +201,7 @@ __global__ void __launch_bounds__(kThreads) dot_kernel(const Args a) {
 // orientation go to the tensor cores, which take it as it is (4096 x 4096, one
 // row: 10.5 us there, 24 here).
 template <int W, int MR>
-__global__ void __launch_bounds__(kThreads) column_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads) column_kernel(const Args<LayerEpi> a) {
     constexpr int COLS = 32 * W;
     __shared__ __align__(16) float red[kWarps][MR][COLS];
     pdl_trigger();
@@ -265,8 +280,9 @@ __global__ void __launch_bounds__(kThreads) column_kernel(const Args a) {
     }
 }
 
-template <class K>
-cudaError_t launch(K kernel, dim3 grid, int threads, int cluster, const Args &a, cudaStream_t s) {
+template <class K, class E>
+cudaError_t launch(K kernel, dim3 grid, int threads, int cluster, const Args<E> &a,
+                   cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3((unsigned)threads);
@@ -285,24 +301,24 @@ cudaError_t launch(K kernel, dim3 grid, int threads, int cluster, const Args &a,
 
 constexpr int kSms = 152;
 
-template <class T, class O, int W, int MR>
-cudaError_t run(Args a, int transW, cudaStream_t s) {
+template <class T, class O, int W, int MR, class E>
+cudaError_t run(Args<E> a, int transW, cudaStream_t s) {
     const int groups = (a.epi.M + MR - 1) / MR;
     const unsigned gy = (unsigned)(groups < 65535 ? groups : 65535);
     if (transW) {
         // warps a group of features: until about 24 warps an SM are busy, each
         // with at least one piece of K a lane
-        constexpr int F = kFeatures<T, MR>;
+        constexpr int F = kFeatures<T, MR> / (std::is_same<E, GatedEpi>::value ? 2 : 1);
         const int64_t sets = (a.epi.N + F - 1) / F;
         a.split = 1;
         while (a.split < kWarps && sets * gy * a.split < kSms * 24 &&
                (int64_t)a.K > (int64_t)a.split * 32 * W)
             a.split *= 2;
         const int64_t per_cta = kWarps / a.split;
-        return launch(dot_kernel<T, O, W, MR>, dim3((unsigned)((sets + per_cta - 1) / per_cta), gy),
+        return launch(dot_kernel<T, O, W, MR, E>, dim3((unsigned)((sets + per_cta - 1) / per_cta), gy),
                       kThreads, 1, a, s);
     }
-    if constexpr (std::is_same<T, float>::value) {
+    if constexpr (std::is_same<T, float>::value && std::is_same<E, LayerEpi>::value) {
         const int64_t strips = (a.epi.N + 32 * W - 1) / (32 * W);
         int size = 1;
         while (size < 8 && strips * gy * size < kSms * 2 && a.K > size * kWarps * 4) size *= 2;
@@ -312,8 +328,8 @@ cudaError_t run(Args a, int transW, cudaStream_t s) {
     return cudaErrorInvalidValue;
 }
 
-template <class T, class O, int W>
-cudaError_t by_rows(const Args &a, int transW, cudaStream_t s) {
+template <class T, class O, int W, class E>
+cudaError_t by_rows(const Args<E> &a, int transW, cudaStream_t s) {
     if (a.epi.M == 1) return run<T, O, W, 1>(a, transW, s);
     if (a.epi.M == 2) return run<T, O, W, 2>(a, transW, s);
     if (a.epi.M <= 4 || sizeof(T) < 4) return run<T, O, W, 4>(a, transW, s);
@@ -321,30 +337,42 @@ cudaError_t by_rows(const Args &a, int transW, cudaStream_t s) {
     return cudaErrorInvalidValue;
 }
 
-template <class T, class O>
-cudaError_t by_alignment(const Args &a, int transW, cudaStream_t s) {
+template <class T, class O, class E>
+cudaError_t by_alignment(const Args<E> &a, int transW, cudaStream_t s) {
     constexpr int W = 16 / sizeof(T);
     auto ok = [](const void *p, int64_t ld) {
         return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * (int64_t)sizeof(T) % 16 == 0;
     };
-    const bool vec = transW ? ok(a.X, a.ldx) && ok(a.W, a.ldw) && a.K % W == 0
+    const bool vec = transW ? ok(a.X, a.ldx) && ok(a.W, a.ldw) && ok(a.W2, a.ldw2) && a.K % W == 0
                             : ok(a.W, a.ldw) && a.epi.N % W == 0;
     return vec ? by_rows<T, O, W>(a, transW, s) : by_rows<T, O, 1>(a, transW, s);
+}
+
+template <class E>
+cudaError_t by_type(int in_type, const Args<E> &a, int transW, cudaStream_t s) {
+    switch (in_type) {
+        case SGEMM_F32: return by_alignment<float, float>(a, transW, s);
+        case SGEMM_BF16: return by_alignment<__nv_bfloat16, __nv_bfloat16>(a, transW, s);
+        case SGEMM_F16: return by_alignment<__half, __half>(a, transW, s);
+        default:
+            return a.epi.type == SGEMM_BF16 ? by_alignment<uint8_t, __nv_bfloat16>(a, transW, s)
+                                            : by_alignment<uint8_t, __half>(a, transW, s);
+    }
 }
 
 }  // namespace rows
 
 cudaError_t launch_linear_rows(int in_type, const void *X, int64_t ldx, const void *W, int64_t ldw,
                                int transW, int K, const LayerEpi &epi, cudaStream_t s) {
-    const rows::Args a = {X, W, ldx, ldw, K, 1, epi};
-    switch (in_type) {
-        case SGEMM_F32: return rows::by_alignment<float, float>(a, transW, s);
-        case SGEMM_BF16: return rows::by_alignment<__nv_bfloat16, __nv_bfloat16>(a, transW, s);
-        case SGEMM_F16: return rows::by_alignment<__half, __half>(a, transW, s);
-        default:
-            return epi.type == SGEMM_BF16 ? rows::by_alignment<uint8_t, __nv_bfloat16>(a, transW, s)
-                                          : rows::by_alignment<uint8_t, __half>(a, transW, s);
-    }
+    const rows::Args<LayerEpi> a = {X, W, nullptr, ldx, ldw, 0, K, 1, epi};
+    return rows::by_type(in_type, a, transW, s);
+}
+
+cudaError_t launch_gated_rows(int in_type, const void *X, int64_t ldx, const void *Wg, int64_t ldwg,
+                              const void *Wu, int64_t ldwu, int K, const GatedEpi &epi,
+                              cudaStream_t s) {
+    const rows::Args<GatedEpi> a = {X, Wg, Wu, ldx, ldwg, ldwu, K, 1, epi};
+    return rows::by_type(in_type, a, 1, s);
 }
 
 }  // namespace sgemm

@@ -254,6 +254,177 @@ __device__ __forceinline__ void join_parts(const LayerEpi &e, uint32_t ring, int
     }
 }
 
+// ------------------------------------------------------------------ forms
+
+// The forms of the kernels that take more than one matrix on a side (gated_tc.cu,
+// gated_f32.cu):
+//   kGated  B's rows of a tile are half of one matrix's and half of another's, which
+//           meet in the epilogue: BN accumulator columns are BN / 2 outputs;
+//   kSum    D = A B^T + A2 B2^T, the reductions one behind the other.
+// kPlain: neither.
+enum Form { kPlain, kGated, kSum };
+
+// Tensor maps: the operands (A2: kSum; B2: kGated, kSum), and what is stored (Z2: kGated).
+struct Maps {
+    const CUtensorMap *A, *A2, *B, *B2, *Y, *Z, *Z2;
+};
+
+// ------------------------------------------------------------------ gated tiles
+
+// Whether the epilogue reads global memory.
+__device__ __forceinline__ bool reads_global(const LayerEpi &e) {
+    return e.bias != nullptr || e.R != nullptr || e.sx != nullptr;
+}
+__device__ __forceinline__ bool reads_global(const GatedEpi &e) {
+    return e.bg != nullptr || e.bu != nullptr || e.sx != nullptr;
+}
+
+// v = v sx s[col ..] + b[col ..] for 32 columns of a 16-bit layer (s and b may be null).
+template <class O>
+__device__ __forceinline__ void scale_and_bias32(float (&v)[32], float sx, const float *s,
+                                                 const void *b, int col) {
+    if (s != nullptr) {
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+            const float4 f = *reinterpret_cast<const float4 *>(s + col + j);
+            v[j] *= sx * f.x;
+            v[j + 1] *= sx * f.y;
+            v[j + 2] *= sx * f.z;
+            v[j + 3] *= sx * f.w;
+        }
+    }
+    if (b != nullptr) {
+#pragma unroll
+        for (int j = 0; j < 32; j += 8) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(static_cast<const O *>(b) + col + j);
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = unpack2<O>(w[i]);
+                v[j + 2 * i] += f.x;
+                v[j + 2 * i + 1] += f.y;
+            }
+        }
+    }
+}
+
+// 16 gates and their factors of this lane's row into the warp's staging block: row r's
+// 16-byte chunk j (0 to 3 the gates, 4 to 7 the factors) at j ^ (r & 7) of its 128 bytes.
+__device__ __forceinline__ void stage_pair16(uint32_t stage, int lane, const float *g,
+                                             const float *u) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        tc::st_shared_v4(stage + (uint32_t)lane * 128u + ((uint32_t)(j ^ (lane & 7)) << 4),
+                         g[4 * j], g[4 * j + 1], g[4 * j + 2], g[4 * j + 3]);
+        tc::st_shared_v4(stage + (uint32_t)lane * 128u + ((uint32_t)((4 + j) ^ (lane & 7)) << 4),
+                         u[4 * j], u[4 * j + 1], u[4 * j + 2], u[4 * j + 3]);
+    }
+}
+
+// The gated epilogue on the first `rows` rows (from row0 on) of such a block: a
+// column a lane, the warp's halves four rows apart (which meet no bank twice), U rows
+// (4 or 8) in flight.
+template <class O, int U>
+__device__ __forceinline__ void finish_gated_staged(const GatedEpi &e, uint32_t stage, int lane,
+                                                    int row0, int rows, int col0) {
+    static_assert(U == 4 || U == 8, "rows of a turn");
+    const int col = col0 + (lane & 15), far = (lane >> 4) * 4;
+    if (col >= e.N) return;
+    GatedTerms<O, 1> t;
+    t.load(e, col);
+#pragma unroll 1
+    for (int r0 = 0; r0 < rows; r0 += 2 * U) {
+        float g[U], u[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int r = r0 + far + (i & 3) + 8 * (i >> 2);
+            const uint32_t line = stage + (uint32_t)r * 128u + (uint32_t)((lane & 3) * 4);
+            const int c = (lane & 15) >> 2;
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(g[i])
+                         : "r"(line + ((uint32_t)(c ^ (r & 7)) << 4)) : "memory");
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(u[i])
+                         : "r"(line + ((uint32_t)((4 + c) ^ (r & 7)) << 4)) : "memory");
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int r = r0 + far + (i & 3) + 8 * (i >> 2);
+            const float sx = e.sx != nullptr && r < rows ? e.sx[row0 + r] : 1.f;
+            g[i] = fmaf(g[i], sx * t.sg[0], t.bg[0]);
+            u[i] = fmaf(u[i], sx * t.su[0], t.bu[0]);
+        }
+        auto store = [&](void *base, int64_t ld, const float (&x)[U]) {
+            O *p = static_cast<O *>(base) + row0 * ld + col;
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int r = r0 + far + (i & 3) + 8 * (i >> 2);
+                if (r < rows) p[r * ld] = from_f32<O>(x[i]);
+            }
+        };
+        if (e.Zg != nullptr) store(e.Zg, e.ldg, g);
+        if (e.Zu != nullptr) store(e.Zu, e.ldu, u);
+        activate_all<O>(g, e.act);
+#pragma unroll
+        for (int i = 0; i < U; ++i) g[i] *= u[i];
+        store(e.H, e.ldh, g);
+    }
+}
+
+// join_parts of a gated tile: the two groups of four accumulator columns that a lane
+// adds up are a group's gates and their factors.
+template <int PARTS, int CTAS, int BN, class O>
+__device__ __forceinline__ void join_parts(const GatedEpi &e, uint32_t ring, int part, int half,
+                                           int m0, int n0, int rows) {
+    constexpr int LPR = BN / 8, RPW = 32 / LPR;   // lanes a row, rows a warp
+    constexpr int STEP = kThreads / 32 * RPW * PARTS;
+    constexpr int U = PARTS == 2 ? 4 : PARTS == 8 ? 1 : 2;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int c = lane % LPR;
+    const int col = n0 + 4 * c;
+    if (col >= e.N) return;
+    GatedTerms<O, 4> t;
+    t.load(e, col);
+    uint32_t base[PARTS];
+#pragma unroll
+    for (int j = 0; j < PARTS; ++j) base[j] = cluster_addr(ring, CTAS * j + half);
+    for (int r0 = (warp * PARTS + part) * RPW + lane / LPR; r0 < rows; r0 += U * STEP) {
+        float4 x[U][2][PARTS];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int r = r0 + u * STEP;
+            if (r >= rows) break;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t at = (uint32_t)(r * BN * 4) +
+                                    ((uint32_t)((c + h * LPR) ^ (r & 7)) << 4);
+#pragma unroll
+                for (int j = 0; j < PARTS; ++j) x[u][h][j] = ld_cluster_v4(base[j] + at);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int r = r0 + u * STEP;
+            if (r >= rows) break;
+            float v[2][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float4 s = x[u][h][0];
+#pragma unroll
+                for (int j = 1; j < PARTS; ++j) {
+                    s.x += x[u][h][j].x;
+                    s.y += x[u][h][j].y;
+                    s.z += x[u][h][j].z;
+                    s.w += x[u][h][j].w;
+                }
+                v[h][0] = s.x;
+                v[h][1] = s.y;
+                v[h][2] = s.z;
+                v[h][3] = s.w;
+            }
+            finish_gated_group<O, 4>(e, t, m0 + r, col, v[0], v[1]);
+        }
+    }
+}
+
 // ------------------------------------------------------------------ host side
 
 inline CUtensorMapDataType map_type(int type) {
@@ -320,6 +491,13 @@ cudaError_t capacity(Capacity &cap);   // linear_tc.cu
 struct Piece {
     int tile0, tiles, parts, room;
 };
+
+// CTAs of a launch.
+template <int CTAS, bool SPLIT>
+long long ctas_of(const Piece &piece) {
+    const long long most = piece.room < piece.tiles ? piece.room : piece.tiles;
+    return CTAS * (SPLIT ? (long long)piece.tiles * piece.parts : most);
+}
 
 // Tiles of ctas * 128 x bn; a kernel is built for a few shapes.
 struct TileShape {
