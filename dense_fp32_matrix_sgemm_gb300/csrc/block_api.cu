@@ -126,7 +126,7 @@ GatedBackward gated_backward_plan(int dtype, int64_t M, int64_t N, int64_t K, co
     GatedBackward p = {};
     const int size = dtype_size(dtype);
     const int64_t wr = transW ? N : K, wc = transW ? K : N;
-    p.parts = grad_parts(M, N);
+    p.parts = gated_parts(dtype, M, N);
     if (db) p.part_bytes = round256((size_t)p.parts * 2 * N * sizeof(float));
     if (K == 0) return p;
     if (dtype == SGEMM_F32) {
@@ -213,10 +213,18 @@ int gated_linear_backward(int dtype, int64_t M, int64_t N, int64_t K, const void
         if (dx && e == cudaSuccess) e = place(Wg, ldwg, wr, wc, size, ws, s);
         if (dx && e == cudaSuccess) e = place(Wu, ldwu, wr, wc, size, ws, s);
     }
-    int left = (int)dx + (int)dwg + (int)dwu + (int)db, done = 0;
+    int left = (int)dx + (int)dwg + (int)dwu + (int)db, done = 0, half = 0;
+    if (dx && dwg && dwu && gated_side_by_side(dtype, {(int)M, (int)K, (int)N},
+                                               {(int)wr, (int)wc, (int)M}))
+        half = kChainHalf;
+    if (!dx && dwg && dwu) {
+        const ProductSize one = {(int)wr, (int)wc, (int)M};
+        if (f32 ? linear_f32_side_by_side(one, one) : linear_tc_side_by_side(dtype, one, one))
+            half = kChainHalf;
+    }
     auto place_in_chain = [&] {
         --left;
-        return (done++ > 0 ? kChainPrev : 0) | (left > 0 ? kChainNext : 0);
+        return (done++ > 0 ? kChainPrev : 0) | (left > 0 ? kChainNext : 0) | half;
     };
     if (dx && e == cudaSuccess) {
         const LayerEpi epi = plain_epi(dtype, dX, lddx, M, K);

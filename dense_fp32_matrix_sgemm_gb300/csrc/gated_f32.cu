@@ -94,6 +94,14 @@ constexpr Costs<3> kByInput = {{{2, 256}, {2, 128}, {1, 128}}, {1.66, 0.89, 1.05
                                {5.0, 3.0, 3.0}};
 
 }  // namespace f32
+
+bool f32_three_side_by_side(const ProductSize &sum, const ProductSize &product,
+                            const Capacity &cap) {
+    const int bk = f32::kBk;
+    return three_side_by_side({sum.M, sum.N, 2 * ((sum.K + bk - 1) / bk * bk)}, product, bk, cap,
+                              f32::kCosts);
+}
+
 }  // namespace ltc
 
 cudaError_t launch_gated_f32(const F32Planes &X, const F32Planes &Wg, const F32Planes &Wu, int K,
@@ -123,6 +131,7 @@ cudaError_t launch_sum_f32(const F32Planes (&A)[2], const F32Planes (&B)[2], int
     Capacity cap;
     cudaError_t e = capacity(cap);
     if (e != cudaSuccess) return e;
+    if (chain & kChainHalf) cap = cap.half();
     const Plan plan = plan_tiles(epi.M, epi.N, 2 * ((K + f32::kBk - 1) / f32::kBk), cap, f32::kCosts);
     return run_plan(f32::kCosts, plan, chain, [&](auto w, auto split, const Piece &p, int at) {
         constexpr TileShape t = f32::kCosts.shape[w()];

@@ -134,6 +134,7 @@ cudaError_t sum_dispatch(int type, const TcOperand (&A)[2], const TcOperand (&B)
     Capacity cap;
     cudaError_t e = capacity(cap);
     if (e != cudaSuccess) return e;
+    if (chain & kChainHalf) cap = cap.half();
     const int bk = kRowBytes / dtype_size(type);
     const Plan plan = plan_tiles(epi.M, epi.N, 2 * ((K + bk - 1) / bk), cap, kByFeature);
     return run_plan(kByFeature, plan, chain, [&](auto w, auto split, const Piece &p, int at) {
@@ -143,6 +144,16 @@ cudaError_t sum_dispatch(int type, const TcOperand (&A)[2], const TcOperand (&B)
 }
 
 }  // namespace ltc
+
+bool gated_side_by_side(int in_type, const ProductSize &sum, const ProductSize &product) {
+    using namespace ltc;
+    Capacity cap;
+    if (capacity(cap) != cudaSuccess) return false;
+    if (in_type == SGEMM_F32) return f32_three_side_by_side(sum, product, cap);
+    const int bk = kRowBytes / dtype_size(in_type);
+    return three_side_by_side({sum.M, sum.N, 2 * ((sum.K + bk - 1) / bk * bk)}, product, bk, cap,
+                              kByFeature);
+}
 
 cudaError_t launch_gated_tc(int in_type, const TcOperand &X, const TcOperand &Wg,
                             const TcOperand &Wu, int K, const GatedEpi &epi, cudaStream_t s) {

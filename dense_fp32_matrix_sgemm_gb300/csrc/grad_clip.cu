@@ -11,10 +11,11 @@
 // that never cross a tensor; a CTA takes a run of consecutive chunks, forward in the sum and
 // backward in the scaling, so that what each CTA read last, which L2 (129 MB) still holds, is
 // read first.
-// A thread adds the squares of 16 to 64 elements in fp32 and adds that sum to a running sum
-// in 64 bits (one such addition for all of them).  Where the fp32 sum has left the range
-// in which it is exact to rounding (elements beyond 1e15, or all below 1e-12), the thread forms it
-// again in 64 bits from the same registers.  CTAs' sums are stored in 64 bits and added in
+// A warp adds the squares of its 512 to 1024 elements of a chunk in fp32 and its first lane
+// adds that sum to a running one in 64 bits: 64-bit additions run at two a clock and SM here, so
+// one a thread instead of one a warp was felt (12 MB in 28 tensors 22.9 us).  Where the fp32 sum
+// has left the range in which it is exact to rounding (elements beyond 1e15, or all below 1e-12), the warp
+// forms it again in 64 bits from the same registers.  CTAs' sums are stored in 64 bits and added in
 // a fixed order by every CTA of the second launch: no atomics, the same bits every time.
 #include <cstdint>
 #include <type_traits>
@@ -28,205 +29,264 @@
 namespace sgemm {
 namespace clip {
 
-constexpr int kThreads = 256;
-constexpr int kAccesses = 8;                            // of 16 bytes, in flight a thread
+constexpr int kThreads = 512;
+constexpr int kCtas = 152 * 2;                          // of a launch at most: two an SM
+constexpr int kAccesses = 4;                            // of 16 bytes, in flight a thread
 constexpr int kChunk = kThreads * 16 * kAccesses;       // bytes
 
-// One tensor of a launch.  Elements are counted from the 16-byte boundary at or below its
-// first one: it holds those from `shift` to `end`.
+// One tensor of a launch.  Bytes are counted from the 16-byte boundary at or below its first
+// element: it holds those from `lo` to `hi`.
 struct Tensor {
     const char *x;   // that boundary
-    char *y;         // the same place of the result: x + anything; null: not scaled
-    int64_t end;
+    char *y;         // the same place of the result
+    int64_t hi;
     int first;       // chunks before it in this launch
-    uint8_t type, shift, same;   // same: y's boundary is one too
+    uint8_t type, lo, same;   // same: y's boundary is one too
 };
+// start[b]: the tensor that CTA b's first chunk is in (a search would be dependent reads of
+// arguments that no cache holds yet).
 template <int MOST>
 struct Table {
     int count, chunks;   // tensors, chunks
+    uint16_t start[kCtas + 1];
     Tensor t[MOST];
 };
 // a kernel's arguments may take 32764 bytes
 constexpr int kMost = 1000;
 static_assert(sizeof(Table<kMost>) <= 32700, "kernel arguments");
 
-// The tensor of the table that chunk c is in.
-template <int MOST>
-__device__ __forceinline__ int tensor_of(const Table<MOST> &table, int c) {
-    int lo = 0, hi = table.count - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (table.t[mid].first <= c) lo = mid;
-        else hi = mid - 1;
-    }
-    return lo;
+__host__ __device__ inline int first_chunk(int chunks, int cta, int ctas) {
+    return (int)((int64_t)chunks * cta / ctas);
 }
 
-// f(tensor, first element of the chunk) for this CTA's chunks, forward or backward.
-template <bool BACK, int MOST, class F>
-__device__ __forceinline__ void for_chunks(const Table<MOST> &table, F f) {
-    const int c0 = (int)((int64_t)table.chunks * blockIdx.x / gridDim.x);
-    const int c1 = (int)((int64_t)table.chunks * (blockIdx.x + 1) / gridDim.x);
-    if (c0 >= c1) return;
-    int i = tensor_of(table, BACK ? c1 - 1 : c0);
-    for (int k = 0; k < c1 - c0; ++k) {
-        const int c = BACK ? c1 - 1 - k : c0 + k;
+// This CTA's chunks, one after another, forward or backward: the chunk's tensor and where in
+// it the chunk begins.
+template <bool BACK, int MOST>
+struct Walk {
+    const Table<MOST> &table;
+    int c, left, i;
+    __device__ __forceinline__ explicit Walk(const Table<MOST> &t) : table(t) {
+        const int c0 = first_chunk(t.chunks, blockIdx.x, gridDim.x);
+        const int c1 = first_chunk(t.chunks, blockIdx.x + 1, gridDim.x);
+        left = c1 - c0;
+        c = BACK ? c1 - 1 : c0;
+        i = t.start[blockIdx.x + (BACK ? 1 : 0)];
+        if (left > 0) settle();
+    }
+    __device__ __forceinline__ void settle() {
         if (BACK) {
             while (table.t[i].first > c) --i;
         } else {
             while (i + 1 < table.count && table.t[i + 1].first <= c) ++i;
         }
-        const Tensor &t = table.t[i];
-        f(t, (int64_t)(c - t.first) * (t.type == SGEMM_F32 ? kChunk / 4 : kChunk / 2));
     }
-}
+    __device__ __forceinline__ const Tensor &tensor() const { return table.t[i]; }
+    __device__ __forceinline__ int64_t base() const {
+        return (int64_t)(c - table.t[i].first) * kChunk;
+    }
+    __device__ __forceinline__ void next() {
+        c += BACK ? -1 : 1;
+        if (--left > 0) settle();
+    }
+};
 
-// W elements from `at` on, those that the tensor has (others are 0).
-template <class T>
-struct Piece {
-    static constexpr int W = 16 / sizeof(T);
-    Raw<T, W> raw;
-    __device__ __forceinline__ void load(const Tensor &t, int64_t at) {
-        const T *x = reinterpret_cast<const T *>(t.x);
-        if (at >= t.shift && at + W <= t.end) {
-            raw.u = __ldcg(reinterpret_cast<const uint4 *>(x + at));
-        } else {
-            float f[W];
+// This thread's pieces of a chunk, as loaded; bytes that the tensor has not are 0.
+struct Pieces {
+    uint4 u[kAccesses];
+    template <bool LAST>   // (not to be read again)
+    __device__ __forceinline__ void load(const Tensor &t, int64_t base) {
+        const int64_t at = base + threadIdx.x * 16;
 #pragma unroll
-            for (int j = 0; j < W; ++j)
-                f[j] = at + j >= t.shift && at + j < t.end ? to_f32(x[at + j]) : 0.f;
-            if constexpr (W == 4)
-                raw.u = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]),
-                                   __float_as_uint(f[2]), __float_as_uint(f[3]));
-            else
-                raw.u = make_uint4(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]), pack2<T>(f[4], f[5]),
-                                   pack2<T>(f[6], f[7]));
+        for (int i = 0; i < kAccesses; ++i) {
+            const int64_t b = at + i * kThreads * 16;
+            const uint4 *p = reinterpret_cast<const uint4 *>(t.x + b);
+            u[i] = make_uint4(0, 0, 0, 0);
+            if (b >= t.lo && b + 16 <= t.hi)
+                u[i] = LAST ? __ldcs(p) : __ldcg(p);
+            else if (b < t.hi && b + 16 > t.lo)
+                u[i] = part(t, b);
         }
+    }
+    // (every type's elements are made of whole 2-byte halves)
+    __device__ __noinline__ static uint4 part(const Tensor &t, int64_t b) {
+        uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int h = 0; h < 8; ++h)
+            if (b + 2 * h >= t.lo && b + 2 * h < t.hi)
+                w[h / 2] |= (uint32_t)*reinterpret_cast<const uint16_t *>(t.x + b + 2 * h)
+                            << (16 * (h % 2));
+        return make_uint4(w[0], w[1], w[2], w[3]);
     }
 };
 
 template <class T>
-__device__ __forceinline__ double chunk_squares(const Tensor &t, int64_t base) {
-    using P = Piece<T>;
-    P p[kAccesses];
+__device__ __forceinline__ void values(uint4 u, float (&f)[16 / sizeof(T)]) {
+    Raw<T, 16 / sizeof(T)> r;
+    r.u = u;
+    r.get(f);
+}
+
+// d summed over the warp in a fixed order, in each of its lanes.
+__device__ __forceinline__ double warp_sum(double d) {
+    if (!__any_sync(0xffffffffu, d != 0.0)) return 0.0;
 #pragma unroll
-    for (int i = 0; i < kAccesses; ++i) p[i].load(t, base + (i * kThreads + threadIdx.x) * P::W);
+    for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+    return d;
+}
+
+// The sum of squares of the warp's elements of a chunk.
+template <class T>
+__device__ __forceinline__ double chunk_squares(const Pieces &p) {
+    constexpr int W = 16 / sizeof(T);
     float s[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < kAccesses; ++i) {
-        float f[P::W];
-        p[i].raw.get(f);
+        float f[W];
+        values<T>(p.u[i], f);
 #pragma unroll
-        for (int j = 0; j < P::W; ++j) s[j & 1] = fmaf(f[j], f[j], s[j & 1]);
+        for (int j = 0; j < W; ++j) s[j & 1] = fmaf(f[j], f[j], s[j & 1]);
     }
-    const float sum = s[0] + s[1];
+    float sum = s[0] + s[1];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     // Below 2^-80 squares of elements may have lost their digits, from 2^100 on they may have
     // passed fp32's range.  (f16's squares, from 2^-48 to 2^32, do neither.)
     if constexpr (!std::is_same<T, __half>::value) {
-        if (!(sum >= 0x1p-80f && sum < 0x1p100f)) {
+        if (!(sum >= 0x1p-80f && sum < 0x1p100f)) {   // (the same in every lane)
+            // (past a tensor's end there are zeros: fetching the code below for them was half of a
+            // small list's time)
+            uint32_t any = 0;
+#pragma unroll
+            for (int i = 0; i < kAccesses; ++i) any |= p.u[i].x | p.u[i].y | p.u[i].z | p.u[i].w;
+            if (!__any_sync(0xffffffffu, any != 0)) return 0.0;
             double d = 0.0;
 #pragma unroll
             for (int i = 0; i < kAccesses; ++i) {
-                float f[P::W];
-                p[i].raw.get(f);
+                float f[W];
+                values<T>(p.u[i], f);
 #pragma unroll
-                for (int j = 0; j < P::W; ++j)
+                for (int j = 0; j < W; ++j)
                     if (f[j] != 0.f) d = fma((double)f[j], (double)f[j], d);   // (a NaN is not 0)
             }
-            return d;
+            return warp_sum(d);
         }
     }
     return (double)sum;
 }
 
-// d summed over the CTA, in each of its threads; in a fixed order.
-__device__ __forceinline__ double block_sum(double d, double *red) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = d;
-    __syncthreads();
-    double s = 0.0;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) s += red[w];
-    return s;
-}
-
-// partial[blockIdx.x] = the sum of squares of this CTA's chunks.
+// partial[blockIdx.x] = the sum of squares of this CTA's chunks.  A chunk's loads are issued
+// before the one before it is summed.
 template <int MOST>
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kThreads, 2)
 squares_kernel(const __grid_constant__ Table<MOST> table, double *partial) {
     __shared__ double red[kThreads / 32];
     pdl_trigger();
     pdl_wait();
     double d = 0.0;
-    for_chunks<false>(table, [&](const Tensor &t, int64_t base) {
-        switch (t.type) {
-            case SGEMM_F32: d += chunk_squares<float>(t, base); break;
-            case SGEMM_BF16: d += chunk_squares<__nv_bfloat16>(t, base); break;
-            default: d += chunk_squares<__half>(t, base); break;
+    const bool first = (threadIdx.x & 31) == 0;
+    Walk<false, MOST> w(table);
+    Pieces p, ahead;
+    if (w.left > 0) ahead.load<false>(w.tensor(), w.base());
+    while (w.left > 0) {
+        const int type = w.tensor().type;
+        p = ahead;
+        w.next();
+        if (w.left > 0) ahead.load<false>(w.tensor(), w.base());
+        double s;
+        switch (type) {
+            case SGEMM_F32: s = chunk_squares<float>(p); break;
+            case SGEMM_BF16: s = chunk_squares<__nv_bfloat16>(p); break;
+            default: s = chunk_squares<__half>(p); break;
         }
-    });
-    const double s = block_sum(d, red);
-    if (threadIdx.x == 0) partial[blockIdx.x] = s;
+        if (first) d += s;
+    }
+    if (first) red[threadIdx.x >> 5] = d;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        const double s = warp_sum(threadIdx.x < kThreads / 32 ? red[threadIdx.x] : 0.0);
+        if (threadIdx.x == 0) partial[blockIdx.x] = s;
+    }
 }
 
 template <class T>
-__device__ __forceinline__ void scale_chunk(const Tensor &t, int64_t base, float coef,
-                                            float rest) {
-    using P = Piece<T>;
-    P p[kAccesses];
-#pragma unroll
-    for (int i = 0; i < kAccesses; ++i) p[i].load(t, base + (i * kThreads + threadIdx.x) * P::W);
-    T *const y = reinterpret_cast<T *>(t.y);
+__device__ __forceinline__ void scale_chunk(const Pieces &p, const Tensor &t, int64_t base,
+                                            float2 factor) {
+    constexpr int W = 16 / sizeof(T);
+    const int64_t first = base + threadIdx.x * 16;
 #pragma unroll
     for (int i = 0; i < kAccesses; ++i) {
-        const int64_t at = base + (i * kThreads + threadIdx.x) * P::W;
-        if (at >= t.end) continue;
-        float f[P::W];
-        p[i].raw.get(f);
+        const int64_t at = first + i * kThreads * 16;
+        if (at >= t.hi) continue;
+        float f[W];
+        values<T>(p.u[i], f);
 #pragma unroll
-        for (int j = 0; j < P::W; ++j) f[j] = f[j] * coef * rest;
-        if (t.same && at >= t.shift && at + P::W <= t.end) {
-            put<T, P::W>(y + at, f);
+        for (int j = 0; j < W; ++j) f[j] = f[j] * factor.x * factor.y;
+        if (t.same && at >= t.lo && at + 16 <= t.hi) {
+            Raw<T, W> r;
+            put<T, W>(reinterpret_cast<T *>(&r), f);
+            __stcs(reinterpret_cast<uint4 *>(t.y + at), r.u);
         } else {
 #pragma unroll
-            for (int j = 0; j < P::W; ++j)
-                if (at + j >= t.shift && at + j < t.end) y[at + j] = from_f32<T>(f[j]);
+            for (int j = 0; j < W; ++j) {
+                const int64_t b = at + j * (int)sizeof(T);
+                if (b >= t.lo && b < t.hi) *reinterpret_cast<T *>(t.y + b) = from_f32<T>(f[j]);
+            }
         }
     }
 }
 
 // The norm from all CTAs' sums (*norm, by the first CTA), and this CTA's chunks scaled.
 template <int MOST>
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kThreads, 2)
 scale_kernel(const __grid_constant__ Table<MOST> table, const double *partial, int parts,
              float max_norm, float eps, float *norm) {
-    __shared__ double red[kThreads / 32];
+    __shared__ float2 shared_factor;
     pdl_trigger();
     pdl_wait();
-    double d = 0.0;
-    for (int i = threadIdx.x; i < parts; i += kThreads) d += __ldcg(partial + i);
-    const double n = sqrt(block_sum(d, red));
-    if (norm != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)n;
-    const double c = (double)max_norm / (n + (double)eps);
-    // (a NaN stays one; a factor that fp32 holds with few digits, for norms beyond 1e36 times
-    // max_norm, is applied in two steps)
-    const bool tiny = c < 0x1p-120;
-    const float coef = c > 1.0 ? 1.f : (float)(tiny ? c * 0x1p64 : c);
-    const float rest = tiny ? 0x1p-64f : 1.f;
-    for_chunks<true>(table, [&](const Tensor &t, int64_t base) {
-        if (coef == 1.f && t.y == t.x) return;   // in place: unchanged
-        switch (t.type) {
-            case SGEMM_F32: scale_chunk<float>(t, base, coef, rest); break;
-            case SGEMM_BF16: scale_chunk<__nv_bfloat16>(t, base, coef, rest); break;
-            default: scale_chunk<__half>(t, base, coef, rest); break;
+    if (threadIdx.x < 32) {
+        constexpr int U = 10;   // in flight; a launch's sums of CTAs in one go
+        double d = 0.0;
+        for (int i = threadIdx.x; i < parts; i += 32 * U) {
+            double x[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                x[u] = i + 32 * u < parts ? __ldcg(partial + i + 32 * u) : 0.0;
+#pragma unroll
+            for (int u = 0; u < U; ++u) d += x[u];
         }
-    });
+        const double n = sqrt(warp_sum(d));
+        if (threadIdx.x == 0) {
+            if (norm != nullptr && blockIdx.x == 0) *norm = (float)n;
+            const double c = (double)max_norm / (n + (double)eps);
+            // (a NaN stays one; a factor that fp32 holds with few digits, for norms beyond
+            // 1e36 times max_norm, is applied in two steps)
+            const bool tiny = c < 0x1p-120;
+            shared_factor = make_float2(c > 1.0 ? 1.f : (float)(tiny ? c * 0x1p64 : c),
+                                        tiny ? 0x1p-64f : 1.f);
+        }
+    }
+    Walk<true, MOST> w(table);
+    Pieces p;
+    if (w.left > 0) p.load<true>(w.tensor(), w.base());
+    __syncthreads();
+    const float2 factor = shared_factor;
+    auto changes = [&](const Tensor &t) { return !(factor.x == 1.f && t.y == t.x); };
+    while (w.left > 0) {
+        const Tensor &t = w.tensor();
+        const int64_t base = w.base();
+        if (changes(t)) {
+            switch (t.type) {
+                case SGEMM_F32: scale_chunk<float>(p, t, base, factor); break;
+                case SGEMM_BF16: scale_chunk<__nv_bfloat16>(p, t, base, factor); break;
+                default: scale_chunk<__half>(p, t, base, factor); break;
+            }
+        }
+        w.next();
+        if (w.left > 0 && changes(w.tensor())) p.load<true>(w.tensor(), w.base());
+    }
 }
 
 // ------------------------------------------------------------------ host side
-
-constexpr int kCtas = 152 * 4;   // of a launch at most
 
 template <class... P, class... A>
 cudaError_t launch(void (*kernel)(P...), int grid, cudaStream_t s, const A &...args) {
@@ -242,6 +302,8 @@ cudaError_t launch(void (*kernel)(P...), int grid, cudaStream_t s, const A &...a
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+int grid_of(int chunks) { return chunks < kCtas ? chunks : kCtas; }
+
 // Tensors first .. of the list, as many as a table takes, without the empty ones; returns the
 // next one's number.
 template <int MOST>
@@ -251,30 +313,33 @@ int64_t fill(Table<MOST> &table, int64_t first, int64_t count, const int *types,
     int64_t i = first;
     for (; i < count && table.count < MOST; ++i) {
         if (sizes[i] == 0) continue;
-        const int size = dtype_size(types[i]), per = kChunk / size;
         Tensor &t = table.t[table.count];
         const uintptr_t x = reinterpret_cast<uintptr_t>(X[i]);
         const uintptr_t y = Y != nullptr ? reinterpret_cast<uintptr_t>(Y[i]) : x;
         const int off = (int)(x % 16);
-        const int64_t end = sizes[i] + off / size, chunks = (end + per - 1) / per;
+        const int64_t hi = off + sizes[i] * dtype_size(types[i]), chunks = (hi + kChunk - 1) / kChunk;
         if (table.chunks + chunks > 0x7fffffff) {
             if (table.count == 0) return -1;
             break;
         }
         t.x = reinterpret_cast<const char *>(x - off);
         t.y = reinterpret_cast<char *>(y - off);
-        t.end = end;
+        t.hi = hi;
         t.first = table.chunks;
         t.type = (uint8_t)types[i];
-        t.shift = (uint8_t)(off / size);
+        t.lo = (uint8_t)off;
         t.same = (y - off) % 16 == 0;
         table.chunks += (int)chunks;
         ++table.count;
     }
+    const int ctas = grid_of(table.chunks);
+    for (int b = 0, k = 0; b <= ctas && table.count > 0; ++b) {
+        const int c = first_chunk(table.chunks, b, ctas);
+        while (k + 1 < table.count && table.t[k + 1].first <= c) ++k;
+        table.start[b] = (uint16_t)k;
+    }
     return i;
 }
-
-int grid_of(int chunks) { return chunks < kCtas ? chunks : kCtas; }
 
 template <int MOST>
 cudaError_t run(int64_t count, const int *types, const int64_t *sizes, const void *const *X,
@@ -296,6 +361,7 @@ cudaError_t run(int64_t count, const int *types, const int64_t *sizes, const voi
     const double *sums = partial;
     if (Y == nullptr || parts == 0) {
         table.count = table.chunks = 0;
+        table.start[0] = table.start[1] = 0;
         return launch(scale_kernel<MOST>, 1, s, table, sums, parts, max_norm, eps, norm);
     }
     i = 0;

@@ -80,6 +80,10 @@ cudaError_t launch_gated_rows(int in_type, const void *X, int64_t ldx, const voi
                               const void *Wu, int64_t ldwu, int K, const GatedEpi &epi,
                               cudaStream_t s);
 
+// Whether the gated layer's gradients are better planned for half of the SMs each: the
+// sum of two products (K: of each) and two products alike.
+bool gated_side_by_side(int in_type, const ProductSize &sum, const ProductSize &product);
+
 // Whether two products of a chain are better run side by side than in turn.
 bool linear_tc_side_by_side(int in_type, const ProductSize &a, const ProductSize &b);
 bool linear_f32_side_by_side(const ProductSize &a, const ProductSize &b);
@@ -136,7 +140,8 @@ cudaError_t launch_column_sum(int type, const float *partial, int parts, int64_t
                               int chain, cudaStream_t s);
 
 // The gated layer's dZg = dH Zu act'(Zg) and dZu = dH act(Zg) (f32 with plane > 0: as
-// planes) with partial column sums of both, `parts` (grad_parts) rows of 2 N floats.  gated_grad.cu
+// planes) with partial column sums of both, `parts` rows of 2 N floats.  gated_grad.cu
+int gated_parts(int type, int64_t M, int64_t N);
 cudaError_t launch_gated_dz(int type, const void *dH, int64_t lddh, const void *Zg, int64_t ldzg,
                             const void *Zu, int64_t ldzu, int act, int M, int N, void *dZg,
                             void *dZu, int64_t lddz, int64_t plane, float *partial, int chain,

@@ -361,15 +361,20 @@ __device__ __forceinline__ void linear_f32_body(const Maps &map, const Params<E>
                                      run[4 * j], run[4 * j + 1], run[4 * j + 2], run[4 * j + 3]);
                 }
             } else if constexpr (FORM == kGated) {
+                // 16 outputs at a time, in a rolled loop (its code is fetched once): the first 16
+                // gates and factors leave, the others move down
                 const int rows = min(32, p.epi.M - row0);
-#pragma unroll
-                for (int c = 0; c < OUT / 32; ++c) {   // 16 outputs at a time
-                    if (n0 + 16 * c >= p.epi.N) break;
+#pragma unroll 1
+                for (int c = 0; c < OUT / 32 && n0 + 16 * c < p.epi.N; ++c) {
                     __syncwarp();   // the previous block has been read
-                    stage_pair16(stage, lane, run + 16 * c, run + OUT / 2 + 16 * c);
+                    stage_pair16(stage, lane, run, run + OUT / 2);
                     __syncwarp();
-                    finish_gated_staged<float, BN == 256 ? 4 : 8>(p.epi, stage, lane, row0, rows,
-                                                                  n0 + 16 * c);
+#pragma unroll
+                    for (int j = 0; j + 16 < OUT / 2; ++j) {
+                        run[j] = run[j + 16];
+                        run[OUT / 2 + j] = run[OUT / 2 + j + 16];
+                    }
+                    finish_gated_staged<float, 8>(p.epi, stage, lane, row0, rows, n0 + 16 * c);
                 }
             } else {
                 const int rows = min(32, p.epi.M - row0);

@@ -362,9 +362,7 @@ __device__ __forceinline__ void finish_gated_staged(const GatedEpi &e, uint32_t 
         };
         if (e.Zg != nullptr) store(e.Zg, e.ldg, g);
         if (e.Zu != nullptr) store(e.Zu, e.ldu, u);
-        activate_all<O>(g, e.act);
-#pragma unroll
-        for (int i = 0; i < U; ++i) g[i] *= u[i];
+        gate_all<O>(g, u, e.act);
         store(e.H, e.ldh, g);
     }
 }
@@ -577,6 +575,26 @@ bool side_by_side(const ProductSize &a, const ProductSize &b, int k_stage, const
     const double ha = us(a, half), hb = us(b, half);
     return (ha > hb ? ha : hb) < us(a, cap) + us(b, cap) - 4.0;
 }
+
+// Three products of a chain, the second and the third alike: planned for half of the SMs
+// each, two run at a time, and the time is that of the longest or half of them all.  For
+// products that leave SMs idle: those that fill them lose what they share in L2 (gradients of
+// 4096 x 8192 x 4096 bf16 660 us in turn, 830 so; of 500 x 777 x 1001 f32 45.7 and 42.6).
+template <int SHAPES>
+bool three_side_by_side(const ProductSize &a, const ProductSize &b, int k_stage,
+                        const Capacity &cap, const Costs<SHAPES> &cost) {
+    auto us = [&](const ProductSize &p, const Capacity &c) {
+        return plan_tiles(p.M, p.N, (p.K + k_stage - 1) / k_stage, c, cost).us;
+    };
+    const Capacity half = cap.half();
+    if (half.clusters[0] < 1) return false;
+    const double ha = us(a, half), hb = us(b, half), in_turn = us(a, cap) + 2 * us(b, cap) - 8.0;
+    const double all = ha + 2 * hb > 2 * ha ? (ha + 2 * hb) / 2 : ha;
+    return (all > hb ? all : hb) < 0.9 * in_turn;
+}
+
+bool f32_three_side_by_side(const ProductSize &sum, const ProductSize &product,
+                            const Capacity &cap);   // gated_f32.cu
 
 // f(w as a constant).
 template <int W, int SHAPES, class F>

@@ -195,9 +195,7 @@ __device__ __forceinline__ void finish_gated_rows(const Params<GatedEpi> &p, con
                 tc::bulk_commit_group();
             }
         }
-        activate_all<O>(v, e.act);
-#pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] *= u[j];
+        gate_all<O>(v, u, e.act);
         if (e.Zg != nullptr || e.Zu != nullptr) {
             if (lane == 0) tc::bulk_wait_group_read<0>();
             __syncwarp();
