@@ -93,7 +93,6 @@ struct Walk {
 // This thread's pieces of a chunk, as loaded; bytes that the tensor has not are 0.
 struct Pieces {
     uint4 u[kAccesses];
-    template <bool LAST>   // (not to be read again)
     __device__ __forceinline__ void load(const Tensor &t, int64_t base) {
         const int64_t at = base + threadIdx.x * 16;
 #pragma unroll
@@ -102,7 +101,7 @@ struct Pieces {
             const uint4 *p = reinterpret_cast<const uint4 *>(t.x + b);
             u[i] = make_uint4(0, 0, 0, 0);
             if (b >= t.lo && b + 16 <= t.hi)
-                u[i] = LAST ? __ldcs(p) : __ldcg(p);
+                u[i] = __ldcg(p);
             else if (b < t.hi && b + 16 > t.lo)
                 u[i] = part(t, b);
         }
@@ -134,6 +133,23 @@ __device__ __forceinline__ double warp_sum(double d) {
     return d;
 }
 
+// The sum of squares of a thread's pieces in 64 bits.  (Not inlined: the registers it takes
+// would leave the rest of the kernel spilling, 4.1 TB/s of bf16 instead of 6.6.)
+template <class T>
+__device__ __noinline__ double wide_squares(uint4 a, uint4 b, uint4 c, uint4 d) {
+    const uint4 u[4] = {a, b, c, d};
+    double s = 0.0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float f[16 / sizeof(T)];
+        values<T>(u[i], f);
+#pragma unroll
+        for (int j = 0; j < 16 / (int)sizeof(T); ++j)
+            if (f[j] != 0.f) s = fma((double)f[j], (double)f[j], s);   // (a NaN is not 0)
+    }
+    return s;
+}
+
 // The sum of squares of the warp's elements of a chunk.
 template <class T>
 __device__ __forceinline__ double chunk_squares(const Pieces &p) {
@@ -153,22 +169,14 @@ __device__ __forceinline__ double chunk_squares(const Pieces &p) {
     // passed fp32's range.  (f16's squares, from 2^-48 to 2^32, do neither.)
     if constexpr (!std::is_same<T, __half>::value) {
         if (!(sum >= 0x1p-80f && sum < 0x1p100f)) {   // (the same in every lane)
-            // (past a tensor's end there are zeros: fetching the code below for them was half of a
-            // small list's time)
+            // (past a tensor's end there are zeros: fetching the 64-bit code for them was half of
+            // a small list's time)
             uint32_t any = 0;
 #pragma unroll
             for (int i = 0; i < kAccesses; ++i) any |= p.u[i].x | p.u[i].y | p.u[i].z | p.u[i].w;
             if (!__any_sync(0xffffffffu, any != 0)) return 0.0;
-            double d = 0.0;
-#pragma unroll
-            for (int i = 0; i < kAccesses; ++i) {
-                float f[W];
-                values<T>(p.u[i], f);
-#pragma unroll
-                for (int j = 0; j < W; ++j)
-                    if (f[j] != 0.f) d = fma((double)f[j], (double)f[j], d);   // (a NaN is not 0)
-            }
-            return warp_sum(d);
+            static_assert(kAccesses == 4, "the arguments below");
+            return warp_sum(wide_squares<T>(p.u[0], p.u[1], p.u[2], p.u[3]));
         }
     }
     return (double)sum;
@@ -186,12 +194,12 @@ squares_kernel(const __grid_constant__ Table<MOST> table, double *partial) {
     const bool first = (threadIdx.x & 31) == 0;
     Walk<false, MOST> w(table);
     Pieces p, ahead;
-    if (w.left > 0) ahead.load<false>(w.tensor(), w.base());
+    if (w.left > 0) ahead.load(w.tensor(), w.base());
     while (w.left > 0) {
         const int type = w.tensor().type;
         p = ahead;
         w.next();
-        if (w.left > 0) ahead.load<false>(w.tensor(), w.base());
+        if (w.left > 0) ahead.load(w.tensor(), w.base());
         double s;
         switch (type) {
             case SGEMM_F32: s = chunk_squares<float>(p); break;
@@ -267,7 +275,7 @@ scale_kernel(const __grid_constant__ Table<MOST> table, const double *partial, i
     }
     Walk<true, MOST> w(table);
     Pieces p;
-    if (w.left > 0) p.load<true>(w.tensor(), w.base());
+    if (w.left > 0) p.load(w.tensor(), w.base());
     __syncthreads();
     const float2 factor = shared_factor;
     auto changes = [&](const Tensor &t) { return !(factor.x == 1.f && t.y == t.x); };
@@ -282,7 +290,7 @@ scale_kernel(const __grid_constant__ Table<MOST> table, const double *partial, i
             }
         }
         w.next();
-        if (w.left > 0 && changes(w.tensor())) p.load<true>(w.tensor(), w.base());
+        if (w.left > 0 && changes(w.tensor())) p.load(w.tensor(), w.base());
     }
 }
 

@@ -18,9 +18,11 @@
 #include <cuda_runtime.h>
 
 #include "device_utils.cuh"
+#include "gemm_args.h"
 #include "layer_math.cuh"
 #include "layers.h"
 #include "row_reduce.cuh"
+#include "tc_issue.cuh"
 
 namespace sgemm {
 namespace norm {
@@ -356,6 +358,209 @@ __global__ void __launch_bounds__(MAXT) layer_grad_kernel(const LayerGradArgs a)
     }
 }
 
+// The same where rows are long and many.  What bounded it there was the turn: about twenty
+// instructions an element, in two phases that all of an SM's warps took together.  So here
+//   - a group's rows come by bulk copies into a ring of its own in shared memory, three rows or
+//     more ahead (issued by the group's first warp), and take no registers before they are used;
+//   - groups meet in barriers of their own, so that one's sums run beside another's products;
+//   - the arithmetic is in pairs (packed fp32), the weights stay in fp32.
+// (8192 x 4096 bf16 with the stream's gradient: 55 us by the kernel above, 50 here.)
+//   full[group, stage]: a row has landed; the group's barrier of a turn, which the sums need
+//   anyway, also says that the row before it has been read to its end: its stage is filled again.
+// Waits are bounded; one that runs out raises the library's status word, and the group goes on
+// (without waiting again) to its end, as all barriers are met whatever was read.
+struct LayerRingArgs {
+    LayerGradArgs g;
+    int tpr, groups, stages;
+    unsigned *error;
+};
+constexpr int kRingThreads = 512;
+constexpr int kRingBytes = 208 * 1024;
+constexpr int kRingStages = 4;
+
+// An access's elements as pairs.
+template <class T, int W>
+__device__ __forceinline__ void pairs(const Raw<T, W> &r, float2 (&f)[W / 2]) {
+    float v[W];
+    r.get(v);
+#pragma unroll
+    for (int j = 0; j < W / 2; ++j) f[j] = make_float2(v[2 * j], v[2 * j + 1]);
+}
+
+template <class T>
+__global__ void __launch_bounds__(kRingThreads, 1) layer_grad_ring_kernel(const LayerRingArgs args) {
+    constexpr int W = 16 / sizeof(T), NV = 16 / W, P = W / 2;   // 16 columns a thread
+    const LayerGradArgs &a = args.g;
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ float red[2][2][16];
+    __shared__ uint64_t full[16 * kRingStages];
+    __shared__ int abort_word;
+    volatile int *abort = &abort_word;
+    const int tpr = args.tpr, groups = args.groups, stages = args.stages;
+    const int row_bytes = a.D * (int)sizeof(T), streams = a.dS != nullptr ? 3 : 2;
+    if (threadIdx.x < 16 * kRingStages)
+        tc::mbar_init(tc::smem_u32_generic(full + threadIdx.x), 1);
+    if (threadIdx.x == 0) *abort = 0;
+    tc::fence_barrier_init();
+    pdl_trigger();
+    __syncthreads();
+    pdl_wait();
+    const int y = threadIdx.x / tpr, x = threadIdx.x - y * tpr, warps = tpr >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const bool mine = y < groups;
+    // this group's rows row0, row0 + step, ...
+    const int64_t row0 = (int64_t)blockIdx.x * groups + y, step = (int64_t)gridDim.x * groups;
+    const int turns = mine && row0 < a.rows ? (int)((a.rows - 1 - row0) / step) + 1 : 0;
+    const uint32_t full0 = tc::smem_u32_generic(full + (mine ? y * kRingStages : 0));
+    const T *const rows = reinterpret_cast<const T *>(ring + (mine ? y : 0) * stages * streams * row_bytes);
+    auto issue = [&](int t) {   // by the group's first warp, a stream a lane
+        const int s = t % stages;
+        const int64_t row = row0 + t * step;
+        if (lane == 0) tc::mbar_arrive_expect_tx(full0 + 8 * s, (uint32_t)(streams * row_bytes));
+        __syncwarp();
+        if (lane < streams) {
+            const T *from = lane == 0   ? static_cast<const T *>(a.dY) + row * a.lddy
+                            : lane == 1 ? static_cast<const T *>(a.S) + row * a.lds
+                                        : static_cast<const T *>(a.dS) + row * a.ldds;
+            const uint32_t to = tc::smem_u32_generic(rows) + (uint32_t)((s * streams + lane) * row_bytes);
+            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes"
+                         " [%0], [%1], %2, [%3];"
+                         :: "r"(to), "l"(from), "r"(row_bytes), "r"(full0 + 8 * s) : "memory");
+        }
+        __syncwarp();
+    };
+    if (x < 32)
+        for (int t = 0; t < min(stages, turns); ++t) issue(t);
+    float2 w[NV][P], dw[NV][P], db[NV][P];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * tpr + x) * W;
+        pairs<T, W>(load_or_zero<T, W>(static_cast<const T *>(a.w) + c, mine && c < a.D), w[i]);
+#pragma unroll
+        for (int j = 0; j < P; ++j) dw[i][j] = db[i][j] = make_float2(0.f, 0.f);
+    }
+    float next_mean = 0.f, next_rstd = 0.f;
+    auto load_statistics = [&](int t) {
+        if (t >= turns) return;
+        next_mean = a.mean[row0 + t * step];
+        next_rstd = a.rstd[row0 + t * step];
+    };
+    load_statistics(0);
+    for (int t = 0; t < turns; ++t) {
+        const int64_t row = row0 + t * step;
+        const float2 mean = make_float2(-next_mean, -next_mean), rstd = make_float2(next_rstd, next_rstd);
+        load_statistics(t + 1);
+        const T *dy = rows + (t % stages) * streams * a.D, *s = dy + a.D, *ds = s + a.D;
+        (void)tc::wait(full0 + 8 * (t % stages), (t / stages) & 1, abort);
+        Raw<T, W> vy[NV], vs[NV];
+        float2 sg = make_float2(0.f, 0.f), sgn = sg;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * tpr + x) * W;
+            vy[i] = load_or_zero<T, W>(dy + c, c < a.D);
+            vs[i] = load_or_zero<T, W>(s + c, c < a.D);
+            float2 fy[P], fs[P];
+            pairs<T, W>(vy[i], fy);
+            pairs<T, W>(vs[i], fs);
+#pragma unroll
+            for (int j = 0; j < P; ++j) {
+                const float2 n = __fmul2_rn(__fadd2_rn(fs[j], mean), rstd);
+                const float2 g = __fmul2_rn(fy[j], w[i][j]);
+                sg = __fadd2_rn(sg, g);
+                sgn = __ffma2_rn(g, n, sgn);
+                dw[i][j] = __ffma2_rn(fy[j], n, dw[i][j]);
+                db[i][j] = __fadd2_rn(db[i][j], fy[j]);
+            }
+        }
+        // the lower half of the warp adds up g, the upper one g n
+        const bool upper = lane >= 16;
+        float k = (upper ? sgn.x + sgn.y : sg.x + sg.y) +
+                  __shfl_xor_sync(0xffffffffu, upper ? sg.x + sg.y : sgn.x + sgn.y, 16);
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) k += __shfl_xor_sync(0xffffffffu, k, o);
+        if (warps > 1) {
+            // two buffers: a warp may reach the next turn's while another still reads this one's
+            if ((lane & 15) == 0) red[t & 1][lane >> 4][warp] = k;
+            asm volatile("bar.sync %0, %1;" :: "r"(1 + y), "r"(tpr) : "memory");
+            k = (lane & 15) < warps ? red[t & 1][lane >> 4][y * warps + (lane & 15)] : 0.f;
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) k += __shfl_xor_sync(0xffffffffu, k, o);
+        } else {
+            __syncwarp();
+        }
+        // (the mean by a division: a rounded 1 / D would double its error)
+        k = -rstd.x * (k / (float)a.D);
+        const float kg = __shfl_sync(0xffffffffu, k, 0), kn = __shfl_sync(0xffffffffu, k, 16);
+        if (x < 32 && t > 0 && t - 1 + stages < turns) issue(t - 1 + stages);
+        // dx = ds - rstd mean g + rstd g - rstd mean(g n) n
+        const float2 kg2 = make_float2(kg, kg), kn2 = make_float2(kn, kn);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * tpr + x) * W;
+            if (c >= a.D) continue;
+            float2 fy[P], fs[P], fd[P];
+            float dx[W];
+            pairs<T, W>(vy[i], fy);
+            pairs<T, W>(vs[i], fs);
+            pairs<T, W>(load_or_zero<T, W>(ds + c, streams == 3), fd);
+#pragma unroll
+            for (int j = 0; j < P; ++j) {
+                const float2 n = __fmul2_rn(__fadd2_rn(fs[j], mean), rstd);
+                const float2 g = __fmul2_rn(fy[j], w[i][j]);
+                const float2 d = __ffma2_rn(n, kn2, __ffma2_rn(g, rstd, kg2));
+                dx[2 * j] = d.x + fd[j].x;
+                dx[2 * j + 1] = d.y + fd[j].y;
+            }
+            put<T, W>(static_cast<T *>(a.dX) + row * a.lddx + c, dx);
+        }
+    }
+    if (*abort && x < 32) {   // an aborted group does not leave with copies in flight
+        int ignored = 0;
+        for (int t = max(0, turns - stages); t < turns; ++t)
+            (void)tc::mbar_wait(full0 + 8 * (t % stages), (t / stages) & 1, &ignored);
+        if (x == 0 && args.error != nullptr) atomicOr(args.error, 1u);
+    }
+    __syncthreads();   // the ring is free
+    if (a.partial == nullptr) return;
+    // one row of partial sums a CTA: its groups' sums are added in their order
+    float2 *sums = reinterpret_cast<float2 *>(ring);
+    const int width = tpr * 8;
+    auto join = [&](float2 (&d)[NV][P]) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < P; ++j)
+                if (mine) sums[y * width + (i * P + j) * tpr + x] = d[i][j];
+        __syncthreads();
+        if (y == 0)
+            for (int k = 1; k < groups; ++k)
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+#pragma unroll
+                    for (int j = 0; j < P; ++j)
+                        d[i][j] = __fadd2_rn(d[i][j], sums[k * width + (i * P + j) * tpr + x]);
+        __syncthreads();
+    };
+    if (groups > 1) {
+        join(dw);
+        join(db);
+    }
+    if (y > 0) return;
+    float *to = a.partial + (int64_t)blockIdx.x * 2 * a.D;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * tpr + x) * W;
+        if (c >= a.D) continue;
+#pragma unroll
+        for (int j = 0; j < P; j += 2) {
+            *reinterpret_cast<float4 *>(to + c + 2 * j) =
+                make_float4(dw[i][j].x, dw[i][j].y, dw[i][j + 1].x, dw[i][j + 1].y);
+            *reinterpret_cast<float4 *>(to + a.D + c + 2 * j) =
+                make_float4(db[i][j].x, db[i][j].y, db[i][j + 1].x, db[i][j + 1].y);
+        }
+    }
+}
+
 // Rows wider than a group's registers: the CTA reads each of its rows twice and keeps its
 // columns' sums in its own row of the workspace.
 template <class T>
@@ -437,9 +642,28 @@ struct GradShape {
     int w, nv;      // elements an access, accesses a thread; nv 0: the wide kernel
     Shape sh;
     int ctas;
+    bool ring;
 };
+// Whether the ring takes rows of 16-byte pieces: of 1 KB or more (shorter rows would be many
+// small copies) up to 512 threads' 16 columns, and enough of them for four turns a CTA.
+bool ring_takes(int type, int64_t rows, int64_t D, Shape sh) {
+    return sh.tpr > 0 && sh.tpr <= 512 && D * dtype_size(type) >= 1024 &&
+           rows >= 152 * 4 * (512 / sh.tpr);
+}
 GradShape grad_shape(int type, int64_t rows, int64_t D, bool vec) {
-    GradShape g;
+    GradShape g = {};
+    if (vec) {
+        const int w = 16 / dtype_size(type);
+        g.sh = shape_for(D / w, 16 / w);
+        if (ring_takes(type, rows, D, g.sh)) {
+            g.sh.groups = 512 / g.sh.tpr;
+            g.w = w;
+            g.nv = 16 / w;
+            g.ctas = 152;
+            g.ring = true;
+            return g;
+        }
+    }
     g.w = vec ? 16 / dtype_size(type) : 1;
     const int64_t n = (D + g.w - 1) / g.w;
     g.nv = vec ? 2 : 8;
@@ -460,8 +684,35 @@ GradShape grad_shape(int type, int64_t rows, int64_t D, bool vec) {
 }
 
 template <class T>
+cudaError_t launch_ring(const LayerGradArgs &a, const GradShape &g, cudaStream_t s) {
+    static PerContext<bool> configured;
+    bool done = false;
+    if (!configured.get(current_context_id(), done)) {
+        const cudaError_t e = cudaFuncSetAttribute(
+            layer_grad_ring_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+        if (e != cudaSuccess) return e;
+        configured.put(current_context_id(), true);
+    }
+    const int stage = g.sh.groups * (a.dS != nullptr ? 3 : 2) * a.D * (int)sizeof(T);
+    const int stages = kRingBytes / stage < kRingStages ? kRingBytes / stage : kRingStages;
+    const LayerRingArgs args = {a, g.sh.tpr, g.sh.groups, stages, device_error_word()};
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)g.ctas);
+    cfg.blockDim = dim3(kRingThreads);
+    cfg.dynamicSmemBytes = kRingBytes;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, layer_grad_ring_kernel<T>, args);
+}
+
+template <class T>
 cudaError_t grad_dispatch(const LayerGradArgs &a, const GradShape &g, cudaStream_t s) {
     constexpr int W = 16 / sizeof(T);
+    if (g.ring) return launch_ring<T>(a, g, s);
     const dim3 grid((unsigned)g.ctas), block((unsigned)g.sh.tpr, (unsigned)g.sh.groups);
     if (g.nv == 0) return launch(layer_grad_wide_kernel<T>, grid, block, a, s);
     if (g.w == 1)

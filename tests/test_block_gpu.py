@@ -535,6 +535,37 @@ def test_add_layernorm_backward_strides(pad, offset, t):
     run_layernorm_backward(400, 520, t, True, pad, offset)
 
 
+# rows long and many enough for the ring: whole and ragged turns, groups that do not fill the CTA
+@pytest.mark.parametrize("t", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("rows,d", [(9801, 520), (9728, 1024), (2501, 4096), (3700, 2008), (1300, 8192),
+                                    (1999, 3000)])
+def test_add_layernorm_backward_of_many_rows(rows, d, t):
+    run_layernorm_backward(rows, d, t, True)
+    run_layernorm_backward(rows, d, t, False, pad=8)
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+def test_add_layernorm_backward_in_place(t):
+    # dX may be dY or dS itself: through the C ABI, one and many rows
+    dtype, code = TYPES[t], 0 if t == "f32" else 1
+    for rows, d in ((3, 264), (1300, 4096), (700, 9001)):
+        g = gen(rows)
+        dy, s, ds = (normal(g, rows, d, dtype=dtype) for _ in range(3))
+        mean, rstd, w = normal(g, rows), normal(g, rows).abs() + 0.5, normal(g, d, dtype=dtype)
+        dx, dw, db = sg.add_layernorm_backward(dy, s, mean, rstd, w, ds)
+        need = sg.add_layernorm_backward_workspace_size(code, rows, d)
+        ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+        for over in (0, 1):
+            a, b = dy.clone(), ds.clone()
+            out, dw2, db2 = (a, b)[over], torch.empty_like(dw), torch.empty_like(db)
+            sg.sgemm_add_layernorm_backward(code, rows, d, a.data_ptr(), d, s.data_ptr(), d,
+                                            mean.data_ptr(), rstd.data_ptr(), w.data_ptr(),
+                                            b.data_ptr(), d, out.data_ptr(), d, dw2.data_ptr(),
+                                            db2.data_ptr(), ws.data_ptr(), need,
+                                            torch.cuda.current_stream().cuda_stream)
+            assert torch.equal(out, dx) and torch.equal(dw2, dw) and torch.equal(db2, db)
+
+
 def test_add_layernorm_backward_empty_and_parts():
     e = lambda *s: torch.ones(*s, device="cuda")  # noqa: E731
     dx, dw, db = sg.add_layernorm_backward(e(0, 8), e(0, 8), e(0), e(0), e(8))
