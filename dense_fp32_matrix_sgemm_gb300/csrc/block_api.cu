@@ -44,6 +44,29 @@ int gated_vector_width(int type, const GatedEpi &e) {
     return size == 2 && all(8) ? 8 : all(4) ? 4 : 1;
 }
 
+// Operands that TMA cannot read where they lie, copied to the workspace in one launch.
+class Placing {
+public:
+    Placing(char *ws, int size) : ws_(ws), size_(size) {}
+    void add(const void *&p, int64_t &ld, int64_t rows, int64_t cols) {
+        if (tma_ok(p, ld, size_)) return;
+        const int64_t to = padded_ld(cols, size_);
+        jobs_[count_++] = {p, ws_, ld * size_, to * size_, rows, cols * size_, 0};
+        p = ws_;
+        ld = to;
+        ws_ += round256((size_t)rows * to * size_);
+    }
+    cudaError_t run(cudaStream_t s) {
+        return count_ > 0 ? launch_repack3(jobs_, count_, s) : cudaSuccess;
+    }
+
+private:
+    RepackJob jobs_[3];
+    int count_ = 0;
+    char *ws_;
+    int size_;
+};
+
 int check_gated_sizes(int64_t M, int64_t N, int64_t K) {
     CHECK(check_sizes(M, N, K, "M, N, K"));
     if (N > kMaxDim / 2)
@@ -103,9 +126,11 @@ int gated_linear(int dtype, int64_t M, int64_t N, int64_t K, const void *X, int6
         return launched(launch_gated_f32({ws, M, K, true}, {wsg, wr, wc, transW != 0},
                                          {wsu, wr, wc, transW != 0}, (int)K, epi, s));
     }
-    cudaError_t e = place(X, ldx, M, K, size, ws, s);
-    if (e == cudaSuccess) e = place(Wg, ldwg, wr, wc, size, ws, s);
-    if (e == cudaSuccess) e = place(Wu, ldwu, wr, wc, size, ws, s);
+    Placing placing(ws, size);
+    placing.add(X, ldx, M, K);
+    placing.add(Wg, ldwg, wr, wc);
+    placing.add(Wu, ldwu, wr, wc);
+    const cudaError_t e = placing.run(s);
     if (e != cudaSuccess) return launched(e);
     return launched(launch_gated_tc(dtype, {X, ldx, true}, {Wg, ldwg, transW != 0},
                                     {Wu, ldwu, transW != 0}, (int)K, epi, s));
@@ -209,9 +234,11 @@ int gated_linear_backward(int dtype, int64_t M, int64_t N, int64_t K, const void
         if (dx) in[count++] = {static_cast<const float *>(Wu), ldwu, wr, wc, wsu};
         e = launch_f32_split(in, count, kChainPrev, s);
     } else if (products) {
-        if (dw) e = place(X, ldx, M, K, size, ws, s);
-        if (dx && e == cudaSuccess) e = place(Wg, ldwg, wr, wc, size, ws, s);
-        if (dx && e == cudaSuccess) e = place(Wu, ldwu, wr, wc, size, ws, s);
+        Placing placing(ws, size);
+        if (dw) placing.add(X, ldx, M, K);
+        if (dx) placing.add(Wg, ldwg, wr, wc);
+        if (dx) placing.add(Wu, ldwu, wr, wc);
+        e = placing.run(s);
     }
     int left = (int)dx + (int)dwg + (int)dwu + (int)db, done = 0, half = 0;
     if (dx && dwg && dwu && gated_side_by_side(dtype, {(int)M, (int)K, (int)N},

@@ -144,6 +144,71 @@ __global__ void __launch_bounds__(1024) column_sum2_kernel(const float *partial,
     chain_end(chain);
 }
 
+// Rows copied to rows with 16-byte boundaries, up to three matrices a launch.  A warp takes 512
+// bytes of a row at a time, a lane 16 of them: loads of the largest word that the source's
+// rows allow (a lane's share their sectors through L1), one store.  Bytes past a row's end go
+// to the destination's gap as zeros.  From piece to piece a warp steps without a division.
+struct RepackArgs {
+    RepackJob job[3];
+    int blocks[3];
+};
+template <class U>
+__device__ __forceinline__ void repack_rows(const RepackJob &j, int64_t warp, int64_t warps) {
+    constexpr int N = 16 / sizeof(U);
+    const int lane = threadIdx.x & 31;
+    const int pieces = (int)((j.row_bytes + 511) / 512);
+    const int64_t dr = warps / pieces;
+    const int dc = (int)(warps - dr * pieces);
+    int64_t r = warp / pieces;
+    int pc = (int)(warp - r * pieces);
+    for (; r < j.rows; r += dr, pc += dc) {
+        if (pc >= pieces) {
+            pc -= pieces;
+            if (++r >= j.rows) break;
+        }
+        const int64_t at = (int64_t)pc * 512 + lane * 16;
+        if (at >= j.row_bytes) continue;
+        const char *from = static_cast<const char *>(j.src) + r * j.src_ld + at;
+        U w[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            w[i] = at + i * (int)sizeof(U) < j.row_bytes
+                       ? *reinterpret_cast<const U *>(from + i * sizeof(U)) : U{};
+        uint4 v;
+        if constexpr (sizeof(U) == 8) {
+            v = make_uint4(w[0].x, w[0].y, w[1].x, w[1].y);
+        } else {
+            uint32_t d[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                d[i * sizeof(U) / 4] |= (uint32_t)w[i] << (8 * (i * sizeof(U) % 4));
+            v = make_uint4(d[0], d[1], d[2], d[3]);
+        }
+        *reinterpret_cast<uint4 *>(static_cast<char *>(j.dst) + r * j.dst_ld + at) = v;
+    }
+}
+__global__ void __launch_bounds__(kThreads) repack3_kernel(const RepackArgs a) {
+    pdl_trigger();
+    pdl_wait();
+    int block = (int)blockIdx.x, which = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        if (which == i && block >= a.blocks[i]) {
+            block -= a.blocks[i];
+            which = i + 1;
+        }
+    const RepackJob j = which == 0 ? a.job[0] : which == 1 ? a.job[1] : a.job[2];
+    const int blocks = which == 0 ? a.blocks[0] : which == 1 ? a.blocks[1] : a.blocks[2];
+    const int64_t warp = (int64_t)block * (kThreads / 32) + (threadIdx.x >> 5);
+    const int64_t warps = (int64_t)blocks * (kThreads / 32);
+    switch (j.word) {
+        case 8: repack_rows<uint2>(j, warp, warps); break;
+        case 4: repack_rows<uint32_t>(j, warp, warps); break;
+        case 2: repack_rows<uint16_t>(j, warp, warps); break;
+        default: repack_rows<uint8_t>(j, warp, warps); break;
+    }
+}
+
 bool aligned16(const void *p, int64_t ld, int size) {
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * size % 16 == 0;
 }
@@ -203,6 +268,23 @@ cudaError_t launch_gated_dz(int type, const void *dH, int64_t lddh, const void *
     if (type == SGEMM_F32) return gated::dz_types<float>(a, vec, parts, s);
     if (type == SGEMM_BF16) return gated::dz_types<__nv_bfloat16>(a, vec, parts, s);
     return gated::dz_types<__half>(a, vec, parts, s);
+}
+
+// One launch for up to three matrices; the words are chosen here.
+cudaError_t launch_repack3(const RepackJob *jobs, int count, cudaStream_t s) {
+    gated::RepackArgs a = {};
+    int blocks = 0;
+    for (int i = 0; i < count; ++i) {
+        RepackJob &j = a.job[i];
+        j = jobs[i];
+        const uintptr_t bits = reinterpret_cast<uintptr_t>(j.src) | (uintptr_t)j.src_ld |
+                               (uintptr_t)j.row_bytes;
+        j.word = bits % 8 == 0 ? 8 : bits % 4 == 0 ? 4 : bits % 2 == 0 ? 2 : 1;
+        const int64_t need = (j.rows * ((j.row_bytes + 511) / 512) + 7) / 8;
+        a.blocks[i] = (int)(need < 152 * 8 ? need : 152 * 8);
+        blocks += a.blocks[i];
+    }
+    return gated::launch(gated::repack3_kernel, dim3((unsigned)blocks), gated::kThreads, s, a);
 }
 
 cudaError_t launch_column_sum2(int type, const float *partial, int parts, int64_t N, void *out,

@@ -9,9 +9,9 @@
 // through memory.  With a pair of CTAs the even one brings the gate's weights and the
 // odd one the factor's: what a CTA loads, multiplies and holds is what it is in a
 // plain product of 2 N features, and so are the tile costs; the results to write are
-// half as many (unless both pre-activations are kept).  A single CTA brings 32 rows of
-// each weight; weights stored K x N (64 features a line of the shared-memory layout)
-// take 64 of each there.
+// half as many (unless both pre-activations are kept).  A CTA on its own brings both weights'
+// rows, as many of each as the launch says (weights stored K x N, 64 features a line of the
+// shared-memory layout: 64).
 // The sum is the gradient of the layer's input, dZg Wg + dZu Wu: one accumulator runs
 // over both reductions, so it is rounded once and written once.
 #include <cstdint>
@@ -43,10 +43,9 @@ sum_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
 
 template <int CTAS, int BN, class O, bool SPLIT>
 cudaError_t launch_gated(int type, const TcOperand &X, const TcOperand &Wg, const TcOperand &Wu,
-                         int K, const GatedEpi &epi, const Piece &piece, int chain,
+                         int K, const GatedEpi &epi, const Piece &piece, int out, int chain,
                          cudaStream_t s) {
     using S = Shape<CTAS, BN, SPLIT>;
-    constexpr int OUT = BN / 2;
     static PerContext<bool> configured;
     bool done = false;
     cudaError_t e;
@@ -55,14 +54,24 @@ cudaError_t launch_gated(int type, const TcOperand &X, const TcOperand &Wg, cons
         if (e != cudaSuccess) return e;
         configured.put(current_context_id(), true);
     }
-    if (OUT < 64 && !Wg.kmajor) return cudaErrorInvalidValue;
     Params<GatedEpi> p;
     p.epi = epi;
     const int a_rows = fill_params<CTAS, BN>(p, type, epi.M, 2 * epi.N, K, X.kmajor, Wg.kmajor,
                                              piece, chain);
+    p.out = out;
+    if constexpr (CTAS == 1) {
+        p.tiles_n = (epi.N + out - 1) / out;
+        p.a_tile = a_rows * kRowBytes;
+        p.sub = p.a_tile + 2 * out * kRowBytes;
+        // (the MMAs read 128 rows of A wherever the tile ends: the last one's stay in the ring)
+        const int over = S::A_TILE > p.sub ? S::A_TILE - p.sub : 0;
+        p.stages = (S::STAGES * S::STAGE - over) / (S::KS * p.sub);
+        if (p.stages > kMostStages) p.stages = kMostStages;
+        p.idesc = instruction_desc(type, BM, 2 * out, X.kmajor, Wg.kmajor);
+    }
     CUtensorMap tmX, tmG, tmU, tmH = {}, tmZg = {}, tmZu = {};
     if (!operand_map(&tmX, X, type, epi.M, K, a_rows) ||
-        !operand_map(&tmG, Wg, type, epi.N, K, OUT) || !operand_map(&tmU, Wu, type, epi.N, K, OUT))
+        !operand_map(&tmG, Wg, type, epi.N, K, out) || !operand_map(&tmU, Wu, type, epi.N, K, out))
         return cudaErrorInvalidValue;
     p.tma = !SPLIT && epi.vec == 8 && out_map(&tmH, epi.H, epi.type, epi.ldh, epi.N, epi.M) &&
             (epi.Zg == nullptr || out_map(&tmZg, epi.Zg, epi.type, epi.ldg, epi.N, epi.M)) &&
@@ -100,11 +109,55 @@ cudaError_t launch_sum(int type, const TcOperand (&A)[2], const TcOperand (&B)[2
                               tmB[1], tmY, p);
 }
 
-// Costs as linear_tc.cu's; the shapes differ by the weights' storage.
-constexpr Costs<3> kByFeature = {{{2, 256}, {2, 128}, {1, 64}}, {0.27, 0.165, 0.15},
-                                 {6.5, 5.5, 4.5}, {5.0, 3.0, 1.5}};
-constexpr Costs<3> kByInput = {{{2, 256}, {2, 128}, {1, 128}}, {0.27, 0.165, 0.24}, {6.5, 5.5, 4.5},
-                               {5.0, 3.0, 3.0}};
+// Costs as linear_tc.cu's.
+constexpr Costs<3> kSumCosts = {{{2, 256}, {2, 128}, {1, 64}}, {0.27, 0.165, 0.15},
+                                {6.5, 5.5, 4.5}, {5.0, 3.0, 1.5}};
+constexpr Costs<2> kPairs = {{{2, 256}, {2, 128}}, {0.27, 0.165}, {6.5, 5.5}, {5.0, 3.0}};
+
+// Tiles of a CTA on its own: 128 rows and `out` outputs, a multiple of 8 up to 128, in `parts`
+// parts of K.  The width is what makes whole rounds of the SMs (64 x 8192 x 4096: 128 tiles of 64
+// outputs leave 24 SMs idle, 256 of 32 take two rounds, 147 of 56 one).
+struct Single {
+    int out = 64, parts = 1;
+    int64_t tiles = 0;
+    double us = 1e30;
+};
+constexpr int kNarrow = 64, kWide = 128;   // the most outputs of either kernel
+
+// Costs in us.  128 bytes of K take the issuing thread's three copies (0.15), the operands'
+// way from L2, or, where no other row tile shares the weights, theirs from HBM at 45 bytes a ns
+// and SM (kPairs' tiles at 41); the rest of a launch is 4.5, 5 % more of it all where whole tiles
+// come from HBM, and joining parts 0.7 to 1.3 and 1 for 64 outputs of 128 rows.  Against the other
+// choices, weights out of L2, outputs / parts:
+//   64 x 8192 x 4096 bf16 56/1 24.1 (64/1 24.2, 32/1 28.4, 112/2 26.1); e4m3 56/1 15.6 (32/1 19.2)
+//   64 x 11264 x 4096 bf16 80/1 31.8 (40/1 32.4, 64/1 39.9)
+//   64 x 4096 x 4096 bf16 56/2 15.6 (32/1 16.4, 16/1 27.7); e4m3 56/2 10.6 (32/1 12.4)
+//   64 x 1024 x 4096 bf16 32/4 8.9 (16/2 11.8, 8/1 15.4); 64 x 2048 x 1024 16/1 6.7 (32/2 7.3)
+//   64 x 14336 x 4096 e4m3 48/1 23.4 (96/1 26.4)
+//   256 x 4096 x 4096 bf16 pairs' 128-wide tiles 18.7 (56/1 20.6, 32/1 28.4)
+//   512 x 1024 x 1024 bf16 32/1 6.7 (64/1 7.3, 64/2 8.8); 1000^3 56/1 10.3 (128/1 14.2)
+Single plan_single(int M, int N, int kblocks, const Capacity &cap, bool any_out) {
+    Single best;
+    const int row_tiles = (M + BM - 1) / BM;
+    const double rows = (M < BM ? M : BM) / (double)BM;
+    for (int out = any_out ? 8 : kNarrow; out <= (any_out ? kWide : kNarrow); out += 8) {
+        const int64_t tiles = (int64_t)row_tiles * ((N + out - 1) / out);
+        if (tiles > 0x7fffffff) continue;
+        const double l2 = 0.08 * rows + 0.0028 * out, hbm = 0.0057 * out / row_tiles;
+        const double block = hbm > l2 ? hbm : l2, stage = block > 0.15 ? block : 0.15;
+        for (int parts = 1; parts <= 8; parts *= 2) {
+            if (parts > 1 && (tiles > cap.of(parts) || kblocks < 2 * parts)) break;
+            const int64_t rounds = parts > 1 ? 1 : (tiles + cap.sms - 1) / cap.sms;
+            double us = rounds * ((kblocks + parts - 1) / parts) * stage + 4.5;
+            if (parts > 1)
+                us += (parts == 2 ? 0.7 : parts == 4 ? 1.0 : 1.3) + rows * out / 64;
+            else if (stage == hbm)
+                us *= 1.05;
+            if (us < best.us) best = {out, parts, tiles, us};
+        }
+    }
+    return best;
+}
 
 template <class O>
 cudaError_t gated_dispatch(int type, const TcOperand &X, const TcOperand &Wg, const TcOperand &Wu,
@@ -114,17 +167,28 @@ cudaError_t gated_dispatch(int type, const TcOperand &X, const TcOperand &Wg, co
     if (e != cudaSuccess) return e;
     const int bk = kRowBytes / dtype_size(type);
     const int kblocks = (K + bk - 1) / bk;
-    if (Wg.kmajor) {
-        const Plan plan = plan_tiles(epi.M, 2 * epi.N, kblocks, cap, kByFeature);
-        return run_plan(kByFeature, plan, 0, [&](auto w, auto split, const Piece &p, int at) {
-            constexpr TileShape t = kByFeature.shape[w()];
-            return launch_gated<t.ctas, t.bn, O, split()>(type, X, Wg, Wu, K, epi, p, at, s);
-        });
+    Costs<2> pairs = kPairs;
+    for (int w = 0; w < 2; ++w) {   // (see plan_single)
+        const int bm = kPairs.shape[w].ctas * BM;
+        const double hbm = 0.0063 * (kPairs.shape[w].bn / 4) / ((epi.M + bm - 1) / bm);
+        if (hbm > pairs.stage[w]) pairs.stage[w] = hbm;
     }
-    const Plan plan = plan_tiles(epi.M, 2 * epi.N, kblocks, cap, kByInput);
-    return run_plan(kByInput, plan, 0, [&](auto w, auto split, const Piece &p, int at) {
-        constexpr TileShape t = kByInput.shape[w()];
-        return launch_gated<t.ctas, t.bn, O, split()>(type, X, Wg, Wu, K, epi, p, at, s);
+    const Plan plan = plan_tiles(epi.M, 2 * epi.N, kblocks, cap, pairs);
+    const Single one = plan_single(epi.M, epi.N, kblocks, cap, Wg.kmajor);
+    if (one.us < plan.us) {
+        const Piece p = {0, (int)one.tiles, one.parts, cap.sms};
+        auto launch = [&](auto wide, auto split) {
+            return launch_gated<1, 2 * (wide() ? kWide : kNarrow), O, split()>(
+                type, X, Wg, Wu, K, epi, p, one.out, 0, s);
+        };
+        const std::true_type yes;
+        const std::false_type no;
+        if (one.out > kNarrow) return one.parts > 1 ? launch(yes, yes) : launch(yes, no);
+        return one.parts > 1 ? launch(no, yes) : launch(no, no);
+    }
+    return run_plan(kPairs, plan, 0, [&](auto w, auto split, const Piece &p, int at) {
+        constexpr TileShape t = kPairs.shape[w()];
+        return launch_gated<t.ctas, t.bn, O, split()>(type, X, Wg, Wu, K, epi, p, t.bn / 2, at, s);
     });
 }
 
@@ -136,9 +200,9 @@ cudaError_t sum_dispatch(int type, const TcOperand (&A)[2], const TcOperand (&B)
     if (e != cudaSuccess) return e;
     if (chain & kChainHalf) cap = cap.half();
     const int bk = kRowBytes / dtype_size(type);
-    const Plan plan = plan_tiles(epi.M, epi.N, 2 * ((K + bk - 1) / bk), cap, kByFeature);
-    return run_plan(kByFeature, plan, chain, [&](auto w, auto split, const Piece &p, int at) {
-        constexpr TileShape t = kByFeature.shape[w()];
+    const Plan plan = plan_tiles(epi.M, epi.N, 2 * ((K + bk - 1) / bk), cap, kSumCosts);
+    return run_plan(kSumCosts, plan, chain, [&](auto w, auto split, const Piece &p, int at) {
+        constexpr TileShape t = kSumCosts.shape[w()];
         return launch_sum<t.ctas, t.bn, O, split()>(type, A, B, K, epi, p, at, s);
     });
 }
@@ -152,7 +216,7 @@ bool gated_side_by_side(int in_type, const ProductSize &sum, const ProductSize &
     if (in_type == SGEMM_F32) return f32_three_side_by_side(sum, product, cap);
     const int bk = kRowBytes / dtype_size(in_type);
     return three_side_by_side({sum.M, sum.N, 2 * ((sum.K + bk - 1) / bk * bk)}, product, bk, cap,
-                              kByFeature);
+                              kSumCosts);
 }
 
 cudaError_t launch_gated_tc(int in_type, const TcOperand &X, const TcOperand &Wg,

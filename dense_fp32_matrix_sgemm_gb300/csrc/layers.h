@@ -146,6 +146,14 @@ cudaError_t launch_gated_dz(int type, const void *dH, int64_t lddh, const void *
                             const void *Zu, int64_t ldzu, int act, int M, int N, void *dZg,
                             void *dZu, int64_t lddz, int64_t plane, float *partial, int chain,
                             cudaStream_t s);
+// Rows of row_bytes bytes copied to rows dst_ld bytes apart, both 16-byte aligned there.
+struct RepackJob {
+    const void *src;
+    void *dst;
+    int64_t src_ld, dst_ld, rows, row_bytes;   // bytes
+    int word;                                  // set by the launch
+};
+cudaError_t launch_repack3(const RepackJob *jobs, int count, cudaStream_t s);   // one to three
 // out[c] and out2[c] = sums over `parts` rows of partial[part][c] and partial[part][N + c],
 // added in a fixed order; either output may be null.
 cudaError_t launch_column_sum2(int type, const float *partial, int parts, int64_t N, void *out,

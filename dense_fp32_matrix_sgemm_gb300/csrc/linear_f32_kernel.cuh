@@ -374,7 +374,8 @@ __device__ __forceinline__ void linear_f32_body(const Maps &map, const Params<E>
                         run[j] = run[j + 16];
                         run[OUT / 2 + j] = run[OUT / 2 + j + 16];
                     }
-                    finish_gated_staged<float, 8>(p.epi, stage, lane, row0, rows, n0 + 16 * c);
+                    finish_gated_staged<float, 8>(p.epi, stage, lane, row0, rows, n0 + 16 * c,
+                                                  p.epi.N);
                 }
             } else {
                 const int rows = min(32, p.epi.M - row0);
@@ -418,9 +419,18 @@ __device__ __forceinline__ void linear_f32_body(const Maps &map, const Params<E>
         const int m0 = (tm * CTAS + half) * BM;
         const int rows = min(BM, p.epi.M - m0);
         const int n0 = tn * OUT;
-        if (parts == 2) join_parts<2, CTAS, BN, float>(p.epi, ring, part, half, m0, n0, rows);
-        if (parts == 4) join_parts<4, CTAS, BN, float>(p.epi, ring, part, half, m0, n0, rows);
-        if (parts == 8) join_parts<8, CTAS, BN, float>(p.epi, ring, part, half, m0, n0, rows);
+        if constexpr (FORM == kGated) {
+            if (parts == 2)
+                join_gated<2, CTAS, BN, float>(p.epi, ring, part, half, m0, n0, rows, OUT);
+            if (parts == 4)
+                join_gated<4, CTAS, BN, float>(p.epi, ring, part, half, m0, n0, rows, OUT);
+            if (parts == 8)
+                join_gated<8, CTAS, BN, float>(p.epi, ring, part, half, m0, n0, rows, OUT);
+        } else {
+            if (parts == 2) join_parts<2, CTAS, BN, float>(p.epi, ring, part, half, m0, n0, rows);
+            if (parts == 4) join_parts<4, CTAS, BN, float>(p.epi, ring, part, half, m0, n0, rows);
+            if (parts == 8) join_parts<8, CTAS, BN, float>(p.epi, ring, part, half, m0, n0, rows);
+        }
     }
     if (*abort_flag && threadIdx.x == 0 && p.error != nullptr) atomicOr(p.error, 1u);
     if (warp == 1 && *abort_flag) {

@@ -279,13 +279,15 @@ __device__ __forceinline__ bool reads_global(const GatedEpi &e) {
     return e.bg != nullptr || e.bu != nullptr || e.sx != nullptr;
 }
 
-// v = v sx s[col ..] + b[col ..] for 32 columns of a 16-bit layer (s and b may be null).
+// v = v sx s[col ..] + b[col ..] for n of 32 columns (a multiple of 8) of a 16-bit layer (s
+// and b may be null).
 template <class O>
 __device__ __forceinline__ void scale_and_bias32(float (&v)[32], float sx, const float *s,
-                                                 const void *b, int col) {
+                                                 const void *b, int col, int n) {
     if (s != nullptr) {
 #pragma unroll
         for (int j = 0; j < 32; j += 4) {
+            if (j >= n) break;
             const float4 f = *reinterpret_cast<const float4 *>(s + col + j);
             v[j] *= sx * f.x;
             v[j + 1] *= sx * f.y;
@@ -296,6 +298,7 @@ __device__ __forceinline__ void scale_and_bias32(float (&v)[32], float sx, const
     if (b != nullptr) {
 #pragma unroll
         for (int j = 0; j < 32; j += 8) {
+            if (j >= n) break;
             const uint4 x = *reinterpret_cast<const uint4 *>(static_cast<const O *>(b) + col + j);
             const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
@@ -306,6 +309,20 @@ __device__ __forceinline__ void scale_and_bias32(float (&v)[32], float sx, const
             }
         }
     }
+}
+
+// Brings the columns' scales and biases into L2 while the tile's product runs.
+template <class O>
+__device__ __forceinline__ void prefetch_terms(const GatedEpi &e, int lane, int col, int end) {
+    const int c = col + 32 * (lane >> 2);   // four lanes for each 32 columns, one a vector
+    if (c >= end) return;
+    const void *const p = (lane & 3) == 0   ? static_cast<const void *>(e.sg + c)
+                          : (lane & 3) == 1 ? static_cast<const void *>(e.su + c)
+                          : (lane & 3) == 2 ? static_cast<const void *>(static_cast<const O *>(e.bg) + c)
+                                            : static_cast<const void *>(static_cast<const O *>(e.bu) + c);
+    const bool given = (lane & 3) == 0 ? e.sg != nullptr : (lane & 3) == 1 ? e.su != nullptr
+                       : (lane & 3) == 2 ? e.bg != nullptr : e.bu != nullptr;
+    if (given) prefetch_l2(p);
 }
 
 // 16 gates and their factors of this lane's row into the warp's staging block: row r's
@@ -321,15 +338,15 @@ __device__ __forceinline__ void stage_pair16(uint32_t stage, int lane, const flo
     }
 }
 
-// The gated epilogue on the first `rows` rows (from row0 on) of such a block: a
-// column a lane, the warp's halves four rows apart (which meet no bank twice), U rows
+// The gated epilogue on the first `rows` rows (from row0 on) of such a block, up to column
+// `end`: a column a lane, the warp's halves four rows apart (which meet no bank twice), U rows
 // (4 or 8) in flight.
 template <class O, int U>
 __device__ __forceinline__ void finish_gated_staged(const GatedEpi &e, uint32_t stage, int lane,
-                                                    int row0, int rows, int col0) {
+                                                    int row0, int rows, int col0, int end) {
     static_assert(U == 4 || U == 8, "rows of a turn");
     const int col = col0 + (lane & 15), far = (lane >> 4) * 4;
-    if (col >= e.N) return;
+    if (col >= end) return;
     GatedTerms<O, 1> t;
     t.load(e, col);
 #pragma unroll 1
@@ -367,18 +384,18 @@ __device__ __forceinline__ void finish_gated_staged(const GatedEpi &e, uint32_t 
     }
 }
 
-// join_parts of a gated tile: the two groups of four accumulator columns that a lane
-// adds up are a group's gates and their factors.
+// join_parts of a gated tile of `out` outputs: the two groups of four accumulator columns that
+// a lane adds up are a group's gates and, `out` columns on, their factors.
 template <int PARTS, int CTAS, int BN, class O>
-__device__ __forceinline__ void join_parts(const GatedEpi &e, uint32_t ring, int part, int half,
-                                           int m0, int n0, int rows) {
+__device__ __forceinline__ void join_gated(const GatedEpi &e, uint32_t ring, int part, int half,
+                                           int m0, int n0, int rows, int out) {
     constexpr int LPR = BN / 8, RPW = 32 / LPR;   // lanes a row, rows a warp
     constexpr int STEP = kThreads / 32 * RPW * PARTS;
     constexpr int U = PARTS == 2 ? 4 : PARTS == 8 ? 1 : 2;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = lane % LPR;
     const int col = n0 + 4 * c;
-    if (col >= e.N) return;
+    if (4 * c >= out || col >= e.N) return;
     GatedTerms<O, 4> t;
     t.load(e, col);
     uint32_t base[PARTS];
@@ -393,7 +410,7 @@ __device__ __forceinline__ void join_parts(const GatedEpi &e, uint32_t ring, int
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const uint32_t at = (uint32_t)(r * BN * 4) +
-                                    ((uint32_t)((c + h * LPR) ^ (r & 7)) << 4);
+                                    ((uint32_t)((c + h * (out / 4)) ^ (r & 7)) << 4);
 #pragma unroll
                 for (int j = 0; j < PARTS; ++j) x[u][h][j] = ld_cluster_v4(base[j] + at);
             }

@@ -7,6 +7,8 @@
 namespace sgemm {
 namespace ltc {
 
+constexpr int kMostStages = 12;   // of a gated CTA on its own
+
 template <int CTAS, int BN, bool SPLIT>
 struct Shape {
     static constexpr int BROWS = BN / CTAS;   // of B in a CTA
@@ -38,6 +40,8 @@ struct Params {
     int a_bytes;             // bytes A's boxes bring to a CTA's stage
     uint32_t idesc;
     int fp8;
+    int out;                 // kGated, a CTA on its own: outputs of a tile,
+    int a_tile, sub, stages; //   bytes of A's rows and of 128 bytes of K in a stage, stages
     int tma;                 // Y and Z leave by TMA store, whole blocks of 32 columns
     unsigned *error;
 };
@@ -148,43 +152,59 @@ __device__ __forceinline__ void finish_rows(const Params<LayerEpi> &p, const voi
     }
 }
 
-// The same for tiles whose accumulators hold a gate and its factor BN / 2 columns
-// apart: 32 outputs at a time, both sums in registers.  A staging block holds two of
-// the three results, so the pre-activations leave first.  (The wait for them to be
-// read overlaps the next tile's MMAs.)
+// n (a multiple of 8) of 32 values of this lane's row as 16-byte stores.
+template <class O>
+__device__ __forceinline__ void store_row8s(void *base, int64_t ld, int row, int col, int n,
+                                            const float (&v)[32]) {
+    O *p = static_cast<O *>(base) + row * ld + col;
+#pragma unroll
+    for (int j = 0; j < 32; j += 8)
+        if (j < n)
+            *reinterpret_cast<uint4 *>(p + j) =
+                make_uint4(pack2<O>(v[j], v[j + 1]), pack2<O>(v[j + 2], v[j + 3]),
+                           pack2<O>(v[j + 4], v[j + 5]), pack2<O>(v[j + 6], v[j + 7]));
+}
+
+// finish_rows for tiles whose accumulators hold gates and, some columns on, their factors:
+// 32 outputs at a time, up to column `end`, both sums in registers.  A staging block holds
+// two of the three results, so the pre-activations leave first.  (The wait for them to be
+// read overlaps the next tile's MMAs.)  Fewer than 32 outputs (a tile's width is a multiple
+// of 8) leave by 16-byte stores, a row a lane; what is not aligned to that passes through the
+// staging block.
 template <int BLOCKS, class O>
 __device__ __forceinline__ void finish_gated_rows(const Params<GatedEpi> &p, const Maps &map,
                                                   uint32_t gate, uint32_t up, int q, int lane,
-                                                  int m0, int n0, uint32_t stage) {
+                                                  int m0, int n0, int end, uint32_t stage) {
     const GatedEpi &e = p.epi;
     const int row0 = m0 + 32 * q;
     if (row0 >= e.M) return;
     const int row = row0 + lane;
+    const bool in = row < e.M, keep = e.Zg != nullptr || e.Zu != nullptr;
     const uint32_t lanes = (uint32_t)(32 * q) << 16;
-    const float sx = e.sx != nullptr && row < e.M ? e.sx[row] : 1.f;
+    const float sx = e.sx != nullptr && in ? e.sx[row] : 1.f;
 #pragma unroll 1
-    for (int c = 0; c < BLOCKS && n0 + 32 * c < e.N; ++c) {
-        const int col = n0 + 32 * c;
+    for (int c = 0; c < BLOCKS && n0 + 32 * c < end; ++c) {
+        const int col = n0 + 32 * c, n = min(32, end - col);
         if (lane == 0) tc::bulk_wait_group_read<0>();   // the staging block is free
         float v[32], u[32];
         __syncwarp();   // the loads are warp-collective
         tc::tmem_ld_32(gate + lanes + (uint32_t)(32 * c), v);
         tc::tmem_ld_32(up + lanes + (uint32_t)(32 * c), u);
-        if (!p.tma || col + 32 > e.N) {
+        if (!p.tma || n % 8 != 0) {
             const int rows = min(32, e.M - row0);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                if (col + 16 * h >= e.N) break;
+                if (16 * h >= n) break;
                 __syncwarp();   // the block has been read
                 stage_pair16(stage, lane, v + 16 * h, u + 16 * h);
                 __syncwarp();
-                finish_gated_staged<O, 8>(e, stage, lane, row0, rows, col + 16 * h);
+                finish_gated_staged<O, 8>(e, stage, lane, row0, rows, col + 16 * h, end);
             }
             continue;
         }
-        scale_and_bias32<O>(v, sx, e.sg, e.bg, col);
-        scale_and_bias32<O>(u, sx, e.su, e.bu, col);
-        if (e.Zg != nullptr || e.Zu != nullptr) {
+        scale_and_bias32<O>(v, sx, e.sg, e.bg, col, n);
+        scale_and_bias32<O>(u, sx, e.su, e.bu, col, n);
+        if (keep && n == 32) {
             if (e.Zg != nullptr) stage_row<O>(stage, lane, v);
             if (e.Zu != nullptr) stage_row<O>(stage + 2048u, lane, u);
             tc::fence_proxy_async_smem();
@@ -194,9 +214,16 @@ __device__ __forceinline__ void finish_gated_rows(const Params<GatedEpi> &p, con
                 if (e.Zu != nullptr) tma_store(map.Z2, stage + 2048u, col, row0);
                 tc::bulk_commit_group();
             }
+        } else if (keep && in) {
+            if (e.Zg != nullptr) store_row8s<O>(e.Zg, e.ldg, row, col, n, v);
+            if (e.Zu != nullptr) store_row8s<O>(e.Zu, e.ldu, row, col, n, u);
         }
         gate_all<O>(v, u, e.act);
-        if (e.Zg != nullptr || e.Zu != nullptr) {
+        if (n < 32) {
+            if (in) store_row8s<O>(e.H, e.ldh, row, col, n, v);
+            continue;
+        }
+        if (keep) {
             if (lane == 0) tc::bulk_wait_group_read<0>();
             __syncwarp();
         }
@@ -213,20 +240,33 @@ __device__ __forceinline__ void finish_gated_rows(const Params<GatedEpi> &p, con
 template <Form FORM, int CTAS, int BN, class O, bool SPLIT, class E>
 __device__ __forceinline__ void linear_tc_body(const Maps &map, const Params<E> &p) {
     using S = Shape<CTAS, BN, SPLIT>;
-    constexpr int STAGES = S::STAGES, ACCS = S::ACCS;
+    constexpr int STAGES = FORM == kGated && CTAS == 1 ? kMostStages : S::STAGES, ACCS = S::ACCS;
+    constexpr int BARS = 2 * STAGES + 2 * ACCS + 1;
+    static_assert(BARS * 8 + 8 <= 256, "barrier area");
     constexpr bool CLUSTER = CTAS == 2 || SPLIT;
-    constexpr int OUT = FORM == kGated ? BN / 2 : BN;   // output columns of a tile
+    // output columns of a tile, a multiple of 8 up to 64 for a gated CTA on its own
+    constexpr int OUT = FORM == kGated ? BN / 2 : BN;
+    constexpr bool ANY_OUT = FORM == kGated && CTAS == 1;
+    const int out = ANY_OUT ? p.out : OUT;
+    // Such a tile's stages are as large as its rows and outputs need, and as many as fit the
+    // ring's place: 64 x 4096 x 4096 bf16 in tiles of 32 outputs was held by the 48 KB of
+    // weights that whole tiles' stages had in flight (XX us, YY so).
+    constexpr int RING = S::STAGES * S::STAGE;
+    const int a_tile = ANY_OUT ? p.a_tile : S::A_TILE, sub = ANY_OUT ? p.sub : S::SUB;
+    const int stage_bytes = ANY_OUT ? S::KS * sub : S::STAGE;
+    const int stages = ANY_OUT ? p.stages : S::STAGES;
+    using Ring = typename std::conditional<ANY_OUT, tc::AnyRing, tc::Ring<S::STAGES>>::type;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw_addr = tc::smem_u32_generic(smem_raw);
     uint8_t *smem = smem_raw + ((1024 - (raw_addr & 1023)) & 1023);
     const uint32_t ring = tc::smem_u32_generic(smem);
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + STAGES * S::STAGE + S::STAGING);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S::STAGES * S::STAGE + S::STAGING);
     const uint32_t full0 = tc::smem_u32_generic(bars);
     const uint32_t empty0 = full0 + 8 * STAGES;
     const uint32_t accf0 = empty0 + 8 * STAGES;   // accumulator b holds a finished tile
     const uint32_t acce0 = accf0 + 8 * ACCS;      // accumulator b has been drained
     const uint32_t done_bar = acce0 + 8 * ACCS;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + S::BARS);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + BARS);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
     // (broadcast: the compiler then knows that a warp takes one role as a whole)
@@ -251,7 +291,7 @@ __device__ __forceinline__ void linear_tc_body(const Maps &map, const Params<E> 
     const int nk = kb1 - kb0;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < STAGES; ++s) {
+        for (int s = 0; s < stages; ++s) {
             tc::mbar_init(full0 + 8 * s, 1);
             tc::mbar_init(empty0 + 8 * s, 1);
         }
@@ -294,12 +334,12 @@ __device__ __forceinline__ void linear_tc_body(const Maps &map, const Params<E> 
         if constexpr (FORM == kGated) {
             // one matrix's rows in the even CTA, the other's in the odd one; both in
             // a CTA on its own
-            const int n0 = tn * OUT;
+            const int n0 = tn * out;
 #pragma unroll
             for (int h = 0; h < 3 - CTAS; ++h) {
                 const CUtensorMap *w = (CTAS == 2 ? half : h) ? map.B2 : map.B;
-                const int at = h * OUT * kRowBytes;
-                if (OUT < 64 || p.b_kmajor) {   // (32 features an MN-major line are not laid out)
+                const int at = h * out * kRowBytes;
+                if (p.b_kmajor) {
                     f(w, at, k0, n0);
                 } else {
 #pragma unroll
@@ -322,7 +362,7 @@ __device__ __forceinline__ void linear_tc_body(const Maps &map, const Params<E> 
         // 8192 and back of 64 rows 39.2 -> 38.4 us in bf16, 28.8 -> 27.8 in 8 bits
         int tm, tn;
         raster(p.tiles_m, p.tiles_n, p.group_m, p.tile0 + first, tm, tn);
-        for (int kb = kb0; kb < min(kb1, kb0 + S::KS * STAGES); ++kb)
+        for (int kb = kb0; kb < min(kb1, kb0 + S::KS * stages); ++kb)
             boxes_of_b(tn, kb, [&](const CUtensorMap *w, int, int c0, int c1) {
                 tma_prefetch(w, c0, c1);
             });
@@ -333,16 +373,17 @@ __device__ __forceinline__ void linear_tc_body(const Maps &map, const Params<E> 
     if (warp == 0) {
         if (tc::elect_one()) {
             // ---------------- TMA producer: this CTA's rows of A and B
-            const uint32_t tx = (uint32_t)(CTAS * (p.a_bytes + S::B_TILE));
+            const int b_bytes = ANY_OUT ? 2 * out * kRowBytes : S::B_TILE;
+            const uint32_t tx = (uint32_t)(CTAS * (p.a_bytes + b_bytes));
             const uint32_t fulls = CTAS == 2 ? cluster_addr(full0, leader) : full0;
-            tc::Ring<STAGES> r;
+            Ring r(stages);
             bool stop = false;
             for (int i = 0; i < ntiles && !stop; ++i) {
                 int tm, tn;
                 raster(p.tiles_m, p.tiles_n, p.group_m, p.tile0 + first + i * stride, tm, tn);
                 const int m0 = (tm * CTAS + half) * BM;
                 for (int kb = kb0; kb < kb1; kb += S::KS) {
-                    if (r.used == STAGES && !tc::wait(empty0 + 8 * r.s, r.parity ^ 1, abort_flag)) {
+                    if (r.used == stages && !tc::wait(empty0 + 8 * r.s, r.parity ^ 1, abort_flag)) {
                         stop = true;
                         break;
                     }
@@ -352,7 +393,7 @@ __device__ __forceinline__ void linear_tc_body(const Maps &map, const Params<E> 
 #pragma unroll
                     for (int j = 0; j < S::KS; ++j) {
                         if (j >= subs) break;
-                        const uint32_t st = ring + r.s * S::STAGE + j * S::SUB;
+                        const uint32_t st = ring + r.s * stage_bytes + j * sub;
                         const CUtensorMap *a = map.A;
                         int ka = kb + j;
                         if constexpr (FORM == kSum) {
@@ -370,7 +411,7 @@ __device__ __forceinline__ void linear_tc_body(const Maps &map, const Params<E> 
                                 tma_load<CTAS>(st + c * kBox, a, fb, m0 + 64 * c, k0);
                         }
                         boxes_of_b(tn, kb + j, [&](const CUtensorMap *w, int at, int c0, int c1) {
-                            tma_load<CTAS>(st + S::A_TILE + at, w, fb, c0, c1);
+                            tma_load<CTAS>(st + a_tile + at, w, fb, c0, c1);
                         });
                     }
                     r.next();
@@ -383,7 +424,7 @@ __device__ __forceinline__ void linear_tc_body(const Maps &map, const Params<E> 
         if (half == 0 && tc::elect_one()) {
             // ---------------- MMA issuer, for the whole pair
             const uint64_t astep = p.a_kmajor ? 2 : 128, bstep = p.b_kmajor ? 2 : 128;
-            tc::Ring<STAGES> r;
+            Ring r(stages);
             bool stop = false;
             for (int i = 0; i < ntiles && !stop; ++i) {
                 const int b = i % ACCS, u = i / ACCS;
@@ -399,10 +440,10 @@ __device__ __forceinline__ void linear_tc_body(const Maps &map, const Params<E> 
 #pragma unroll
                     for (int j = 0; j < S::KS; ++j) {
                         if (kb + j >= nk) break;
-                        const uint32_t st = ring + r.s * S::STAGE + j * S::SUB;
+                        const uint32_t st = ring + r.s * stage_bytes + j * sub;
                         const uint64_t ad = p.a_kmajor ? tc::kmajor_desc<128>(st) : mnmajor_desc(st);
-                        const uint64_t bd = p.b_kmajor ? tc::kmajor_desc<128>(st + S::A_TILE)
-                                                       : mnmajor_desc(st + S::A_TILE);
+                        const uint64_t bd = p.b_kmajor ? tc::kmajor_desc<128>(st + a_tile)
+                                                       : mnmajor_desc(st + a_tile);
                         if (p.fp8) {
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
@@ -426,13 +467,15 @@ __device__ __forceinline__ void linear_tc_body(const Maps &map, const Params<E> 
         // ---------------- epilogue: this CTA's rows
         if (reads_global(p.epi)) chain_fence(p.chain);   // through L1
         const int q = warp & 3, side = (warp - 2) >> 2;
-        const uint32_t stage = ring + STAGES * S::STAGE + (uint32_t)((warp - 2) * kStage);
+        const uint32_t stage = ring + RING + (uint32_t)((warp - 2) * kStage);
         for (int i = 0; i < ntiles; ++i) {
             const int b = i % ACCS, u = i / ACCS;
             int tm, tn;
             raster(p.tiles_m, p.tiles_n, p.group_m, p.tile0 + first + i * stride, tm, tn);
-            const int m0 = (tm * CTAS + half) * BM, n0 = tn * OUT + side * (OUT / 2);
-            if constexpr (FORM != kGated)
+            const int m0 = (tm * CTAS + half) * BM, n0 = tn * out + side * (OUT / 2);
+            if constexpr (FORM == kGated)
+                prefetch_terms<O>(p.epi, lane, n0, min(p.epi.N, (tn + 1) * out));
+            else
                 prefetch_residual<O>(p.epi, m0 + 32 * q + lane, n0, BN / 2);
             const bool ok = tc::wait(accf0 + 8 * b, u & 1, abort_flag);
             __syncwarp();
@@ -460,11 +503,10 @@ __device__ __forceinline__ void linear_tc_body(const Maps &map, const Params<E> 
                     }
                 }
             } else if constexpr (FORM == kGated) {
-                // blocks of 32 outputs a side; the narrowest tile's one block is side 0's
-                constexpr int BLOCKS = OUT / 64 > 0 ? OUT / 64 : 1;
+                constexpr int BLOCKS = OUT / 64;   // of 32 outputs a side
                 const uint32_t gate = tmem + (uint32_t)(b * BN + side * 32 * BLOCKS);
-                if (OUT >= 64 || side == 0)
-                    finish_gated_rows<BLOCKS, O>(p, map, gate, gate + OUT, q, lane, m0, n0, stage);
+                finish_gated_rows<BLOCKS, O>(p, map, gate, gate + (uint32_t)out, q, lane, m0, n0,
+                                             min(p.epi.N, (tn + 1) * out), stage);
             } else {
                 finish_rows<BN / 2, O>(p, map.Y, map.Z, acc, q, lane, m0, n0, stage);
             }
@@ -492,10 +534,16 @@ __device__ __forceinline__ void linear_tc_body(const Maps &map, const Params<E> 
         raster(p.tiles_m, p.tiles_n, p.group_m, p.tile0 + first, tm, tn);
         const int m0 = (tm * CTAS + half) * BM;
         const int rows = min(BM, p.epi.M - m0);
-        const int n0 = tn * OUT;
-        if (parts == 2) join_parts<2, CTAS, BN, O>(p.epi, ring, part, half, m0, n0, rows);
-        if (parts == 4) join_parts<4, CTAS, BN, O>(p.epi, ring, part, half, m0, n0, rows);
-        if (parts == 8) join_parts<8, CTAS, BN, O>(p.epi, ring, part, half, m0, n0, rows);
+        const int n0 = tn * out;
+        if constexpr (FORM == kGated) {
+            if (parts == 2) join_gated<2, CTAS, BN, O>(p.epi, ring, part, half, m0, n0, rows, out);
+            if (parts == 4) join_gated<4, CTAS, BN, O>(p.epi, ring, part, half, m0, n0, rows, out);
+            if (parts == 8) join_gated<8, CTAS, BN, O>(p.epi, ring, part, half, m0, n0, rows, out);
+        } else {
+            if (parts == 2) join_parts<2, CTAS, BN, O>(p.epi, ring, part, half, m0, n0, rows);
+            if (parts == 4) join_parts<4, CTAS, BN, O>(p.epi, ring, part, half, m0, n0, rows);
+            if (parts == 8) join_parts<8, CTAS, BN, O>(p.epi, ring, part, half, m0, n0, rows);
+        }
     }
     if (*abort_flag && threadIdx.x == 0 && p.error != nullptr) atomicOr(p.error, 1u);
     if (warp == 1 && *abort_flag) {

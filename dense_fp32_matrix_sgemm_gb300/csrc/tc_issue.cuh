@@ -35,6 +35,8 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int
 template <int N>
 struct Ring {
     int s = 0, parity = 0, used = 0;
+    Ring() = default;
+    __device__ __forceinline__ explicit Ring(int) {}
     __device__ __forceinline__ void next() {
         if (used < N) ++used;
         if (++s == N) {
@@ -44,10 +46,23 @@ struct Ring {
     }
 };
 
+// The same of a number of stages that the launch says.
+struct AnyRing {
+    int n, s = 0, parity = 0, used = 0;
+    __device__ __forceinline__ explicit AnyRing(int stages) : n(stages) {}
+    __device__ __forceinline__ void next() {
+        if (used < n) ++used;
+        if (++s == n) {
+            s = 0;
+            parity ^= 1;
+        }
+    }
+};
+
 // Waits (bounded) until the latest fill of every used stage has landed: a CTA
 // that gave up does not leave with copies in flight.
-template <int N>
-__device__ __forceinline__ void drain_ring(const Ring<N> &r, uint32_t full0) {
+template <class R>
+__device__ __forceinline__ void drain_ring(const R &r, uint32_t full0) {
     for (int s = 0; s < r.used; ++s) {
         const int parity = s < r.s ? r.parity : r.parity ^ 1;
         const long long t0 = clock64();

@@ -120,6 +120,17 @@ def test_gated_strides_and_offsets(m, pad, offset, t):
         run_gated(m, 171, 201, t, "none", pad=pad, offset=offset, w_kn=True)
 
 
+# tiles of every width that the rounds of SMs call for, whole and in parts of K, of few and many rows
+@pytest.mark.parametrize("t", ["bf16", "e4m3"])
+@pytest.mark.parametrize("m,n,k", [(64, 8192, 264), (9, 11264, 136), (100, 300, 4096), (8, 4096, 2208),
+                                   (130, 1369, 1001), (33, 16000, 72), (40, 1216, 200), (70, 2432, 129),
+                                   (128, 24, 2048), (2000, 600, 264), (120, 19000, 64)])
+def test_gated_tile_widths(m, n, k, t):
+    run_gated(m, n, k, t, "silu", bias=True, preact=True)
+    run_gated(m, n, k, t, "gelu")
+    run_gated(m, n, k, t, "none", preact=True, pad=8)
+
+
 # long sums: tiles with K split over clusters, whole waves followed by a split rest
 @pytest.mark.parametrize("m,n,k,t", [(1024, 1024, 8192, "f32"), (1000, 1025, 8200, "bf16"),
                                      (1020, 1020, 16400, "e4m3"), (2560, 1280, 2600, "f32"),
