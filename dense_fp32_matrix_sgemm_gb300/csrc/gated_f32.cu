@@ -34,9 +34,9 @@ sum_f32_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
 
 template <int CTAS, int BN, bool SPLIT>
 cudaError_t launch_gated(const F32Planes &X, const F32Planes &Wg, const F32Planes &Wu, int K,
-                         const GatedEpi &epi, const Piece &piece, int chain, cudaStream_t s) {
+                         const GatedEpi &epi, const Piece &piece, int out, int chain,
+                         cudaStream_t s) {
     using S = Shape<CTAS, BN, SPLIT>;
-    constexpr int OUT = BN / 2;
     static PerContext<bool> configured;
     bool done = false;
     cudaError_t e;
@@ -46,15 +46,17 @@ cudaError_t launch_gated(const F32Planes &X, const F32Planes &Wg, const F32Plane
         if (e != cudaSuccess) return e;
         configured.put(current_context_id(), true);
     }
-    if (OUT < 64 && !Wg.kmajor) return cudaErrorInvalidValue;
     Params<GatedEpi> p;
     p.epi = epi;
     const int a_rows = fill_params<CTAS, BN>(p, epi.M, 2 * epi.N, K, X.kmajor, Wg.kmajor, piece,
                                              chain);
+    p.out = out;
+    p.tiles_n = (epi.N + out - 1) / out;
+    p.idesc = instruction_desc(SGEMM_BF16, CTAS * BM, 2 * out, X.kmajor, Wg.kmajor);
     CUtensorMap tmX, tmG, tmU;
     if (!plane_map(&tmX, X.planes, X.rows, X.cols, X.kmajor ? a_rows : 64) ||
-        !plane_map(&tmG, Wg.planes, Wg.rows, Wg.cols, Wg.kmajor ? OUT : 64) ||
-        !plane_map(&tmU, Wu.planes, Wu.rows, Wu.cols, Wu.kmajor ? OUT : 64))
+        !plane_map(&tmG, Wg.planes, Wg.rows, Wg.cols, Wg.kmajor ? out : 64) ||
+        !plane_map(&tmU, Wu.planes, Wu.rows, Wu.cols, Wu.kmajor ? out : 64))
         return cudaErrorInvalidValue;
     Config c(ctas_of<CTAS, SPLIT>(piece), S::SMEM, SPLIT ? CTAS * piece.parts : CTAS, s);
     return cudaLaunchKernelEx(&c.cfg, gated_f32_kernel<CTAS, BN, SPLIT>, tmX, tmG, tmU, p);
@@ -89,9 +91,32 @@ cudaError_t launch_sum(const F32Planes (&A)[2], const F32Planes (&B)[2], int K, 
                               tmB[1], tmY, p);
 }
 
-// The shapes of weights stored K x N: no 64-wide tile (32 features of each weight).
-constexpr Costs<3> kByInput = {{{2, 256}, {2, 128}, {1, 128}}, {1.66, 0.89, 1.05}, {8.5, 8.0, 6.0},
-                               {5.0, 3.0, 3.0}};
+// Tiles of a CTA on its own (of weights stored K x N the second: a shared-memory line is 64
+// features).
+constexpr Costs<2> kSingles = {{{1, 64}, {1, 128}}, {0.78, 1.05}, {6.0, 6.0}, {1.5, 3.0}};
+constexpr Costs<1> kSingle = {{{1, 128}}, {1.05}, {6.0}, {3.0}};
+
+// Pairs' tiles of 256 rows and `out` outputs, a multiple of 16 up to 128 (weights stored K x N: 64
+// or 128), at costs between kCosts' widths.  The width is what makes whole rounds of the SMs:
+// 1000 x 1369 x 1001 takes 44 tiles of 128 outputs on 76 pairs, 76 of 72 (42 us, 32 so).
+struct Pairs {
+    int out = 128;
+    Plan plan;
+};
+Pairs plan_pairs(int M, int N, int kblocks, const Capacity &cap, bool any_out) {
+    Pairs best;
+    const int step = any_out ? 16 : 64;
+    for (int out = step; out <= 128; out += step) {
+        const Costs<1> cost = {{{2, 2 * out}}, {0.12 + 0.01203 * out}, {7.5 + 0.0078 * out},
+                               {1.0 + 0.031 * out}};
+        const Plan plan = plan_tiles(M, 2 * N, kblocks, cap, cost);
+        if (plan.us < best.plan.us) {
+            best.out = out;
+            best.plan = plan;
+        }
+    }
+    return best;
+}
 
 }  // namespace f32
 
@@ -111,17 +136,25 @@ cudaError_t launch_gated_f32(const F32Planes &X, const F32Planes &Wg, const F32P
     cudaError_t e = capacity(cap);
     if (e != cudaSuccess) return e;
     const int kblocks = (K + f32::kBk - 1) / f32::kBk;
-    if (Wg.kmajor) {
-        const Plan plan = plan_tiles(epi.M, 2 * epi.N, kblocks, cap, f32::kCosts);
-        return run_plan(f32::kCosts, plan, 0, [&](auto w, auto split, const Piece &p, int at) {
-            constexpr TileShape t = f32::kCosts.shape[w()];
-            return f32::launch_gated<t.ctas, t.bn, split()>(X, Wg, Wu, K, epi, p, at, s);
+    const f32::Pairs pairs = f32::plan_pairs(epi.M, epi.N, kblocks, cap, Wg.kmajor);
+    const Plan one = Wg.kmajor ? plan_tiles(epi.M, 2 * epi.N, kblocks, cap, f32::kSingles)
+                               : plan_tiles(epi.M, 2 * epi.N, kblocks, cap, f32::kSingle);
+    auto launch = [&](auto ctas, auto bn, auto split, const Piece &p, int out, int at) {
+        return f32::launch_gated<ctas(), bn(), split()>(X, Wg, Wu, K, epi, p, out, at, s);
+    };
+    using std::integral_constant;
+    if (one.us < pairs.plan.us) {
+        const bool narrow = Wg.kmajor && one.shape == 0;
+        return run_plan(f32::kSingles, one, 0, [&](auto, auto split, const Piece &p, int at) {
+            const integral_constant<int, 1> single;
+            return narrow ? launch(single, integral_constant<int, 64>(), split, p, 32, at)
+                          : launch(single, integral_constant<int, 128>(), split, p, 64, at);
         });
     }
-    const Plan plan = plan_tiles(epi.M, 2 * epi.N, kblocks, cap, f32::kByInput);
-    return run_plan(f32::kByInput, plan, 0, [&](auto w, auto split, const Piece &p, int at) {
-        constexpr TileShape t = f32::kByInput.shape[w()];
-        return f32::launch_gated<t.ctas, t.bn, split()>(X, Wg, Wu, K, epi, p, at, s);
+    return run_plan(f32::kSingle, pairs.plan, 0, [&](auto, auto split, const Piece &p, int at) {
+        const integral_constant<int, 2> pair;
+        return pairs.out > 64 ? launch(pair, integral_constant<int, 256>(), split, p, pairs.out, at)
+                              : launch(pair, integral_constant<int, 128>(), split, p, pairs.out, at);
     });
 }
 

@@ -59,16 +59,14 @@ cudaError_t launch_gated(int type, const TcOperand &X, const TcOperand &Wg, cons
     const int a_rows = fill_params<CTAS, BN>(p, type, epi.M, 2 * epi.N, K, X.kmajor, Wg.kmajor,
                                              piece, chain);
     p.out = out;
-    if constexpr (CTAS == 1) {
-        p.tiles_n = (epi.N + out - 1) / out;
-        p.a_tile = a_rows * kRowBytes;
-        p.sub = p.a_tile + 2 * out * kRowBytes;
-        // (the MMAs read 128 rows of A wherever the tile ends: the last one's stay in the ring)
-        const int over = S::A_TILE > p.sub ? S::A_TILE - p.sub : 0;
-        p.stages = (S::STAGES * S::STAGE - over) / (S::KS * p.sub);
-        if (p.stages > kMostStages) p.stages = kMostStages;
-        p.idesc = instruction_desc(type, BM, 2 * out, X.kmajor, Wg.kmajor);
-    }
+    p.tiles_n = (epi.N + out - 1) / out;
+    p.a_tile = a_rows * kRowBytes;
+    p.sub = p.a_tile + (3 - CTAS) * out * kRowBytes;
+    // (the MMAs read 128 rows of A wherever the tile ends: the last one's stay in the ring)
+    const int over = S::A_TILE > p.sub ? S::A_TILE - p.sub : 0;
+    p.stages = (S::STAGES * S::STAGE - over) / (S::KS * p.sub);
+    if (p.stages > kMostStages) p.stages = kMostStages;
+    p.idesc = instruction_desc(type, CTAS * BM, 2 * out, X.kmajor, Wg.kmajor);
     CUtensorMap tmX, tmG, tmU, tmH = {}, tmZg = {}, tmZu = {};
     if (!operand_map(&tmX, X, type, epi.M, K, a_rows) ||
         !operand_map(&tmG, Wg, type, epi.N, K, out) || !operand_map(&tmU, Wu, type, epi.N, K, out))
@@ -112,7 +110,29 @@ cudaError_t launch_sum(int type, const TcOperand (&A)[2], const TcOperand (&B)[2
 // Costs as linear_tc.cu's.
 constexpr Costs<3> kSumCosts = {{{2, 256}, {2, 128}, {1, 64}}, {0.27, 0.165, 0.15},
                                 {6.5, 5.5, 4.5}, {5.0, 3.0, 1.5}};
-constexpr Costs<2> kPairs = {{{2, 256}, {2, 128}}, {0.27, 0.165}, {6.5, 5.5}, {5.0, 3.0}};
+
+// Pairs' tiles of 256 rows and `out` outputs (a multiple of 16 up to 128; weights stored K x N:
+// 64 or 128): kSumCosts between its widths, and the weights' way from HBM as in plan_single
+// (here at 41 bytes a ns and SM).
+struct Pairs {
+    int out = 128;
+    Plan plan;
+};
+Pairs plan_pairs(int M, int N, int kblocks, const Capacity &cap, bool any_out) {
+    Pairs best;
+    const int row_tiles = (M + 2 * BM - 1) / (2 * BM), step = any_out ? 16 : 64;
+    for (int out = step; out <= 128; out += step) {
+        const double l2 = out < 64 ? 0.165 : 0.06 + 0.00164 * out, hbm = 0.0031 * out / row_tiles;
+        const Costs<1> cost = {{{2, 2 * out}}, {hbm > l2 ? hbm : l2},
+                               {out < 64 ? 5.5 : 4.5 + 0.0156 * out}, {1.0 + 0.031 * out}};
+        const Plan plan = plan_tiles(M, 2 * N, kblocks, cap, cost);
+        if (plan.us < best.plan.us) {
+            best.out = out;
+            best.plan = plan;
+        }
+    }
+    return best;
+}
 
 // Tiles of a CTA on its own: 128 rows and `out` outputs, a multiple of 8 up to 128, in `parts`
 // parts of K.  The width is what makes whole rounds of the SMs (64 x 8192 x 4096: 128 tiles of 64
@@ -126,7 +146,7 @@ constexpr int kNarrow = 64, kWide = 128;   // the most outputs of either kernel
 
 // Costs in us.  128 bytes of K take the issuing thread's three copies (0.15), the operands'
 // way from L2, or, where no other row tile shares the weights, theirs from HBM at 45 bytes a ns
-// and SM (kPairs' tiles at 41); the rest of a launch is 4.5, 5 % more of it all where whole tiles
+// and SM; the rest of a launch is 4.5, 5 % more of it all where whole tiles
 // come from HBM, and joining parts 0.7 to 1.3 and 1 for 64 outputs of 128 rows.  Against the other
 // choices, weights out of L2, outputs / parts:
 //   64 x 8192 x 4096 bf16 56/1 24.1 (64/1 24.2, 32/1 28.4, 112/2 26.1); e4m3 56/1 15.6 (32/1 19.2)
@@ -167,15 +187,9 @@ cudaError_t gated_dispatch(int type, const TcOperand &X, const TcOperand &Wg, co
     if (e != cudaSuccess) return e;
     const int bk = kRowBytes / dtype_size(type);
     const int kblocks = (K + bk - 1) / bk;
-    Costs<2> pairs = kPairs;
-    for (int w = 0; w < 2; ++w) {   // (see plan_single)
-        const int bm = kPairs.shape[w].ctas * BM;
-        const double hbm = 0.0063 * (kPairs.shape[w].bn / 4) / ((epi.M + bm - 1) / bm);
-        if (hbm > pairs.stage[w]) pairs.stage[w] = hbm;
-    }
-    const Plan plan = plan_tiles(epi.M, 2 * epi.N, kblocks, cap, pairs);
+    const Pairs pairs = plan_pairs(epi.M, epi.N, kblocks, cap, Wg.kmajor);
     const Single one = plan_single(epi.M, epi.N, kblocks, cap, Wg.kmajor);
-    if (one.us < plan.us) {
+    if (one.us < pairs.plan.us) {
         const Piece p = {0, (int)one.tiles, one.parts, cap.sms};
         auto launch = [&](auto wide, auto split) {
             return launch_gated<1, 2 * (wide() ? kWide : kNarrow), O, split()>(
@@ -186,9 +200,11 @@ cudaError_t gated_dispatch(int type, const TcOperand &X, const TcOperand &Wg, co
         if (one.out > kNarrow) return one.parts > 1 ? launch(yes, yes) : launch(yes, no);
         return one.parts > 1 ? launch(no, yes) : launch(no, no);
     }
-    return run_plan(kPairs, plan, 0, [&](auto w, auto split, const Piece &p, int at) {
-        constexpr TileShape t = kPairs.shape[w()];
-        return launch_gated<t.ctas, t.bn, O, split()>(type, X, Wg, Wu, K, epi, p, t.bn / 2, at, s);
+    return run_plan(Costs<1>(), pairs.plan, 0, [&](auto, auto split, const Piece &p, int at) {
+        return pairs.out > kNarrow
+                   ? launch_gated<2, 2 * kWide, O, split()>(type, X, Wg, Wu, K, epi, p, pairs.out, at, s)
+                   : launch_gated<2, 2 * kNarrow, O, split()>(type, X, Wg, Wu, K, epi, p, pairs.out, at,
+                                                              s);
     });
 }
 

@@ -34,6 +34,7 @@ struct Params {
     E epi;
     int kblocks;
     int kblocks1;       // kSum: of the first product's K, where the second begins
+    int out;            // kGated, pairs: outputs of a tile
     int tiles_m, tiles_n, group_m;
     int tile0, tiles;        // this launch's tiles: tile0 .. tile0 + tiles - 1
     int chain;
@@ -111,7 +112,11 @@ template <Form FORM, int CTAS, int BN, bool SPLIT, class E>
 __device__ __forceinline__ void linear_f32_body(const Maps &map, const Params<E> &p) {
     using S = Shape<CTAS, BN, SPLIT>;
     constexpr int RING = S::RING, SLOTS = S::SLOTS, COLS = BN / 2;
-    constexpr int OUT = FORM == kGated ? BN / 2 : BN;   // output columns of a tile
+    // output columns of a tile; of pairs' gated ones any multiple of 8 up to OUT (weights stored
+    // K x N: OUT)
+    constexpr int OUT = FORM == kGated ? BN / 2 : BN;
+    constexpr bool ANY_OUT = FORM == kGated && CTAS == 2;
+    const int out = ANY_OUT ? p.out : OUT;
     constexpr bool CLUSTER = CTAS == 2 || SPLIT;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw_addr = tc::smem_u32_generic(smem_raw);
@@ -177,7 +182,8 @@ __device__ __forceinline__ void linear_f32_body(const Maps &map, const Params<E>
     if (warp == 0) {
         if (tc::elect_one()) {
             // ---------------- TMA producer: a stage's planes in the issuer's order
-            const uint32_t tx = (uint32_t)(CTAS * (p.a_bytes + S::B_TILE));
+            const uint32_t tx =
+                (uint32_t)(CTAS * (p.a_bytes + (ANY_OUT ? out * kRowBytes : S::B_TILE)));
             const uint32_t fulls = CTAS == 2 ? cluster_addr(full0, leader) : full0;
             tc::Ring<RING> r;
             bool stop = false;
@@ -215,7 +221,7 @@ __device__ __forceinline__ void linear_f32_body(const Maps &map, const Params<E>
                         }
                         if constexpr (FORM == kGated) {
                             // (the weights' places as in linear_tc_body)
-                            const int n0 = tn * OUT;
+                            const int n0 = tn * out;
 #pragma unroll
                             for (int h = 0; h < 3 - CTAS; ++h) {
                                 const CUtensorMap *w = (CTAS == 2 ? half : h) ? map.B2 : mb;
@@ -312,7 +318,10 @@ __device__ __forceinline__ void linear_f32_body(const Maps &map, const Params<E>
         for (int i = 0; i < ntiles && !stop; ++i) {
             int tm, tn;
             raster(p.tiles_m, p.tiles_n, p.group_m, p.tile0 + first + i * stride, tm, tn);
-            const int row0 = (tm * CTAS + half) * BM + 32 * q, n0 = tn * OUT + side * (OUT / 2);
+            // a side's columns: half of them, in blocks of 16 for gated tiles
+            const int wide = ANY_OUT ? (out + 31) / 32 * 16 : OUT / 2;
+            const int row0 = (tm * CTAS + half) * BM + 32 * q, n0 = tn * out + side * wide;
+            const int end = min(p.epi.N, tn * out + min(out, (side + 1) * wide));
             if constexpr (FORM != kGated) prefetch_residual<float>(p.epi, row0 + lane, n0, COLS);
             float run[COLS];
 #pragma unroll
@@ -327,12 +336,12 @@ __device__ __forceinline__ void linear_f32_body(const Maps &map, const Params<E>
                 }
                 tc::fence_after_sync();
                 // (kGated: half of the side's columns are gates, half their factors)
-                const uint32_t base = tmem + (uint32_t)(slot.s * BN + side * (OUT / 2)) +
+                const uint32_t base = tmem + (uint32_t)(slot.s * BN + side * wide) +
                                       ((uint32_t)(32 * q) << 16);
 #pragma unroll
                 for (int b = 0; b < COLS / 16; ++b) {
                     float v[16];
-                    const int at = FORM == kGated && b >= OUT / 32 ? OUT + 16 * b - OUT / 2 : 16 * b;
+                    const int at = FORM == kGated && b >= OUT / 32 ? out + 16 * b - OUT / 2 : 16 * b;
                     tc::tmem_ld_16(base + at, v);
 #pragma unroll
                     for (int j = 0; j < 16; ++j) run[16 * b + j] += v[j];
@@ -355,9 +364,12 @@ __device__ __forceinline__ void linear_f32_body(const Maps &map, const Params<E>
                 const int r = 32 * q + lane;
 #pragma unroll
                 for (int j = 0; j < COLS / 4; ++j) {
-                    const int at = FORM == kGated && j >= OUT / 8 ? OUT / 4 + j - OUT / 8 : j;
+                    const bool up = FORM == kGated && j >= OUT / 8;
+                    const int at = side * (wide / 4) + (up ? j - OUT / 8 : j);
+                    // (past a side's columns are the other one's, or none)
+                    if (ANY_OUT && 4 * (up ? j - OUT / 8 : j) >= min(wide, out - side * wide)) continue;
                     tc::st_shared_v4(ring + (uint32_t)(r * BN * 4) +
-                                         ((uint32_t)((side * (OUT / 8) + at) ^ (r & 7)) << 4),
+                                         ((uint32_t)((at + (up ? out / 4 : 0)) ^ (r & 7)) << 4),
                                      run[4 * j], run[4 * j + 1], run[4 * j + 2], run[4 * j + 3]);
                 }
             } else if constexpr (FORM == kGated) {
@@ -365,7 +377,7 @@ __device__ __forceinline__ void linear_f32_body(const Maps &map, const Params<E>
                 // gates and factors leave, the others move down
                 const int rows = min(32, p.epi.M - row0);
 #pragma unroll 1
-                for (int c = 0; c < OUT / 32 && n0 + 16 * c < p.epi.N; ++c) {
+                for (int c = 0; c < OUT / 32 && n0 + 16 * c < end; ++c) {
                     __syncwarp();   // the previous block has been read
                     stage_pair16(stage, lane, run, run + OUT / 2);
                     __syncwarp();
@@ -374,8 +386,7 @@ __device__ __forceinline__ void linear_f32_body(const Maps &map, const Params<E>
                         run[j] = run[j + 16];
                         run[OUT / 2 + j] = run[OUT / 2 + j + 16];
                     }
-                    finish_gated_staged<float, 8>(p.epi, stage, lane, row0, rows, n0 + 16 * c,
-                                                  p.epi.N);
+                    finish_gated_staged<float, 8>(p.epi, stage, lane, row0, rows, n0 + 16 * c, end);
                 }
             } else {
                 const int rows = min(32, p.epi.M - row0);
@@ -418,14 +429,14 @@ __device__ __forceinline__ void linear_f32_body(const Maps &map, const Params<E>
         raster(p.tiles_m, p.tiles_n, p.group_m, p.tile0 + first, tm, tn);
         const int m0 = (tm * CTAS + half) * BM;
         const int rows = min(BM, p.epi.M - m0);
-        const int n0 = tn * OUT;
+        const int n0 = tn * out;
         if constexpr (FORM == kGated) {
             if (parts == 2)
-                join_gated<2, CTAS, BN, float>(p.epi, ring, part, half, m0, n0, rows, OUT);
+                join_gated<2, CTAS, BN, float>(p.epi, ring, part, half, m0, n0, rows, out);
             if (parts == 4)
-                join_gated<4, CTAS, BN, float>(p.epi, ring, part, half, m0, n0, rows, OUT);
+                join_gated<4, CTAS, BN, float>(p.epi, ring, part, half, m0, n0, rows, out);
             if (parts == 8)
-                join_gated<8, CTAS, BN, float>(p.epi, ring, part, half, m0, n0, rows, OUT);
+                join_gated<8, CTAS, BN, float>(p.epi, ring, part, half, m0, n0, rows, out);
         } else {
             if (parts == 2) join_parts<2, CTAS, BN, float>(p.epi, ring, part, half, m0, n0, rows);
             if (parts == 4) join_parts<4, CTAS, BN, float>(p.epi, ring, part, half, m0, n0, rows);

@@ -7,7 +7,7 @@
 namespace sgemm {
 namespace ltc {
 
-constexpr int kMostStages = 12;   // of a gated CTA on its own
+constexpr int kMostStages = 12;   // of a gated tile
 
 template <int CTAS, int BN, bool SPLIT>
 struct Shape {
@@ -40,7 +40,7 @@ struct Params {
     int a_bytes;             // bytes A's boxes bring to a CTA's stage
     uint32_t idesc;
     int fp8;
-    int out;                 // kGated, a CTA on its own: outputs of a tile,
+    int out;                 // kGated: outputs of a tile,
     int a_tile, sub, stages; //   bytes of A's rows and of 128 bytes of K in a stage, stages
     int tma;                 // Y and Z leave by TMA store, whole blocks of 32 columns
     unsigned *error;
@@ -240,17 +240,18 @@ __device__ __forceinline__ void finish_gated_rows(const Params<GatedEpi> &p, con
 template <Form FORM, int CTAS, int BN, class O, bool SPLIT, class E>
 __device__ __forceinline__ void linear_tc_body(const Maps &map, const Params<E> &p) {
     using S = Shape<CTAS, BN, SPLIT>;
-    constexpr int STAGES = FORM == kGated && CTAS == 1 ? kMostStages : S::STAGES, ACCS = S::ACCS;
+    constexpr int STAGES = FORM == kGated ? kMostStages : S::STAGES, ACCS = S::ACCS;
     constexpr int BARS = 2 * STAGES + 2 * ACCS + 1;
     static_assert(BARS * 8 + 8 <= 256, "barrier area");
     constexpr bool CLUSTER = CTAS == 2 || SPLIT;
-    // output columns of a tile, a multiple of 8 up to 64 for a gated CTA on its own
+    // output columns of a tile; gated ones any multiple of 8 up to OUT (weights stored K x N:
+    // OUT)
     constexpr int OUT = FORM == kGated ? BN / 2 : BN;
-    constexpr bool ANY_OUT = FORM == kGated && CTAS == 1;
+    constexpr bool ANY_OUT = FORM == kGated;
     const int out = ANY_OUT ? p.out : OUT;
     // Such a tile's stages are as large as its rows and outputs need, and as many as fit the
     // ring's place: 64 x 4096 x 4096 bf16 in tiles of 32 outputs was held by the 48 KB of
-    // weights that whole tiles' stages had in flight (XX us, YY so).
+    // weights that whole tiles' stages had in flight (18.6 us, 16.4 so).
     constexpr int RING = S::STAGES * S::STAGE;
     const int a_tile = ANY_OUT ? p.a_tile : S::A_TILE, sub = ANY_OUT ? p.sub : S::SUB;
     const int stage_bytes = ANY_OUT ? S::KS * sub : S::STAGE;
@@ -373,7 +374,7 @@ __device__ __forceinline__ void linear_tc_body(const Maps &map, const Params<E> 
     if (warp == 0) {
         if (tc::elect_one()) {
             // ---------------- TMA producer: this CTA's rows of A and B
-            const int b_bytes = ANY_OUT ? 2 * out * kRowBytes : S::B_TILE;
+            const int b_bytes = ANY_OUT ? (3 - CTAS) * out * kRowBytes : S::B_TILE;
             const uint32_t tx = (uint32_t)(CTAS * (p.a_bytes + b_bytes));
             const uint32_t fulls = CTAS == 2 ? cluster_addr(full0, leader) : full0;
             Ring r(stages);
@@ -472,9 +473,12 @@ __device__ __forceinline__ void linear_tc_body(const Maps &map, const Params<E> 
             const int b = i % ACCS, u = i / ACCS;
             int tm, tn;
             raster(p.tiles_m, p.tiles_n, p.group_m, p.tile0 + first + i * stride, tm, tn);
-            const int m0 = (tm * CTAS + half) * BM, n0 = tn * out + side * (OUT / 2);
+            const int m0 = (tm * CTAS + half) * BM;
+            // a side's columns: half of them, in blocks of 32 for gated tiles
+            const int wide = ANY_OUT ? (out + 63) / 64 * 32 : OUT / 2;
+            const int n0 = tn * out + side * wide, end = min(p.epi.N, tn * out + min(out, (side + 1) * wide));
             if constexpr (FORM == kGated)
-                prefetch_terms<O>(p.epi, lane, n0, min(p.epi.N, (tn + 1) * out));
+                prefetch_terms<O>(p.epi, lane, n0, end);
             else
                 prefetch_residual<O>(p.epi, m0 + 32 * q + lane, n0, BN / 2);
             const bool ok = tc::wait(accf0 + 8 * b, u & 1, abort_flag);
@@ -503,10 +507,9 @@ __device__ __forceinline__ void linear_tc_body(const Maps &map, const Params<E> 
                     }
                 }
             } else if constexpr (FORM == kGated) {
-                constexpr int BLOCKS = OUT / 64;   // of 32 outputs a side
-                const uint32_t gate = tmem + (uint32_t)(b * BN + side * 32 * BLOCKS);
-                finish_gated_rows<BLOCKS, O>(p, map, gate, gate + (uint32_t)out, q, lane, m0, n0,
-                                             min(p.epi.N, (tn + 1) * out), stage);
+                const uint32_t gate = tmem + (uint32_t)(b * BN + side * wide);
+                finish_gated_rows<OUT / 64, O>(p, map, gate, gate + (uint32_t)out, q, lane, m0, n0,
+                                               end, stage);
             } else {
                 finish_rows<BN / 2, O>(p, map.Y, map.Z, acc, q, lane, m0, n0, stage);
             }
