@@ -80,6 +80,47 @@ struct Raw {
         }
     }
 };
+// 8- and 4-byte accesses, for rows that are aligned to no more.
+template <class T>
+struct Half {   // 8 bytes
+    static constexpr int W = 8 / sizeof(T);
+    uint2 u;
+    __device__ __forceinline__ void load(const T *p) { u = *reinterpret_cast<const uint2 *>(p); }
+    __device__ __forceinline__ void zero() { u = make_uint2(0, 0); }
+    __device__ __forceinline__ void get(float (&f)[W]) const {
+        if constexpr (W == 2) {
+            f[0] = __uint_as_float(u.x);
+            f[1] = __uint_as_float(u.y);
+        } else {
+            const float2 a = unpack2<T>(u.x), b = unpack2<T>(u.y);
+            f[0] = a.x;
+            f[1] = a.y;
+            f[2] = b.x;
+            f[3] = b.y;
+        }
+    }
+};
+template <>
+struct Raw<float, 2> : Half<float> {};
+template <>
+struct Raw<__nv_bfloat16, 4> : Half<__nv_bfloat16> {};
+template <>
+struct Raw<__half, 4> : Half<__half> {};
+template <class T>
+struct Pair16 {   // 4 bytes of a 16-bit type
+    uint32_t u;
+    __device__ __forceinline__ void load(const T *p) { u = *reinterpret_cast<const uint32_t *>(p); }
+    __device__ __forceinline__ void zero() { u = 0; }
+    __device__ __forceinline__ void get(float (&f)[2]) const {
+        const float2 v = unpack2<T>(u);
+        f[0] = v.x;
+        f[1] = v.y;
+    }
+};
+template <>
+struct Raw<__nv_bfloat16, 2> : Pair16<__nv_bfloat16> {};
+template <>
+struct Raw<__half, 2> : Pair16<__half> {};
 template <class T>
 struct Raw<T, 1> {
     T u;
@@ -93,6 +134,12 @@ template <class T, int W>
 __device__ __forceinline__ void put(T *p, const float (&f)[W]) {
     if constexpr (W == 1) {
         *p = from_f32<T>(f[0]);
+    } else if constexpr (W * sizeof(T) == 8 && sizeof(T) == 4) {
+        *reinterpret_cast<float2 *>(p) = make_float2(f[0], f[1]);
+    } else if constexpr (W * sizeof(T) == 8) {
+        *reinterpret_cast<uint2 *>(p) = make_uint2(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]));
+    } else if constexpr (W * sizeof(T) == 4) {
+        *reinterpret_cast<uint32_t *>(p) = pack2<T>(f[0], f[1]);
     } else if constexpr (sizeof(T) == 4) {
         *reinterpret_cast<float4 *>(p) = make_float4(f[0], f[1], f[2], f[3]);
     } else {

@@ -14,6 +14,7 @@
 // in registers over a group's rows, go to the workspace a row a CTA, and are added in a fixed
 // order by one more pass.
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda_runtime.h>
 
@@ -254,7 +255,7 @@ __global__ void __launch_bounds__(MAXT) layer_grad_kernel(const LayerGradArgs a)
     };
     // where they do not, it is brought to L2 in the meantime, a lane a 128-byte line
     auto prefetch_row = [&](int64_t row) {
-        constexpr int LANES = W > 1 ? 128 / (W * (int)sizeof(T)) : 32;
+        constexpr int LANES = W * (int)sizeof(T) >= 4 ? 128 / (W * (int)sizeof(T)) : 32;
         if (row >= a.rows || threadIdx.x % LANES != 0) return;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -606,34 +607,52 @@ cudaError_t launch_row(const LayerRowArgs &a, Shape sh, cudaStream_t s) {
     return launch(layer_row_kernel<T, W, NV, kMaxThreads, QUANT>, grid, block, a, s);
 }
 
-template <class T, bool QUANT>
-cudaError_t row_dispatch(const LayerRowArgs &a, bool vec, cudaStream_t s) {
-    constexpr int W = 16 / sizeof(T);
-    if (vec) {
-        const int64_t n = a.D / W;
-        Shape sh = shape_for(n, 1);
-        // few rows: as many threads as possible on each, for its latency
-        if (sh.tpr > 0 && a.rows <= 304) return launch_row<T, W, 1, QUANT>(a, sh, s);
-        sh = shape_for(n, 4);
-        if (sh.tpr > 0) return launch_row<T, W, 4, QUANT>(a, sh, s);
-    } else {
-        const Shape sh = shape_for(a.D, 8);
-        if (sh.tpr > 0) return launch_row<T, 1, 8, QUANT>(a, sh, s);
+// Widest access of a call's rows, in elements: 16 bytes down to one element, by halves.
+template <class... M>
+int access_of(int size, int64_t D, const M &...aligned) {
+    for (int w = 16 / size; w > 1; w /= 2)
+        if (D % w == 0 && (aligned(w) && ...)) return w;
+    return 1;
+}
+
+// NV accesses of W elements a thread.  Rows of one element an access that need more than 512
+// threads at eight take sixteen: one CTA an SM would wait for each of its phases alone.
+template <class T, int W, bool QUANT>
+cudaError_t row_accesses(const LayerRowArgs &a, cudaStream_t s) {
+    constexpr bool WHOLE = W * sizeof(T) == 16;
+    const int64_t n = a.D / W;
+    // few rows: as many threads as possible on each, for its latency
+    Shape sh = shape_for(n, 1);
+    if (WHOLE && sh.tpr > 0 && a.rows <= 304) return launch_row<T, W, 1, QUANT>(a, sh, s);
+    constexpr int NV = WHOLE ? 4 : W * sizeof(T) == 8 ? 4 : 8;
+    sh = shape_for(n, NV);
+    if (sh.tpr > 0 && (WHOLE || sh.tpr <= 512)) return launch_row<T, W, NV, QUANT>(a, sh, s);
+    if constexpr (!WHOLE) {
+        sh = shape_for(n, 2 * NV);
+        if (sh.tpr > 0) return launch_row<T, W, 2 * NV, QUANT>(a, sh, s);
     }
     return launch(layer_row_wide_kernel<T, QUANT>, dim3((unsigned)a.rows), dim3(kMaxThreads), a, s);
 }
 
+template <class T, bool QUANT>
+cudaError_t row_dispatch(const LayerRowArgs &a, cudaStream_t s) {
+    constexpr int size = sizeof(T);
+    const int w = access_of(size, a.D, [&](int w) {
+        return aligned_to(a.X, a.ldx, size, w) && aligned_to(a.R, a.ldr, size, w) &&
+               aligned_to(a.w, 0, size, w) && aligned_to(a.b, 0, size, w) &&
+               aligned_to(a.S, a.lds, size, w) && aligned_to(a.Y, a.ldy, QUANT ? 1 : size, w);
+    });
+    if constexpr (size == 2)
+        if (w == 8) return row_accesses<T, 8, QUANT>(a, s);
+    if (w == 4) return row_accesses<T, 4, QUANT>(a, s);
+    return w == 2 ? row_accesses<T, 2, QUANT>(a, s) : row_accesses<T, 1, QUANT>(a, s);
+}
+
 template <bool QUANT>
 cudaError_t row_types(int type, const LayerRowArgs &a, cudaStream_t s) {
-    const int size = dtype_size(type), w = 16 / size;
-    const bool vec = a.D % w == 0 && aligned16(a.X, a.ldx, size) && aligned16(a.R, a.ldr, size) &&
-                     aligned16(a.w, 0, size) && aligned16(a.b, 0, size) &&
-                     aligned16(a.S, a.lds, size) &&
-                     (QUANT ? reinterpret_cast<uintptr_t>(a.Y) % 8 == 0 && a.ldy % 8 == 0
-                            : aligned16(a.Y, a.ldy, size));
-    if (type == SGEMM_F32) return row_dispatch<float, QUANT>(a, vec, s);
-    if (type == SGEMM_BF16) return row_dispatch<__nv_bfloat16, QUANT>(a, vec, s);
-    return row_dispatch<__half, QUANT>(a, vec, s);
+    if (type == SGEMM_F32) return row_dispatch<float, QUANT>(a, s);
+    if (type == SGEMM_BF16) return row_dispatch<__nv_bfloat16, QUANT>(a, s);
+    return row_dispatch<__half, QUANT>(a, s);
 }
 
 // The backward pass's row groups: as many CTAs as the SMs hold at once, at most one group
@@ -650,10 +669,10 @@ bool ring_takes(int type, int64_t rows, int64_t D, Shape sh) {
     return sh.tpr > 0 && sh.tpr <= 512 && D * dtype_size(type) >= 1024 &&
            rows >= 152 * 4 * (512 / sh.tpr);
 }
-GradShape grad_shape(int type, int64_t rows, int64_t D, bool vec) {
+GradShape grad_shape(int type, int64_t rows, int64_t D, int w) {
     GradShape g = {};
-    if (vec) {
-        const int w = 16 / dtype_size(type);
+    const bool whole = w * dtype_size(type) == 16;
+    if (whole) {
         g.sh = shape_for(D / w, 16 / w);
         if (ring_takes(type, rows, D, g.sh)) {
             g.sh.groups = 512 / g.sh.tpr;
@@ -664,9 +683,9 @@ GradShape grad_shape(int type, int64_t rows, int64_t D, bool vec) {
             return g;
         }
     }
-    g.w = vec ? 16 / dtype_size(type) : 1;
-    const int64_t n = (D + g.w - 1) / g.w;
-    g.nv = vec ? 2 : 8;
+    g.w = w;
+    const int64_t n = (D + w - 1) / w;
+    g.nv = whole ? 2 : w * dtype_size(type) == 8 ? 4 : 8;
     g.sh = shape_for(n, g.nv);
     if (g.sh.tpr == 0) {
         g.nv = 0;
@@ -715,11 +734,17 @@ cudaError_t grad_dispatch(const LayerGradArgs &a, const GradShape &g, cudaStream
     if (g.ring) return launch_ring<T>(a, g, s);
     const dim3 grid((unsigned)g.ctas), block((unsigned)g.sh.tpr, (unsigned)g.sh.groups);
     if (g.nv == 0) return launch(layer_grad_wide_kernel<T>, grid, block, a, s);
-    if (g.w == 1)
-        return g.sh.tpr <= 512 ? launch(layer_grad_kernel<T, 1, 8, 512>, grid, block, a, s)
-                               : launch(layer_grad_kernel<T, 1, 8, kMaxThreads>, grid, block, a, s);
-    return g.sh.tpr <= 512 ? launch(layer_grad_kernel<T, W, 2, 512>, grid, block, a, s)
-                           : launch(layer_grad_kernel<T, W, 2, kMaxThreads>, grid, block, a, s);
+    auto run = [&](auto w, auto nv) {
+        return g.sh.tpr <= 512
+                   ? launch(layer_grad_kernel<T, w(), nv(), 512>, grid, block, a, s)
+                   : launch(layer_grad_kernel<T, w(), nv(), kMaxThreads>, grid, block, a, s);
+    };
+    using std::integral_constant;
+    if (g.w == W) return run(integral_constant<int, W>(), integral_constant<int, 2>());
+    if (g.w == W / 2) return run(integral_constant<int, W / 2>(), integral_constant<int, 4>());
+    if constexpr (W == 8)
+        if (g.w == 2) return run(integral_constant<int, 2>(), integral_constant<int, 8>());
+    return run(integral_constant<int, 1>(), integral_constant<int, 8>());
 }
 
 }  // namespace
@@ -735,12 +760,15 @@ cudaError_t launch_add_layernorm(int type, int64_t rows, int64_t D, const void *
                               : norm::row_types<false>(type, a, s);
 }
 
-// Rows of partial sums, the larger of the aligned and the unaligned plan (the caller's
-// pointers decide which one runs).
+// Rows of partial sums, the most of any access's plan (the caller's pointers decide which
+// one runs).
 int layernorm_backward_parts(int type, int64_t rows, int64_t D) {
-    const norm::GradShape a = norm::grad_shape(type, rows, D, true);
-    const norm::GradShape b = norm::grad_shape(type, rows, D, false);
-    return a.ctas > b.ctas ? a.ctas : b.ctas;
+    int most = 0;
+    for (int w = 16 / dtype_size(type); w >= 1; w /= 2) {
+        const int ctas = norm::grad_shape(type, rows, D, w).ctas;
+        most = ctas > most ? ctas : most;
+    }
+    return most;
 }
 
 cudaError_t launch_add_layernorm_backward(int type, int64_t rows, int64_t D, const void *dY,
@@ -748,11 +776,14 @@ cudaError_t launch_add_layernorm_backward(int type, int64_t rows, int64_t D, con
                                           const float *mean, const float *rstd, const void *w,
                                           const void *dS, int64_t ldds, void *dX, int64_t lddx,
                                           void *dw, void *db, float *partial, cudaStream_t s) {
-    const int size = dtype_size(type), width = 16 / size;
-    const bool vec = D % width == 0 && norm::aligned16(dY, lddy, size) &&
-                     norm::aligned16(S, lds, size) && norm::aligned16(w, 0, size) &&
-                     norm::aligned16(dS, ldds, size) && norm::aligned16(dX, lddx, size);
-    const norm::GradShape g = norm::grad_shape(type, rows, D, vec);
+    const int size = dtype_size(type);
+    const int width = norm::access_of(size, D, [&](int n) {
+        using norm::aligned_to;
+        return aligned_to(dY, lddy, size, n) && aligned_to(S, lds, size, n) &&
+               aligned_to(w, 0, size, n) && aligned_to(dS, ldds, size, n) &&
+               aligned_to(dX, lddx, size, n);
+    });
+    const norm::GradShape g = norm::grad_shape(type, rows, D, width);
     const bool sums = dw != nullptr || db != nullptr;
     const norm::LayerGradArgs a = {dY,   S,    w,    dS,   dX,   mean, rstd, sums ? partial : nullptr,
                                    lddy, lds, ldds, lddx, rows, (int)D};

@@ -59,6 +59,8 @@ __device__ __forceinline__ void store_codes(uint8_t *p, const float (&y)[W]) {
                                                    to_e4m3x4(y[4], y[5], y[6], y[7]));
     } else if constexpr (W == 4) {
         *reinterpret_cast<uint32_t *>(p) = to_e4m3x4(y[0], y[1], y[2], y[3]);
+    } else if constexpr (W == 2) {
+        *reinterpret_cast<uint16_t *>(p) = (uint16_t)to_e4m3x4(y[0], y[1], 0.f, 0.f);
     } else {
 #pragma unroll
         for (int i = 0; i < W; ++i) p[i] = to_e4m3(y[i]);
@@ -79,6 +81,14 @@ inline Shape shape_for(int64_t n, int nv) {
     s.tpr = per <= 32 ? 32 : (int)((per + 31) / 32 * 32);
     s.groups = s.tpr >= 256 ? 1 : 256 / s.tpr;
     return s;
+}
+
+// Elements of the widest access (16, 8 or 4 bytes, or one element) that rows of D elements allow:
+// what every base and leading dimension (of `size`-byte elements; an 8-bit output's of one byte
+// an element) is a multiple of.
+inline bool aligned_to(const void *p, int64_t ld, int size, int elements) {
+    return p == nullptr ||
+           (reinterpret_cast<uintptr_t>(p) % (uintptr_t)(size * elements) == 0 && ld % elements == 0);
 }
 
 inline bool aligned16(const void *p, int64_t ld, int size) {

@@ -450,6 +450,24 @@ def test_add_layernorm_strides(pad, offset, quantize, t):
     run_layernorm(400, 520, t, False, True, quantize, pad, offset)
 
 
+# accesses of 8 and 4 bytes and of one element, groups of every width
+@pytest.mark.parametrize("t", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("rows,d", [(3, 12), (40, 1002), (320, 1004), (330, 6428), (500, 6426), (310, 6427),
+                                    (2, 12004), (2, 12002), (3, 12001), (1, 16386)])
+def test_add_layernorm_accesses(rows, d, t):
+    run_layernorm(rows, d, t, True, True, False)
+    run_layernorm(rows, d, t, True, True, True)
+    run_layernorm_backward(rows, d, t, True)
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+@pytest.mark.parametrize("pad,offset", [(4, 0), (2, 0), (0, 2), (0, 4), (6, 2)])
+def test_add_layernorm_accesses_by_alignment(pad, offset, t):
+    run_layernorm(20, 512, t, True, True, False, pad, offset)
+    run_layernorm(20, 512, t, True, True, True, pad, offset)
+    run_layernorm_backward(400, 520, t, True, pad, offset)
+
+
 @pytest.mark.parametrize("rows,d", [(4, 64), (9, 1001), (3, 4096), (400, 4096), (2, 40000)])
 @pytest.mark.parametrize("mean", [1e2, -1e4])
 def test_add_layernorm_keeps_a_large_mean_out_of_the_variance(rows, d, mean):
