@@ -41,7 +41,7 @@ int gated_vector_width(int type, const GatedEpi &e) {
                aligned(e.bg, bytes) && aligned(e.bu, bytes) && aligned(e.sg, n == 8 ? 16 : 4) &&
                aligned(e.su, n == 8 ? 16 : 4);
     };
-    return size == 2 && all(8) ? 8 : all(4) ? 4 : 1;
+    return size == 2 && all(8) ? 8 : all(4) ? 4 : size == 2 && all(2) ? 2 : 1;
 }
 
 // Operands that TMA cannot read where they lie, copied to the workspace in one launch.

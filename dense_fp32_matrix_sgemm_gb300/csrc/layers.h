@@ -42,8 +42,8 @@ struct LayerEpi {
 // What happens to the two accumulators of a gated layer:
 //   z = acc * (sx ? sx[row] * s[col] : 1) + b[col] for the gate (g) and its factor (u)
 //   H = act(zg) zu;  Zg = zg, Zu = zu where they are kept
-// vec: 8 (16-bit types only: 16-byte accesses), 4 or 1 elements that every base and
-// leading dimension is aligned to.
+// vec: 8 (16-bit types only: 16-byte accesses), 4, 2 (16-bit types) or 1 elements that every
+// base and leading dimension is aligned to.
 struct GatedEpi {
     void *H, *Zg, *Zu;
     const void *bg, *bu;

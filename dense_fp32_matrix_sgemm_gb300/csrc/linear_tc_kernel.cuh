@@ -165,12 +165,66 @@ __device__ __forceinline__ void store_row8s(void *base, int64_t ld, int row, int
                            pack2<O>(v[j + 4], v[j + 5]), pack2<O>(v[j + 6], v[j + 7]));
 }
 
+// v = v sx s[col ..] + b[col ..] for n of 32 columns, s and b of any alignment: a lane loads
+// its column's terms and the warp shares them.
+template <class O>
+__device__ __forceinline__ void scale_and_bias_any(float (&v)[32], float sx, const float *s,
+                                                   const void *b, int col, int n, int lane) {
+    if (s != nullptr) {
+        const float x = lane < n ? s[col + lane] : 0.f;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] *= sx * __shfl_sync(0xffffffffu, x, j);
+    }
+    if (b != nullptr) {
+        const float x = lane < n ? to_f32(static_cast<const O *>(b)[col + lane]) : 0.f;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] += __shfl_sync(0xffffffffu, x, j);
+    }
+}
+
+// n of 32 values of every lane's row into rows of any alignment, through the staging block: a
+// row at a time, a column a lane, or (vec >= 2: rows of whole 4-byte words, n even) two rows of
+// pairs.  (Finished from fp32 a column a lane, 4096 x 4095 x 1024 took 59 us, where aligned rows
+// take 39; 40 so.)
+template <class O>
+__device__ __forceinline__ void store_rows_any(uint32_t stage, int lane, void *base, int64_t ld,
+                                               int vec, int row0, int rows, int col, int n,
+                                               const float (&v)[32]) {
+    __syncwarp();   // the block is free
+    stage_row<O>(stage, lane, v);
+    __syncwarp();
+    O *const p = static_cast<O *>(base) + row0 * ld + col;
+    // element (r, c): 16-byte chunk c / 8 of row r at its place of the swizzle
+    if (vec >= 2 && n % 2 == 0) {
+        const int c = 2 * (lane & 15), half = lane >> 4;
+        O *to = p + half * ld + c;
+#pragma unroll 8
+        for (int r = half; r < rows; r += 2, to += 2 * ld) {
+            uint32_t x;
+            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x)
+                         : "r"(stage + (uint32_t)r * 64u + ((uint32_t)((c >> 3) ^ ((r >> 1) & 3)) << 4) +
+                               (uint32_t)(c & 7) * 2u) : "memory");
+            if (c < n) *reinterpret_cast<uint32_t *>(to) = x;
+        }
+    } else {
+        O *to = p + lane;
+#pragma unroll 8
+        for (int r = 0; r < rows; ++r, to += ld) {
+            uint16_t x;
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x)
+                         : "r"(stage + (uint32_t)r * 64u + ((uint32_t)((lane >> 3) ^ ((r >> 1) & 3)) << 4) +
+                               (uint32_t)(lane & 7) * 2u) : "memory");
+            if (lane < n) *reinterpret_cast<uint16_t *>(to) = x;
+        }
+    }
+}
+
 // finish_rows for tiles whose accumulators hold gates and, some columns on, their factors:
 // 32 outputs at a time, up to column `end`, both sums in registers.  A staging block holds
 // two of the three results, so the pre-activations leave first.  (The wait for them to be
 // read overlaps the next tile's MMAs.)  Fewer than 32 outputs (a tile's width is a multiple
 // of 8) leave by 16-byte stores, a row a lane; what is not aligned to that passes through the
-// staging block.
+// staging block in smaller stores.
 template <int BLOCKS, class O>
 __device__ __forceinline__ void finish_gated_rows(const Params<GatedEpi> &p, const Maps &map,
                                                   uint32_t gate, uint32_t up, int q, int lane,
@@ -192,14 +246,14 @@ __device__ __forceinline__ void finish_gated_rows(const Params<GatedEpi> &p, con
         tc::tmem_ld_32(up + lanes + (uint32_t)(32 * c), u);
         if (!p.tma || n % 8 != 0) {
             const int rows = min(32, e.M - row0);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (16 * h >= n) break;
-                __syncwarp();   // the block has been read
-                stage_pair16(stage, lane, v + 16 * h, u + 16 * h);
-                __syncwarp();
-                finish_gated_staged<O, 8>(e, stage, lane, row0, rows, col + 16 * h, end);
-            }
+            scale_and_bias_any<O>(v, sx, e.sg, e.bg, col, n, lane);
+            scale_and_bias_any<O>(u, sx, e.su, e.bu, col, n, lane);
+            if (e.Zg != nullptr)
+                store_rows_any<O>(stage, lane, e.Zg, e.ldg, e.vec, row0, rows, col, n, v);
+            if (e.Zu != nullptr)
+                store_rows_any<O>(stage, lane, e.Zu, e.ldu, e.vec, row0, rows, col, n, u);
+            gate_all<O>(v, u, e.act);
+            store_rows_any<O>(stage, lane, e.H, e.ldh, e.vec, row0, rows, col, n, v);
             continue;
         }
         scale_and_bias32<O>(v, sx, e.sg, e.bg, col, n);
