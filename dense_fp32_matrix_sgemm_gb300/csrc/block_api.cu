@@ -262,7 +262,8 @@ int gated_linear_backward(int dtype, int64_t M, int64_t N, int64_t K, const void
                                at, s);
         else
             e = launch_sum_tc(dtype, {{zg, p.lddz, true}, {zu, p.lddz, true}},
-                              {{Wg, ldwg, transW == 0}, {Wu, ldwu, transW == 0}}, (int)N, epi, at, s);
+                              {{Wg, ldwg, transW == 0}, {Wu, ldwu, transW == 0}}, 2, (int)N, epi, at,
+                              s);
     }
     for (int i = 0; i < 2 && e == cudaSuccess; ++i) {
         if (!(i == 0 ? dwg : dwu)) continue;
@@ -274,7 +275,8 @@ int gated_linear_backward(int dtype, int64_t M, int64_t N, int64_t K, const void
             e = launch_linear_f32(transW ? G : Xp, transW ? Xp : G, (int)M, epi, at, s);
         } else {
             const TcOperand G = {z, p.lddz, false}, Xo = {X, ldx, false};
-            e = launch_linear_tc(dtype, transW ? G : Xo, transW ? Xo : G, (int)M, epi, at, s);
+            const TcOperand &A = transW ? G : Xo, &B = transW ? Xo : G;
+            e = launch_sum_tc(dtype, {A, A}, {B, B}, 1, (int)M, epi, at, s);
         }
     }
     if (db && e == cudaSuccess)

@@ -253,19 +253,20 @@ scale_kernel(const __grid_constant__ Table<MOST> table, const double *partial, i
     pdl_wait();
     if (threadIdx.x < 32) {
         constexpr int U = 10;   // in flight; a launch's sums of CTAs in one go
-        double d = 0.0;
+        double sum = 0.0;
         for (int i = threadIdx.x; i < parts; i += 32 * U) {
             double x[U];
 #pragma unroll
             for (int u = 0; u < U; ++u)
                 x[u] = i + 32 * u < parts ? __ldcg(partial + i + 32 * u) : 0.0;
 #pragma unroll
-            for (int u = 0; u < U; ++u) d += x[u];
+            for (int u = 0; u < U; ++u) sum += x[u];
         }
-        const double n = sqrt(warp_sum(d));
+        const double n = sqrt(warp_sum(sum));
         if (threadIdx.x == 0) {
             if (norm != nullptr && blockIdx.x == 0) *norm = (float)n;
-            const double c = (double)max_norm / (n + (double)eps);
+            // (nothing to scale where both are 0)
+            const double d = n + (double)eps, c = d == 0.0 ? 1.0 : (double)max_norm / d;
             // (a NaN stays one; a factor that fp32 holds with few digits, for norms beyond
             // 1e36 times max_norm, is applied in two steps)
             const bool tiny = c < 0x1p-120;

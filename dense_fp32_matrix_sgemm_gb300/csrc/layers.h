@@ -71,9 +71,9 @@ struct ProductSize {
 // launch_linear_tc takes them; both weights stored in one order.
 cudaError_t launch_gated_tc(int in_type, const TcOperand &X, const TcOperand &Wg,
                             const TcOperand &Wu, int K, const GatedEpi &epi, cudaStream_t s);
-// D = A1 B1^T + A2 B2^T, each reduction K long.
-cudaError_t launch_sum_tc(int in_type, const TcOperand (&A)[2], const TcOperand (&B)[2], int K,
-                          const LayerEpi &epi, int chain, cudaStream_t s);
+// D = A1 B1^T + A2 B2^T, each reduction K long (count 1: the first alone).  epi: Y alone.
+cudaError_t launch_sum_tc(int in_type, const TcOperand (&A)[2], const TcOperand (&B)[2], int count,
+                          int K, const LayerEpi &epi, int chain, cudaStream_t s);
 // The gated product of few rows on the CUDA cores, one pass over both weights; any type and
 // alignment, weights stored by output features.  linear_rows.cu.
 cudaError_t launch_gated_rows(int in_type, const void *X, int64_t ldx, const void *Wg, int64_t ldwg,

@@ -260,7 +260,8 @@ __device__ __forceinline__ void join_parts(const LayerEpi &e, uint32_t ring, int
 // gated_f32.cu):
 //   kGated  B's rows of a tile are half of one matrix's and half of another's, which
 //           meet in the epilogue: BN accumulator columns are BN / 2 outputs;
-//   kSum    D = A B^T + A2 B2^T, the reductions one behind the other.
+//   kSum    D = A B^T + A2 B2^T, the reductions one behind the other, and no other terms (or
+//           D = A B^T alone: the gradients of the weights).
 // kPlain: neither.
 enum Form { kPlain, kGated, kSum };
 

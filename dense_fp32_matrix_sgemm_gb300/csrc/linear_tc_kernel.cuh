@@ -62,15 +62,52 @@ __device__ __forceinline__ void stage_row(uint32_t block, int lane, const float 
                         "r"(pack2<O>(v[8 * c + 6], v[8 * c + 7])) : "memory");
 }
 
+// n of 32 values of every lane's row into rows of any alignment, through the staging block: a
+// row at a time, a column a lane, or (vec >= 2: rows of whole 4-byte words, n even) two rows of
+// pairs.  (Finished from fp32 a column a lane, 4096 x 4095 x 1024 took 59 us, where aligned rows
+// take 39; 40 so.)
+template <class O>
+__device__ __forceinline__ void store_rows_any(uint32_t stage, int lane, void *base, int64_t ld,
+                                               int vec, int row0, int rows, int col, int n,
+                                               const float (&v)[32]) {
+    __syncwarp();   // the block is free
+    stage_row<O>(stage, lane, v);
+    __syncwarp();
+    O *const p = static_cast<O *>(base) + row0 * ld + col;
+    // element (r, c): 16-byte chunk c / 8 of row r at its place of the swizzle
+    if (vec >= 2 && n % 2 == 0) {
+        const int c = 2 * (lane & 15), half = lane >> 4;
+        O *to = p + half * ld + c;
+#pragma unroll 8
+        for (int r = half; r < rows; r += 2, to += 2 * ld) {
+            uint32_t x;
+            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x)
+                         : "r"(stage + (uint32_t)r * 64u + ((uint32_t)((c >> 3) ^ ((r >> 1) & 3)) << 4) +
+                               (uint32_t)(c & 7) * 2u) : "memory");
+            if (c < n) *reinterpret_cast<uint32_t *>(to) = x;
+        }
+    } else {
+        O *to = p + lane;
+#pragma unroll 8
+        for (int r = 0; r < rows; ++r, to += ld) {
+            uint16_t x;
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x)
+                         : "r"(stage + (uint32_t)r * 64u + ((uint32_t)((lane >> 3) ^ ((r >> 1) & 3)) << 4) +
+                               (uint32_t)(lane & 7) * 2u) : "memory");
+            if (lane < n) *reinterpret_cast<uint16_t *>(to) = x;
+        }
+    }
+}
+
 // Finishes COLS columns of the 32 tile rows of TMEM lane quarter q, a row a
 // lane, 32 columns at a time: the epilogue runs on the accumulators in
 // registers, Y and Z leave by TMA as whole 64-byte row pieces.  What TMA cannot
 // store (rows that are not 16-byte aligned, the last block of a width that is
 // not a multiple of 32) passes through the staging block in fp32 and is
-// finished with a column a lane.  The loop is kept rolled: a problem of one
+// finished with a column a lane (SUMS: there are no terms; by store_rows_any).  The loop is kept rolled: a problem of one
 // tile a CTA runs this code once, and fetching it cold costs more than running
 // it.
-template <int COLS, class O>
+template <int COLS, class O, bool SUMS>
 __device__ __forceinline__ void finish_rows(const Params<LayerEpi> &p, const void *tmY,
                                             const void *tmZ, uint32_t acc, int q, int lane, int m0,
                                             int n0, uint32_t stage) {
@@ -97,12 +134,19 @@ __device__ __forceinline__ void finish_rows(const Params<LayerEpi> &p, const voi
         tc::tmem_ld_32(lane_base + (uint32_t)(32 * c), v);
         if (!fast) {
             const int rows = min(32, e.M - row0);
+            if constexpr (SUMS) {
+                const bool words = reinterpret_cast<uintptr_t>(e.Y) % 4 == 0 && e.ldy % 2 == 0;
+                store_rows_any<O>(stage, lane, e.Y, e.ldy, words ? 2 : 1, row0, rows, col,
+                                  min(32, e.N - col), v);
+            } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                tc::st_shared_v4(stage + (uint32_t)lane * 128u + ((uint32_t)(j ^ (lane & 7)) << 4),
-                                 v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-            __syncwarp();
-            finish_staged<O, 8>(e, stage, lane, row0, rows, col + lane);
+                for (int j = 0; j < 8; ++j)
+                    tc::st_shared_v4(stage + (uint32_t)lane * 128u +
+                                         ((uint32_t)(j ^ (lane & 7)) << 4),
+                                     v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                __syncwarp();
+                finish_staged<O, 8>(e, stage, lane, row0, rows, col + lane);
+            }
             continue;   // (the next block's __syncwarp keeps it from overwriting this one)
         }
         if (e.sx != nullptr) {
@@ -179,43 +223,6 @@ __device__ __forceinline__ void scale_and_bias_any(float (&v)[32], float sx, con
         const float x = lane < n ? to_f32(static_cast<const O *>(b)[col + lane]) : 0.f;
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] += __shfl_sync(0xffffffffu, x, j);
-    }
-}
-
-// n of 32 values of every lane's row into rows of any alignment, through the staging block: a
-// row at a time, a column a lane, or (vec >= 2: rows of whole 4-byte words, n even) two rows of
-// pairs.  (Finished from fp32 a column a lane, 4096 x 4095 x 1024 took 59 us, where aligned rows
-// take 39; 40 so.)
-template <class O>
-__device__ __forceinline__ void store_rows_any(uint32_t stage, int lane, void *base, int64_t ld,
-                                               int vec, int row0, int rows, int col, int n,
-                                               const float (&v)[32]) {
-    __syncwarp();   // the block is free
-    stage_row<O>(stage, lane, v);
-    __syncwarp();
-    O *const p = static_cast<O *>(base) + row0 * ld + col;
-    // element (r, c): 16-byte chunk c / 8 of row r at its place of the swizzle
-    if (vec >= 2 && n % 2 == 0) {
-        const int c = 2 * (lane & 15), half = lane >> 4;
-        O *to = p + half * ld + c;
-#pragma unroll 8
-        for (int r = half; r < rows; r += 2, to += 2 * ld) {
-            uint32_t x;
-            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x)
-                         : "r"(stage + (uint32_t)r * 64u + ((uint32_t)((c >> 3) ^ ((r >> 1) & 3)) << 4) +
-                               (uint32_t)(c & 7) * 2u) : "memory");
-            if (c < n) *reinterpret_cast<uint32_t *>(to) = x;
-        }
-    } else {
-        O *to = p + lane;
-#pragma unroll 8
-        for (int r = 0; r < rows; ++r, to += ld) {
-            uint16_t x;
-            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x)
-                         : "r"(stage + (uint32_t)r * 64u + ((uint32_t)((lane >> 3) ^ ((r >> 1) & 3)) << 4) +
-                               (uint32_t)(lane & 7) * 2u) : "memory");
-            if (lane < n) *reinterpret_cast<uint16_t *>(to) = x;
-        }
     }
 }
 
@@ -565,7 +572,7 @@ __device__ __forceinline__ void linear_tc_body(const Maps &map, const Params<E> 
                 finish_gated_rows<OUT / 64, O>(p, map, gate, gate + (uint32_t)out, q, lane, m0, n0,
                                                end, stage);
             } else {
-                finish_rows<BN / 2, O>(p, map.Y, map.Z, acc, q, lane, m0, n0, stage);
+                finish_rows<BN / 2, O, FORM == kSum>(p, map.Y, map.Z, acc, q, lane, m0, n0, stage);
             }
             tc::fence_before_sync();   // the TMEM loads above precede the release
             __syncwarp();

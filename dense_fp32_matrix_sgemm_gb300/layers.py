@@ -186,12 +186,22 @@ def add_layernorm_backward(dy, s, mean, rstd, weight, ds=None, *, need_dweight=T
                                           workspace)
 
 
+def _listed(tensors):
+    """A list of tensors from one tensor or any iterable of them."""
+    if isinstance(tensors, torch.Tensor):
+        return [tensors]
+    try:
+        return list(tensors)
+    except TypeError:
+        raise TypeError("expected a tensor or an iterable of tensors") from None
+
+
 def grad_norm(tensors, *, workspace=None, stream=None):
-    """The 2-norm of all elements of a list of tensors, a float32 CUDA scalar.
+    """The 2-norm of all elements of a tensor or of an iterable of them, a float32 CUDA scalar.
 
     float32, bfloat16 and float16 tensors of one device in any mixture, of any shape and
     any order of dense strides.  The sum is held in 64 bits."""
-    tensors = list(tensors)
+    tensors = _listed(tensors)
     if stream is not None and tensors:
         with _on(stream, tensors[0]):
             return grad_norm(tensors, workspace=workspace)
@@ -199,14 +209,14 @@ def grad_norm(tensors, *, workspace=None, stream=None):
 
 
 def clip_grad_norm(tensors, max_norm, *, eps=1e-6, out=None, workspace=None, stream=None):
-    """Scales every tensor of a list by min(1, max_norm / (norm + eps)), norm as ``grad_norm``
-    gives it, and returns the norm.  Nothing waits for the norm on the host.
+    """Scales every tensor of an iterable (or one tensor) by min(1, max_norm / (norm + eps)), norm
+    as ``grad_norm`` gives it, and returns the norm.  Nothing waits for the norm on the host.
 
     In place, or with ``out`` (tensors of the same types, shapes and strides) there.  No
     result may overlap another one or another tensor of the list, so none is in the list
     twice.  An infinite norm scales by 0 (an infinite element becomes NaN); a NaN reaches
     every element."""
-    tensors = list(tensors)
+    tensors, out = _listed(tensors), None if out is None else _listed(out)
     if stream is not None and tensors:
         with _on(stream, tensors[0]):
             return clip_grad_norm(tensors, max_norm, eps=eps, out=out, workspace=workspace)

@@ -8,7 +8,7 @@ Serving: the weights brought to 8 bits once; every step the norm writes 8-bit
 rows with scales, both products read 8-bit operands, and the second adds the
 residual stream in its epilogue.
 
-    python examples/feed_forward.py [--tokens 512] [--width 1024] [--hidden 4096] [--steps 20]
+    python examples/feed_forward.py [--tokens 512] [--width 1024] [--hidden 4096] [--steps 20] [--max-norm 1]
 
 prints the loss of a few training steps on a fixed regression target and how far
 the 8-bit block's output is from the trained 16-bit one's.
@@ -48,7 +48,10 @@ class FeedForward:
         dx, dg = sg.add_rmsnorm_backward(dy, s, rstd, self.g, dout)   # the residual's gradient joins
         return dx, {"g": dg, "w1": dw1, "b1": db1, "w2": dw2}
 
-    def step(self, grads, rate):
+    def step(self, grads, rate, max_norm=None):
+        """One step; with ``max_norm`` along the gradients clipped by their common norm."""
+        if max_norm is not None:
+            sg.clip_grad_norm(grads.values(), max_norm)
         for name, d in grads.items():
             p = getattr(self, name)
             p.add_(d, alpha=-rate)
@@ -67,7 +70,7 @@ class FeedForward:
         return sg.linear(hq, q2, residual=s, x_scale=hs, w_scale=s2, out_dtype=x.dtype)
 
 
-def run(tokens=512, width=1024, hidden=4096, steps=20, dtype=torch.bfloat16):
+def run(tokens=512, width=1024, hidden=4096, steps=20, dtype=torch.bfloat16, max_norm=None):
     """(losses of the training steps, relative difference of the served output)"""
     g = torch.Generator(device="cuda").manual_seed(1)
     x, r, target = ((torch.randn(tokens, width, generator=g, device="cuda") * 0.5).to(dtype)
@@ -80,7 +83,7 @@ def run(tokens=512, width=1024, hidden=4096, steps=20, dtype=torch.bfloat16):
         losses.append(float(diff.float().square().mean()))
         _, grads = block.backward(diff * (2.0 / tokens), saved)
         # the second product's curvature grows with the hidden width (h has a mean)
-        block.step(grads, 1.0 / hidden)
+        block.step(grads, 1.0 / hidden, max_norm)
     out = block.forward(x, r)[0].float()
     block.quantize()
     served = block.serve(x, r).float()
@@ -91,7 +94,8 @@ if __name__ == "__main__":
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     for name, default in (("tokens", 512), ("width", 1024), ("hidden", 4096), ("steps", 20)):
         ap.add_argument("--" + name, type=int, default=default)
+    ap.add_argument("--max-norm", type=float, help="clip the gradients to this norm")
     a = ap.parse_args()
-    losses, off = run(a.tokens, a.width, a.hidden, a.steps)
+    losses, off = run(a.tokens, a.width, a.hidden, a.steps, max_norm=a.max_norm)
     print("loss:", " ".join("%.4f" % v for v in losses))
     print("8-bit against 16-bit output: %.2f %% in the 2-norm" % (100 * off))

@@ -142,7 +142,8 @@ uint64_t sgemm_add_layernorm_backward_workspace_size(int dtype, int64_t rows, in
  * The sum is held in 64 bits: values beyond 2^64 or below 2^-64 keep their
  * digits, and the norm is infinite only if it is beyond 3.4e38 or an element
  * is infinite.  An infinite norm gives the factor 0 (infinite elements become NaN), a
- * NaN makes the norm and, scaled, every element NaN.
+ * NaN makes the norm and, scaled, every element NaN.  Where norm + eps is 0 the
+ * factor is 1.
  * An empty list has norm 0.
  *   workspace   sgemm_clip_grad_norm_workspace_size(count, dtypes, sizes)
  *               bytes, 256-byte aligned.

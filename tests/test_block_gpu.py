@@ -747,6 +747,28 @@ def test_clip_zeros_nan_and_infinity():
         assert not any(x.any() for x in a)
 
 
+def test_clip_of_nothing_but_zeros_without_eps():
+    # norm + eps is 0: the factor is 1, not 0 / 0
+    a = torch.zeros(100, device="cuda")
+    for max_norm in (0.0, 1.0, float("inf")):
+        assert float(sg.clip_grad_norm([a], max_norm, eps=0.0)) == 0 and not a.any()
+
+
+def test_clip_takes_one_tensor_and_any_iterable():
+    a, b = normal(gen(1), 50, 7), normal(gen(2), 33)
+    want = exact_norm([a])
+    assert abs(float(sg.grad_norm(a)) - want) <= 10 * EPS * want
+    out = torch.empty_like(a)
+    sg.clip_grad_norm(a, 1.0, out=out)
+    kept = a.clone()
+    sg.clip_grad_norm(a, 1.0)
+    assert torch.equal(a, out) and not torch.equal(a, kept)
+    want = exact_norm([a, b])
+    norm = sg.clip_grad_norm((t for t in (a, b)), 0.5, out=iter([a, b]))
+    assert abs(float(norm) - want) <= 10 * EPS * want
+    assert exact_norm([a, b]) == pytest.approx(0.5, rel=1e-5)
+
+
 def test_clip_leaves_tensors_below_the_norm_as_they_are():
     a = some(("bf16", "f32"))
     a[3].fill_(float(2.0 ** -130))
@@ -865,3 +887,59 @@ def test_gated_block_in_8_bits():
         got = sg.linear(hq, qd, residual=s, x_scale=hs, w_scale=sdown)
         ref = want[:rows_used]
         assert float((got.double() - ref).norm() / ref.norm()) < 0.08
+
+
+def example(name):
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        name + ".py")
+    spec = importlib.util.spec_from_file_location(name + "_example", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
+
+
+@pytest.mark.parametrize("t", ["bf16", "f16"])
+def test_gated_example(t):
+    """It runs, and its gradients are the formula's: against autograd in 64 bits, 2 % in the
+    2-norm (as test_gated_block_trains_as_its_formula_says); the served output is within 8 %."""
+    module, dtype = example("gated_feed_forward"), TYPES[t]
+    losses, norms, off = module.run(130, 256, 520, 3, dtype)
+    assert all(np.isfinite(losses)) and all(np.isfinite(norms)) and off < 0.08
+    block = module.GatedFeedForward(256, 520, dtype)
+    g = gen(3)
+    x, r, dout = (normal(g, 40, 256, dtype=dtype) for _ in range(3))
+    out, saved = block.forward(x, r)
+    dx, grads = block.backward(dout, saved)
+    p = [v.double().requires_grad_(True) for v in (x, block.g, block.c, block.wg, block.wu, block.wd)]
+    S = p[0] + r.double()
+    Y = torch.nn.functional.layer_norm(S, (256,), p[1], p[2], 1e-5)
+    O = (torch.nn.functional.silu(Y @ p[3].t()) * (Y @ p[4].t())) @ p[5].t() + S
+    want = torch.autograd.grad((O * dout.double()).sum(), p)
+    for got, ref in zip([out, dx, *grads], [O.detach(), *want]):
+        assert float((got.double() - ref).norm() / ref.norm()) < 0.02
+    before = [getattr(block, n).clone() for n in block.PARAMETERS]
+    norm = block.step(grads, 0.5, 1e-2)
+    assert exact_norm(grads) <= 1e-2 * (1 + UNIT[dtype] + 12 * EPS) and float(norm) > 1e-2
+    # p + d alpha is rounded once more where it is stored
+    for old, n, d in zip(before, block.PARAMETERS, grads):
+        want = old.double() - 0.5 * d.double()
+        check(getattr(block, n), want, (UNIT[dtype] + 4 * EPS) * (want.abs() + d.double().abs()) +
+              TINY[dtype], n)
+
+
+def test_feed_forward_example_clips():
+    module = example("feed_forward")
+    losses, _ = module.run(70, 128, 256, 3, torch.bfloat16, max_norm=1e-3)
+    assert all(np.isfinite(losses))
+    block = module.FeedForward(128, 256, torch.float32)
+    g = gen(4)
+    x, r, dout = (normal(g, 30, 128) for _ in range(3))
+    _, saved = block.forward(x, r)
+    _, grads = block.backward(dout, saved)
+    before, want = block.w1.clone(), exact_norm(grads.values())
+    block.step(grads, 1.0, max_norm=0.25 * want)
+    assert exact_norm(grads.values()) == pytest.approx(0.25 * want, rel=1e-5)
+    check(block.w1, before.double() - grads["w1"].double(),
+          2 * EPS * (before.double().abs() + grads["w1"].double().abs()) + 1e-30, "w1")
