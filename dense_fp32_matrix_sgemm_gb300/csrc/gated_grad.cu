@@ -209,8 +209,8 @@ __global__ void __launch_bounds__(kThreads) repack3_kernel(const RepackArgs a) {
     }
 }
 
-bool aligned16(const void *p, int64_t ld, int size) {
-    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * size % 16 == 0;
+bool aligned_to(const void *p, int64_t ld, int size, int elements) {
+    return reinterpret_cast<uintptr_t>(p) % (uintptr_t)(size * elements) == 0 && ld % elements == 0;
 }
 
 template <class... P, class... A>
@@ -228,12 +228,15 @@ cudaError_t launch(void (*kernel)(P...), dim3 grid, int block, cudaStream_t s, A
 }
 
 template <class T>
-cudaError_t dz_types(const DzArgs &a, bool vec, int parts, cudaStream_t s) {
-    constexpr int W = 16 / sizeof(T);
-    const int strip = 32 * (vec ? W : 1);
+cudaError_t dz_types(const DzArgs &a, int w, int parts, cudaStream_t s) {
+    const int strip = 32 * w;
     const dim3 grid((unsigned)((a.N + strip - 1) / strip), (unsigned)parts);
-    return vec ? launch(gated_dz_kernel<T, W>, grid, kThreads, s, a)
-               : launch(gated_dz_kernel<T, 1>, grid, kThreads, s, a);
+    if constexpr (sizeof(T) == 2) {
+        if (w == 8) return launch(gated_dz_kernel<T, 8>, grid, kThreads, s, a);
+        if (w == 2) return launch(gated_dz_kernel<T, 2>, grid, kThreads, s, a);
+    }
+    return w == 4 ? launch(gated_dz_kernel<T, 4>, grid, kThreads, s, a)
+                  : launch(gated_dz_kernel<T, 1>, grid, kThreads, s, a);
 }
 
 }  // namespace gated
@@ -255,19 +258,23 @@ cudaError_t launch_gated_dz(int type, const void *dH, int64_t lddh, const void *
                             const void *Zu, int64_t ldzu, int act, int M, int N, void *dZg,
                             void *dZu, int64_t lddz, int64_t plane, float *partial, int chain,
                             cudaStream_t s) {
-    using gated::aligned16;
-    const int size = dtype_size(type), w = 16 / size;
-    const bool vec = N % w == 0 && aligned16(dH, lddh, size) && aligned16(Zg, ldzg, size) &&
-                     aligned16(Zu, ldzu, size) &&
-                     (plane != 0 || dZg == nullptr ||
-                      (aligned16(dZg, lddz, size) && aligned16(dZu, lddz, size)));
+    // the widest access that all rows allow: 16 bytes, for the 16-bit types 8 or 4, or one element
+    // (what is written lies in the workspace, whose rows are aligned)
+    using gated::aligned_to;
+    const int size = dtype_size(type);
+    auto all = [&](int w) {
+        return N % w == 0 && aligned_to(dH, lddh, size, w) && aligned_to(Zg, ldzg, size, w) &&
+               aligned_to(Zu, ldzu, size, w);
+    };
+    int w = 16 / size;
+    while (w > 1 && !all(w)) w = size == 4 ? 1 : w / 2;
     const int parts = gated_parts(type, M, N);
     const gated::DzArgs a = {dH,   Zg,   Zu,    dZg, dZu, partial, lddh,
                              ldzg, ldzu, lddz, plane, M,  N,   act,     (M + parts - 1) / parts,
                              chain};
-    if (type == SGEMM_F32) return gated::dz_types<float>(a, vec, parts, s);
-    if (type == SGEMM_BF16) return gated::dz_types<__nv_bfloat16>(a, vec, parts, s);
-    return gated::dz_types<__half>(a, vec, parts, s);
+    if (type == SGEMM_F32) return gated::dz_types<float>(a, w, parts, s);
+    if (type == SGEMM_BF16) return gated::dz_types<__nv_bfloat16>(a, w, parts, s);
+    return gated::dz_types<__half>(a, w, parts, s);
 }
 
 // One launch for up to three matrices; the words are chosen here.
