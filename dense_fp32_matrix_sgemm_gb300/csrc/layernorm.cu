@@ -350,12 +350,22 @@ __global__ void __launch_bounds__(MAXT) layer_grad_kernel(const LayerGradArgs a)
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (i * blockDim.x + threadIdx.x) * W;
+        if (c >= a.D) continue;   // (D is a multiple of W)
+        if constexpr (W % 4 == 0) {
 #pragma unroll
-        for (int j = 0; j < W; ++j)
-            if (c + j < a.D) {
+            for (int j = 0; j < W; j += 4) {
+                *reinterpret_cast<float4 *>(to + c + j) =
+                    make_float4(dw[i][j], dw[i][j + 1], dw[i][j + 2], dw[i][j + 3]);
+                *reinterpret_cast<float4 *>(to + a.D + c + j) =
+                    make_float4(db[i][j], db[i][j + 1], db[i][j + 2], db[i][j + 3]);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < W; ++j) {
                 to[c + j] = dw[i][j];
                 to[a.D + c + j] = db[i][j];
             }
+        }
     }
 }
 
@@ -365,7 +375,7 @@ __global__ void __launch_bounds__(MAXT) layer_grad_kernel(const LayerGradArgs a)
 //     more ahead (issued by the group's first warp), and take no registers before they are used;
 //   - groups meet in barriers of their own, so that one's sums run beside another's products;
 //   - the arithmetic is in pairs (packed fp32), the weights stay in fp32.
-// (8192 x 4096 bf16 with the stream's gradient: 55 us by the kernel above, 50 here.)
+// (16384 x 4096 bf16 with the stream's gradient: 95 us by the kernel above, 89 here.)
 //   full[group, stage]: a row has landed; the group's barrier of a turn, which the sums need
 //   anyway, also says that the row before it has been read to its end: its stage is filled again.
 // Waits are bounded; one that runs out raises the library's status word, and the group goes on
@@ -664,10 +674,13 @@ struct GradShape {
     bool ring;
 };
 // Whether the ring takes rows of 16-byte pieces: of 1 KB or more (shorter rows would be many
-// small copies) up to 512 threads' 16 columns, and enough of them for four turns a CTA.
+// small copies) up to 512 threads' 16 columns, and enough of them for twenty turns a CTA, as it
+// starts and ends later (ring / the other kernel, us: 16384 x 4096 bf16 89.5 / 95.0, 8192 x 4096
+// 50.5 / 51.8, 4096 x 4096 31.4 / 30.5, 16384 x 1024 30.0 / 28.1, 5200 x 8192 66.3 / 68.0; f32 8192 x
+// 4096 88.9 / 93.3, 2600 x 8192 68.6 / 62.5).
 bool ring_takes(int type, int64_t rows, int64_t D, Shape sh) {
     return sh.tpr > 0 && sh.tpr <= 512 && D * dtype_size(type) >= 1024 &&
-           rows >= 152 * 4 * (512 / sh.tpr);
+           rows >= 152 * 20 * (512 / sh.tpr);
 }
 GradShape grad_shape(int type, int64_t rows, int64_t D, int w) {
     GradShape g = {};

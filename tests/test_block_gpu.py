@@ -566,8 +566,8 @@ def test_add_layernorm_backward_strides(pad, offset, t):
 
 # rows long and many enough for the ring: whole and ragged turns, groups that do not fill the CTA
 @pytest.mark.parametrize("t", ["f32", "bf16", "f16"])
-@pytest.mark.parametrize("rows,d", [(9801, 520), (9728, 1024), (2501, 4096), (3700, 2008), (1300, 8192),
-                                    (1999, 3000)])
+@pytest.mark.parametrize("rows,d", [(9801, 520), (2501, 4096), (1300, 8192), (48700, 520), (24321, 1024),
+                                    (6081, 4096), (12163, 2008), (3041, 8192), (6200, 3000)])
 def test_add_layernorm_backward_of_many_rows(rows, d, t):
     run_layernorm_backward(rows, d, t, True)
     run_layernorm_backward(rows, d, t, False, pad=8)
@@ -577,7 +577,7 @@ def test_add_layernorm_backward_of_many_rows(rows, d, t):
 def test_add_layernorm_backward_in_place(t):
     # dX may be dY or dS itself: through the C ABI, one and many rows
     dtype, code = TYPES[t], 0 if t == "f32" else 1
-    for rows, d in ((3, 264), (1300, 4096), (700, 9001)):
+    for rows, d in ((3, 264), (1300, 4096), (6100, 4096), (700, 9001)):
         g = gen(rows)
         dy, s, ds = (normal(g, rows, d, dtype=dtype) for _ in range(3))
         mean, rstd, w = normal(g, rows), normal(g, rows).abs() + 0.5, normal(g, d, dtype=dtype)
