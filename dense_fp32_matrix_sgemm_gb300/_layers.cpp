@@ -205,6 +205,16 @@ at::Tensor fresh(const at::Tensor &like, at::IntArrayRef size, ScalarType type) 
     return at::detail::empty_cuda(size, type, like.device(), c10::nullopt);
 }
 
+// Contiguous tensor of `size` from element `offset` of a fresh one on: outputs of a few values each
+// share one allocation (an allocation takes 0.6 us, this 0.2).
+at::Tensor part(const at::Tensor &of, int64_t offset, at::IntArrayRef size) {
+    at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(of.storage()), of.key_set(),
+                                                            of.dtype());
+    t.unsafeGetTensorImpl()->set_storage_offset(offset);
+    t.unsafeGetTensorImpl()->set_sizes_contiguous(size);
+    return t;
+}
+
 // Scratch memory: the caller's where it is large enough, else torch's.
 struct Scratch {
     at::Tensor own;
@@ -544,8 +554,9 @@ PyObject *gated_linear_backward(PyObject *, PyObject *const *a, Py_ssize_t n_arg
             du = like_weight();
         }
         if (flag(a[9])) {
-            bg = fresh(dh, {n}, t);
-            bu = fresh(dh, {n}, t);
+            const at::Tensor both = fresh(dh, {2 * n}, t);
+            bg = part(both, 0, {n});
+            bu = part(both, n, {n});
         }
         auto ptr = [](const at::Tensor &v) { return v.defined() ? v.data_ptr() : nullptr; };
         const int64_t ldw = std::max<int64_t>(W.trans ? k : n, 1);
@@ -585,9 +596,9 @@ PyObject *add_layernorm(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
         at::Tensor s, scale;
         if (present(a[3])) s = fresh(x, {rows, d}, t);
         at::Tensor y = fresh(x, {rows, d}, quantize ? ScalarType::Float8_e4m3fn : t);
-        at::Tensor mean = fresh(x, {rows}, ScalarType::Float);
-        at::Tensor rstd = fresh(x, {rows}, ScalarType::Float);
-        if (quantize) scale = fresh(x, {rows}, ScalarType::Float);
+        const at::Tensor few = fresh(x, {(quantize ? 3 : 2) * rows}, ScalarType::Float);
+        at::Tensor mean = part(few, 0, {rows}), rstd = part(few, rows, {rows});
+        if (quantize) scale = part(few, 2 * rows, {rows});
         check_status(f_add_layernorm(type, rows, d, X.p, X.ld, R.p, R.ld, w, b, (float)eps,
                                      s.defined() ? s.data_ptr() : nullptr, ld, y.data_ptr(), ld,
                                      quantize ? (float *)scale.data_ptr() : nullptr,
@@ -625,8 +636,13 @@ PyObject *add_layernorm_backward(PyObject *, PyObject *const *a, Py_ssize_t n_ar
         void *w = vector(a[4], "weight", dy, t, d);
         const bool need_w = flag(a[6]), need_b = flag(a[7]);
         at::Tensor dx = fresh(dy, {rows, d}, t), dw, db;
-        if (need_w) dw = fresh(dy, {d}, t);
-        if (need_b) db = fresh(dy, {d}, t);
+        if (need_w && need_b) {
+            const at::Tensor both = fresh(dy, {2 * d}, t);
+            dw = part(both, 0, {d});
+            db = part(both, d, {d});
+        } else if (need_w || need_b) {
+            (need_w ? dw : db) = fresh(dy, {d}, t);
+        }
         const Scratch s(a[8], need_w || need_b ? f_add_layernorm_backward_ws(type, rows, d) : 0, dy);
         check_status(f_add_layernorm_backward(
             type, rows, d, G.p, G.ld, S.p, S.ld, (const float *)mean, (const float *)rstd, w, D.p,

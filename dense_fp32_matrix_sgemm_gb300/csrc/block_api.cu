@@ -290,28 +290,34 @@ int check_norm(int dtype, int64_t rows, int64_t D) {
     return check_sizes(rows, D, 0, "rows, D");
 }
 
-// Whether a result overlaps a tensor other than its own or another result.
+// Whether a result overlaps a tensor other than its own or another result.  Both lists'
+// ranges in order of their addresses (as tensors of one buffer come), then one walk over both.
 bool results_overlap(int64_t count, const int *dtypes, const int64_t *sizes, const void *const *X,
                      void *const *Y) {
     struct Range {
         uintptr_t begin, end;
-        bool result;
     };
-    std::vector<Range> r;
-    r.reserve(2 * (size_t)count);
+    std::vector<Range> in, out;   // in: tensors that are not scaled in place
+    in.reserve((size_t)count);
+    out.reserve((size_t)count);
     for (int64_t i = 0; i < count; ++i) {
         if (sizes[i] == 0) continue;
         const uintptr_t bytes = (uintptr_t)sizes[i] * dtype_size(dtypes[i]);
         const uintptr_t x = reinterpret_cast<uintptr_t>(X[i]), y = reinterpret_cast<uintptr_t>(Y[i]);
-        if (x != y) r.push_back({x, x + bytes, false});
-        r.push_back({y, y + bytes, true});
+        if (x != y) in.push_back({x, x + bytes});
+        out.push_back({y, y + bytes});
     }
-    std::sort(r.begin(), r.end(), [](const Range &a, const Range &b) { return a.begin < b.begin; });
+    const auto before = [](const Range &a, const Range &b) { return a.begin < b.begin; };
+    for (std::vector<Range> *r : {&in, &out})
+        if (!std::is_sorted(r->begin(), r->end(), before)) std::sort(r->begin(), r->end(), before);
     uintptr_t results = 0, all = 0;   // where those so far end
-    for (const Range &a : r) {
-        if (a.begin < (a.result ? all : results)) return true;
+    auto i = in.begin();
+    for (auto o = out.begin(); o != out.end() || i != in.end();) {
+        const bool result = i == in.end() || (o != out.end() && o->begin < i->begin);
+        const Range a = result ? *o++ : *i++;
+        if (a.begin < (result ? all : results)) return true;
         all = std::max(all, a.end);
-        if (a.result) results = std::max(results, a.end);
+        if (result) results = std::max(results, a.end);
     }
     return false;
 }

@@ -188,6 +188,8 @@ def add_layernorm_backward(dy, s, mean, rstd, weight, ds=None, *, need_dweight=T
 
 def _listed(tensors):
     """A list of tensors from one tensor or any iterable of them."""
+    if isinstance(tensors, (list, tuple)):
+        return tensors
     if isinstance(tensors, torch.Tensor):
         return [tensors]
     try:
