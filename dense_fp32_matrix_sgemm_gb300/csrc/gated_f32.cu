@@ -98,7 +98,7 @@ constexpr Costs<1> kSingle = {{{1, 128}}, {1.05}, {6.0}, {3.0}};
 
 // Pairs' tiles of 256 rows and `out` outputs, a multiple of 16 up to 128 (weights stored K x N: 64
 // or 128), at costs between kCosts' widths.  The width is what makes whole rounds of the SMs:
-// 1000 x 1369 x 1001 takes 44 tiles of 128 outputs on 76 pairs, 76 of 72 (42 us, 32 so).
+// 1000 x 1369 x 1001 takes 44 tiles of 128 outputs on 76 pairs, 72 of 80 (42 us, 32 so).
 struct Pairs {
     int out = 128;
     Plan plan;
