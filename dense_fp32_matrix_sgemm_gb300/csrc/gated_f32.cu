@@ -120,11 +120,8 @@ Pairs plan_pairs(int M, int N, int kblocks, const Capacity &cap, bool any_out) {
 
 }  // namespace f32
 
-bool f32_three_side_by_side(const ProductSize &sum, const ProductSize &product,
-                            const Capacity &cap) {
-    const int bk = f32::kBk;
-    return three_side_by_side({sum.M, sum.N, 2 * ((sum.K + bk - 1) / bk * bk)}, product, bk, cap,
-                              f32::kCosts);
+bool f32_alike_side_by_side(const ProductSize &p, const Capacity &cap) {
+    return alike_side_by_side(p, f32::kBk, cap, f32::kCosts, f32::kCosts);
 }
 
 }  // namespace ltc
@@ -164,7 +161,6 @@ cudaError_t launch_sum_f32(const F32Planes (&A)[2], const F32Planes (&B)[2], int
     Capacity cap;
     cudaError_t e = capacity(cap);
     if (e != cudaSuccess) return e;
-    if (chain & kChainHalf) cap = cap.half();
     const Plan plan = plan_tiles(epi.M, epi.N, 2 * ((K + f32::kBk - 1) / f32::kBk), cap, f32::kCosts);
     return run_plan(f32::kCosts, plan, chain, [&](auto w, auto split, const Piece &p, int at) {
         constexpr TileShape t = f32::kCosts.shape[w()];

@@ -113,6 +113,10 @@ cudaError_t launch_sum(int type, const TcOperand (&A)[2], const TcOperand (&B)[2
 // Costs as linear_tc.cu's.
 constexpr Costs<3> kSumCosts = {{{2, 256}, {2, 128}, {1, 64}}, {0.27, 0.165, 0.15},
                                 {6.5, 5.5, 4.5}, {5.0, 3.0, 1.5}};
+// The same beside another product: the 128-wide tiles of both share L2's way to the SMs
+// (gradients of 4096 x 2816 x 1024, which took them at 0.165, 97 us; in turn 82).
+constexpr Costs<3> kHalfCosts = {{{2, 256}, {2, 128}, {1, 64}}, {0.27, 0.2, 0.15}, {6.5, 5.5, 4.5},
+                                 {5.0, 3.0, 1.5}};
 
 // Pairs' tiles of 256 rows and `out` outputs (a multiple of 16 up to 128; weights stored K x N:
 // 64 or 128): kSumCosts between its widths, and the weights' way from HBM as in plan_single
@@ -219,7 +223,8 @@ cudaError_t sum_dispatch(int type, const TcOperand (&A)[2], const TcOperand (&B)
     if (e != cudaSuccess) return e;
     if (chain & kChainHalf) cap = cap.half();
     const int bk = kRowBytes / dtype_size(type);
-    const Plan plan = plan_tiles(epi.M, epi.N, count * ((K + bk - 1) / bk), cap, kSumCosts);
+    const Plan plan = plan_tiles(epi.M, epi.N, count * ((K + bk - 1) / bk), cap,
+                                 chain & kChainHalf ? kHalfCosts : kSumCosts);
     return run_plan(kSumCosts, plan, chain, [&](auto w, auto split, const Piece &p, int at) {
         constexpr TileShape t = kSumCosts.shape[w()];
         return launch_sum<t.ctas, t.bn, O, split()>(type, A, B, count, K, epi, p, at, s);
@@ -228,14 +233,12 @@ cudaError_t sum_dispatch(int type, const TcOperand (&A)[2], const TcOperand (&B)
 
 }  // namespace ltc
 
-bool gated_side_by_side(int in_type, const ProductSize &sum, const ProductSize &product) {
+bool gated_side_by_side(int in_type, const ProductSize &product) {
     using namespace ltc;
     Capacity cap;
     if (capacity(cap) != cudaSuccess) return false;
-    if (in_type == SGEMM_F32) return f32_three_side_by_side(sum, product, cap);
-    const int bk = kRowBytes / dtype_size(in_type);
-    return three_side_by_side({sum.M, sum.N, 2 * ((sum.K + bk - 1) / bk * bk)}, product, bk, cap,
-                              kSumCosts);
+    if (in_type == SGEMM_F32) return f32_alike_side_by_side(product, cap);
+    return alike_side_by_side(product, kRowBytes / dtype_size(in_type), cap, kSumCosts, kHalfCosts);
 }
 
 cudaError_t launch_gated_tc(int in_type, const TcOperand &X, const TcOperand &Wg,

@@ -80,9 +80,9 @@ cudaError_t launch_gated_rows(int in_type, const void *X, int64_t ldx, const voi
                               const void *Wu, int64_t ldwu, int K, const GatedEpi &epi,
                               cudaStream_t s);
 
-// Whether the gated layer's gradients are better planned for half of the SMs each: the
-// sum of two products (K: of each) and two products alike.
-bool gated_side_by_side(int in_type, const ProductSize &sum, const ProductSize &product);
+// Whether the gated layer's two weight gradients, each of this size, are better planned for
+// half of the SMs each.
+bool gated_side_by_side(int in_type, const ProductSize &product);
 
 // Whether two products of a chain are better run side by side than in turn.
 bool linear_tc_side_by_side(int in_type, const ProductSize &a, const ProductSize &b);

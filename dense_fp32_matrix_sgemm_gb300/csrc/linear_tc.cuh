@@ -594,25 +594,30 @@ bool side_by_side(const ProductSize &a, const ProductSize &b, int k_stage, const
     return (ha > hb ? ha : hb) < us(a, cap) + us(b, cap) - 4.0;
 }
 
-// Three products of a chain, the second and the third alike: planned for half of the SMs
-// each, two run at a time, and the time is that of the longest or half of them all.  For
-// products that leave SMs idle: those that fill them lose what they share in L2 (gradients of
-// 4096 x 8192 x 4096 bf16 660 us in turn, 830 so; of 500 x 777 x 1001 f32 45.7 and 42.6).
+// Whether two products alike of a chain are better planned for half of the SMs each.  In turn, whole
+// tiles of the second fill the SMs that the first one's last round leaves; planned with K split
+// there is 4 us of overlap.  (bf16 gradients of 2048^3 63.4 us in turn, 58.1 so; f32 of 1024^3 67.2
+// and 55.1.  Below 8 us there is nothing to gain.)  A plan of two launches takes the other one's
+// SMs for its second (gradients of 4096 x 2816 x 1024 bf16 82.2 us in turn, 102.8 so).
 template <int SHAPES>
-bool three_side_by_side(const ProductSize &a, const ProductSize &b, int k_stage,
-                        const Capacity &cap, const Costs<SHAPES> &cost) {
-    auto us = [&](const ProductSize &p, const Capacity &c) {
-        return plan_tiles(p.M, p.N, (p.K + k_stage - 1) / k_stage, c, cost).us;
-    };
+bool alike_side_by_side(const ProductSize &p, int k_stage, const Capacity &cap,
+                        const Costs<SHAPES> &cost, const Costs<SHAPES> &half_cost) {
     const Capacity half = cap.half();
     if (half.clusters[0] < 1) return false;
-    const double ha = us(a, half), hb = us(b, half), in_turn = us(a, cap) + 2 * us(b, cap) - 8.0;
-    const double all = ha + 2 * hb > 2 * ha ? (ha + 2 * hb) / 2 : ha;
-    return (all > hb ? all : hb) < 0.9 * in_turn;
+    const int kblocks = (p.K + k_stage - 1) / k_stage;
+    const Plan full = plan_tiles(p.M, p.N, kblocks, cap, cost);
+    double in_turn = 2 * full.us - 4.0;
+    if (full.pieces == 1 && full.piece[0].parts == 1) {
+        const long long tiles = 2LL * full.piece[0].tiles, room = cap.of(cost.shape[full.shape].ctas);
+        const double both = (double)((tiles + room - 1) / room) * kblocks * cost.stage[full.shape] +
+                            cost.fixed[full.shape];
+        if (both < in_turn) in_turn = both;
+    }
+    const Plan halved = plan_tiles(p.M, p.N, kblocks, half, half_cost);
+    return in_turn > 8.0 && halved.pieces == 1 && halved.us <= 1.01 * in_turn;
 }
 
-bool f32_three_side_by_side(const ProductSize &sum, const ProductSize &product,
-                            const Capacity &cap);   // gated_f32.cu
+bool f32_alike_side_by_side(const ProductSize &p, const Capacity &cap);   // gated_f32.cu
 
 // f(w as a constant).
 template <int W, int SHAPES, class F>
