@@ -54,6 +54,46 @@ __device__ __forceinline__ float2 group_sum2(float a, float b, float2 *red) {
     return make_float2(a, b);
 }
 
+// Rows that start off a 16-byte boundary, all of a call's by as much in a row (an odd number of
+// elements a row): `head` elements lead to the first boundary, `accesses` whole accesses follow,
+// and the row's two ends (fewer than 32 elements) go one element a thread.  The last access
+// that fits is left to the ends, as a vector's two accesses that hold its columns (load_moved)
+// might pass the vector's end.
+struct Shifted {
+    int head, accesses;
+    // the thread's element of the ends; D or more: none
+    __device__ __forceinline__ int end(int W) const {
+        const int x = threadIdx.x;
+        return x < head ? x : accesses * W + x;
+    }
+};
+template <class T, int W>
+__device__ __forceinline__ Shifted shifted(const void *row, int D) {
+    const int past = (int)(reinterpret_cast<uintptr_t>(row) / sizeof(T) % W);
+    if (past == 0) return {0, D / W};
+    return {W - past, max(D / W - 1, 0)};
+}
+
+// Columns head + k W .. of a vector on a boundary, from its accesses k and k + 1.
+template <class T, int W>
+__device__ __forceinline__ Raw<T, W> load_moved(const T *p, int k, int head, bool in) {
+    const Raw<T, W> lo = load_or_zero<T, W>(p + k * W, in);
+    if (head == 0) return lo;   // (the same for a warp)
+    const Raw<T, W> hi = load_or_zero<T, W>(p + (k + 1) * W, in);
+    const uint32_t v[8] = {lo.u.x, lo.u.y, lo.u.z, lo.u.w, hi.u.x, hi.u.y, hi.u.z, hi.u.w};
+    constexpr int WORD = 4 / (int)sizeof(T);   // elements
+    const int words = head / WORD, bits = 16 * (head % WORD);
+    uint32_t a[6], b[5];
+#pragma unroll
+    for (int i = 0; i < 6; ++i) a[i] = words & 2 ? v[i + 2] : v[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) b[i] = words & 1 ? a[i + 1] : a[i];
+    Raw<T, W> r;
+    r.u = make_uint4(__funnelshift_r(b[0], b[1], bits), __funnelshift_r(b[1], b[2], bits),
+                     __funnelshift_r(b[2], b[3], bits), __funnelshift_r(b[3], b[4], bits));
+    return r;
+}
+
 struct LayerRowArgs {
     const void *X, *R, *w, *b;
     void *S, *Y;
@@ -63,8 +103,9 @@ struct LayerRowArgs {
     int D;
 };
 
-// QUANT: 8-bit output.
-template <class T, int W, int NV, int MAXT, bool QUANT>
+// QUANT: 8-bit output.  SHIFT: rows off the boundary (in 64 registers, MAXT 1024: moving the weights
+// takes 93, which leaves an SM too few warps: 1280 x 6427 bf16 18.8 -> 14.7 us).
+template <class T, int W, int NV, int MAXT, bool QUANT, bool SHIFT>
 __global__ void __launch_bounds__(MAXT) layer_row_kernel(const LayerRowArgs a) {
     __shared__ float2 red[3][32];
     pdl_trigger();
@@ -75,19 +116,29 @@ __global__ void __launch_bounds__(MAXT) layer_row_kernel(const LayerRowArgs a) {
     const T *r = static_cast<const T *>(a.R) + row * a.ldr;
     const T *w = static_cast<const T *>(a.w);
     const T *b = static_cast<const T *>(a.b);
+    const Shifted at = SHIFT ? shifted<T, W>(x, a.D)  : Shifted{0, 0};
+    const int end = SHIFT ? at.end(W) : a.D, limit = SHIFT ? at.head + at.accesses * W : a.D;
+    const bool ends = end < a.D;
+    auto column = [&](int i) {
+        const int c = (i * blockDim.x + threadIdx.x) * W;
+        return SHIFT ? c + at.head : c;
+    };
+    auto in = [&](int i) { return column(i) < limit; };
     Raw<T, W> vx[NV], vr[NV];
+    Raw<T, 1> ex, er;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = (i * blockDim.x + threadIdx.x) * W;
-        const bool in = live && c < a.D;
-        vx[i] = load_or_zero<T, W>(x + c, in);
-        if (a.R != nullptr) vr[i] = load_or_zero<T, W>(r + c, in);
+        vx[i] = load_or_zero<T, W>(x + column(i), live && in(i));
+        if (a.R != nullptr) vr[i] = load_or_zero<T, W>(r + column(i), live && in(i));
     }
-    float s[NV][W];
+    if constexpr (SHIFT) {
+        ex = load_or_zero<T, 1>(x + end, live && ends);
+        er = load_or_zero<T, 1>(r + end, live && ends && a.R != nullptr);
+    }
+    float s[NV][W], e[1] = {0.f};
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = (i * blockDim.x + threadIdx.x) * W;
         vx[i].get(s[i]);
         if (a.R != nullptr) {
             float r[W];
@@ -95,24 +146,30 @@ __global__ void __launch_bounds__(MAXT) layer_row_kernel(const LayerRowArgs a) {
 #pragma unroll
             for (int j = 0; j < W; ++j) s[i][j] += r[j];
         }
-        if (a.S != nullptr && live && c < a.D)
-            put<T, W>(static_cast<T *>(a.S) + row * a.lds + c, s[i]);
+        if (a.S != nullptr && live && in(i))
+            put<T, W>(static_cast<T *>(a.S) + row * a.lds + column(i), s[i]);
 #pragma unroll
         for (int j = 0; j < W; ++j) sum += s[i][j];
+    }
+    if constexpr (SHIFT) {
+        e[0] = to_f32(ex.u) + to_f32(er.u);
+        if (a.S != nullptr && live && ends)
+            put<T, 1>(static_cast<T *>(a.S) + row * a.lds + end, e);
+        sum += e[0];
     }
     const float width = (float)max(a.D, 1);   // (no elements: a mean and a variance of 0)
     const float first = group_sum2(sum, 0.f, red[0]).x / width;
     float off = 0.f, square = 0.f;
+    auto differ = [&](float &s, bool in) {
+        s = in ? s - first : 0.f;
+        off += s;
+        square = fmaf(s, s, square);
+    };
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = (i * blockDim.x + threadIdx.x) * W;
+    for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int j = 0; j < W; ++j) {
-            s[i][j] = c < a.D ? s[i][j] - first : 0.f;
-            off += s[i][j];
-            square = fmaf(s[i][j], s[i][j], square);
-        }
-    }
+        for (int j = 0; j < W; ++j) differ(s[i][j], in(i));
+    if constexpr (SHIFT) differ(e[0], ends);
     const float2 t = group_sum2(off, square, red[1]);
     const float shift = t.x / width;
     const float rstd = 1.f / sqrtf(max_nan(t.y / width - shift * shift, 0.f) + a.eps);
@@ -123,17 +180,26 @@ __global__ void __launch_bounds__(MAXT) layer_row_kernel(const LayerRowArgs a) {
     float top = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = (i * blockDim.x + threadIdx.x) * W;
-        const bool in = c < a.D;
         float fw[W], fb[W];
-        load_or_zero<T, W>(w + c, in).get(fw);
-        load_or_zero<T, W>(b + c, in && b != nullptr).get(fb);
+        if constexpr (SHIFT) {
+            load_moved<T, W>(w, (int)(i * blockDim.x + threadIdx.x), at.head, in(i)).get(fw);
+            load_moved<T, W>(b, (int)(i * blockDim.x + threadIdx.x), at.head, in(i) && b != nullptr).get(fb);
+        } else {
+            load_or_zero<T, W>(w + column(i), in(i)).get(fw);
+            load_or_zero<T, W>(b + column(i), in(i) && b != nullptr).get(fb);
+        }
 #pragma unroll
         for (int j = 0; j < W; ++j) {
             s[i][j] = fmaf((s[i][j] - shift) * rstd, fw[j], fb[j]);
-            if (QUANT && in) top = max_nan(top, fabsf(s[i][j]));
+            if (QUANT && in(i)) top = max_nan(top, fabsf(s[i][j]));
         }
-        if (!QUANT && live && in) put<T, W>(static_cast<T *>(a.Y) + row * a.ldy + c, s[i]);
+        if (!QUANT && live && in(i))
+            put<T, W>(static_cast<T *>(a.Y) + row * a.ldy + column(i), s[i]);
+    }
+    if (SHIFT && ends) {
+        e[0] = fmaf((e[0] - shift) * rstd, to_f32(w[end]), b != nullptr ? to_f32(b[end]) : 0.f);
+        top = max_nan(top, fabsf(e[0]));
+        if (!QUANT && live) put<T, 1>(static_cast<T *>(a.Y) + row * a.ldy + end, e);
     }
     if constexpr (QUANT) {
         const float amax = max_nan(group_reduce(0.f, top, red[2]).y, kAmaxFloor);
@@ -142,12 +208,12 @@ __global__ void __launch_bounds__(MAXT) layer_row_kernel(const LayerRowArgs a) {
         uint8_t *q = static_cast<uint8_t *>(a.Y) + row * a.ldy;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (i * blockDim.x + threadIdx.x) * W;
-            if (!live || c >= a.D) continue;
+            if (!live || !in(i)) continue;
 #pragma unroll
             for (int j = 0; j < W; ++j) s[i][j] *= inv;
-            store_codes<W>(q + c, s[i]);
+            store_codes<W>(q + column(i), s[i]);
         }
+        if (SHIFT && live && ends) q[end] = to_e4m3(e[0] * inv);
     }
 }
 
@@ -369,10 +435,139 @@ __global__ void __launch_bounds__(MAXT) layer_grad_kernel(const LayerGradArgs a)
     }
 }
 
+// The same for rows off the boundary, two accesses a thread.  All of a group's rows are so by as
+// much (a multiple of eight groups lies between two), so that a thread's columns stay; the groups
+// of a CTA hold different ones, and their sums are added by columns.
+template <class T>
+__global__ void __launch_bounds__(512) layer_grad_shift_kernel(const LayerGradArgs a) {
+    constexpr int W = 16 / sizeof(T), NV = 2;
+    __shared__ float2 red[2][32];
+    pdl_trigger();
+    pdl_wait();
+    const int64_t group = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    const int64_t groups = (int64_t)gridDim.x * blockDim.y;
+    const Shifted at = shifted<T, W>(static_cast<const T *>(a.S) + group * a.lds, a.D);
+    const int end = at.end(W);
+    const bool ends = end < a.D;
+    auto access = [&](int i) { return i * (int)blockDim.x + (int)threadIdx.x; };
+    auto column = [&](int i) { return access(i) * W + at.head; };
+    auto in = [&](int i) { return access(i) < at.accesses; };
+    Raw<T, W> vw[NV];
+    float dw[NV][W], db[NV][W], end_dw = 0.f, end_db = 0.f;
+    const float end_w = ends ? to_f32(static_cast<const T *>(a.w)[end]) : 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        vw[i] = load_moved<T, W>(static_cast<const T *>(a.w), access(i), at.head, in(i));
+#pragma unroll
+        for (int j = 0; j < W; ++j) dw[i][j] = db[i][j] = 0.f;
+    }
+    const int64_t first = (int64_t)blockIdx.x * blockDim.y;
+    const int turns = first < a.rows ? (int)((a.rows - 1 - first) / groups) + 1 : 0;
+    Raw<T, W> ny[NV], ns[NV];
+    Raw<T, 1> end_ny, end_ns;
+    float nm = 0.f, nr = 0.f;
+    auto load_row = [&](int64_t row) {
+        const bool live = row < a.rows;
+        const T *dy = static_cast<const T *>(a.dY) + row * a.lddy;
+        const T *s = static_cast<const T *>(a.S) + row * a.lds;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            ny[i] = load_or_zero<T, W>(dy + column(i), live && in(i));
+            ns[i] = load_or_zero<T, W>(s + column(i), live && in(i));
+        }
+        end_ny = load_or_zero<T, 1>(dy + end, live && ends);
+        end_ns = load_or_zero<T, 1>(s + end, live && ends);
+        nm = live ? a.mean[row] : 0.f;
+        nr = live ? a.rstd[row] : 0.f;
+    };
+    if (turns > 0) load_row(group);
+    for (int t = 0; t < turns; ++t) {
+        const int64_t row = group + t * groups;
+        const bool live = row < a.rows, stream = live && a.dS != nullptr;
+        const T *more = static_cast<const T *>(a.dS) + row * a.ldds;
+        Raw<T, W> vy[NV], vs[NV], vd[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            vy[i] = ny[i];
+            vs[i] = ns[i];
+            vd[i] = load_or_zero<T, W>(more + column(i), stream && in(i));
+        }
+        const Raw<T, 1> end_d = load_or_zero<T, 1>(more + end, stream && ends);
+        const float end_y = to_f32(end_ny.u), end_s = to_f32(end_ns.u);
+        const float mean = nm, rstd = nr;
+        if (t + 1 < turns) load_row(row + groups);
+        float sg = 0.f, sgn = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float dy[W], s[W], w[W];
+            vy[i].get(dy);
+            vs[i].get(s);
+            vw[i].get(w);
+#pragma unroll
+            for (int j = 0; j < W; ++j) {
+                const float n = (s[j] - mean) * rstd, g = dy[j] * w[j];
+                sg += g;
+                sgn = fmaf(g, n, sgn);
+                dw[i][j] = fmaf(dy[j], n, dw[i][j]);
+                db[i][j] += dy[j];
+            }
+        }
+        const float end_n = (end_s - mean) * rstd, end_g = end_y * end_w;
+        if (ends) {
+            sg += end_g;
+            sgn = fmaf(end_g, end_n, sgn);
+            end_dw = fmaf(end_y, end_n, end_dw);
+            end_db += end_y;
+        }
+        const float2 k = group_sum2(sg, sgn, red[t & 1]);   // (as above)
+        const float kg = k.x / (float)a.D, kn = k.y / (float)a.D;
+        if (!live) continue;
+        T *to = static_cast<T *>(a.dX) + row * a.lddx;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (!in(i)) continue;
+            float dy[W], s[W], w[W], ds[W], dx[W];
+            vy[i].get(dy);
+            vs[i].get(s);
+            vw[i].get(w);
+            vd[i].get(ds);
+#pragma unroll
+            for (int j = 0; j < W; ++j) {
+                const float n = (s[j] - mean) * rstd;
+                dx[j] = fmaf(rstd, fmaf(-n, kn, fmaf(dy[j], w[j], -kg)), ds[j]);
+            }
+            put<T, W>(to + column(i), dx);
+        }
+        if (ends)
+            to[end] = from_f32<T>(fmaf(rstd, fmaf(-end_n, kn, end_g - kg), to_f32(end_d.u)));
+    }
+    if (a.partial == nullptr) return;
+    __shared__ float sums[512 * NV * W];   // D a group
+    float *mine = sums + threadIdx.y * a.D;
+    auto join = [&](const float (&d)[NV][W], float end_d, float *to) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < W; ++j)
+                if (in(i)) mine[column(i) + j] = d[i][j];
+        if (ends) mine[end] = end_d;
+        __syncthreads();
+        for (int c = threadIdx.y * blockDim.x + threadIdx.x; c < a.D; c += blockDim.x * blockDim.y) {
+            float sum = sums[c];
+            for (int y = 1; y < (int)blockDim.y; ++y) sum += sums[y * a.D + c];
+            to[c] = sum;
+        }
+        __syncthreads();
+    };
+    float *to = a.partial + (int64_t)blockIdx.x * 2 * a.D;
+    join(dw, end_dw, to);
+    join(db, end_db, to + a.D);
+}
+
 // The same where rows are long and many.  What bounded it there was the turn: about twenty
 // instructions an element, in two phases that all of an SM's warps took together.  So here
-//   - a group's rows come by bulk copies into a ring of its own in shared memory, three rows or
-//     more ahead (issued by the group's first warp), and take no registers before they are used;
+//   - a group's rows come by bulk copies into a ring of its own in shared memory, up to three rows
+//     ahead (issued by the group's first warp), and take no registers before they are used;
 //   - groups meet in barriers of their own, so that one's sums run beside another's products;
 //   - the arithmetic is in pairs (packed fp32), the weights stay in fp32.
 // (16384 x 4096 bf16 with the stream's gradient: 95 us by the kernel above, 89 here.)
@@ -609,12 +804,13 @@ __global__ void __launch_bounds__(kMaxThreads) layer_grad_wide_kernel(const Laye
 
 // ------------------------------------------------------------------ host side
 
-template <class T, int W, int NV, bool QUANT>
+template <class T, int W, int NV, bool QUANT, bool SHIFT = false>
 cudaError_t launch_row(const LayerRowArgs &a, Shape sh, cudaStream_t s) {
     const dim3 grid((unsigned)((a.rows + sh.groups - 1) / sh.groups));
     const dim3 block((unsigned)sh.tpr, (unsigned)sh.groups);
-    if (sh.tpr <= 512) return launch(layer_row_kernel<T, W, NV, 512, QUANT>, grid, block, a, s);
-    return launch(layer_row_kernel<T, W, NV, kMaxThreads, QUANT>, grid, block, a, s);
+    if (sh.tpr <= 512 && !SHIFT)
+        return launch(layer_row_kernel<T, W, NV, SHIFT ? kMaxThreads : 512, QUANT, SHIFT>, grid, block, a, s);
+    return launch(layer_row_kernel<T, W, NV, kMaxThreads, QUANT, SHIFT>, grid, block, a, s);
 }
 
 // Widest access of a call's rows, in elements: 16 bytes down to one element, by halves.
@@ -631,9 +827,9 @@ template <class T, int W, bool QUANT>
 cudaError_t row_accesses(const LayerRowArgs &a, cudaStream_t s) {
     constexpr bool WHOLE = W * sizeof(T) == 16;
     const int64_t n = a.D / W;
-    // few rows: as many threads as possible on each, for its latency
+    // few rows: as many threads as possible on each, for its latency (1 x 1001 bf16 4.3 -> 3.1 us)
     Shape sh = shape_for(n, 1);
-    if (WHOLE && sh.tpr > 0 && a.rows <= 304) return launch_row<T, W, 1, QUANT>(a, sh, s);
+    if (sh.tpr > 0 && a.rows <= 304) return launch_row<T, W, 1, QUANT>(a, sh, s);
     constexpr int NV = WHOLE ? 4 : W * sizeof(T) == 8 ? 4 : 8;
     sh = shape_for(n, NV);
     if (sh.tpr > 0 && (WHOLE || sh.tpr <= 512)) return launch_row<T, W, NV, QUANT>(a, sh, s);
@@ -644,6 +840,12 @@ cudaError_t row_accesses(const LayerRowArgs &a, cudaStream_t s) {
     return launch(layer_row_wide_kernel<T, QUANT>, dim3((unsigned)a.rows), dim3(kMaxThreads), a, s);
 }
 
+// Elements that p lies past a boundary of 16 bytes' worth of the rows' elements (8-bit outputs: of
+// as many bytes).
+int past(const void *p, int size, int whole) {
+    return (int)(reinterpret_cast<uintptr_t>(p) / size % whole);
+}
+
 template <class T, bool QUANT>
 cudaError_t row_dispatch(const LayerRowArgs &a, cudaStream_t s) {
     constexpr int size = sizeof(T);
@@ -652,10 +854,29 @@ cudaError_t row_dispatch(const LayerRowArgs &a, cudaStream_t s) {
                aligned_to(a.w, 0, size, w) && aligned_to(a.b, 0, size, w) &&
                aligned_to(a.S, a.lds, size, w) && aligned_to(a.Y, a.ldy, QUANT ? 1 : size, w);
     });
+    constexpr int W = 16 / size;
+    if (w == W) return row_accesses<T, W, QUANT>(a, s);
+    if (w == W / 2) return row_accesses<T, W / 2, QUANT>(a, s);
+    // Rows that take narrower accesses yet lie alike: from a boundary of its own for each row
+    // (1280 x 6427 bf16 40.6 -> 14.7 us, f32 49.5 -> 26.4; 6428 in 8-byte accesses 13.8, else
+    // 17.7), but few and short ones by one narrow access a thread (16 x 777 3.0, else 3.4), and
+    // rows of less than 1 KB, whose ends would weigh too much (20000 x 77 13.8, else 22.1).
+    const bool narrow = (a.rows <= 304 && a.D / w <= kMaxThreads) || a.D * size < 1024;
+    const int m = past(a.X, size, W);
+    auto alike = [&](const void *p, int64_t ld, int size) {
+        return p == nullptr || (past(p, size, W) == m && (ld - a.ldx) % W == 0);
+    };
+    if (!narrow && alike(a.R, a.ldr, size) && alike(a.S, a.lds, size) &&
+        alike(a.Y, a.ldy, QUANT ? 1 : size) && aligned_to(a.w, 0, size, W) &&
+        aligned_to(a.b, 0, size, W)) {
+        Shape sh = shape_for(a.D / W, 1);
+        if (sh.tpr > 0 && a.rows <= 304) return launch_row<T, W, 1, QUANT, true>(a, sh, s);
+        sh = shape_for(a.D / W, 4);
+        if (sh.tpr > 0) return launch_row<T, W, 4, QUANT, true>(a, sh, s);
+    }
     if constexpr (size == 2)
-        if (w == 8) return row_accesses<T, 8, QUANT>(a, s);
-    if (w == 4) return row_accesses<T, 4, QUANT>(a, s);
-    return w == 2 ? row_accesses<T, 2, QUANT>(a, s) : row_accesses<T, 1, QUANT>(a, s);
+        if (w == 2) return row_accesses<T, 2, QUANT>(a, s);
+    return row_accesses<T, 1, QUANT>(a, s);
 }
 
 template <bool QUANT>
@@ -671,7 +892,7 @@ struct GradShape {
     int w, nv;      // elements an access, accesses a thread; nv 0: the wide kernel
     Shape sh;
     int ctas;
-    bool ring;
+    bool ring, shift;
 };
 // Whether the ring takes rows of 16-byte pieces: of 1 KB or more (shorter rows would be many
 // small copies) up to 512 threads' 16 columns, and enough of them for twenty turns a CTA, as it
@@ -682,10 +903,11 @@ bool ring_takes(int type, int64_t rows, int64_t D, Shape sh) {
     return sh.tpr > 0 && sh.tpr <= 512 && D * dtype_size(type) >= 1024 &&
            rows >= 152 * 20 * (512 / sh.tpr);
 }
-GradShape grad_shape(int type, int64_t rows, int64_t D, int w) {
+GradShape grad_shape(int type, int64_t rows, int64_t D, int w, bool shift) {
     GradShape g = {};
     const bool whole = w * dtype_size(type) == 16;
-    if (whole) {
+    g.shift = shift;
+    if (whole && !shift) {
         g.sh = shape_for(D / w, 16 / w);
         if (ring_takes(type, rows, D, g.sh)) {
             g.sh.groups = 512 / g.sh.tpr;
@@ -746,6 +968,7 @@ cudaError_t grad_dispatch(const LayerGradArgs &a, const GradShape &g, cudaStream
     constexpr int W = 16 / sizeof(T);
     if (g.ring) return launch_ring<T>(a, g, s);
     const dim3 grid((unsigned)g.ctas), block((unsigned)g.sh.tpr, (unsigned)g.sh.groups);
+    if (g.shift) return launch(layer_grad_shift_kernel<T>, grid, block, a, s);
     if (g.nv == 0) return launch(layer_grad_wide_kernel<T>, grid, block, a, s);
     auto run = [&](auto w, auto nv) {
         return g.sh.tpr <= 512
@@ -778,10 +1001,11 @@ cudaError_t launch_add_layernorm(int type, int64_t rows, int64_t D, const void *
 int layernorm_backward_parts(int type, int64_t rows, int64_t D) {
     int most = 0;
     for (int w = 16 / dtype_size(type); w >= 1; w /= 2) {
-        const int ctas = norm::grad_shape(type, rows, D, w).ctas;
+        const int ctas = norm::grad_shape(type, rows, D, w, false).ctas;
         most = ctas > most ? ctas : most;
     }
-    return most;
+    const int shifted = norm::grad_shape(type, rows, D, 16 / dtype_size(type), true).ctas;
+    return shifted > most ? shifted : most;
 }
 
 cudaError_t launch_add_layernorm_backward(int type, int64_t rows, int64_t D, const void *dY,
@@ -796,7 +1020,19 @@ cudaError_t launch_add_layernorm_backward(int type, int64_t rows, int64_t D, con
                aligned_to(w, 0, size, n) && aligned_to(dS, ldds, size, n) &&
                aligned_to(dX, lddx, size, n);
     });
-    const norm::GradShape g = norm::grad_shape(type, rows, D, width);
+    const int whole = 16 / size;
+    norm::GradShape g = norm::grad_shape(type, rows, D, width, false);
+    auto alike = [&](const void *p, int64_t ld) {
+        return p == nullptr || (norm::past(p, size, whole) == norm::past(S, size, whole) &&
+                                (ld - lds) % whole == 0);
+    };
+    // As in row_dispatch, but where the sums by columns at the end do not weigh more (1280 x 6427
+    // bf16 57.6 -> 24.0 us, 4096 x 1001 f32 16.6 -> 12.7, but 1000 x 1001 bf16 8.4 -> 9.5).
+    if (width < whole / 2 && rows * D >= (1 << 21) && D * size >= 1024 && alike(dY, lddy) &&
+        alike(dS, ldds) && alike(dX, lddx) && norm::aligned_to(w, 0, size, whole)) {
+        const norm::GradShape from_boundary = norm::grad_shape(type, rows, D, whole, true);
+        if (from_boundary.nv > 0 && from_boundary.sh.tpr <= 512) g = from_boundary;
+    }
     const bool sums = dw != nullptr || db != nullptr;
     const norm::LayerGradArgs a = {dY,   S,    w,    dS,   dX,   mean, rstd, sums ? partial : nullptr,
                                    lddy, lds, ldds, lddx, rows, (int)D};

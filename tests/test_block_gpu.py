@@ -392,15 +392,16 @@ NORM_SIZES = [(1, 1), (1, 4096), (3, 7), (5, 64), (9, 200), (33, 256), (40, 1001
               (2, 8192), (310, 8192), (2, 16384), (311, 16000), (2, 40000), (3, 9001), (5000, 72)]
 
 
-def run_layernorm(rows, d, t, residual=True, bias=True, quantize=False, pad=0, offset=0, mean=0.0):
+def run_layernorm(rows, d, t, residual=True, bias=True, quantize=False, pad=0, offset=0, mean=0.0,
+                  call=sg.add_layernorm):
     dtype = TYPES[t]
     g = gen(rows + 31 * d)
     x, r = normal(g, rows, d), normal(g, rows, d, dtype=dtype)
     x = (x + mean).to(dtype)
     w = (1 + normal(g, d, std=0.2)).to(dtype)
     b = normal(g, d, std=0.3, dtype=dtype) if bias else None
-    got = sg.add_layernorm(strided(x, pad, offset), w, b, strided(r, pad, offset) if residual else None,
-                           eps=1e-5, quantize=quantize)
+    got = call(strided(x, pad, offset), w, b, strided(r, pad, offset) if residual else None, eps=1e-5,
+               quantize=quantize)
     torch.cuda.synchronize()
     s = x.double() + (r.double() if residual else 0)
     m = s.mean(1, keepdim=True)
@@ -523,15 +524,15 @@ def test_add_layernorm_empty():
     assert y.shape == (0, 8)
 
 
-def run_layernorm_backward(rows, d, t, stream=True, pad=0, offset=0):
+def run_layernorm_backward(rows, d, t, stream=True, pad=0, offset=0, call=sg.add_layernorm_backward):
     dtype = TYPES[t]
     g = gen(rows + 37 * d)
     s, dy, ds = (normal(g, rows, d, dtype=dtype) for _ in range(3))
     w = (1 + normal(g, d, std=0.2)).to(dtype)
     mean = s.double().mean(1).float()
     rstd = torch.rsqrt((s.double() - mean.double()[:, None]).square().mean(1) + 1e-5).float()
-    dx, dw, db = sg.add_layernorm_backward(strided(dy, pad, offset), strided(s, pad, offset), mean,
-                                           rstd, w, strided(ds, pad, offset) if stream else None)
+    dx, dw, db = call(strided(dy, pad, offset), strided(s, pad, offset), mean, rstd, w,
+                      strided(ds, pad, offset) if stream else None)
     torch.cuda.synchronize()
     R = rstd.double()[:, None]
     n, DY = (s.double() - mean.double()[:, None]) * R, dy.double()
@@ -577,7 +578,7 @@ def test_add_layernorm_backward_of_many_rows(rows, d, t):
 def test_add_layernorm_backward_in_place(t):
     # dX may be dY or dS itself: through the C ABI, one and many rows
     dtype, code = TYPES[t], 0 if t == "f32" else 1
-    for rows, d in ((3, 264), (1300, 4096), (6100, 4096), (700, 9001)):
+    for rows, d in ((3, 264), (1300, 4096), (6100, 4096), (700, 9001), (2100, 1001)):
         g = gen(rows)
         dy, s, ds = (normal(g, rows, d, dtype=dtype) for _ in range(3))
         mean, rstd, w = normal(g, rows), normal(g, rows).abs() + 0.5, normal(g, d, dtype=dtype)
@@ -607,6 +608,100 @@ def test_add_layernorm_backward_empty_and_parts():
         assert torch.equal(a[0], dx)
         assert torch.equal(a[1], dw) if w else a[1] is None
         assert torch.equal(a[2], db) if b else a[2] is None
+
+
+# Rows that start off a 16-byte boundary: in torch's layout those of an odd width, and by the C ABI
+# with every matrix as far off it.
+@pytest.mark.parametrize("t", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("rows,d", [(305, 513), (400, 519), (1000, 1001), (500, 2050), (306, 8191),
+                                    (2000, 257), (310, 32001), (20, 2049), (304, 9001), (313, 515)])
+def test_add_layernorm_rows_off_the_boundary(rows, d, t):
+    for quantize in (False, True):
+        run_layernorm(rows, d, t, True, True, quantize)
+        run_layernorm(rows, d, t, False, False, quantize)
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("rows,d", [(4100, 513), (2100, 1001), (1100, 2047), (530, 4095), (300, 8191),
+                                    (17001, 257), (1025, 2049), (4091, 517)])
+def test_add_layernorm_backward_rows_off_the_boundary(rows, d, t):
+    run_layernorm_backward(rows, d, t, True)
+    run_layernorm_backward(rows, d, t, False)
+
+
+def off_by(rows, d, ld, offset, dtype, fill=None):
+    """(rows, d) of leading dimension ld, `offset` elements past an allocation's start; what lies
+    around it is 77, which no call may write."""
+    buffer = torch.full((offset + rows * ld + 16,), 77.0, device="cuda").to(dtype)
+    at = buffer[offset:offset + rows * ld].view(rows, ld)[:, :d]
+    if fill is not None:
+        at.copy_(fill)
+    return buffer, at
+
+
+def assert_untouched(buffer, at):
+    around = buffer.clone()
+    around[at.storage_offset():at.storage_offset() + at.shape[0] * at.stride(0)].view(
+        at.shape[0], at.stride(0))[:, :at.shape[1]] = torch.full((), 77.0, device="cuda").to(at.dtype)
+    assert (around.float() == torch.full((), 77.0, device="cuda").to(at.dtype).float()).all()
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,d,ld", [(310, 1024, 1027), (320, 1003, 1003), (309, 515, 520), (340, 2061, 2065)])
+def test_add_layernorm_alike_off_the_boundary(rows, d, ld, t):
+    dtype, code = TYPES[t], 0 if t == "f32" else 1
+
+    def forward(offset, in_place):
+        def call(x, w, b, r, eps, quantize):
+            _, X = off_by(rows, d, ld, offset, dtype, x)
+            R = off_by(rows, d, ld, offset, dtype, r)[1] if r is not None else None
+            kept, S = (None, R) if in_place and r is not None else off_by(rows, d, ld, offset, dtype)
+            out = torch.float8_e4m3fn if quantize else dtype
+            buffer, Y = off_by(rows, d, ld, offset, out)
+            scale, mean, rstd = (torch.empty(rows, device="cuda") for _ in range(3))
+            sg.sgemm_add_layernorm(code, rows, d, X.data_ptr(), ld, R.data_ptr() if r is not None else 0,
+                                   ld, w.data_ptr(), b.data_ptr() if b is not None else 0, eps,
+                                   S.data_ptr(), ld, Y.data_ptr(), ld,
+                                   scale.data_ptr() if quantize else 0, mean.data_ptr(),
+                                   rstd.data_ptr(), torch.cuda.current_stream().cuda_stream)
+            assert_untouched(buffer, Y)
+            if kept is not None:
+                assert_untouched(kept, S)
+            return ((Y, scale) if quantize else (Y,)) + (S, mean, rstd)
+        return call
+
+    for offset in range(0, 9, 1 if t == "bf16" else 2):
+        for quantize in (False, True):
+            run_layernorm(rows, d, t, True, True, quantize, call=forward(offset, False))
+        run_layernorm(rows, d, t, True, False, False, call=forward(offset + 1, True))
+        run_layernorm(rows, d, t, False, False, True, call=forward(offset, False))
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,d,ld", [(2100, 1024, 1027), (1100, 2043, 2043), (4200, 515, 520)])
+def test_add_layernorm_backward_alike_off_the_boundary(rows, d, ld, t):
+    dtype, code = TYPES[t], 0 if t == "f32" else 1
+
+    def backward(offset, in_place):
+        def call(dy, s, mean, rstd, w, ds):
+            (kept, DY), (_, S) = (off_by(rows, d, ld, offset, dtype, v) for v in (dy, s))
+            DS = off_by(rows, d, ld, offset, dtype, ds)[1] if ds is not None else None
+            buffer, DX = (kept, DY) if in_place else off_by(rows, d, ld, offset, dtype)
+            dw, db = (torch.empty(d, dtype=dtype, device="cuda") for _ in range(2))
+            need = sg.add_layernorm_backward_workspace_size(code, rows, d)
+            ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+            sg.sgemm_add_layernorm_backward(code, rows, d, DY.data_ptr(), ld, S.data_ptr(), ld,
+                                            mean.data_ptr(), rstd.data_ptr(), w.data_ptr(),
+                                            DS.data_ptr() if ds is not None else 0, ld, DX.data_ptr(),
+                                            ld, dw.data_ptr(), db.data_ptr(), ws.data_ptr(), need,
+                                            torch.cuda.current_stream().cuda_stream)
+            assert_untouched(buffer, DX)
+            return DX, dw, db
+        return call
+
+    for offset in range(0, 9, 1 if t == "bf16" else 2):
+        run_layernorm_backward(rows, d, t, True, call=backward(offset, False))
+        run_layernorm_backward(rows, d, t, offset % 4 == 0, call=backward(offset + 1, True))
 
 
 def test_add_layernorm_gradient_against_differences():
