@@ -119,8 +119,11 @@ constexpr Costs<3> kHalfCosts = {{{2, 256}, {2, 128}, {1, 64}}, {0.27, 0.2, 0.15
                                  {5.0, 3.0, 1.5}};
 
 // Pairs' tiles of 256 rows and `out` outputs (a multiple of 16 up to 128; weights stored K x N:
-// 64 or 128): kSumCosts between its widths, and the weights' way from HBM as in plan_single
-// (here at 41 bytes a ns and SM).
+// 64 or 128): kSumCosts between its widths, the weights' way from HBM as in plan_single
+// (here at 41 bytes a ns and SM), and tile_epilogue.
+// A tile's epilogue: the eight warps take it in blocks of 32 outputs, two at a time (SiLU; 4096 x 4096
+// x 128 bf16 in tiles of 128 outputs 21.7 us, of 96 24.7, of 80 28.1, of 64 25.3, of 32 39).
+double tile_epilogue(int out) { return out <= 64 ? 1.45 : 2.4; }
 struct Pairs {
     int out = 128;
     Plan plan;
@@ -131,7 +134,8 @@ Pairs plan_pairs(int M, int N, int kblocks, const Capacity &cap, bool any_out) {
     for (int out = step; out <= 128; out += step) {
         const double l2 = out < 64 ? 0.165 : 0.06 + 0.00164 * out, hbm = 0.0031 * out / row_tiles;
         const Costs<1> cost = {{{2, 2 * out}}, {hbm > l2 ? hbm : l2},
-                               {out < 64 ? 5.5 : 4.5 + 0.0156 * out}, {1.0 + 0.031 * out}};
+                               {out < 64 ? 5.5 : 4.5 + 0.0156 * out}, {1.0 + 0.031 * out},
+                               {tile_epilogue(out)}};
         const Plan plan = plan_tiles(M, 2 * N, kblocks, cap, cost);
         if (plan.us < best.plan.us) {
             best.out = out;
@@ -175,7 +179,9 @@ Single plan_single(int M, int N, int kblocks, const Capacity &cap, bool any_out)
         for (int parts = 1; parts <= 8; parts *= 2) {
             if (parts > 1 && (tiles > cap.of(parts) || kblocks < 2 * parts)) break;
             const int64_t rounds = parts > 1 ? 1 : (tiles + cap.sms - 1) / cap.sms;
-            double us = rounds * ((kblocks + parts - 1) / parts) * stage + 4.5;
+            const double product = ((kblocks + parts - 1) / parts) * stage;
+            const double epilogue = 1.15 * tile_epilogue(out);   // (3000 x 4000 x 300 112/1 26.1, pairs 24.4)
+            double us = product + (rounds - 1) * (product > epilogue ? product : epilogue) + 4.5;
             if (parts > 1)
                 us += (parts == 2 ? 0.7 : parts == 4 ? 1.0 : 1.3) + rows * out / 64;
             else if (stage == hbm)

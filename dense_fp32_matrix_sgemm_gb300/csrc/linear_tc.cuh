@@ -531,11 +531,18 @@ struct Plan {
 
 // The shapes and, in microseconds, what 128 bytes (f32: 64) of K of a tile take,
 // what a launch takes besides, and the joining of the parts of a split tile of 128
-// rows (next to 1 us a split launch).
+// rows (next to 1 us a split launch).  epilogue: what a tile's results take beside the next
+// tile's product (0: less than any).
 template <int SHAPES>
 struct Costs {
     TileShape shape[SHAPES];
-    double stage[SHAPES], fixed[SHAPES], join[SHAPES];
+    double stage[SHAPES], fixed[SHAPES], join[SHAPES], epilogue[SHAPES] = {};
+    // `rounds` tiles one behind the other
+    double rounds_us(int w, long long rounds, int kblocks) const {
+        const double product = (double)kblocks * stage[w];
+        return epilogue[w] > product ? product + (rounds - 1) * epilogue[w]
+                                     : (double)rounds * kblocks * stage[w];
+    }
 };
 
 template <int SHAPES>
@@ -564,14 +571,14 @@ Plan plan_tiles(int M, int N, int kblocks, const Capacity &cap, const Costs<SHAP
         const int tiles = (int)all, room = cap.of(ctas);
         const long long waves = tiles / room;
         const int tail = (int)(tiles - waves * room);
-        take((double)(waves + (tail > 0)) * kblocks * cost.stage[w] + cost.fixed[w], w,
-             {0, tiles, 1, room}, {}, 1);
+        take(cost.rounds_us(w, waves + (tail > 0), kblocks) + cost.fixed[w], w, {0, tiles, 1, room},
+             {}, 1);
         for (int parts = 2; parts <= (ctas == 2 ? 4 : 8); parts *= 2) {
             const double whole = split(w, tiles, parts);
             if (whole > 0) take(whole, w, {0, tiles, parts, 0}, {}, 1);
             const double rest = ctas == 2 && waves > 0 && tail > 0 ? split(w, tail, parts) : -1;
             if (rest > 0)
-                take((double)waves * kblocks * cost.stage[w] + cost.fixed[w] + rest, w,
+                take(cost.rounds_us(w, waves, kblocks) + cost.fixed[w] + rest, w,
                      {0, tiles - tail, 1, room}, {tiles - tail, tail, parts, 0}, 2);
         }
     }
