@@ -265,8 +265,9 @@ scale_kernel(const __grid_constant__ Table<MOST> table, const double *partial, i
         const double n = sqrt(warp_sum(sum));
         if (threadIdx.x == 0) {
             if (norm != nullptr && blockIdx.x == 0) *norm = (float)n;
-            // (nothing to scale where both are 0)
-            const double d = n + (double)eps, c = d == 0.0 ? 1.0 : (double)max_norm / d;
+            // (nothing to scale where both are 0; no bound scales nothing, an infinite norm or not)
+            const double d = n + (double)eps, bound = (double)max_norm;
+            const double c = d == 0.0 || (isinf(bound) && isinf(d)) ? 1.0 : bound / d;
             // (a NaN stays one; a factor that fp32 holds with few digits, for norms beyond
             // 1e36 times max_norm, is applied in two steps)
             const bool tiny = c < 0x1p-120;

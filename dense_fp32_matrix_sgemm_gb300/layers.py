@@ -216,8 +216,8 @@ def clip_grad_norm(tensors, max_norm, *, eps=1e-6, out=None, workspace=None, str
 
     In place, or with ``out`` (tensors of the same types, shapes and strides) there.  No
     result may overlap another one or another tensor of the list, so none is in the list
-    twice.  An infinite norm scales by 0 (an infinite element becomes NaN); a NaN reaches
-    every element."""
+    twice.  An infinite norm scales by 0 (an infinite element becomes NaN), an infinite
+    max_norm by 1; a NaN reaches every element."""
     tensors, out = _listed(tensors), None if out is None else _listed(out)
     if stream is not None and tensors:
         with _on(stream, tensors[0]):

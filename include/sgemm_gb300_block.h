@@ -138,12 +138,12 @@ uint64_t sgemm_add_layernorm_backward_workspace_size(int dtype, int64_t rows, in
  *               two results overlap, so no tensor is in the list twice when
  *               it is scaled in place.
  *   norm        one float, or NULL.
- *   max_norm    >= 0; infinity scales nothing.      eps  >= 0.
+ *   max_norm    >= 0; infinity scales nothing, whatever norm is not a NaN.      eps  >= 0.
  * The sum is held in 64 bits: values beyond 2^64 or below 2^-64 keep their
  * digits, and the norm is infinite only if it is beyond 3.4e38 or an element
- * is infinite.  An infinite norm gives the factor 0 (infinite elements become NaN), a
- * NaN makes the norm and, scaled, every element NaN.  Where norm + eps is 0 the
- * factor is 1.
+ * is infinite.  An infinite norm gives the factor 0 (infinite elements become NaN) for a
+ * finite max_norm, a NaN makes the norm and, scaled, every element NaN.  Where norm + eps
+ * is 0 the factor is 1.
  * An empty list has norm 0.
  *   workspace   sgemm_clip_grad_norm_workspace_size(count, dtypes, sizes)
  *               bytes, 256-byte aligned.

@@ -849,6 +849,20 @@ def test_clip_of_nothing_but_zeros_without_eps():
         assert float(sg.clip_grad_norm([a], max_norm, eps=0.0)) == 0 and not a.any()
 
 
+def test_clip_without_a_bound_scales_nothing():
+    for value in (2.0, float("inf")):
+        a = normal(gen(3), 4000)
+        a[7] = value
+        kept, out = a.clone(), torch.empty_like(a)
+        assert float(sg.clip_grad_norm([a], float("inf"), out=[out])) == float(sg.grad_norm([a]))
+        assert torch.equal(out, kept)
+        sg.clip_grad_norm([a], float("inf"))
+        assert torch.equal(a, kept)
+    a[8] = float("nan")
+    sg.clip_grad_norm([a], float("inf"))
+    assert torch.isnan(a).all()
+
+
 def test_clip_takes_one_tensor_and_any_iterable():
     a, b = normal(gen(1), 50, 7), normal(gen(2), 33)
     want = exact_norm([a])
