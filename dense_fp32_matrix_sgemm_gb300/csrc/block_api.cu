@@ -14,10 +14,24 @@
 namespace sgemm {
 namespace {
 
-// The gated product of few rows on the CUDA cores: linear's rule for the two weights as one
-// of twice the features.  Weights stored K x N go to the tensor cores.
+// The gated product of few rows on the CUDA cores, where its tiles on the tensor cores
+// take longer; us there / here, weights of both out of L2 (features x K):
+//   bf16   11264 x 4096  1 row 31.0 / 30.9, 2 rows 37.0 / 30.8; 4096 x 4096  2 rows 14.3 / 14.9, 4 rows
+//          25.2 / 14.8; 2048 x 2048  4 rows 7.1 / 8.3, 6 rows 10.2 / 8.2; 2048 x 1024  6 rows 6.4 / 6.8
+//   e4m3   11264 x 4096  1 row 21.7 / 19.4; 4096 x 4096  1 row 9.3 / 10.7, 2 rows 14.5 / 10.5; 2048 x
+//          2048  2 rows 5.1 / 6.8, 3 rows 6.8 / 6.7; 2048 x 1024  3 rows 5.3 / 5.9
+//   f32    4096 x 4096  16 rows 88 / 91, 24 rows 128 / 91
+//   f32 stored K x N   11264 x 4096  1 row 71 / 284, 4 rows 167 / 284; 4096 x 4096  4 rows 48 / 92, 8 rows
+//          105 / 92; 1024 x 1024  8 rows 9.2 / 12.7, 12 rows 17 / 13; 333 x 300  16 rows 5.8 / 9.5
 bool gated_on_cuda_cores(int type, int64_t M, int64_t N, int64_t K, int transW) {
-    return K == 0 || (transW && on_cuda_cores(type, M, 2 * N, K, 1));
+    if (K == 0) return true;
+    const int64_t weights = 2 * N * K;
+    if (type == SGEMM_F32)
+        return M <= (transW || weights <= 1 << 18 ? 16 : weights <= 1 << 21 ? 8 : 4);
+    if (!transW) return false;
+    if (type == SGEMM_E4M3)
+        return M <= (weights <= 1 << 22 ? 4 : weights <= 1 << 23 ? 2 : weights <= 1 << 25 ? 1 : 0);
+    return M <= (weights <= 1 << 22 ? 8 : weights <= 1 << 23 ? 4 : weights <= 1 << 24 ? 2 : 1);
 }
 
 size_t gated_bytes(int dtype, int64_t M, int64_t N, int64_t K, const void *X, int64_t ldx,
@@ -114,7 +128,8 @@ int gated_linear(int dtype, int64_t M, int64_t N, int64_t K, const void *X, int6
     if (K == 0) epi.sx = epi.sg = epi.su = nullptr;   // an empty sum is 0 in any unit
     epi.vec = gated_vector_width(out_dtype, epi);
     if (gated_on_cuda_cores(dtype, M, N, K, transW))
-        return launched(launch_gated_rows(dtype, X, ldx, Wg, ldwg, Wu, ldwu, (int)K, epi, s));
+        return launched(launch_gated_rows(dtype, X, ldx, Wg, ldwg, Wu, ldwu, K == 0 ? 1 : transW,
+                                          (int)K, epi, s));   // (K == 0: no weight is read)
     char *ws = static_cast<char *>(workspace);
     if (dtype == SGEMM_F32) {
         char *const wsg = ws + f32_planes_bytes(M, K), *const wsu = wsg + f32_planes_bytes(wr, wc);

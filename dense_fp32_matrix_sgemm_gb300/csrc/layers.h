@@ -77,7 +77,7 @@ cudaError_t launch_sum_tc(int in_type, const TcOperand (&A)[2], const TcOperand 
 // The gated product of few rows on the CUDA cores, one pass over both weights; any type and
 // alignment, weights stored by output features.  linear_rows.cu.
 cudaError_t launch_gated_rows(int in_type, const void *X, int64_t ldx, const void *Wg, int64_t ldwg,
-                              const void *Wu, int64_t ldwu, int K, const GatedEpi &epi,
+                              const void *Wu, int64_t ldwu, int transW, int K, const GatedEpi &epi,
                               cudaStream_t s);
 
 // Whether the gated layer's two weight gradients, each of this size, are better planned for

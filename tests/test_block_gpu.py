@@ -120,6 +120,24 @@ def test_gated_strides_and_offsets(m, pad, offset, t):
         run_gated(m, 171, 201, t, "none", pad=pad, offset=offset, w_kn=True)
 
 
+# few rows: f32 weights by columns, and both sides of the rows that go to the CUDA cores
+@pytest.mark.parametrize("m", [1, 2, 3, 4, 5, 8, 9, 16, 17])
+@pytest.mark.parametrize("n,k", [(1, 1), (7, 300), (132, 64), (256, 512), (1000, 257), (4100, 129),
+                                 (2052, 2000)])
+def test_gated_few_rows_by_columns(m, n, k):
+    run_gated(m, n, k, "f32", "silu", bias=True, preact=True, w_kn=True)
+    run_gated(m, n, k, "f32", "gelu", w_kn=True, pad=8)
+    run_gated(m, n, k, "f32", "relu", preact=True, w_kn=True, pad=3, offset=1)
+
+
+@pytest.mark.parametrize("t", ["bf16", "f16", "e4m3"])
+@pytest.mark.parametrize("m", [1, 2, 3, 4, 5, 7, 8, 9])
+@pytest.mark.parametrize("n,k", [(40, 1000), (2048, 1024), (2048, 2048), (2050, 1031), (4104, 2048)])
+def test_gated_few_rows(m, n, k, t):
+    run_gated(m, n, k, t, "silu", bias=True, preact=True)
+    run_gated(m, n, k, t, "gelu_erf", pad=3, offset=1)
+
+
 # tiles of every width that the rounds of SMs call for, whole and in parts of K, of few and many rows
 @pytest.mark.parametrize("t", ["bf16", "e4m3"])
 @pytest.mark.parametrize("m,n,k", [(64, 8192, 264), (9, 11264, 136), (100, 300, 4096), (8, 4096, 2208),
