@@ -21,13 +21,12 @@ namespace {
 //   e4m3   11264 x 4096  1 row 21.7 / 19.4; 4096 x 4096  1 row 9.3 / 10.7, 2 rows 14.5 / 10.5; 2048 x
 //          2048  2 rows 5.1 / 6.8, 3 rows 6.8 / 6.7; 2048 x 1024  3 rows 5.3 / 5.9
 //   f32    4096 x 4096  16 rows 88 / 91, 24 rows 128 / 91
-//   f32 stored K x N   11264 x 4096  1 row 71 / 284, 4 rows 167 / 284; 4096 x 4096  4 rows 48 / 92, 8 rows
-//          105 / 92; 1024 x 1024  8 rows 9.2 / 12.7, 12 rows 17 / 13; 333 x 300  16 rows 5.8 / 9.5
+//   f32 stored K x N   11264 x 4096  1 row 55 / 285, 16 rows 241 / 285; 4096 x 4096  1 row 23 / 93,
+//          16 rows 68 / 94; 1024 x 1024  16 rows 13.5 / 14.2; 300 x 333  16 rows 7.0 / 10.0
 bool gated_on_cuda_cores(int type, int64_t M, int64_t N, int64_t K, int transW) {
     if (K == 0) return true;
     const int64_t weights = 2 * N * K;
-    if (type == SGEMM_F32)
-        return M <= (transW || weights <= 1 << 18 ? 16 : weights <= 1 << 21 ? 8 : 4);
+    if (type == SGEMM_F32) return M <= 16;
     if (!transW) return false;
     if (type == SGEMM_E4M3)
         return M <= (weights <= 1 << 22 ? 4 : weights <= 1 << 23 ? 2 : weights <= 1 << 25 ? 1 : 0);
@@ -259,7 +258,8 @@ int gated_linear_backward(int dtype, int64_t M, int64_t N, int64_t K, const void
     // is no slower.  Large products: the weights' first (gradients of 2048 x 5632 x 2048 bf16 136.4 ->
     // 132.8 us, 1000 x 1376 x 1008 f32 77.4 -> 74.3); small ones: dX first (300^3 bf16 11.0, else 12.3;
     // 512 x 1280 x 236 f32 21.9, else 29.0).
-    const int half = dwg && dwu && gated_side_by_side(dtype, {(int)wr, (int)wc, (int)M}) ? kChainHalf : 0;
+    const int half =
+        dwg && dwu && gated_side_by_side(dtype, {(int)wr, (int)wc, (int)M}) ? kChainHalf : 0;
     const bool weights_first = (double)M * N * K >= (double)(1 << 30);
     int left = (int)dx + (int)dwg + (int)dwu + (int)db, done = 0;
     auto place_in_chain = [&] {

@@ -279,8 +279,9 @@ __global__ void __launch_bounds__(kThreads) column_kernel(const Args<LayerEpi> a
     }
 }
 
-// The same on both of the gated layer's weights.  (11264 x 4096, one row: 70.5 us, 5.2 TB/s; four
-// 167, as registers for both weights' sums leave fewer loads in flight.)
+// The same on both of the gated layer's weights, a warp taking four consecutive k at a time so that a
+// row of X costs one load for them.  (11264 x 4096, one row: 70.5 -> 55 us, 6.7
+// TB/s; four 167 -> 72; eight, whose 170 registers leave one CTA an SM, 128; 4096 x 4096, eight: 39.)
 template <int W, int MR>
 __global__ void __launch_bounds__(kThreads) gated_column_kernel(const Args<GatedEpi> a) {
     constexpr int COLS = 32 * W;
@@ -292,16 +293,18 @@ __global__ void __launch_bounds__(kThreads) gated_column_kernel(const Args<Gated
     const uint32_t rank = cluster_rank(), size = cluster_size();
     const int strip = (int)(blockIdx.x / size);
     const int c = strip * COLS + lane * W;
+    const bool x_whole = reinterpret_cast<uintptr_t>(a.X) % 16 == 0 && a.ldx % 4 == 0 && a.K % 4 == 0;
     const int groups = (a.epi.M + MR - 1) / MR;
     for (int g = blockIdx.y; g < groups; g += gridDim.y) {
         const int m0 = g * MR;
-        float acc[2][MR][W];
+        constexpr int P = (W + 1) / 2;   // pairs of columns
+        float2 acc[2][MR][P];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int m = 0; m < MR; ++m)
 #pragma unroll
-                for (int j = 0; j < W; ++j) acc[h][m][j] = 0.f;
+                for (int j = 0; j < P; ++j) acc[h][m][j] = make_float2(0.f, 0.f);
         if (c < a.epi.N) {
             const float *wg = static_cast<const float *>(a.W) + c;
             const float *wu = static_cast<const float *>(a.W2) + c;
@@ -309,26 +312,34 @@ __global__ void __launch_bounds__(kThreads) gated_column_kernel(const Args<Gated
 #pragma unroll
             for (int m = 0; m < MR; ++m)
                 x[m] = static_cast<const float *>(a.X) + min(m0 + m, a.epi.M - 1) * a.ldx;
-            const int step = kWarps * (int)size;
-            constexpr int U = MR <= 4 ? 4 : 2;   // k in flight
-            for (int k = (int)rank * kWarps + warp; k < a.K; k += U * step) {
-                Raw<float, W> vw[U][2];
-                float vx[U][MR];
+            const int step = 4 * kWarps * (int)size;
+            for (int k = 4 * ((int)rank * kWarps + warp); k < a.K; k += step) {
+                Raw<float, W> vw[4][2];
+                float vx[MR][4];
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int ku = k + u * step;
-                    if (ku < a.K) {
-                        vw[u][0].load(wg + ku * a.ldw);
-                        vw[u][1].load(wu + ku * a.ldw2);
+                for (int u = 0; u < 4; ++u) {
+                    vw[u][0].zero();
+                    vw[u][1].zero();
+                    if (k + u < a.K) {
+                        vw[u][0].load(wg + (k + u) * a.ldw);
+                        vw[u][1].load(wu + (k + u) * a.ldw2);
                     }
                 }
 #pragma unroll
-                for (int u = 0; u < U; ++u)
+                for (int m = 0; m < MR; ++m) {
+                    if (x_whole) {   // (then K is a multiple of 4)
+                        const float4 v = *reinterpret_cast<const float4 *>(x[m] + k);
+                        vx[m][0] = v.x;
+                        vx[m][1] = v.y;
+                        vx[m][2] = v.z;
+                        vx[m][3] = v.w;
+                    } else {
 #pragma unroll
-                    for (int m = 0; m < MR; ++m) vx[u][m] = x[m][min(k + u * step, a.K - 1)];
+                        for (int u = 0; u < 4; ++u) vx[m][u] = k + u < a.K ? x[m][k + u] : 0.f;
+                    }
+                }
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    if (k + u * step >= a.K) break;
+                for (int u = 0; u < 4; ++u)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         float f[W];
@@ -336,10 +347,12 @@ __global__ void __launch_bounds__(kThreads) gated_column_kernel(const Args<Gated
 #pragma unroll
                         for (int m = 0; m < MR; ++m)
 #pragma unroll
-                            for (int j = 0; j < W; ++j)
-                                acc[h][m][j] = fmaf(vx[u][m], f[j], acc[h][m][j]);
+                            for (int j = 0; j < P; ++j)
+                                acc[h][m][j] = __ffma2_rn(
+                                    make_float2(vx[m][u], vx[m][u]),
+                                    make_float2(f[2 * j], W > 1 ? f[(2 * j + 1) % W] : 0.f),
+                                    acc[h][m][j]);
                     }
-                }
             }
         }
 #pragma unroll
@@ -348,7 +361,8 @@ __global__ void __launch_bounds__(kThreads) gated_column_kernel(const Args<Gated
 #pragma unroll
             for (int m = 0; m < MR; ++m)
 #pragma unroll
-                for (int j = 0; j < W; ++j) red[warp][m][j * 32 + lane] = acc[h][m][j];
+                for (int j = 0; j < W; ++j)
+                    red[warp][m][j * 32 + lane] = j % 2 == 0 ? acc[h][m][j / 2].x : acc[h][m][j / 2].y;
             __syncthreads();
             for (int i = threadIdx.x; i < MR * COLS; i += kThreads) {
                 float s = 0.f;
@@ -416,12 +430,19 @@ cudaError_t run(Args<E> a, int transW, cudaStream_t s) {
     if constexpr (std::is_same<T, float>::value) {
         const int64_t strips = (a.epi.N + 32 * W - 1) / (32 * W);
         int size = 1;
-        while (size < 8 && strips * gy * size < kSms * 2 && a.K > size * kWarps * 4) size *= 2;
-        const dim3 grid((unsigned)(strips * size), gy);
-        if constexpr (std::is_same<E, GatedEpi>::value)
-            return launch(gated_column_kernel<W, MR>, grid, kThreads, size, a, s);
-        else
-            return launch(column_kernel<W, MR>, grid, kThreads, size, a, s);
+        if constexpr (std::is_same<E, GatedEpi>::value) {
+            // As large as all clusters still run at once: an SM holds 3, 2 or 1 CTAs, and clusters
+            // find room in nine tenths of that (14336 x 4096, one row: 224 CTAs 73.6 us, 448 90.6;
+            // 4096 x 4096, 8 rows: 128 CTAs 38.1, 256 59).
+            constexpr int CTAS = kSms * (MR == 1 ? 3 : MR <= 4 ? 2 : 1) * 9 / 10;
+            while (size < 8 && strips * gy * 2 * size <= CTAS && a.K > size * kWarps * 4) size *= 2;
+            return launch(gated_column_kernel<W, MR>, dim3((unsigned)(strips * size), gy), kThreads,
+                          size, a, s);
+        } else {
+            while (size < 8 && strips * gy * size < kSms * 2 && a.K > size * kWarps * 4) size *= 2;
+            return launch(column_kernel<W, MR>, dim3((unsigned)(strips * size), gy), kThreads, size, a,
+                          s);
+        }
     }
     return cudaErrorInvalidValue;
 }
