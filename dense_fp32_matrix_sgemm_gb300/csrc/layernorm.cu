@@ -581,7 +581,7 @@ struct LayerRingArgs {
     unsigned *error;
 };
 constexpr int kRingThreads = 512;
-constexpr int kRingBytes = 208 * 1024;
+constexpr int kRingBytes = 208 * 1024, kWideRingBytes = 225 * 1024;
 constexpr int kRingStages = 4;
 
 // An access's elements as pairs.
@@ -593,9 +593,12 @@ __device__ __forceinline__ void pairs(const Raw<T, W> &r, float2 (&f)[W / 2]) {
     for (int j = 0; j < W / 2; ++j) f[j] = make_float2(v[2 * j], v[2 * j + 1]);
 }
 
-template <class T>
+// WIDE: 32 columns a thread, for which registers hold the columns' sums only: a row is read from the
+// ring again for its products, the weights from L2 (16-bit rows beyond 8192 columns: 8192 x 12288 bf16
+// 383 us in 1024 threads of 16 columns, whose 64 registers spill, 183 here).
+template <class T, bool WIDE>
 __global__ void __launch_bounds__(kRingThreads, 1) layer_grad_ring_kernel(const LayerRingArgs args) {
-    constexpr int W = 16 / sizeof(T), NV = 16 / W, P = W / 2;   // 16 columns a thread
+    constexpr int W = 16 / sizeof(T), NV = (WIDE ? 32 : 16) / W, P = W / 2;   // 16 columns a thread
     const LayerGradArgs &a = args.g;
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ float red[2][2][16];
@@ -637,11 +640,14 @@ __global__ void __launch_bounds__(kRingThreads, 1) layer_grad_ring_kernel(const 
     };
     if (x < 32)
         for (int t = 0; t < min(stages, turns); ++t) issue(t);
-    float2 w[NV][P], dw[NV][P], db[NV][P];
+    float2 w[WIDE ? 1 : NV][P], dw[NV][P], db[NV][P];
+    auto load_weights = [&](int c, float2 (&w)[P]) {
+        pairs<T, W>(load_or_zero<T, W>(static_cast<const T *>(a.w) + c, mine && c < a.D), w);
+    };
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (i * tpr + x) * W;
-        pairs<T, W>(load_or_zero<T, W>(static_cast<const T *>(a.w) + c, mine && c < a.D), w[i]);
+        if constexpr (!WIDE) load_weights(c, w[i]);
 #pragma unroll
         for (int j = 0; j < P; ++j) dw[i][j] = db[i][j] = make_float2(0.f, 0.f);
     }
@@ -658,20 +664,21 @@ __global__ void __launch_bounds__(kRingThreads, 1) layer_grad_ring_kernel(const 
         load_statistics(t + 1);
         const T *dy = rows + (t % stages) * streams * a.D, *s = dy + a.D, *ds = s + a.D;
         (void)tc::wait(full0 + 8 * (t % stages), (t / stages) & 1, abort);
-        Raw<T, W> vy[NV], vs[NV];
+        Raw<T, W> vy[WIDE ? 1 : NV], vs[WIDE ? 1 : NV];
         float2 sg = make_float2(0.f, 0.f), sgn = sg;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (i * tpr + x) * W;
-            vy[i] = load_or_zero<T, W>(dy + c, c < a.D);
-            vs[i] = load_or_zero<T, W>(s + c, c < a.D);
+            const int c = (i * tpr + x) * W, held = WIDE ? 0 : i;
+            if constexpr (WIDE) load_weights(c, w[0]);
+            vy[held] = load_or_zero<T, W>(dy + c, c < a.D);
+            vs[held] = load_or_zero<T, W>(s + c, c < a.D);
             float2 fy[P], fs[P];
-            pairs<T, W>(vy[i], fy);
-            pairs<T, W>(vs[i], fs);
+            pairs<T, W>(vy[held], fy);
+            pairs<T, W>(vs[held], fs);
 #pragma unroll
             for (int j = 0; j < P; ++j) {
                 const float2 n = __fmul2_rn(__fadd2_rn(fs[j], mean), rstd);
-                const float2 g = __fmul2_rn(fy[j], w[i][j]);
+                const float2 g = __fmul2_rn(fy[j], w[held][j]);
                 sg = __fadd2_rn(sg, g);
                 sgn = __ffma2_rn(g, n, sgn);
                 dw[i][j] = __ffma2_rn(fy[j], n, dw[i][j]);
@@ -702,17 +709,22 @@ __global__ void __launch_bounds__(kRingThreads, 1) layer_grad_ring_kernel(const 
         const float2 kg2 = make_float2(kg, kg), kn2 = make_float2(kn, kn);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (i * tpr + x) * W;
+            const int c = (i * tpr + x) * W, held = WIDE ? 0 : i;
             if (c >= a.D) continue;
             float2 fy[P], fs[P], fd[P];
             float dx[W];
-            pairs<T, W>(vy[i], fy);
-            pairs<T, W>(vs[i], fs);
+            if constexpr (WIDE) {
+                load_weights(c, w[0]);
+                vy[0].load(dy + c);
+                vs[0].load(s + c);
+            }
+            pairs<T, W>(vy[held], fy);
+            pairs<T, W>(vs[held], fs);
             pairs<T, W>(load_or_zero<T, W>(ds + c, streams == 3), fd);
 #pragma unroll
             for (int j = 0; j < P; ++j) {
                 const float2 n = __fmul2_rn(__fadd2_rn(fs[j], mean), rstd);
-                const float2 g = __fmul2_rn(fy[j], w[i][j]);
+                const float2 g = __fmul2_rn(fy[j], w[held][j]);
                 const float2 d = __ffma2_rn(n, kn2, __ffma2_rn(g, rstd, kg2));
                 dx[2 * j] = d.x + fd[j].x;
                 dx[2 * j + 1] = d.y + fd[j].y;
@@ -730,7 +742,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) layer_grad_ring_kernel(const 
     if (a.partial == nullptr) return;
     // one row of partial sums a CTA: its groups' sums are added in their order
     float2 *sums = reinterpret_cast<float2 *>(ring);
-    const int width = tpr * 8;
+    const int width = tpr * NV * P;
     auto join = [&](float2 (&d)[NV][P]) {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
@@ -892,7 +904,7 @@ struct GradShape {
     int w, nv;      // elements an access, accesses a thread; nv 0: the wide kernel
     Shape sh;
     int ctas;
-    bool ring, shift;
+    bool ring, wide, shift;   // wide: the ring's 32 columns a thread
 };
 // Whether the ring takes rows of 16-byte pieces: of 1 KB or more (shorter rows would be many
 // small copies) up to 512 threads' 16 columns, and enough of them for twenty turns a CTA, as it
@@ -917,6 +929,14 @@ GradShape grad_shape(int type, int64_t rows, int64_t D, int w, bool shift) {
             g.ring = true;
             return g;
         }
+        if (w == 8 && g.sh.tpr > 512) {   // up to 16384 columns
+            g.sh = {shape_for(D / w, 4).tpr, 1};
+            g.w = w;
+            g.nv = 4;
+            g.ctas = rows < 152 ? (int)rows : 152;
+            g.ring = g.wide = true;
+            return g;
+        }
     }
     g.w = w;
     const int64_t n = shift ? D / w : (D + w - 1) / w;   // (a row's ends are no accesses)
@@ -937,36 +957,39 @@ GradShape grad_shape(int type, int64_t rows, int64_t D, int w, bool shift) {
     return g;
 }
 
-template <class T>
+template <class T, bool WIDE>
 cudaError_t launch_ring(const LayerGradArgs &a, const GradShape &g, cudaStream_t s) {
+    constexpr int RING = WIDE ? kWideRingBytes : kRingBytes;
     static PerContext<bool> configured;
     bool done = false;
     if (!configured.get(current_context_id(), done)) {
         const cudaError_t e = cudaFuncSetAttribute(
-            layer_grad_ring_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+            layer_grad_ring_kernel<T, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, RING);
         if (e != cudaSuccess) return e;
         configured.put(current_context_id(), true);
     }
     const int stage = g.sh.groups * (a.dS != nullptr ? 3 : 2) * a.D * (int)sizeof(T);
-    const int stages = kRingBytes / stage < kRingStages ? kRingBytes / stage : kRingStages;
+    const int stages = RING / stage < kRingStages ? RING / stage : kRingStages;
     const LayerRingArgs args = {a, g.sh.tpr, g.sh.groups, stages, device_error_word()};
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)g.ctas);
     cfg.blockDim = dim3(kRingThreads);
-    cfg.dynamicSmemBytes = kRingBytes;
+    cfg.dynamicSmemBytes = RING;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, layer_grad_ring_kernel<T>, args);
+    return cudaLaunchKernelEx(&cfg, layer_grad_ring_kernel<T, WIDE>, args);
 }
 
 template <class T>
 cudaError_t grad_dispatch(const LayerGradArgs &a, const GradShape &g, cudaStream_t s) {
     constexpr int W = 16 / sizeof(T);
-    if (g.ring) return launch_ring<T>(a, g, s);
+    if constexpr (W == 8)
+        if (g.wide) return launch_ring<T, true>(a, g, s);
+    if (g.ring) return launch_ring<T, false>(a, g, s);
     const dim3 grid((unsigned)g.ctas), block((unsigned)g.sh.tpr, (unsigned)g.sh.groups);
     if (g.shift) return launch(layer_grad_shift_kernel<T>, grid, block, a, s);
     if (g.nv == 0) return launch(layer_grad_wide_kernel<T>, grid, block, a, s);

@@ -592,11 +592,20 @@ def test_add_layernorm_backward_of_many_rows(rows, d, t):
     run_layernorm_backward(rows, d, t, False, pad=8)
 
 
+# 16-bit rows of 32 columns a thread: two and three rows in the ring, every number of turns
+@pytest.mark.parametrize("t", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("rows,d", [(1, 8200), (2, 16384), (151, 9008), (153, 12288), (306, 10240),
+                                    (458, 16376), (700, 8264), (1000, 12296)])
+def test_add_layernorm_backward_of_wide_rows(rows, d, t):
+    run_layernorm_backward(rows, d, t, True)
+    run_layernorm_backward(rows, d, t, False, pad=8)
+
+
 @pytest.mark.parametrize("t", ["f32", "bf16"])
 def test_add_layernorm_backward_in_place(t):
     # dX may be dY or dS itself: through the C ABI, one and many rows
     dtype, code = TYPES[t], 0 if t == "f32" else 1
-    for rows, d in ((3, 264), (1300, 4096), (6100, 4096), (700, 9001), (2100, 1001)):
+    for rows, d in ((3, 264), (1300, 4096), (6100, 4096), (700, 9001), (2100, 1001), (900, 12288)):
         g = gen(rows)
         dy, s, ds = (normal(g, rows, d, dtype=dtype) for _ in range(3))
         mean, rstd, w = normal(g, rows), normal(g, rows).abs() + 0.5, normal(g, d, dtype=dtype)
