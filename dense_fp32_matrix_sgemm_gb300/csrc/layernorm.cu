@@ -999,7 +999,11 @@ cudaError_t grad_dispatch(const LayerGradArgs &a, const GradShape &g, cudaStream
                    : launch(layer_grad_kernel<T, w(), nv(), kMaxThreads>, grid, block, a, s);
     };
     using std::integral_constant;
-    if (g.w == W) return run(integral_constant<int, W>(), integral_constant<int, 2>());
+    if constexpr (W == 8) {   // (more threads than 512: the ring)
+        if (g.w == W) return launch(layer_grad_kernel<T, W, 2, 512>, grid, block, a, s);
+    } else {
+        if (g.w == W) return run(integral_constant<int, W>(), integral_constant<int, 2>());
+    }
     if (g.w == W / 2) return run(integral_constant<int, W / 2>(), integral_constant<int, 4>());
     if constexpr (W == 8)
         if (g.w == 2) return run(integral_constant<int, 2>(), integral_constant<int, 8>());
