@@ -315,13 +315,14 @@ cudaError_t launch(void (*kernel)(P...), int grid, cudaStream_t s, const A &...a
 int grid_of(int chunks) { return chunks < kCtas ? chunks : kCtas; }
 
 // Tensors first .. of the list, as many as a table takes, without the empty ones; returns the
-// next one's number.
+// next one's number, that of a tensor with elements or `count`: the empty ones behind a full
+// table are passed over too, as a call for them alone would only clear the table.
 template <int MOST>
 int64_t fill(Table<MOST> &table, int64_t first, int64_t count, const int *types,
              const int64_t *sizes, const void *const *X, void *const *Y) {
     table.count = table.chunks = 0;
     int64_t i = first;
-    for (; i < count && table.count < MOST; ++i) {
+    for (; i < count && (table.count < MOST || sizes[i] == 0); ++i) {
         if (sizes[i] == 0) continue;
         Tensor &t = table.t[table.count];
         const uintptr_t x = reinterpret_cast<uintptr_t>(X[i]);
@@ -361,7 +362,7 @@ cudaError_t run(int64_t count, const int *types, const int64_t *sizes, const voi
     while (i < count) {
         i = fill(table, i, count, types, sizes, X, Y);
         if (i < 0) return cudaErrorInvalidValue;
-        if (table.chunks == 0) break;
+        if (table.chunks == 0) break;   // (a list of empty tensors)
         const cudaError_t e = launch(squares_kernel<MOST>, grid_of(table.chunks), s, table,
                                      partial + parts);
         if (e != cudaSuccess) return e;
@@ -379,7 +380,6 @@ cudaError_t run(int64_t count, const int *types, const int64_t *sizes, const voi
         const bool first = i == 0;
         if (tables == 1) i = count;   // it still holds the list
         else i = fill(table, i, count, types, sizes, X, Y);
-        if (table.chunks == 0) break;
         const cudaError_t e = launch(scale_kernel<MOST>, grid_of(table.chunks), s, table, sums,
                                      parts, max_norm, eps, first ? norm : (float *)nullptr);
         if (e != cudaSuccess) return e;

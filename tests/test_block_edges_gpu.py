@@ -1,0 +1,78 @@
+"""The gated block's operators on the GPU where they can go wrong, against 64 bits.
+
+EPS = 2^-23, u the output's unit roundoff, 2^-150 half of fp32's smallest step.
+"""
+import math
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+import dense_fp32_matrix_sgemm_gb300 as sg  # noqa: E402
+from test_layers_gpu import EPS, UNIT, check, gen, normal  # noqa: E402
+
+
+@pytest.fixture(scope="module", autouse=True)
+def no_pipeline_errors():
+    sg.device_status(reset=True)
+    yield
+    assert sg.device_status(reset=True) == 0
+
+
+# ------------------------------------------------------------------ clip_grad_norm
+
+# Roundings on the way to a sum of squares: a thread's FMAs of 16 (f32: 8) squares in each of two
+# chains, their join, five additions across the warp; from there on 64 bits hold the sum.  Each
+# errs by EPS / 2 of a sum of positive terms, and the square root halves that.
+NORM_TOL = {t: (n + 6) / 4 * EPS for t, n in ((torch.float32, 8), (torch.bfloat16, 16), (torch.float16, 16))}
+
+
+def check_clipped(tensors, max_norm, how, eps=1e-6):
+    """Clips copies of `tensors` in place or into `out`, or takes the norm alone (`how`)."""
+    norm = math.sqrt(sum(float(t.double().square().sum()) for t in tensors if t.numel()))
+    factor = min(1.0, max_norm / (norm + eps))
+    tol = max(NORM_TOL[t.dtype] for t in tensors)
+    given = [t.clone() for t in tensors]
+    if how == "norm":
+        result, got, factor = sg.grad_norm(given), given, 1.0
+    elif how == "in place":
+        result, got = sg.clip_grad_norm(given, max_norm, eps=eps), given
+    else:
+        got = [torch.full_like(t, float("nan")) for t in tensors]
+        result = sg.clip_grad_norm(given, max_norm, eps=eps, out=got)
+    # (the norm is rounded once; a bound for the second order of all that)
+    assert abs(float(result) - norm) <= 1.001 * (tol + EPS / 2) * norm, (float(result), norm)
+    flat = lambda ts: torch.cat([t.double().flatten() for t in ts])  # noqa: E731
+    want = flat(tensors) * factor
+    # the factor and the product are rounded in fp32, the result to its type
+    each = lambda f: torch.cat([torch.full((t.numel(),), f(t.dtype), dtype=torch.float64, device="cuda")  # noqa: E731
+                                for t in tensors])
+    step = {torch.float32: 0.0, torch.bfloat16: 2.0 ** -134, torch.float16: 2.0 ** -25}   # half of the smallest
+    check(flat(got), want, (1.001 * (tol + EPS) + each(UNIT.get)) * want.abs() + each(step.get) +
+          1.01 * 2.0 ** -150, how)
+    if how == "out":
+        assert all(torch.equal(a, b) for a, b in zip(given, tensors))
+
+
+HOW = ("in place", "out", "norm")
+
+
+@pytest.mark.parametrize("how", HOW)
+@pytest.mark.parametrize("empty", [0, 1, 2, 1000])
+@pytest.mark.parametrize("full", [31, 32, 33, 255, 256, 257, 999, 1000, 1001, 2000])
+def test_clip_lists_with_empty_tensors(full, empty, how):
+    # behind as many tensors as a launch's table holds, before them and among them
+    g = gen(full)
+    flat = normal(g, full * 5)
+    some, none = list(flat.view(full, 5)), [flat[:0]] * empty
+    check_clipped(some + none, 1.0, how)
+    if empty > 0:
+        check_clipped(none + some, 1.0, how)
+        check_clipped(none + some[:full // 2] + none + some[full // 2:] + none, 1.0, how)
+
+
+@pytest.mark.parametrize("how", HOW)
+def test_clip_lists_of_empty_tensors(how):
+    for count in (1, 33, 257, 1000, 1001, 2300):
+        check_clipped([torch.empty(0, device="cuda")] * count, 1.0, how)
