@@ -10,7 +10,7 @@ pytestmark = pytest.mark.gpu
 
 torch = pytest.importorskip("torch")
 import dense_fp32_matrix_sgemm_gb300 as sg  # noqa: E402
-from test_layers_gpu import EPS, UNIT, check, gen, normal  # noqa: E402
+from test_layers_gpu import EPS, TYPES, UNIT, check, gen, normal  # noqa: E402
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -76,3 +76,15 @@ def test_clip_lists_with_empty_tensors(full, empty, how):
 def test_clip_lists_of_empty_tensors(how):
     for count in (1, 33, 257, 1000, 1001, 2300):
         check_clipped([torch.empty(0, device="cuda")] * count, 1.0, how)
+
+
+@pytest.mark.parametrize("how", HOW)
+@pytest.mark.parametrize("types", [("f32",), ("bf16",), ("f16",), ("bf16", "f32", "f16")])
+def test_clip_errs_by_its_roundings(types, how):
+    # the largest errors are those of whole chunks of equal elements, whose roundings agree
+    for value in (1.0 / 3, 1.1, 0.7):
+        check_clipped([torch.full((n,), value, device="cuda").to(TYPES[types[i % len(types)]])
+                       for i, n in enumerate((50000, 16384, 8192, 777))], 0.3, how)
+    g = gen(11)
+    check_clipped([normal(g, n).to(TYPES[types[i % len(types)]]) for i, n in enumerate((100000, 8193, 7))],
+                  0.3, how)
