@@ -268,11 +268,14 @@ scale_kernel(const __grid_constant__ Table<MOST> table, const double *partial, i
             // (nothing to scale where both are 0; no bound scales nothing, an infinite norm or not)
             const double d = n + (double)eps, bound = (double)max_norm;
             const double c = d == 0.0 || (isinf(bound) && isinf(d)) ? 1.0 : bound / d;
-            // (a NaN stays one; a factor that fp32 holds with few digits, for norms beyond
-            // 1e36 times max_norm, is applied in two steps)
-            const bool tiny = c < 0x1p-120;
-            shared_factor = make_float2(c > 1.0 ? 1.f : (float)(tiny ? c * 0x1p64 : c),
-                                        tiny ? 0x1p-64f : 1.f);
+            // A factor that fp32 holds with few digits or not at all is applied in two steps, the
+            // second a power of two; what the first one's product loses below fp32's normal range,
+            // the second makes 0.  (Down to 2^-278, whose product with any element is 0.  A NaN
+            // stays one.)
+            const bool tiny = c < 0x1p-120, far = c < 0x1p-184;
+            const double held = far ? c * 0x1p148 : tiny ? c * 0x1p64 : c;
+            shared_factor = make_float2(c > 1.0 ? 1.f : (float)held,
+                                        far ? 0x1p-148f : tiny ? 0x1p-64f : 1.f);
         }
     }
     Walk<true, MOST> w(table);

@@ -88,3 +88,15 @@ def test_clip_errs_by_its_roundings(types, how):
     g = gen(11)
     check_clipped([normal(g, n).to(TYPES[types[i % len(types)]]) for i, n in enumerate((100000, 8193, 7))],
                   0.3, how)
+
+
+@pytest.mark.parametrize("how", ["in place", "out"])
+@pytest.mark.parametrize("types", [("f32",), ("bf16",), ("f32", "bf16")])
+@pytest.mark.parametrize("bits", [-20, -50, -57, -60, -66, -70, -90, -100, -120, -126, -140, -149])
+def test_clip_to_a_norm_far_below(bits, types, how):
+    # factors from 2^-146 down to 2^-275, far beyond what fp32 holds; the results are fp32 numbers
+    g = gen(13)
+    tensors = [normal(g, n, std=2.0 ** 121).to(TYPES[types[i % len(types)]]) for i, n in enumerate((900, 61))]
+    check_clipped(tensors, 2.0 ** bits, how)
+    if bits > -149:   # (an fp32 number)
+        check_clipped(tensors, 1.5 * 2.0 ** bits, how)
