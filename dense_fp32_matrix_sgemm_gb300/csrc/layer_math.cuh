@@ -361,31 +361,36 @@ __device__ __forceinline__ float activate_grad(float z, int act) {
 // waits for together, as soon as one lane's z is large (a gated layer of 1000 x 1369 x 1001
 // spent 10 us on SiLU and 18 on GELU behind a product of 28; 1 and 1.5 so).  With a = -|t| log2 e
 // in two words, exp(-|t|) = 2^hi (1 + lo ln 2) by the hardware's power of two (2^-22); its
-// reciprocal of 1 + e, in [1/2, 1], is corrected by a step of Newton's.  The power is kept
-// 2^24 times as large up to the product with z, so that SiLU's values reach as far down as
-// fp32's subnormal ones.
-__device__ __forceinline__ float gate_sigmoid(float t) {
+// reciprocal of 1 + e, in [1/2, 1], is corrected by a step of Newton's.  For t < 0 the sigmoid is
+// left 2^40 times as large until z or a slope's factor (up to 300) has met it: its own value is
+// subnormal from t = -87.3 on and 0 from -104, where SiLU has digits down to z = -108.6.
+struct GateSigmoid {
+    float p, unit;   // the sigmoid is p unit; unit: 1 or 2^-40
+};
+__device__ __forceinline__ GateSigmoid gate_sigmoid(float t) {
     t = hold(t, 128.f);   // (an infinity has no second word; 2^-184 is 0 all the same)
     const float u = fabsf(t);
     const float hi = -kLog2E * u;
     const float lo = fmaf(-1.925963033500e-8f, u, fmaf(-kLog2E, u, -hi));   // log2 e - kLog2E
     float e, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(hi + 24.f));
-    // (hi + 24 is rounded: what that loses goes to lo)
-    const float rest = lo + (hi - ((hi + 24.f) - 24.f));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(hi + 40.f));
+    // (hi + 40 is rounded: what that loses goes to lo)
+    const float rest = lo + (hi - ((hi + 40.f) - 40.f));
     e = fmaf(e * rest, 0.6931471805599453f, e);
-    const float d = fmaf(e, 0x1p-24f, 1.f);
+    const float d = fmaf(e, 0x1p-40f, 1.f);
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
     r = fmaf(r, fmaf(-d, r, 1.f), r);
-    return t < 0.f ? e * r * 0x1p-24f : r;
+    return t < 0.f ? GateSigmoid{e * r, 0x1p-40f} : GateSigmoid{r, 1.f};
 }
 
 template <class T>
 __device__ __forceinline__ float gate(float z, int act) {
     if constexpr (sizeof(T) == 4) {
-        if (act == SGEMM_ACT_SILU) return z * gate_sigmoid(z);
-        if (act == SGEMM_ACT_GELU)
-            return z * gate_sigmoid(2.f * kGeluC * (z + kGeluK * z * z * z));
+        if (act == SGEMM_ACT_SILU || act == SGEMM_ACT_GELU) {
+            const GateSigmoid s = gate_sigmoid(
+                act == SGEMM_ACT_SILU ? z : 2.f * kGeluC * (z + kGeluK * z * z * z));
+            return z * s.p * s.unit;
+        }
     }
     return activate<T>(z, act);
 }
@@ -417,17 +422,18 @@ __device__ __forceinline__ float activate_both(float z, int act, float &slope) {
             return z < 0.f ? 0.f : z;
         case SGEMM_ACT_GELU: {
             const float h2 = h * h;
-            float p;
             if constexpr (sizeof(T) == 4) {
-                p = gate_sigmoid(2.f * kGeluC * (h + kGeluK * h2 * h));
-                slope = p + 2.f * kGeluC * h * p * (1.f - p) * (1.f + 3.f * kGeluK * h2);
+                const GateSigmoid s = gate_sigmoid(2.f * kGeluC * (h + kGeluK * h2 * h));
+                const float q = 2.f * kGeluC * h * (1.f + 3.f * kGeluK * h2);
+                slope = s.p * fmaf(q, 1.f - s.p * s.unit, 1.f) * s.unit;
+                return z * s.p * s.unit;
             } else {   // the same with the constants multiplied out
-                p = sigmoid_of_power(h, fmaf(h2, -2.f * kGeluC * kGeluK * kLog2E,
-                                             -2.f * kGeluC * kLog2E));
+                const float p = sigmoid_of_power(h, fmaf(h2, -2.f * kGeluC * kGeluK * kLog2E,
+                                                         -2.f * kGeluC * kLog2E));
                 const float q = h * fmaf(h2, 6.f * kGeluC * kGeluK, 2.f * kGeluC);
                 slope = fmaf(q, fmaf(-p, p, p), p);
+                return z * p;
             }
-            return z * p;
         }
         case SGEMM_ACT_GELU_ERF: {
             float e;
@@ -436,9 +442,15 @@ __device__ __forceinline__ float activate_both(float z, int act, float &slope) {
             return z * p;
         }
         case SGEMM_ACT_SILU: {
-            const float p = sizeof(T) == 4 ? gate_sigmoid(h) : sigmoid<T>(h);
-            slope = p * (1.f + h * (1.f - p));
-            return z * p;
+            if constexpr (sizeof(T) == 4) {
+                const GateSigmoid s = gate_sigmoid(h);
+                slope = s.p * (1.f + h * (1.f - s.p * s.unit)) * s.unit;
+                return z * s.p * s.unit;
+            } else {
+                const float p = sigmoid<T>(h);
+                slope = p * (1.f + h * (1.f - p));
+                return z * p;
+            }
         }
         default: slope = 1.f; return z;
     }

@@ -100,3 +100,51 @@ def test_clip_to_a_norm_far_below(bits, types, how):
     check_clipped(tensors, 2.0 ** bits, how)
     if bits > -149:   # (an fp32 number)
         check_clipped(tensors, 1.5 * 2.0 ** bits, how)
+
+
+# ------------------------------------------------------------------ activations in f32
+
+# Where the sigmoid is at fp32's lower end.  z exact in few bits, so that any order of the product's
+# sums gives it exactly.  The sigmoid errs by 2^-22 (the power of two), 2 EPS (reciprocal, products) and,
+# in the tanh form, by 4 EPS of its argument, a product of seven rounded factors; the result is
+# rounded once, at the lower end to half of fp32's smallest step.
+def sigmoid_argument(z, name):
+    if name == "silu":
+        return z, torch.ones_like(z)
+    c = 2 * (2 / math.pi) ** 0.5
+    return c * (z + 0.044715 * z ** 3), c * (1 + 3 * 0.044715 * z ** 2)
+
+
+def tails(name):
+    if name == "silu":
+        z = torch.arange(-112, -84, 1 / 8, device="cuda")
+    else:
+        z = torch.arange(-11, -9, 1 / 128, device="cuda")
+    t, slope = sigmoid_argument(z.double(), name)
+    p = torch.sigmoid(t)
+    rel = 8 * EPS + (4 * EPS * t.abs() if name == "gelu" else 0.0)
+    return z, z.double() * p, p + z.double() * p * (1 - p) * slope, rel
+
+
+@pytest.mark.parametrize("name", ["silu", "gelu"])
+@pytest.mark.parametrize("w_kn", [False, True])
+@pytest.mark.parametrize("m", [1, 3, 16, 17, 300])
+def test_gated_f32_activations_reach_the_smallest_numbers(m, w_kn, name):
+    z, want, _, rel = tails(name)
+    one, zero = torch.ones_like(z), torch.zeros_like(z)
+    ws = [torch.stack(w) if w_kn else torch.stack(w, 1) for w in ((z, zero), (zero, one))]
+    h, zg, zu = sg.gated_linear(torch.ones(m, 2, device="cuda"), *[w.t() if w_kn else w for w in ws],
+                                activation=name, save_preact=True)
+    assert torch.equal(zg, z.expand(m, -1)) and torch.equal(zu, one.expand(m, -1))
+    check(h, want.expand(m, -1), (rel * want.abs() + 1.01 * 2.0 ** -150).expand(m, -1), name)
+
+
+@pytest.mark.parametrize("name", ["silu", "gelu"])
+def test_gated_f32_slopes_reach_the_smallest_numbers(name):
+    # the biases' gradients of one row are dZ itself, unrounded
+    z, value, slope, rel = tails(name)
+    one, k = torch.ones(1, z.numel(), device="cuda"), torch.zeros(z.numel(), 1, device="cuda")
+    got = sg.gated_linear_backward(one, torch.zeros(1, 1, device="cuda"), k, k, z[None], one, activation=name,
+                                   need_dx=False, need_dw=False)
+    check(got[3], slope, (rel + 8 * EPS) * slope.abs() + 1.01 * 2.0 ** -150, name)
+    check(got[4], value, rel * value.abs() + 1.01 * 2.0 ** -150, name)
