@@ -412,10 +412,12 @@ __device__ __forceinline__ void gate_all(float (&g)[N], const float (&u)[N], int
 }
 
 // act(z) and d act / dz together: both come from one sigmoid or Phi (where z is held,
-// that is 0 or 1 beyond).
+// that is 0 or 1 beyond; the value's factor is held below only, so that an infinite stored z
+// gives the limits 0 and infinity).
 template <class T>
 __device__ __forceinline__ float activate_both(float z, int act, float &slope) {
     const float h = hold(z, act == SGEMM_ACT_GELU ? 16.f : act == SGEMM_ACT_GELU_ERF ? 32.f : 256.f);
+    const float v = fmaxf(z, h);
     switch (act) {
         case SGEMM_ACT_RELU:
             slope = z > 0.f ? 1.f : 0.f;
@@ -426,30 +428,30 @@ __device__ __forceinline__ float activate_both(float z, int act, float &slope) {
                 const GateSigmoid s = gate_sigmoid(2.f * kGeluC * (h + kGeluK * h2 * h));
                 const float q = 2.f * kGeluC * h * (1.f + 3.f * kGeluK * h2);
                 slope = s.p * fmaf(q, 1.f - s.p * s.unit, 1.f) * s.unit;
-                return z * s.p * s.unit;
+                return v * s.p * s.unit;
             } else {   // the same with the constants multiplied out
                 const float p = sigmoid_of_power(h, fmaf(h2, -2.f * kGeluC * kGeluK * kLog2E,
                                                          -2.f * kGeluC * kLog2E));
                 const float q = h * fmaf(h2, 6.f * kGeluC * kGeluK, 2.f * kGeluC);
                 slope = fmaf(q, fmaf(-p, p, p), p);
-                return z * p;
+                return v * p;
             }
         }
         case SGEMM_ACT_GELU_ERF: {
             float e;
             const float p = normal_cdf<T>(h, e);
             slope = fmaf(h * (kRsqrt2Pi * (sizeof(T) == 4 ? 1.f : kTail)), e, p);
-            return z * p;
+            return v * p;
         }
         case SGEMM_ACT_SILU: {
             if constexpr (sizeof(T) == 4) {
                 const GateSigmoid s = gate_sigmoid(h);
                 slope = s.p * (1.f + h * (1.f - s.p * s.unit)) * s.unit;
-                return z * s.p * s.unit;
+                return v * s.p * s.unit;
             } else {
                 const float p = sigmoid<T>(h);
                 slope = p * (1.f + h * (1.f - p));
-                return z * p;
+                return v * p;
             }
         }
         default: slope = 1.f; return z;

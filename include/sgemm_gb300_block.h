@@ -70,8 +70,10 @@ uint64_t sgemm_gated_linear_workspace_size(int dtype, int64_t M, int64_t N, int6
  * Each of dX, dWg, dWu, db_gate, db_up may be NULL: it is then not computed.
  * dtype is the type of every matrix: SGEMM_F32, SGEMM_BF16 or SGEMM_F16.  For
  * the 16-bit types dZg and dZu enter the products rounded to the type (the
- * biases' sums are of the unrounded values).  X is read for dWg and dWu only,
- * the weights for dX only.  No output overlaps an input or another output.
+ * biases' sums are of the unrounded values).  Where zg is infinite (a stored one may
+ * have left its type's range), act' and act are their limits: 0 and 0, or 1 and infinity.
+ * X is read for dWg and dWu only, the weights for dX only.  No output overlaps an input
+ * or another output.
  */
 int sgemm_gated_linear_backward(int dtype, int64_t M, int64_t N, int64_t K,
                                 const void *dH, int64_t lddh, const void *Zg, int64_t ldzg,

@@ -148,3 +148,29 @@ def test_gated_f32_slopes_reach_the_smallest_numbers(name):
                                    need_dx=False, need_dw=False)
     check(got[3], slope, (rel + 8 * EPS) * slope.abs() + 1.01 * 2.0 ** -150, name)
     check(got[4], value, rel * value.abs() + 1.01 * 2.0 ** -150, name)
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("name", ["relu", "gelu", "gelu_erf", "silu"])
+def test_gated_gradients_at_an_infinite_gate(name, t):
+    # a stored pre-activation may have left its type's range: act and act' are then their limits,
+    # as at any z so far down (both 0) or up
+    g = gen(17)
+    m, n, k = 70, 136, 64
+    x, wg, wu, zg, zu, dh = (normal(g, *s, dtype=TYPES[t]) for s in
+                             ((m, k), (n, k), (n, k), (m, n), (m, n), (m, n)))
+    grads = lambda: sg.gated_linear_backward(dh, x, wg, wu, zg, zu, activation=name)  # noqa: E731
+    zg[5, 7] = zg[69, 135] = -60000.0
+    want = grads()
+    zg[5, 7] = zg[69, 135] = float("-inf")
+    got = grads()
+    assert all(torch.isfinite(v).all() and torch.equal(v, w) for v, w in zip(got, want))
+    zg[5, 7] = float("inf")   # dZu is infinite there, dZg as for any large z
+    zg[69, 135] = -60000.0
+    dx, dwg, dwu, dbg, dbu = grads()
+    zg[5, 7] = 60000.0
+    want = grads()
+    assert torch.equal(dwg, want[1]) and torch.equal(dbg, want[3])
+    keep = torch.arange(n, device="cuda") != 7
+    assert torch.equal(dwu[keep], want[2][keep]) and torch.equal(dbu[keep], want[4][keep])
+    assert torch.isinf(dbu[7]) and not torch.isfinite(dx[5]).any()
