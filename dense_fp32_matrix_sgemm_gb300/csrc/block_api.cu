@@ -20,9 +20,12 @@ namespace {
 //          25.2 / 14.8; 2048 x 2048  4 rows 7.1 / 8.3, 6 rows 10.2 / 8.2; 2048 x 1024  6 rows 6.4 / 6.8
 //   e4m3   11264 x 4096  1 row 21.7 / 19.4; 4096 x 4096  1 row 9.3 / 10.7, 2 rows 14.5 / 10.5; 2048 x
 //          2048  2 rows 5.1 / 6.8, 3 rows 6.8 / 6.7; 2048 x 1024  3 rows 5.3 / 5.9
-//   f32    4096 x 4096  16 rows 88 / 91, 24 rows 128 / 91
-//   f32 stored K x N   11264 x 4096  1 row 55 / 285, 16 rows 241 / 285; 4096 x 4096  1 row 23 / 93,
-//          16 rows 68 / 94; 1024 x 1024  16 rows 13.5 / 14.2; 300 x 333  16 rows 7.0 / 10.0
+//   f32    11264 x 4096  4 rows 286 / 76, 8 rows 286 / 106, 16 rows 286 / 212; 4096 x 4096  8 rows 91 / 44,
+//          16 rows 91 / 90, 24 rows 91 / 128; 2048 x 2048  16 rows 24.9 / 21.3; 1024 x 1024  16 rows
+//          11.8 / 7.6; 300 x 333  16 rows 9.4 / 5.8
+//   f32 stored K x N   11264 x 4096  1 row 285 / 55, 8 rows 284 / 127, 16 rows 285 / 241; 4096 x 4096
+//          1 row 93 / 23, 16 rows 93 / 68; 2048 x 2048  8 rows 24.8 / 23.9, 16 rows 25.0 / 20.0;
+//          1024 x 1024  16 rows 12.7 / 13.0; 300 x 333  16 rows 9.5 / 6.5
 bool gated_on_cuda_cores(int type, int64_t M, int64_t N, int64_t K, int transW) {
     if (K == 0) return true;
     const int64_t weights = 2 * N * K;

@@ -4,6 +4,12 @@
 // with both bias gradients' column sums in the same pass, and the sum of two outputs'
 // partial rows.  HBM bounds both: three reads and two writes an element (f32: two times
 // three planes of 2 bytes written), each in 16-byte accesses.
+// In the 16-bit types both dZ leave rounded to the type, as the tensor cores multiply 16-bit
+// operands: held in two terms each they would double the products, which are nine tenths of the
+// time.  It adds one rounding (2^-8 in bf16) to each term of the gradients' sums: of 2048 x 2048 x
+// 1024 bf16 they are off by 2.35e-3 of their 2-norm, 1.66e-3 (their own rounding) with dZ in fp32,
+// 2.9e-3 to 3.4e-3 where every step of the formula is rounded to bf16.  The biases' sums are of
+// the unrounded values.
 #include <cstdint>
 
 #include <cuda_runtime.h>

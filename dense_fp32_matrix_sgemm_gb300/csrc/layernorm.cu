@@ -910,7 +910,9 @@ struct GradShape {
 // small copies) up to 512 threads' 16 columns, and enough of them for twenty turns a CTA, as it
 // starts and ends later (ring / the other kernel, us: 16384 x 4096 bf16 89.5 / 95.0, 8192 x 4096
 // 50.5 / 51.8, 4096 x 4096 31.4 / 30.5, 16384 x 1024 30.0 / 28.1, 5200 x 8192 66.3 / 68.0; f32 8192 x
-// 4096 88.9 / 93.3, 2600 x 8192 68.6 / 62.5).
+// 4096 88.9 / 93.3, 2600 x 8192 68.6 / 62.5).  Widths whose groups leave many of the 512 threads idle,
+// or are one a CTA, lose time here that others do not: 8192 rows of 4096 / 5120 / 6144 / 7168 / 8192
+// bf16 columns 51 / 83 / 84 / 92 / 95 us, where their bytes take 40 / 50 / 59 / 69 / 79.
 bool ring_takes(int type, int64_t rows, int64_t D, Shape sh) {
     return sh.tpr > 0 && sh.tpr <= 512 && D * dtype_size(type) >= 1024 &&
            rows >= 152 * 20 * (512 / sh.tpr);

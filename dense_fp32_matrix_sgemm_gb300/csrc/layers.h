@@ -74,8 +74,10 @@ cudaError_t launch_gated_tc(int in_type, const TcOperand &X, const TcOperand &Wg
 // D = A1 B1^T + A2 B2^T, each reduction K long (count 1: the first alone).  epi: Y alone.
 cudaError_t launch_sum_tc(int in_type, const TcOperand (&A)[2], const TcOperand (&B)[2], int count,
                           int K, const LayerEpi &epi, int chain, cudaStream_t s);
-// The gated product of few rows on the CUDA cores, one pass over both weights; any type and
-// alignment, weights stored by output features.  linear_rows.cu.
+// The gated product of few rows on the CUDA cores, one pass over both weights for each few of them
+// (f32: 8 rows, the others 4): any type and alignment of weights stored by output features
+// (transW == 1), f32 alone of weights stored K x N (cudaErrorInvalidValue for the others, which
+// the tensor cores take as they are).  linear_rows.cu.
 cudaError_t launch_gated_rows(int in_type, const void *X, int64_t ldx, const void *Wg, int64_t ldwg,
                               const void *Wu, int64_t ldwu, int transW, int K, const GatedEpi &epi,
                               cudaStream_t s);

@@ -150,7 +150,8 @@ def gated_linear_backward(dh, x, w_gate, w_up, z_gate, z_up, *, activation="silu
                           need_dw=True, need_db=True, workspace=None, stream=None):
     """Gradients (dx, dw_gate, dw_up, db_gate, db_up) of ``gated_linear`` from dh (M, N), its x
     and weights, and the stored pre-activations; None where not asked for.  The weights'
-    gradients have the weights' storage order.  float32, bfloat16 or float16."""
+    gradients have the weights' storage order.  float32, bfloat16 or float16 (the gradients of the
+    pre-activations enter the 16-bit products rounded to the type)."""
     if stream is not None:
         with _on(stream, dh):
             return gated_linear_backward(dh, x, w_gate, w_up, z_gate, z_up, activation=activation,

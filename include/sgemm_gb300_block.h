@@ -100,7 +100,8 @@ uint64_t sgemm_gated_linear_backward_workspace_size(int dtype, int64_t M, int64_
  *   S, q_scale, Y   as in sgemm_add_rmsnorm (8-bit codes when q_scale is given).
  *   mean, rstd      each NULL, or `rows` floats.
  * A NaN or infinity makes its own row's values as the formula gives them and
- * touches no other row.  Rows of no elements (D == 0) have mean 0, rstd =
+ * touches no other row.  A row's sums are formed in 32 bits: where sum_d (s - mean)^2 passes
+ * 3.4e38 it is infinite and rstd 0.  Rows of no elements (D == 0) have mean 0, rstd =
  * eps^(-1/2) and the scale of a row of zeros.
  */
 int sgemm_add_layernorm(int dtype, int64_t rows, int64_t D, const void *X, int64_t ldx,
